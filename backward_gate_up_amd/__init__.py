@@ -26,10 +26,13 @@ import torch
 
 from . import _lib as _L
 from ._lib import SwiGLUError, STAGE_NAMES, NUM_STAGES  # noqa: F401
+from .serve import (moe_route, moe_experts, moe_infer, w4_quantize, w4_pack, w4_linear, infer_w4,  # noqa: F401
+                    W4Weight)
 
 __all__ = ["fwd", "bwd", "infer", "infer_noalloc", "SwiGLUMLPFunction", "swiglu_mlp", "SwiGLUMLP",
            "SwiGLUMLPPacked", "saved_bytes",
-           "infer_workspace_bytes", "bwd_workspace_bytes", "SwiGLUError", "StageTimer"]
+           "infer_workspace_bytes", "bwd_workspace_bytes", "SwiGLUError", "StageTimer",
+           "moe_route", "moe_experts", "moe_infer", "w4_quantize", "w4_pack", "w4_linear", "infer_w4", "W4Weight"]
 
 _DT = {torch.bfloat16: _L.BF16, torch.float16: _L.FP16, torch.float32: _L.FP32}
 

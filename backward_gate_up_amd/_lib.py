@@ -15,9 +15,18 @@ STATUS = {
 NOALLOC_SCRATCH_BYTES = 32 << 20
 FLAG_TWO_ROUND = 1
 FLAG_LINEAR_WEIGHTS = 2
-NUM_STAGES = 10
+NUM_STAGES = 13
 STAGE_NAMES = ("gateup_swiglu", "down_proj", "dgu_inplace", "dwd", "dwgu", "dx",
-               "infer_gateup", "infer_down", "dwd+dgu", "dwgu+dx")
+               "infer_gateup", "infer_down", "dwd+dgu", "dwgu+dx",
+               "moe_route", "few_gateup", "few_down")
+FEW_MAX_T = 65536
+
+
+class W4(ctypes.Structure):
+    """swiglu_w4_t."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("experts", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("group", ctypes.c_int32), ("has_zeros", ctypes.c_int32)]
 
 _lib = None
 
@@ -61,6 +70,23 @@ def lib():
     L.swiglu_mlp_infer_ex.restype = i32
     L.swiglu_mlp_infer_noalloc.argtypes = [vp] * 5 + [i64] * 3 + [i32, u32, vp]
     L.swiglu_mlp_infer_noalloc.restype = i32
+    w4 = ctypes.POINTER(W4)
+    for name, args, res in (
+            ("moe_route", [vp] * 4 + [i64] * 4 + [i32, i32, vp], i32),
+            ("moe_workspace_bytes", [i64] * 3 + [i32], sz),
+            ("moe_experts", [vp] * 8 + [sz] + [i64] * 5 + [i32, vp], i32),
+            ("moe_infer", [vp] * 7 + [sz] + [i64] * 5 + [i32, i32, vp], i32),
+            ("moe_experts_w4", [vp] * 3 + [w4] * 3 + [vp, vp, sz, i64, i64, i32, vp], i32),
+            ("moe_infer_w4", [vp, vp] + [w4] * 3 + [vp, vp, sz, i64, i64, i32, i32, vp], i32),
+            ("w4_bytes", [i64] * 3 + [i32, i32], sz),
+            ("w4_quantize", [vp] * 4 + [i64] * 3 + [i32, i32, vp], i32),
+            ("w4_pack", [vp] * 4 + [i64] * 3 + [i32, vp], i32),
+            ("w4_dequantize", [w4, vp, i32, vp], i32),
+            ("w4_linear", [vp, w4, vp, i64, i32, vp], i32),
+            ("w4_infer_workspace_bytes", [i64, i64, i32], sz),
+            ("w4_infer", [vp] + [w4] * 3 + [vp, vp, sz, i64, i32, vp], i32)):
+        f = getattr(L, "swiglu_mlp_" + name)
+        f.argtypes, f.restype = args, res
     L.swiglu_mlp_status_string.argtypes = [i32]
     L.swiglu_mlp_status_string.restype = ctypes.c_char_p
     L.swiglu_mlp_timer_start.argtypes = [i32]

@@ -1,9 +1,10 @@
 """Build the HIP library in-tree: backward_gate_up_amd/libswiglu_mlp.so (gfx950).
 
 The kernels are instantiated in eighteen translation units (csrc/instantiate.hip
-compiled once per dtype, entry point and weight layout) plus the C ABI
-(csrc/swiglu_mlp.hip);
-they compile in parallel and are linked into one shared library.
+compiled once per dtype, entry point and weight layout), the few-token serving
+kernels in nine more (csrc/few_instantiate.hip, once per dtype and weight
+format), plus the C ABI (csrc/swiglu_mlp.hip, csrc/few.hip); they compile in
+parallel and are linked into one shared library.
 """
 
 import os
@@ -35,6 +36,9 @@ UNITS = [("abi", "swiglu_mlp.hip", [])] + [
      [f"-DSWIGLU_INST_DTYPE={i}", f"-DSWIGLU_INST_OP={j}", f"-DSWIGLU_INST_LIN={k}"])
     for i, dt in enumerate(("bf16", "fp16", "fp32")) for j, op in enumerate(("fwd", "bwd", "infer"))
     for k, lay in enumerate(("kernel", "linear"))
+] + [("few", "few.hip", [])] + [
+    (f"{dt}_few_{fmt}", "few_instantiate.hip", [f"-DSWIGLU_INST_DTYPE={i}", f"-DSWIGLU_INST_FMT={fmt}"])
+    for i, dt in enumerate(("bf16", "fp16", "fp32")) for fmt in (0, 32, 64, 128) if fmt == 0 or dt != "fp32"
 ]
 
 

@@ -1872,6 +1872,9 @@ struct Timer {
 };
 extern Timer g_timer;  // defined once, in swiglu_mlp.hip
 
+// Stage ids of the few-token serving kernels (include/swiglu_mlp.h).
+enum { STAGE_ROUTE = 10, STAGE_FEW_GATEUP = 11, STAGE_FEW_DOWN = 12 };
+
 struct StageScope {
   int s;
   hipStream_t st;

@@ -1,0 +1,311 @@
+"""Serving with few tokens: a mixture of SwiGLU experts and 4-bit weights.
+
+Op level, as in the package's other wrappers (every arithmetic step runs in the
+HIP kernels behind the C ABI of include/swiglu_mlp.h; no fallback):
+
+* ``moe_route``   top-k experts of each token and their weights
+* ``moe_experts`` the chosen experts' SwiGLU blocks, weighted and summed
+* ``moe_infer``   both in one call
+* ``w4_quantize``, ``w4_pack``, ``W4Weight``  4-bit weights with group scales
+* ``w4_linear``   y = x W^T with a 4-bit weight
+* ``infer_w4``    the dense SwiGLU block with 4-bit weights
+
+and the modules ``SwiGLUMoE`` and ``SwiGLUMLPW4``. Weights are in the nn.Linear
+layout. The operators have no backward: inputs that need gradients are refused
+while autograd is on.
+"""
+
+import ctypes
+
+import torch
+
+from . import _lib as _L
+from ._lib import SwiGLUError
+
+_DT = {torch.bfloat16: _L.BF16, torch.float16: _L.FP16, torch.float32: _L.FP32}
+_DT16 = {torch.bfloat16: _L.BF16, torch.float16: _L.FP16}
+
+
+def _check(rc, where):
+    if rc != 0:
+        raise SwiGLUError(rc, where)
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _ptr(t):
+    return t.data_ptr() if t.numel() else None
+
+
+def _code(t, table=_DT):
+    try:
+        return table[t.dtype]
+    except KeyError:
+        names = ", ".join(str(d)[6:] for d in table)
+        raise TypeError(f"unsupported dtype {t.dtype}; use {names}") from None
+
+
+def _no_grad(*tensors):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise RuntimeError("the few-token serving operators have no backward: call them under torch.no_grad()")
+
+
+def _on_gpu(x):
+    if x.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU (cuda/HIP device)")
+
+
+def _buf(t, shape, dtype, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.device != device or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _workspace(ws, need, device):
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return ws
+
+
+class W4Weight:
+    """A weight [N, K], or a stack [E, N, K], in 4 bits with a scale (and a
+    zero point) for each ``group`` of K, in the kernels' packed layout.
+    ``dtype`` is the type of the scales and of the activations it multiplies.
+    Made by ``w4_pack`` or ``W4Weight.quantize``; ``dequantize`` writes it back
+    as rows."""
+
+    def __init__(self, data, shape, group, has_zeros, dtype):
+        self.data, self.shape, self.group = data, tuple(shape), int(group)
+        self.has_zeros, self.dtype = bool(has_zeros), dtype
+        self.experts = self.shape[0] if len(self.shape) == 3 else 1
+        self._c = _L.W4(data.data_ptr(), self.experts, self.shape[-2], self.shape[-1], self.group, int(self.has_zeros))
+        self._ref = ctypes.byref(self._c)
+
+    device = property(lambda self: self.data.device)
+    requires_grad = False
+
+    @classmethod
+    def quantize(cls, w, group=128, zeros=False):
+        """The nearest 4-bit weight of ``w`` under ``w4_quantize``'s rule."""
+        return w4_pack(*w4_quantize(w, group, zeros))
+
+    def dequantize(self):
+        """The weight as rows in ``dtype``, each value rounded once (for
+        prompts long enough that ``infer(..., linear=True)`` is the faster)."""
+        w = torch.empty(self.shape, dtype=self.dtype, device=self.device)
+        _check(_L.lib().swiglu_mlp_w4_dequantize(self._ref, w.data_ptr(), _DT16[self.dtype], _stream(w.device)),
+               "swiglu_mlp_w4_dequantize")
+        return w
+
+    def __repr__(self):
+        z = ", zeros" if self.has_zeros else ""
+        return f"W4Weight({list(self.shape)}, group={self.group}{z}, dtype={self.dtype}, device={self.device})"
+
+
+def _w4_shape(shape, group):
+    if len(shape) not in (2, 3):
+        raise ValueError("a 4-bit weight is [N, K] or [E, N, K]")
+    *lead, N, K = shape
+    if group not in (32, 64, 128) or K <= 0 or K % group or N <= 0 or N % 8:
+        raise ValueError(f"4-bit weights need group 32, 64 or 128 dividing K, and N a multiple of 8: "
+                         f"got N={N}, K={K}, group={group}")
+    return (lead[0] if lead else 1), N, K
+
+
+def w4_quantize(w, group=128, zeros=False):
+    """(codes, scales, zero points or None) of ``w`` [N, K] or [E, N, K]: codes
+    [.., N, K/2] uint8, two to a byte (the even k in the low half), scales
+    [.., N, K/group] in w's dtype, zero points [.., N, K/group] uint8. Without
+    zero points scale = max|w| / 7.5 and code = round(w / scale) + 8, with
+    them scale = (max(w, 0) - min(w, 0)) / 15 and code = round(w / scale) +
+    round(-min / scale), all clamped to 0..15."""
+    w = w.detach().contiguous()
+    _on_gpu(w)
+    dt = _code(w, _DT16)
+    E, N, K = _w4_shape(w.shape, group)
+    lead, g = w.shape[:-1], (*w.shape[:-1], K // group)
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty(g, dtype=w.dtype, device=w.device)
+    zp = torch.empty(g, dtype=torch.uint8, device=w.device) if zeros else None
+    rc = _L.lib().swiglu_mlp_w4_quantize(w.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                         zp.data_ptr() if zeros else None, E, N, K, group, dt, _stream(w.device))
+    _check(rc, "swiglu_mlp_w4_quantize")
+    return codes, scales, zp
+
+
+def w4_pack(codes, scales, zeros=None):
+    """The ``W4Weight`` of codes, scales and zero points laid out as
+    ``w4_quantize`` returns them (any quantiser's, with codes and zero points
+    0..15). W = scale * (code - zero), zero = 8 where ``zeros`` is None."""
+    codes, scales = codes.contiguous(), scales.contiguous()
+    _on_gpu(codes)
+    _code(scales, _DT16)
+    if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or scales.dim() != codes.dim():
+        raise ValueError("codes must be uint8 [.., N, K/2] and scales [.., N, K/group]")
+    K = 2 * codes.shape[-1]
+    if scales.shape[:-1] != codes.shape[:-1] or scales.shape[-1] == 0 or K % scales.shape[-1]:
+        raise ValueError(f"scales {tuple(scales.shape)} do not divide codes {tuple(codes.shape)} into groups")
+    group = K // scales.shape[-1]
+    shape = (*codes.shape[:-1], K)
+    E, N, K = _w4_shape(shape, group)
+    if scales.device != codes.device:
+        raise ValueError("all tensors must be on one device")
+    if zeros is not None:
+        zeros = zeros.contiguous()
+        if zeros.dtype != torch.uint8 or zeros.shape != scales.shape or zeros.device != codes.device:
+            raise ValueError("zeros must be uint8, shaped like scales, on the same device")
+    L = _L.lib()
+    data = torch.empty(L.swiglu_mlp_w4_bytes(E, N, K, group, zeros is not None), dtype=torch.uint8, device=codes.device)
+    rc = L.swiglu_mlp_w4_pack(codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+                              data.data_ptr(), E, N, K, group, _stream(codes.device))
+    _check(rc, "swiglu_mlp_w4_pack")
+    return W4Weight(data, shape, group, zeros is not None, scales.dtype)
+
+
+def moe_route(x, w_router, top_k, renormalize=True, weights=None, ids=None):
+    """The router: (weights [T, k] fp32, ids [T, k] int32) of the ``top_k``
+    largest logits of x[T, D] w_router[E, D]^T per token, in descending order
+    (equal logits: the lower index first). Weights are the softmax over all
+    experts, divided by the chosen ones' sum with ``renormalize``."""
+    _no_grad(x, w_router)
+    x, w_router = x.contiguous(), w_router.contiguous()
+    T, D, E = _router_shapes(x, w_router, top_k)
+    weights = _buf(weights, (T, top_k), torch.float32, x.device, "weights")
+    ids = _buf(ids, (T, top_k), torch.int32, x.device, "ids")
+    rc = _L.lib().swiglu_mlp_moe_route(_ptr(x), w_router.data_ptr(), _ptr(weights), _ptr(ids), T, D, E, top_k,
+                                       bool(renormalize), _code(x), _stream(x.device))
+    _check(rc, "swiglu_mlp_moe_route")
+    return weights, ids
+
+
+def _router_shapes(x, w_router, top_k):
+    if x.dim() != 2 or w_router.dim() != 2 or x.shape[1] != w_router.shape[1]:
+        raise ValueError(f"expected X[T,D] and a router weight [E,D]: {tuple(x.shape)}, {tuple(w_router.shape)}")
+    if w_router.dtype != x.dtype or w_router.device != x.device:
+        raise ValueError("all tensors must share dtype and device")
+    _on_gpu(x)
+    E = w_router.shape[0]
+    if not 1 <= top_k <= min(E, 32):
+        raise ValueError(f"top_k must be between 1 and min(E, 32): got {top_k} of {E}")
+    return x.shape[0], x.shape[1], E
+
+
+def _expert_shapes(x, wg, wu, wd):
+    """(E, H, 4-bit?) after checking the experts' weights against x."""
+    w4 = isinstance(wg, W4Weight)
+    if isinstance(wu, W4Weight) != w4 or isinstance(wd, W4Weight) != w4:
+        raise TypeError("the experts' weights must be all tensors or all W4Weight")
+    if x.dim() != 2 or len(wg.shape) != 3:
+        raise ValueError("expected X[T,D] and weights [E,H,D], [E,H,D], [E,D,H]")
+    E, H, D = wg.shape
+    if x.shape[1] != D or tuple(wu.shape) != (E, H, D) or tuple(wd.shape) != (E, D, H):
+        raise ValueError(f"shape mismatch (expected Wg[E,H,D], Wu[E,H,D], Wd[E,D,H]): X{tuple(x.shape)} "
+                         f"Wg{tuple(wg.shape)} Wu{tuple(wu.shape)} Wd{tuple(wd.shape)}")
+    for t in (wg, wu, wd):
+        if t.dtype != x.dtype or t.device != x.device:
+            raise ValueError("all tensors must share dtype and device")
+    if w4 and not wg.group == wu.group == wd.group:
+        raise ValueError("the three weights must share their group size")
+    _on_gpu(x)
+    return E, H, w4
+
+
+def moe_experts(x, weights, ids, wg, wu, wd, y=None, workspace=None):
+    """Y[t] = sum over j of weights[t, j] * SwiGLU block of expert ids[t, j] on
+    x[t]. x [T, D]; weights fp32 and ids int32 [T, k]; wg, wu [E, H, D] and wd
+    [E, D, H], tensors of x's dtype or three ``W4Weight``. An id outside
+    [0, E) chooses nothing (dropped tokens, experts of another device)."""
+    _no_grad(x, weights, *(() if isinstance(wg, W4Weight) else (wg, wu, wd)))
+    x, weights, ids = x.contiguous(), weights.contiguous(), ids.contiguous()
+    E, H, w4 = _expert_shapes(x, wg, wu, wd)
+    T, D = x.shape
+    if (ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or weights.shape != ids.shape
+            or weights.dtype != torch.float32 or ids.device != x.device or weights.device != x.device):
+        raise ValueError("weights must be fp32 and ids int32, both [T, k] on x's device")
+    k, dt, L = ids.shape[1], _code(x), _L.lib()
+    y = _buf(y, (T, D), x.dtype, x.device, "y")
+    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, H, k, dt), x.device)
+    nbytes = ws.numel() * ws.element_size()
+    if w4:
+        rc = L.swiglu_mlp_moe_experts_w4(_ptr(x), _ptr(weights), _ptr(ids), wg._ref, wu._ref, wd._ref, _ptr(y),
+                                         _ptr(ws), nbytes, T, k, dt, _stream(x.device))
+    else:
+        wg, wu, wd = wg.contiguous(), wu.contiguous(), wd.contiguous()
+        rc = L.swiglu_mlp_moe_experts(_ptr(x), _ptr(weights), _ptr(ids), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(),
+                                      _ptr(y), _ptr(ws), nbytes, T, D, H, E, k, dt, _stream(x.device))
+    _check(rc, "swiglu_mlp_moe_experts")
+    return y
+
+
+def moe_infer(x, w_router, wg, wu, wd, top_k, renormalize=True, y=None, workspace=None):
+    """A whole mixture-of-experts layer: ``moe_route`` then ``moe_experts``,
+    three launches in one call. x [T, D], w_router [E, D]; wg, wu [E, H, D] and
+    wd [E, D, H], tensors of x's dtype or three ``W4Weight``."""
+    _no_grad(x, w_router, *(() if isinstance(wg, W4Weight) else (wg, wu, wd)))
+    x, w_router = x.contiguous(), w_router.contiguous()
+    T, D, E = _router_shapes(x, w_router, top_k)
+    E2, H, w4 = _expert_shapes(x, wg, wu, wd)
+    if E2 != E:
+        raise ValueError(f"the router has {E} experts, the weights {E2}")
+    dt, L = _code(x), _L.lib()
+    y = _buf(y, (T, D), x.dtype, x.device, "y")
+    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, H, top_k, dt), x.device)
+    nbytes = ws.numel() * ws.element_size()
+    if w4:
+        rc = L.swiglu_mlp_moe_infer_w4(_ptr(x), w_router.data_ptr(), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws),
+                                       nbytes, T, top_k, bool(renormalize), dt, _stream(x.device))
+    else:
+        wg, wu, wd = wg.contiguous(), wu.contiguous(), wd.contiguous()
+        rc = L.swiglu_mlp_moe_infer(_ptr(x), w_router.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), _ptr(y),
+                                    _ptr(ws), nbytes, T, D, H, E, top_k, bool(renormalize), dt, _stream(x.device))
+    _check(rc, "swiglu_mlp_moe_infer")
+    return y
+
+
+def w4_linear(x, w, y=None):
+    """Y[T, N] = x[T, K] W^T with a 4-bit weight [N, K]; one launch."""
+    _no_grad(x)
+    x = x.contiguous()
+    if x.dim() != 2 or len(w.shape) != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"shape mismatch (expected X[T,K], W[N,K]): X{tuple(x.shape)} W{tuple(w.shape)}")
+    if w.dtype != x.dtype or w.device != x.device:
+        raise ValueError("all tensors must share dtype and device")
+    _on_gpu(x)
+    T = x.shape[0]
+    y = _buf(y, (T, w.shape[0]), x.dtype, x.device, "y")
+    _check(_L.lib().swiglu_mlp_w4_linear(_ptr(x), w._ref, _ptr(y), T, _DT16[x.dtype], _stream(x.device)),
+           "swiglu_mlp_w4_linear")
+    return y
+
+
+def infer_w4(x, wg, wu, wd, y=None, workspace=None):
+    """The no-grad SwiGLU block Y = (SiLU(x Wg^T) * (x Wu^T)) Wd^T with 4-bit
+    weights wg, wu [H, D] and wd [D, H]; two launches, workspace A[T, H]."""
+    _no_grad(x)
+    x = x.contiguous()
+    if x.dim() != 2 or len(wg.shape) != 2:
+        raise ValueError("expected X[T,D] and weights [H,D], [H,D], [D,H]")
+    T, D = x.shape
+    H = wg.shape[0]
+    if tuple(wg.shape) != (H, D) or tuple(wu.shape) != (H, D) or tuple(wd.shape) != (D, H):
+        raise ValueError(f"shape mismatch (expected Wg[H,D], Wu[H,D], Wd[D,H]): X{tuple(x.shape)} "
+                         f"Wg{tuple(wg.shape)} Wu{tuple(wu.shape)} Wd{tuple(wd.shape)}")
+    for t in (wg, wu, wd):
+        if t.dtype != x.dtype or t.device != x.device:
+            raise ValueError("all tensors must share dtype and device")
+    if not wg.group == wu.group == wd.group:
+        raise ValueError("the three weights must share their group size")
+    _on_gpu(x)
+    dt, L = _DT16[x.dtype], _L.lib()
+    y = _buf(y, (T, D), x.dtype, x.device, "y")
+    ws = _workspace(workspace, T * H * 2, x.device)
+    rc = L.swiglu_mlp_w4_infer(_ptr(x), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), T,
+                               dt, _stream(x.device))
+    _check(rc, "swiglu_mlp_w4_infer")
+    return y

@@ -201,6 +201,94 @@ int swiglu_mlp_infer_noalloc(const void* X, const void* Wg, const void* Wu, cons
                              void* Y, int64_t T, int64_t D, int64_t H, int dtype,
                              unsigned flags, hipStream_t stream);
 
+/* ---- Serving with few tokens ----------------------------------------------
+ * A mixture of SwiGLU experts and products with 4-bit weights, for the calls
+ * whose time is that of reading the weights (a decoding step: one token per
+ * sequence). No backward. All weights are in the nn.Linear layout; sums are
+ * fp32, A is rounded once to the storage type between the two launches, Y
+ * once at the end. Any T up to SWIGLU_FEW_MAX_T is computed, in chunks of 64
+ * tokens that each read the weights they need again; the kernels are meant
+ * for T up to about 64.
+ *
+ * Router (swiglu_mlp_moe_route): logits l = X Wr^T over E experts, the k
+ * largest of each token in descending order (equal logits: the lower index
+ * first; NaN before everything), weights softmax(l) over all E, divided by
+ * the chosen ones' sum when `renorm` is nonzero. X [T, D], Wr [E, D] in one
+ * dtype; weights fp32 and ids int32 [T, k], 4-byte aligned. The order is that of the exact logits: those
+ * closer to a neighbour than the fp32 sums can tell apart are summed again in
+ * fp64 (among the 64 leading ones of a token).
+ *
+ * Experts (swiglu_mlp_moe_experts): Y[t] = sum_j weights[t][j] *
+ * ((SiLU(X[t] Wg_e^T) * (X[t] Wu_e^T)) Wd_e^T), e = ids[t][j]; Wg, Wu
+ * [E, H, D], Wd [E, D, H]. An id outside [0, E) chooses nothing (a dropped or
+ * padded token, an expert of another device); a token without a choice gets
+ * zeros. A token may choose one expert more than once. swiglu_mlp_moe_infer
+ * is the router and the experts in one call (the choices stay in the
+ * workspace). 1 <= k <= min(E, 32), E <= 1024, D and H as above.
+ *
+ * 4-bit weights (bf16 and fp16 storage): W[n][k] = scale[n][k / group] *
+ * (code[n][k] - zero[n][k / group]), codes 0..15, group 32, 64 or 128
+ * dividing K, N a multiple of 8; zero = 8 where there are no zero points.
+ * The kernels read a packed layout that swiglu_mlp_w4_pack writes once from
+ * codes [X][N][K/2] (two to a byte, the even k in the low half), scales
+ * [X][N][K/group] in the storage type and zeros [X][N][K/group] bytes (or
+ * NULL). swiglu_mlp_w4_quantize makes codes, scales and, where zeros is not
+ * NULL, zero points from a 16-bit W [X][N][K]; swiglu_mlp_w4_dequantize
+ * writes the packed weight back as rows (for a long prompt, whose products
+ * are bound by arithmetic). Products are exact per code and scaled in fp32:
+ * no weight is rounded. */
+#define SWIGLU_FEW_MAX_T 65536
+
+typedef struct {
+  const void* data; /* swiglu_mlp_w4_bytes() bytes written by swiglu_mlp_w4_pack */
+  int64_t experts;  /* matrices: 1 for a dense weight */
+  int64_t N, K;     /* out_features, in_features */
+  int32_t group;
+  int32_t has_zeros;
+} swiglu_w4_t;
+
+int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, int64_t T,
+                         int64_t D, int64_t E, int64_t k, int renorm, int dtype, hipStream_t stream);
+
+/* Bytes of a mixture's workspace: the A plane [T k, H] and the router's
+ * weights and ids, each 256-byte aligned. Contents on entry do not matter;
+ * calls that share one must be stream-ordered. 0 on bad args. */
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t H, int64_t k, int dtype);
+
+int swiglu_mlp_moe_experts(const void* X, const float* weights, const int32_t* ids, const void* Wg,
+                           const void* Wu, const void* Wd, void* Y, void* workspace,
+                           size_t workspace_bytes, int64_t T, int64_t D, int64_t H, int64_t E,
+                           int64_t k, int dtype, hipStream_t stream);
+int swiglu_mlp_moe_infer(const void* X, const void* Wr, const void* Wg, const void* Wu, const void* Wd,
+                         void* Y, void* workspace, size_t workspace_bytes, int64_t T, int64_t D,
+                         int64_t H, int64_t E, int64_t k, int renorm, int dtype, hipStream_t stream);
+int swiglu_mlp_moe_experts_w4(const void* X, const float* weights, const int32_t* ids,
+                              const swiglu_w4_t* Wg, const swiglu_w4_t* Wu, const swiglu_w4_t* Wd,
+                              void* Y, void* workspace, size_t workspace_bytes, int64_t T, int64_t k,
+                              int dtype, hipStream_t stream);
+int swiglu_mlp_moe_infer_w4(const void* X, const void* Wr, const swiglu_w4_t* Wg,
+                            const swiglu_w4_t* Wu, const swiglu_w4_t* Wd, void* Y, void* workspace,
+                            size_t workspace_bytes, int64_t T, int64_t k, int renorm, int dtype,
+                            hipStream_t stream);
+
+/* Bytes of a packed weight (0 on bad args). */
+size_t swiglu_mlp_w4_bytes(int64_t experts, int64_t N, int64_t K, int group, int has_zeros);
+int swiglu_mlp_w4_quantize(const void* W, void* codes, void* scales, void* zeros, int64_t experts,
+                           int64_t N, int64_t K, int group, int dtype, hipStream_t stream);
+int swiglu_mlp_w4_pack(const void* codes, const void* scales, const void* zeros, void* data,
+                       int64_t experts, int64_t N, int64_t K, int group, hipStream_t stream);
+int swiglu_mlp_w4_dequantize(const swiglu_w4_t* w, void* W, int dtype, hipStream_t stream);
+
+/* Y [T, N] = X [T, K] W^T. One launch, no workspace. */
+int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T, int dtype,
+                         hipStream_t stream);
+
+/* The dense block with 4-bit weights, two launches; workspace: A [T, H]. */
+size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t H, int dtype);
+int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* Wg, const swiglu_w4_t* Wu,
+                        const swiglu_w4_t* Wd, void* Y, void* workspace, size_t workspace_bytes,
+                        int64_t T, int dtype, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* swiglu_mlp_status_string(int status);
 
@@ -211,6 +299,8 @@ const char* swiglu_mlp_status_string(int status);
  *   4 [dWg | dWu] = X^T [dG | dU]      5 dI single accumulator
  *   6 no-grad gate/up (A only)         7 no-grad down projection
  *   8 stages 3 + 2 in one launch       9 stages 4 + 5 in one launch
+ *  10 router                          11 few-token gate/up (experts, 4-bit)
+ *  12 few-token down projection or 4-bit product
  * (bf16/fp16 run every stage as its own launch; in fp32 with T > 512 the
  * backward runs as launches 8 and 9, where the long-K weight-gradient tiles
  * are dispatched first and the short tiles of the other stage fill in
@@ -221,7 +311,7 @@ const char* swiglu_mlp_status_string(int status);
  * waits for the recorded events and writes, for each of the first `n` stages,
  * the summed milliseconds to ms[s] and the launch count to count[s], then
  * disables recording. Not thread-safe; meant for a benchmark's timed loop. */
-#define SWIGLU_NUM_STAGES 10
+#define SWIGLU_NUM_STAGES 13
 int swiglu_mlp_timer_start(int capacity);
 int swiglu_mlp_timer_stop(double* ms, int* count, int n);
 
