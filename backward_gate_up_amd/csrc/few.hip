@@ -30,7 +30,9 @@ extern template int run_route<Fp32>(const Args&, hipStream_t);
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-static bool ld_ok(int64_t v, size_t e) { return v > 0 && (v & 7) == 0 && v <= max_ld(e); }
+// The kernels address a chunk's up to 64 * 32 rows of either width with 32-bit
+// byte offsets.
+static bool ld_ok(int64_t v) { return v > 0 && (v & 7) == 0 && v <= SWIGLU_FEW_MAX_D; }
 
 static int check_few(int64_t T, int64_t E, int64_t k) {
   if (T < 0 || T > SWIGLU_FEW_MAX_T) return SWIGLU_ERR_SHAPE;
@@ -40,7 +42,7 @@ static int check_few(int64_t T, int64_t E, int64_t k) {
 
 static int check_group(int64_t N, int64_t K, int group) {
   if (group != 32 && group != 64 && group != 128) return SWIGLU_ERR_SHAPE;
-  if (!ld_ok(N, 2) || !ld_ok(K, 2) || K % group) return SWIGLU_ERR_SHAPE;
+  if (!ld_ok(N) || !ld_ok(K) || K % group) return SWIGLU_ERR_SHAPE;
   return SWIGLU_OK;
 }
 static int check_w4(const swiglu_w4_t* w) {
@@ -162,7 +164,7 @@ static int moe_rows(const void* X, const void* Wr, bool routed, const float* wei
                     int64_t D, int64_t H, int64_t E, int64_t k, int renorm, int dtype, hipStream_t stream) {
   const size_t e = elt_bytes(dtype);
   if (!e) return SWIGLU_ERR_DTYPE;
-  if (!ld_ok(D, e) || !ld_ok(H, e)) return SWIGLU_ERR_SHAPE;
+  if (!ld_ok(D) || !ld_ok(H)) return SWIGLU_ERR_SHAPE;
   int rc = check_few(T, E, k);
   if (rc) return rc;
   if (routed && !Wr) return SWIGLU_ERR_NULL;
@@ -216,7 +218,7 @@ int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t*
                          int64_t k, int renorm, int dtype, hipStream_t stream) {
   const size_t e = elt_bytes(dtype);
   if (!e) return SWIGLU_ERR_DTYPE;
-  if (!ld_ok(D, e)) return SWIGLU_ERR_SHAPE;
+  if (!ld_ok(D)) return SWIGLU_ERR_SHAPE;
   int rc = check_few(T, E, k);
   if (rc) return rc;
   const Range in[] = {{X, (size_t)T * D * e}, {Wr, (size_t)E * D * e}};
@@ -231,7 +233,7 @@ int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t*
 
 size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t H, int64_t k, int dtype) {
   const size_t e = elt_bytes(dtype);
-  if (!e || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(H, e) || k < 1 || k > few::kMaxTopK) return 0;
+  if (!e || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(H) || k < 1 || k > few::kMaxTopK) return 0;
   return moe_plan(T, H, k, e).total;
 }
 
@@ -344,7 +346,7 @@ int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T
 
 size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t H, int dtype) {
   const size_t e = elt_bytes(dtype);
-  if (e != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(H, e)) return 0;
+  if (e != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(H)) return 0;
   return (size_t)T * H * e;
 }
 

@@ -53,6 +53,7 @@ struct Args {
   const int* ids;    // [T, k]; nullptr: dense
   const float* wts;  // [T, k]; nullptr: dense
   int T, k, E, N, K;
+  uint32_t kinv;     // ceil(65536 / k): p / k = p * kinv >> 16 for a chunk's p < 2048, k <= 32
 };
 
 // ---- MFMA steps -------------------------------------------------------------
@@ -77,96 +78,70 @@ __device__ __forceinline__ f32x4_t step_mfma(u32x4_t a, u32x4_t w, f32x4_t c) {
 }
 
 __device__ __forceinline__ u32x4_t load16(const char* p) { return *(const u32x4_t*)p; }
-// weights are read once: keep them from displacing the tokens in L2
-__device__ __forceinline__ u32x4_t load16_once(const char* p) {
-  return __builtin_nontemporal_load((const u32x4_t*)p);
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
 // ---- weight streams ---------------------------------------------------------
-// stream<>::run adds the products of steps [s0, s1) to acc[n][m] (NT weight
-// blocks x MT token blocks of 16). xp[m]: the lane's token row plus its 16-byte
-// chunk; double-buffered blocks of U steps, so U .. 2 U steps of every stream
-// are in flight. Loads past s1 repeat the last step (in range, not used).
+// A stream adds the products of K steps [s0, s1) to acc[n][m]: NT weight blocks
+// of 16 rows x MT token blocks of 16. A ring of U steps stays in flight: each
+// step's registers are refilled as soon as its products are issued. Offsets
+// past the end of the run or of K go out of the buffers' range, so those loads
+// return zeros without a memory access: no remainder code, and neither the next
+// row nor a NaN there is multiplied in.
+//
+// Tokens: rows of K elements at row_off[m] from x (bytes).
 
 // Rows of 16-bit or fp32 weights; a step is 64 bytes of K.
 // R: registers a lane may hold (512 per SIMD lane over its waves).
 template <class E, int NT, int MT, int R>
 struct RowStream {
-  static constexpr int kFit = (R - 24 - 8 * NT * MT) / (8 * (NT + MT));  // two buffers, sums, addresses
-  static constexpr int U = kFit >= 8 ? 8 : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
-  const char* wp[NT];
-  int full;      // steps that lie wholly inside K
-  bool in_tail;  // this lane's chunk of the partial last step lies inside K
+  static constexpr int kFit = (R - 40 - 4 * NT * MT) / (4 * (NT + MT));
+  static constexpr int U = kFit >= 16 ? 16 : kFit >= 8 ? 8 : 4;
+  __amdgpu_buffer_rsrc_t w[NT], x;
+  uint32_t w_off, x_off[MT];
+  int kb;  // bytes of K
 
-  __device__ __forceinline__ void init(const Weight* const (&w)[NT], int e, int row0, int N, int K, int lane) {
-    const int row = min(row0 + (lane & 15), N - 1);
-    const int64_t kb = (int64_t)K * E::kBytes;
+  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, int N, int K, const char* xb,
+                                       const uint32_t (&row_off)[MT], uint32_t x_bytes, int lane) {
+    kb = K * E::kBytes;
+    const int rows = min(16, N - row0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) wp[n] = w[n]->w + (int64_t)e * w[n]->expert + (int64_t)row * kb + (lane >> 4) * 16;
-    full = (int)(kb >> 6);
-    in_tail = (lane >> 4) * 16 < (int)(kb & 63);
+    for (int n = 0; n < NT; ++n)
+      w[n] = make_rsrc32(wt[n]->w + (int64_t)e * wt[n]->expert + (int64_t)row0 * kb, rows * kb);
+    x = make_rsrc32(xb, (int)x_bytes);
+    w_off = (uint32_t)min(lane & 15, rows - 1) * (uint32_t)kb;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x_off[m] = row_off[m];
   }
-  static __device__ __forceinline__ int steps(int K) { return (int)(((int64_t)K * E::kBytes + 63) >> 6); }
+  static __device__ __forceinline__ int steps(int K) { return (K * E::kBytes + 63) >> 6; }
 
   struct Buf {
-    u32x4_t w[U][NT], x[U][MT];
+    u32x4_t w[NT], x[MT];
   };
-  __device__ __forceinline__ void load(Buf& b, const char* const (&xp)[MT], int s, int last) const {
+  __device__ __forceinline__ void load(Buf& b, int off, int end) const {
+    const bool in = off < end;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t off = (int64_t)min(s + u, last) * 64;
+    for (int n = 0; n < NT; ++n) b.w[n] = load16(w[n], in ? w_off + off : kOOB);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) b.w[u][n] = load16_once(wp[n] + off);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) b.x[u][m] = load16(xp[m] + off);
-    }
+    for (int m = 0; m < MT; ++m) b.x[m] = load16(x, in ? x_off[m] + off : kOOB);
   }
-  __device__ __forceinline__ void compute(const Buf& b, f32x4_t (&acc)[NT][MT], int left) const {
+  __device__ __forceinline__ void run(f32x4_t (&acc)[NT][MT], int s0, int s1, int lane) const {
+    const int end = min(s1 * 64, kb);
+    int off = s0 * 64 + (lane >> 4) * 16;
+    Buf b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) {
+    for (int u = 0; u < U; ++u) load(b[u], off + 64 * u, end);
+    for (int s = s0; s < s1; s += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[n][m] = step_mfma<E>(b.x[u][m], b.w[u][n], acc[n][m]);
+          for (int m = 0; m < MT; ++m) acc[n][m] = step_mfma<E>(b[u].x[m], b[u].w[n], acc[n][m]);
+        load(b[u], off + 64 * (U + u), end);
       }
-  }
-  __device__ __forceinline__ void run(f32x4_t (&acc)[NT][MT], const char* const (&xp)[MT], int s0, int s1) const {
-    const int e1 = min(s1, full), n = e1 - s0;
-    if (n > 0) {
-      Buf b0, b1;
-      load(b0, xp, s0, e1 - 1);
-      int s = s0;
-      for (; s + 2 * U <= e1; s += 2 * U) {
-        load(b1, xp, s + U, e1 - 1);
-        compute(b0, acc, U);
-        if (s + 2 * U < e1) load(b0, xp, s + 2 * U, e1 - 1);
-        compute(b1, acc, U);
-      }
-      if (s < e1) {
-        if (s + U < e1) load(b1, xp, s + U, e1 - 1);
-        compute(b0, acc, e1 - s);
-        if (s + U < e1) compute(b1, acc, e1 - s - U);
-      }
-    }
-    if (s1 > full && s1 > s0) {
-      // the partial last step: chunks past K are zero on both sides, so
-      // neither the next row nor a NaN there is multiplied in
-      const int64_t off = in_tail ? (int64_t)full * 64 : 0;
-      const u32x4_t zero{0, 0, 0, 0};
-      u32x4_t w[NT], x[MT];
-#pragma unroll
-      for (int n2 = 0; n2 < NT; ++n2) w[n2] = load16(in_tail ? wp[n2] + off : wp[n2] - 16 * ((threadIdx.x & 63) >> 4));
-#pragma unroll
-      for (int m = 0; m < MT; ++m) x[m] = load16(in_tail ? xp[m] + off : xp[m] - 16 * ((threadIdx.x & 63) >> 4));
-#pragma unroll
-      for (int n2 = 0; n2 < NT; ++n2) w[n2] = in_tail ? w[n2] : zero;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        x[m] = in_tail ? x[m] : zero;
-#pragma unroll
-        for (int n2 = 0; n2 < NT; ++n2) acc[n2][m] = step_mfma<E>(x[m], w[n2], acc[n2][m]);
-      }
+      off += 64 * U;
     }
   }
 };
@@ -181,59 +156,60 @@ struct RowStream {
 // group's sum, 2^-19 of it in bf16: far below the storage type's half step.
 template <class E, int G, int NT, int MT, int R>
 struct W4Stream {
-  static constexpr int U = R < 256 || MT == 4 ? 1 : 2;
   static constexpr int GP = 128 / G;  // groups per tile
+  static constexpr int U = R < 256 || MT > 1 ? 1 : 2;
   static constexpr float kOff = std::is_same<E, Bf16>::value ? 128.0f : 64.0f;
-  const u32x4_t* wp[NT];
-  const char* sp[NT];
-  const uint16_t* zp[NT];
-  int full;
-  int tail_k;  // K elements in the partial last tile
+  __amdgpu_buffer_rsrc_t w[NT], s[NT], z[NT], x;
+  uint32_t x_off[MT];
+  int kb, lane;
+  bool has_zero;
 
-  __device__ __forceinline__ void init(const Weight* const (&w)[NT], int e, int row0, int N, int K, int lane) {
+  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, int N, int K, const char* xb,
+                                       const uint32_t (&row_off)[MT], uint32_t x_bytes, int ln) {
     const int nkt = steps(K);
+    kb = K * 2;
+    lane = ln;
+    has_zero = wt[0]->zero != nullptr;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int64_t tile = (int64_t)e * w[n]->expert + (int64_t)(row0 >> 4) * nkt;
-      wp[n] = (const u32x4_t*)w[n]->w + tile * 64 + lane;
-      sp[n] = w[n]->scale + (tile * 16 + (lane & 15)) * (GP * 2);
-      zp[n] = w[n]->zero ? (const uint16_t*)w[n]->zero + tile * 16 + (lane & 15) : nullptr;
+      const int64_t tile = (int64_t)e * wt[n]->expert + (int64_t)(row0 >> 4) * nkt;
+      w[n] = make_rsrc32(wt[n]->w + tile * 1024, nkt * 1024);
+      s[n] = make_rsrc32(wt[n]->scale + tile * (32 * GP), nkt * (32 * GP));
+      z[n] = make_rsrc32(wt[n]->zero + tile * 32, has_zero ? nkt * 32 : 0);
     }
-    full = K >> 7;
-    tail_k = (K & 127) - (lane >> 4) * 8;
+    x = make_rsrc32(xb, (int)x_bytes);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x_off[m] = row_off[m];
   }
   static __device__ __forceinline__ int steps(int K) { return (K + 127) >> 7; }
 
   struct Buf {
-    u32x4_t w[U][NT], x[U][4][MT];
-    uint32_t s[U][NT][GP == 4 ? 2 : 1];
-    uint32_t z[U][NT];
+    u32x4_t w[NT], x[4][MT];
+    uint32_t s[NT][GP == 4 ? 2 : 1];
+    uint32_t z[NT];
   };
-  __device__ __forceinline__ void load_w(Buf& b, int u, int64_t s) const {
+  __device__ __forceinline__ void load(Buf& b, int t, int end) const {
+    const bool in = t < end;
+    const uint32_t row = lane & 15;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      b.w[u][n] = __builtin_nontemporal_load(wp[n] + s * 64);
-      const char* p = sp[n] + s * (16 * GP * 2);
-      if constexpr (GP == 1) b.s[u][n][0] = *(const uint16_t*)p;
-      else if constexpr (GP == 2) b.s[u][n][0] = *(const uint32_t*)p;
+      b.w[n] = load16(w[n], in ? (uint32_t)t * 1024 + lane * 16 : kOOB);
+      const uint32_t so = in ? ((uint32_t)t * 16 + row) * (2 * GP) : kOOB;
+      if constexpr (GP == 1) b.s[n][0] = __builtin_amdgcn_raw_buffer_load_b16(s[n], so, 0, 0);
+      else if constexpr (GP == 2) b.s[n][0] = __builtin_amdgcn_raw_buffer_load_b32(s[n], so, 0, 0);
       else {
-        const u32x2_t v = *(const u32x2_t*)p;
-        b.s[u][n][0] = v[0];
-        b.s[u][n][1] = v[1];
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(s[n], so, 0, 0);
+        b.s[n][0] = v[0];
+        b.s[n][1] = v[1];
       }
-      b.z[u][n] = zp[n] ? zp[n][s * 16] : 0x8888u;
+      b.z[n] = 0x8888u;
+      if (has_zero) b.z[n] = __builtin_amdgcn_raw_buffer_load_b16(z[n], in ? ((uint32_t)t * 16 + row) * 2 : kOOB, 0, 0);
     }
-  }
-  __device__ __forceinline__ void load(Buf& b, const char* const (&xp)[MT], int s, int last) const {
+    const int off = t * 256 + (lane >> 4) * 16, xe = in ? kb : 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t = min(s + u, last);
-      load_w(b, u, t);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) b.x[u][i][m] = load16(xp[m] + t * 256 + i * 64);
-    }
+      for (int m = 0; m < MT; ++m) b.x[i][m] = load16(x, off + 64 * i < xe ? x_off[m] + off + 64 * i : kOOB);
   }
   // eight codes of one dword as the MFMA operand OFF + q
   static __device__ __forceinline__ u32x4_t widen(uint32_t v) {
@@ -253,25 +229,25 @@ struct W4Stream {
     const uint32_t h = (s[g >> 1] >> ((g & 1) * 16)) & 0xffffu;
     return E::to_f32(__builtin_bit_cast(typename E::elem, (uint16_t)h));
   }
-  __device__ __forceinline__ void tile(const Buf& b, int u, f32x4_t (&acc)[NT][MT]) const {
+  __device__ __forceinline__ void tile(const Buf& b, f32x4_t (&acc)[NT][MT]) const {
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
       f32x4_t part[NT][MT] = {}, xs[MT] = {};
 #pragma unroll
       for (int i = 4 / GP * g; i < 4 / GP * (g + 1); ++i) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) xs[m] = step_mfma<E>(b.x[u][i][m], ones(), xs[m]);
+        for (int m = 0; m < MT; ++m) xs[m] = step_mfma<E>(b.x[i][m], ones(), xs[m]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const u32x4_t q = widen(b.w[u][n][i]);
+          const u32x4_t q = widen(b.w[n][i]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) part[n][m] = step_mfma<E>(b.x[u][i][m], q, part[n][m]);
+          for (int m = 0; m < MT; ++m) part[n][m] = step_mfma<E>(b.x[i][m], q, part[n][m]);
         }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float sc = scale_of(b.s[u][n], g);
-        const float off = kOff + (float)((b.z[u][n] >> (4 * g)) & 15u);
+        const float sc = scale_of(b.s[n], g);
+        const float off = kOff + (float)((b.z[n] >> (4 * g)) & 15u);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -279,43 +255,17 @@ struct W4Stream {
       }
     }
   }
-  __device__ __forceinline__ void compute(const Buf& b, f32x4_t (&acc)[NT][MT], int left) const {
+  __device__ __forceinline__ void run(f32x4_t (&acc)[NT][MT], int s0, int s1, int) const {
+    Buf b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) tile(b, u, acc);
-  }
-  __device__ __forceinline__ void run(f32x4_t (&acc)[NT][MT], const char* const (&xp)[MT], int s0, int s1) const {
-    const int e1 = min(s1, full), n = e1 - s0;
-    if (n > 0) {
-      Buf b0, b1;
-      load(b0, xp, s0, e1 - 1);
-      int s = s0;
-      for (; s + 2 * U <= e1; s += 2 * U) {
-        load(b1, xp, s + U, e1 - 1);
-        compute(b0, acc, U);
-        if (s + 2 * U < e1) load(b0, xp, s + 2 * U, e1 - 1);
-        compute(b1, acc, U);
+    for (int u = 0; u < U; ++u) load(b[u], s0 + u, s1);
+    for (int t = s0; t < s1; t += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Buf c = b[u];
+        load(b[u], t + U + u, s1);
+        tile(c, acc);
       }
-      if (s < e1) {
-        if (s + U < e1) load(b1, xp, s + U, e1 - 1);
-        compute(b0, acc, e1 - s);
-        if (s + U < e1) compute(b1, acc, e1 - s - U);
-      }
-    }
-    if (s1 > full && s1 > s0) {
-      // the partial last tile: token chunks past K are zero (the codes and
-      // scales there are zero by the layout)
-      Buf b;
-      load_w(b, 0, full);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const bool in = 32 * i < tail_k;
-          const u32x4_t v = load16(in ? xp[m] + (int64_t)full * 256 + i * 64 : xp[m] - 16 * ((threadIdx.x & 63) >> 4));
-          b.x[0][i][m] = in ? v : u32x4_t{0, 0, 0, 0};
-        }
-      tile(b, 0, acc);
     }
   }
 };
@@ -395,20 +345,20 @@ template <class E, int FMT, int NW, int MT>
 __device__ __forceinline__ void gateup_block(const Args& g, int e, int row0, int t0, const int16_t* list, int n,
                                              float* red) {
   using S = typename StreamOf<E, FMT, 2, MT, 256>::type;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const char* xp[MT];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t row[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int i = min(16 * m + (lane & 15), n - 1);
-    const int t = t0 + (list ? list[i] / g.k : i);
-    xp[m] = g.x + (int64_t)t * g.K * E::kBytes + (lane >> 4) * 16;
+    row[m] = (uint32_t)(list ? (list[i] * g.kinv) >> 16 : i) * (uint32_t)(g.K * E::kBytes);
   }
   S s;
   const Weight* const w[2] = {&g.w0, &g.w1};
-  s.init(w, e, row0, g.N, g.K, lane);
+  s.init(w, e, row0, g.N, g.K, g.x + (int64_t)t0 * g.K * E::kBytes, row, (uint32_t)(min(kChunk, g.T - t0) * g.K) * E::kBytes,
+         lane);
   const int steps = S::steps(g.K), per = (steps + NW - 1) / NW;
   f32x4_t acc[2][MT] = {};
-  s.run(acc, xp, wave * per, min(steps, (wave + 1) * per));
+  s.run(acc, wave * per, min(steps, (wave + 1) * per), lane);
   // the waves' sums meet in LDS; thread -> (token row, hidden column), waves added in order
 #pragma unroll
   for (int n2 = 0; n2 < 2; ++n2)
@@ -484,26 +434,27 @@ template <class E, int FMT, int NW, int MT>
 __device__ __forceinline__ void down_block(const Args& g, DownShared<NW>& sh, int e, int row0, int t0, int n, int s0,
                                            int s1) {
   using S = typename StreamOf<E, FMT, 1, MT, NW == 16 ? 128 : 256>::type;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool routed = g.ids != nullptr;
   const int16_t* list = sh.list[wave];
-  const char* xp[MT];
+  uint32_t row[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int i = min(16 * m + (lane & 15), n - 1);
-    const int64_t p = routed ? (int64_t)t0 * g.k + list[i] : t0 + i;
-    xp[m] = g.x + p * g.K * E::kBytes + (lane >> 4) * 16;
+    row[m] = (uint32_t)(routed ? list[i] : i) * (uint32_t)(g.K * E::kBytes);
   }
   S s;
   const Weight* const w[1] = {&g.w0};
-  s.init(w, e, row0, g.N, g.K, lane);
+  s.init(w, e, row0, g.N, g.K, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, row,
+         (uint32_t)(min(kChunk, g.T - t0) * g.k * g.K) * E::kBytes, lane);
   f32x4_t acc[1][MT] = {};
-  s.run(acc, xp, s0, s1);
+  s.run(acc, s0, s1, lane);
   float* y = sh.y[wave];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     // one group of 16 lanes (4 token rows) at a time: a token listed twice
     // for one expert is then added twice, in order
+#pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       if ((lane >> 4) == q) {
 #pragma unroll
@@ -511,7 +462,7 @@ __device__ __forceinline__ void down_block(const Args& g, DownShared<NW>& sh, in
           const int i = 16 * m + 4 * q + j;
           if (i < n) {
             const int p = routed ? list[i] : i;
-            float* at = y + (routed ? p / g.k : p) * 16 + (lane & 15);
+            float* at = y + (routed ? (p * g.kinv) >> 16 : (uint32_t)p) * 16 + (lane & 15);
             *at += (routed ? sh.wts[p] : 1.0f) * acc[0][m][j];
           }
         }
@@ -599,7 +550,7 @@ static int launch_down(const Args& g, hipStream_t s) {
 // y = x W^T (dense), or the down projection of a block.
 template <class E, int FMT>
 int run_down(const Call& c, const char* x, int64_t K, int64_t N) {
-  const Args g{x, c.wd, c.wd, c.y, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K};
+  const Args g{x, c.wd, c.wd, c.y, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k};
   const int64_t groups = (N + 15) / 16 * ((c.T + kChunk - 1) / kChunk);
   if (groups >= 1024) return launch_down<E, FMT, 4>(g, c.stream);
   if (groups >= 512 || c.T > 16) return launch_down<E, FMT, 8>(g, c.stream);
@@ -608,7 +559,7 @@ int run_down(const Call& c, const char* x, int64_t K, int64_t N) {
 
 template <class E, int FMT>
 int run_block(const Call& c) {
-  const Args g{c.x, c.wg, c.wu, c.a, c.ids, c.wts, (int)c.T, c.k, c.E, (int)c.H, (int)c.D};
+  const Args g{c.x, c.wg, c.wu, c.a, c.ids, c.wts, (int)c.T, c.k, c.E, (int)c.H, (int)c.D, (65535u + c.k) / c.k};
   const int64_t pairs = (c.T < kChunk ? c.T : kChunk) * c.k;
   const int slots = c.ids ? (int)(pairs < c.E ? pairs : c.E) : 1;
   const int64_t groups = (c.H + 15) / 16 * slots * ((c.T + kChunk - 1) / kChunk);

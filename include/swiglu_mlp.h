@@ -224,7 +224,8 @@ int swiglu_mlp_infer_noalloc(const void* X, const void* Wg, const void* Wu, cons
  * padded token, an expert of another device); a token without a choice gets
  * zeros. A token may choose one expert more than once. swiglu_mlp_moe_infer
  * is the router and the experts in one call (the choices stay in the
- * workspace). 1 <= k <= min(E, 32), E <= 1024, D and H as above.
+ * workspace). 1 <= k <= min(E, 32), E <= 1024, D and H multiples of 8 up to
+ * SWIGLU_FEW_MAX_D.
  *
  * 4-bit weights (bf16 and fp16 storage): W[n][k] = scale[n][k / group] *
  * (code[n][k] - zero[n][k / group]), codes 0..15, group 32, 64 or 128
@@ -238,6 +239,7 @@ int swiglu_mlp_infer_noalloc(const void* X, const void* Wg, const void* Wu, cons
  * are bound by arithmetic). Products are exact per code and scaled in fp32:
  * no weight is rounded. */
 #define SWIGLU_FEW_MAX_T 65536
+#define SWIGLU_FEW_MAX_D 131072
 
 typedef struct {
   const void* data; /* swiglu_mlp_w4_bytes() bytes written by swiglu_mlp_w4_pack */
