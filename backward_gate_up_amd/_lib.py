@@ -73,7 +73,7 @@ def lib():
     w4 = ctypes.POINTER(W4)
     for name, args, res in (
             ("moe_route", [vp] * 4 + [i64] * 4 + [i32, i32, vp], i32),
-            ("moe_workspace_bytes", [i64] * 3 + [i32], sz),
+            ("moe_workspace_bytes", [i64] * 4 + [i32], sz),
             ("moe_experts", [vp] * 8 + [sz] + [i64] * 5 + [i32, vp], i32),
             ("moe_infer", [vp] * 7 + [sz] + [i64] * 5 + [i32, i32, vp], i32),
             ("moe_experts_w4", [vp] * 3 + [w4] * 3 + [vp, vp, sz, i64, i64, i32, vp], i32),
@@ -83,7 +83,7 @@ def lib():
             ("w4_pack", [vp] * 4 + [i64] * 3 + [i32, vp], i32),
             ("w4_dequantize", [w4, vp, i32, vp], i32),
             ("w4_linear", [vp, w4, vp, i64, i32, vp], i32),
-            ("w4_infer_workspace_bytes", [i64, i64, i32], sz),
+            ("w4_infer_workspace_bytes", [i64] * 3 + [i32], sz),
             ("w4_infer", [vp] + [w4] * 3 + [vp, vp, sz, i64, i32, vp], i32)):
         f = getattr(L, "swiglu_mlp_" + name)
         f.argtypes, f.restype = args, res

@@ -10,7 +10,7 @@ namespace swiglu {
 namespace few {
 #define SWIGLU_DECLARE_FEW(E, FMT)                     \
   extern template int run_block<E, FMT>(const Call&);  \
-  extern template int run_down<E, FMT>(const Call&, const char*, int64_t, int64_t);
+  extern template int run_linear<E, FMT>(const Call&);
 SWIGLU_DECLARE_FEW(Bf16, 32)
 SWIGLU_DECLARE_FEW(Bf16, 64)
 SWIGLU_DECLARE_FEW(Bf16, 128)
@@ -55,12 +55,10 @@ static Range w4_range(const swiglu_w4_t* w) {
   return {w->data, w4::layout(w->experts, w->N, w->K, w->group, w->has_zeros != 0).total};
 }
 static few::Weight w4_weight(const swiglu_w4_t* w) {
-  const w4::Layout l = w4::layout(w->experts, w->N, w->K, w->group, w->has_zeros != 0);
-  const char* d = (const char*)w->data;
-  return {d, d + l.scales, w->has_zeros ? d + l.zeros : nullptr, l.tiles};
+  return {(const char*)w->data, w4::layout(w->experts, w->N, w->K, w->group, w->has_zeros != 0).expert};
 }
 static few::Weight row_weight(const void* w, int64_t N, int64_t K, size_t e) {
-  return {(const char*)w, nullptr, nullptr, (int64_t)(N * K * e)};
+  return {(const char*)w, (int64_t)(N * K * e)};
 }
 
 static int run_block_for(int dtype, int group, const few::Call& c) {
@@ -74,15 +72,11 @@ static int run_block_for(int dtype, int group, const few::Call& c) {
     return group == 32 ? run_block<Bf16, 32>(c) : group == 64 ? run_block<Bf16, 64>(c) : run_block<Bf16, 128>(c);
   return group == 32 ? run_block<Fp16, 32>(c) : group == 64 ? run_block<Fp16, 64>(c) : run_block<Fp16, 128>(c);
 }
-static int run_down_for(int dtype, int group, const few::Call& c, const char* x, int64_t K, int64_t N) {
+static int run_linear_for(int dtype, int group, const few::Call& c) {
   using namespace few;
   if (dtype == SWIGLU_BF16)
-    return group == 32   ? run_down<Bf16, 32>(c, x, K, N)
-           : group == 64 ? run_down<Bf16, 64>(c, x, K, N)
-                         : run_down<Bf16, 128>(c, x, K, N);
-  return group == 32   ? run_down<Fp16, 32>(c, x, K, N)
-         : group == 64 ? run_down<Fp16, 64>(c, x, K, N)
-                       : run_down<Fp16, 128>(c, x, K, N);
+    return group == 32 ? run_linear<Bf16, 32>(c) : group == 64 ? run_linear<Bf16, 64>(c) : run_linear<Bf16, 128>(c);
+  return group == 32 ? run_linear<Fp16, 32>(c) : group == 64 ? run_linear<Fp16, 64>(c) : run_linear<Fp16, 128>(c);
 }
 
 // Weights and ids of the router are read and written one word at a time.
@@ -105,14 +99,14 @@ static int check_alias(const Range* out, int no, const Range* in, int ni) {
   return SWIGLU_OK;
 }
 
-// A mixture's workspace: the A plane, then the router's weights and ids.
+// A mixture's workspace: the block's, then the router's weights and ids.
 struct MoePlan {
   size_t wts, ids, total;
 };
-static MoePlan moe_plan(int64_t T, int64_t H, int64_t k, size_t e) {
+static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
   const size_t p = (size_t)T * k;
   MoePlan m;
-  m.wts = up256(p * H * e);
+  m.wts = few::block_plan(T, D, H, k, e).total;
   m.ids = m.wts + up256(p * 4);
   m.total = m.ids + up256(p * 4);
   return m;
@@ -124,7 +118,7 @@ static int moe_call(const void* X, const void* Wr, const float* weights, const i
                     few::Call& c, void* Y, void* ws, size_t ws_bytes, int64_t T, int64_t k, int renorm, int dtype,
                     int group, hipStream_t stream) {
   const size_t e = elt_bytes(dtype);
-  const MoePlan m = moe_plan(T, c.H, k, e);
+  const MoePlan m = moe_plan(T, c.D, c.H, k, e);
   const size_t p4 = (size_t)T * k * 4;
   const bool routed = Wr != nullptr;
   const Range in[] = {{X, (size_t)T * c.D * e}, w[0], w[1], w[2], {Wr, routed ? (size_t)c.E * c.D * e : 0},
@@ -139,7 +133,7 @@ static int moe_call(const void* X, const void* Wr, const float* weights, const i
   if (T == 0) return SWIGLU_OK;
   c.x = (const char*)X;
   c.y = (char*)Y;
-  c.a = (char*)ws;
+  c.ws = (char*)ws;
   c.T = T;
   c.k = (int)k;
   c.stream = stream;
@@ -187,7 +181,8 @@ static int moe_w4(const void* X, const void* Wr, bool routed, const float* weigh
   int rc;
   if ((rc = check_w4(wg)) || (rc = check_w4(wu)) || (rc = check_w4(wd))) return rc;
   if (wu->N != wg->N || wu->K != wg->K || wd->N != wg->K || wd->K != wg->N || wu->experts != wg->experts ||
-      wd->experts != wg->experts || wu->group != wg->group || wd->group != wg->group)
+      wd->experts != wg->experts || wu->group != wg->group || wd->group != wg->group || !wu->has_zeros != !wg->has_zeros ||
+      !wd->has_zeros != !wg->has_zeros)
     return SWIGLU_ERR_SHAPE;
   if ((rc = check_few(T, wg->experts, k))) return rc;
   if (routed && !Wr) return SWIGLU_ERR_NULL;
@@ -198,6 +193,7 @@ static int moe_w4(const void* X, const void* Wr, bool routed, const float* weigh
   c.D = wg->K;
   c.H = wg->N;
   c.E = wg->experts;
+  c.zeros = wg->has_zeros != 0;
   const Range w[3] = {w4_range(wg), w4_range(wu), w4_range(wd)};
   return moe_call(X, routed ? Wr : nullptr, weights, ids, w, c, Y, ws, ws_bytes, T, k, renorm, dtype, wg->group,
                   stream);
@@ -231,10 +227,10 @@ int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t*
   return route::run_route<Fp32>(r, stream);
 }
 
-size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t H, int64_t k, int dtype) {
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t k, int dtype) {
   const size_t e = elt_bytes(dtype);
-  if (!e || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(H) || k < 1 || k > few::kMaxTopK) return 0;
-  return moe_plan(T, H, k, e).total;
+  if (!e || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(D) || !ld_ok(H) || k < 1 || k > few::kMaxTopK) return 0;
+  return moe_plan(T, D, H, k, e).total;
 }
 
 int swiglu_mlp_moe_experts(const void* X, const float* weights, const int32_t* ids, const void* Wg, const void* Wu,
@@ -300,7 +296,7 @@ int swiglu_mlp_w4_pack(const void* codes, const void* scales, const void* zeros,
   const Range out[] = {{data, l.total}};
   if ((rc = check_ptrs(in, 3)) || (rc = check_ptrs(out, 1)) || (rc = check_alias(out, 1, in, 3))) return rc;
   if ((rc = check_device())) return rc;
-  hipLaunchKernelGGL(w4::w4_pack, blocks_for(experts * l.tiles * 64), dim3(256), 0, stream, (const uint8_t*)codes,
+  hipLaunchKernelGGL(w4::w4_pack, blocks_for(experts * l.recs * 64), dim3(256), 0, stream, (const uint8_t*)codes,
                      (const uint16_t*)scales, (const uint8_t*)zeros, (char*)data, l, experts, (int)N, (int)K, group);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
@@ -338,16 +334,20 @@ int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T
   c.wd = w4_weight(w);
   c.y = (char*)Y;
   c.T = T;
+  c.x = (const char*)X;
+  c.D = w->N;
+  c.H = w->K;
   c.k = 1;
   c.E = 1;
+  c.zeros = w->has_zeros != 0;
   c.stream = stream;
-  return run_down_for(dtype, w->group, c, (const char*)X, w->K, w->N);
+  return run_linear_for(dtype, w->group, c);
 }
 
-size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t H, int dtype) {
+size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t D, int64_t H, int dtype) {
   const size_t e = elt_bytes(dtype);
-  if (e != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(H)) return 0;
-  return (size_t)T * H * e;
+  if (e != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(D) || !ld_ok(H)) return 0;
+  return few::block_plan(T, D, H, 1, e).total;
 }
 
 int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t* wu, const swiglu_w4_t* wd, void* Y,
@@ -357,9 +357,10 @@ int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t*
   int rc;
   if ((rc = check_w4(wg)) || (rc = check_w4(wu)) || (rc = check_w4(wd))) return rc;
   if (wu->N != wg->N || wu->K != wg->K || wd->N != wg->K || wd->K != wg->N || wg->experts != 1 || wu->experts != 1 ||
-      wd->experts != 1 || wu->group != wg->group || wd->group != wg->group || T < 0 || T > SWIGLU_FEW_MAX_T)
+      wd->experts != 1 || wu->group != wg->group || wd->group != wg->group || !wu->has_zeros != !wg->has_zeros ||
+      !wd->has_zeros != !wg->has_zeros || T < 0 || T > SWIGLU_FEW_MAX_T)
     return SWIGLU_ERR_SHAPE;
-  const size_t td = (size_t)T * wg->K * e, need = (size_t)T * wg->N * e;
+  const size_t td = (size_t)T * wg->K * e, need = few::block_plan(T, wg->K, wg->N, 1, e).total;
   const Range in[] = {{X, td}, w4_range(wg), w4_range(wu), w4_range(wd)};
   const Range out[] = {{Y, td}, {workspace, need}};
   if ((rc = check_ptrs(in, 4)) || (rc = check_ptrs(out, 1))) return rc;
@@ -373,13 +374,14 @@ int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t*
   c.wg = w4_weight(wg);
   c.wu = w4_weight(wu);
   c.wd = w4_weight(wd);
-  c.a = (char*)workspace;
+  c.ws = (char*)workspace;
   c.y = (char*)Y;
   c.T = T;
   c.D = wg->K;
   c.H = wg->N;
   c.k = 1;
   c.E = 1;
+  c.zeros = wg->has_zeros != 0;
   c.stream = stream;
   return run_block_for(dtype, wg->group, c);
 }

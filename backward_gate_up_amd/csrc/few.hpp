@@ -10,13 +10,17 @@
 //
 // What bounds it: with a handful of tokens per expert each weight is used a
 // few times, so the time is that of reading the chosen experts' weights once
-// from HBM. A wave streams 16 weight rows (an MFMA column block) straight
-// into registers, 16 bytes per lane in the operand order of
-// v_mfma_f32_16x16x32 (lane l: row l % 16, 16-byte chunk l / 16 of each
-// 64-byte step), so no weight passes through LDS. Tokens are the MFMA's other
-// operand: row l % 16 of the expert's token list, gathered. Rows past the
-// list repeat its last token and are dropped afterwards: an MFMA row depends
-// on no other row, so neither they nor another token's NaN can leak.
+// from HBM. Every wave streams its own run of K through a private ring in LDS
+// with direct-to-LDS loads of whole 128-byte lines (16 weight rows and the
+// expert's token rows side by side), and reads them back as the operands of
+// v_mfma_f32_16x16x32; the waves never wait for one another inside the run.
+// Loading the operands straight into registers measured 27 GB/s per CU: a
+// wave's 64 lanes then touch 16 rows, neighbouring lanes different lines, and
+// the address unit takes each 16-byte piece on its own.
+//
+// Rows of the token operand past the expert's list are zeros or repeats and
+// are dropped afterwards: an MFMA row depends on no other row, so neither
+// they nor another token's NaN can leak.
 //
 // Experts are visited per chunk of 64 tokens (grid z): each workgroup reads
 // the chunk's ids, finds its expert as the n-th one that occurs, and lists
@@ -32,18 +36,17 @@ constexpr int kChunk = 64;              // tokens per grid z slice
 constexpr int kMaxTopK = 32;            // choices per token
 constexpr int kMaxPairs = kChunk * kMaxTopK;
 constexpr int kMaxExperts = 1024;
+constexpr int NW = 4;                   // waves per workgroup, splitting K
 
 // One weight as the kernels address it. Rows: E matrices [N, K], row-major.
-// 4 bits: per 16 rows and 128 K one tile of 1 KiB, lane l's 16 bytes holding
-// row l % 16, K 32 s + 8 (l / 16) .. + 7 in dword s; inside a dword the
-// nibble of the even K 2p is at bit 4p, of the odd K 2p + 1 at bit 16 + 4p.
-// Scales [E][N/16][K/128][16][128/g] in the storage type; zero points
-// [E][N/16][K/128][16] as 128/g nibbles of a 16-bit word.
+// 4 bits: E x [N/16][K/128] records, each 1 KiB of codes (lane l's 16 bytes
+// hold row l % 16, K 32 s + 8 (l / 16) .. + 7 in dword s; inside a dword the
+// nibble of the even K 2p is at bit 4p, of the odd K 2p + 1 at bit 16 + 4p),
+// then the scales [16][128/g] in the storage type, then, where the weight has
+// zero points, 16 words of 16 bits with 128/g nibbles each.
 struct Weight {
   const char* w;
-  const char* scale;
-  const char* zero;  // nullptr: every zero point is 8
-  int64_t expert;    // bytes (rows) or 1 KiB tiles (4 bits) per expert
+  int64_t expert;  // bytes per expert
 };
 
 struct Args {
@@ -54,6 +57,11 @@ struct Args {
   const float* wts;  // [T, k]; nullptr: dense
   int T, k, E, N, K;
   uint32_t kinv;     // ceil(65536 / k): p / k = p * kinv >> 16 for a chunk's p < 2048, k <= 32
+  int zeros;         // 4 bits: the weights have zero points (else every one is 8)
+  int splits;        // down: workgroups per output tile
+  float* partial;    // down, splits > 1: [splits][T][N]
+  unsigned* ctr;     // gate/up: n_ctr arrival counters to clear for the down launch;
+  int n_ctr;         // down, splits > 1: one per (chunk, output tile)
 };
 
 // ---- MFMA steps -------------------------------------------------------------
@@ -77,139 +85,151 @@ __device__ __forceinline__ f32x4_t step_mfma(u32x4_t a, u32x4_t w, f32x4_t c) {
   }
 }
 
-__device__ __forceinline__ u32x4_t load16(const char* p) { return *(const u32x4_t*)p; }
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// ---- weight streams ---------------------------------------------------------
-// A stream adds the products of K steps [s0, s1) to acc[n][m]: NT weight blocks
-// of 16 rows x MT token blocks of 16. A ring of U steps stays in flight: each
-// step's registers are refilled as soon as its products are issued. Offsets
-// past the end of the run or of K go out of the buffers' range, so those loads
-// return zeros without a memory access: no remainder code, and neither the next
-// row nor a NaN there is multiplied in.
+// Four bytes per lane to LDS address lds + 4 * lane (see dma16).
+__device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rs), "{m0}"(lds) : "memory");
+}
+
+// ---- streams ------------------------------------------------------------------
+// A stream adds the products of the K stages [s0, s1) to acc[n][m]: NT weight
+// blocks of 16 rows x token rows in blocks of 16. Its ring of NS slots is the
+// wave's own: stage s waits for its own loads only (vmcnt counts a wave's
+// loads in issue order), reads slot s % NS, and refills it. Stages past the
+// run and bytes past K are asked for beyond the buffers' range, which loads
+// zeros without a memory access: no remainder code, and neither the next row
+// nor a NaN there is multiplied in.
 //
-// Tokens: rows of K elements at row_off[m] from x (bytes).
+// XR: token rows held per stage, 16, 32 or 64, or fewer than 16 (what one
+// load instruction covers): then rows XR .. 15 of the operand repeat them.
 
-// Rows of 16-bit or fp32 weights; a step is 64 bytes of K.
-// R: registers a lane may hold (512 per SIMD lane over its waves).
-template <class E, int NT, int MT, int R>
+// Rows of 16-bit or fp32 values: a stage is 128 bytes of K, 16 rows x 128 B in
+// two loads of 8 rows. Chunk c of row r sits at position c ^ kc_swz(r), so the
+// 16 rows one read takes fall on distinct banks.
+template <class E, int NT, int XR, int LW>
 struct RowStream {
-  static constexpr int kFit = (R - 40 - 4 * NT * MT) / (4 * (NT + MT));
-  static constexpr int U = kFit >= 16 ? 16 : kFit >= 8 ? 8 : 4;
-  __amdgpu_buffer_rsrc_t w[NT], x;
-  uint32_t w_off, x_off[MT];
-  int kb;  // bytes of K
+  static constexpr int MT = XR < 16 ? 1 : XR / 16;
+  static constexpr int XD = XR / 8;        // token loads per stage
+  static constexpr int D = 2 * NT + XD;    // loads per stage
+  static constexpr int SLOT = D * 1024;
+  static constexpr int NS = LW / SLOT < 8 ? LW / SLOT : 8;
+  static_assert(NS >= 2 && XR >= 8 && (NS - 1) * D <= 63, "ring");
+  i32x4_t rw[NT], rx;
+  uint32_t w_off[2], x_off[XD];
+  int kb;
 
-  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, int N, int K, const char* xb,
-                                       const uint32_t (&row_off)[MT], uint32_t x_bytes, int lane) {
-    kb = K * E::kBytes;
-    const int rows = min(16, N - row0);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      w[n] = make_rsrc32(wt[n]->w + (int64_t)e * wt[n]->expert + (int64_t)row0 * kb, rows * kb);
-    x = make_rsrc32(xb, (int)x_bytes);
-    w_off = (uint32_t)min(lane & 15, rows - 1) * (uint32_t)kb;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x_off[m] = row_off[m];
-  }
-  static __device__ __forceinline__ int steps(int K) { return (K * E::kBytes + 63) >> 6; }
+  static __device__ __forceinline__ int stages(int K) { return (K * E::kBytes + 127) >> 7; }
+  // the token row (0 .. XR - 1) whose chunk this lane fetches in load j
+  static __device__ __forceinline__ int x_row(int j, int lane) { return 8 * j + (lane >> 3); }
 
-  struct Buf {
-    u32x4_t w[NT], x[MT];
-  };
-  __device__ __forceinline__ void load(Buf& b, int off, int end) const {
-    const bool in = off < end;
+  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, const Args& g, const char* xb,
+                                       uint32_t x_bytes, const uint32_t (&row)[XD], int lane) {
+    kb = g.K * E::kBytes;
+    const int rows = min(16, g.N - row0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) b.w[n] = load16(w[n], in ? w_off + off : kOOB);
+    for (int n = 0; n < NT; ++n)  // rows past N read as zeros
+      rw[n] = rsrc_words(wt[n]->w + (int64_t)e * wt[n]->expert + (int64_t)row0 * kb, (int64_t)rows * kb);
+    rx = rsrc_words(xb, x_bytes);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) b.x[m] = load16(x, in ? x_off[m] + off : kOOB);
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      w_off[j] = r < rows ? (uint32_t)r * (uint32_t)kb : kOOB;
+    }
+#pragma unroll
+    for (int j = 0; j < XD; ++j) x_off[j] = row[j];
   }
-  __device__ __forceinline__ void run(f32x4_t (&acc)[NT][MT], int s0, int s1, int lane) const {
-    const int end = min(s1 * 64, kb);
-    int off = s0 * 64 + (lane >> 4) * 16;
-    Buf b[U];
+  __device__ __forceinline__ void issue(uint32_t slot, int s, int s1, int lane) const {
+    const int end = s < s1 ? kb : 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(b[u], off + 64 * u, end);
-    for (int s = s0; s < s1; s += U) {
+    for (int j = 0; j < (XD > 2 ? XD : 2); ++j) {
+      const int r = 8 * j + (lane >> 3);
+      const int off = s * 128 + (((lane & 7) ^ kc_swz(r)) << 4);
+      const bool in = off < end;
+      if (j < 2) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[n][m] = step_mfma<E>(b[u].x[m], b[u].w[n], acc[n][m]);
-        load(b[u], off + 64 * (U + u), end);
+        for (int n = 0; n < NT; ++n) dma16(slot + n * 2048 + j * 1024, rw[n], in ? w_off[j] + off : kOOB, 0u);
       }
-      off += 64 * U;
+      if (j < XD) dma16(slot + NT * 2048 + j * 1024, rx, in ? x_off[j] + off : kOOB, 0u);
+    }
+  }
+  __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane) const {
+    const int r = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = r * 128 + (((4 * h + c) ^ kc_swz(r)) << 4);
+      const int ax = XR < 16 ? (r & 7) * 128 + (((4 * h + c) ^ kc_swz(r & 7)) << 4) : at;
+      u32x4_t xv[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xv[m] = *(const u32x4_t*)(slot + NT * 2048 + m * 2048 + ax);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const u32x4_t wv = *(const u32x4_t*)(slot + n * 2048 + at);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = step_mfma<E>(xv[m], wv, acc[n][m]);
+      }
     }
   }
 };
 
-// 4-bit codes; a step is one tile of 128 K. The products run on integers: the
-// nibble q goes into the mantissa of 128 (bf16) or 64 (fp16), which makes the
-// operand OFF + q exactly with one shift and one and-or per two values. Per
-// group of g the fp32 sum of x (OFF + q) is corrected by (OFF + z) times the
-// sum of x (one more MFMA against ones, shared by all weight blocks) and
-// scaled, so a scale costs two operations per output and group and no weight is
-// rounded. The offset costs accuracy of about OFF / 5 fp32 roundings of the
+// 4-bit codes; a stage is one record of 128 K. The products run on integers:
+// the nibble q goes into the mantissa of 128 (bf16) or 64 (fp16), which makes
+// the operand OFF + q exactly with one shift and one and-or per two values.
+// Per group of g the fp32 sum of x (OFF + q) is corrected by (OFF + z) times
+// the sum of x (one more MFMA against ones, shared by all weight blocks) and
+// scaled, so a scale costs two operations per output and group and no weight
+// is rounded. The offset costs accuracy of about OFF / 5 fp32 roundings of the
 // group's sum, 2^-19 of it in bf16: far below the storage type's half step.
-template <class E, int G, int NT, int MT, int R>
+// Token rows are 256 B per stage; chunk c of row r at position c ^ (r & 15).
+template <class E, int G, int NT, int XR, int LW>
 struct W4Stream {
-  static constexpr int GP = 128 / G;  // groups per tile
-  static constexpr int U = R < 256 || MT > 1 ? 1 : 2;
+  static constexpr int GP = 128 / G;  // groups per record
+  static constexpr int MT = XR < 16 ? 1 : XR / 16;
+  static constexpr int XD = XR / 4;
+  static constexpr int D = 2 * NT + XD;
+  static constexpr int WS = 1024 + 256;  // a record's place in a slot
+  static constexpr int SLOT = NT * WS + XD * 1024;
+  static constexpr int NS = LW / SLOT < 8 ? LW / SLOT : 8;
+  static_assert(NS >= 2 && XR >= 4 && (NS - 1) * D <= 63, "ring");
   static constexpr float kOff = std::is_same<E, Bf16>::value ? 128.0f : 64.0f;
-  __amdgpu_buffer_rsrc_t w[NT], s[NT], z[NT], x;
-  uint32_t x_off[MT];
-  int kb, lane;
-  bool has_zero;
+  i32x4_t rw[NT], rx;
+  uint32_t x_off[XD];
+  int kb, rec, zeros;
 
-  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, int N, int K, const char* xb,
-                                       const uint32_t (&row_off)[MT], uint32_t x_bytes, int ln) {
-    const int nkt = steps(K);
-    kb = K * 2;
-    lane = ln;
-    has_zero = wt[0]->zero != nullptr;
+  static __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
+  static __device__ __forceinline__ int x_row(int j, int lane) { return 4 * j + (lane >> 4); }
+
+  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, const Args& g, const char* xb,
+                                       uint32_t x_bytes, const uint32_t (&row)[XD], int lane) {
+    kb = g.K * 2;
+    zeros = g.zeros;
+    rec = 1024 + 32 * GP + (zeros ? 32 : 0);
+    const int len = stages(g.K) * rec;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int64_t tile = (int64_t)e * wt[n]->expert + (int64_t)(row0 >> 4) * nkt;
-      w[n] = make_rsrc32(wt[n]->w + tile * 1024, nkt * 1024);
-      s[n] = make_rsrc32(wt[n]->scale + tile * (32 * GP), nkt * (32 * GP));
-      z[n] = make_rsrc32(wt[n]->zero + tile * 32, has_zero ? nkt * 32 : 0);
-    }
-    x = make_rsrc32(xb, (int)x_bytes);
+    for (int n = 0; n < NT; ++n)
+      rw[n] = rsrc_words(wt[n]->w + (int64_t)e * wt[n]->expert + (int64_t)(row0 >> 4) * len, len);
+    rx = rsrc_words(xb, x_bytes);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x_off[m] = row_off[m];
+    for (int j = 0; j < XD; ++j) x_off[j] = row[j];
   }
-  static __device__ __forceinline__ int steps(int K) { return (K + 127) >> 7; }
-
-  struct Buf {
-    u32x4_t w[NT], x[4][MT];
-    uint32_t s[NT][GP == 4 ? 2 : 1];
-    uint32_t z[NT];
-  };
-  __device__ __forceinline__ void load(Buf& b, int t, int end) const {
-    const bool in = t < end;
-    const uint32_t row = lane & 15;
+  __device__ __forceinline__ void issue(uint32_t slot, int s, int s1, int lane) const {
+    const bool live = s < s1;
+    const uint32_t at = (uint32_t)s * rec;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      b.w[n] = load16(w[n], in ? (uint32_t)t * 1024 + lane * 16 : kOOB);
-      const uint32_t so = in ? ((uint32_t)t * 16 + row) * (2 * GP) : kOOB;
-      if constexpr (GP == 1) b.s[n][0] = __builtin_amdgcn_raw_buffer_load_b16(s[n], so, 0, 0);
-      else if constexpr (GP == 2) b.s[n][0] = __builtin_amdgcn_raw_buffer_load_b32(s[n], so, 0, 0);
-      else {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b64(s[n], so, 0, 0);
-        b.s[n][0] = v[0];
-        b.s[n][1] = v[1];
-      }
-      b.z[n] = 0x8888u;
-      if (has_zero) b.z[n] = __builtin_amdgcn_raw_buffer_load_b16(z[n], in ? ((uint32_t)t * 16 + row) * 2 : kOOB, 0, 0);
+      dma16(slot + n * WS, rw[n], live ? at + lane * 16 : kOOB, 0u);
+      dma4(slot + n * WS + 1024, rw[n], live && 1024 + lane * 4 < rec ? at + 1024 + lane * 4 : kOOB);
     }
-    const int off = t * 256 + (lane >> 4) * 16, xe = in ? kb : 0;
+    const int end = live ? kb : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) b.x[i][m] = load16(x, off + 64 * i < xe ? x_off[m] + off + 64 * i : kOOB);
+    for (int j = 0; j < XD; ++j) {
+      const int r = 4 * j + (lane >> 4);
+      const int off = s * 256 + (((lane & 15) ^ (r & 15)) << 4);
+      dma16(slot + NT * WS + j * 1024, rx, off < end ? x_off[j] + off : kOOB, 0u);
+    }
   }
   // eight codes of one dword as the MFMA operand OFF + q
   static __device__ __forceinline__ u32x4_t widen(uint32_t v) {
@@ -225,60 +245,78 @@ struct W4Stream {
     constexpr uint32_t o = std::is_same<E, Bf16>::value ? 0x3f803f80u : 0x3c003c00u;
     return u32x4_t{o, o, o, o};
   }
-  static __device__ __forceinline__ float scale_of(const uint32_t (&s)[GP == 4 ? 2 : 1], int g) {
-    const uint32_t h = (s[g >> 1] >> ((g & 1) * 16)) & 0xffffu;
-    return E::to_f32(__builtin_bit_cast(typename E::elem, (uint16_t)h));
-  }
-  __device__ __forceinline__ void tile(const Buf& b, f32x4_t (&acc)[NT][MT]) const {
+  __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane) const {
+    const int r = lane & 15, c = lane >> 4, rr = XR < 16 ? r & (XR - 1) : r;
+    u32x4_t code[NT];
+    typename E::elem sc[NT][GP];
+    uint32_t z[NT];
 #pragma unroll
-    for (int g = 0; g < GP; ++g) {
+    for (int n = 0; n < NT; ++n) {
+      code[n] = *(const u32x4_t*)(slot + n * WS + lane * 16);
+      const typename E::elem* sp = (const typename E::elem*)(slot + n * WS + 1024) + r * GP;
+#pragma unroll
+      for (int q = 0; q < GP; ++q) sc[n][q] = sp[q];
+      z[n] = zeros ? *(const uint16_t*)(slot + n * WS + 1024 + 32 * GP + r * 2) : 0x8888u;
+    }
+#pragma unroll
+    for (int q = 0; q < GP; ++q) {
       f32x4_t part[NT][MT] = {}, xs[MT] = {};
 #pragma unroll
-      for (int i = 4 / GP * g; i < 4 / GP * (g + 1); ++i) {
+      for (int i = 4 / GP * q; i < 4 / GP * (q + 1); ++i) {
+        u32x4_t xv[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) xs[m] = step_mfma<E>(b.x[i][m], ones(), xs[m]);
+        for (int m = 0; m < MT; ++m) {
+          xv[m] = *(const u32x4_t*)(slot + NT * WS + (16 * m + rr) * 256 + (((4 * i + c) ^ rr) << 4));
+          xs[m] = step_mfma<E>(xv[m], ones(), xs[m]);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const u32x4_t q = widen(b.w[n][i]);
+          const u32x4_t w = widen(code[n][i]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) part[n][m] = step_mfma<E>(b.x[i][m], q, part[n][m]);
+          for (int m = 0; m < MT; ++m) part[n][m] = step_mfma<E>(xv[m], w, part[n][m]);
         }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float sc = scale_of(b.s[n], g);
-        const float off = kOff + (float)((b.z[n] >> (4 * g)) & 15u);
+        const float s = E::to_f32(sc[n][q]);
+        const float off = kOff + (float)((z[n] >> (4 * q)) & 15u);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[n][m][j] = fmaf(sc, fmaf(-off, xs[m][j], part[n][m][j]), acc[n][m][j]);
-      }
-    }
-  }
-  __device__ __forceinline__ void run(f32x4_t (&acc)[NT][MT], int s0, int s1, int) const {
-    Buf b[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(b[u], s0 + u, s1);
-    for (int t = s0; t < s1; t += U) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const Buf c = b[u];
-        load(b[u], t + U + u, s1);
-        tile(c, acc);
+          for (int j = 0; j < 4; ++j) acc[n][m][j] = fmaf(s, fmaf(-off, xs[m][j], part[n][m][j]), acc[n][m][j]);
       }
     }
   }
 };
 
 // FMT 0: rows; 32, 64, 128: 4 bits with groups of that size
-template <class E, int FMT, int NT, int MT, int R>
+template <class E, int FMT, int NT, int XR, int LW>
 struct StreamOf {
-  using type = W4Stream<E, FMT, NT, MT, R>;
+  using type = W4Stream<E, FMT, NT, XR, LW>;
 };
-template <class E, int NT, int MT, int R>
-struct StreamOf<E, 0, NT, MT, R> {
-  using type = RowStream<E, NT, MT, R>;
+template <class E, int NT, int XR, int LW>
+struct StreamOf<E, 0, NT, XR, LW> {
+  using type = RowStream<E, NT, XR, LW>;
 };
+
+// Runs stages [s0, s1) of a stream in the wave's ring (LDS address and pointer).
+template <class S, int NT>
+__device__ __forceinline__ void run_stream(const S& st, f32x4_t (&acc)[NT][S::MT], char* ring, int s0, int s1, int lane) {
+  if (s0 >= s1) return;
+  const uint32_t at = lds_addr(ring);
+#pragma unroll
+  for (int p = 0; p < S::NS; ++p) st.issue(at + p * S::SLOT, s0 + p, s1, lane);
+  int slot = 0;
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    ring::wait_vmcnt<(S::NS - 1) * S::D>();
+    st.compute(ring + slot * S::SLOT, acc, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+    st.issue(at + slot * S::SLOT, s + S::NS, s1, lane);
+    slot = slot + 1 == S::NS ? 0 : slot + 1;
+  }
+  ring::wait_vmcnt<0>();  // the surplus stages' loads (zeros) have landed too
+}
 
 // ---- a chunk's choices --------------------------------------------------------
 // ids of the chunk's pairs, and the experts that occur, in ascending order.
@@ -321,9 +359,16 @@ __device__ __forceinline__ void read_choices(Choices& c, const Args& g, int t0, 
   __syncthreads();
 }
 
-// One wave: the pairs that chose e, ranks [64 pass, 64 pass + 64), into
-// list[0 .. 63] in ascending order. Returns how many pairs chose e in all.
-__device__ __forceinline__ int list_pairs(const Choices& c, int P, int e, int pass, int16_t* list, int lane) {
+// The pairs that chose one expert, as one wave holds them: lane i has the i-th
+// (its index in the chunk), n of them.
+struct Picked {
+  int pair, n;
+};
+
+// One wave: the pairs that chose e, ranks [64 pass, 64 pass + 64); total: how
+// many chose e in all. list: 64 entries of the wave's own.
+__device__ __forceinline__ Picked list_pairs(const Choices& c, int P, int e, int pass, int16_t* list, int lane,
+                                             int& total) {
   int n = 0;
   for (int r = 0; r < P; r += 64) {
     const bool hit = r + lane < P && c.id[r + lane] == e;
@@ -332,185 +377,287 @@ __device__ __forceinline__ int list_pairs(const Choices& c, int P, int e, int pa
     if (hit && at >= 0 && at < 64) list[at] = (int16_t)(r + lane);
     n += __popcll(m);
   }
-  // the list is this wave's own: wait for its writes, no barrier
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  return n;
+  total = n;
+  const int got = min(64, n - 64 * pass);
+  return {lane < got ? (int)list[lane] : 0, got};
+}
+// The same from a mask of at most 64 pairs, in registers.
+__device__ __forceinline__ Picked mask_pairs(uint64_t m, int lane) {
+  const bool in = (m >> lane) & 1;
+  const int rank = __popcll(m & ((1ull << lane) - 1));
+  // lanes in the mask send their index to lane `rank`, the others to lane 63,
+  // which then only matters when the mask is full and nobody else sends
+  const int v = __builtin_amdgcn_ds_permute((in ? rank : 63) * 4, lane);
+  return {v, (int)__popcll(m)};
 }
 
 // ---- gate/up ------------------------------------------------------------------
-// NW waves split K. Registers per lane: two workgroups of 4 waves or one of 8
-// share a CU's four SIMDs, so 256.
-template <class E, int FMT, int NW, int MT>
-__device__ __forceinline__ void gateup_block(const Args& g, int e, int row0, int t0, const int16_t* list, int n,
-                                             float* red) {
-  using S = typename StreamOf<E, FMT, 2, MT, 256>::type;
+template <class E, int FMT, int XR, int LW>
+__device__ __forceinline__ void gateup_block(const Args& g, int e, int row0, int t0, const Picked& p, int first, int n,
+                                             char* lds) {
+  using S = typename StreamOf<E, FMT, 2, XR, LW>::type;
+  constexpr int MT = S::MT;
+  static_assert(NW * 2 * MT * 1024 <= NW * LW, "the sums fit in the rings");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t row[MT];
+  uint32_t row[S::XD];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int i = min(16 * m + (lane & 15), n - 1);
-    row[m] = (uint32_t)(list ? (list[i] * g.kinv) >> 16 : i) * (uint32_t)(g.K * E::kBytes);
+  for (int j = 0; j < S::XD; ++j) {
+    const int i = S::x_row(j, lane);
+    const int pair = __shfl(p.pair, first + i);
+    row[j] = i < n ? ((pair * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB;
   }
   S s;
   const Weight* const w[2] = {&g.w0, &g.w1};
-  s.init(w, e, row0, g.N, g.K, g.x + (int64_t)t0 * g.K * E::kBytes, row, (uint32_t)(min(kChunk, g.T - t0) * g.K) * E::kBytes,
+  s.init(w, e, row0, g, g.x + (int64_t)t0 * g.K * E::kBytes, (uint32_t)(min(kChunk, g.T - t0) * g.K) * E::kBytes, row,
          lane);
-  const int steps = S::steps(g.K), per = (steps + NW - 1) / NW;
+  const int stages = S::stages(g.K), per = (stages + NW - 1) / NW;
   f32x4_t acc[2][MT] = {};
-  s.run(acc, wave * per, min(steps, (wave + 1) * per), lane);
+  run_stream<S, 2>(s, acc, lds + wave * LW, wave * per, min(stages, (wave + 1) * per), lane);
   // the waves' sums meet in LDS; thread -> (token row, hidden column), waves added in order
+  float* red = (float*)lds;
+  __syncthreads();
 #pragma unroll
   for (int n2 = 0; n2 < 2; ++n2)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      *(f32x4_t*)(red + (((wave * 2 + n2) * MT + m) * 64 + lane) * 4) = acc[n2][m];
+    for (int m = 0; m < MT; ++m) *(f32x4_t*)(red + (((wave * 2 + n2) * MT + m) * 64 + lane) * 4) = acc[n2][m];
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 256; i += NW * 64) {
-    const int col = i & 15, row = i >> 4;  // token row of the list, hidden column
-    const int at = ((row >> 4) * 64 + ((row & 15) >> 2) * 16 + col) * 4 + (row & 3);
+  for (int i0 = 0; i0 < MT * 256; i0 += NW * 64) {
+    const int i = i0 + threadIdx.x;
+    const int col = i & 15, r = i >> 4;  // token row of the list, hidden column
+    const int at = ((r >> 4) * 64 + ((r & 15) >> 2) * 16 + col) * 4 + (r & 3);
     float gate = 0.f, up = 0.f;
 #pragma unroll
     for (int v = 0; v < NW; ++v) {
       gate += red[(v * 2 + 0) * MT * 256 + at];
       up += red[(v * 2 + 1) * MT * 256 + at];
     }
+    const int pair = __shfl(p.pair, first + r);
     const int h = row0 + col;
-    if (row < n && h < g.N) {
-      const int64_t p = list ? (int64_t)t0 * g.k + list[row] : t0 + row;
+    if (r < n && h < g.N) {
       // g and u stay in fp32; A is rounded once, to the storage type the
       // down projection's matrix instructions take
-      ((typename E::elem*)g.out)[p * g.N + h] = E::from_f32(gate * sigmoid_f32<E>(gate) * up);
+      ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] =
+          E::from_f32(gate * sigmoid_f32<E>(gate) * up);
     }
   }
   __syncthreads();
 }
 
-template <class E, int FMT, int NW>
+// The block with as many token rows as the list needs. 4 bits: at most 32 (64
+// rows of 256 bytes would leave no room for a ring); more go in two passes.
+template <class E, int FMT, int LW>
+__device__ __forceinline__ void gateup_rows(const Args& g, int e, int row0, int t0, const Picked& p, char* lds) {
+  constexpr int kFew = FMT ? 4 : 8;
+  if (p.n <= kFew) gateup_block<E, FMT, kFew, LW>(g, e, row0, t0, p, 0, p.n, lds);
+  else if (p.n <= 16) gateup_block<E, FMT, 16, LW>(g, e, row0, t0, p, 0, p.n, lds);
+  else if constexpr (LW >= 32768) {
+    if (FMT || p.n <= 32) {
+      for (int f = 0; f < p.n; f += 32) gateup_block<E, FMT, 32, LW>(g, e, row0, t0, p, f, min(32, p.n - f), lds);
+    } else if constexpr (FMT == 0) {
+      gateup_block<E, FMT, 64, LW>(g, e, row0, t0, p, 0, p.n, lds);
+    }
+  } else {
+    for (int f = 0; f < p.n; f += 16) gateup_block<E, FMT, 16, LW>(g, e, row0, t0, p, f, min(16, p.n - f), lds);
+  }
+}
+
+// LW: ring bytes per wave. 18 KiB lets two workgroups share a CU; 36 KiB (one)
+// is for longer lists of tokens.
+template <class E, int FMT, int LW>
 __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
+  __shared__ __attribute__((aligned(1024))) char lds[NW * LW];
   __shared__ Choices ch;
-  __shared__ int16_t list[64];
-  __shared__ int count;  // pairs that chose the workgroup's expert
-  __shared__ __attribute__((aligned(16))) float red[NW * 2 * 4 * 256];
-  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0);
-  const int row0 = blockIdx.x * 16;
+  __shared__ int16_t list[NW][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0), P = tc * g.k;
+  const int row0 = blockIdx.x * 16, slot = blockIdx.y;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < g.n_ctr; i += NW * 64) g.ctr[i] = 0u;
+  // the workgroup's expert, and how to list its pairs: all tokens (dense), a
+  // mask of at most 64 pairs, or a scan of the chunk's choices in LDS
+  const bool small = P <= 64;
   int e = 0, total = tc;
-  const bool routed = g.ids != nullptr;
-  if (routed) {
+  Picked p{lane, tc};
+  if (g.ids && small) {
+    const int id = lane < P ? g.ids[(int64_t)t0 * g.k + lane] : -1;
+    uint64_t left = __ballot((unsigned)id < (unsigned)g.E), m = 0;
+    for (int i = 0; i <= slot; ++i) {
+      if (!left) return;  // fewer experts occur than there are slots
+      e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+      m = __ballot(id == e);
+      left &= ~m;
+    }
+    p = mask_pairs(m, lane);
+  } else if (g.ids) {
     read_choices(ch, g, t0, tc);
-    if ((int)blockIdx.y >= ch.hits) return;
-    e = ch.expert[blockIdx.y];
+    if (slot >= ch.hits) return;
+    e = ch.expert[slot];
   }
   for (int pass = 0; 64 * pass < total; ++pass) {
-    if (routed) {
-      if (threadIdx.x < 64) {
-        const int n = list_pairs(ch, tc * g.k, e, pass, list, threadIdx.x);
-        if (threadIdx.x == 0) count = n;
-      }
-      __syncthreads();
-      total = count;
-    }
-    const int n = min(64, total - 64 * pass);
-    const int16_t* l = routed ? list : nullptr;
-    if (n <= 16) gateup_block<E, FMT, NW, 1>(g, e, row0, t0, l, n, red);
-    else if (n <= 32) gateup_block<E, FMT, NW, 2>(g, e, row0, t0, l, n, red);
-    else gateup_block<E, FMT, NW, 4>(g, e, row0, t0, l, n, red);
+    if (g.ids && !small) p = list_pairs(ch, P, e, pass, list[wave], lane, total);
+    gateup_rows<E, FMT, LW>(g, e, row0, t0, p, lds);
   }
 }
 
 // ---- down -----------------------------------------------------------------------
-// The K axis of an output tile is the list of (expert that occurs, K step); the
-// workgroup's NW waves take equal runs of it. At an expert's end the block of
-// sums is weighted and added to the wave's own [token][column] tile in LDS.
-template <int NW>
-struct DownShared {
-  Choices ch;
-  float wts[kMaxPairs];
-  int16_t list[NW][64];
-  float y[NW][kChunk * 16];
-};
-
-template <class E, int FMT, int NW, int MT>
-__device__ __forceinline__ void down_block(const Args& g, DownShared<NW>& sh, int e, int row0, int t0, int n, int s0,
-                                           int s1) {
-  using S = typename StreamOf<E, FMT, 1, MT, NW == 16 ? 128 : 256>::type;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// The K axis of an output tile is the list of (expert that occurs, K stage); the
+// splits x NW waves take equal runs of it. At an expert's end the block of sums
+// is weighted and added to the wave's own [token][column] tile in LDS.
+template <class E, int FMT, int XR, int LW>
+__device__ __forceinline__ void down_block(const Args& g, int e, int row0, int t0, const Picked& p, int first, int n,
+                                           int s0, int s1, char* ring, float* y) {
+  using S = typename StreamOf<E, FMT, 1, XR, LW>::type;
+  constexpr int MT = S::MT;
+  const int lane = threadIdx.x & 63;
   const bool routed = g.ids != nullptr;
-  const int16_t* list = sh.list[wave];
-  uint32_t row[MT];
+  uint32_t row[S::XD];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int i = min(16 * m + (lane & 15), n - 1);
-    row[m] = (uint32_t)(routed ? list[i] : i) * (uint32_t)(g.K * E::kBytes);
+  for (int j = 0; j < S::XD; ++j) {
+    const int i = S::x_row(j, lane);
+    const int pair = __shfl(p.pair, first + i);
+    row[j] = i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB;
   }
+  // this lane's output rows are the list's 16 m + 4 (lane / 16) + j
+  const int mine = __shfl(p.pair, (first + lane) & 63);
+  const float wt = routed && lane < n ? g.wts[(int64_t)t0 * g.k + mine] : 1.0f;
   S s;
   const Weight* const w[1] = {&g.w0};
-  s.init(w, e, row0, g.N, g.K, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, row,
-         (uint32_t)(min(kChunk, g.T - t0) * g.k * g.K) * E::kBytes, lane);
+  s.init(w, e, row0, g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes,
+         (uint32_t)(min(kChunk, g.T - t0) * g.k * g.K) * E::kBytes, row, lane);
   f32x4_t acc[1][MT] = {};
-  s.run(acc, s0, s1, lane);
-  float* y = sh.y[wave];
+  run_stream<S, 1>(s, acc, ring, s0, s1, lane);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     // one group of 16 lanes (4 token rows) at a time: a token listed twice
     // for one expert is then added twice, in order
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
-      if ((lane >> 4) == q) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 16 * m + 4 * q + j;
-          if (i < n) {
-            const int p = routed ? list[i] : i;
-            float* at = y + (routed ? (p * g.kinv) >> 16 : (uint32_t)p) * 16 + (lane & 15);
-            *at += (routed ? sh.wts[p] : 1.0f) * acc[0][m][j];
-          }
+      for (int j = 0; j < 4; ++j) {
+        const int i = 16 * m + 4 * q + j;
+        if (i < n) {
+          const int pair = __builtin_amdgcn_readlane(mine, i);
+          const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wt), i));
+          if ((lane >> 4) == q) y[((pair * g.kinv) >> 16) * 16 + (lane & 15)] += f * acc[0][m][j];
         }
       }
-      __builtin_amdgcn_wave_barrier();
     }
   }
 }
 
-template <class E, int FMT, int NW>
-__global__ void __launch_bounds__(NW * 64, NW == 16 ? 4 : 2) few_down(const Args g) {
-  __shared__ __attribute__((aligned(16))) DownShared<NW> sh;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0);
-  const int row0 = blockIdx.x * 16;
-  const bool routed = g.ids != nullptr;
-  int hits = 1;
-  if (routed) {
-    for (int i = threadIdx.x; i < tc * g.k; i += blockDim.x) sh.wts[i] = g.wts[(int64_t)t0 * g.k + i];
-    read_choices(sh.ch, g, t0, tc);
-    hits = sh.ch.hits;
+template <class E, int FMT, int LW>
+__device__ __forceinline__ void down_rows(const Args& g, int e, int row0, int t0, const Picked& p, int s0, int s1,
+                                          char* ring, float* y) {
+  constexpr int kFew = FMT ? 4 : 8;
+  if (p.n <= kFew) down_block<E, FMT, kFew, LW>(g, e, row0, t0, p, 0, p.n, s0, s1, ring, y);
+  else if (p.n <= 16) down_block<E, FMT, 16, LW>(g, e, row0, t0, p, 0, p.n, s0, s1, ring, y);
+  else if constexpr (LW >= 32768) {
+    if (FMT || p.n <= 32) {
+      for (int f = 0; f < p.n; f += 32)
+        down_block<E, FMT, 32, LW>(g, e, row0, t0, p, f, min(32, p.n - f), s0, s1, ring, y);
+    } else if constexpr (FMT == 0) {
+      down_block<E, FMT, 64, LW>(g, e, row0, t0, p, 0, p.n, s0, s1, ring, y);
+    }
+  } else {
+    for (int f = 0; f < p.n; f += 16)
+      down_block<E, FMT, 16, LW>(g, e, row0, t0, p, f, min(16, p.n - f), s0, s1, ring, y);
   }
-  for (int i = lane; i < tc * 16; i += 64) sh.y[wave][i] = 0.f;
-  const int steps = StreamOf<E, FMT, 1, 1, 256>::type::steps(g.K);
-  const int all = hits * steps;
-  int at = (int)((int64_t)all * wave / NW);
-  const int end = (int)((int64_t)all * (wave + 1) / NW);
+}
+
+// LW 16 KiB: two workgroups per CU (at most 16 tokens), 32 KiB: one.
+template <class E, int FMT, int LW>
+__global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
+  constexpr int YT = LW >= 32768 ? kChunk : 16;  // tokens
+  __shared__ __attribute__((aligned(1024))) char lds[NW * LW];
+  __shared__ __attribute__((aligned(16))) float ysum[NW][YT * 16];
+  __shared__ Choices ch;
+  __shared__ int16_t list[NW][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0), P = tc * g.k;
+  const int row0 = blockIdx.x * 16;
+  char* ring = lds + wave * LW;
+  float* y = ysum[wave];
+  for (int i = lane; i < tc * 16; i += 64) y[i] = 0.f;
+  const int stages = StreamOf<E, FMT, 1, 16, LW>::type::stages(g.K);
+  const int parts = g.splits * NW, part = blockIdx.y * NW + wave;
+  // the experts that occur: one (dense), those of at most 64 pairs in
+  // registers, or the chunk's choices in LDS
+  const bool small = P <= 64;
+  int hits = 1, id = -1;
+  uint64_t left = 0;
+  if (g.ids && small) {
+    id = lane < P ? g.ids[(int64_t)t0 * g.k + lane] : -1;
+    left = __ballot((unsigned)id < (unsigned)g.E);
+    hits = 0;
+    for (uint64_t l = left; l; ++hits)
+      l &= ~__ballot(id == __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)l) - 1));
+  } else if (g.ids) {
+    read_choices(ch, g, t0, tc);
+    hits = ch.hits;
+  }
+  // the wave's run [at, end) of the tile's hits * stages
+  int at = (int)((int64_t)hits * stages * part / parts);
+  const int end = (int)((int64_t)hits * stages * (part + 1) / parts);
+  int i = g.ids && small ? 0 : at / stages;  // small: experts are found one after another
   while (at < end) {
-    const int slot = at / steps, s0 = at - slot * steps, s1 = min(steps, s0 + (end - at));
-    const int e = routed ? sh.ch.expert[slot] : 0;
-    int total = tc;
+    int e = 0, total = tc;
+    Picked p{lane, tc};
+    if (g.ids && small) {
+      e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+      const uint64_t m = __ballot(id == e);
+      left &= ~m;
+      if ((i + 1) * stages <= at) {
+        ++i;
+        continue;
+      }
+      p = mask_pairs(m, lane);
+    } else if (g.ids) {
+      e = ch.expert[i];
+    }
+    const int s0 = at - i * stages, s1 = min(stages, s0 + end - at);
     for (int pass = 0; 64 * pass < total; ++pass) {
-      if (routed) total = list_pairs(sh.ch, tc * g.k, e, pass, sh.list[wave], lane);
-      const int n = min(64, total - 64 * pass);
-      if (n <= 16) down_block<E, FMT, NW, 1>(g, sh, e, row0, t0, n, s0, s1);
-      else if (n <= 32) down_block<E, FMT, NW, 2>(g, sh, e, row0, t0, n, s0, s1);
-      else down_block<E, FMT, NW, 4>(g, sh, e, row0, t0, n, s0, s1);
+      if (g.ids && !small) p = list_pairs(ch, P, e, pass, list[wave], lane, total);
+      down_rows<E, FMT, LW>(g, e, row0, t0, p, s0, s1, ring, y);
     }
     at += s1 - s0;
+    ++i;
   }
   __syncthreads();
   // four columns of one token per thread; the waves' sums in order
-  for (int i = threadIdx.x; i < tc * 4; i += blockDim.x) {
+  const bool direct = g.splits == 1;
+  for (int i = threadIdx.x; i < tc * 4; i += NW * 64) {
     f32x4_t v{};
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += *(const f32x4_t*)(sh.y[w] + i * 4);
+    for (int w = 0; w < NW; ++w) v += *(const f32x4_t*)(ysum[w] + i * 4);
     const int t = t0 + (i >> 2), n = row0 + (i & 3) * 4;
     if (n >= g.N) continue;  // N is a multiple of 8: all four columns or none
+    if (direct) {
+      typename E::vec4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);
+      *(typename E::vec4*)((typename E::elem*)g.out + (int64_t)t * g.N + n) = o;
+    } else {
+      store_partial(g.partial + ((int64_t)blockIdx.y * g.T + t0) * g.N, tc, g.N, t - t0, n, v);
+    }
+  }
+  if (direct) return;
+  // Arrival, as in stream_gemm: device-coherent partials, each wave waits for
+  // its own, then one atomic add; the last workgroup adds the splits in order.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  int* last = (int*)lds;
+  if (threadIdx.x == 0)
+    *last = __hip_atomic_fetch_add(g.ctr + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(g.splits - 1);
+  __syncthreads();
+  if (!*last) return;
+  for (int i = threadIdx.x; i < tc * 4; i += NW * 64) {
+    const int t = t0 + (i >> 2), n = row0 + (i & 3) * 4;
+    if (n >= g.N) continue;
+    f32x4_t v{};
+    for (int sp = 0; sp < g.splits; ++sp)
+      v += load_partial(g.partial + ((int64_t)sp * g.T + t0) * g.N, tc, g.N, t - t0, n);
     typename E::vec4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);
@@ -519,52 +666,95 @@ __global__ void __launch_bounds__(NW * 64, NW == 16 ? 4 : 2) few_down(const Args
 }
 
 // ---- launches ---------------------------------------------------------------------
+// Workgroups per output tile of a block's down projection: about two per CU
+// over all tiles, so that all CUs pull weights (one CU alone reads at a few
+// tens of GB/s). 16-column tiles: D = 2048 has 128 of them.
+static inline int down_splits(int64_t T, int64_t D) {
+  const int64_t tiles = (D + 15) / 16 * ((T + kChunk - 1) / kChunk);
+  const int64_t s = 512 / tiles;
+  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+}
+// Workspace of a block: the A plane, then where the down projection is split
+// one counter per output tile and the partial sums, each 256-byte aligned.
+struct BlockPlan {
+  size_t ctr, partial, total;
+  int splits, n_ctr;
+};
+static inline BlockPlan block_plan(int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  BlockPlan p;
+  p.splits = down_splits(T, D);
+  p.n_ctr = p.splits > 1 ? (int)((D + 15) / 16 * ((T + kChunk - 1) / kChunk)) : 0;
+  p.ctr = up((size_t)T * k * H * e);
+  p.partial = p.ctr + up((size_t)p.n_ctr * 4);
+  p.total = p.partial + (p.splits > 1 ? up((size_t)p.splits * T * D * 4) : 0);
+  return p;
+}
+
 // A whole call; the host has checked it.
 struct Call {
   const char* x;
   Weight wg, wu, wd;  // linear: wd only
-  char* a;            // workspace: the A plane, [T * k, H]
+  char* ws;           // workspace (block_plan)
   char* y;
   const int* ids;
   const float* wts;
   int64_t T, D, H;
-  int k, E;
+  int k, E, zeros;
   hipStream_t stream;
 };
 
-template <class E, int FMT, int NW>
+template <class E, int FMT, int LW>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(STAGE_FEW_GATEUP, s);
   const dim3 grid((g.N + 15) / 16, slots, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_gateup<E, FMT, NW>), grid, dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_gateup<E, FMT, LW>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
-template <class E, int FMT, int NW>
+template <class E, int FMT, int LW>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
-  const dim3 grid((g.N + 15) / 16, 1, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_down<E, FMT, NW>), grid, dim3(NW * 64), 0, s, g);
+  const dim3 grid((g.N + 15) / 16, g.splits, (g.T + kChunk - 1) / kChunk);
+  hipLaunchKernelGGL((few_down<E, FMT, LW>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
+// Two workgroups per CU with short rings while no list is longer than their
+// token rows.
+static inline bool short_rings(int64_t T, int fmt) { return T <= (fmt ? 4 : 16); }
 
-// y = x W^T (dense), or the down projection of a block.
+static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, char* out) {
+  return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
+              c.zeros, 1, nullptr, nullptr, 0};
+}
 template <class E, int FMT>
-int run_down(const Call& c, const char* x, int64_t K, int64_t N) {
-  const Args g{x, c.wd, c.wd, c.y, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k};
-  const int64_t groups = (N + 15) / 16 * ((c.T + kChunk - 1) / kChunk);
-  if (groups >= 1024) return launch_down<E, FMT, 4>(g, c.stream);
-  if (groups >= 512 || c.T > 16) return launch_down<E, FMT, 8>(g, c.stream);
-  return launch_down<E, FMT, 16>(g, c.stream);
+static int down_for(const Args& g, hipStream_t s) {
+  return short_rings(g.T, FMT) ? launch_down<E, FMT, 16384>(g, s) : launch_down<E, FMT, 32768>(g, s);
+}
+
+// y = x W^T (dense).
+template <class E, int FMT>
+int run_linear(const Call& c) {
+  return down_for<E, FMT>(args_of(c, c.x, c.D, c.H, c.y), c.stream);
 }
 
 template <class E, int FMT>
 int run_block(const Call& c) {
-  const Args g{c.x, c.wg, c.wu, c.a, c.ids, c.wts, (int)c.T, c.k, c.E, (int)c.H, (int)c.D, (65535u + c.k) / c.k};
+  const BlockPlan p = block_plan(c.T, c.D, c.H, c.k, E::kBytes);
+  Args g = args_of(c, c.x, c.H, c.D, c.ws);
+  g.w0 = c.wg;
+  g.w1 = c.wu;
+  g.ctr = (unsigned*)(c.ws + p.ctr);
+  g.n_ctr = p.n_ctr;
   const int64_t pairs = (c.T < kChunk ? c.T : kChunk) * c.k;
   const int slots = c.ids ? (int)(pairs < c.E ? pairs : c.E) : 1;
-  const int64_t groups = (c.H + 15) / 16 * slots * ((c.T + kChunk - 1) / kChunk);
-  const int rc = groups >= 512 ? launch_gateup<E, FMT, 4>(g, slots, c.stream) : launch_gateup<E, FMT, 8>(g, slots, c.stream);
-  return rc ? rc : run_down<E, FMT>(c, c.a, c.H, c.D);
+  const int rc = short_rings(c.T, FMT) ? launch_gateup<E, FMT, 18432>(g, slots, c.stream)
+                                       : launch_gateup<E, FMT, 36864>(g, slots, c.stream);
+  if (rc) return rc;
+  Args d = args_of(c, c.ws, c.D, c.H, c.y);
+  d.splits = p.splits;
+  d.partial = (float*)(c.ws + p.partial);
+  d.ctr = g.ctr;
+  return down_for<E, FMT>(d, c.stream);
 }
 
 }  // namespace few

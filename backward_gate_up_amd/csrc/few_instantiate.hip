@@ -20,7 +20,7 @@ using InstE = Fp32;
 namespace few {
 template int run_block<InstE, SWIGLU_INST_FMT>(const Call&);
 #if SWIGLU_INST_FMT != 0
-template int run_down<InstE, SWIGLU_INST_FMT>(const Call&, const char*, int64_t, int64_t);
+template int run_linear<InstE, SWIGLU_INST_FMT>(const Call&);
 #endif
 }  // namespace few
 #if SWIGLU_INST_FMT == 0

@@ -6,35 +6,36 @@
 namespace swiglu {
 namespace w4 {
 
-// Byte offsets of a packed weight's parts (each 256-byte aligned).
+// Records of a packed weight (see few::Weight): bytes of one, records and
+// bytes per expert, bytes in all.
 struct Layout {
-  int64_t tiles;   // 1 KiB tiles per expert
-  size_t scales, zeros, total;
+  int rec;
+  int64_t recs, expert;
+  size_t total;
 };
 static inline Layout layout(int64_t experts, int64_t N, int64_t K, int group, bool zeros) {
-  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   Layout l;
-  l.tiles = ((N + 15) / 16) * ((K + 127) / 128);
-  const size_t n = (size_t)(experts * l.tiles);
-  l.scales = n * 1024;
-  l.zeros = up(l.scales + n * 16 * (128 / group) * 2);
-  l.total = l.zeros + (zeros ? up(n * 32) : 0);
+  l.rec = 1024 + 32 * (128 / group) + (zeros ? 32 : 0);
+  l.recs = ((N + 15) / 16) * ((K + 127) / 128);
+  l.expert = l.recs * l.rec;
+  l.total = (size_t)(experts * l.expert);
   return l;
 }
 
-// codes [X][N][K/2], scales [X][N][K/g], zeros [X][N][K/g] (or NULL) to tiles.
-// One thread per 16-byte lane slot; rows and K past the matrix get code and
-// scale 0.
+// codes [X][N][K/2], scales [X][N][K/g], zeros [X][N][K/g] (or NULL) to
+// records. One thread per 16-byte lane slot; rows and K past the matrix get
+// code and scale 0.
 __global__ void w4_pack(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, char* out, Layout l,
                         int64_t experts, int N, int K, int group) {
-  const int64_t n = experts * l.tiles * 64;
+  const int64_t n = experts * l.recs * 64;
   const int nkt = (K + 127) / 128, gp = 128 / group, ng = K / group;
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
     const int lane = (int)(i & 63);
-    const int64_t tile = i >> 6, x = tile / l.tiles, in = tile % l.tiles;
+    const int64_t tile = i >> 6, x = tile / l.recs, in = tile % l.recs;
     const int row = (int)(in / nkt) * 16 + (lane & 15), kt = (int)(in % nkt);
     const int64_t r = x * N + row;
+    char* rec = out + tile * l.rec;
     u32x4_t v{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -48,22 +49,21 @@ __global__ void w4_pack(const uint8_t* codes, const uint16_t* scales, const uint
         }
       }
     }
-    ((u32x4_t*)out)[i] = v;
+    ((u32x4_t*)rec)[lane] = v;
     if (lane < 16) {
-      uint16_t* so = (uint16_t*)(out + l.scales) + (tile * 16 + lane) * gp;
       uint32_t z = 0;
       for (int g = 0; g < gp; ++g) {
         const int at = kt * gp + g;
         const bool ok = row < N && at < ng;
-        so[g] = ok ? scales[r * ng + at] : (uint16_t)0;
+        ((uint16_t*)(rec + 1024))[lane * gp + g] = ok ? scales[r * ng + at] : (uint16_t)0;
         if (zeros && ok) z |= (uint32_t)(zeros[r * ng + at] & 15) << (4 * g);
       }
-      if (zeros) ((uint16_t*)(out + l.zeros))[tile * 16 + lane] = (uint16_t)z;
+      if (zeros) ((uint16_t*)(rec + 1024 + 32 * gp))[lane] = (uint16_t)z;
     }
   }
 }
 
-// Tiles back to rows: W = rnd(scale * (code - zero)), eight K of one row per thread.
+// Records back to rows: W = rnd(scale * (code - zero)), eight K of one row per thread.
 template <class E>
 __global__ void w4_unpack(const char* data, Layout l, int has_zeros, int64_t experts, int N, int K, int group,
                           typename E::elem* w) {
@@ -72,12 +72,12 @@ __global__ void w4_unpack(const char* data, Layout l, int has_zeros, int64_t exp
   typedef typename E::elem vec8 __attribute__((ext_vector_type(8)));
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
     const int64_t r = i / k8, x = r / N;
-    const int row = (int)(r % N), k = (int)(i % k8) * 8, kt = k >> 7, in = k & 127;
-    const int64_t tile = x * l.tiles + (int64_t)(row >> 4) * nkt + kt;
+    const int row = (int)(r % N), k = (int)(i % k8) * 8, in = k & 127;
+    const char* rec = data + x * l.expert + ((int64_t)(row >> 4) * nkt + (k >> 7)) * l.rec;
     const int lane = (row & 15) + 16 * ((in >> 3) & 3), g = in / group;
-    const uint32_t v = ((const uint32_t*)data)[(tile * 64 + lane) * 4 + (in >> 5)];
-    const typename E::elem sc = ((const typename E::elem*)(data + l.scales))[(tile * 16 + (row & 15)) * gp + g];
-    const int z = has_zeros ? (((const uint16_t*)(data + l.zeros))[tile * 16 + (row & 15)] >> (4 * g)) & 15 : 8;
+    const uint32_t v = ((const uint32_t*)rec)[lane * 4 + (in >> 5)];
+    const typename E::elem sc = ((const typename E::elem*)(rec + 1024))[(row & 15) * gp + g];
+    const int z = has_zeros ? (((const uint16_t*)(rec + 1024 + 32 * gp))[row & 15] >> (4 * g)) & 15 : 8;
     vec8 o;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {

@@ -210,10 +210,15 @@ def _expert_shapes(x, wg, wu, wd):
     for t in (wg, wu, wd):
         if t.dtype != x.dtype or t.device != x.device:
             raise ValueError("all tensors must share dtype and device")
-    if w4 and not wg.group == wu.group == wd.group:
-        raise ValueError("the three weights must share their group size")
+    if w4:
+        _same_form(wg, wu, wd)
     _on_gpu(x)
     return E, H, w4
+
+
+def _same_form(wg, wu, wd):
+    if not (wg.group, wg.has_zeros) == (wu.group, wu.has_zeros) == (wd.group, wd.has_zeros):
+        raise ValueError("the three weights must share their group size and have zero points all or none")
 
 
 def moe_experts(x, weights, ids, wg, wu, wd, y=None, workspace=None):
@@ -230,7 +235,7 @@ def moe_experts(x, weights, ids, wg, wu, wd, y=None, workspace=None):
         raise ValueError("weights must be fp32 and ids int32, both [T, k] on x's device")
     k, dt, L = ids.shape[1], _code(x), _L.lib()
     y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, H, k, dt), x.device)
+    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, k, dt), x.device)
     nbytes = ws.numel() * ws.element_size()
     if w4:
         rc = L.swiglu_mlp_moe_experts_w4(_ptr(x), _ptr(weights), _ptr(ids), wg._ref, wu._ref, wd._ref, _ptr(y),
@@ -255,7 +260,7 @@ def moe_infer(x, w_router, wg, wu, wd, top_k, renormalize=True, y=None, workspac
         raise ValueError(f"the router has {E} experts, the weights {E2}")
     dt, L = _code(x), _L.lib()
     y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, H, top_k, dt), x.device)
+    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, top_k, dt), x.device)
     nbytes = ws.numel() * ws.element_size()
     if w4:
         rc = L.swiglu_mlp_moe_infer_w4(_ptr(x), w_router.data_ptr(), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws),
@@ -286,7 +291,7 @@ def w4_linear(x, w, y=None):
 
 def infer_w4(x, wg, wu, wd, y=None, workspace=None):
     """The no-grad SwiGLU block Y = (SiLU(x Wg^T) * (x Wu^T)) Wd^T with 4-bit
-    weights wg, wu [H, D] and wd [D, H]; two launches, workspace A[T, H]."""
+    weights wg, wu [H, D] and wd [D, H]; two launches."""
     _no_grad(x)
     x = x.contiguous()
     if x.dim() != 2 or len(wg.shape) != 2:
@@ -299,12 +304,11 @@ def infer_w4(x, wg, wu, wd, y=None, workspace=None):
     for t in (wg, wu, wd):
         if t.dtype != x.dtype or t.device != x.device:
             raise ValueError("all tensors must share dtype and device")
-    if not wg.group == wu.group == wd.group:
-        raise ValueError("the three weights must share their group size")
+    _same_form(wg, wu, wd)
     _on_gpu(x)
     dt, L = _DT16[x.dtype], _L.lib()
     y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, T * H * 2, x.device)
+    ws = _workspace(workspace, L.swiglu_mlp_w4_infer_workspace_bytes(T, D, H, dt), x.device)
     rc = L.swiglu_mlp_w4_infer(_ptr(x), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), T,
                                dt, _stream(x.device))
     _check(rc, "swiglu_mlp_w4_infer")

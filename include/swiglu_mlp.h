@@ -252,10 +252,12 @@ typedef struct {
 int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, int64_t T,
                          int64_t D, int64_t E, int64_t k, int renorm, int dtype, hipStream_t stream);
 
-/* Bytes of a mixture's workspace: the A plane [T k, H] and the router's
- * weights and ids, each 256-byte aligned. Contents on entry do not matter;
- * calls that share one must be stream-ordered. 0 on bad args. */
-size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t H, int64_t k, int dtype);
+/* Bytes of a mixture's workspace: the A plane [T k, H], the arrival counters
+ * and fp32 partial sums of the down projection where its K is split over
+ * workgroups, and the router's weights and ids, each 256-byte aligned.
+ * Contents on entry do not matter; calls that share one must be
+ * stream-ordered. 0 on bad args. */
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t k, int dtype);
 
 int swiglu_mlp_moe_experts(const void* X, const float* weights, const int32_t* ids, const void* Wg,
                            const void* Wu, const void* Wd, void* Y, void* workspace,
@@ -285,8 +287,10 @@ int swiglu_mlp_w4_dequantize(const swiglu_w4_t* w, void* W, int dtype, hipStream
 int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T, int dtype,
                          hipStream_t stream);
 
-/* The dense block with 4-bit weights, two launches; workspace: A [T, H]. */
-size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t H, int dtype);
+/* The dense block with 4-bit weights, two launches; workspace: A [T, H], then
+ * counters and partial sums as a mixture's. The three weights share group
+ * size and have zero points all or none. */
+size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t D, int64_t H, int dtype);
 int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* Wg, const swiglu_w4_t* Wu,
                         const swiglu_w4_t* Wd, void* Y, void* workspace, size_t workspace_bytes,
                         int64_t T, int dtype, hipStream_t stream);

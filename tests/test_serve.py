@@ -173,10 +173,11 @@ def test_host_validation_codes():
     assert block(wu=_w4(4, 128, 64)) == 2 and block(wd=_w4(5)) == 2 and block(wu=_w4(4, group=64)) == 2
     assert block(ws=None, n=0) == 6 and block(n=4 * 64 * 2 - 1) == 6
     # the queries
-    assert L.swiglu_mlp_moe_workspace_bytes(4, 128, 2, 0) == 8 * 128 * 2 + 256 + 256
-    assert L.swiglu_mlp_moe_workspace_bytes(0, 128, 2, 0) == 0 and L.swiglu_mlp_moe_workspace_bytes(4, 128, 33, 0) == 0
-    assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 0) == 4 * 1024 + 4 * 16 * 4 * 2
-    assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 1) == 4 * 1024 + 4 * 16 * 4 * 2 + 256
+    ws = L.swiglu_mlp_moe_workspace_bytes
+    assert ws(4, 64, 128, 2, 0) >= 8 * 128 * 2 + 256 + 256 and ws(200, 8192, 128, 2, 0) == 400 * 128 * 2 + 2 * 1792
+    assert ws(0, 64, 128, 2, 0) == 0 and ws(4, 64, 128, 33, 0) == 0 and ws(4, 60, 128, 2, 0) == 0
+    assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 0) == 4 * (1024 + 16 * 4 * 2)
+    assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 1) == 4 * (1024 + 16 * 4 * 2 + 32)
     assert L.swiglu_mlp_w4_bytes(1, 64, 100, 32, 0) == 0
 
 
@@ -459,7 +460,7 @@ def test_strides_streams_buffers_and_graph():
     assert torch.equal(m.moe_experts(x[3:], p[3:], ids[3:], *w), y[3:])
     # another stream, with the caller's own buffers
     out = torch.empty_like(y)
-    need = _lib.lib().swiglu_mlp_moe_workspace_bytes(T, H, k, 0)
+    need = _lib.lib().swiglu_mlp_moe_workspace_bytes(T, D, H, k, 0)
     buf = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
