@@ -89,6 +89,19 @@ __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
+// A descriptor that is the same on every lane, in scalar registers (one that
+// changes inside a loop the compiler may keep in vector registers, which the
+// loads from inline assembly cannot take). A vector instruction's write of a
+// scalar register needs 5 wait states before a memory instruction reads it,
+// and the compiler does not know that the assembly is one: they are put here.
+__device__ __forceinline__ i32x4_t scalar_rsrc(i32x4_t r) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
+  r[3] = kRsrcWord3;
+  asm volatile("s_nop 4" : "+s"(r));
+  return r;
+}
+
 // Four bytes per lane to LDS address lds + 4 * lane (see dma16).
 __device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff) {
   lds = __builtin_amdgcn_readfirstlane(lds);
@@ -96,16 +109,18 @@ __device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff) {
 }
 
 // ---- streams ------------------------------------------------------------------
-// A stream adds the products of the K stages [s0, s1) to acc[n][m]: NT weight
-// blocks of 16 rows x token rows in blocks of 16. Its ring of NS slots is the
-// wave's own: stage s waits for its own loads only (vmcnt counts a wave's
-// loads in issue order), reads slot s % NS, and refills it. Stages past the
-// run and bytes past K are asked for beyond the buffers' range, which loads
-// zeros without a memory access: no remainder code, and neither the next row
-// nor a NaN there is multiplied in.
+// A stage holds some K of NT weight blocks of 16 rows and of XR token rows; its
+// products are added to acc[n][m]. A wave's stages run through its ring of NS
+// slots: a stage waits for its own loads only (vmcnt counts a wave's loads in
+// issue order), its slot is read, and refilled with the stage NS further on,
+// of whichever weight rows or expert that belongs to. Stages past the end and
+// bytes past K are asked for beyond the buffers' range, which loads zeros
+// without a memory access: no remainder code, and neither the next row nor a
+// NaN there is multiplied in.
 //
-// XR: token rows held per stage, 16, 32 or 64, or fewer than 16 (what one
-// load instruction covers): then rows XR .. 15 of the operand repeat them.
+// XR: token rows per stage, 16 or 32, or fewer (what one load instruction
+// covers): then rows XR .. 15 of the operand repeat them. A longer list of
+// tokens takes several passes over the weights.
 
 // Rows of 16-bit or fp32 values: a stage is 128 bytes of K, 16 rows x 128 B in
 // two loads of 8 rows. Chunk c of row r sits at position c ^ kc_swz(r), so the
@@ -126,24 +141,25 @@ struct RowStream {
   // the token row (0 .. XR - 1) whose chunk this lane fetches in load j
   static __device__ __forceinline__ int x_row(int j, int lane) { return 8 * j + (lane >> 3); }
 
-  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, const Args& g, const char* xb,
-                                       uint32_t x_bytes, const uint32_t (&row)[XD], int lane) {
+  // what does not change over a launch
+  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int lane) {
     kb = g.K * E::kBytes;
-    const int rows = min(16, g.N - row0);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)  // rows past N read as zeros
-      rw[n] = rsrc_words(wt[n]->w + (int64_t)e * wt[n]->expert + (int64_t)row0 * kb, (int64_t)rows * kb);
     rx = rsrc_words(xb, x_bytes);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = 8 * j + (lane >> 3);
-      w_off[j] = r < rows ? (uint32_t)r * (uint32_t)kb : kOOB;
-    }
-#pragma unroll
-    for (int j = 0; j < XD; ++j) x_off[j] = row[j];
+    for (int j = 0; j < 2; ++j) w_off[j] = (uint32_t)(8 * j + (lane >> 3)) * (uint32_t)kb;
   }
-  __device__ __forceinline__ void issue(uint32_t slot, int s, int s1, int lane) const {
-    const int end = s < s1 ? kb : 0;
+  // block n: rows row0 .. row0 + 15 of expert e's weight; rows past N read as zeros
+  __device__ __forceinline__ void weight(int n, const Weight& wt, int e, int row0, int N) {
+    const int rows = max(0, min(16, N - row0));
+    rw[n] = rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)row0 * kb, (int64_t)rows * kb);
+  }
+  // loads stage s into the slot; not live: zeros
+  __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
+    const int end = live ? kb : 0;
+    const i32x4_t xr = scalar_rsrc(rx);
+    i32x4_t w[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) w[n] = scalar_rsrc(rw[n]);
 #pragma unroll
     for (int j = 0; j < (XD > 2 ? XD : 2); ++j) {
       const int r = 8 * j + (lane >> 3);
@@ -151,9 +167,9 @@ struct RowStream {
       const bool in = off < end;
       if (j < 2) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) dma16(slot + n * 2048 + j * 1024, rw[n], in ? w_off[j] + off : kOOB, 0u);
+        for (int n = 0; n < NT; ++n) dma16(slot + n * 2048 + j * 1024, w[n], in ? w_off[j] + off : kOOB, 0u);
       }
-      if (j < XD) dma16(slot + NT * 2048 + j * 1024, rx, in ? x_off[j] + off : kOOB, 0u);
+      if (j < XD) dma16(slot + NT * 2048 + j * 1024, xr, in ? x_off[j] + off : kOOB, 0u);
     }
   }
   __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane) const {
@@ -202,33 +218,31 @@ struct W4Stream {
   static __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
   static __device__ __forceinline__ int x_row(int j, int lane) { return 4 * j + (lane >> 4); }
 
-  __device__ __forceinline__ void init(const Weight* const (&wt)[NT], int e, int row0, const Args& g, const char* xb,
-                                       uint32_t x_bytes, const uint32_t (&row)[XD], int lane) {
+  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int) {
     kb = g.K * 2;
     zeros = g.zeros;
     rec = 1024 + 32 * GP + (zeros ? 32 : 0);
-    const int len = stages(g.K) * rec;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      rw[n] = rsrc_words(wt[n]->w + (int64_t)e * wt[n]->expert + (int64_t)(row0 >> 4) * len, len);
     rx = rsrc_words(xb, x_bytes);
-#pragma unroll
-    for (int j = 0; j < XD; ++j) x_off[j] = row[j];
   }
-  __device__ __forceinline__ void issue(uint32_t slot, int s, int s1, int lane) const {
-    const bool live = s < s1;
+  __device__ __forceinline__ void weight(int n, const Weight& wt, int e, int row0, int N) {
+    const int len = row0 < N ? stages(kb >> 1) * rec : 0;
+    rw[n] = rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)(row0 >> 4) * len, len);
+  }
+  __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
     const uint32_t at = (uint32_t)s * rec;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      dma16(slot + n * WS, rw[n], live ? at + lane * 16 : kOOB, 0u);
-      dma4(slot + n * WS + 1024, rw[n], live && 1024 + lane * 4 < rec ? at + 1024 + lane * 4 : kOOB);
+      const i32x4_t w = scalar_rsrc(rw[n]);
+      dma16(slot + n * WS, w, live ? at + lane * 16 : kOOB, 0u);
+      dma4(slot + n * WS + 1024, w, live && 1024 + lane * 4 < rec ? at + 1024 + lane * 4 : kOOB);
     }
     const int end = live ? kb : 0;
+    const i32x4_t xr = scalar_rsrc(rx);
 #pragma unroll
     for (int j = 0; j < XD; ++j) {
       const int r = 4 * j + (lane >> 4);
       const int off = s * 256 + (((lane & 15) ^ (r & 15)) << 4);
-      dma16(slot + NT * WS + j * 1024, rx, off < end ? x_off[j] + off : kOOB, 0u);
+      dma16(slot + NT * WS + j * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
     }
   }
   // eight codes of one dword as the MFMA operand OFF + q
@@ -299,24 +313,30 @@ struct StreamOf<E, 0, NT, XR, LW> {
   using type = RowStream<E, NT, XR, LW>;
 };
 
-// Runs stages [s0, s1) of a stream in the wave's ring (LDS address and pointer).
-template <class S, int NT>
-__device__ __forceinline__ void run_stream(const S& st, f32x4_t (&acc)[NT][S::MT], char* ring, int s0, int s1, int lane) {
-  if (s0 >= s1) return;
-  const uint32_t at = lds_addr(ring);
-#pragma unroll
-  for (int p = 0; p < S::NS; ++p) st.issue(at + p * S::SLOT, s0 + p, s1, lane);
-  int slot = 0;
+// The wave's ring: R.step<S>() = wait for the oldest stage, multiply it, and
+// fetch the stage that `issue` (a callable: LDS slot address) says is next.
+template <class S>
+struct Ring {
+  char* lds;
+  uint32_t addr;
+  int slot;
+  template <class Issue>
+  __device__ __forceinline__ void start(char* p, Issue&& issue) {
+    lds = p;
+    addr = lds_addr(p);
+    slot = 0;
 #pragma unroll 1
-  for (int s = s0; s < s1; ++s) {
+    for (int i = 0; i < S::NS; ++i) issue(addr + i * S::SLOT);
+  }
+  template <int NT, class Issue>
+  __device__ __forceinline__ void step(const S& st, f32x4_t (&acc)[NT][S::MT], int lane, Issue&& issue) {
     ring::wait_vmcnt<(S::NS - 1) * S::D>();
-    st.compute(ring + slot * S::SLOT, acc, lane);
+    st.compute(lds + slot * S::SLOT, acc, lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
-    st.issue(at + slot * S::SLOT, s + S::NS, s1, lane);
+    issue(addr + slot * S::SLOT);
     slot = slot + 1 == S::NS ? 0 : slot + 1;
   }
-  ring::wait_vmcnt<0>();  // the surplus stages' loads (zeros) have landed too
-}
+};
 
 // ---- a chunk's choices --------------------------------------------------------
 // ids of the chunk's pairs, and the experts that occur, in ascending order.
@@ -392,245 +412,286 @@ __device__ __forceinline__ Picked mask_pairs(uint64_t m, int lane) {
   return {v, (int)__popcll(m)};
 }
 
+// Walks the experts that occur in a chunk, and for each the passes of at most
+// XR of its pairs. Dense: one expert, all tokens.
+struct Walk {
+  const Args* g;
+  const Choices* ch;  // more than 64 pairs
+  int16_t* list;
+  int P, id;          // id: lane's pair's expert (at most 64 pairs)
+  uint64_t left;
+  int hits, i, e, first, total;
+  Picked p;           // pairs [first, first + 64) of the expert's list
+
+  // All threads (a barrier in the last case). Stands before the first expert.
+  __device__ __forceinline__ void open(const Args& a, Choices& c, int16_t* scratch, int t0, int tc, int lane) {
+    g = &a;
+    ch = &c;
+    list = scratch;
+    P = tc * a.k;
+    i = -1;
+    first = total = 0;
+    left = 0;
+    if (!a.ids) {
+      hits = 1;
+    } else if (P <= 64) {
+      id = lane < P ? a.ids[(int64_t)t0 * a.k + lane] : -1;
+      left = __ballot((unsigned)id < (unsigned)a.E);
+      hits = 0;
+      for (uint64_t l = left; l; ++hits)
+        l &= ~__ballot(id == __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)l) - 1));
+    } else {
+      read_choices(c, a, t0, tc);
+      hits = __builtin_amdgcn_readfirstlane(c.hits);
+    }
+  }
+  // The n-th expert (n > i), first pass.
+  __device__ __forceinline__ void expert(int n, int lane) {
+    first = 0;
+    if (!g->ids) {
+      e = 0;
+      p = {lane, P};
+      total = P;
+    } else if (P <= 64) {
+      uint64_t m = 0;
+      for (; i < n; ++i) {
+        e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+        m = __ballot(id == e);
+        left &= ~m;
+      }
+      p = mask_pairs(m, lane);
+      total = p.n;
+    } else {
+      e = __builtin_amdgcn_readfirstlane(ch->expert[n]);
+      p = list_pairs(*ch, P, e, 0, list, lane, total);
+    }
+    i = n;
+  }
+  // Moves to the expert's next pass, if there is one.
+  __device__ __forceinline__ bool next_pass(int XR, int lane) {
+    if (first + XR >= total) return false;
+    first += XR;
+    if ((first & 63) == 0) p = list_pairs(*ch, P, e, first >> 6, list, lane, total);
+    return true;
+  }
+  __device__ __forceinline__ int rows(int XR) const { return min(XR, total - first); }
+  // lane i: the pass's i-th pair
+  __device__ __forceinline__ int pair(int i) const { return __shfl(p.pair, ((first & 63) + i) & 63); }
+};
+
 // ---- gate/up ------------------------------------------------------------------
-template <class E, int FMT, int XR, int LW>
-__device__ __forceinline__ void gateup_block(const Args& g, int e, int row0, int t0, const Picked& p, int first, int n,
-                                             char* lds) {
-  using S = typename StreamOf<E, FMT, 2, XR, LW>::type;
-  constexpr int MT = S::MT;
-  static_assert(NW * 2 * MT * 1024 <= NW * LW, "the sums fit in the rings");
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t row[S::XD];
-#pragma unroll
-  for (int j = 0; j < S::XD; ++j) {
-    const int i = S::x_row(j, lane);
-    const int pair = __shfl(p.pair, first + i);
-    row[j] = i < n ? ((pair * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB;
-  }
-  S s;
-  const Weight* const w[2] = {&g.w0, &g.w1};
-  s.init(w, e, row0, g, g.x + (int64_t)t0 * g.K * E::kBytes, (uint32_t)(min(kChunk, g.T - t0) * g.K) * E::kBytes, row,
-         lane);
-  const int stages = S::stages(g.K), per = (stages + NW - 1) / NW;
-  f32x4_t acc[2][MT] = {};
-  run_stream<S, 2>(s, acc, lds + wave * LW, wave * per, min(stages, (wave + 1) * per), lane);
-  // the waves' sums meet in LDS; thread -> (token row, hidden column), waves added in order
-  float* red = (float*)lds;
-  __syncthreads();
-#pragma unroll
-  for (int n2 = 0; n2 < 2; ++n2)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) *(f32x4_t*)(red + (((wave * 2 + n2) * MT + m) * 64 + lane) * 4) = acc[n2][m];
-  __syncthreads();
-  for (int i0 = 0; i0 < MT * 256; i0 += NW * 64) {
-    const int i = i0 + threadIdx.x;
-    const int col = i & 15, r = i >> 4;  // token row of the list, hidden column
-    const int at = ((r >> 4) * 64 + ((r & 15) >> 2) * 16 + col) * 4 + (r & 3);
-    float gate = 0.f, up = 0.f;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) {
-      gate += red[(v * 2 + 0) * MT * 256 + at];
-      up += red[(v * 2 + 1) * MT * 256 + at];
-    }
-    const int pair = __shfl(p.pair, first + r);
-    const int h = row0 + col;
-    if (r < n && h < g.N) {
-      // g and u stay in fp32; A is rounded once, to the storage type the
-      // down projection's matrix instructions take
-      ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] =
-          E::from_f32(gate * sigmoid_f32<E>(gate) * up);
-    }
-  }
-  __syncthreads();
-}
-
-// The block with as many token rows as the list needs. 4 bits: at most 32 (64
-// rows of 256 bytes would leave no room for a ring); more go in two passes.
-template <class E, int FMT, int LW>
-__device__ __forceinline__ void gateup_rows(const Args& g, int e, int row0, int t0, const Picked& p, char* lds) {
-  constexpr int kFew = FMT ? 4 : 8;
-  if (p.n <= kFew) gateup_block<E, FMT, kFew, LW>(g, e, row0, t0, p, 0, p.n, lds);
-  else if (p.n <= 16) gateup_block<E, FMT, 16, LW>(g, e, row0, t0, p, 0, p.n, lds);
-  else if constexpr (LW >= 32768) {
-    if (FMT || p.n <= 32) {
-      for (int f = 0; f < p.n; f += 32) gateup_block<E, FMT, 32, LW>(g, e, row0, t0, p, f, min(32, p.n - f), lds);
-    } else if constexpr (FMT == 0) {
-      gateup_block<E, FMT, 64, LW>(g, e, row0, t0, p, 0, p.n, lds);
-    }
-  } else {
-    for (int f = 0; f < p.n; f += 16) gateup_block<E, FMT, 16, LW>(g, e, row0, t0, p, f, min(16, p.n - f), lds);
-  }
-}
-
-// LW: ring bytes per wave. 18 KiB lets two workgroups share a CU; 36 KiB (one)
-// is for longer lists of tokens.
-template <class E, int FMT, int LW>
+// An item is a tile of 16 HB hidden columns of one pass; the workgroup takes a
+// run of items, its waves a quarter of K each. The rings run on from item to
+// item: while the waves' sums of one meet in LDS, the loads of the next are
+// in flight.
+template <class E, int FMT, int HB, int XR, int LW>
 __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
+  using S = typename StreamOf<E, FMT, 2 * HB, XR, LW>::type;
+  constexpr int MT = S::MT, NT = 2 * HB;
   __shared__ __attribute__((aligned(1024))) char lds[NW * LW];
+  __shared__ __attribute__((aligned(16))) float red[NW * NT * MT * 256];
   __shared__ Choices ch;
   __shared__ int16_t list[NW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0), P = tc * g.k;
-  const int row0 = blockIdx.x * 16, slot = blockIdx.y;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0);
+  if (blockIdx.x == 0 && blockIdx.z == 0)
     for (int i = threadIdx.x; i < g.n_ctr; i += NW * 64) g.ctr[i] = 0u;
-  // the workgroup's expert, and how to list its pairs: all tokens (dense), a
-  // mask of at most 64 pairs, or a scan of the chunk's choices in LDS
-  const bool small = P <= 64;
-  int e = 0, total = tc;
-  Picked p{lane, tc};
-  if (g.ids && small) {
-    const int id = lane < P ? g.ids[(int64_t)t0 * g.k + lane] : -1;
-    uint64_t left = __ballot((unsigned)id < (unsigned)g.E), m = 0;
-    for (int i = 0; i <= slot; ++i) {
-      if (!left) return;  // fewer experts occur than there are slots
-      e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
-      m = __ballot(id == e);
-      left &= ~m;
+  Walk use;  // the item being multiplied
+  use.open(g, ch, list[wave], t0, tc, lane);
+  const int tiles = (g.N + 16 * HB - 1) / (16 * HB), items = use.hits * tiles;
+  int item = (int)((int64_t)items * blockIdx.x / gridDim.x);
+  const int last = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+  if (item >= last) return;
+  Walk get = use;  // the item being loaded
+  S st;
+  st.init(g, g.x + (int64_t)t0 * g.K * E::kBytes, (uint32_t)(tc * g.K) * E::kBytes, lane);
+  const int stages = S::stages(g.K), per = (stages + NW - 1) / NW;
+  const int s0 = wave * per, s1 = min(stages, s0 + per);
+
+  // loading side: the next stage of the current item, then the next item
+  int get_item = item, get_s = s0;
+  bool more = true;
+  auto set_rows = [&] {
+    const int n = get.rows(XR);
+#pragma unroll
+    for (int j = 0; j < S::XD; ++j) {
+      const int i = S::x_row(j, lane), pair = get.pair(i);
+      st.x_off[j] = i < n ? ((pair * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB;
     }
-    p = mask_pairs(m, lane);
-  } else if (g.ids) {
-    read_choices(ch, g, t0, tc);
-    if (slot >= ch.hits) return;
-    e = ch.expert[slot];
+  };
+  auto set_weights = [&] {
+    const int row0 = (get_item % tiles) * 16 * HB;
+#pragma unroll
+    for (int b = 0; b < HB; ++b) {
+      st.weight(2 * b, g.w0, get.e, row0 + 16 * b, g.N);
+      st.weight(2 * b + 1, g.w1, get.e, row0 + 16 * b, g.N);
+    }
+  };
+  auto issue = [&](uint32_t slot) {
+    st.issue(slot, get_s, more && get_s < s1, lane);
+    if (++get_s < s0 + per || !more) return;
+    get_s = s0;
+    if (get.next_pass(XR, lane)) {
+      set_rows();
+      return;
+    }
+    more = ++get_item < last;
+    if (!more) return;
+    if (get.first || get_item % tiles == 0) {
+      get.expert(get_item / tiles, lane);
+      set_rows();
+    }
+    set_weights();
+  };
+  get.expert(item / tiles, lane);
+  set_rows();
+  set_weights();
+  Ring<S> r;
+  r.start(lds + wave * LW, issue);
+
+  use.expert(item / tiles, lane);
+  while (true) {
+    f32x4_t acc[NT][MT] = {};
+#pragma unroll 1
+    for (int s = 0; s < per; ++s) r.step(st, acc, lane, issue);
+    ring::lds_barrier();  // the last item's sums have been read
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) *(f32x4_t*)(red + (((wave * NT + n) * MT + m) * 64 + lane) * 4) = acc[n][m];
+    ring::lds_barrier();
+    // thread -> (token row of the pass, hidden column); the waves' sums in order
+    const int n = use.rows(XR), row0 = (item % tiles) * 16 * HB;
+#pragma unroll 1
+    for (int i0 = 0; i0 < HB * MT * 256; i0 += NW * 64) {
+      const int i = i0 + threadIdx.x, b = i / (MT * 256);
+      const int col = i & 15, row = (i >> 4) % (16 * MT);
+      const int at = ((row >> 4) * 64 + ((row & 15) >> 2) * 16 + col) * 4 + (row & 3);
+      float gate = 0.f, up = 0.f;
+#pragma unroll
+      for (int v = 0; v < NW; ++v) {
+        gate += red[(v * NT + 2 * b) * MT * 256 + at];
+        up += red[(v * NT + 2 * b + 1) * MT * 256 + at];
+      }
+      const int pair = use.pair(row), h = row0 + 16 * b + col;
+      if (row < n && h < g.N) {
+        // g and u stay in fp32; A is rounded once, to the storage type the
+        // down projection's matrix instructions take
+        ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] =
+            E::from_f32(gate * sigmoid_f32<E>(gate) * up);
+      }
+    }
+    if (use.next_pass(XR, lane)) continue;
+    if (++item >= last) break;
+    if (use.first || item % tiles == 0) use.expert(item / tiles, lane);
   }
-  for (int pass = 0; 64 * pass < total; ++pass) {
-    if (g.ids && !small) p = list_pairs(ch, P, e, pass, list[wave], lane, total);
-    gateup_rows<E, FMT, LW>(g, e, row0, t0, p, lds);
-  }
+  ring::wait_vmcnt<0>();  // no load may land in LDS after the workgroup's end
 }
 
 // ---- down -----------------------------------------------------------------------
-// The K axis of an output tile is the list of (expert that occurs, K stage); the
-// splits x NW waves take equal runs of it. At an expert's end the block of sums
-// is weighted and added to the wave's own [token][column] tile in LDS.
-template <class E, int FMT, int XR, int LW>
-__device__ __forceinline__ void down_block(const Args& g, int e, int row0, int t0, const Picked& p, int first, int n,
-                                           int s0, int s1, char* ring, float* y) {
-  using S = typename StreamOf<E, FMT, 1, XR, LW>::type;
-  constexpr int MT = S::MT;
-  const int lane = threadIdx.x & 63;
-  const bool routed = g.ids != nullptr;
-  uint32_t row[S::XD];
-#pragma unroll
-  for (int j = 0; j < S::XD; ++j) {
-    const int i = S::x_row(j, lane);
-    const int pair = __shfl(p.pair, first + i);
-    row[j] = i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB;
-  }
-  // this lane's output rows are the list's 16 m + 4 (lane / 16) + j
-  const int mine = __shfl(p.pair, (first + lane) & 63);
-  const float wt = routed && lane < n ? g.wts[(int64_t)t0 * g.k + mine] : 1.0f;
-  S s;
-  const Weight* const w[1] = {&g.w0};
-  s.init(w, e, row0, g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes,
-         (uint32_t)(min(kChunk, g.T - t0) * g.k * g.K) * E::kBytes, row, lane);
-  f32x4_t acc[1][MT] = {};
-  run_stream<S, 1>(s, acc, ring, s0, s1, lane);
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    // one group of 16 lanes (4 token rows) at a time: a token listed twice
-    // for one expert is then added twice, in order
-#pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 16 * m + 4 * q + j;
-        if (i < n) {
-          const int pair = __builtin_amdgcn_readlane(mine, i);
-          const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wt), i));
-          if ((lane >> 4) == q) y[((pair * g.kinv) >> 16) * 16 + (lane & 15)] += f * acc[0][m][j];
-        }
-      }
-    }
-  }
-}
-
-template <class E, int FMT, int LW>
-__device__ __forceinline__ void down_rows(const Args& g, int e, int row0, int t0, const Picked& p, int s0, int s1,
-                                          char* ring, float* y) {
-  constexpr int kFew = FMT ? 4 : 8;
-  if (p.n <= kFew) down_block<E, FMT, kFew, LW>(g, e, row0, t0, p, 0, p.n, s0, s1, ring, y);
-  else if (p.n <= 16) down_block<E, FMT, 16, LW>(g, e, row0, t0, p, 0, p.n, s0, s1, ring, y);
-  else if constexpr (LW >= 32768) {
-    if (FMT || p.n <= 32) {
-      for (int f = 0; f < p.n; f += 32)
-        down_block<E, FMT, 32, LW>(g, e, row0, t0, p, f, min(32, p.n - f), s0, s1, ring, y);
-    } else if constexpr (FMT == 0) {
-      down_block<E, FMT, 64, LW>(g, e, row0, t0, p, 0, p.n, s0, s1, ring, y);
-    }
-  } else {
-    for (int f = 0; f < p.n; f += 16)
-      down_block<E, FMT, 16, LW>(g, e, row0, t0, p, f, min(16, p.n - f), s0, s1, ring, y);
-  }
-}
-
-// LW 16 KiB: two workgroups per CU (at most 16 tokens), 32 KiB: one.
-template <class E, int FMT, int LW>
+// The K axis of an output tile of 16 NT columns is the list of (expert that
+// occurs, K stage); the splits x NW waves take equal runs of it. At an expert's
+// end the block of sums is weighted and added to the wave's own
+// [token][column] tile in LDS. TC: tokens that tile has room for.
+template <class E, int FMT, int NT, int XR, int LW, int TC>
 __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
-  constexpr int YT = LW >= 32768 ? kChunk : 16;  // tokens
+  using S = typename StreamOf<E, FMT, NT, XR, LW>::type;
+  constexpr int MT = S::MT, C = 16 * NT;
   __shared__ __attribute__((aligned(1024))) char lds[NW * LW];
-  __shared__ __attribute__((aligned(16))) float ysum[NW][YT * 16];
+  __shared__ __attribute__((aligned(16))) float ysum[NW][TC * C];
   __shared__ Choices ch;
   __shared__ int16_t list[NW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0), P = tc * g.k;
-  const int row0 = blockIdx.x * 16;
-  char* ring = lds + wave * LW;
+  const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0);
+  const int col0 = blockIdx.x * C;
+  const bool routed = g.ids != nullptr;
   float* y = ysum[wave];
-  for (int i = lane; i < tc * 16; i += 64) y[i] = 0.f;
-  const int stages = StreamOf<E, FMT, 1, 16, LW>::type::stages(g.K);
-  const int parts = g.splits * NW, part = blockIdx.y * NW + wave;
-  // the experts that occur: one (dense), those of at most 64 pairs in
-  // registers, or the chunk's choices in LDS
-  const bool small = P <= 64;
-  int hits = 1, id = -1;
-  uint64_t left = 0;
-  if (g.ids && small) {
-    id = lane < P ? g.ids[(int64_t)t0 * g.k + lane] : -1;
-    left = __ballot((unsigned)id < (unsigned)g.E);
-    hits = 0;
-    for (uint64_t l = left; l; ++hits)
-      l &= ~__ballot(id == __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)l) - 1));
-  } else if (g.ids) {
-    read_choices(ch, g, t0, tc);
-    hits = ch.hits;
-  }
-  // the wave's run [at, end) of the tile's hits * stages
-  int at = (int)((int64_t)hits * stages * part / parts);
-  const int end = (int)((int64_t)hits * stages * (part + 1) / parts);
-  int i = g.ids && small ? 0 : at / stages;  // small: experts are found one after another
-  while (at < end) {
-    int e = 0, total = tc;
-    Picked p{lane, tc};
-    if (g.ids && small) {
-      e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
-      const uint64_t m = __ballot(id == e);
-      left &= ~m;
-      if ((i + 1) * stages <= at) {
-        ++i;
-        continue;
+  for (int i = lane; i < tc * C; i += 64) y[i] = 0.f;
+  Walk use;
+  use.open(g, ch, list[wave], t0, tc, lane);
+  const int stages = S::stages(g.K), parts = g.splits * NW, part = blockIdx.y * NW + wave;
+  int at = (int)((int64_t)use.hits * stages * part / parts);
+  const int end = (int)((int64_t)use.hits * stages * (part + 1) / parts);
+  if (at < end) {
+    Walk get = use;
+    S st;
+    st.init(g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, (uint32_t)(tc * g.k * g.K) * E::kBytes, lane);
+    auto set_rows = [&] {
+      const int n = get.rows(XR);
+#pragma unroll
+      for (int j = 0; j < S::XD; ++j) {
+        const int i = S::x_row(j, lane), pair = get.pair(i);
+        st.x_off[j] = i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB;
       }
-      p = mask_pairs(m, lane);
-    } else if (g.ids) {
-      e = ch.expert[i];
+    };
+    // the run's stages of the n-th expert
+    const int run0 = at;
+    auto begin_of = [&](int n) { return max(0, run0 - n * stages); };
+    auto end_of = [&](int n) { return min(stages, end - n * stages); };
+    int get_s = 0, get_end = 0;
+    bool more = true;
+    auto open_expert = [&](int n) {
+      get.expert(n, lane);
+      set_rows();
+#pragma unroll
+      for (int b = 0; b < NT; ++b) st.weight(b, g.w0, get.e, col0 + 16 * b, g.N);
+      get_s = begin_of(n);
+      get_end = end_of(n);
+    };
+    auto issue = [&](uint32_t slot) {
+      st.issue(slot, get_s, more, lane);
+      if (!more || ++get_s < get_end) return;
+      if (get.next_pass(XR, lane)) {
+        set_rows();
+        get_s = begin_of(get.i);
+        return;
+      }
+      more = (get.i + 1) * stages < end;
+      if (more) open_expert(get.i + 1);
+    };
+    open_expert(at / stages);
+    Ring<S> r;
+    r.start(lds + wave * LW, issue);
+    for (int n = at / stages; n * stages < end; ++n) {
+      use.expert(n, lane);
+      const int count = end_of(n) - begin_of(n);
+      do {
+        const int rows = use.rows(XR), mine = use.pair(lane);
+        const float wt = routed && lane < rows ? g.wts[(int64_t)t0 * g.k + mine] : 1.0f;
+        f32x4_t acc[NT][MT] = {};
+#pragma unroll 1
+        for (int s = 0; s < count; ++s) r.step(st, acc, lane, issue);
+        // one token row at a time: a token listed twice for one expert is
+        // then added twice, in order
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int i = 16 * m + 4 * q + j;
+              if (i < rows) {
+                const int pair = __builtin_amdgcn_readlane(mine, i);
+                const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wt), i));
+                if ((lane >> 4) == q) {
+#pragma unroll
+                  for (int b = 0; b < NT; ++b)
+                    y[((pair * g.kinv) >> 16) * C + 16 * b + (lane & 15)] += f * acc[b][m][j];
+                }
+              }
+            }
+      } while (use.next_pass(XR, lane));
     }
-    const int s0 = at - i * stages, s1 = min(stages, s0 + end - at);
-    for (int pass = 0; 64 * pass < total; ++pass) {
-      if (g.ids && !small) p = list_pairs(ch, P, e, pass, list[wave], lane, total);
-      down_rows<E, FMT, LW>(g, e, row0, t0, p, s0, s1, ring, y);
-    }
-    at += s1 - s0;
-    ++i;
+    ring::wait_vmcnt<0>();  // no load may land in LDS after the rings' end
   }
   __syncthreads();
   // four columns of one token per thread; the waves' sums in order
   const bool direct = g.splits == 1;
-  for (int i = threadIdx.x; i < tc * 4; i += NW * 64) {
+  for (int i = threadIdx.x; i < tc * (C / 4); i += NW * 64) {
     f32x4_t v{};
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += *(const f32x4_t*)(ysum[w] + i * 4);
-    const int t = t0 + (i >> 2), n = row0 + (i & 3) * 4;
+    const int t = t0 + i / (C / 4), n = col0 + i % (C / 4) * 4;
     if (n >= g.N) continue;  // N is a multiple of 8: all four columns or none
     if (direct) {
       typename E::vec4 o;
@@ -646,14 +707,14 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
   // its own, then one atomic add; the last workgroup adds the splits in order.
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  int* last = (int*)lds;
+  int* arrived = (int*)lds;
   if (threadIdx.x == 0)
-    *last = __hip_atomic_fetch_add(g.ctr + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(g.splits - 1);
+    *arrived = __hip_atomic_fetch_add(g.ctr + blockIdx.z * gridDim.x + blockIdx.x, 1u, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(g.splits - 1);
   __syncthreads();
-  if (!*last) return;
-  for (int i = threadIdx.x; i < tc * 4; i += NW * 64) {
-    const int t = t0 + (i >> 2), n = row0 + (i & 3) * 4;
+  if (!*arrived) return;
+  for (int i = threadIdx.x; i < tc * (C / 4); i += NW * 64) {
+    const int t = t0 + i / (C / 4), n = col0 + i % (C / 4) * 4;
     if (n >= g.N) continue;
     f32x4_t v{};
     for (int sp = 0; sp < g.splits; ++sp)
@@ -666,13 +727,17 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
 }
 
 // ---- launches ---------------------------------------------------------------------
-// Workgroups per output tile of a block's down projection: about two per CU
-// over all tiles, so that all CUs pull weights (one CU alone reads at a few
-// tens of GB/s). 16-column tiles: D = 2048 has 128 of them.
+// Token rows per stage: as few as the largest possible list needs, 32 at most.
+static inline int token_rows(int64_t T, bool w4) { return T <= (w4 ? 4 : 8) ? 8 : T <= 16 ? 16 : 32; }
+
+// Columns of a down tile, and workgroups per tile: about as many over all tiles
+// as run at once, so that all CUs pull weights (one CU alone reads at a few
+// tens of GB/s).
+static inline int down_cols(int64_t T) { return T <= 16 ? 16 : 32; }
 static inline int down_splits(int64_t T, int64_t D) {
-  const int64_t tiles = (D + 15) / 16 * ((T + kChunk - 1) / kChunk);
-  const int64_t s = 512 / tiles;
-  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+  const int64_t tiles = (D + down_cols(T) - 1) / down_cols(T) * ((T + kChunk - 1) / kChunk);
+  const int64_t s = ((T <= 16 ? 512 : 256) + tiles - 1) / tiles;
+  return s > 8 ? 8 : (int)s;
 }
 // Workspace of a block: the A plane, then where the down projection is split
 // one counter per output tile and the partial sums, each 256-byte aligned.
@@ -684,7 +749,7 @@ static inline BlockPlan block_plan(int64_t T, int64_t D, int64_t H, int64_t k, s
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   BlockPlan p;
   p.splits = down_splits(T, D);
-  p.n_ctr = p.splits > 1 ? (int)((D + 15) / 16 * ((T + kChunk - 1) / kChunk)) : 0;
+  p.n_ctr = p.splits > 1 ? (int)((D + down_cols(T) - 1) / down_cols(T) * ((T + kChunk - 1) / kChunk)) : 0;
   p.ctr = up((size_t)T * k * H * e);
   p.partial = p.ctr + up((size_t)p.n_ctr * 4);
   p.total = p.partial + (p.splits > 1 ? up((size_t)p.splits * T * D * 4) : 0);
@@ -704,23 +769,23 @@ struct Call {
   hipStream_t stream;
 };
 
-template <class E, int FMT, int LW>
+// Ring bytes per wave: two workgroups share a CU's LDS where at most 16 token
+// rows are held, else one has it.
+template <class E, int FMT, int HB, int XR, int LW>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(STAGE_FEW_GATEUP, s);
-  const dim3 grid((g.N + 15) / 16, slots, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_gateup<E, FMT, LW>), grid, dim3(NW * 64), 0, s, g);
+  const int64_t items = (int64_t)slots * ((g.N + 16 * HB - 1) / (16 * HB)), fit = (XR <= 16 ? 2 : 1) * dev_ncu();
+  const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
+  hipLaunchKernelGGL((few_gateup<E, FMT, HB, XR, LW>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
-template <class E, int FMT, int LW>
+template <class E, int FMT, int NT, int XR, int LW, int TC>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
-  const dim3 grid((g.N + 15) / 16, g.splits, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_down<E, FMT, LW>), grid, dim3(NW * 64), 0, s, g);
+  const dim3 grid((g.N + 16 * NT - 1) / (16 * NT), g.splits, (g.T + kChunk - 1) / kChunk);
+  hipLaunchKernelGGL((few_down<E, FMT, NT, XR, LW, TC>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
-// Two workgroups per CU with short rings while no list is longer than their
-// token rows.
-static inline bool short_rings(int64_t T, int fmt) { return T <= (fmt ? 4 : 16); }
 
 static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, char* out) {
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
@@ -728,7 +793,21 @@ static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, c
 }
 template <class E, int FMT>
 static int down_for(const Args& g, hipStream_t s) {
-  return short_rings(g.T, FMT) ? launch_down<E, FMT, 16384>(g, s) : launch_down<E, FMT, 32768>(g, s);
+  constexpr int kFew = FMT ? 4 : 8;
+  switch (token_rows(g.T, FMT != 0)) {
+    case 8: return launch_down<E, FMT, 1, kFew, 16384, 16>(g, s);
+    case 16: return launch_down<E, FMT, 1, 16, 16384, 16>(g, s);
+    default: return launch_down<E, FMT, 2, 32, 28672, 64>(g, s);
+  }
+}
+template <class E, int FMT>
+static int gateup_for(const Args& g, int slots, hipStream_t s) {
+  constexpr int kFew = FMT ? 4 : 8;
+  switch (token_rows(g.T, FMT != 0)) {
+    case 8: return launch_gateup<E, FMT, 1, kFew, 16384>(g, slots, s);
+    case 16: return launch_gateup<E, FMT, 1, 16, 16384>(g, slots, s);
+    default: return launch_gateup<E, FMT, FMT ? 1 : 2, 32, FMT ? 32768 : 28672>(g, slots, s);
+  }
 }
 
 // y = x W^T (dense).
@@ -747,8 +826,7 @@ int run_block(const Call& c) {
   g.n_ctr = p.n_ctr;
   const int64_t pairs = (c.T < kChunk ? c.T : kChunk) * c.k;
   const int slots = c.ids ? (int)(pairs < c.E ? pairs : c.E) : 1;
-  const int rc = short_rings(c.T, FMT) ? launch_gateup<E, FMT, 18432>(g, slots, c.stream)
-                                       : launch_gateup<E, FMT, 36864>(g, slots, c.stream);
+  const int rc = gateup_for<E, FMT>(g, slots, c.stream);
   if (rc) return rc;
   Args d = args_of(c, c.ws, c.D, c.H, c.y);
   d.splits = p.splits;
