@@ -118,31 +118,39 @@ __device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff) {
 // without a memory access: no remainder code, and neither the next row nor a
 // NaN there is multiplied in.
 //
-// XR: token rows per stage, 16 or 32, or fewer (what one load instruction
+// XR: token rows per stage, 16 to 64, or fewer (what one load instruction
 // covers): then rows XR .. 15 of the operand repeat them. A longer list of
 // tokens takes several passes over the weights.
+//
+// SH: waves that share the token rows. 1: the ring is the wave's own, with rows
+// and weights side by side, and the waves split K. NW: the ring is the
+// workgroup's, each wave loads its part of the rows and its own weight blocks,
+// and the waves split the weight rows. With more than 16 token rows a private
+// copy of them would leave no LDS for weights in flight.
 
 // Rows of 16-bit or fp32 values: a stage is 128 bytes of K, 16 rows x 128 B in
 // two loads of 8 rows. Chunk c of row r sits at position c ^ kc_swz(r), so the
 // 16 rows one read takes fall on distinct banks.
-template <class E, int NT, int XR, int LW>
+template <class E, int NT, int XR, int SH, int LDS>
 struct RowStream {
   static constexpr int MT = XR < 16 ? 1 : XR / 16;
-  static constexpr int XD = XR / 8;        // token loads per stage
-  static constexpr int D = 2 * NT + XD;    // loads per stage
-  static constexpr int SLOT = D * 1024;
-  static constexpr int NS = LW / SLOT < 8 ? LW / SLOT : 8;
-  static_assert(NS >= 2 && XR >= 8 && (NS - 1) * D <= 63, "ring");
+  static constexpr int XD = XR / 8 / SH;   // token loads per stage and wave
+  static constexpr int D = 2 * NT + XD;    // loads per stage and wave
+  static constexpr int SLOT = SH * D * 1024;
+  static constexpr int NS = LDS / SLOT < 8 ? LDS / SLOT : 8;
+  static_assert(NS >= 2 && XD >= 1 && (NS - 1) * D <= 63, "ring");
   i32x4_t rw[NT], rx;
   uint32_t w_off[2], x_off[XD];
-  int kb;
+  int kb, share, w_at;  // share: the wave's part of the token rows; w_at: its weights in a slot
 
   static __device__ __forceinline__ int stages(int K) { return (K * E::kBytes + 127) >> 7; }
   // the token row (0 .. XR - 1) whose chunk this lane fetches in load j
-  static __device__ __forceinline__ int x_row(int j, int lane) { return 8 * j + (lane >> 3); }
+  __device__ __forceinline__ int x_row(int j, int lane) const { return 8 * (share * XD + j) + (lane >> 3); }
 
   // what does not change over a launch
-  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int lane) {
+  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int wave, int lane) {
+    share = SH > 1 ? wave : 0;
+    w_at = XR * 128 + share * NT * 2048;
     kb = g.K * E::kBytes;
     rx = rsrc_words(xb, x_bytes);
 #pragma unroll
@@ -161,15 +169,15 @@ struct RowStream {
 #pragma unroll
     for (int n = 0; n < NT; ++n) w[n] = scalar_rsrc(rw[n]);
 #pragma unroll
-    for (int j = 0; j < (XD > 2 ? XD : 2); ++j) {
-      const int r = 8 * j + (lane >> 3);
-      const int off = s * 128 + (((lane & 7) ^ kc_swz(r)) << 4);
-      const bool in = off < end;
-      if (j < 2) {
+    for (int j = 0; j < 2; ++j) {
+      const int off = s * 128 + (((lane & 7) ^ kc_swz(8 * j + (lane >> 3))) << 4);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) dma16(slot + n * 2048 + j * 1024, w[n], in ? w_off[j] + off : kOOB, 0u);
-      }
-      if (j < XD) dma16(slot + NT * 2048 + j * 1024, xr, in ? x_off[j] + off : kOOB, 0u);
+      for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, w[n], off < end ? w_off[j] + off : kOOB, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < XD; ++j) {
+      const int off = s * 128 + (((lane & 7) ^ kc_swz(x_row(j, lane))) << 4);
+      dma16(slot + (share * XD + j) * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
     }
   }
   __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane) const {
@@ -180,10 +188,10 @@ struct RowStream {
       const int ax = XR < 16 ? (r & 7) * 128 + (((4 * h + c) ^ kc_swz(r & 7)) << 4) : at;
       u32x4_t xv[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xv[m] = *(const u32x4_t*)(slot + NT * 2048 + m * 2048 + ax);
+      for (int m = 0; m < MT; ++m) xv[m] = *(const u32x4_t*)(slot + m * 2048 + ax);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const u32x4_t wv = *(const u32x4_t*)(slot + n * 2048 + at);
+        const u32x4_t wv = *(const u32x4_t*)(slot + w_at + n * 2048 + at);
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[n][m] = step_mfma<E>(xv[m], wv, acc[n][m]);
       }
@@ -200,25 +208,27 @@ struct RowStream {
 // is rounded. The offset costs accuracy of about OFF / 5 fp32 roundings of the
 // group's sum, 2^-19 of it in bf16: far below the storage type's half step.
 // Token rows are 256 B per stage; chunk c of row r at position c ^ (r & 15).
-template <class E, int G, int NT, int XR, int LW>
+template <class E, int G, int NT, int XR, int SH, int LDS>
 struct W4Stream {
   static constexpr int GP = 128 / G;  // groups per record
   static constexpr int MT = XR < 16 ? 1 : XR / 16;
-  static constexpr int XD = XR / 4;
+  static constexpr int XD = XR / 4 / SH;
   static constexpr int D = 2 * NT + XD;
   static constexpr int WS = 1024 + 256;  // a record's place in a slot
-  static constexpr int SLOT = NT * WS + XD * 1024;
-  static constexpr int NS = LW / SLOT < 8 ? LW / SLOT : 8;
-  static_assert(NS >= 2 && XR >= 4 && (NS - 1) * D <= 63, "ring");
+  static constexpr int SLOT = SH * (NT * WS + XD * 1024);
+  static constexpr int NS = LDS / SLOT < 8 ? LDS / SLOT : 8;
+  static_assert(NS >= 2 && XD >= 1 && (NS - 1) * D <= 63, "ring");
   static constexpr float kOff = std::is_same<E, Bf16>::value ? 128.0f : 64.0f;
   i32x4_t rw[NT], rx;
   uint32_t x_off[XD];
-  int kb, rec, zeros;
+  int kb, rec, zeros, share, w_at;
 
   static __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
-  static __device__ __forceinline__ int x_row(int j, int lane) { return 4 * j + (lane >> 4); }
+  __device__ __forceinline__ int x_row(int j, int lane) const { return 4 * (share * XD + j) + (lane >> 4); }
 
-  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int) {
+  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int wave, int) {
+    share = SH > 1 ? wave : 0;
+    w_at = XR * 256 + share * NT * WS;
     kb = g.K * 2;
     zeros = g.zeros;
     rec = 1024 + 32 * GP + (zeros ? 32 : 0);
@@ -233,16 +243,15 @@ struct W4Stream {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const i32x4_t w = scalar_rsrc(rw[n]);
-      dma16(slot + n * WS, w, live ? at + lane * 16 : kOOB, 0u);
-      dma4(slot + n * WS + 1024, w, live && 1024 + lane * 4 < rec ? at + 1024 + lane * 4 : kOOB);
+      dma16(slot + w_at + n * WS, w, live ? at + lane * 16 : kOOB, 0u);
+      dma4(slot + w_at + n * WS + 1024, w, live && 1024 + lane * 4 < rec ? at + 1024 + lane * 4 : kOOB);
     }
     const int end = live ? kb : 0;
     const i32x4_t xr = scalar_rsrc(rx);
 #pragma unroll
     for (int j = 0; j < XD; ++j) {
-      const int r = 4 * j + (lane >> 4);
-      const int off = s * 256 + (((lane & 15) ^ (r & 15)) << 4);
-      dma16(slot + NT * WS + j * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
+      const int off = s * 256 + (((lane & 15) ^ (x_row(j, lane) & 15)) << 4);
+      dma16(slot + (share * XD + j) * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
     }
   }
   // eight codes of one dword as the MFMA operand OFF + q
@@ -266,11 +275,11 @@ struct W4Stream {
     uint32_t z[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      code[n] = *(const u32x4_t*)(slot + n * WS + lane * 16);
-      const typename E::elem* sp = (const typename E::elem*)(slot + n * WS + 1024) + r * GP;
+      code[n] = *(const u32x4_t*)(slot + w_at + n * WS + lane * 16);
+      const typename E::elem* sp = (const typename E::elem*)(slot + w_at + n * WS + 1024) + r * GP;
 #pragma unroll
       for (int q = 0; q < GP; ++q) sc[n][q] = sp[q];
-      z[n] = zeros ? *(const uint16_t*)(slot + n * WS + 1024 + 32 * GP + r * 2) : 0x8888u;
+      z[n] = zeros ? *(const uint16_t*)(slot + w_at + n * WS + 1024 + 32 * GP + r * 2) : 0x8888u;
     }
 #pragma unroll
     for (int q = 0; q < GP; ++q) {
@@ -280,7 +289,7 @@ struct W4Stream {
         u32x4_t xv[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          xv[m] = *(const u32x4_t*)(slot + NT * WS + (16 * m + rr) * 256 + (((4 * i + c) ^ rr) << 4));
+          xv[m] = *(const u32x4_t*)(slot + (16 * m + rr) * 256 + (((4 * i + c) ^ rr) << 4));
           xs[m] = step_mfma<E>(xv[m], ones(), xs[m]);
         }
 #pragma unroll
@@ -304,18 +313,20 @@ struct W4Stream {
 };
 
 // FMT 0: rows; 32, 64, 128: 4 bits with groups of that size
-template <class E, int FMT, int NT, int XR, int LW>
+template <class E, int FMT, int NT, int XR, int SH, int LDS>
 struct StreamOf {
-  using type = W4Stream<E, FMT, NT, XR, LW>;
+  using type = W4Stream<E, FMT, NT, XR, SH, LDS>;
 };
-template <class E, int NT, int XR, int LW>
-struct StreamOf<E, 0, NT, XR, LW> {
-  using type = RowStream<E, NT, XR, LW>;
+template <class E, int NT, int XR, int SH, int LDS>
+struct StreamOf<E, 0, NT, XR, SH, LDS> {
+  using type = RowStream<E, NT, XR, SH, LDS>;
 };
 
-// The wave's ring: R.step<S>() = wait for the oldest stage, multiply it, and
-// fetch the stage that `issue` (a callable: LDS slot address) says is next.
-template <class S>
+// A ring: step() = wait for the oldest stage, multiply it, and fetch the stage
+// that `issue` (a callable: LDS slot address) says is next. In a shared ring the
+// barrier that publishes a stage also says that the one before it has been
+// read, so that one's slot is refilled, and NS - 1 stages are in flight.
+template <class S, int SH>
 struct Ring {
   char* lds;
   uint32_t addr;
@@ -326,14 +337,21 @@ struct Ring {
     addr = lds_addr(p);
     slot = 0;
 #pragma unroll 1
-    for (int i = 0; i < S::NS; ++i) issue(addr + i * S::SLOT);
+    for (int i = 0; i < (SH > 1 ? S::NS - 1 : S::NS); ++i) issue(addr + i * S::SLOT);
   }
   template <int NT, class Issue>
   __device__ __forceinline__ void step(const S& st, f32x4_t (&acc)[NT][S::MT], int lane, Issue&& issue) {
-    ring::wait_vmcnt<(S::NS - 1) * S::D>();
-    st.compute(lds + slot * S::SLOT, acc, lane);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
-    issue(addr + slot * S::SLOT);
+    if constexpr (SH > 1) {
+      ring::wait_vmcnt<(S::NS - 2) * S::D>();
+      ring::lds_barrier();
+      issue(addr + (slot ? slot - 1 : S::NS - 1) * S::SLOT);
+      st.compute(lds + slot * S::SLOT, acc, lane);
+    } else {
+      ring::wait_vmcnt<(S::NS - 1) * S::D>();
+      st.compute(lds + slot * S::SLOT, acc, lane);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
+      issue(addr + slot * S::SLOT);
+    }
     slot = slot + 1 == S::NS ? 0 : slot + 1;
   }
 };
@@ -480,16 +498,18 @@ struct Walk {
 };
 
 // ---- gate/up ------------------------------------------------------------------
-// An item is a tile of 16 HB hidden columns of one pass; the workgroup takes a
-// run of items, its waves a quarter of K each. The rings run on from item to
-// item: while the waves' sums of one meet in LDS, the loads of the next are
-// in flight.
-template <class E, int FMT, int HB, int XR, int LW>
+// An item is a tile of hidden columns of one pass; the workgroup takes a run of
+// items. SH = 1: 16 HB columns, the waves take a quarter of K each and their
+// sums meet in LDS; SH = NW: 16 HB columns per wave, all of K. The rings run on
+// from item to item: while one is finished, the loads of the next are in flight.
+// RING: bytes of LDS for the workgroup's rings.
+template <class E, int FMT, int HB, int XR, int SH, int RING>
 __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
-  using S = typename StreamOf<E, FMT, 2 * HB, XR, LW>::type;
-  constexpr int MT = S::MT, NT = 2 * HB;
-  __shared__ __attribute__((aligned(1024))) char lds[NW * LW];
-  __shared__ __attribute__((aligned(16))) float red[NW * NT * MT * 256];
+  constexpr int NT = 2 * HB, COLS = 16 * HB * SH;
+  using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
+  constexpr int MT = S::MT;
+  __shared__ __attribute__((aligned(1024))) char lds[RING];
+  __shared__ __attribute__((aligned(16))) float red[SH > 1 ? 4 : NW * NT * MT * 256];
   __shared__ Choices ch;
   __shared__ int16_t list[NW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -498,15 +518,16 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
     for (int i = threadIdx.x; i < g.n_ctr; i += NW * 64) g.ctr[i] = 0u;
   Walk use;  // the item being multiplied
   use.open(g, ch, list[wave], t0, tc, lane);
-  const int tiles = (g.N + 16 * HB - 1) / (16 * HB), items = use.hits * tiles;
+  const int tiles = (g.N + COLS - 1) / COLS, items = use.hits * tiles;
   int item = (int)((int64_t)items * blockIdx.x / gridDim.x);
   const int last = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
   if (item >= last) return;
   Walk get = use;  // the item being loaded
   S st;
-  st.init(g, g.x + (int64_t)t0 * g.K * E::kBytes, (uint32_t)(tc * g.K) * E::kBytes, lane);
-  const int stages = S::stages(g.K), per = (stages + NW - 1) / NW;
-  const int s0 = wave * per, s1 = min(stages, s0 + per);
+  st.init(g, g.x + (int64_t)t0 * g.K * E::kBytes, (uint32_t)(tc * g.K) * E::kBytes, wave, lane);
+  const int stages = S::stages(g.K), per = SH > 1 ? stages : (stages + NW - 1) / NW;
+  const int s0 = SH > 1 ? 0 : wave * per, s1 = min(stages, s0 + per);
+  const int wcol = SH > 1 ? 16 * HB * wave : 0;  // the wave's first column of a tile
 
   // loading side: the next stage of the current item, then the next item
   int get_item = item, get_s = s0;
@@ -515,12 +536,12 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
     const int n = get.rows(XR);
 #pragma unroll
     for (int j = 0; j < S::XD; ++j) {
-      const int i = S::x_row(j, lane), pair = get.pair(i);
+      const int i = st.x_row(j, lane), pair = get.pair(i);
       st.x_off[j] = i < n ? ((pair * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB;
     }
   };
   auto set_weights = [&] {
-    const int row0 = (get_item % tiles) * 16 * HB;
+    const int row0 = (get_item % tiles) * COLS + wcol;
 #pragma unroll
     for (int b = 0; b < HB; ++b) {
       st.weight(2 * b, g.w0, get.e, row0 + 16 * b, g.N);
@@ -546,39 +567,54 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
   get.expert(item / tiles, lane);
   set_rows();
   set_weights();
-  Ring<S> r;
-  r.start(lds + wave * LW, issue);
+  Ring<S, SH> r;
+  r.start(lds + (SH > 1 ? 0 : wave * (RING / NW)), issue);
 
+  // g and u stay in fp32; A is rounded once, to the storage type the down
+  // projection's matrix instructions take
+  auto store = [&](int pair, int h, float gate, float up) {
+    ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] = E::from_f32(gate * sigmoid_f32<E>(gate) * up);
+  };
   use.expert(item / tiles, lane);
   while (true) {
     f32x4_t acc[NT][MT] = {};
 #pragma unroll 1
     for (int s = 0; s < per; ++s) r.step(st, acc, lane, issue);
-    ring::lds_barrier();  // the last item's sums have been read
+    const int n = use.rows(XR), row0 = (item % tiles) * COLS + wcol;
+    if constexpr (SH > 1) {
+      // the wave has all of K: lane -> hidden column l % 16, token rows 4 (l / 16) + j
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) *(f32x4_t*)(red + (((wave * NT + n) * MT + m) * 64 + lane) * 4) = acc[n][m];
-    ring::lds_barrier();
-    // thread -> (token row of the pass, hidden column); the waves' sums in order
-    const int n = use.rows(XR), row0 = (item % tiles) * 16 * HB;
+        for (int j = 0; j < 4; ++j) {
+          const int i = 16 * m + 4 * (lane >> 4) + j, pair = use.pair(i);
+#pragma unroll
+          for (int b = 0; b < HB; ++b) {
+            const int h = row0 + 16 * b + (lane & 15);
+            if (i < n && h < g.N) store(pair, h, acc[2 * b][m][j], acc[2 * b + 1][m][j]);
+          }
+        }
+    } else {
+      ring::lds_barrier();  // the last item's sums have been read
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) *(f32x4_t*)(red + (((wave * NT + n) * MT + m) * 64 + lane) * 4) = acc[n][m];
+      ring::lds_barrier();
+      // thread -> (token row of the pass, hidden column); the waves' sums in order
 #pragma unroll 1
-    for (int i0 = 0; i0 < HB * MT * 256; i0 += NW * 64) {
-      const int i = i0 + threadIdx.x, b = i / (MT * 256);
-      const int col = i & 15, row = (i >> 4) % (16 * MT);
-      const int at = ((row >> 4) * 64 + ((row & 15) >> 2) * 16 + col) * 4 + (row & 3);
-      float gate = 0.f, up = 0.f;
+      for (int i0 = 0; i0 < HB * MT * 256; i0 += NW * 64) {
+        const int i = i0 + threadIdx.x, b = i / (MT * 256);
+        const int col = i & 15, row = (i >> 4) % (16 * MT);
+        const int at = ((row >> 4) * 64 + ((row & 15) >> 2) * 16 + col) * 4 + (row & 3);
+        float gate = 0.f, up = 0.f;
 #pragma unroll
-      for (int v = 0; v < NW; ++v) {
-        gate += red[(v * NT + 2 * b) * MT * 256 + at];
-        up += red[(v * NT + 2 * b + 1) * MT * 256 + at];
-      }
-      const int pair = use.pair(row), h = row0 + 16 * b + col;
-      if (row < n && h < g.N) {
-        // g and u stay in fp32; A is rounded once, to the storage type the
-        // down projection's matrix instructions take
-        ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] =
-            E::from_f32(gate * sigmoid_f32<E>(gate) * up);
+        for (int v = 0; v < NW; ++v) {
+          gate += red[(v * NT + 2 * b) * MT * 256 + at];
+          up += red[(v * NT + 2 * b + 1) * MT * 256 + at];
+        }
+        const int pair = use.pair(row), h = row0 + 16 * b + col;
+        if (row < n && h < g.N) store(pair, h, gate, up);
       }
     }
     if (use.next_pass(XR, lane)) continue;
@@ -589,38 +625,40 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
 }
 
 // ---- down -----------------------------------------------------------------------
-// The K axis of an output tile of 16 NT columns is the list of (expert that
-// occurs, K stage); the splits x NW waves take equal runs of it. At an expert's
-// end the block of sums is weighted and added to the wave's own
-// [token][column] tile in LDS. TC: tokens that tile has room for.
-template <class E, int FMT, int NT, int XR, int LW, int TC>
+// The K axis of an output tile is the list of (expert that occurs, K stage);
+// equal runs of it go to the splits (SH = NW: 16 NT columns per wave) or the
+// splits x NW waves (SH = 1: 16 NT columns for all). At an expert's end the
+// block of sums is weighted and added to the wave's own [token][column] tile in
+// LDS. TC: tokens that tile has room for.
+template <class E, int FMT, int NT, int XR, int SH, int RING, int TC>
 __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
-  using S = typename StreamOf<E, FMT, NT, XR, LW>::type;
+  using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
   constexpr int MT = S::MT, C = 16 * NT;
-  __shared__ __attribute__((aligned(1024))) char lds[NW * LW];
+  __shared__ __attribute__((aligned(1024))) char lds[RING];
   __shared__ __attribute__((aligned(16))) float ysum[NW][TC * C];
   __shared__ Choices ch;
   __shared__ int16_t list[NW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0);
-  const int col0 = blockIdx.x * C;
+  const int wg0 = blockIdx.x * C * SH, col0 = wg0 + (SH > 1 ? wave * C : 0);  // the workgroup's, the wave's columns
   const bool routed = g.ids != nullptr;
   float* y = ysum[wave];
   for (int i = lane; i < tc * C; i += 64) y[i] = 0.f;
   Walk use;
   use.open(g, ch, list[wave], t0, tc, lane);
-  const int stages = S::stages(g.K), parts = g.splits * NW, part = blockIdx.y * NW + wave;
+  const int stages = S::stages(g.K), parts = g.splits * (NW / SH),
+            part = SH > 1 ? (int)blockIdx.y : (int)blockIdx.y * NW + wave;
   int at = (int)((int64_t)use.hits * stages * part / parts);
   const int end = (int)((int64_t)use.hits * stages * (part + 1) / parts);
   if (at < end) {
     Walk get = use;
     S st;
-    st.init(g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, (uint32_t)(tc * g.k * g.K) * E::kBytes, lane);
+    st.init(g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, (uint32_t)(tc * g.k * g.K) * E::kBytes, wave, lane);
     auto set_rows = [&] {
       const int n = get.rows(XR);
 #pragma unroll
       for (int j = 0; j < S::XD; ++j) {
-        const int i = S::x_row(j, lane), pair = get.pair(i);
+        const int i = st.x_row(j, lane), pair = get.pair(i);
         st.x_off[j] = i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB;
       }
     };
@@ -650,8 +688,8 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
       if (more) open_expert(get.i + 1);
     };
     open_expert(at / stages);
-    Ring<S> r;
-    r.start(lds + wave * LW, issue);
+    Ring<S, SH> r;
+    r.start(lds + (SH > 1 ? 0 : wave * (RING / NW)), issue);
     for (int n = at / stages; n * stages < end; ++n) {
       use.expert(n, lane);
       const int count = end_of(n) - begin_of(n);
@@ -685,13 +723,19 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
     ring::wait_vmcnt<0>();  // no load may land in LDS after the rings' end
   }
   __syncthreads();
-  // four columns of one token per thread; the waves' sums in order
+  // four columns of one token per thread; the waves' sums of a column in order
+  constexpr int Q = C * SH / 4;  // such quads per token
   const bool direct = g.splits == 1;
-  for (int i = threadIdx.x; i < tc * (C / 4); i += NW * 64) {
+  for (int i = threadIdx.x; i < tc * Q; i += NW * 64) {
+    const int row = i / Q, q = i % Q;
     f32x4_t v{};
+    if constexpr (SH > 1) {
+      v = *(const f32x4_t*)(ysum[q / (C / 4)] + row * C + q % (C / 4) * 4);
+    } else {
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += *(const f32x4_t*)(ysum[w] + i * 4);
-    const int t = t0 + i / (C / 4), n = col0 + i % (C / 4) * 4;
+      for (int w = 0; w < NW; ++w) v += *(const f32x4_t*)(ysum[w] + i * 4);
+    }
+    const int t = t0 + row, n = wg0 + q * 4;
     if (n >= g.N) continue;  // N is a multiple of 8: all four columns or none
     if (direct) {
       typename E::vec4 o;
@@ -699,7 +743,7 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
       for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);
       *(typename E::vec4*)((typename E::elem*)g.out + (int64_t)t * g.N + n) = o;
     } else {
-      store_partial(g.partial + ((int64_t)blockIdx.y * g.T + t0) * g.N, tc, g.N, t - t0, n, v);
+      store_partial(g.partial + ((int64_t)blockIdx.y * g.T + t0) * g.N, tc, g.N, row, n, v);
     }
   }
   if (direct) return;
@@ -713,27 +757,27 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
                                       __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(g.splits - 1);
   __syncthreads();
   if (!*arrived) return;
-  for (int i = threadIdx.x; i < tc * (C / 4); i += NW * 64) {
-    const int t = t0 + i / (C / 4), n = col0 + i % (C / 4) * 4;
+  for (int i = threadIdx.x; i < tc * Q; i += NW * 64) {
+    const int row = i / Q, n = wg0 + i % Q * 4;
     if (n >= g.N) continue;
     f32x4_t v{};
     for (int sp = 0; sp < g.splits; ++sp)
-      v += load_partial(g.partial + ((int64_t)sp * g.T + t0) * g.N, tc, g.N, t - t0, n);
+      v += load_partial(g.partial + ((int64_t)sp * g.T + t0) * g.N, tc, g.N, row, n);
     typename E::vec4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);
-    *(typename E::vec4*)((typename E::elem*)g.out + (int64_t)t * g.N + n) = o;
+    *(typename E::vec4*)((typename E::elem*)g.out + (int64_t)(t0 + row) * g.N + n) = o;
   }
 }
 
 // ---- launches ---------------------------------------------------------------------
-// Token rows per stage: as few as the largest possible list needs, 32 at most.
-static inline int token_rows(int64_t T, bool w4) { return T <= (w4 ? 4 : 8) ? 8 : T <= 16 ? 16 : 32; }
+// Token rows per stage: as few as the largest possible list needs.
+static inline int token_rows(int64_t T, bool w4) { return T <= (w4 ? 4 : 8) ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 // Columns of a down tile, and workgroups per tile: about as many over all tiles
 // as run at once, so that all CUs pull weights (one CU alone reads at a few
 // tens of GB/s).
-static inline int down_cols(int64_t T) { return T <= 16 ? 16 : 32; }
+static inline int down_cols(int64_t T) { return T <= 16 ? 16 : 64; }
 static inline int down_splits(int64_t T, int64_t D) {
   const int64_t tiles = (D + down_cols(T) - 1) / down_cols(T) * ((T + kChunk - 1) / kChunk);
   const int64_t s = ((T <= 16 ? 512 : 256) + tiles - 1) / tiles;
@@ -769,21 +813,24 @@ struct Call {
   hipStream_t stream;
 };
 
-// Ring bytes per wave: two workgroups share a CU's LDS where at most 16 token
-// rows are held, else one has it.
-template <class E, int FMT, int HB, int XR, int LW>
+// Two workgroups share a CU's LDS where at most 16 token rows are held
+// (private rings), else one has it (a shared ring).
+template <class E, int FMT, int XR>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(STAGE_FEW_GATEUP, s);
-  const int64_t items = (int64_t)slots * ((g.N + 16 * HB - 1) / (16 * HB)), fit = (XR <= 16 ? 2 : 1) * dev_ncu();
+  constexpr int SH = XR <= 16 ? 1 : NW;
+  const int64_t items = (int64_t)slots * ((g.N + 16 * SH - 1) / (16 * SH)), fit = (SH == 1 ? 2 : 1) * dev_ncu();
   const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_gateup<E, FMT, HB, XR, LW>), grid, dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_gateup<E, FMT, 1, XR, SH, SH == 1 ? 65536 : 147456>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
-template <class E, int FMT, int NT, int XR, int LW, int TC>
+template <class E, int FMT, int XR>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
-  const dim3 grid((g.N + 16 * NT - 1) / (16 * NT), g.splits, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_down<E, FMT, NT, XR, LW, TC>), grid, dim3(NW * 64), 0, s, g);
+  constexpr int SH = XR <= 16 ? 1 : NW;
+  const dim3 grid((g.N + 16 * SH - 1) / (16 * SH), g.splits, (g.T + kChunk - 1) / kChunk);
+  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, SH, SH == 1 ? 65536 : 131072, SH == 1 ? 16 : kChunk>), grid,
+                     dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 
@@ -793,20 +840,20 @@ static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, c
 }
 template <class E, int FMT>
 static int down_for(const Args& g, hipStream_t s) {
-  constexpr int kFew = FMT ? 4 : 8;
   switch (token_rows(g.T, FMT != 0)) {
-    case 8: return launch_down<E, FMT, 1, kFew, 16384, 16>(g, s);
-    case 16: return launch_down<E, FMT, 1, 16, 16384, 16>(g, s);
-    default: return launch_down<E, FMT, 2, 32, 28672, 64>(g, s);
+    case 8: return launch_down<E, FMT, FMT ? 4 : 8>(g, s);
+    case 16: return launch_down<E, FMT, 16>(g, s);
+    case 32: return launch_down<E, FMT, 32>(g, s);
+    default: return launch_down<E, FMT, 64>(g, s);
   }
 }
 template <class E, int FMT>
 static int gateup_for(const Args& g, int slots, hipStream_t s) {
-  constexpr int kFew = FMT ? 4 : 8;
   switch (token_rows(g.T, FMT != 0)) {
-    case 8: return launch_gateup<E, FMT, 1, kFew, 16384>(g, slots, s);
-    case 16: return launch_gateup<E, FMT, 1, 16, 16384>(g, slots, s);
-    default: return launch_gateup<E, FMT, FMT ? 1 : 2, 32, FMT ? 32768 : 28672>(g, slots, s);
+    case 8: return launch_gateup<E, FMT, FMT ? 4 : 8>(g, slots, s);
+    case 16: return launch_gateup<E, FMT, 16>(g, slots, s);
+    case 32: return launch_gateup<E, FMT, 32>(g, slots, s);
+    default: return launch_gateup<E, FMT, 64>(g, slots, s);
   }
 }
 
