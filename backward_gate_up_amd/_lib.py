@@ -72,8 +72,9 @@ def lib():
     L.swiglu_mlp_infer_noalloc.restype = i32
     w4 = ctypes.POINTER(W4)
     for name, args, res in (
-            ("moe_route", [vp] * 4 + [i64] * 4 + [i32, i32, vp], i32),
-            ("moe_workspace_bytes", [i64] * 4 + [i32], sz),
+            ("moe_route", [vp] * 5 + [sz] + [i64] * 4 + [i32, i32, vp], i32),
+            ("moe_route_workspace_bytes", [i64] * 3 + [i32], sz),
+            ("moe_workspace_bytes", [i64] * 5 + [i32], sz),
             ("moe_experts", [vp] * 8 + [sz] + [i64] * 5 + [i32, vp], i32),
             ("moe_infer", [vp] * 7 + [sz] + [i64] * 5 + [i32, i32, vp], i32),
             ("moe_experts_w4", [vp] * 3 + [w4] * 3 + [vp, vp, sz, i64, i64, i32, vp], i32),

@@ -23,9 +23,9 @@ extern template int run_block<Fp16, 0>(const Call&);
 extern template int run_block<Fp32, 0>(const Call&);
 }  // namespace few
 namespace route {
-extern template int run_route<Bf16>(const Args&, hipStream_t);
-extern template int run_route<Fp16>(const Args&, hipStream_t);
-extern template int run_route<Fp32>(const Args&, hipStream_t);
+extern template int run_route<Bf16>(Args, hipStream_t);
+extern template int run_route<Fp16>(Args, hipStream_t);
+extern template int run_route<Fp32>(Args, hipStream_t);
 }  // namespace route
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -99,14 +99,23 @@ static int check_alias(const Range* out, int no, const Range* in, int ni) {
   return SWIGLU_OK;
 }
 
-// A mixture's workspace: the block's, then the router's weights and ids.
+static int run_route_for(int dtype, const route::Args& r, hipStream_t stream) {
+  if (dtype == SWIGLU_BF16) return route::run_route<Bf16>(r, stream);
+  if (dtype == SWIGLU_FP16) return route::run_route<Fp16>(r, stream);
+  return route::run_route<Fp32>(r, stream);
+}
+
+// A mixture's workspace: the block's, which is free while the router runs and
+// holds its workspace, then the router's weights and ids.
 struct MoePlan {
   size_t wts, ids, total;
 };
-static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
+static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, size_t e) {
   const size_t p = (size_t)T * k;
   MoePlan m;
   m.wts = few::block_plan(T, D, H, k, e).total;
+  const size_t r = up256(route::route_bytes(T, D, E, e));
+  if (m.wts < r) m.wts = r;
   m.ids = m.wts + up256(p * 4);
   m.total = m.ids + up256(p * 4);
   return m;
@@ -118,7 +127,7 @@ static int moe_call(const void* X, const void* Wr, const float* weights, const i
                     few::Call& c, void* Y, void* ws, size_t ws_bytes, int64_t T, int64_t k, int renorm, int dtype,
                     int group, hipStream_t stream) {
   const size_t e = elt_bytes(dtype);
-  const MoePlan m = moe_plan(T, c.D, c.H, k, e);
+  const MoePlan m = moe_plan(T, c.D, c.H, c.E, k, e);
   const size_t p4 = (size_t)T * k * 4;
   const bool routed = Wr != nullptr;
   const Range in[] = {{X, (size_t)T * c.D * e}, w[0], w[1], w[2], {Wr, routed ? (size_t)c.E * c.D * e : 0},
@@ -142,11 +151,8 @@ static int moe_call(const void* X, const void* Wr, const float* weights, const i
   if (routed) {
     float* rw = (float*)((char*)ws + m.wts);
     int* ri = (int*)((char*)ws + m.ids);
-    const route::Args r{(const char*)X, (const char*)Wr, rw, ri, (int)T, (int)c.D, c.E, (int)k, renorm != 0};
-    rc = dtype == SWIGLU_BF16   ? route::run_route<Bf16>(r, stream)
-         : dtype == SWIGLU_FP16 ? route::run_route<Fp16>(r, stream)
-                                : route::run_route<Fp32>(r, stream);
-    if (rc) return rc;
+    const route::Args r{(const char*)X, (const char*)Wr, rw, ri, (int)T, (int)c.D, c.E, (int)k, renorm != 0, (float*)ws, 1};
+    if ((rc = run_route_for(dtype, r, stream))) return rc;
     c.wts = rw;
     c.ids = ri;
   }
@@ -210,27 +216,37 @@ using namespace swiglu;
 
 extern "C" {
 
-int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, int64_t T, int64_t D, int64_t E,
-                         int64_t k, int renorm, int dtype, hipStream_t stream) {
+size_t swiglu_mlp_moe_route_workspace_bytes(int64_t T, int64_t D, int64_t E, int dtype) {
+  const size_t e = elt_bytes(dtype);
+  if (!e || !ld_ok(D) || check_few(T, E, 1)) return 0;
+  return route::route_bytes(T, D, E, e);
+}
+
+int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, void* workspace,
+                         size_t workspace_bytes, int64_t T, int64_t D, int64_t E, int64_t k, int renorm, int dtype,
+                         hipStream_t stream) {
   const size_t e = elt_bytes(dtype);
   if (!e) return SWIGLU_ERR_DTYPE;
   if (!ld_ok(D)) return SWIGLU_ERR_SHAPE;
   int rc = check_few(T, E, k);
   if (rc) return rc;
+  const size_t need = route::route_bytes(T, D, E, e);
   const Range in[] = {{X, (size_t)T * D * e}, {Wr, (size_t)E * D * e}};
-  const Range out[] = {{weights, (size_t)T * k * 4}, {ids, (size_t)T * k * 4}};
-  if ((rc = check_ptrs(in, 2)) || (rc = check_words(out, 2)) || (rc = check_alias(out, 2, in, 2))) return rc;
+  const Range out[] = {{weights, (size_t)T * k * 4}, {ids, (size_t)T * k * 4}, {workspace, need}};
+  if ((rc = check_ptrs(in, 2)) || (rc = check_words(out, 2))) return rc;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_WORKSPACE;
+  if (workspace && !aligned16(workspace)) return SWIGLU_ERR_ALIGN;
+  if ((rc = check_alias(out, 3, in, 2))) return rc;
   if ((rc = check_device())) return rc;
-  const route::Args r{(const char*)X, (const char*)Wr, weights, (int*)ids, (int)T, (int)D, (int)E, (int)k, renorm != 0};
-  if (dtype == SWIGLU_BF16) return route::run_route<Bf16>(r, stream);
-  if (dtype == SWIGLU_FP16) return route::run_route<Fp16>(r, stream);
-  return route::run_route<Fp32>(r, stream);
+  const route::Args r{(const char*)X, (const char*)Wr, weights, (int*)ids, (int)T, (int)D, (int)E, (int)k, renorm != 0,
+                      (float*)workspace, 1};
+  return run_route_for(dtype, r, stream);
 }
 
-size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t k, int dtype) {
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int dtype) {
   const size_t e = elt_bytes(dtype);
-  if (!e || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(D) || !ld_ok(H) || k < 1 || k > few::kMaxTopK) return 0;
-  return moe_plan(T, D, H, k, e).total;
+  if (!e || T <= 0 || !ld_ok(D) || !ld_ok(H) || check_few(T, E, k)) return 0;
+  return moe_plan(T, D, H, E, k, e).total;
 }
 
 int swiglu_mlp_moe_experts(const void* X, const float* weights, const int32_t* ids, const void* Wg, const void* Wu,

@@ -36,7 +36,6 @@ constexpr int kChunk = 64;              // tokens per grid z slice
 constexpr int kMaxTopK = 32;            // choices per token
 constexpr int kMaxPairs = kChunk * kMaxTopK;
 constexpr int kMaxExperts = 1024;
-constexpr int NW = 4;                   // waves per workgroup, splitting K
 
 // One weight as the kernels address it. Rows: E matrices [N, K], row-major.
 // 4 bits: E x [N/16][K/128] records, each 1 KiB of codes (lane l's 16 bytes
@@ -123,10 +122,10 @@ __device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff) {
 // tokens takes several passes over the weights.
 //
 // SH: waves that share the token rows. 1: the ring is the wave's own, with rows
-// and weights side by side, and the waves split K. NW: the ring is the
-// workgroup's, each wave loads its part of the rows and its own weight blocks,
-// and the waves split the weight rows. With more than 16 token rows a private
-// copy of them would leave no LDS for weights in flight.
+// and weights side by side, and the waves split K. Else the ring is those
+// waves' together: each loads its part of the rows and its own weight blocks,
+// and they split the weight rows. With more than 16 token rows a private copy
+// of them would leave no LDS for weights in flight.
 
 // Rows of 16-bit or fp32 values: a stage is 128 bytes of K, 16 rows x 128 B in
 // two loads of 8 rows. Chunk c of row r sits at position c ^ kc_swz(r), so the
@@ -180,7 +179,16 @@ struct RowStream {
       dma16(slot + (share * XD + j) * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
     }
   }
+  struct Nothing {
+    __device__ __forceinline__ void token(int, u32x4_t) {}
+    __device__ __forceinline__ void weight(int, u32x4_t) {}
+  };
   __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane) const {
+    compute(slot, acc, lane, Nothing{});
+  }
+  // `see` is shown every operand on the way
+  template <class See>
+  __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane, See&& see) const {
     const int r = lane & 15, c = lane >> 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -188,10 +196,14 @@ struct RowStream {
       const int ax = XR < 16 ? (r & 7) * 128 + (((4 * h + c) ^ kc_swz(r & 7)) << 4) : at;
       u32x4_t xv[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xv[m] = *(const u32x4_t*)(slot + m * 2048 + ax);
+      for (int m = 0; m < MT; ++m) {
+        xv[m] = *(const u32x4_t*)(slot + m * 2048 + ax);
+        see.token(m, xv[m]);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const u32x4_t wv = *(const u32x4_t*)(slot + w_at + n * 2048 + at);
+        see.weight(n, wv);
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[n][m] = step_mfma<E>(xv[m], wv, acc[n][m]);
       }
@@ -339,16 +351,16 @@ struct Ring {
 #pragma unroll 1
     for (int i = 0; i < (SH > 1 ? S::NS - 1 : S::NS); ++i) issue(addr + i * S::SLOT);
   }
-  template <int NT, class Issue>
-  __device__ __forceinline__ void step(const S& st, f32x4_t (&acc)[NT][S::MT], int lane, Issue&& issue) {
+  template <int NT, class Issue, class... See>
+  __device__ __forceinline__ void step(const S& st, f32x4_t (&acc)[NT][S::MT], int lane, Issue&& issue, See&&... see) {
     if constexpr (SH > 1) {
       ring::wait_vmcnt<(S::NS - 2) * S::D>();
       ring::lds_barrier();
       issue(addr + (slot ? slot - 1 : S::NS - 1) * S::SLOT);
-      st.compute(lds + slot * S::SLOT, acc, lane);
+      st.compute(lds + slot * S::SLOT, acc, lane, see...);
     } else {
       ring::wait_vmcnt<(S::NS - 1) * S::D>();
-      st.compute(lds + slot * S::SLOT, acc, lane);
+      st.compute(lds + slot * S::SLOT, acc, lane, see...);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
       issue(addr + slot * S::SLOT);
     }
@@ -499,11 +511,11 @@ struct Walk {
 
 // ---- gate/up ------------------------------------------------------------------
 // An item is a tile of hidden columns of one pass; the workgroup takes a run of
-// items. SH = 1: 16 HB columns, the waves take a quarter of K each and their
-// sums meet in LDS; SH = NW: 16 HB columns per wave, all of K. The rings run on
+// items. SH = 1: 16 HB columns, the waves take equal parts of K and their sums
+// meet in LDS; SH = NW: 16 HB columns per wave, all of K. The rings run on
 // from item to item: while one is finished, the loads of the next are in flight.
 // RING: bytes of LDS for the workgroup's rings.
-template <class E, int FMT, int HB, int XR, int SH, int RING>
+template <class E, int FMT, int HB, int XR, int NW, int SH, int RING>
 __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
   constexpr int NT = 2 * HB, COLS = 16 * HB * SH;
   using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
@@ -626,34 +638,36 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
 
 // ---- down -----------------------------------------------------------------------
 // The K axis of an output tile is the list of (expert that occurs, K stage);
-// equal runs of it go to the splits (SH = NW: 16 NT columns per wave) or the
-// splits x NW waves (SH = 1: 16 NT columns for all). At an expert's end the
-// block of sums is weighted and added to the wave's own [token][column] tile in
-// LDS. TC: tokens that tile has room for.
-template <class E, int FMT, int NT, int XR, int SH, int RING, int TC>
+// equal runs of it go to the splits x NW / SH groups of SH waves (16 NT columns
+// for each wave of a group). At an expert's end the block of sums is weighted
+// and added to the wave's own [token][column] tile in LDS. TC: tokens that tile
+// has room for. Groups of a shared ring meet at barriers, so they take equally
+// many steps; more than one of them only for a dense product.
+template <class E, int FMT, int NT, int XR, int NW, int SH, int RING, int TC>
 __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
-  using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
-  constexpr int MT = S::MT, C = 16 * NT;
+  using S = typename StreamOf<E, FMT, NT, XR, SH, RING / (NW / SH)>::type;
+  constexpr int MT = S::MT, C = 16 * NT, KG = NW / SH;  // KG: groups
   __shared__ __attribute__((aligned(1024))) char lds[RING];
   __shared__ __attribute__((aligned(16))) float ysum[NW][TC * C];
   __shared__ Choices ch;
   __shared__ int16_t list[NW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.z * kChunk, tc = min(kChunk, g.T - t0);
-  const int wg0 = blockIdx.x * C * SH, col0 = wg0 + (SH > 1 ? wave * C : 0);  // the workgroup's, the wave's columns
+  const int wg0 = blockIdx.x * C * SH, col0 = wg0 + wave % SH * C;  // the workgroup's, the wave's columns
+  const int group = wave / SH;
   const bool routed = g.ids != nullptr;
   float* y = ysum[wave];
   for (int i = lane; i < tc * C; i += 64) y[i] = 0.f;
   Walk use;
   use.open(g, ch, list[wave], t0, tc, lane);
-  const int stages = S::stages(g.K), parts = g.splits * (NW / SH),
-            part = SH > 1 ? (int)blockIdx.y : (int)blockIdx.y * NW + wave;
+  const int stages = S::stages(g.K), parts = g.splits * KG, part = blockIdx.y * KG + group;
   int at = (int)((int64_t)use.hits * stages * part / parts);
   const int end = (int)((int64_t)use.hits * stages * (part + 1) / parts);
-  if (at < end) {
+  // groups that meet at barriers enter together, one without a stage too
+  if (KG > 1 && SH > 1 ? use.hits > 0 : at < end) {
     Walk get = use;
     S st;
-    st.init(g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, (uint32_t)(tc * g.k * g.K) * E::kBytes, wave, lane);
+    st.init(g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, (uint32_t)(tc * g.k * g.K) * E::kBytes, wave % SH, lane);
     auto set_rows = [&] {
       const int n = get.rows(XR);
 #pragma unroll
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
     auto begin_of = [&](int n) { return max(0, run0 - n * stages); };
     auto end_of = [&](int n) { return min(stages, end - n * stages); };
     int get_s = 0, get_end = 0;
-    bool more = true;
+    bool more = at < end;
     auto open_expert = [&](int n) {
       get.expert(n, lane);
       set_rows();
@@ -689,7 +703,7 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
     };
     open_expert(at / stages);
     Ring<S, SH> r;
-    r.start(lds + (SH > 1 ? 0 : wave * (RING / NW)), issue);
+    r.start(lds + group * (RING / KG), issue);
     for (int n = at / stages; n * stages < end; ++n) {
       use.expert(n, lane);
       const int count = end_of(n) - begin_of(n);
@@ -720,6 +734,11 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
             }
       } while (use.next_pass(XR, lane));
     }
+    if constexpr (SH > 1 && KG > 1) {
+      // one dead step for a group with a stage less than another
+      f32x4_t none[NT][MT] = {};
+      if (end - run0 < (use.hits * stages + parts - 1) / parts) r.step(st, none, lane, issue);
+    }
     ring::wait_vmcnt<0>();  // no load may land in LDS after the rings' end
   }
   __syncthreads();
@@ -730,7 +749,8 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
     const int row = i / Q, q = i % Q;
     f32x4_t v{};
     if constexpr (SH > 1) {
-      v = *(const f32x4_t*)(ysum[q / (C / 4)] + row * C + q % (C / 4) * 4);
+#pragma unroll
+      for (int w = 0; w < KG; ++w) v += *(const f32x4_t*)(ysum[w * SH + q / (C / 4)] + row * C + q % (C / 4) * 4);
     } else {
 #pragma unroll
       for (int w = 0; w < NW; ++w) v += *(const f32x4_t*)(ysum[w] + i * 4);
@@ -771,13 +791,16 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
 }
 
 // ---- launches ---------------------------------------------------------------------
-// Token rows per stage: as few as the largest possible list needs.
-static inline int token_rows(int64_t T, bool w4) { return T <= (w4 ? 4 : 8) ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+// Token rows per stage: as few as the largest possible list needs. (Eight waves
+// cannot share the loads of 32 rows of 128 bytes.)
+static inline int token_rows(int64_t T, bool w4) {
+  return T <= (w4 ? 4 : 8) ? 8 : T <= 16 ? 16 : w4 && T <= 32 ? 32 : 64;
+}
 
 // Columns of a down tile, and workgroups per tile: about as many over all tiles
 // as run at once, so that all CUs pull weights (one CU alone reads at a few
 // tens of GB/s).
-static inline int down_cols(int64_t T) { return T <= 16 ? 16 : 64; }
+static inline int down_cols(int64_t T) { return T <= 16 ? 16 : 128; }
 static inline int down_splits(int64_t T, int64_t D) {
   const int64_t tiles = (D + down_cols(T) - 1) / down_cols(T) * ((T + kChunk - 1) / kChunk);
   const int64_t s = ((T <= 16 ? 512 : 256) + tiles - 1) / tiles;
@@ -813,24 +836,27 @@ struct Call {
   hipStream_t stream;
 };
 
-// Two workgroups share a CU's LDS where at most 16 token rows are held
-// (private rings), else one has it (a shared ring).
+// At most 16 token rows: two workgroups of 4 waves with private rings share a
+// CU. More: one workgroup of 8 waves with a shared ring.
 template <class E, int FMT, int XR>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(STAGE_FEW_GATEUP, s);
-  constexpr int SH = XR <= 16 ? 1 : NW;
-  const int64_t items = (int64_t)slots * ((g.N + 16 * SH - 1) / (16 * SH)), fit = (SH == 1 ? 2 : 1) * dev_ncu();
+  constexpr bool kOwn = XR <= 16;
+  constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : 8;
+  const int64_t items = (int64_t)slots * ((g.N + 16 * SH - 1) / (16 * SH)), fit = (kOwn ? 2 : 1) * dev_ncu();
   const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_gateup<E, FMT, 1, XR, SH, SH == 1 ? 65536 : 147456>), grid, dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_gateup<E, FMT, 1, XR, NW, SH, kOwn ? 65536 : 147456>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
-template <class E, int FMT, int XR>
+// SH: waves that share the rows when there are more than 16.
+template <class E, int FMT, int XR, int SHARE>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
-  constexpr int SH = XR <= 16 ? 1 : NW;
+  constexpr bool kOwn = XR <= 16;
+  constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : SHARE;
   const dim3 grid((g.N + 16 * SH - 1) / (16 * SH), g.splits, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, SH, SH == 1 ? 65536 : 131072, SH == 1 ? 16 : kChunk>), grid,
-                     dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, kOwn ? 65536 : 122880, kOwn ? 16 : kChunk>), grid, dim3(NW * 64),
+                     0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 
@@ -838,13 +864,14 @@ static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, c
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
               c.zeros, 1, nullptr, nullptr, 0};
 }
-template <class E, int FMT>
+template <class E, int FMT, int SHARE>
 static int down_for(const Args& g, hipStream_t s) {
   switch (token_rows(g.T, FMT != 0)) {
-    case 8: return launch_down<E, FMT, FMT ? 4 : 8>(g, s);
-    case 16: return launch_down<E, FMT, 16>(g, s);
-    case 32: return launch_down<E, FMT, 32>(g, s);
-    default: return launch_down<E, FMT, 64>(g, s);
+    case 8: return launch_down<E, FMT, FMT ? 4 : 8, 1>(g, s);
+    case 16: return launch_down<E, FMT, 16, 1>(g, s);
+    case 32:
+      if constexpr (FMT != 0) return launch_down<E, FMT, 32, SHARE>(g, s);
+    default: return launch_down<E, FMT, 64, SHARE>(g, s);
   }
 }
 template <class E, int FMT>
@@ -852,15 +879,18 @@ static int gateup_for(const Args& g, int slots, hipStream_t s) {
   switch (token_rows(g.T, FMT != 0)) {
     case 8: return launch_gateup<E, FMT, FMT ? 4 : 8>(g, slots, s);
     case 16: return launch_gateup<E, FMT, 16>(g, slots, s);
-    case 32: return launch_gateup<E, FMT, 32>(g, slots, s);
+    case 32:
+      if constexpr (FMT != 0) return launch_gateup<E, FMT, 32>(g, slots, s);
     default: return launch_gateup<E, FMT, 64>(g, slots, s);
   }
 }
 
-// y = x W^T (dense).
+// y = x W^T (dense). Tiles of 64 columns with two groups of 4 waves along K where
+// the rows are shared: its K cannot be split over workgroups, whose arrival
+// counters no earlier launch would have cleared.
 template <class E, int FMT>
 int run_linear(const Call& c) {
-  return down_for<E, FMT>(args_of(c, c.x, c.D, c.H, c.y), c.stream);
+  return down_for<E, FMT, 4>(args_of(c, c.x, c.D, c.H, c.y), c.stream);
 }
 
 template <class E, int FMT>
@@ -879,7 +909,7 @@ int run_block(const Call& c) {
   d.splits = p.splits;
   d.partial = (float*)(c.ws + p.partial);
   d.ctr = g.ctr;
-  return down_for<E, FMT>(d, c.stream);
+  return down_for<E, FMT, 8>(d, c.stream);
 }
 
 }  // namespace few

@@ -25,7 +25,7 @@ template int run_linear<InstE, SWIGLU_INST_FMT>(const Call&);
 }  // namespace few
 #if SWIGLU_INST_FMT == 0
 namespace route {
-template int run_route<InstE>(const Args&, hipStream_t);
+template int run_route<InstE>(Args, hipStream_t);
 }
 #endif
 }  // namespace swiglu

@@ -3,11 +3,12 @@
 //   descending order (equal logits: the lower index), their p as weights,
 //   divided by their sum when renormalised.
 //
-// A workgroup takes 16 MT tokens and all experts: its NW waves split K, each
-// streams the router's weight as the operand of v_mfma_f32_16x16x32 through a
-// ring of registers, the sums meet in LDS, and one wave per token picks the
-// experts. One token is bound by the latency of that chain, thousands by each
-// CU's reading of the weight from L2 (E D values per 16 MT tokens).
+// Few tokens: one launch forms the logits, 16 experts and 16 tokens to a
+// workgroup, with K split over its waves and over workgroups so that many CUs
+// read the router's weight (one alone pulls 25 GB/s from HBM: 256 KiB took it
+// 10 us); a second one adds the parts and picks, one wave per token. Many
+// tokens: one launch, 32 tokens and all experts to a workgroup, bound by each
+// CU's reading of the weight from L2 (E D values per 32 tokens).
 //
 // The order of the logits decides which experts run, so it is made exact: an
 // fp32 sum is off by at most gamma |x| |w_e| (gamma counts the roundings of the
@@ -28,6 +29,8 @@ struct Args {
   float* wts;      // [T, k]
   int* ids;        // [T, k]
   int T, D, E, k, renorm;
+  float* part;     // few tokens: [splits][T][E] logits, then [splits][E] and [splits][T] sums of squares
+  int splits;
 };
 
 // Monotone map of fp32 to unsigned: larger value, larger key; NaN above all.
@@ -127,13 +130,13 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
-// Top-k, softmax and exact order of one token by one wave. l: its E logits
-// (LDS), bound: the largest |error| of one of them. NPL: logits per lane.
+// Top-k, softmax and exact order of one token by one wave. l: its logits,
+// expert i * 64 + lane in l[i]; bound: the largest |error| of one of them.
 template <class E, int NPL>
-__device__ __forceinline__ void choose(const Args& g, int t, const float* l, float bound, int lane) {
+__device__ __forceinline__ void choose(const Args& g, int t, const float (&l)[NPL], float bound, int lane) {
   uint32_t key[NPL];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) key[i] = i * 64 + lane < g.E ? order_key(l[i * 64 + lane]) : 0u;
+  for (int i = 0; i < NPL; ++i) key[i] = i * 64 + lane < g.E ? order_key(l[i]) : 0u;
 
   // Candidates in descending order of the fp32 logit, lane c holding the
   // c-th: the k largest and whatever follows within twice the bound.
@@ -172,7 +175,7 @@ __device__ __forceinline__ void choose(const Args& g, int t, const float* l, flo
   if (!g.renorm) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (i * 64 + lane < g.E) sum += expf(l[i * 64 + lane] - mx);
+      if (i * 64 + lane < g.E) sum += expf(l[i] - mx);
     sum = wave_sum(sum);
   }
   // neighbours closer than the bound: both recomputed in fp64
@@ -213,163 +216,239 @@ __device__ __forceinline__ void choose(const Args& g, int t, const float* l, flo
   }
 }
 
-// NB: expert blocks of 16 per pass over K; U: steps in flight.
-template <class E, int NW, int MT, int NB, int U>
-__global__ void __launch_bounds__(NW * 64, 1) route_topk(const Args g) {
-  constexpr int kTok = 16 * MT, kHalf = NW > 8 ? 8 : NW;
-  // logits [16 MT][E + 1], then the sums of kHalf waves
-  extern __shared__ __attribute__((aligned(16))) float sh[];
-  __shared__ float x2[kTok], w2[kMaxExperts];
-  __shared__ uint32_t w2max;
+// Sums of squares of the operands a stream shows it.
+template <class E, int NT, int MT>
+struct Squares {
+  float x[MT] = {}, w[NT] = {};
+  __device__ __forceinline__ void token(int m, u32x4_t v) { x[m] = add_squares<E>(v, x[m]); }
+  __device__ __forceinline__ void weight(int n, u32x4_t v) { w[n] = add_squares<E>(v, w[n]); }
+};
+// Over the four lanes that hold one row's chunks: every lane gets row lane & 15's.
+__device__ __forceinline__ float over_chunks(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Roundings of one logit's chain: a matrix instruction of 32 exact products
+// (fp32: four of 4 rounded ones) counted as 8 (16) of them, two to a stage,
+// then the parts' sums; 1 % for the roundings of the norms.
+template <class E>
+__device__ __forceinline__ float gamma_of(int stages, int parts) {
+  return 1.01f * (float)(stages * 2 * (E::kBytes == 4 ? 16 : 8) + parts) * 0x1p-24f;
+}
+
+// Few tokens, first launch: 16 experts (grid x), a part of K (y), XR tokens (z).
+constexpr int kPartWaves = 4;
+template <class E, int XR>
+__global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g) {
+  using S = few::RowStream<E, 1, XR, 1, 16384>;
+  __shared__ __attribute__((aligned(1024))) char lds[kPartWaves * 16384];
+  __shared__ float x2[kPartWaves][16], w2[kPartWaves][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.x * kTok, tc = min(kTok, g.T - t0);
-  const int ldl = g.E + 1;
-  float* logits = sh;
-  float* red = sh + ((kTok * ldl + 3) & ~3);
-  for (int i = threadIdx.x; i < kTok; i += NW * 64) x2[i] = 0.f;
-  for (int i = threadIdx.x; i < g.E; i += NW * 64) w2[i] = 0.f;
-  if (threadIdx.x == 0) w2max = 0u;
-  __syncthreads();
+  const int e0 = blockIdx.x * 16, t0 = blockIdx.z * XR, tc = min(XR, g.T - t0);
+  few::Args a{};
+  a.K = g.D;
+  S st;
   const int kb = g.D * E::kBytes;
-  const int steps = (kb + 63) >> 6, per = (steps + NW - 1) / NW;
-  const int s0 = wave * per, s1 = min(steps, s0 + per);
-  const int end = min(s1 * 64, kb);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc32(g.x + (int64_t)t0 * kb, tc * kb);
-  uint32_t x_off[MT];
+  st.init(a, g.x + (int64_t)t0 * kb, (uint32_t)(tc * kb), 0, lane);
+  st.weight(0, few::Weight{g.w, 0}, 0, e0, g.E);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) x_off[m] = (uint32_t)min(16 * m + (lane & 15), tc - 1) * (uint32_t)kb;
-  for (int b0 = 0; b0 * 16 < g.E; b0 += NB) {
-    const int nb = min(NB, (g.E + 15) / 16 - b0), rows = min(NB * 16, g.E - b0 * 16);
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc32(g.w + (int64_t)b0 * 16 * kb, rows * kb);
-    const uint32_t w_off = (uint32_t)(lane & 15) * (uint32_t)kb, blk = 16u * (uint32_t)kb;
-    struct Buf {
-      u32x4_t x[MT], w[NB];
-    } buf[U];
-    // rows past E and chunks past the run or K read as zeros
-    auto load = [&](Buf& b, int off) {
-      const bool in = off < end;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) b.x[m] = few::load16(xr, in ? x_off[m] + off : kOOB);
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        if (i < nb) b.w[i] = few::load16(wr, in ? w_off + i * blk + off : kOOB);
-    };
-    f32x4_t acc[NB][MT] = {};
-    float xs[MT] = {}, ws[NB] = {};
-    int off = s0 * 64 + (lane >> 4) * 16;
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(buf[u], off + 64 * u);
-    for (int s = s0; s < s1; s += U) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xs[m] = add_squares<E>(buf[u].x[m], xs[m]);
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          if (i < nb) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[i][m] = few::step_mfma<E>(buf[u].x[m], buf[u].w[i], acc[i][m]);
-            ws[i] = add_squares<E>(buf[u].w[i], ws[i]);
-          }
-        load(buf[u], off + 64 * (U + u));
-      }
-      off += 64 * U;
-    }
-    // Norms: any order of these sums will do, they only decide what is recomputed.
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float v = xs[m] + __shfl_xor(xs[m], 16);
-      v += __shfl_xor(v, 32);
-      if (b0 == 0 && lane < 16) atomicAdd(&x2[16 * m + lane], v);
-    }
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      if (i < nb) {
-        float v = ws[i] + __shfl_xor(ws[i], 16);
-        v += __shfl_xor(v, 32);
-        const int e = (b0 + i) * 16 + lane;
-        if (lane < 16 && e < g.E) atomicAdd(&w2[e], v);
-      }
-    // logits: the upper half of the waves hands over to the lower, which meet in LDS
-    if constexpr (NW > 8) {
-      if (wave >= kHalf) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            if (i < nb) *(f32x4_t*)(red + (((wave - kHalf) * NB + i) * MT + m) * 256 + lane * 4) = acc[i][m];
-      }
-      __syncthreads();
-      if (wave < NW - kHalf) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            if (i < nb) acc[i][m] += *(const f32x4_t*)(red + ((wave * NB + i) * MT + m) * 256 + lane * 4);
-      }
-    }
-    if (wave < kHalf) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (i < nb) *(f32x4_t*)(red + ((wave * NB + i) * MT + m) * 256 + lane * 4) = acc[i][m];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nb * MT * 256; i += NW * 64) {
-      const int col = i & 15, row = (i >> 4) & 15, m = (i >> 8) % MT, b = (i >> 8) / MT;
-      const int e = (b0 + b) * 16 + col, t = 16 * m + row;
-      const int at = (b * MT + m) * 256 + ((row >> 2) * 16 + col) * 4 + (row & 3);
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kHalf; ++w) v += red[w * NB * MT * 256 + at];
-      if (e < g.E && t < tc) logits[t * ldl + e] = v;
-    }
-    __syncthreads();
-  }
-  // not negative, so the bits order as the values do (a NaN above all)
-  for (int i = threadIdx.x; i < g.E; i += NW * 64) atomicMax(&w2max, __builtin_bit_cast(uint32_t, fabsf(w2[i])));
+  for (int j = 0; j < S::XD; ++j) st.x_off[j] = st.x_row(j, lane) < tc ? (uint32_t)st.x_row(j, lane) * kb : kOOB;
+  const int stages = S::stages(g.D), parts = g.splits * kPartWaves, part = blockIdx.y * kPartWaves + wave;
+  int s = stages * part / parts;
+  const int s1 = stages * (part + 1) / parts, n = s1 - s;
+  auto issue = [&](uint32_t slot) {
+    st.issue(slot, s, s < s1, lane);
+    ++s;
+  };
+  few::Ring<S, 1> r;
+  r.start(lds + wave * 16384, issue);
+  f32x4_t acc[1][1] = {};
+  Squares<E, 1, 1> sq;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) r.step(st, acc, lane, issue, sq);
+  ring::wait_vmcnt<0>();
   __syncthreads();
-  // roundings of one logit's chain: a matrix instruction of 32 exact products
-  // (fp32: four of 4 rounded ones) counted as 8 (16), then the waves' sums;
-  // 1 % for the roundings of the norms
-  const float gamma = 1.01f * (float)(per * (E::kBytes == 4 ? 16 : 8) + NW) * 0x1p-24f;
-  const float wn = __builtin_bit_cast(float, w2max);
-  for (int r = wave; r < tc; r += NW) {
-    const float bound = gamma * sqrtf(x2[r]) * sqrtf(wn);
-    const float* l = logits + r * ldl;
-    if (g.E <= 64) choose<E, 1>(g, t0 + r, l, bound, lane);
-    else if (g.E <= 128) choose<E, 2>(g, t0 + r, l, bound, lane);
-    else choose<E, 16>(g, t0 + r, l, bound, lane);
+  float* red = (float*)lds;
+  *(f32x4_t*)(red + wave * 256 + lane * 4) = acc[0][0];
+  const float xv = over_chunks(sq.x[0]), wv = over_chunks(sq.w[0]);
+  if (lane < 16) {
+    x2[wave][lane] = xv;
+    w2[wave][lane] = wv;
+  }
+  __syncthreads();
+  const int col = threadIdx.x & 15, row = threadIdx.x >> 4, e = e0 + col, t = t0 + row;
+  const int at = ((row >> 2) * 16 + col) * 4 + (row & 3);
+  float v = 0.f, vx = 0.f, vw = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPartWaves; ++w) {
+    v += red[w * 256 + at];
+    vx += x2[w][row];
+    vw += w2[w][col];
+  }
+  float* pw = g.part + (int64_t)g.splits * g.T * g.E;
+  float* px = pw + g.splits * g.E;
+  if (row < tc && e < g.E) g.part[((int64_t)blockIdx.y * g.T + t) * g.E + e] = v;
+  if (row == 0 && blockIdx.z == 0 && e < g.E) pw[blockIdx.y * g.E + e] = vw;
+  if (col == 0 && blockIdx.x == 0 && row < tc) px[(int64_t)blockIdx.y * g.T + t] = vx;
+}
+
+// Second launch: one wave per token.
+template <class E, int NPL>
+__global__ void __launch_bounds__(256) route_pick(const Args g) {
+  const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= g.T) return;
+  const float* pw = g.part + (int64_t)g.splits * g.T * g.E;
+  const float* px = pw + g.splits * g.E;
+  float l[NPL], wmax = 0.f, x2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = i * 64 + lane;
+    float v = 0.f, w = 0.f;
+    if (e < g.E)
+      for (int s = 0; s < g.splits; ++s) {
+        v += g.part[((int64_t)s * g.T + t) * g.E + e];
+        w += pw[s * g.E + e];
+      }
+    l[i] = v;
+    wmax = fmaxf(wmax, w);
+  }
+  for (int s = 0; s < g.splits; ++s) x2 += px[(int64_t)s * g.T + t];
+  // not negative, so the bits order as the values do
+  wmax = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, wmax)));
+  const int parts = g.splits * kPartWaves, stages = (g.D * E::kBytes + 127) >> 7;
+  const float bound = gamma_of<E>((stages + parts - 1) / parts, parts) * sqrtf(x2) * sqrtf(wmax);
+  choose<E, NPL>(g, t, l, bound, lane);
+}
+
+// Many tokens: 32 per workgroup. Two groups of 4 waves halve K; in a group each
+// wave takes 32 of every 128 experts and a quarter of the token rows' loads.
+constexpr int kManyTok = 32, kManyRing = 60 * 1024;
+template <class E, int NPL>
+__global__ void __launch_bounds__(512, 2) route_tokens(const Args g) {
+  using S = few::RowStream<E, 2, kManyTok, 4, kManyRing>;
+  constexpr int LD = NPL * 64 + 1;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kManyRing];
+  __shared__ float logits[kManyTok * LD], x2[2][kManyTok];
+  __shared__ uint32_t w2max[2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave >> 2, member = wave & 3;
+  const int t0 = blockIdx.x * kManyTok, tc = min(kManyTok, g.T - t0);
+  if (threadIdx.x < 2) w2max[threadIdx.x] = 0u;
+  few::Args a{};
+  a.K = g.D;
+  S st;
+  const int kb = g.D * E::kBytes;
+  st.init(a, g.x + (int64_t)t0 * kb, (uint32_t)(tc * kb), member, lane);
+  const int xrow = st.x_row(0, lane);
+  st.x_off[0] = xrow < tc ? (uint32_t)xrow * kb : kOOB;
+  // both groups take equally many steps (they meet at barriers); one may be dead
+  const int stages = S::stages(g.D), per = (stages + 1) / 2, s0 = group * per, s1 = min(stages, s0 + per);
+  const int passes = (g.E + 127) / 128;
+  int s = s0, pass = 0;
+  auto set_weights = [&] {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) st.weight(n, few::Weight{g.w, 0}, 0, pass * 128 + member * 32 + n * 16, g.E);
+  };
+  auto issue = [&](uint32_t slot) {
+    st.issue(slot, s, s < s1 && pass < passes, lane);
+    if (++s < s0 + per) return;
+    s = s0;
+    if (++pass < passes) set_weights();
+  };
+  set_weights();
+  few::Ring<S, 4> r;
+  r.start(lds + group * kManyRing, issue);
+  for (int p = 0; p < passes; ++p) {
+    f32x4_t acc[2][2] = {};
+    Squares<E, 2, 2> sq;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) r.step(st, acc, lane, issue, sq);
+    // group 0 writes its sums, group 1 adds its own
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+      if (w == group) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int e = p * 128 + member * 32 + n * 16 + (lane & 15), row = 16 * m + 4 * (lane >> 4) + j;
+              if (e < g.E) logits[row * LD + e] = w ? logits[row * LD + e] + acc[n][m][j] : acc[n][m][j];
+            }
+      }
+      ring::lds_barrier();
+    }
+    // norms: not negative, so the bits order as the values do
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float v = over_chunks(sq.w[n]);
+      atomicMax(&w2max[group], __builtin_bit_cast(uint32_t, v));
+    }
+    if (p == 0 && member == 0) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float v = over_chunks(sq.x[m]);
+        if (lane < 16) x2[group][16 * m + lane] = v;
+      }
+    }
+  }
+  ring::wait_vmcnt<0>();
+  __syncthreads();
+  // |w|^2 of any expert is at most the sum of the groups' largest parts
+  const float wn = sqrtf(__builtin_bit_cast(float, w2max[0]) + __builtin_bit_cast(float, w2max[1]));
+  const float gamma = gamma_of<E>(per, 2);
+  for (int row = wave; row < tc; row += 8) {
+    float l[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) l[i] = logits[row * LD + i * 64 + lane];
+    choose<E, NPL>(g, t0 + row, l, gamma * sqrtf(x2[0][row] + x2[1][row]) * wn, lane);
   }
 }
 
-template <class E, int NW, int MT, int NB, int U>
-static int launch(const Args& g, hipStream_t stream) {
-  const size_t lds = (size_t)(((16 * MT * (g.E + 1) + 3) & ~3) + (NW > 8 ? 8 : NW) * NB * MT * 256) * 4;
-  // above 64 KiB of dynamic LDS the kernel has to be told, once per device
-  static std::atomic<bool> told[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return SWIGLU_ERR_DEVICE;
-  if (!told[dev].load(std::memory_order_relaxed)) {
-    if (hipFuncSetAttribute((const void*)route_topk<E, NW, MT, NB, U>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            152 * 1024) != hipSuccess)
-      return SWIGLU_ERR_LAUNCH;
-    told[dev].store(true, std::memory_order_relaxed);
-  }
-  StageScope scope(STAGE_ROUTE, stream);
-  hipLaunchKernelGGL((route_topk<E, NW, MT, NB, U>), dim3((g.T + 16 * MT - 1) / (16 * MT)), dim3(NW * 64), lds, stream,
-                     g);
-  return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
+// Workgroups along K of the few-token logits: about 128 over all, each wave
+// with at least one stage.
+static inline int route_splits(int64_t T, int64_t D, int64_t E, size_t e) {
+  const int64_t tiles = (E + 15) / 16 * ((T + 15) / 16), stages = ((int64_t)D * e + 127) / 128;
+  int64_t s = 128 / tiles;
+  if (s > stages / kPartWaves) s = stages / kPartWaves;
+  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
 }
+static inline bool route_many(int64_t T, int64_t E) { return T > 1024 && E <= 256; }
+static inline size_t route_bytes(int64_t T, int64_t D, int64_t E, size_t e) {
+  if (T == 0 || route_many(T, E)) return 0;
+  return (size_t)route_splits(T, D, E, e) * (size_t)(T * E + E + T) * 4;
+}
+
+#define SWIGLU_ROUTE_LAUNCH(kernel, grid, threads)                               \
+  do {                                                                           \
+    StageScope scope(STAGE_ROUTE, stream);                                       \
+    hipLaunchKernelGGL((kernel), dim3 grid, dim3(threads), 0, stream, g);        \
+    if (hipGetLastError() != hipSuccess) return SWIGLU_ERR_LAUNCH;               \
+  } while (0)
 
 template <class E>
-int run_route(const Args& g, hipStream_t stream) {
+int run_route(Args g, hipStream_t stream) {
   if (g.T == 0) return SWIGLU_OK;
-  if (g.T > 2048 && g.E <= 128) return launch<E, 8, 2, 8, 2>(g, stream);
-  if (g.E <= 64) return launch<E, 16, 1, 4, 2>(g, stream);
-  return launch<E, 16, 1, 8, 1>(g, stream);
+  if (route_many(g.T, g.E)) {
+    const int tiles = (g.T + kManyTok - 1) / kManyTok;
+    if (g.E <= 128) SWIGLU_ROUTE_LAUNCH((route_tokens<E, 2>), (tiles), 512);
+    else SWIGLU_ROUTE_LAUNCH((route_tokens<E, 4>), (tiles), 512);
+    return SWIGLU_OK;
+  }
+  g.splits = route_splits(g.T, g.D, g.E, E::kBytes);
+  const unsigned blocks = (g.E + 15) / 16;
+  if (g.T <= 8) SWIGLU_ROUTE_LAUNCH((route_logits<E, 8>), (blocks, g.splits, 1), kPartWaves * 64);
+  else SWIGLU_ROUTE_LAUNCH((route_logits<E, 16>), (blocks, g.splits, (g.T + 15) / 16), kPartWaves * 64);
+  const unsigned groups = (g.T + 3) / 4;
+  if (g.E <= 64) SWIGLU_ROUTE_LAUNCH((route_pick<E, 1>), (groups), 256);
+  else if (g.E <= 128) SWIGLU_ROUTE_LAUNCH((route_pick<E, 2>), (groups), 256);
+  else if (g.E <= 256) SWIGLU_ROUTE_LAUNCH((route_pick<E, 4>), (groups), 256);
+  else SWIGLU_ROUTE_LAUNCH((route_pick<E, 16>), (groups), 256);
+  return SWIGLU_OK;
 }
+#undef SWIGLU_ROUTE_LAUNCH
 
 }  // namespace route
 }  // namespace swiglu

@@ -168,7 +168,7 @@ def w4_pack(codes, scales, zeros=None):
     return W4Weight(data, shape, group, zeros is not None, scales.dtype)
 
 
-def moe_route(x, w_router, top_k, renormalize=True, weights=None, ids=None):
+def moe_route(x, w_router, top_k, renormalize=True, weights=None, ids=None, workspace=None):
     """The router: (weights [T, k] fp32, ids [T, k] int32) of the ``top_k``
     largest logits of x[T, D] w_router[E, D]^T per token, in descending order
     (equal logits: the lower index first). Weights are the softmax over all
@@ -178,8 +178,11 @@ def moe_route(x, w_router, top_k, renormalize=True, weights=None, ids=None):
     T, D, E = _router_shapes(x, w_router, top_k)
     weights = _buf(weights, (T, top_k), torch.float32, x.device, "weights")
     ids = _buf(ids, (T, top_k), torch.int32, x.device, "ids")
-    rc = _L.lib().swiglu_mlp_moe_route(_ptr(x), w_router.data_ptr(), _ptr(weights), _ptr(ids), T, D, E, top_k,
-                                       bool(renormalize), _code(x), _stream(x.device))
+    dt, L = _code(x), _L.lib()
+    ws = _workspace(workspace, L.swiglu_mlp_moe_route_workspace_bytes(T, D, E, dt), x.device)
+    rc = L.swiglu_mlp_moe_route(_ptr(x), w_router.data_ptr(), _ptr(weights), _ptr(ids), _ptr(ws),
+                                ws.numel() * ws.element_size(), T, D, E, top_k, bool(renormalize), dt,
+                                _stream(x.device))
     _check(rc, "swiglu_mlp_moe_route")
     return weights, ids
 
@@ -235,7 +238,7 @@ def moe_experts(x, weights, ids, wg, wu, wd, y=None, workspace=None):
         raise ValueError("weights must be fp32 and ids int32, both [T, k] on x's device")
     k, dt, L = ids.shape[1], _code(x), _L.lib()
     y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, k, dt), x.device)
+    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, k, dt), x.device)
     nbytes = ws.numel() * ws.element_size()
     if w4:
         rc = L.swiglu_mlp_moe_experts_w4(_ptr(x), _ptr(weights), _ptr(ids), wg._ref, wu._ref, wd._ref, _ptr(y),
@@ -260,7 +263,7 @@ def moe_infer(x, w_router, wg, wu, wd, top_k, renormalize=True, y=None, workspac
         raise ValueError(f"the router has {E} experts, the weights {E2}")
     dt, L = _code(x), _L.lib()
     y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, top_k, dt), x.device)
+    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, top_k, dt), x.device)
     nbytes = ws.numel() * ws.element_size()
     if w4:
         rc = L.swiglu_mlp_moe_infer_w4(_ptr(x), w_router.data_ptr(), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws),

@@ -249,15 +249,20 @@ typedef struct {
   int32_t has_zeros;
 } swiglu_w4_t;
 
-int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, int64_t T,
-                         int64_t D, int64_t E, int64_t k, int renorm, int dtype, hipStream_t stream);
+/* workspace: the logits' partial sums for T <= 1024 or E > 256, else none
+ * (may be NULL). Contents on entry do not matter. 0 bytes on bad args. */
+size_t swiglu_mlp_moe_route_workspace_bytes(int64_t T, int64_t D, int64_t E, int dtype);
+int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, void* workspace,
+                         size_t workspace_bytes, int64_t T, int64_t D, int64_t E, int64_t k, int renorm,
+                         int dtype, hipStream_t stream);
 
 /* Bytes of a mixture's workspace: the A plane [T k, H], the arrival counters
  * and fp32 partial sums of the down projection where its K is split over
- * workgroups, and the router's weights and ids, each 256-byte aligned.
+ * workgroups (before them, in the same place, the router's workspace), and
+ * the router's weights and ids, each 256-byte aligned.
  * Contents on entry do not matter; calls that share one must be
  * stream-ordered. 0 on bad args. */
-size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t k, int dtype);
+size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int dtype);
 
 int swiglu_mlp_moe_experts(const void* X, const float* weights, const int32_t* ids, const void* Wg,
                            const void* Wu, const void* Wd, void* Y, void* workspace,

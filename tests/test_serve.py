@@ -131,8 +131,8 @@ def _codes(L):
     r = ctypes.byref
     at = [B + (i << 34) for i in range(10)]
 
-    def route(X=at[0], W=at[1], P=at[2], I=at[3], T=4, D=64, E=8, k=2, dt=0):
-        return L.swiglu_mlp_moe_route(X, W, P, I, T, D, E, k, 1, dt, None)
+    def route(X=at[0], W=at[1], P=at[2], I=at[3], T=4, D=64, E=8, k=2, dt=0, ws=at[9], n=1 << 30):
+        return L.swiglu_mlp_moe_route(X, W, P, I, ws, n, T, D, E, k, 1, dt, None)
 
     def experts(X=at[0], P=at[1], I=at[2], Wg=at[3], Wu=at[4], Wd=at[5], Y=at[6], ws=at[7], n=1 << 30, T=4, D=64, H=128,
                 E=8, k=2, dt=0):
@@ -174,8 +174,12 @@ def test_host_validation_codes():
     assert block(ws=None, n=0) == 6 and block(n=4 * 64 * 2 - 1) == 6
     # the queries
     ws = L.swiglu_mlp_moe_workspace_bytes
-    assert ws(4, 64, 128, 2, 0) >= 8 * 128 * 2 + 256 + 256 and ws(200, 8192, 128, 2, 0) == 400 * 128 * 2 + 2 * 1792
-    assert ws(0, 64, 128, 2, 0) == 0 and ws(4, 64, 128, 33, 0) == 0 and ws(4, 60, 128, 2, 0) == 0
+    assert ws(4, 64, 128, 8, 2, 0) >= 8 * 128 * 2 + 256 + 256 and ws(200, 65536, 128, 8, 2, 0) == 400 * 128 * 2 + 2 * 1792
+    assert ws(0, 64, 128, 8, 2, 0) == 0 and ws(4, 64, 128, 64, 33, 0) == 0 and ws(4, 60, 128, 8, 2, 0) == 0
+    rw = L.swiglu_mlp_moe_route_workspace_bytes
+    assert rw(4, 64, 8, 0) == 4 * (4 * 8 + 8 + 4) and rw(4096, 64, 8, 0) == 0 and rw(4, 60, 8, 0) == 0
+    assert route(ws=None, n=0) == 6 and route(n=100) == 6 and route(ws=at[9] + 4) == 4 and route(ws=at[2]) == 5
+    assert route(ws=None, n=0, T=4096, X=at[0] + 8) == 4  # no workspace needed there: the next check speaks
     assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 0) == 4 * (1024 + 16 * 4 * 2)
     assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 1) == 4 * (1024 + 16 * 4 * 2 + 32)
     assert L.swiglu_mlp_w4_bytes(1, 64, 100, 32, 0) == 0
@@ -187,7 +191,8 @@ def test_host_validation_codes():
 @gpu
 @pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("T,E,k,D", [(1, 8, 2, 1024), (1, 64, 8, 2048), (5, 3, 3, 8), (16, 130, 7, 136), (17, 1, 1, 64),
-                                     (33, 128, 8, 1000), (100, 1024, 32, 256), (1000, 60, 4, 520), (0, 8, 2, 64)])
+                                     (33, 128, 8, 1000), (100, 1024, 32, 256), (1000, 60, 4, 520), (0, 8, 2, 64),
+                                     (1030, 64, 8, 264), (1100, 129, 3, 72), (1025, 256, 2, 1000)])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route(T, E, k, D, dt, renorm):
     banner(f"route {dt} T={T} E={E} k={k} D={D} renorm={renorm}")
@@ -460,7 +465,7 @@ def test_strides_streams_buffers_and_graph():
     assert torch.equal(m.moe_experts(x[3:], p[3:], ids[3:], *w), y[3:])
     # another stream, with the caller's own buffers
     out = torch.empty_like(y)
-    need = _lib.lib().swiglu_mlp_moe_workspace_bytes(T, D, H, k, 0)
+    need = _lib.lib().swiglu_mlp_moe_workspace_bytes(T, D, H, E, k, 0)
     buf = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
