@@ -110,10 +110,10 @@ static int run_route_for(int dtype, const route::Args& r, hipStream_t stream) {
 struct MoePlan {
   size_t wts, ids, total;
 };
-static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, size_t e) {
+static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, bool w4, size_t e) {
   const size_t p = (size_t)T * k;
   MoePlan m;
-  m.wts = few::block_plan(T, D, H, k, e).total;
+  m.wts = few::block_plan(few::shape_of(T, k, E, true, w4), T, D, H, k, e).total;
   const size_t r = up256(route::route_bytes(T, D, E, e));
   if (m.wts < r) m.wts = r;
   m.ids = m.wts + up256(p * 4);
@@ -127,7 +127,7 @@ static int moe_call(const void* X, const void* Wr, const float* weights, const i
                     few::Call& c, void* Y, void* ws, size_t ws_bytes, int64_t T, int64_t k, int renorm, int dtype,
                     int group, hipStream_t stream) {
   const size_t e = elt_bytes(dtype);
-  const MoePlan m = moe_plan(T, c.D, c.H, c.E, k, e);
+  const MoePlan m = moe_plan(T, c.D, c.H, c.E, k, group != 0, e);
   const size_t p4 = (size_t)T * k * 4;
   const bool routed = Wr != nullptr;
   const Range in[] = {{X, (size_t)T * c.D * e}, w[0], w[1], w[2], {Wr, routed ? (size_t)c.E * c.D * e : 0},
@@ -246,7 +246,9 @@ int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t*
 size_t swiglu_mlp_moe_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int dtype) {
   const size_t e = elt_bytes(dtype);
   if (!e || T <= 0 || !ld_ok(D) || !ld_ok(H) || check_few(T, E, k)) return 0;
-  return moe_plan(T, D, H, E, k, e).total;
+  // the larger of the two weight formats' plans
+  const size_t rows = moe_plan(T, D, H, E, k, false, e).total, w4 = moe_plan(T, D, H, E, k, true, e).total;
+  return rows > w4 ? rows : w4;
 }
 
 int swiglu_mlp_moe_experts(const void* X, const float* weights, const int32_t* ids, const void* Wg, const void* Wu,
@@ -363,7 +365,7 @@ int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T
 size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t D, int64_t H, int dtype) {
   const size_t e = elt_bytes(dtype);
   if (e != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(D) || !ld_ok(H)) return 0;
-  return few::block_plan(T, D, H, 1, e).total;
+  return few::block_plan(few::shape_of(T, 1, 1, false, true), T, D, H, 1, e).total;
 }
 
 int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t* wu, const swiglu_w4_t* wd, void* Y,
@@ -376,7 +378,7 @@ int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t*
       wd->experts != 1 || wu->group != wg->group || wd->group != wg->group || !wu->has_zeros != !wg->has_zeros ||
       !wd->has_zeros != !wg->has_zeros || T < 0 || T > SWIGLU_FEW_MAX_T)
     return SWIGLU_ERR_SHAPE;
-  const size_t td = (size_t)T * wg->K * e, need = few::block_plan(T, wg->K, wg->N, 1, e).total;
+  const size_t td = (size_t)T * wg->K * e, need = few::block_plan(few::shape_of(T, 1, 1, false, true), T, wg->K, wg->N, 1, e).total;
   const Range in[] = {{X, td}, w4_range(wg), w4_range(wu), w4_range(wd)};
   const Range out[] = {{Y, td}, {workspace, need}};
   if ((rc = check_ptrs(in, 4)) || (rc = check_ptrs(out, 1))) return rc;

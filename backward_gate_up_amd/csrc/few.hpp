@@ -102,9 +102,11 @@ __device__ __forceinline__ i32x4_t scalar_rsrc(i32x4_t r) {
 }
 
 // Four bytes per lane to LDS address lds + 4 * lane (see dma16).
-__device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff) {
+__device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff, uint32_t soff) {
   lds = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rs), "{m0}"(lds) : "memory");
+  soff = __builtin_amdgcn_readfirstlane(soff);
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rs), "s"(soff), "{m0}"(lds)
+               : "memory");
 }
 
 // ---- streams ------------------------------------------------------------------
@@ -153,31 +155,55 @@ struct RowStream {
     kb = g.K * E::kBytes;
     rx = rsrc_words(xb, x_bytes);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) w_off[j] = (uint32_t)(8 * j + (lane >> 3)) * (uint32_t)kb;
+    for (int j = 0; j < 2; ++j) {
+      const int r = 8 * j + (lane >> 3);
+      w_off[j] = (uint32_t)r * (uint32_t)kb + chunk(r, lane);
+    }
+  }
+  // the byte of a stage's 128 that this lane fetches of row r
+  static __device__ __forceinline__ uint32_t chunk(int r, int lane) { return ((lane & 7) ^ kc_swz(r)) << 4; }
+  // load j's token row starts at byte `row` of the tokens (kOOB: there is none)
+  __device__ __forceinline__ void token_row(int j, uint32_t row, int lane) {
+    x_off[j] = row == kOOB ? kOOB : row + chunk(x_row(j, lane), lane);
   }
   // block n: rows row0 .. row0 + 15 of expert e's weight; rows past N read as zeros
   __device__ __forceinline__ void weight(int n, const Weight& wt, int e, int row0, int N) {
     const int rows = max(0, min(16, N - row0));
     rw[n] = rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)row0 * kb, (int64_t)rows * kb);
   }
-  // loads stage s into the slot; not live: zeros
+  // Loads stage s into the slot; not live: zeros. K advances through the scalar
+  // offset, which the range check leaves out; a dead stage has buffers of no
+  // bytes, so that the lanes' offsets never change, except that those past K
+  // in a partial last stage go out of range.
   __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
-    const int end = live ? kb : 0;
-    const i32x4_t xr = scalar_rsrc(rx);
-    i32x4_t w[NT];
+    const uint32_t at = live ? (uint32_t)s * 128u : 0u;
+    const int left = kb - (int)at;
+    i32x4_t w[NT], xr = rx;
+    xr[2] = live ? xr[2] : 0;
+    xr = scalar_rsrc(xr);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) w[n] = scalar_rsrc(rw[n]);
+    for (int n = 0; n < NT; ++n) {
+      w[n] = rw[n];
+      w[n][2] = live ? w[n][2] : 0;
+      w[n] = scalar_rsrc(w[n]);
+    }
+    uint32_t wo[2], xo[XD];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int off = s * 128 + (((lane & 7) ^ kc_swz(8 * j + (lane >> 3))) << 4);
+    for (int j = 0; j < 2; ++j) wo[j] = w_off[j];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, w[n], off < end ? w_off[j] + off : kOOB, 0u);
+    for (int j = 0; j < XD; ++j) xo[j] = x_off[j];
+    if (left < 128) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) wo[j] = (int)chunk(8 * j + (lane >> 3), lane) < left ? wo[j] : kOOB;
+#pragma unroll
+      for (int j = 0; j < XD; ++j) xo[j] = (int)chunk(x_row(j, lane), lane) < left ? xo[j] : kOOB;
     }
 #pragma unroll
-    for (int j = 0; j < XD; ++j) {
-      const int off = s * 128 + (((lane & 7) ^ kc_swz(x_row(j, lane))) << 4);
-      dma16(slot + (share * XD + j) * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
-    }
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, w[n], wo[j], at);
+#pragma unroll
+    for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, xr, xo[j], at);
   }
   struct Nothing {
     __device__ __forceinline__ void token(int, u32x4_t) {}
@@ -250,30 +276,50 @@ struct W4Stream {
     const int len = row0 < N ? stages(kb >> 1) * rec : 0;
     rw[n] = rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)(row0 >> 4) * len, len);
   }
+  static __device__ __forceinline__ uint32_t chunk(int r, int lane) { return ((lane & 15) ^ (r & 15)) << 4; }
+  __device__ __forceinline__ void token_row(int j, uint32_t row, int lane) {
+    x_off[j] = row == kOOB ? kOOB : row + chunk(x_row(j, lane), lane);
+  }
   __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
-    const uint32_t at = (uint32_t)s * rec;
+    const uint32_t at = live ? (uint32_t)s * (uint32_t)rec : 0u, atx = live ? (uint32_t)s * 256u : 0u;
+    const int left = kb - (int)atx;
+    i32x4_t xr = rx;
+    xr[2] = live ? xr[2] : 0;
+    xr = scalar_rsrc(xr);
+    const uint32_t scales = 1024 + lane * 4 < rec ? 1024 + lane * 4 : kOOB;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const i32x4_t w = scalar_rsrc(rw[n]);
-      dma16(slot + w_at + n * WS, w, live ? at + lane * 16 : kOOB, 0u);
-      dma4(slot + w_at + n * WS + 1024, w, live && 1024 + lane * 4 < rec ? at + 1024 + lane * 4 : kOOB);
+      i32x4_t w = rw[n];
+      w[2] = live ? w[2] : 0;
+      w = scalar_rsrc(w);
+      dma16(slot + w_at + n * WS, w, lane * 16, at);
+      dma4(slot + w_at + n * WS + 1024, w, scales, at);
     }
-    const int end = live ? kb : 0;
-    const i32x4_t xr = scalar_rsrc(rx);
+    uint32_t xo[XD];
 #pragma unroll
-    for (int j = 0; j < XD; ++j) {
-      const int off = s * 256 + (((lane & 15) ^ (x_row(j, lane) & 15)) << 4);
-      dma16(slot + (share * XD + j) * 1024, xr, off < end ? x_off[j] + off : kOOB, 0u);
+    for (int j = 0; j < XD; ++j) xo[j] = x_off[j];
+    if (left < 256) {
+#pragma unroll
+      for (int j = 0; j < XD; ++j) xo[j] = (int)chunk(x_row(j, lane), lane) < left ? xo[j] : kOOB;
     }
+#pragma unroll
+    for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, xr, xo[j], atx);
+  }
+  // (v & m) | o in one instruction: its operands have to be registers, and the
+  // compiler, which knows the constants, would take two with literals
+  static __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t m, uint32_t o) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(m), "v"(o));
+    return r;
   }
   // eight codes of one dword as the MFMA operand OFF + q
   static __device__ __forceinline__ u32x4_t widen(uint32_t v) {
     if constexpr (std::is_same<E, Bf16>::value) {
       constexpr uint32_t m = 0x000f000fu, o = 0x43004300u;  // 128 + q: mantissa step 1
-      return u32x4_t{(v & m) | o, ((v >> 4) & m) | o, ((v >> 8) & m) | o, ((v >> 12) & m) | o};
+      return u32x4_t{and_or(v, m, o), and_or(v >> 4, m, o), and_or(v >> 8, m, o), and_or(v >> 12, m, o)};
     } else {
       constexpr uint32_t m = 0x00f000f0u, o = 0x54005400u;  // 64 + q: mantissa step 1/16
-      return u32x4_t{((v << 4) & m) | o, (v & m) | o, ((v >> 4) & m) | o, ((v >> 8) & m) | o};
+      return u32x4_t{and_or(v << 4, m, o), and_or(v, m, o), and_or(v >> 4, m, o), and_or(v >> 8, m, o)};
     }
   }
   static __device__ __forceinline__ u32x4_t ones() {
@@ -475,7 +521,7 @@ struct Walk {
       hits = __builtin_amdgcn_readfirstlane(c.hits);
     }
   }
-  // The n-th expert (n > i), first pass.
+  // The n-th expert (n >= i), first pass.
   __device__ __forceinline__ void expert(int n, int lane) {
     first = 0;
     if (!g->ids) {
@@ -483,13 +529,11 @@ struct Walk {
       p = {lane, P};
       total = P;
     } else if (P <= 64) {
-      uint64_t m = 0;
       for (; i < n; ++i) {
         e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
-        m = __ballot(id == e);
-        left &= ~m;
+        left &= ~__ballot(id == e);
       }
-      p = mask_pairs(m, lane);
+      p = mask_pairs(__ballot(id == e), lane);
       total = p.n;
     } else {
       e = __builtin_amdgcn_readfirstlane(ch->expert[n]);
@@ -531,9 +575,12 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
   Walk use;  // the item being multiplied
   use.open(g, ch, list[wave], t0, tc, lane);
   const int tiles = (g.N + COLS - 1) / COLS, items = use.hits * tiles;
-  int item = (int)((int64_t)items * blockIdx.x / gridDim.x);
-  const int last = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
-  if (item >= last) return;
+  // (divisions are done by vector instructions: back to scalar registers)
+  int left = __builtin_amdgcn_readfirstlane((int)((int64_t)items * blockIdx.x / gridDim.x));
+  const int last = __builtin_amdgcn_readfirstlane((int)((int64_t)items * (blockIdx.x + 1) / gridDim.x));
+  if (left >= last) return;
+  int nth = __builtin_amdgcn_readfirstlane(left / tiles), tile = left - nth * tiles;  // the item: expert, tile
+  left = last - left;
   Walk get = use;  // the item being loaded
   S st;
   st.init(g, g.x + (int64_t)t0 * g.K * E::kBytes, (uint32_t)(tc * g.K) * E::kBytes, wave, lane);
@@ -542,18 +589,17 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
   const int wcol = SH > 1 ? 16 * HB * wave : 0;  // the wave's first column of a tile
 
   // loading side: the next stage of the current item, then the next item
-  int get_item = item, get_s = s0;
-  bool more = true;
+  int get_nth = nth, get_tile = tile, get_left = left, get_s = s0;
   auto set_rows = [&] {
     const int n = get.rows(XR);
 #pragma unroll
     for (int j = 0; j < S::XD; ++j) {
       const int i = st.x_row(j, lane), pair = get.pair(i);
-      st.x_off[j] = i < n ? ((pair * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB;
+      st.token_row(j, i < n ? ((pair * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB, lane);
     }
   };
   auto set_weights = [&] {
-    const int row0 = (get_item % tiles) * COLS + wcol;
+    const int row0 = get_tile * COLS + wcol;
 #pragma unroll
     for (int b = 0; b < HB; ++b) {
       st.weight(2 * b, g.w0, get.e, row0 + 16 * b, g.N);
@@ -561,22 +607,26 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
     }
   };
   auto issue = [&](uint32_t slot) {
-    st.issue(slot, get_s, more && get_s < s1, lane);
-    if (++get_s < s0 + per || !more) return;
+    st.issue(slot, get_s, get_left > 0 && get_s < s1, lane);
+    if (++get_s < s0 + per || get_left == 0) return;
     get_s = s0;
     if (get.next_pass(XR, lane)) {
       set_rows();
       return;
     }
-    more = ++get_item < last;
-    if (!more) return;
-    if (get.first || get_item % tiles == 0) {
-      get.expert(get_item / tiles, lane);
+    if (--get_left == 0) return;
+    const bool turn = ++get_tile == tiles;
+    if (turn) {
+      get_tile = 0;
+      ++get_nth;
+    }
+    if (get.first || turn) {
+      get.expert(get_nth, lane);
       set_rows();
     }
     set_weights();
   };
-  get.expert(item / tiles, lane);
+  get.expert(nth, lane);
   set_rows();
   set_weights();
   Ring<S, SH> r;
@@ -587,12 +637,12 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
   auto store = [&](int pair, int h, float gate, float up) {
     ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] = E::from_f32(gate * sigmoid_f32<E>(gate) * up);
   };
-  use.expert(item / tiles, lane);
+  use.expert(nth, lane);
   while (true) {
     f32x4_t acc[NT][MT] = {};
 #pragma unroll 1
     for (int s = 0; s < per; ++s) r.step(st, acc, lane, issue);
-    const int n = use.rows(XR), row0 = (item % tiles) * COLS + wcol;
+    const int n = use.rows(XR), row0 = tile * COLS + wcol;
     if constexpr (SH > 1) {
       // the wave has all of K: lane -> hidden column l % 16, token rows 4 (l / 16) + j
 #pragma unroll
@@ -630,8 +680,13 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
       }
     }
     if (use.next_pass(XR, lane)) continue;
-    if (++item >= last) break;
-    if (use.first || item % tiles == 0) use.expert(item / tiles, lane);
+    if (--left == 0) break;
+    const bool turn = ++tile == tiles;
+    if (turn) {
+      tile = 0;
+      ++nth;
+    }
+    if (use.first || turn) use.expert(nth, lane);
   }
   ring::wait_vmcnt<0>();  // no load may land in LDS after the workgroup's end
 }
@@ -661,8 +716,10 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
   Walk use;
   use.open(g, ch, list[wave], t0, tc, lane);
   const int stages = S::stages(g.K), parts = g.splits * KG, part = blockIdx.y * KG + group;
-  int at = (int)((int64_t)use.hits * stages * part / parts);
-  const int end = (int)((int64_t)use.hits * stages * (part + 1) / parts);
+  // (divisions are done by vector instructions: back to scalar registers)
+  int at = __builtin_amdgcn_readfirstlane((int)((int64_t)use.hits * stages * part / parts));
+  const int end = __builtin_amdgcn_readfirstlane((int)((int64_t)use.hits * stages * (part + 1) / parts));
+  const int nth = __builtin_amdgcn_readfirstlane(at / stages);
   // groups that meet at barriers enter together, one without a stage too
   if (KG > 1 && SH > 1 ? use.hits > 0 : at < end) {
     Walk get = use;
@@ -673,7 +730,7 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
 #pragma unroll
       for (int j = 0; j < S::XD; ++j) {
         const int i = st.x_row(j, lane), pair = get.pair(i);
-        st.x_off[j] = i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB;
+        st.token_row(j, i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB, lane);
       }
     };
     // the run's stages of the n-th expert
@@ -701,10 +758,10 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
       more = (get.i + 1) * stages < end;
       if (more) open_expert(get.i + 1);
     };
-    open_expert(at / stages);
+    open_expert(nth);
     Ring<S, SH> r;
     r.start(lds + group * (RING / KG), issue);
-    for (int n = at / stages; n * stages < end; ++n) {
+    for (int n = nth; n * stages < end; ++n) {
       use.expert(n, lane);
       const int count = end_of(n) - begin_of(n);
       do {
@@ -791,20 +848,31 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
 }
 
 // ---- launches ---------------------------------------------------------------------
-// Token rows per stage: as few as the largest possible list needs. (Eight waves
-// cannot share the loads of 32 rows of 128 bytes.)
-static inline int token_rows(int64_t T, bool w4) {
-  return T <= (w4 ? 4 : 8) ? 8 : T <= 16 ? 16 : w4 && T <= 32 ? 32 : 64;
+// Token rows per stage (8: as few as a load instruction covers, 8 or in 4 bits
+// 4). Dense: what the tokens need. Routed: what an expert's share of the pairs
+// mostly needs, T k / E on average; a more crowded expert takes several passes
+// over its weights. Above 16 rows waves have to share them, and 8 waves cannot
+// share the loads of 32 rows of 128 bytes.
+struct Shape {
+  int rows;   // token rows
+  bool own;   // private rings: two workgroups of 4 waves per CU; else one of 8 waves
+};
+static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool w4) {
+  const int64_t few = w4 ? 4 : 8, load = routed ? T * k : 0;  // load <= m E: m pairs per expert on average
+  int rows = 64;
+  if (T <= few || (routed && 4 * load <= few * E)) rows = 8;
+  else if (T <= 16 || (routed && load <= 6 * E)) rows = 16;
+  else if (w4 && (T <= 32 || (routed && load <= 12 * E))) rows = 32;
+  return {rows, rows <= 16};
 }
 
 // Columns of a down tile, and workgroups per tile: about as many over all tiles
-// as run at once, so that all CUs pull weights (one CU alone reads at a few
-// tens of GB/s).
-static inline int down_cols(int64_t T) { return T <= 16 ? 16 : 128; }
-static inline int down_splits(int64_t T, int64_t D) {
-  const int64_t tiles = (D + down_cols(T) - 1) / down_cols(T) * ((T + kChunk - 1) / kChunk);
-  const int64_t s = ((T <= 16 ? 512 : 256) + tiles - 1) / tiles;
-  return s > 8 ? 8 : (int)s;
+// as run at once, so that all CUs pull weights.
+static inline int down_cols(const Shape& f) { return f.own ? 16 : 128; }
+static inline int down_splits(const Shape& f, int64_t T, int64_t D) {
+  const int64_t tiles = (D + down_cols(f) - 1) / down_cols(f) * ((T + kChunk - 1) / kChunk);
+  const int64_t s = ((f.own ? 512 : 256) + tiles - 1) / tiles, most = f.own ? 8 : 32;
+  return (int)(s > most ? most : s);
 }
 // Workspace of a block: the A plane, then where the down projection is split
 // one counter per output tile and the partial sums, each 256-byte aligned.
@@ -812,11 +880,11 @@ struct BlockPlan {
   size_t ctr, partial, total;
   int splits, n_ctr;
 };
-static inline BlockPlan block_plan(int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
+static inline BlockPlan block_plan(const Shape& f, int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   BlockPlan p;
-  p.splits = down_splits(T, D);
-  p.n_ctr = p.splits > 1 ? (int)((D + down_cols(T) - 1) / down_cols(T) * ((T + kChunk - 1) / kChunk)) : 0;
+  p.splits = down_splits(f, T, D);
+  p.n_ctr = p.splits > 1 ? (int)((D + down_cols(f) - 1) / down_cols(f) * ((T + kChunk - 1) / kChunk)) : 0;
   p.ctr = up((size_t)T * k * H * e);
   p.partial = p.ctr + up((size_t)p.n_ctr * 4);
   p.total = p.partial + (p.splits > 1 ? up((size_t)p.splits * T * D * 4) : 0);
@@ -836,8 +904,7 @@ struct Call {
   hipStream_t stream;
 };
 
-// At most 16 token rows: two workgroups of 4 waves with private rings share a
-// CU. More: one workgroup of 8 waves with a shared ring.
+// TC: tokens a private down tile has room for, 16 or a whole chunk.
 template <class E, int FMT, int XR>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(STAGE_FEW_GATEUP, s);
@@ -849,14 +916,14 @@ static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 // SH: waves that share the rows when there are more than 16.
-template <class E, int FMT, int XR, int SHARE>
+template <class E, int FMT, int XR, int SHARE, int TC>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
   constexpr bool kOwn = XR <= 16;
   constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : SHARE;
+  constexpr int RING = kOwn ? (TC > 16 ? 57344 : 65536) : 122880;
   const dim3 grid((g.N + 16 * SH - 1) / (16 * SH), g.splits, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, kOwn ? 65536 : 122880, kOwn ? 16 : kChunk>), grid, dim3(NW * 64),
-                     0, s, g);
+  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, RING, TC>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 
@@ -864,25 +931,28 @@ static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, c
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
               c.zeros, 1, nullptr, nullptr, 0};
 }
-template <class E, int FMT, int SHARE>
-static int down_for(const Args& g, hipStream_t s) {
-  switch (token_rows(g.T, FMT != 0)) {
-    case 8: return launch_down<E, FMT, FMT ? 4 : 8, 1>(g, s);
-    case 16: return launch_down<E, FMT, 16, 1>(g, s);
-    case 32:
-      if constexpr (FMT != 0) return launch_down<E, FMT, 32, SHARE>(g, s);
-    default: return launch_down<E, FMT, 64, SHARE>(g, s);
+template <class E, int FMT, int SHARE, bool ROUTED>
+static int down_for(const Args& g, const Shape& f, hipStream_t s) {
+  constexpr int kFew = FMT ? 4 : 8;
+  if constexpr (ROUTED) {  // short lists of a long chunk
+    if (g.T > 16 && f.rows == 8) return launch_down<E, FMT, kFew, 1, kChunk>(g, s);
+    if (g.T > 16 && f.rows == 16) return launch_down<E, FMT, 16, 1, kChunk>(g, s);
   }
+  if (f.rows == 8) return launch_down<E, FMT, kFew, 1, 16>(g, s);
+  if (f.rows == 16) return launch_down<E, FMT, 16, 1, 16>(g, s);
+  if constexpr (FMT != 0) {
+    if (f.rows == 32) return launch_down<E, FMT, 32, SHARE, kChunk>(g, s);
+  }
+  return launch_down<E, FMT, 64, SHARE, kChunk>(g, s);
 }
 template <class E, int FMT>
-static int gateup_for(const Args& g, int slots, hipStream_t s) {
-  switch (token_rows(g.T, FMT != 0)) {
-    case 8: return launch_gateup<E, FMT, FMT ? 4 : 8>(g, slots, s);
-    case 16: return launch_gateup<E, FMT, 16>(g, slots, s);
-    case 32:
-      if constexpr (FMT != 0) return launch_gateup<E, FMT, 32>(g, slots, s);
-    default: return launch_gateup<E, FMT, 64>(g, slots, s);
+static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
+  if (f.rows == 8) return launch_gateup<E, FMT, FMT ? 4 : 8>(g, slots, s);
+  if (f.rows == 16) return launch_gateup<E, FMT, 16>(g, slots, s);
+  if constexpr (FMT != 0) {
+    if (f.rows == 32) return launch_gateup<E, FMT, 32>(g, slots, s);
   }
+  return launch_gateup<E, FMT, 64>(g, slots, s);
 }
 
 // y = x W^T (dense). Tiles of 64 columns with two groups of 4 waves along K where
@@ -890,12 +960,13 @@ static int gateup_for(const Args& g, int slots, hipStream_t s) {
 // counters no earlier launch would have cleared.
 template <class E, int FMT>
 int run_linear(const Call& c) {
-  return down_for<E, FMT, 4>(args_of(c, c.x, c.D, c.H, c.y), c.stream);
+  return down_for<E, FMT, 4, false>(args_of(c, c.x, c.D, c.H, c.y), shape_of(c.T, 1, 1, false, FMT != 0), c.stream);
 }
 
 template <class E, int FMT>
 int run_block(const Call& c) {
-  const BlockPlan p = block_plan(c.T, c.D, c.H, c.k, E::kBytes);
+  const Shape f = shape_of(c.T, c.k, c.E, c.ids != nullptr, FMT != 0);
+  const BlockPlan p = block_plan(f, c.T, c.D, c.H, c.k, E::kBytes);
   Args g = args_of(c, c.x, c.H, c.D, c.ws);
   g.w0 = c.wg;
   g.w1 = c.wu;
@@ -903,13 +974,13 @@ int run_block(const Call& c) {
   g.n_ctr = p.n_ctr;
   const int64_t pairs = (c.T < kChunk ? c.T : kChunk) * c.k;
   const int slots = c.ids ? (int)(pairs < c.E ? pairs : c.E) : 1;
-  const int rc = gateup_for<E, FMT>(g, slots, c.stream);
+  const int rc = gateup_for<E, FMT>(g, f, slots, c.stream);
   if (rc) return rc;
   Args d = args_of(c, c.ws, c.D, c.H, c.y);
   d.splits = p.splits;
   d.partial = (float*)(c.ws + p.partial);
   d.ctr = g.ctr;
-  return down_for<E, FMT, 8>(d, c.stream);
+  return down_for<E, FMT, 8, true>(d, f, c.stream);
 }
 
 }  // namespace few

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g)
   st.init(a, g.x + (int64_t)t0 * kb, (uint32_t)(tc * kb), 0, lane);
   st.weight(0, few::Weight{g.w, 0}, 0, e0, g.E);
 #pragma unroll
-  for (int j = 0; j < S::XD; ++j) st.x_off[j] = st.x_row(j, lane) < tc ? (uint32_t)st.x_row(j, lane) * kb : kOOB;
+  for (int j = 0; j < S::XD; ++j) st.token_row(j, st.x_row(j, lane) < tc ? (uint32_t)st.x_row(j, lane) * kb : kOOB, lane);
   const int stages = S::stages(g.D), parts = g.splits * kPartWaves, part = blockIdx.y * kPartWaves + wave;
   int s = stages * part / parts;
   const int s1 = stages * (part + 1) / parts, n = s1 - s;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(512, 2) route_tokens(const Args g) {
   const int kb = g.D * E::kBytes;
   st.init(a, g.x + (int64_t)t0 * kb, (uint32_t)(tc * kb), member, lane);
   const int xrow = st.x_row(0, lane);
-  st.x_off[0] = xrow < tc ? (uint32_t)xrow * kb : kOOB;
+  st.token_row(0, xrow < tc ? (uint32_t)xrow * kb : kOOB, lane);
   // both groups take equally many steps (they meet at barriers); one may be dead
   const int stages = S::stages(g.D), per = (stages + 1) / 2, s0 = group * per, s1 = min(stages, s0 + per);
   const int passes = (g.E + 127) / 128;

@@ -282,14 +282,17 @@ def test_moe(T, E, k, D, H, dt):
 
 
 @gpu
-@pytest.mark.parametrize("T,k,E", [(40, 3, 8), (64, 1, 4), (70, 2, 2), (16, 4, 6)])
+@pytest.mark.parametrize("T,k,E", [(40, 3, 8), (64, 1, 4), (70, 2, 2), (16, 4, 6), (30, 2, 80), (64, 2, 24), (40, 1, 30),
+                                   (64, 8, 100)])
 def test_experts_choices(T, k, E):
     """One expert taking every token, dropped ids, a token without a choice,
     one expert chosen twice by a token, zero weights."""
     banner(f"choices T={T} k={k} E={E}")
-    D, H, dt = 136, 104, torch.bfloat16
+    D, H, dt = 160, 96, torch.bfloat16
     g = gen(T)
     x, w = randn(g, (T, D), 1, dt), expert_weights(g, E, D, H, dt)
+    raw = [make_w4(g, s, 32, False, dt) for s in ((E, H, D), (E, H, D), (E, D, H))]
+    w4 = [ref_w4(*r) for r in raw]
     p = torch.rand((T, k), generator=g)
     for kind in ("one", "drop", "twice", "none"):
         ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
@@ -307,6 +310,8 @@ def test_experts_choices(T, k, E):
         y = m.moe_experts(x.cuda(), q.cuda(), ids.cuda(), *cuda(w))
         ref = ref_experts(f64(x), f64(q), ids.numpy(), *map(f64, w))
         assert_local(f64(y), ref, bound(dt, 2), (kind, T, k))
+        y4 = m.moe_experts(x.cuda(), q.cuda(), ids.cuda(), *(m.w4_pack(*cuda(r)) for r in raw))
+        assert_local(f64(y4), ref_experts(f64(x), f64(q), ids.numpy(), *w4), bound(dt, 2), (kind, "4 bits", T, k))
         empty = ((ids < 0) | (ids >= E)).all(1)
         assert not f64(y)[empty.numpy()].any()
         assert torch.equal(y, m.moe_experts(x.cuda(), q.cuda(), ids.cuda(), *cuda(w)))  # fixed order of sums
@@ -434,7 +439,9 @@ def test_infer_w4(T, D, H, group, zeros, dt):
 
 @gpu
 @pytest.mark.parametrize("T,E,k,D,H,group,zeros", [(1, 8, 2, 128, 256, 128, False), (7, 12, 4, 96, 160, 32, True),
-                                                   (40, 3, 2, 320, 64, 64, False), (64, 2, 2, 128, 128, 128, True)])
+                                                   (40, 3, 2, 320, 64, 64, False), (64, 2, 2, 128, 128, 128, True),
+                                                   (40, 64, 1, 128, 96, 32, False), (60, 20, 2, 256, 128, 64, True),
+                                                   (60, 12, 2, 128, 384, 128, False)])
 def test_moe_w4(T, E, k, D, H, group, zeros):
     banner(f"moe_w4 T={T} E={E} k={k} D={D} H={H} g={group} zeros={zeros}")
     g = gen(D * E)
