@@ -57,6 +57,7 @@ struct Args {
   int T, k, E, N, K;
   uint32_t kinv;     // ceil(65536 / k): p / k = p * kinv >> 16 for a chunk's p < 2048, k <= 32
   int zeros;         // 4 bits: the weights have zero points (else every one is 8)
+  int halves;        // gate/up: A as [T * k][2][N], the rounded value and what it left
   int splits;        // down: workgroups per output tile
   float* partial;    // down, splits > 1: [splits][T][N]
   unsigned* ctr;     // gate/up: n_ctr arrival counters to clear for the down launch;
@@ -632,10 +633,18 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
   Ring<S, SH> r;
   r.start(lds + (SH > 1 ? 0 : wave * (RING / NW)), issue);
 
-  // g and u stay in fp32; A is rounded once, to the storage type the down
-  // projection's matrix instructions take
+  // g and u stay in fp32; A is rounded to the storage type the down
+  // projection's matrix instructions take. That one rounding would add as much
+  // error to y as y's own (1.41 times the norm, measured), so where the token
+  // operand has room for a second set of rows (few_down) what it left goes into
+  // those; with more tokens it stays out.
   auto store = [&](int pair, int h, float gate, float up) {
-    ((typename E::elem*)g.out)[((int64_t)t0 * g.k + pair) * g.N + h] = E::from_f32(gate * sigmoid_f32<E>(gate) * up);
+    const float a = gate * sigmoid_f32<E>(gate) * up;
+    const typename E::elem hi = E::from_f32(a);
+    const int64_t p = (int64_t)t0 * g.k + pair;
+    typename E::elem* out = (typename E::elem*)g.out + (g.halves ? 2 * p : p) * g.N + h;
+    out[0] = hi;
+    if (g.halves) out[g.N] = E::from_f32(a - E::to_f32(hi));
   };
   use.expert(nth, lane);
   while (true) {
@@ -698,9 +707,14 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
 // and added to the wave's own [token][column] tile in LDS. TC: tokens that tile
 // has room for. Groups of a shared ring meet at barriers, so they take equally
 // many steps; more than one of them only for a dense product.
-template <class E, int FMT, int NT, int XR, int NW, int SH, int RING, int TC>
+// HALVES: A comes as two values (see few_gateup), in rows 0 .. XR - 1 and
+// XR .. 2 XR - 1 of the token operand, which repeats nothing then: no more
+// matrix instructions than with one.
+template <class E, int FMT, int NT, int XR, int NW, int SH, int RING, int TC, bool HALVES>
 __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
-  using S = typename StreamOf<E, FMT, NT, XR, SH, RING / (NW / SH)>::type;
+  using S = typename StreamOf<E, FMT, NT, (HALVES ? 2 * XR : XR), SH, RING / (NW / SH)>::type;
+  static_assert(!HALVES || 2 * XR <= 16, "one block of token rows");
+  constexpr int PARTS = HALVES ? 2 : 1;
   constexpr int MT = S::MT, C = 16 * NT, KG = NW / SH;  // KG: groups
   __shared__ __attribute__((aligned(1024))) char lds[RING];
   __shared__ __attribute__((aligned(16))) float ysum[NW][TC * C];
@@ -724,13 +738,14 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
   if (KG > 1 && SH > 1 ? use.hits > 0 : at < end) {
     Walk get = use;
     S st;
-    st.init(g, g.x + (int64_t)t0 * g.k * g.K * E::kBytes, (uint32_t)(tc * g.k * g.K) * E::kBytes, wave % SH, lane);
+    const uint32_t row_bytes = PARTS * (uint32_t)g.K * E::kBytes;  // of a pair
+    st.init(g, g.x + (int64_t)t0 * g.k * row_bytes, (uint32_t)(tc * g.k) * row_bytes, wave % SH, lane);
     auto set_rows = [&] {
       const int n = get.rows(XR);
 #pragma unroll
       for (int j = 0; j < S::XD; ++j) {
-        const int i = st.x_row(j, lane), pair = get.pair(i);
-        st.token_row(j, i < n ? (uint32_t)pair * (uint32_t)(g.K * E::kBytes) : kOOB, lane);
+        const int i = st.x_row(j, lane) % XR, half = st.x_row(j, lane) / XR, pair = get.pair(i);
+        st.token_row(j, i < n ? (uint32_t)pair * row_bytes + (uint32_t)(half * g.K) * E::kBytes : kOOB, lane);
       }
     };
     // the run's stages of the n-th expert
@@ -778,8 +793,8 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
           for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int i = 16 * m + 4 * q + j;
-              if (i < rows) {
+              const int row = 16 * m + 4 * q + j, i = HALVES ? row % XR : row;
+              if (i < rows && row < PARTS * XR) {
                 const int pair = __builtin_amdgcn_readlane(mine, i);
                 const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wt), i));
                 if ((lane >> 4) == q) {
@@ -879,13 +894,15 @@ static inline int down_splits(const Shape& f, int64_t T, int64_t D) {
 struct BlockPlan {
   size_t ctr, partial, total;
   int splits, n_ctr;
+  bool halves;
 };
 static inline BlockPlan block_plan(const Shape& f, int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   BlockPlan p;
   p.splits = down_splits(f, T, D);
   p.n_ctr = p.splits > 1 ? (int)((D + down_cols(f) - 1) / down_cols(f) * ((T + kChunk - 1) / kChunk)) : 0;
-  p.ctr = up((size_t)T * k * H * e);
+  p.halves = f.rows == 8 && e == 2;
+  p.ctr = up((size_t)T * k * H * e * (p.halves ? 2 : 1));
   p.partial = p.ctr + up((size_t)p.n_ctr * 4);
   p.total = p.partial + (p.splits > 1 ? up((size_t)p.splits * T * D * 4) : 0);
   return p;
@@ -916,34 +933,36 @@ static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 // SH: waves that share the rows when there are more than 16.
-template <class E, int FMT, int XR, int SHARE, int TC>
+template <class E, int FMT, int XR, int SHARE, int TC, bool HALVES>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
   constexpr bool kOwn = XR <= 16;
   constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : SHARE;
   constexpr int RING = kOwn ? (TC > 16 ? 57344 : 65536) : 122880;
   const dim3 grid((g.N + 16 * SH - 1) / (16 * SH), g.splits, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, RING, TC>), grid, dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, RING, TC, HALVES>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 
 static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, char* out) {
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
-              c.zeros, 1, nullptr, nullptr, 0};
+              c.zeros, 0, 1, nullptr, nullptr, 0};
 }
-template <class E, int FMT, int SHARE, bool ROUTED>
+// BLOCK: the down projection of a block, else a dense product.
+template <class E, int FMT, int SHARE, bool BLOCK>
 static int down_for(const Args& g, const Shape& f, hipStream_t s) {
   constexpr int kFew = FMT ? 4 : 8;
-  if constexpr (ROUTED) {  // short lists of a long chunk
-    if (g.T > 16 && f.rows == 8) return launch_down<E, FMT, kFew, 1, kChunk>(g, s);
-    if (g.T > 16 && f.rows == 16) return launch_down<E, FMT, 16, 1, kChunk>(g, s);
+  constexpr bool kHalves = BLOCK && E::kBytes == 2;
+  if constexpr (BLOCK) {  // short lists of a long chunk
+    if (g.T > 16 && f.rows == 8) return launch_down<E, FMT, kFew, 1, kChunk, kHalves>(g, s);
+    if (g.T > 16 && f.rows == 16) return launch_down<E, FMT, 16, 1, kChunk, false>(g, s);
   }
-  if (f.rows == 8) return launch_down<E, FMT, kFew, 1, 16>(g, s);
-  if (f.rows == 16) return launch_down<E, FMT, 16, 1, 16>(g, s);
+  if (f.rows == 8) return launch_down<E, FMT, kFew, 1, 16, kHalves>(g, s);
+  if (f.rows == 16) return launch_down<E, FMT, 16, 1, 16, false>(g, s);
   if constexpr (FMT != 0) {
-    if (f.rows == 32) return launch_down<E, FMT, 32, SHARE, kChunk>(g, s);
+    if (f.rows == 32) return launch_down<E, FMT, 32, SHARE, kChunk, false>(g, s);
   }
-  return launch_down<E, FMT, 64, SHARE, kChunk>(g, s);
+  return launch_down<E, FMT, 64, SHARE, kChunk, false>(g, s);
 }
 template <class E, int FMT>
 static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
@@ -970,6 +989,7 @@ int run_block(const Call& c) {
   Args g = args_of(c, c.x, c.H, c.D, c.ws);
   g.w0 = c.wg;
   g.w1 = c.wu;
+  g.halves = p.halves;
   g.ctr = (unsigned*)(c.ws + p.ctr);
   g.n_ctr = p.n_ctr;
   const int64_t pairs = (c.T < kChunk ? c.T : kChunk) * c.k;

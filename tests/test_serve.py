@@ -1,8 +1,8 @@
 """The few-token serving operators: router, mixture of experts, 4-bit weights.
 
 References are plain fp64 on the CPU from the operators' definitions. Bounds,
-fixed before the first run: a 16-bit result carries two roundings of half a step
-each (A between the two products, the result), so its normalized L2 error over
+fixed before the first run: a 16-bit result carries at most two roundings of half
+a step each (A between the two products, the result), so its normalized L2 error over
 the tensor, each row, each 32 x 32 block and each tile is at most eps =
 2 * (eps / 2) of the type; one product alone (w4_linear) has one. fp32 sums add
 less than 1e-5 of the operands' scale, the framework's bound in that mode.
