@@ -852,9 +852,19 @@ __global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
   for (int i = threadIdx.x; i < tc * Q; i += NW * 64) {
     const int row = i / Q, n = wg0 + i % Q * 4;
     if (n >= g.N) continue;
+    // eight at a time in flight; those past the splits read as zeros
+    const __amdgpu_buffer_rsrc_t part =
+        make_rsrc(g.partial + (int64_t)t0 * g.N, ((int64_t)(g.splits - 1) * g.T + tc) * g.N * 4);
     f32x4_t v{};
-    for (int sp = 0; sp < g.splits; ++sp)
-      v += load_partial(g.partial + ((int64_t)sp * g.T + t0) * g.N, tc, g.N, row, n);
+    for (int s0 = 0; s0 < g.splits; s0 += 8) {
+      u32x4_t b[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        b[s] = __builtin_amdgcn_raw_buffer_load_b128(
+            part, s0 + s < g.splits ? (uint32_t)(((s0 + s) * g.T + row) * g.N + n) * 4u : kOOB, 0, kCoherentPolicy);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) v += __builtin_bit_cast(f32x4_t, b[s]);
+    }
     typename E::vec4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);

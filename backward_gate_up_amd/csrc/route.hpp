@@ -238,7 +238,7 @@ __device__ __forceinline__ float gamma_of(int stages, int parts) {
 }
 
 // Few tokens, first launch: 16 experts (grid x), a part of K (y), XR tokens (z).
-constexpr int kPartWaves = 4;
+constexpr int kPartWaves = 4, kMaxSplits = 4;
 template <class E, int XR>
 __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g) {
   using S = few::RowStream<E, 1, XR, 1, 16384>;
@@ -300,20 +300,36 @@ __global__ void __launch_bounds__(256) route_pick(const Args g) {
   if (t >= g.T) return;
   const float* pw = g.part + (int64_t)g.splits * g.T * g.E;
   const float* px = pw + g.splits * g.E;
+  // all parts in flight at once; those past the splits and the experts read as zeros
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(g.part, (int64_t)g.splits * g.T * g.E * 4);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(pw, g.splits * g.E * 4);
   float l[NPL], wmax = 0.f, x2 = 0.f;
+  float v[NPL][kMaxSplits], w[NPL][kMaxSplits], xp[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = i * 64 + lane;
+      const bool in = e < g.E && s < g.splits;
+      const uint32_t at = (uint32_t)((int64_t)s * g.T + t) * (uint32_t)g.E + e;
+      v[i][s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rp, in ? at * 4u : kOOB, 0, 0));
+      w[i][s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rw, in ? (uint32_t)(s * g.E + e) * 4u : kOOB, 0, 0));
+    }
+    xp[s] = s < g.splits ? px[(int64_t)s * g.T + t] : 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) x2 += xp[s];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const int e = i * 64 + lane;
-    float v = 0.f, w = 0.f;
-    if (e < g.E)
-      for (int s = 0; s < g.splits; ++s) {
-        v += g.part[((int64_t)s * g.T + t) * g.E + e];
-        w += pw[s * g.E + e];
-      }
-    l[i] = v;
-    wmax = fmaxf(wmax, w);
+    float sum = 0.f, sw = 0.f;
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s) {
+      sum += v[i][s];
+      sw += w[i][s];
+    }
+    l[i] = sum;
+    wmax = fmaxf(wmax, sw);
   }
-  for (int s = 0; s < g.splits; ++s) x2 += px[(int64_t)s * g.T + t];
   // not negative, so the bits order as the values do
   wmax = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, wmax)));
   const int parts = g.splits * kPartWaves, stages = (g.D * E::kBytes + 127) >> 7;
@@ -413,7 +429,7 @@ static inline int route_splits(int64_t T, int64_t D, int64_t E, size_t e) {
   const int64_t tiles = (E + 15) / 16 * ((T + 15) / 16), stages = ((int64_t)D * e + 127) / 128;
   int64_t s = 128 / tiles;
   if (s > stages / kPartWaves) s = stages / kPartWaves;
-  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+  return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }
 static inline bool route_many(int64_t T, int64_t E) { return T > 1024 && E <= 256; }
 static inline size_t route_bytes(int64_t T, int64_t D, int64_t E, size_t e) {
