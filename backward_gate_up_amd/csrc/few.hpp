@@ -416,12 +416,19 @@ struct Ring {
 };
 
 // ---- a chunk's choices --------------------------------------------------------
-// ids of the chunk's pairs, and the experts that occur, in ascending order.
+// ids of the chunk's pairs, and which experts occur.
 struct Choices {
-  int16_t id[kMaxPairs];          // -1: chooses nothing
-  int16_t expert[kMaxExperts];    // n-th expert that occurs
-  unsigned seen[kMaxExperts / 32];
-  int hits;
+  int16_t id[kMaxPairs];              // -1: chooses nothing
+  unsigned seen[kMaxExperts / 32];    // bit per expert
+  int upto[kMaxExperts / 32];         // experts that occur up to and with this word
+  // the n-th expert that occurs (n < upto's last)
+  __device__ __forceinline__ int expert(int n, int lane) const {
+    const int u = lane < kMaxExperts / 32 ? upto[lane] : 0x7fffffff;
+    const int word = __ffsll((unsigned long long)__ballot(u > n)) - 1;
+    unsigned v = __builtin_amdgcn_readfirstlane(seen[word]);
+    for (int before = __builtin_amdgcn_readlane(u, word) - __popc(v); before < n; ++before) v &= v - 1;
+    return word * 32 + __ffs((int)v) - 1;
+  }
 };
 
 // All threads; ends with a barrier.
@@ -438,20 +445,13 @@ __device__ __forceinline__ void read_choices(Choices& c, const Args& g, int t0, 
   __syncthreads();
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
-    const int words = (g.E + 31) >> 5;
-    unsigned v = lane < words ? c.seen[lane] : 0u;
-    int before = __popc(v);
+    int n = lane < kMaxExperts / 32 ? __popc(c.seen[lane]) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up(before, d);
-      if (lane >= d) before += o;
+      const int o = __shfl_up(n, d);
+      if (lane >= d) n += o;
     }
-    if (lane == 31) c.hits = before;
-    before -= __popc(v);
-    while (v) {
-      c.expert[before++] = (int16_t)(lane * 32 + __ffs((int)v) - 1);
-      v &= v - 1;
-    }
+    if (lane < kMaxExperts / 32) c.upto[lane] = n;
   }
   __syncthreads();
 }
@@ -519,7 +519,7 @@ struct Walk {
         l &= ~__ballot(id == __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)l) - 1));
     } else {
       read_choices(c, a, t0, tc);
-      hits = __builtin_amdgcn_readfirstlane(c.hits);
+      hits = __builtin_amdgcn_readfirstlane(c.upto[kMaxExperts / 32 - 1]);
     }
   }
   // The n-th expert (n >= i), first pass.
@@ -537,7 +537,7 @@ struct Walk {
       p = mask_pairs(__ballot(id == e), lane);
       total = p.n;
     } else {
-      e = __builtin_amdgcn_readfirstlane(ch->expert[n]);
+      e = ch->expert(n, lane);
       p = list_pairs(*ch, P, e, 0, list, lane, total);
     }
     i = n;
@@ -561,7 +561,7 @@ struct Walk {
 // from item to item: while one is finished, the loads of the next are in flight.
 // RING: bytes of LDS for the workgroup's rings.
 template <class E, int FMT, int HB, int XR, int NW, int SH, int RING>
-__global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
+__global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 : 2)) few_gateup(const Args g) {
   constexpr int NT = 2 * HB, COLS = 16 * HB * SH;
   using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
   constexpr int MT = S::MT;
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(NW * 64, 2) few_gateup(const Args g) {
 // XR .. 2 XR - 1 of the token operand, which repeats nothing then: no more
 // matrix instructions than with one.
 template <class E, int FMT, int NT, int XR, int NW, int SH, int RING, int TC, bool HALVES>
-__global__ void __launch_bounds__(NW * 64, 2) few_down(const Args g) {
+__global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 : 2)) few_down(const Args g) {
   using S = typename StreamOf<E, FMT, NT, (HALVES ? 2 * XR : XR), SH, RING / (NW / SH)>::type;
   static_assert(!HALVES || 2 * XR <= 16, "one block of token rows");
   constexpr int PARTS = HALVES ? 2 : 1;
@@ -931,15 +931,20 @@ struct Call {
   hipStream_t stream;
 };
 
+// Workgroups with private rings that share a CU.
+template <int FMT, int XR>
+constexpr int groups_per_cu() { return FMT != 0 && XR < 16 ? 3 : 2; }
+
 // TC: tokens a private down tile has room for, 16 or a whole chunk.
 template <class E, int FMT, int XR>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(STAGE_FEW_GATEUP, s);
   constexpr bool kOwn = XR <= 16;
   constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : 8;
-  const int64_t items = (int64_t)slots * ((g.N + 16 * SH - 1) / (16 * SH)), fit = (kOwn ? 2 : 1) * dev_ncu();
+  constexpr int PER = kOwn ? groups_per_cu<FMT, XR>() : 1, RING = !kOwn ? 147456 : PER == 2 ? 65536 : 32768;
+  const int64_t items = (int64_t)slots * ((g.N + 16 * SH - 1) / (16 * SH)), fit = PER * dev_ncu();
   const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_gateup<E, FMT, 1, XR, NW, SH, kOwn ? 65536 : 147456>), grid, dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_gateup<E, FMT, 1, XR, NW, SH, RING>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 // SH: waves that share the rows when there are more than 16.
@@ -948,7 +953,8 @@ static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
   constexpr bool kOwn = XR <= 16;
   constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : SHARE;
-  constexpr int RING = kOwn ? (TC > 16 ? 57344 : 65536) : 122880;
+  constexpr int PER = groups_per_cu<FMT, XR>();
+  constexpr int RING = !kOwn ? 122880 : PER > 2 ? (TC > 16 ? 32768 : 40960) : TC > 16 ? 57344 : 65536;
   const dim3 grid((g.N + 16 * SH - 1) / (16 * SH), g.splits, (g.T + kChunk - 1) / kChunk);
   hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, RING, TC, HALVES>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
