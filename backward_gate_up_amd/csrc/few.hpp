@@ -89,11 +89,11 @@ __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// A descriptor that is the same on every lane, in scalar registers (one that
-// changes inside a loop the compiler may keep in vector registers, which the
-// loads from inline assembly cannot take). A vector instruction's write of a
-// scalar register needs 5 wait states before a memory instruction reads it,
-// and the compiler does not know that the assembly is one: they are put here.
+// A descriptor that is the same on every lane, in scalar registers, as the loads
+// from inline assembly take it. A vector instruction's write of a scalar
+// register needs 5 wait states before a memory instruction reads it, and the
+// compiler does not know that the assembly is one: they are put here.
+// (tests/test_serve_isa.py looks for such pairs in the compiled kernels.)
 __device__ __forceinline__ i32x4_t scalar_rsrc(i32x4_t r) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
@@ -154,7 +154,7 @@ struct RowStream {
     share = SH > 1 ? wave : 0;
     w_at = XR * 128 + share * NT * 2048;
     kb = g.K * E::kBytes;
-    rx = rsrc_words(xb, x_bytes);
+    rx = scalar_rsrc(rsrc_words(xb, x_bytes));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = 8 * j + (lane >> 3);
@@ -170,41 +170,31 @@ struct RowStream {
   // block n: rows row0 .. row0 + 15 of expert e's weight; rows past N read as zeros
   __device__ __forceinline__ void weight(int n, const Weight& wt, int e, int row0, int N) {
     const int rows = max(0, min(16, N - row0));
-    rw[n] = rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)row0 * kb, (int64_t)rows * kb);
+    rw[n] = scalar_rsrc(rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)row0 * kb, (int64_t)rows * kb));
   }
   // Loads stage s into the slot; not live: zeros. K advances through the scalar
-  // offset, which the range check leaves out; a dead stage has buffers of no
-  // bytes, so that the lanes' offsets never change, except that those past K
-  // in a partial last stage go out of range.
+  // offset, which the range check leaves out, so the lanes' offsets change only
+  // in a partial last stage, where those past K go out of range.
   __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
-    const uint32_t at = live ? (uint32_t)s * 128u : 0u;
-    const int left = kb - (int)at;
-    i32x4_t w[NT], xr = rx;
-    xr[2] = live ? xr[2] : 0;
-    xr = scalar_rsrc(xr);
+    const uint32_t at = (uint32_t)s * 128u;
+    if (live && kb - (int)at >= 128) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      w[n] = rw[n];
-      w[n][2] = live ? w[n][2] : 0;
-      w[n] = scalar_rsrc(w[n]);
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, rw[n], w_off[j], at);
+#pragma unroll
+      for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, rx, x_off[j], at);
+      return;
     }
-    uint32_t wo[2], xo[XD];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) wo[j] = w_off[j];
-#pragma unroll
-    for (int j = 0; j < XD; ++j) xo[j] = x_off[j];
-    if (left < 128) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) wo[j] = (int)chunk(8 * j + (lane >> 3), lane) < left ? wo[j] : kOOB;
-#pragma unroll
-      for (int j = 0; j < XD; ++j) xo[j] = (int)chunk(x_row(j, lane), lane) < left ? xo[j] : kOOB;
-    }
+    const int left = live ? kb - (int)at : 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, w[n], wo[j], at);
+      for (int n = 0; n < NT; ++n)
+        dma16(slot + w_at + n * 2048 + j * 1024, rw[n], (int)chunk(8 * j + (lane >> 3), lane) < left ? w_off[j] : kOOB, at);
 #pragma unroll
-    for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, xr, xo[j], at);
+    for (int j = 0; j < XD; ++j)
+      dma16(slot + (share * XD + j) * 1024, rx, (int)chunk(x_row(j, lane), lane) < left ? x_off[j] : kOOB, at);
   }
   struct Nothing {
     __device__ __forceinline__ void token(int, u32x4_t) {}
@@ -259,52 +249,50 @@ struct W4Stream {
   static_assert(NS >= 2 && XD >= 1 && (NS - 1) * D <= 63, "ring");
   static constexpr float kOff = std::is_same<E, Bf16>::value ? 128.0f : 64.0f;
   i32x4_t rw[NT], rx;
-  uint32_t x_off[XD];
+  uint32_t x_off[XD], scale_off;
   int kb, rec, zeros, share, w_at;
 
   static __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
   __device__ __forceinline__ int x_row(int j, int lane) const { return 4 * (share * XD + j) + (lane >> 4); }
 
-  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int wave, int) {
+  __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int wave, int lane) {
     share = SH > 1 ? wave : 0;
     w_at = XR * 256 + share * NT * WS;
     kb = g.K * 2;
     zeros = g.zeros;
     rec = 1024 + 32 * GP + (zeros ? 32 : 0);
-    rx = rsrc_words(xb, x_bytes);
+    scale_off = 1024 + lane * 4 < rec ? 1024 + lane * 4 : kOOB;
+    rx = scalar_rsrc(rsrc_words(xb, x_bytes));
   }
   __device__ __forceinline__ void weight(int n, const Weight& wt, int e, int row0, int N) {
     const int len = row0 < N ? stages(kb >> 1) * rec : 0;
-    rw[n] = rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)(row0 >> 4) * len, len);
+    rw[n] = scalar_rsrc(rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)(row0 >> 4) * len, len));
   }
   static __device__ __forceinline__ uint32_t chunk(int r, int lane) { return ((lane & 15) ^ (r & 15)) << 4; }
   __device__ __forceinline__ void token_row(int j, uint32_t row, int lane) {
     x_off[j] = row == kOOB ? kOOB : row + chunk(x_row(j, lane), lane);
   }
   __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
-    const uint32_t at = live ? (uint32_t)s * (uint32_t)rec : 0u, atx = live ? (uint32_t)s * 256u : 0u;
-    const int left = kb - (int)atx;
-    i32x4_t xr = rx;
-    xr[2] = live ? xr[2] : 0;
-    xr = scalar_rsrc(xr);
-    const uint32_t scales = 1024 + lane * 4 < rec ? 1024 + lane * 4 : kOOB;
+    const uint32_t at = (uint32_t)s * (uint32_t)rec, atx = (uint32_t)s * 256u;
+    if (live && kb - (int)atx >= 256) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        dma16(slot + w_at + n * WS, rw[n], lane * 16, at);
+        dma4(slot + w_at + n * WS + 1024, rw[n], scale_off, at);
+      }
+#pragma unroll
+      for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, rx, x_off[j], atx);
+      return;
+    }
+    const int left = live ? kb - (int)atx : 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      i32x4_t w = rw[n];
-      w[2] = live ? w[2] : 0;
-      w = scalar_rsrc(w);
-      dma16(slot + w_at + n * WS, w, lane * 16, at);
-      dma4(slot + w_at + n * WS + 1024, w, scales, at);
-    }
-    uint32_t xo[XD];
-#pragma unroll
-    for (int j = 0; j < XD; ++j) xo[j] = x_off[j];
-    if (left < 256) {
-#pragma unroll
-      for (int j = 0; j < XD; ++j) xo[j] = (int)chunk(x_row(j, lane), lane) < left ? xo[j] : kOOB;
+      dma16(slot + w_at + n * WS, rw[n], live ? lane * 16 : kOOB, at);
+      dma4(slot + w_at + n * WS + 1024, rw[n], live ? scale_off : kOOB, at);
     }
 #pragma unroll
-    for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, xr, xo[j], atx);
+    for (int j = 0; j < XD; ++j)
+      dma16(slot + (share * XD + j) * 1024, rx, (int)chunk(x_row(j, lane), lane) < left ? x_off[j] : kOOB, atx);
   }
   // (v & m) | o in one instruction: its operands have to be registers, and the
   // compiler, which knows the constants, would take two with literals
