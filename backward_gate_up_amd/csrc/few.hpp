@@ -547,10 +547,11 @@ struct Walk {
 // items. SH = 1: 16 HB columns, the waves take equal parts of K and their sums
 // meet in LDS; SH = NW: 16 HB columns per wave, all of K. The rings run on
 // from item to item: while one is finished, the loads of the next are in flight.
-// RING: bytes of LDS for the workgroup's rings.
-template <class E, int FMT, int HB, int XR, int NW, int SH, int RING>
+// RING: bytes of LDS for the workgroup's rings. PLAIN: y = x W^T instead, one
+// weight block per 16 columns and no SwiGLU (dense, w0 and out = y).
+template <class E, int FMT, int HB, int XR, int NW, int SH, int RING, bool PLAIN>
 __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 : 2)) few_gateup(const Args g) {
-  constexpr int NT = 2 * HB, COLS = 16 * HB * SH;
+  constexpr int NT = PLAIN ? HB : 2 * HB, COLS = 16 * HB * SH;
   using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
   constexpr int MT = S::MT;
   __shared__ __attribute__((aligned(1024))) char lds[RING];
@@ -591,8 +592,12 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
     const int row0 = get_tile * COLS + wcol;
 #pragma unroll
     for (int b = 0; b < HB; ++b) {
-      st.weight(2 * b, g.w0, get.e, row0 + 16 * b, g.N);
-      st.weight(2 * b + 1, g.w1, get.e, row0 + 16 * b, g.N);
+      if constexpr (PLAIN) {
+        st.weight(b, g.w0, get.e, row0 + 16 * b, g.N);
+      } else {
+        st.weight(2 * b, g.w0, get.e, row0 + 16 * b, g.N);
+        st.weight(2 * b + 1, g.w1, get.e, row0 + 16 * b, g.N);
+      }
     }
   };
   auto issue = [&](uint32_t slot) {
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
   // operand has room for a second set of rows (few_down) what it left goes into
   // those; with more tokens it stays out.
   auto store = [&](int pair, int h, float gate, float up) {
-    const float a = gate * sigmoid_f32<E>(gate) * up;
+    const float a = PLAIN ? gate : gate * sigmoid_f32<E>(gate) * up;
     const typename E::elem hi = E::from_f32(a);
     const int64_t p = (int64_t)t0 * g.k + pair;
     typename E::elem* out = (typename E::elem*)g.out + (g.halves ? 2 * p : p) * g.N + h;
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 #pragma unroll
           for (int b = 0; b < HB; ++b) {
             const int h = row0 + 16 * b + (lane & 15);
-            if (i < n && h < g.N) store(pair, h, acc[2 * b][m][j], acc[2 * b + 1][m][j]);
+            if (i < n && h < g.N) store(pair, h, acc[PLAIN ? b : 2 * b][m][j], acc[PLAIN ? b : 2 * b + 1][m][j]);
           }
         }
     } else {
@@ -867,8 +872,9 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 // over its weights. Above 16 rows waves have to share them, and 8 waves cannot
 // share the loads of 32 rows of 128 bytes.
 struct Shape {
-  int rows;   // token rows
-  bool own;   // private rings: two workgroups of 4 waves per CU; else one of 8 waves
+  int rows;  // token rows
+  bool own;  // private rings, several workgroups of 4 waves per CU; else one of 8 waves
+  int per;   // workgroups per CU
 };
 static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool w4) {
   const int64_t few = w4 ? 4 : 8, load = routed ? T * k : 0;  // load <= m E: m pairs per expert on average
@@ -876,7 +882,7 @@ static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool 
   if (T <= few || (routed && 4 * load <= few * E)) rows = 8;
   else if (T <= 16 || (routed && load <= 6 * E)) rows = 16;
   else if (w4 && (T <= 32 || (routed && load <= 12 * E))) rows = 32;
-  return {rows, rows <= 16};
+  return {rows, rows <= 16, rows > 16 ? 1 : w4 && rows == 8 ? 3 : 2};
 }
 
 // Columns of a down tile, and workgroups per tile: about as many over all tiles
@@ -884,7 +890,7 @@ static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool 
 static inline int down_cols(const Shape& f) { return f.own ? 16 : 128; }
 static inline int down_splits(const Shape& f, int64_t T, int64_t D) {
   const int64_t tiles = (D + down_cols(f) - 1) / down_cols(f) * ((T + kChunk - 1) / kChunk);
-  const int64_t s = ((f.own ? 512 : 256) + tiles - 1) / tiles, most = f.own ? 8 : 32;
+  const int64_t s = (256 * f.per + tiles - 1) / tiles, most = f.own ? 8 : 32;
   return (int)(s > most ? most : s);
 }
 // Workspace of a block: the A plane, then where the down projection is split
@@ -924,15 +930,15 @@ template <int FMT, int XR>
 constexpr int groups_per_cu() { return FMT != 0 && XR < 16 ? 3 : 2; }
 
 // TC: tokens a private down tile has room for, 16 or a whole chunk.
-template <class E, int FMT, int XR>
+template <class E, int FMT, int HB, int XR, bool PLAIN>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
-  StageScope scope(STAGE_FEW_GATEUP, s);
+  StageScope scope(PLAIN ? STAGE_FEW_DOWN : STAGE_FEW_GATEUP, s);
   constexpr bool kOwn = XR <= 16;
   constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : 8;
   constexpr int PER = kOwn ? groups_per_cu<FMT, XR>() : 1, RING = !kOwn ? 147456 : PER == 2 ? 65536 : 32768;
-  const int64_t items = (int64_t)slots * ((g.N + 16 * SH - 1) / (16 * SH)), fit = PER * dev_ncu();
+  const int64_t items = (int64_t)slots * ((g.N + 16 * HB * SH - 1) / (16 * HB * SH)), fit = PER * dev_ncu();
   const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
-  hipLaunchKernelGGL((few_gateup<E, FMT, 1, XR, NW, SH, RING>), grid, dim3(NW * 64), 0, s, g);
+  hipLaunchKernelGGL((few_gateup<E, FMT, HB, XR, NW, SH, RING, PLAIN>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 // SH: waves that share the rows when there are more than 16.
@@ -952,38 +958,48 @@ static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, c
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
               c.zeros, 0, 1, nullptr, nullptr, 0};
 }
-// BLOCK: the down projection of a block, else a dense product.
-template <class E, int FMT, int SHARE, bool BLOCK>
+template <class E, int FMT>
 static int down_for(const Args& g, const Shape& f, hipStream_t s) {
   constexpr int kFew = FMT ? 4 : 8;
-  constexpr bool kHalves = BLOCK && E::kBytes == 2;
-  if constexpr (BLOCK) {  // short lists of a long chunk
-    if (g.T > 16 && f.rows == 8) return launch_down<E, FMT, kFew, 1, kChunk, kHalves>(g, s);
-    if (g.T > 16 && f.rows == 16) return launch_down<E, FMT, 16, 1, kChunk, false>(g, s);
-  }
-  if (f.rows == 8) return launch_down<E, FMT, kFew, 1, 16, kHalves>(g, s);
-  if (f.rows == 16) return launch_down<E, FMT, 16, 1, 16, false>(g, s);
+  constexpr bool kHalves = E::kBytes == 2;
+  if (f.rows == 8)
+    return g.T > 16 ? launch_down<E, FMT, kFew, 1, kChunk, kHalves>(g, s) : launch_down<E, FMT, kFew, 1, 16, kHalves>(g, s);
+  if (f.rows == 16)
+    return g.T > 16 ? launch_down<E, FMT, 16, 1, kChunk, false>(g, s) : launch_down<E, FMT, 16, 1, 16, false>(g, s);
   if constexpr (FMT != 0) {
-    if (f.rows == 32) return launch_down<E, FMT, 32, SHARE, kChunk, false>(g, s);
+    if (f.rows == 32) return launch_down<E, FMT, 32, 8, kChunk, false>(g, s);
   }
-  return launch_down<E, FMT, 64, SHARE, kChunk, false>(g, s);
+  return launch_down<E, FMT, 64, 8, kChunk, false>(g, s);
 }
 template <class E, int FMT>
 static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
-  if (f.rows == 8) return launch_gateup<E, FMT, FMT ? 4 : 8>(g, slots, s);
-  if (f.rows == 16) return launch_gateup<E, FMT, 16>(g, slots, s);
+  if (f.rows == 8) return launch_gateup<E, FMT, 1, FMT ? 4 : 8, false>(g, slots, s);
+  if (f.rows == 16) return launch_gateup<E, FMT, 1, 16, false>(g, slots, s);
   if constexpr (FMT != 0) {
-    if (f.rows == 32) return launch_gateup<E, FMT, 32>(g, slots, s);
+    if (f.rows == 32) return launch_gateup<E, FMT, 1, 32, false>(g, slots, s);
   }
-  return launch_gateup<E, FMT, 64>(g, slots, s);
+  return launch_gateup<E, FMT, 1, 64, false>(g, slots, s);
 }
 
-// y = x W^T (dense). Tiles of 64 columns with two groups of 4 waves along K where
-// the rows are shared: its K cannot be split over workgroups, whose arrival
-// counters no earlier launch would have cleared.
+// y = x W^T (dense). At most 16 rows: items of 16 columns, or 32 where those
+// still give every workgroup one. More: tiles of 64 columns with two groups of
+// 4 waves along K (its K cannot be split over workgroups, whose arrival counters
+// no earlier launch would have cleared).
 template <class E, int FMT>
 int run_linear(const Call& c) {
-  return down_for<E, FMT, 4, false>(args_of(c, c.x, c.D, c.H, c.y), shape_of(c.T, 1, 1, false, FMT != 0), c.stream);
+  const Args g = args_of(c, c.x, c.D, c.H, c.y);
+  const Shape f = shape_of(c.T, 1, 1, false, true);
+  const bool wide = (c.D + 31) / 32 >= 3 * dev_ncu();
+  if (f.rows == 8) {
+    if (wide) return launch_gateup<E, FMT, 2, 4, true>(g, 1, c.stream);
+    return launch_gateup<E, FMT, 1, 4, true>(g, 1, c.stream);
+  }
+  if (f.rows == 16) {
+    if (wide) return launch_gateup<E, FMT, 2, 16, true>(g, 1, c.stream);
+    return launch_gateup<E, FMT, 1, 16, true>(g, 1, c.stream);
+  }
+  if (f.rows == 32) return launch_down<E, FMT, 32, 4, kChunk, false>(g, c.stream);
+  return launch_down<E, FMT, 64, 4, kChunk, false>(g, c.stream);
 }
 
 template <class E, int FMT>
@@ -1004,7 +1020,7 @@ int run_block(const Call& c) {
   d.splits = p.splits;
   d.partial = (float*)(c.ws + p.partial);
   d.ctr = g.ctr;
-  return down_for<E, FMT, 8, true>(d, f, c.stream);
+  return down_for<E, FMT>(d, f, c.stream);
 }
 
 }  // namespace few
