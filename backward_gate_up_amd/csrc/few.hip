@@ -151,7 +151,7 @@ static int moe_call(const void* X, const void* Wr, const float* weights, const i
   if (routed) {
     float* rw = (float*)((char*)ws + m.wts);
     int* ri = (int*)((char*)ws + m.ids);
-    const route::Args r{(const char*)X, (const char*)Wr, rw, ri, (int)T, (int)c.D, c.E, (int)k, renorm != 0, (float*)ws, 1};
+    const route::Args r{(const char*)X, (const char*)Wr, rw, ri, (int)T, (int)c.D, c.E, (int)k, renorm != 0, (float*)ws, 1, 0};
     if ((rc = run_route_for(dtype, r, stream))) return rc;
     c.wts = rw;
     c.ids = ri;
@@ -239,7 +239,7 @@ int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t*
   if ((rc = check_alias(out, 3, in, 2))) return rc;
   if ((rc = check_device())) return rc;
   const route::Args r{(const char*)X, (const char*)Wr, weights, (int*)ids, (int)T, (int)D, (int)E, (int)k, renorm != 0,
-                      (float*)workspace, 1};
+                      (float*)workspace, 1, 0};
   return run_route_for(dtype, r, stream);
 }
 

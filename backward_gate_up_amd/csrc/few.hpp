@@ -145,7 +145,7 @@ struct RowStream {
   uint32_t w_off[2], x_off[XD];
   int kb, share, w_at;  // share: the wave's part of the token rows; w_at: its weights in a slot
 
-  static __device__ __forceinline__ int stages(int K) { return (K * E::kBytes + 127) >> 7; }
+  static __host__ __device__ __forceinline__ int stages(int K) { return (K * E::kBytes + 127) >> 7; }
   // the token row (0 .. XR - 1) whose chunk this lane fetches in load j
   __device__ __forceinline__ int x_row(int j, int lane) const { return 8 * (share * XD + j) + (lane >> 3); }
 
@@ -252,7 +252,7 @@ struct W4Stream {
   uint32_t x_off[XD], scale_off;
   int kb, rec, zeros, share, w_at;
 
-  static __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
+  static __host__ __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
   __device__ __forceinline__ int x_row(int j, int lane) const { return 4 * (share * XD + j) + (lane >> 4); }
 
   __device__ __forceinline__ void init(const Args& g, const char* xb, uint32_t x_bytes, int wave, int lane) {
@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 #pragma unroll 1
       for (int i0 = 0; i0 < HB * MT * 256; i0 += NW * 64) {
         const int i = i0 + threadIdx.x, b = i / (MT * 256);
+        if (HB * MT * 256 % (NW * 64) != 0 && b >= HB) break;  // whole waves
         const int col = i & 15, row = (i >> 4) % (16 * MT);
         const int at = ((row >> 4) * 64 + ((row & 15) >> 2) * 16 + col) * 4 + (row & 3);
         float gate = 0.f, up = 0.f;
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 struct Shape {
   int rows;  // token rows
   bool own;  // private rings, several workgroups of 4 waves per CU; else one of 8 waves
-  int per;   // workgroups per CU
+  int per;   // such workgroups per CU
 };
 static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool w4) {
   const int64_t few = w4 ? 4 : 8, load = routed ? T * k : 0;  // load <= m E: m pairs per expert on average
@@ -885,30 +886,39 @@ static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool 
   return {rows, rows <= 16, rows > 16 ? 1 : w4 && rows == 8 ? 3 : 2};
 }
 
-// Columns of a down tile, and workgroups per tile: about as many over all tiles
-// as run at once, so that all CUs pull weights.
-static inline int down_cols(const Shape& f) { return f.own ? 16 : 128; }
-static inline int down_splits(const Shape& f, int64_t T, int64_t D) {
-  const int64_t tiles = (D + down_cols(f) - 1) / down_cols(f) * ((T + kChunk - 1) / kChunk);
-  const int64_t s = (256 * f.per + tiles - 1) / tiles, most = f.own ? 8 : 32;
-  return (int)(s > most ? most : s);
+// The down projection's workgroups: columns of a tile, waves, and workgroups per
+// tile, so that all CUs pull weights. One workgroup of many waves per tile adds
+// its sums in LDS; several leave partial sums and count arrivals, which costs
+// about 3 us (T = 1, D = 4096, H = 11008 in 4 bits: 10.2 us with three of 4
+// waves): only where there are too few tiles, or chunks too long for the waves'
+// [token][column] tiles.
+struct DownShape {
+  int cols, waves, splits;
+};
+static inline DownShape down_shape(const Shape& f, int64_t T, int64_t D) {
+  const int cols = f.own ? 16 : 128, most = f.own ? 8 : 32;
+  const int64_t tiles = (D + cols - 1) / cols * ((T + kChunk - 1) / kChunk);
+  if (f.own && T <= 16 && tiles >= 160) return {cols, tiles < 384 ? 16 : tiles < 1024 ? 8 : 4, 1};
+  const int64_t s = (256 * f.per + tiles - 1) / tiles;
+  return {cols, f.own ? 4 : 8, (int)(s > most ? most : s)};
 }
 // Workspace of a block: the A plane, then where the down projection is split
 // one counter per output tile and the partial sums, each 256-byte aligned.
 struct BlockPlan {
   size_t ctr, partial, total;
-  int splits, n_ctr;
+  DownShape down;
+  int n_ctr;
   bool halves;
 };
 static inline BlockPlan block_plan(const Shape& f, int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   BlockPlan p;
-  p.splits = down_splits(f, T, D);
-  p.n_ctr = p.splits > 1 ? (int)((D + down_cols(f) - 1) / down_cols(f) * ((T + kChunk - 1) / kChunk)) : 0;
+  p.down = down_shape(f, T, D);
+  p.n_ctr = p.down.splits > 1 ? (int)((D + p.down.cols - 1) / p.down.cols * ((T + kChunk - 1) / kChunk)) : 0;
   p.halves = f.rows == 8 && e == 2;
   p.ctr = up((size_t)T * k * H * e * (p.halves ? 2 : 1));
   p.partial = p.ctr + up((size_t)p.n_ctr * 4);
-  p.total = p.partial + (p.splits > 1 ? up((size_t)p.splits * T * D * 4) : 0);
+  p.total = p.partial + (p.down.splits > 1 ? up((size_t)p.down.splits * T * D * 4) : 0);
   return p;
 }
 
@@ -930,25 +940,28 @@ template <int FMT, int XR>
 constexpr int groups_per_cu() { return FMT != 0 && XR < 16 ? 3 : 2; }
 
 // TC: tokens a private down tile has room for, 16 or a whole chunk.
-template <class E, int FMT, int HB, int XR, bool PLAIN>
+template <class E, int FMT, int HB, int XR, int NW, bool PLAIN>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(PLAIN ? STAGE_FEW_DOWN : STAGE_FEW_GATEUP, s);
   constexpr bool kOwn = XR <= 16;
-  constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : 8;
-  constexpr int PER = kOwn ? groups_per_cu<FMT, XR>() : 1, RING = !kOwn ? 147456 : PER == 2 ? 65536 : 32768;
+  constexpr int SH = kOwn ? 1 : 8;
+  constexpr int PER = !kOwn || NW > 4 ? 1 : groups_per_cu<FMT, XR>();
+  constexpr int RING = !kOwn ? 147456 : NW > 4 ? 16384 * NW : PER == 2 ? 65536 : 32768;
   const int64_t items = (int64_t)slots * ((g.N + 16 * HB * SH - 1) / (16 * HB * SH)), fit = PER * dev_ncu();
   const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
   hipLaunchKernelGGL((few_gateup<E, FMT, HB, XR, NW, SH, RING, PLAIN>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
-// SH: waves that share the rows when there are more than 16.
-template <class E, int FMT, int XR, int SHARE, int TC, bool HALVES>
+// NW: waves; SHARE: those that share the rows when there are more than 16.
+template <class E, int FMT, int XR, int NW, int SHARE, int TC, bool HALVES>
 static int launch_down(const Args& g, hipStream_t s) {
   StageScope scope(STAGE_FEW_DOWN, s);
   constexpr bool kOwn = XR <= 16;
-  constexpr int NW = kOwn ? 4 : 8, SH = kOwn ? 1 : SHARE;
-  constexpr int PER = groups_per_cu<FMT, XR>();
-  constexpr int RING = !kOwn ? 122880 : PER > 2 ? (TC > 16 ? 32768 : 40960) : TC > 16 ? 57344 : 65536;
+  constexpr int SH = kOwn ? 1 : SHARE, PER = groups_per_cu<FMT, XR>();
+  constexpr int RING = !kOwn     ? 122880
+                       : NW > 4  ? (FMT != 0 && XR == 16 ? 16384 : 8192) * NW
+                       : PER > 2 ? (TC > 16 ? 32768 : 40960)
+                                 : (TC > 16 ? 57344 : 65536);
   const dim3 grid((g.N + 16 * SH - 1) / (16 * SH), g.splits, (g.T + kChunk - 1) / kChunk);
   hipLaunchKernelGGL((few_down<E, FMT, 1, XR, NW, SH, RING, TC, HALVES>), grid, dim3(NW * 64), 0, s, g);
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
@@ -958,27 +971,41 @@ static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, c
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
               c.zeros, 0, 1, nullptr, nullptr, 0};
 }
+template <class E, int FMT, int XR, bool HALVES>
+static int down_own(const Args& g, int waves, hipStream_t s) {
+  if (g.T > 16) return launch_down<E, FMT, XR, 4, 1, kChunk, HALVES>(g, s);
+  // 16 rows of 4 bits need rings too long for 16 waves
+  constexpr int kMost = FMT != 0 && XR == 16 ? 8 : 16;
+  if (waves == 16) return launch_down<E, FMT, XR, kMost, 1, 16, HALVES>(g, s);
+  if (waves == 8) return launch_down<E, FMT, XR, 8, 1, 16, HALVES>(g, s);
+  return launch_down<E, FMT, XR, 4, 1, 16, HALVES>(g, s);
+}
 template <class E, int FMT>
-static int down_for(const Args& g, const Shape& f, hipStream_t s) {
-  constexpr int kFew = FMT ? 4 : 8;
-  constexpr bool kHalves = E::kBytes == 2;
-  if (f.rows == 8)
-    return g.T > 16 ? launch_down<E, FMT, kFew, 1, kChunk, kHalves>(g, s) : launch_down<E, FMT, kFew, 1, 16, kHalves>(g, s);
-  if (f.rows == 16)
-    return g.T > 16 ? launch_down<E, FMT, 16, 1, kChunk, false>(g, s) : launch_down<E, FMT, 16, 1, 16, false>(g, s);
+static int down_for(const Args& g, const Shape& f, int waves, hipStream_t s) {
+  if (f.rows == 8) return down_own<E, FMT, FMT ? 4 : 8, E::kBytes == 2>(g, waves, s);
+  if (f.rows == 16) return down_own<E, FMT, 16, false>(g, waves, s);
   if constexpr (FMT != 0) {
-    if (f.rows == 32) return launch_down<E, FMT, 32, 8, kChunk, false>(g, s);
+    if (f.rows == 32) return launch_down<E, FMT, 32, 8, 8, kChunk, false>(g, s);
   }
-  return launch_down<E, FMT, 64, 8, kChunk, false>(g, s);
+  return launch_down<E, FMT, 64, 8, 8, kChunk, false>(g, s);
+}
+// Private rings: 4 waves, or 8 where each CU would run one workgroup at most and K
+// is long (4-bit N = 4096: K = 11008 10.6 -> 9.5 us, K = 4096 5.4 -> 5.6 us).
+template <class E, int FMT, int HB, int XR, bool PLAIN>
+static int gateup_own(const Args& g, int slots, hipStream_t s) {
+  const int64_t items = (int64_t)slots * ((g.N + 16 * HB - 1) / (16 * HB)) * ((g.T + kChunk - 1) / kChunk);
+  const int stages = StreamOf<E, FMT, 1, 16, 1, 16384>::type::stages(g.K);
+  if (items <= dev_ncu() && stages >= 48) return launch_gateup<E, FMT, HB, XR, 8, PLAIN>(g, slots, s);
+  return launch_gateup<E, FMT, HB, XR, 4, PLAIN>(g, slots, s);
 }
 template <class E, int FMT>
 static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
-  if (f.rows == 8) return launch_gateup<E, FMT, 1, FMT ? 4 : 8, false>(g, slots, s);
-  if (f.rows == 16) return launch_gateup<E, FMT, 1, 16, false>(g, slots, s);
+  if (f.rows == 8) return gateup_own<E, FMT, 1, FMT ? 4 : 8, false>(g, slots, s);
+  if (f.rows == 16) return gateup_own<E, FMT, 1, 16, false>(g, slots, s);
   if constexpr (FMT != 0) {
-    if (f.rows == 32) return launch_gateup<E, FMT, 1, 32, false>(g, slots, s);
+    if (f.rows == 32) return launch_gateup<E, FMT, 1, 32, 8, false>(g, slots, s);
   }
-  return launch_gateup<E, FMT, 1, 64, false>(g, slots, s);
+  return launch_gateup<E, FMT, 1, 64, 8, false>(g, slots, s);
 }
 
 // y = x W^T (dense). At most 16 rows: items of 16 columns, or 32 where those
@@ -991,15 +1018,15 @@ int run_linear(const Call& c) {
   const Shape f = shape_of(c.T, 1, 1, false, true);
   const bool wide = (c.D + 31) / 32 >= 3 * dev_ncu();
   if (f.rows == 8) {
-    if (wide) return launch_gateup<E, FMT, 2, 4, true>(g, 1, c.stream);
-    return launch_gateup<E, FMT, 1, 4, true>(g, 1, c.stream);
+    if (wide) return gateup_own<E, FMT, 2, 4, true>(g, 1, c.stream);
+    return gateup_own<E, FMT, 1, 4, true>(g, 1, c.stream);
   }
   if (f.rows == 16) {
-    if (wide) return launch_gateup<E, FMT, 2, 16, true>(g, 1, c.stream);
-    return launch_gateup<E, FMT, 1, 16, true>(g, 1, c.stream);
+    if (wide) return gateup_own<E, FMT, 2, 16, true>(g, 1, c.stream);
+    return gateup_own<E, FMT, 1, 16, true>(g, 1, c.stream);
   }
-  if (f.rows == 32) return launch_down<E, FMT, 32, 4, kChunk, false>(g, c.stream);
-  return launch_down<E, FMT, 64, 4, kChunk, false>(g, c.stream);
+  if (f.rows == 32) return launch_down<E, FMT, 32, 8, 4, kChunk, false>(g, c.stream);
+  return launch_down<E, FMT, 64, 8, 4, kChunk, false>(g, c.stream);
 }
 
 template <class E, int FMT>
@@ -1017,10 +1044,10 @@ int run_block(const Call& c) {
   const int rc = gateup_for<E, FMT>(g, f, slots, c.stream);
   if (rc) return rc;
   Args d = args_of(c, c.ws, c.D, c.H, c.y);
-  d.splits = p.splits;
+  d.splits = p.down.splits;
   d.partial = (float*)(c.ws + p.partial);
   d.ctr = g.ctr;
-  return down_for<E, FMT>(d, f, c.stream);
+  return down_for<E, FMT>(d, f, p.down.waves, c.stream);
 }
 
 }  // namespace few

@@ -3,12 +3,13 @@
 //   descending order (equal logits: the lower index), their p as weights,
 //   divided by their sum when renormalised.
 //
-// Few tokens: one launch forms the logits, 16 experts and 16 tokens to a
-// workgroup, with K split over its waves and over workgroups so that many CUs
-// read the router's weight (one alone pulls 25 GB/s from HBM: 256 KiB took it
-// 10 us); a second one adds the parts and picks, one wave per token. Many
-// tokens: one launch, 32 tokens and all experts to a workgroup, bound by each
-// CU's reading of the weight from L2 (E D values per 32 tokens).
+// One launch forms the logits, with K split over workgroups where there are few
+// tokens so that many CUs read the router's weight (one alone pulls 25 GB/s from
+// HBM: 256 KiB took it 10 us); a second one adds the parts and picks, one wave
+// per token. Few tokens: 16 experts and 16 tokens to a workgroup. Many: 32 tokens
+// and every 128 experts, bound by each CU's reading of the weight from L2 (E D
+// values per 32 tokens) and by LDS. Picking in the first launch measured 20 us
+// more at 8192 tokens: its waves wait for one another's tokens.
 //
 // The order of the logits decides which experts run, so it is made exact: an
 // fp32 sum is off by at most gamma |x| |w_e| (gamma counts the roundings of the
@@ -29,8 +30,9 @@ struct Args {
   float* wts;      // [T, k]
   int* ids;        // [T, k]
   int T, D, E, k, renorm;
-  float* part;     // few tokens: [splits][T][E] logits, then [splits][E] and [splits][T] sums of squares
+  float* part;     // [splits][T][E] logits, then [splits][E] and [splits][T] sums of squares
   int splits;
+  int many;        // which of the two kernels formed the logits
 };
 
 // Monotone map of fp32 to unsigned: larger value, larger key; NaN above all.
@@ -237,7 +239,7 @@ __device__ __forceinline__ float gamma_of(int stages, int parts) {
   return 1.01f * (float)(stages * 2 * (E::kBytes == 4 ? 16 : 8) + parts) * 0x1p-24f;
 }
 
-// Few tokens, first launch: 16 experts (grid x), a part of K (y), XR tokens (z).
+// Few tokens: 16 experts (grid x), a part of K (y), XR tokens (z).
 constexpr int kPartWaves = 4, kMaxSplits = 4;
 template <class E, int XR>
 __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g) {
@@ -332,109 +334,91 @@ __global__ void __launch_bounds__(256) route_pick(const Args g) {
   }
   // not negative, so the bits order as the values do
   wmax = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, wmax)));
-  const int parts = g.splits * kPartWaves, stages = (g.D * E::kBytes + 127) >> 7;
+  const int parts = g.splits * (g.many ? 1 : kPartWaves), stages = (g.D * E::kBytes + 127) >> 7;
   const float bound = gamma_of<E>((stages + parts - 1) / parts, parts) * sqrtf(x2) * sqrtf(wmax);
   choose<E, NPL>(g, t, l, bound, lane);
 }
 
-// Many tokens: 32 per workgroup. Two groups of 4 waves halve K; in a group each
-// wave takes 32 of every 128 experts and a quarter of the token rows' loads.
+// Many tokens: 32 (grid x), a part of K (y). Each of the 4 waves takes 32 of
+// every 128 experts and a quarter of the token rows' loads.
 constexpr int kManyTok = 32, kManyRing = 60 * 1024;
-template <class E, int NPL>
-__global__ void __launch_bounds__(512, 2) route_tokens(const Args g) {
+template <class E>
+__global__ void __launch_bounds__(256, 2) route_logits_many(const Args g) {
   using S = few::RowStream<E, 2, kManyTok, 4, kManyRing>;
-  constexpr int LD = NPL * 64 + 1;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kManyRing];
-  __shared__ float logits[kManyTok * LD], x2[2][kManyTok];
-  __shared__ uint32_t w2max[2];
+  __shared__ __attribute__((aligned(1024))) char lds[kManyRing];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = wave >> 2, member = wave & 3;
   const int t0 = blockIdx.x * kManyTok, tc = min(kManyTok, g.T - t0);
-  if (threadIdx.x < 2) w2max[threadIdx.x] = 0u;
   few::Args a{};
   a.K = g.D;
   S st;
   const int kb = g.D * E::kBytes;
-  st.init(a, g.x + (int64_t)t0 * kb, (uint32_t)(tc * kb), member, lane);
+  st.init(a, g.x + (int64_t)t0 * kb, (uint32_t)(tc * kb), wave, lane);
   const int xrow = st.x_row(0, lane);
   st.token_row(0, xrow < tc ? (uint32_t)xrow * kb : kOOB, lane);
-  // both groups take equally many steps (they meet at barriers); one may be dead
-  const int stages = S::stages(g.D), per = (stages + 1) / 2, s0 = group * per, s1 = min(stages, s0 + per);
+  const int stages = S::stages(g.D), s0 = stages * (int)blockIdx.y / g.splits, s1 = stages * ((int)blockIdx.y + 1) / g.splits;
   const int passes = (g.E + 127) / 128;
   int s = s0, pass = 0;
   auto set_weights = [&] {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) st.weight(n, few::Weight{g.w, 0}, 0, pass * 128 + member * 32 + n * 16, g.E);
+    for (int n = 0; n < 2; ++n) st.weight(n, few::Weight{g.w, 0}, 0, pass * 128 + wave * 32 + n * 16, g.E);
   };
   auto issue = [&](uint32_t slot) {
     st.issue(slot, s, s < s1 && pass < passes, lane);
-    if (++s < s0 + per) return;
+    if (++s < s1) return;
     s = s0;
     if (++pass < passes) set_weights();
   };
   set_weights();
   few::Ring<S, 4> r;
-  r.start(lds + group * kManyRing, issue);
+  r.start(lds, issue);
+  float* part = g.part + ((int64_t)blockIdx.y * g.T + t0) * g.E;
+  float* pw = g.part + (int64_t)g.splits * g.T * g.E;
+  float* px = pw + g.splits * g.E;
   for (int p = 0; p < passes; ++p) {
     f32x4_t acc[2][2] = {};
     Squares<E, 2, 2> sq;
 #pragma unroll 1
-    for (int i = 0; i < per; ++i) r.step(st, acc, lane, issue, sq);
-    // group 0 writes its sums, group 1 adds its own
-#pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-      if (w == group) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int e = p * 128 + member * 32 + n * 16 + (lane & 15), row = 16 * m + 4 * (lane >> 4) + j;
-              if (e < g.E) logits[row * LD + e] = w ? logits[row * LD + e] + acc[n][m][j] : acc[n][m][j];
-            }
-      }
-      ring::lds_barrier();
-    }
-    // norms: not negative, so the bits order as the values do
+    for (int i = s0; i < s1; ++i) r.step(st, acc, lane, issue, sq);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const float v = over_chunks(sq.w[n]);
-      atomicMax(&w2max[group], __builtin_bit_cast(uint32_t, v));
-    }
-    if (p == 0 && member == 0) {
+      const int e = p * 128 + wave * 32 + n * 16 + (lane & 15);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float v = over_chunks(sq.x[m]);
-        if (lane < 16) x2[group][16 * m + lane] = v;
-      }
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = 16 * m + 4 * (lane >> 4) + j;
+          if (e < g.E && row < tc) part[(int64_t)row * g.E + e] = acc[n][m][j];
+        }
+      const float v = over_chunks(sq.w[n]);
+      if (blockIdx.x == 0 && lane < 16 && e < g.E) pw[blockIdx.y * g.E + e] = v;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const float v = over_chunks(sq.x[m]);
+      if (p == 0 && wave == 0 && lane < 16 && 16 * m + lane < tc) px[(int64_t)blockIdx.y * g.T + t0 + 16 * m + lane] = v;
     }
   }
   ring::wait_vmcnt<0>();
-  __syncthreads();
-  // |w|^2 of any expert is at most the sum of the groups' largest parts
-  const float wn = sqrtf(__builtin_bit_cast(float, w2max[0]) + __builtin_bit_cast(float, w2max[1]));
-  const float gamma = gamma_of<E>(per, 2);
-  for (int row = wave; row < tc; row += 8) {
-    float l[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) l[i] = logits[row * LD + i * 64 + lane];
-    choose<E, NPL>(g, t0 + row, l, gamma * sqrtf(x2[0][row] + x2[1][row]) * wn, lane);
-  }
 }
 
-// Workgroups along K of the few-token logits: about 128 over all, each wave
-// with at least one stage.
+static inline bool route_many(int64_t T) { return T >= 512; }
+// Workgroups along K: few tokens, about 128 over all, each wave with at least one
+// stage; many, about two per CU.
 static inline int route_splits(int64_t T, int64_t D, int64_t E, size_t e) {
-  const int64_t tiles = (E + 15) / 16 * ((T + 15) / 16), stages = ((int64_t)D * e + 127) / 128;
-  int64_t s = 128 / tiles;
-  if (s > stages / kPartWaves) s = stages / kPartWaves;
+  const int64_t stages = ((int64_t)D * e + 127) / 128;
+  int64_t s, most;
+  if (route_many(T)) {
+    s = 512 / ((T + kManyTok - 1) / kManyTok);
+    most = stages;
+  } else {
+    s = 128 / ((E + 15) / 16 * ((T + 15) / 16));
+    most = stages / kPartWaves;
+  }
+  if (s > most) s = most;
   return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }
-static inline bool route_many(int64_t T, int64_t E) { return T > 1024 && E <= 256; }
 static inline size_t route_bytes(int64_t T, int64_t D, int64_t E, size_t e) {
-  if (T == 0 || route_many(T, E)) return 0;
-  return (size_t)route_splits(T, D, E, e) * (size_t)(T * E + E + T) * 4;
+  return T == 0 ? 0 : (size_t)route_splits(T, D, E, e) * (size_t)(T * E + E + T) * 4;
 }
 
 #define SWIGLU_ROUTE_LAUNCH(kernel, grid, threads)                               \
@@ -447,16 +431,12 @@ static inline size_t route_bytes(int64_t T, int64_t D, int64_t E, size_t e) {
 template <class E>
 int run_route(Args g, hipStream_t stream) {
   if (g.T == 0) return SWIGLU_OK;
-  if (route_many(g.T, g.E)) {
-    const int tiles = (g.T + kManyTok - 1) / kManyTok;
-    if (g.E <= 128) SWIGLU_ROUTE_LAUNCH((route_tokens<E, 2>), (tiles), 512);
-    else SWIGLU_ROUTE_LAUNCH((route_tokens<E, 4>), (tiles), 512);
-    return SWIGLU_OK;
-  }
   g.splits = route_splits(g.T, g.D, g.E, E::kBytes);
-  const unsigned blocks = (g.E + 15) / 16;
-  if (g.T <= 8) SWIGLU_ROUTE_LAUNCH((route_logits<E, 8>), (blocks, g.splits, 1), kPartWaves * 64);
-  else SWIGLU_ROUTE_LAUNCH((route_logits<E, 16>), (blocks, g.splits, (g.T + 15) / 16), kPartWaves * 64);
+  g.many = route_many(g.T);
+  const unsigned blocks = (g.E + 15) / 16, tiles = (g.T + 15) / 16;
+  if (route_many(g.T)) SWIGLU_ROUTE_LAUNCH((route_logits_many<E>), ((g.T + kManyTok - 1) / kManyTok, g.splits), 256);
+  else if (g.T <= 8) SWIGLU_ROUTE_LAUNCH((route_logits<E, 8>), (blocks, g.splits, 1), kPartWaves * 64);
+  else SWIGLU_ROUTE_LAUNCH((route_logits<E, 16>), (blocks, g.splits, tiles), kPartWaves * 64);
   const unsigned groups = (g.T + 3) / 4;
   if (g.E <= 64) SWIGLU_ROUTE_LAUNCH((route_pick<E, 1>), (groups), 256);
   else if (g.E <= 128) SWIGLU_ROUTE_LAUNCH((route_pick<E, 2>), (groups), 256);

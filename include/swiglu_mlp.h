@@ -249,8 +249,8 @@ typedef struct {
   int32_t has_zeros;
 } swiglu_w4_t;
 
-/* workspace: the logits' partial sums for T <= 1024 or E > 256, else none
- * (may be NULL). Contents on entry do not matter. 0 bytes on bad args. */
+/* workspace: the logits' partial sums. Contents on entry do not matter. 0 bytes
+ * on bad args. */
 size_t swiglu_mlp_moe_route_workspace_bytes(int64_t T, int64_t D, int64_t E, int dtype);
 int swiglu_mlp_moe_route(const void* X, const void* Wr, float* weights, int32_t* ids, void* workspace,
                          size_t workspace_bytes, int64_t T, int64_t D, int64_t E, int64_t k, int renorm,

@@ -177,9 +177,9 @@ def test_host_validation_codes():
     assert ws(4, 64, 128, 8, 2, 0) >= 8 * 128 * 2 + 256 + 256 and ws(200, 65536, 128, 8, 2, 0) == 400 * 128 * 2 + 2 * 1792
     assert ws(0, 64, 128, 8, 2, 0) == 0 and ws(4, 64, 128, 64, 33, 0) == 0 and ws(4, 60, 128, 8, 2, 0) == 0
     rw = L.swiglu_mlp_moe_route_workspace_bytes
-    assert rw(4, 64, 8, 0) == 4 * (4 * 8 + 8 + 4) and rw(4096, 64, 8, 0) == 0 and rw(4, 60, 8, 0) == 0
+    assert rw(4, 64, 8, 0) == 4 * (4 * 8 + 8 + 4) and rw(1 << 14, 64, 8, 0) == 4 * ((1 << 14) * 9 + 8)
+    assert rw(4, 60, 8, 0) == 0 and rw(0, 64, 8, 0) == 0
     assert route(ws=None, n=0) == 6 and route(n=100) == 6 and route(ws=at[9] + 4) == 4 and route(ws=at[2]) == 5
-    assert route(ws=None, n=0, T=4096, X=at[0] + 8) == 4  # no workspace needed there: the next check speaks
     assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 0) == 4 * (1024 + 16 * 4 * 2)
     assert L.swiglu_mlp_w4_bytes(1, 64, 128, 32, 1) == 4 * (1024 + 16 * 4 * 2 + 32)
     assert L.swiglu_mlp_w4_bytes(1, 64, 100, 32, 0) == 0
