@@ -218,25 +218,42 @@ __device__ __forceinline__ void choose(const Args& g, int t, const float (&l)[NP
   }
 }
 
-// Sums of squares of the operands a stream shows it.
+// Sums of squares of the operands a stream shows it (the weights' where asked).
 template <class E, int NT, int MT>
 struct Squares {
+  bool weights;
   float x[MT] = {}, w[NT] = {};
   __device__ __forceinline__ void token(int m, u32x4_t v) { x[m] = add_squares<E>(v, x[m]); }
-  __device__ __forceinline__ void weight(int n, u32x4_t v) { w[n] = add_squares<E>(v, w[n]); }
+  __device__ __forceinline__ void weight(int n, u32x4_t v) {
+    if (weights) w[n] = add_squares<E>(v, w[n]);
+  }
 };
+// One stage's products from zero, then added: the matrix instruction rounds its
+// sum in a way of its own (an error of up to 5 units of 2^-24 of the sum of
+// magnitudes was measured over 32 products and the addend), so a chain of them
+// loses more than a chain of additions.
+template <class S, int SH, int NT, int MT, class Issue, class See>
+__device__ __forceinline__ void add_stage(few::Ring<S, SH>& r, const S& st, f32x4_t (&sum)[NT][MT], int lane, Issue&& issue,
+                                          See&& see) {
+  f32x4_t acc[NT][MT] = {};
+  r.step(st, acc, lane, issue, see);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sum[n][m] += acc[n][m];
+}
 // Over the four lanes that hold one row's chunks: every lane gets row lane & 15's.
 __device__ __forceinline__ float over_chunks(float v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
 
-// Roundings of one logit's chain: a matrix instruction of 32 exact products
-// (fp32: four of 4 rounded ones) counted as 8 (16) of them, two to a stage,
-// then the parts' sums; 1 % for the roundings of the norms.
+// Largest error of a logit over |x| |w|: two matrix instructions of 32 exact
+// products, counted as 8 roundings each (fp32: eight of 4 rounded ones, 4 each),
+// then the additions of the stages and of the parts; 1 % for the norms' roundings.
 template <class E>
 __device__ __forceinline__ float gamma_of(int stages, int parts) {
-  return 1.01f * (float)(stages * 2 * (E::kBytes == 4 ? 16 : 8) + parts) * 0x1p-24f;
+  return 1.01f * (float)((E::kBytes == 4 ? 32 : 16) + stages + parts) * 0x1p-24f;
 }
 
 // Few tokens: 16 experts (grid x), a part of K (y), XR tokens (z).
@@ -266,9 +283,9 @@ __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g)
   few::Ring<S, 1> r;
   r.start(lds + wave * 16384, issue);
   f32x4_t acc[1][1] = {};
-  Squares<E, 1, 1> sq;
+  Squares<E, 1, 1> sq{true};
 #pragma unroll 1
-  for (int i = 0; i < n; ++i) r.step(st, acc, lane, issue, sq);
+  for (int i = 0; i < n; ++i) add_stage(r, st, acc, lane, issue, sq);
   ring::wait_vmcnt<0>();
   __syncthreads();
   float* red = (float*)lds;
@@ -376,9 +393,9 @@ __global__ void __launch_bounds__(256, 2) route_logits_many(const Args g) {
   float* px = pw + g.splits * g.E;
   for (int p = 0; p < passes; ++p) {
     f32x4_t acc[2][2] = {};
-    Squares<E, 2, 2> sq;
+    Squares<E, 2, 2> sq{blockIdx.x == 0};
 #pragma unroll 1
-    for (int i = s0; i < s1; ++i) r.step(st, acc, lane, issue, sq);
+    for (int i = s0; i < s1; ++i) add_stage(r, st, acc, lane, issue, sq);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int e = p * 128 + wave * 32 + n * 16 + (lane & 15);
