@@ -75,7 +75,8 @@ __device__ __forceinline__ double chunk_dot(u32x4_t a, u32x4_t b, double s) {
 }
 
 // x[t] . w[e0] and x[t] . w[e1] in fp64 by one wave, the same on every lane.
-// Four 1 KiB pieces of each row are in flight.
+// Two 1 KiB pieces of each row are in flight: more registers would cost
+// route_pick more waves than the few tokens that come here gain.
 template <class E>
 __device__ __forceinline__ void exact_logits(const Args& g, int t, int e0, int e1, int lane, double (&out)[2]) {
   const int kb = g.D * E::kBytes;
@@ -84,16 +85,16 @@ __device__ __forceinline__ void exact_logits(const Args& g, int t, int e0, int e
   const __amdgpu_buffer_rsrc_t w1 = make_rsrc32(g.w + (int64_t)e1 * kb, kb);
   double s0 = 0.0, s1 = 0.0;
 #pragma unroll 1
-  for (int o = lane * 16; o - lane * 16 < kb; o += 4096) {
-    u32x4_t a[4], b[4], c[4];
+  for (int o = lane * 16; o - lane * 16 < kb; o += 2048) {
+    u32x4_t a[2], b[2], c[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       a[i] = few::load16(xr, o + 1024 * i);
       b[i] = few::load16(w0, o + 1024 * i);
       c[i] = few::load16(w1, o + 1024 * i);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       s0 = chunk_dot<E>(a[i], b[i], s0);
       s1 = chunk_dot<E>(a[i], c[i], s1);
     }
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g)
 
 // Second launch: one wave per token.
 template <class E, int NPL>
-__global__ void __launch_bounds__(256) route_pick(const Args g) {
+__global__ void __launch_bounds__(256, NPL <= 4 ? 8 : 2) route_pick(const Args g) {
   const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= g.T) return;
   const float* pw = g.part + (int64_t)g.splits * g.T * g.E;
