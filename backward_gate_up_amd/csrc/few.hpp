@@ -58,6 +58,7 @@ struct Args {
   uint32_t kinv;     // ceil(65536 / k): p / k = p * kinv >> 16 for a chunk's p < 2048, k <= 32
   int zeros;         // 4 bits: the weights have zero points (else every one is 8)
   int halves;        // gate/up: A as [T * k][2][N], the rounded value and what it left
+  int once;          // rows of whole 128-byte lines, read once
   int splits;        // down: workgroups per output tile
   float* partial;    // down, splits > 1: [splits][T][N]
   unsigned* ctr;     // gate/up: n_ctr arrival counters to clear for the down launch;
@@ -102,6 +103,16 @@ __device__ __forceinline__ i32x4_t scalar_rsrc(i32x4_t r) {
   return r;
 }
 
+// dma16 for whole lines that are read once: a non-temporal load leaves L2 to the
+// tokens (T = 16, E = 64: 165 -> 147 us; where rows share lines, K = 1000, they
+// come twice and it costs 20 %).
+__device__ __forceinline__ void dma16_once(uint32_t lds, i32x4_t rs, uint32_t voff, uint32_t soff) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  soff = __builtin_amdgcn_readfirstlane(soff);
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds" ::"v"(voff), "s"(rs), "s"(soff), "{m0}"(lds)
+               : "memory");
+}
+
 // Four bytes per lane to LDS address lds + 4 * lane (see dma16).
 __device__ __forceinline__ void dma4(uint32_t lds, i32x4_t rs, uint32_t voff, uint32_t soff) {
   lds = __builtin_amdgcn_readfirstlane(lds);
@@ -144,6 +155,7 @@ struct RowStream {
   i32x4_t rw[NT], rx;
   uint32_t w_off[2], x_off[XD];
   int kb, share, w_at;  // share: the wave's part of the token rows; w_at: its weights in a slot
+  bool once;            // no line of the weights is read twice
 
   static __host__ __device__ __forceinline__ int stages(int K) { return (K * E::kBytes + 127) >> 7; }
   // the token row (0 .. XR - 1) whose chunk this lane fetches in load j
@@ -154,6 +166,7 @@ struct RowStream {
     share = SH > 1 ? wave : 0;
     w_at = XR * 128 + share * NT * 2048;
     kb = g.K * E::kBytes;
+    once = g.once != 0;
     rx = scalar_rsrc(rsrc_words(xb, x_bytes));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -178,10 +191,17 @@ struct RowStream {
   __device__ __forceinline__ void issue(uint32_t slot, int s, bool live, int lane) const {
     const uint32_t at = (uint32_t)s * 128u;
     if (live && kb - (int)at >= 128) {
+      if (once) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, rw[n], w_off[j], at);
+          for (int n = 0; n < NT; ++n) dma16_once(slot + w_at + n * 2048 + j * 1024, rw[n], w_off[j], at);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) dma16(slot + w_at + n * 2048 + j * 1024, rw[n], w_off[j], at);
+      }
 #pragma unroll
       for (int j = 0; j < XD; ++j) dma16(slot + (share * XD + j) * 1024, rx, x_off[j], at);
       return;
@@ -969,7 +989,7 @@ static int launch_down(const Args& g, hipStream_t s) {
 
 static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, char* out) {
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
-              c.zeros, 0, 1, nullptr, nullptr, 0};
+              c.zeros, 0, 0, 1, nullptr, nullptr, 0};
 }
 template <class E, int FMT, int XR, bool HALVES>
 static int down_own(const Args& g, int waves, hipStream_t s) {
@@ -1037,6 +1057,7 @@ int run_block(const Call& c) {
   g.w0 = c.wg;
   g.w1 = c.wu;
   g.halves = p.halves;
+  g.once = c.D * E::kBytes % 128 == 0;
   g.ctr = (unsigned*)(c.ws + p.ctr);
   g.n_ctr = p.n_ctr;
   const int64_t pairs = (c.T < kChunk ? c.T : kChunk) * c.k;
@@ -1044,6 +1065,7 @@ int run_block(const Call& c) {
   const int rc = gateup_for<E, FMT>(g, f, slots, c.stream);
   if (rc) return rc;
   Args d = args_of(c, c.ws, c.D, c.H, c.y);
+  d.once = c.H * E::kBytes % 128 == 0;
   d.splits = p.down.splits;
   d.partial = (float*)(c.ws + p.partial);
   d.ctr = g.ctr;
