@@ -15,6 +15,10 @@ transformers MLP modules (gate_proj, up_proj, down_proj nn.Linear layers, so
 their state dicts load unchanged; the kernels read the nn.Linear weight
 layout directly), and ``SwiGLUMLPPacked`` keeps [D, H] / [H, D] weights.
 
+Serving with few tokens (serve.py): a mixture of SwiGLU experts (``moe_route``,
+``moe_experts``, ``moe_infer``, module ``SwiGLUMoE``) and weights in 4 bits with
+group scales (``W4Weight``, ``w4_linear``, ``infer_w4``, module ``SwiGLUMLPW4``).
+
 Weight layouts (``linear``): False (kernel layout): Wg, Wu [D, H], Wd [H, D];
 True (nn.Linear layout): Wg, Wu [H, D], Wd [D, H]. Weight gradients come back
 in the layout of their weights.
@@ -27,12 +31,13 @@ import torch
 from . import _lib as _L
 from ._lib import SwiGLUError, STAGE_NAMES, NUM_STAGES  # noqa: F401
 from .serve import (moe_route, moe_experts, moe_infer, w4_quantize, w4_pack, w4_linear, infer_w4,  # noqa: F401
-                    W4Weight)
+                    W4Weight, SwiGLUMLPW4, SwiGLUMoE)
 
 __all__ = ["fwd", "bwd", "infer", "infer_noalloc", "SwiGLUMLPFunction", "swiglu_mlp", "SwiGLUMLP",
            "SwiGLUMLPPacked", "saved_bytes",
            "infer_workspace_bytes", "bwd_workspace_bytes", "SwiGLUError", "StageTimer",
-           "moe_route", "moe_experts", "moe_infer", "w4_quantize", "w4_pack", "w4_linear", "infer_w4", "W4Weight"]
+           "moe_route", "moe_experts", "moe_infer", "w4_quantize", "w4_pack", "w4_linear", "infer_w4", "W4Weight",
+           "SwiGLUMLPW4", "SwiGLUMoE"]
 
 _DT = {torch.bfloat16: _L.BF16, torch.float16: _L.FP16, torch.float32: _L.FP32}
 

@@ -16,6 +16,7 @@ while autograd is on.
 """
 
 import ctypes
+import functools
 
 import torch
 
@@ -31,12 +32,24 @@ def _check(rc, where):
         raise SwiGLUError(rc, where)
 
 
+# A decoding step is a few calls of about 20 us, so what Python adds to each counts:
+# the raw stream costs 0.1 us where a Stream object costs 2, size queries are kept.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
 def _ptr(t):
     return t.data_ptr() if t.numel() else None
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(query, *sizes):
+    return getattr(_L.lib(), query)(*sizes)
 
 
 def _code(t, table=_DT):
@@ -48,7 +61,9 @@ def _code(t, table=_DT):
 
 
 def _no_grad(*tensors):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+    if not torch.is_grad_enabled():
+        return
+    if any(t.requires_grad for t in tensors):
         raise RuntimeError("the few-token serving operators have no backward: call them under torch.no_grad()")
 
 
@@ -65,12 +80,18 @@ def _buf(t, shape, dtype, device, name):
     return t
 
 
+def _like(y, x):
+    return torch.empty_like(x) if y is None else _buf(y, x.shape, x.dtype, x.device, "y")
+
+
 def _workspace(ws, need, device):
+    """(pointer, bytes, the tensor that holds them)"""
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), need, ws
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return ws
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 class W4Weight:
@@ -84,10 +105,10 @@ class W4Weight:
         self.data, self.shape, self.group = data, tuple(shape), int(group)
         self.has_zeros, self.dtype = bool(has_zeros), dtype
         self.experts = self.shape[0] if len(self.shape) == 3 else 1
+        self.device = data.device
         self._c = _L.W4(data.data_ptr(), self.experts, self.shape[-2], self.shape[-1], self.group, int(self.has_zeros))
         self._ref = ctypes.byref(self._c)
 
-    device = property(lambda self: self.data.device)
     requires_grad = False
 
     @classmethod
@@ -179,10 +200,10 @@ def moe_route(x, w_router, top_k, renormalize=True, weights=None, ids=None, work
     weights = _buf(weights, (T, top_k), torch.float32, x.device, "weights")
     ids = _buf(ids, (T, top_k), torch.int32, x.device, "ids")
     dt, L = _code(x), _L.lib()
-    ws = _workspace(workspace, L.swiglu_mlp_moe_route_workspace_bytes(T, D, E, dt), x.device)
-    rc = L.swiglu_mlp_moe_route(_ptr(x), w_router.data_ptr(), _ptr(weights), _ptr(ids), _ptr(ws),
-                                ws.numel() * ws.element_size(), T, D, E, top_k, bool(renormalize), dt,
-                                _stream(x.device))
+    need = _bytes("swiglu_mlp_moe_route_workspace_bytes", T, D, E, dt)
+    ws, nbytes, keep = _workspace(workspace, need, x.device)
+    rc = L.swiglu_mlp_moe_route(_ptr(x), w_router.data_ptr(), _ptr(weights), _ptr(ids), ws, nbytes, T, D, E, top_k,
+                                bool(renormalize), dt, _stream(x.device))
     _check(rc, "swiglu_mlp_moe_route")
     return weights, ids
 
@@ -207,12 +228,12 @@ def _expert_shapes(x, wg, wu, wd):
     if x.dim() != 2 or len(wg.shape) != 3:
         raise ValueError("expected X[T,D] and weights [E,H,D], [E,H,D], [E,D,H]")
     E, H, D = wg.shape
-    if x.shape[1] != D or tuple(wu.shape) != (E, H, D) or tuple(wd.shape) != (E, D, H):
+    if x.shape[1] != D or wu.shape != wg.shape or wd.shape != (E, D, H):
         raise ValueError(f"shape mismatch (expected Wg[E,H,D], Wu[E,H,D], Wd[E,D,H]): X{tuple(x.shape)} "
                          f"Wg{tuple(wg.shape)} Wu{tuple(wu.shape)} Wd{tuple(wd.shape)}")
-    for t in (wg, wu, wd):
-        if t.dtype != x.dtype or t.device != x.device:
-            raise ValueError("all tensors must share dtype and device")
+    dtype, device = x.dtype, x.device
+    if not (wg.dtype == wu.dtype == wd.dtype == dtype and wg.device == wu.device == wd.device == device):
+        raise ValueError("all tensors must share dtype and device")
     if w4:
         _same_form(wg, wu, wd)
     _on_gpu(x)
@@ -237,16 +258,16 @@ def moe_experts(x, weights, ids, wg, wu, wd, y=None, workspace=None):
             or weights.dtype != torch.float32 or ids.device != x.device or weights.device != x.device):
         raise ValueError("weights must be fp32 and ids int32, both [T, k] on x's device")
     k, dt, L = ids.shape[1], _code(x), _L.lib()
-    y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, k, dt), x.device)
-    nbytes = ws.numel() * ws.element_size()
+    y = _like(y, x)
+    need = _bytes("swiglu_mlp_moe_workspace_bytes", T, D, H, E, k, dt)
+    ws, nbytes, keep = _workspace(workspace, need, x.device)
     if w4:
         rc = L.swiglu_mlp_moe_experts_w4(_ptr(x), _ptr(weights), _ptr(ids), wg._ref, wu._ref, wd._ref, _ptr(y),
-                                         _ptr(ws), nbytes, T, k, dt, _stream(x.device))
+                                         ws, nbytes, T, k, dt, _stream(x.device))
     else:
         wg, wu, wd = wg.contiguous(), wu.contiguous(), wd.contiguous()
         rc = L.swiglu_mlp_moe_experts(_ptr(x), _ptr(weights), _ptr(ids), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(),
-                                      _ptr(y), _ptr(ws), nbytes, T, D, H, E, k, dt, _stream(x.device))
+                                      _ptr(y), ws, nbytes, T, D, H, E, k, dt, _stream(x.device))
     _check(rc, "swiglu_mlp_moe_experts")
     return y
 
@@ -262,16 +283,16 @@ def moe_infer(x, w_router, wg, wu, wd, top_k, renormalize=True, y=None, workspac
     if E2 != E:
         raise ValueError(f"the router has {E} experts, the weights {E2}")
     dt, L = _code(x), _L.lib()
-    y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_moe_workspace_bytes(T, D, H, E, top_k, dt), x.device)
-    nbytes = ws.numel() * ws.element_size()
+    y = _like(y, x)
+    need = _bytes("swiglu_mlp_moe_workspace_bytes", T, D, H, E, top_k, dt)
+    ws, nbytes, keep = _workspace(workspace, need, x.device)
     if w4:
-        rc = L.swiglu_mlp_moe_infer_w4(_ptr(x), w_router.data_ptr(), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws),
+        rc = L.swiglu_mlp_moe_infer_w4(_ptr(x), w_router.data_ptr(), wg._ref, wu._ref, wd._ref, _ptr(y), ws,
                                        nbytes, T, top_k, bool(renormalize), dt, _stream(x.device))
     else:
         wg, wu, wd = wg.contiguous(), wu.contiguous(), wd.contiguous()
         rc = L.swiglu_mlp_moe_infer(_ptr(x), w_router.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), _ptr(y),
-                                    _ptr(ws), nbytes, T, D, H, E, top_k, bool(renormalize), dt, _stream(x.device))
+                                    ws, nbytes, T, D, H, E, top_k, bool(renormalize), dt, _stream(x.device))
     _check(rc, "swiglu_mlp_moe_infer")
     return y
 
@@ -310,9 +331,105 @@ def infer_w4(x, wg, wu, wd, y=None, workspace=None):
     _same_form(wg, wu, wd)
     _on_gpu(x)
     dt, L = _DT16[x.dtype], _L.lib()
-    y = _buf(y, (T, D), x.dtype, x.device, "y")
-    ws = _workspace(workspace, L.swiglu_mlp_w4_infer_workspace_bytes(T, D, H, dt), x.device)
-    rc = L.swiglu_mlp_w4_infer(_ptr(x), wg._ref, wu._ref, wd._ref, _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), T,
-                               dt, _stream(x.device))
+    y = _like(y, x)
+    need = _bytes("swiglu_mlp_w4_infer_workspace_bytes", T, D, H, dt)
+    ws, nbytes, keep = _workspace(workspace, need, x.device)
+    rc = L.swiglu_mlp_w4_infer(_ptr(x), wg._ref, wu._ref, wd._ref, _ptr(y), ws, nbytes, T, dt, _stream(x.device))
     _check(rc, "swiglu_mlp_w4_infer")
     return y
+
+
+class _W4Module(torch.nn.Module):
+    """Keeps 4-bit weights as byte buffers, so that they follow the module to
+    another device and into its state dict, and hands them out as W4Weight."""
+
+    def _keep(self, name, w):
+        self.register_buffer(name, w.data)
+        self._forms[name] = w
+
+    def _weight(self, name):
+        data, w = self._buffers[name], self._forms[name]
+        if data.data_ptr() != w._c.data:
+            w = self._forms[name] = W4Weight(data, w.shape, w.group, w.has_zeros, w.dtype)
+        return w
+
+
+class SwiGLUMLPW4(_W4Module):
+    """The dense SwiGLU block with 4-bit weights, made from a ``SwiGLUMLP`` (or any
+    module with gate_proj, up_proj and down_proj). No gradients. Above
+    ``long_tokens`` tokens the weights are written back to rows and the no-grad
+    path of 16-bit weights runs, which is bound by arithmetic then."""
+
+    def __init__(self, mlp, group=128, zeros=False, long_tokens=512):
+        super().__init__()
+        self._forms, self.long_tokens = {}, long_tokens
+        for name in ("gate_proj", "up_proj", "down_proj"):
+            self._keep(name, W4Weight.quantize(getattr(mlp, name).weight, group, zeros))
+
+    def forward(self, x):
+        w = [self._weight(n) for n in ("gate_proj", "up_proj", "down_proj")]
+        x2 = x.reshape(-1, x.shape[-1])
+        if x2.shape[0] > self.long_tokens:
+            from . import infer
+
+            _no_grad(x)
+            return infer(x2, *(t.dequantize() for t in w), linear=True).reshape(x.shape)
+        return infer_w4(x2, *w).reshape(x.shape)
+
+
+class SwiGLUMoE(_W4Module):
+    """A mixture of SwiGLU experts for inference: ``gate`` (nn.Linear, hidden_size
+    -> num_experts, no bias) and the experts' stacked weights ``gate_proj``,
+    ``up_proj`` [E, H, D] and ``down_proj`` [E, D, H]. ``config`` has hidden_size,
+    moe_intermediate_size (or intermediate_size), num_experts (or
+    num_local_experts), num_experts_per_tok and optionally norm_topk_prob (default
+    true). ``from_experts`` stacks existing blocks, ``quantize_`` puts the experts
+    into 4 bits."""
+
+    def __init__(self, config):
+        super().__init__()
+        pick = lambda *names: next(int(getattr(config, n)) for n in names if getattr(config, n, None) is not None)  # noqa: E731
+        act = getattr(config, "hidden_act", "silu")
+        if act not in ("silu", "swish"):
+            raise ValueError(f"SwiGLUMoE computes SiLU gating; config.hidden_act is {act!r}")
+        D, H = pick("hidden_size"), pick("moe_intermediate_size", "intermediate_size")
+        E, self.top_k = pick("num_experts", "num_local_experts"), pick("num_experts_per_tok")
+        self.renormalize = bool(getattr(config, "norm_topk_prob", True))
+        self._forms = {}
+        self.gate = torch.nn.Linear(D, E, bias=False)
+        par = lambda *shape: torch.nn.Parameter(torch.randn(shape) / shape[-1] ** 0.5)  # noqa: E731
+        self.gate_proj, self.up_proj, self.down_proj = par(E, H, D), par(E, H, D), par(E, D, H)
+
+    @classmethod
+    def from_experts(cls, gate, experts, top_k, renormalize=True):
+        """From a router nn.Linear and a list of blocks with gate_proj, up_proj
+        and down_proj layers (no bias)."""
+        m = cls.__new__(cls)
+        torch.nn.Module.__init__(m)
+        m._forms, m.top_k, m.renormalize, m.gate = {}, int(top_k), bool(renormalize), gate
+        if gate.bias is not None:
+            raise ValueError("the router has no bias term")
+        for name in ("gate_proj", "up_proj", "down_proj"):
+            layers = [getattr(e, name) for e in experts]
+            if any(layer.bias is not None for layer in layers):
+                raise ValueError("SwiGLUMoE has no bias terms")
+            setattr(m, name, torch.nn.Parameter(torch.stack([layer.weight.detach() for layer in layers])))
+        if gate.weight.shape != (len(experts), m.gate_proj.shape[2]):
+            raise ValueError("the router must map hidden_size to the number of experts")
+        return m
+
+    def quantize_(self, group=128, zeros=False):
+        """Replaces the experts' weights by 4-bit ones (in place; not undone)."""
+        for name in ("gate_proj", "up_proj", "down_proj"):
+            w = W4Weight.quantize(getattr(self, name), group, zeros)
+            delattr(self, name)
+            self._keep(name, w)
+        return self
+
+    def forward(self, x):
+        if self._forms:
+            w = [self._weight(n) for n in ("gate_proj", "up_proj", "down_proj")]
+        else:
+            w = [self.gate_proj, self.up_proj, self.down_proj]
+        x2 = x.reshape(-1, x.shape[-1])
+        return moe_infer(x2, self.gate.weight, *w, self.top_k, self.renormalize).reshape(x.shape)

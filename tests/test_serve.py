@@ -499,3 +499,86 @@ def test_strides_streams_buffers_and_graph():
         float(torch.randn(1 << 18, device="cuda").square().sum())
         torch.cuda.synchronize()
         assert torch.equal(out, m.moe_infer(x, wr, *w, k)) and torch.equal(out4, m.moe_infer(x, wr, *w4, k))
+
+
+# ---- modules and the example --------------------------------------------------------
+
+
+def _moe_config(**kw):
+    from types import SimpleNamespace
+
+    return SimpleNamespace(**{**dict(hidden_size=64, moe_intermediate_size=96, num_experts=6, num_experts_per_tok=2), **kw})
+
+
+def test_modules_on_the_host():
+    mod = m.SwiGLUMoE(_moe_config(norm_topk_prob=False))
+    assert mod.gate.weight.shape == (6, 64) and mod.gate_proj.shape == (6, 96, 64) and mod.down_proj.shape == (6, 64, 96)
+    assert mod.top_k == 2 and not mod.renormalize
+    assert set(mod.state_dict()) == {"gate.weight", "gate_proj", "up_proj", "down_proj"}
+    with pytest.raises(ValueError, match="hidden_act"):
+        m.SwiGLUMoE(_moe_config(hidden_act="gelu"))
+    from types import SimpleNamespace
+
+    blocks = [m.SwiGLUMLP(SimpleNamespace(hidden_size=64, intermediate_size=96)) for _ in range(6)]
+    stacked = m.SwiGLUMoE.from_experts(torch.nn.Linear(64, 6, bias=False), blocks, 2)
+    assert torch.equal(stacked.up_proj[3], blocks[3].up_proj.weight) and stacked.down_proj.shape == (6, 64, 96)
+    with pytest.raises(ValueError, match="bias"):
+        m.SwiGLUMoE.from_experts(torch.nn.Linear(64, 6), blocks, 2)
+    with pytest.raises(ValueError, match="experts"):
+        m.SwiGLUMoE.from_experts(torch.nn.Linear(64, 5, bias=False), blocks, 2)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        mod(torch.zeros(2, 3, 64))
+    with pytest.raises(RuntimeError, match="no backward"):
+        mod(torch.zeros(2, 3, 64))
+
+
+@gpu
+def test_modules():
+    banner("modules")
+    dt = torch.bfloat16
+    torch.manual_seed(1)
+    mod = m.SwiGLUMoE(_moe_config(hidden_size=128, moe_intermediate_size=160)).to("cuda", dt)
+    x = randn(gen(5), (3, 5, 128), 1, dt).cuda()
+    with torch.no_grad():
+        y = mod(x)
+        assert y.shape == x.shape
+        args = [mod.gate.weight, mod.gate_proj, mod.up_proj, mod.down_proj]
+        assert torch.equal(y.view(15, 128), m.moe_infer(x.view(15, 128), *args, 2))
+        w = [m.W4Weight.quantize(t, 32, True) for t in args[1:]]
+        y4 = mod.quantize_(32, True)(x)
+        assert torch.equal(y4.view(15, 128), m.moe_infer(x.view(15, 128), args[0], *w, 2))
+        assert set(mod.state_dict()) == {"gate.weight", "gate_proj", "up_proj", "down_proj"}
+        # the buffers may be replaced (a load, another device): the next call takes the new ones
+        old = mod.gate_proj
+        mod.gate_proj = old.clone()
+        old.zero_()
+        assert torch.equal(mod(x), y4)
+        # the dense block: few tokens on the 4-bit kernels, many on rows
+        from types import SimpleNamespace
+
+        mlp = m.SwiGLUMLP(SimpleNamespace(hidden_size=128, intermediate_size=256)).to("cuda", dt)
+        q = m.SwiGLUMLPW4(mlp, 64, long_tokens=40)
+        rows = [q._weight(n).dequantize() for n in ("gate_proj", "up_proj", "down_proj")]
+        ref = ref_block(f64(x.view(15, 128)), *map(f64, rows))
+        # the rows are the 4-bit weights rounded once more: half a step of each of two products' weights
+        assert_local(f64(q(x).view(15, 128)), ref, bound(dt, 4), "dense 4 bits")
+        long = randn(gen(6), (50, 128), 1, dt).cuda()
+        assert torch.equal(q(long), m.infer(long, *rows, linear=True))
+
+
+@gpu
+def test_example(monkeypatch, capsys):
+    banner("example")
+    import importlib.util
+    import os
+    import sys
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_moe.py")
+    spec = importlib.util.spec_from_file_location("serve_moe", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    monkeypatch.setattr(sys, "argv", ["serve_moe.py", "--experts", "12", "--top-k", "3", "--dim", "256", "--hidden", "128",
+                                      "--steps", "3"])
+    # a code's step is max|w| / 7.5, about 0.36 of the weights' deviation in groups of 128, its rounding
+    # 0.10 of it; the three weights' together about 0.18 of the output's norm
+    assert 0.1 < mod.main() < 0.25
