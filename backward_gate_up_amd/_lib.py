@@ -83,7 +83,8 @@ def lib():
             ("w4_quantize", [vp] * 4 + [i64] * 3 + [i32, i32, vp], i32),
             ("w4_pack", [vp] * 4 + [i64] * 3 + [i32, vp], i32),
             ("w4_dequantize", [w4, vp, i32, vp], i32),
-            ("w4_linear", [vp, w4, vp, i64, i32, vp], i32),
+            ("w4_linear_workspace_bytes", [i64] * 3 + [i32], sz),
+            ("w4_linear", [vp, w4, vp, vp, sz, i64, i32, vp], i32),
             ("w4_infer_workspace_bytes", [i64] * 3 + [i32], sz),
             ("w4_infer", [vp] + [w4] * 3 + [vp, vp, sz, i64, i32, vp], i32)):
         f = getattr(L, "swiglu_mlp_" + name)

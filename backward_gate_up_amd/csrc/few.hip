@@ -338,19 +338,30 @@ int swiglu_mlp_w4_dequantize(const swiglu_w4_t* w, void* W, int dtype, hipStream
   return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 
-int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T, int dtype, hipStream_t stream) {
+size_t swiglu_mlp_w4_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype) {
+  if (elt_bytes(dtype) != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(N) || !ld_ok(K)) return 0;
+  return few::linear_bytes(T, N, K);
+}
+
+int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, void* workspace, size_t workspace_bytes,
+                         int64_t T, int dtype, hipStream_t stream) {
   if (elt_bytes(dtype) != 2) return SWIGLU_ERR_DTYPE;
   int rc = check_w4(w);
   if (rc) return rc;
   if (w->experts != 1 || T < 0 || T > SWIGLU_FEW_MAX_T) return SWIGLU_ERR_SHAPE;
+  const size_t need = T ? few::linear_bytes(T, w->N, w->K) : 0;
   const Range in[] = {{X, (size_t)T * w->K * 2}, w4_range(w)};
-  const Range out[] = {{Y, (size_t)T * w->N * 2}};
-  if ((rc = check_ptrs(in, 2)) || (rc = check_ptrs(out, 1)) || (rc = check_alias(out, 1, in, 2))) return rc;
+  const Range out[] = {{Y, (size_t)T * w->N * 2}, {workspace, need}};
+  if ((rc = check_ptrs(in, 2)) || (rc = check_ptrs(out, 1))) return rc;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_WORKSPACE;
+  if (workspace && !aligned16(workspace)) return SWIGLU_ERR_ALIGN;
+  if ((rc = check_alias(out, 2, in, 2))) return rc;
   if ((rc = check_device())) return rc;
   if (T == 0) return SWIGLU_OK;
   few::Call c{};
   c.wd = w4_weight(w);
   c.y = (char*)Y;
+  c.ws = (char*)workspace;
   c.T = T;
   c.x = (const char*)X;
   c.D = w->N;

@@ -269,7 +269,7 @@ struct W4Stream {
   static_assert(NS >= 2 && XD >= 1 && (NS - 1) * D <= 63, "ring");
   static constexpr float kOff = std::is_same<E, Bf16>::value ? 128.0f : 64.0f;
   i32x4_t rw[NT], rx;
-  uint32_t x_off[XD], scale_off;
+  uint32_t x_off[XD], scale_off, mask, base;
   int kb, rec, zeros, share, w_at;
 
   static __host__ __device__ __forceinline__ int stages(int K) { return (K + 127) >> 7; }
@@ -282,6 +282,9 @@ struct W4Stream {
     zeros = g.zeros;
     rec = 1024 + 32 * GP + (zeros ? 32 : 0);
     scale_off = 1024 + lane * 4 < rec ? 1024 + lane * 4 : kOOB;
+    constexpr bool kBf = std::is_same<E, Bf16>::value;
+    asm("s_mov_b32 %0, %1" : "=s"(mask) : "i"(kBf ? 0x000f000f : 0x00f000f0));
+    asm("v_mov_b32 %0, %1" : "=v"(base) : "i"(kBf ? 0x43004300 : 0x54005400));
     rx = scalar_rsrc(rsrc_words(xb, x_bytes));
   }
   __device__ __forceinline__ void weight(int n, const Weight& wt, int e, int row0, int N) {
@@ -314,22 +317,17 @@ struct W4Stream {
     for (int j = 0; j < XD; ++j)
       dma16(slot + (share * XD + j) * 1024, rx, (int)chunk(x_row(j, lane), lane) < left ? x_off[j] : kOOB, atx);
   }
-  // (v & m) | o in one instruction: its operands have to be registers, and the
-  // compiler, which knows the constants, would take two with literals
-  static __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t m, uint32_t o) {
-    uint32_t r;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(m), "v"(o));
-    return r;
-  }
-  // eight codes of one dword as the MFMA operand OFF + q
-  static __device__ __forceinline__ u32x4_t widen(uint32_t v) {
-    if constexpr (std::is_same<E, Bf16>::value) {
-      constexpr uint32_t m = 0x000f000fu, o = 0x43004300u;  // 128 + q: mantissa step 1
-      return u32x4_t{and_or(v, m, o), and_or(v >> 4, m, o), and_or(v >> 8, m, o), and_or(v >> 12, m, o)};
-    } else {
-      constexpr uint32_t m = 0x00f000f0u, o = 0x54005400u;  // 64 + q: mantissa step 1/16
-      return u32x4_t{and_or(v << 4, m, o), and_or(v, m, o), and_or(v >> 4, m, o), and_or(v >> 8, m, o)};
-    }
+  // Eight codes of one dword as the MFMA operand OFF + q: 128 + q in bf16 (mantissa
+  // step 1), 64 + q in fp16 (step 1/16). mask and base come from init, where the
+  // compiler cannot see their values: it would take an and and an or with
+  // literals for what v_and_or_b32 does from registers. (The instruction itself
+  // must stay the compiler's: a matrix instruction that reads a vector
+  // instruction's result needs wait states, which it does not put after assembly.)
+  __device__ __forceinline__ u32x4_t widen(uint32_t v) const {
+    if constexpr (std::is_same<E, Bf16>::value)
+      return u32x4_t{(v & mask) | base, ((v >> 4) & mask) | base, ((v >> 8) & mask) | base, ((v >> 12) & mask) | base};
+    else
+      return u32x4_t{((v << 4) & mask) | base, (v & mask) | base, ((v >> 4) & mask) | base, ((v >> 8) & mask) | base};
   }
   static __device__ __forceinline__ u32x4_t ones() {
     constexpr uint32_t o = std::is_same<E, Bf16>::value ? 0x3f803f80u : 0x3c003c00u;
@@ -852,7 +850,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
       store_partial(g.partial + ((int64_t)blockIdx.y * g.T + t0) * g.N, tc, g.N, row, n, v);
     }
   }
-  if (direct) return;
+  if (direct || !g.ctr) return;  // without counters another launch adds them (few_sum)
   // Arrival, as in stream_gemm: device-coherent partials, each wave waits for
   // its own, then one atomic add; the last workgroup adds the splits in order.
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -884,6 +882,25 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
     for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);
     *(typename E::vec4*)((typename E::elem*)g.out + (int64_t)(t0 + row) * g.N + n) = o;
   }
+}
+
+// y = rnd(sum of the splits' partial sums), four values per thread.
+template <class E>
+__global__ void __launch_bounds__(256) few_sum(const float* partial, typename E::elem* y, int64_t quads, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  f32x4_t v{};
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+    f32x4_t b[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) b[s] = s0 + s < splits ? ((const f32x4_t*)partial)[(s0 + s) * quads + i] : f32x4_t{};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v += b[s];
+  }
+  typename E::vec4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = E::from_f32(v[j]);
+  ((typename E::vec4*)y)[i] = o;
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -960,13 +977,11 @@ template <int FMT, int XR>
 constexpr int groups_per_cu() { return FMT != 0 && XR < 16 ? 3 : 2; }
 
 // TC: tokens a private down tile has room for, 16 or a whole chunk.
-template <class E, int FMT, int HB, int XR, int NW, bool PLAIN>
+template <class E, int FMT, int HB, int XR, int NW, int SH, bool PLAIN>
 static int launch_gateup(const Args& g, int slots, hipStream_t s) {
   StageScope scope(PLAIN ? STAGE_FEW_DOWN : STAGE_FEW_GATEUP, s);
-  constexpr bool kOwn = XR <= 16;
-  constexpr int SH = kOwn ? 1 : 8;
-  constexpr int PER = !kOwn || NW > 4 ? 1 : groups_per_cu<FMT, XR>();
-  constexpr int RING = !kOwn ? 147456 : NW > 4 ? 16384 * NW : PER == 2 ? 65536 : 32768;
+  constexpr int PER = SH > 1 || NW > 4 || XR > 16 ? 1 : groups_per_cu<FMT, XR>();
+  constexpr int RING = SH > 1 ? 147456 : NW > 4 ? 16384 * NW : XR > 16 ? (FMT ? 86016 : 98304) : PER == 2 ? 65536 : 32768;
   const int64_t items = (int64_t)slots * ((g.N + 16 * HB * SH - 1) / (16 * HB * SH)), fit = PER * dev_ncu();
   const dim3 grid((unsigned)(items < fit ? items : fit), 1, (g.T + kChunk - 1) / kChunk);
   hipLaunchKernelGGL((few_gateup<E, FMT, HB, XR, NW, SH, RING, PLAIN>), grid, dim3(NW * 64), 0, s, g);
@@ -1015,26 +1030,43 @@ template <class E, int FMT, int HB, int XR, bool PLAIN>
 static int gateup_own(const Args& g, int slots, hipStream_t s) {
   const int64_t items = (int64_t)slots * ((g.N + 16 * HB - 1) / (16 * HB)) * ((g.T + kChunk - 1) / kChunk);
   const int stages = StreamOf<E, FMT, 1, 16, 1, 16384>::type::stages(g.K);
-  if (items <= dev_ncu() && stages >= 48) return launch_gateup<E, FMT, HB, XR, 8, PLAIN>(g, slots, s);
-  return launch_gateup<E, FMT, HB, XR, 4, PLAIN>(g, slots, s);
+  if (items <= dev_ncu() && stages >= 48) return launch_gateup<E, FMT, HB, XR, 8, 1, PLAIN>(g, slots, s);
+  return launch_gateup<E, FMT, HB, XR, 4, 1, PLAIN>(g, slots, s);
 }
 template <class E, int FMT>
 static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
   if (f.rows == 8) return gateup_own<E, FMT, 1, FMT ? 4 : 8, false>(g, slots, s);
   if (f.rows == 16) return gateup_own<E, FMT, 1, 16, false>(g, slots, s);
+  // With so few tiles of 128 columns that most CUs would idle, tiles of 16 whose
+  // waves split K on private rings, each row loaded by one of them (4 bits: 32
+  // rows at a time, more leave no room).
+  const int64_t tiles = (int64_t)slots * ((g.N + 127) / 128) * ((g.T + kChunk - 1) / kChunk);
+  if (8 * tiles < 3 * dev_ncu()) return launch_gateup<E, FMT, 1, FMT ? 32 : 64, 4, 1, false>(g, slots, s);
   if constexpr (FMT != 0) {
-    if (f.rows == 32) return launch_gateup<E, FMT, 1, 32, 8, false>(g, slots, s);
+    if (f.rows == 32) return launch_gateup<E, FMT, 1, 32, 8, 8, false>(g, slots, s);
   }
-  return launch_gateup<E, FMT, 1, 64, 8, false>(g, slots, s);
+  return launch_gateup<E, FMT, 1, 64, 8, 8, false>(g, slots, s);
 }
 
 // y = x W^T (dense). At most 16 rows: items of 16 columns, or 32 where those
 // still give every workgroup one. More: tiles of 64 columns with two groups of
-// 4 waves along K (its K cannot be split over workgroups, whose arrival counters
-// no earlier launch would have cleared).
+// 4 waves along K; where those are few, K is split over workgroups as well and a
+// second launch adds the parts (N = 1248, K = 9792, T = 48: 57 us without).
+static inline int linear_splits(int64_t T, int64_t N, int64_t K) {
+  if (shape_of(T, 1, 1, false, true).own) return 1;
+  const int64_t tiles = (N + 63) / 64 * ((T + kChunk - 1) / kChunk), most = (K + 127) / 128 / 6;
+  int64_t s = 256 / tiles;
+  if (s > most) s = most;
+  return s < 2 ? 1 : s > 16 ? 16 : (int)s;
+}
+static inline size_t linear_bytes(int64_t T, int64_t N, int64_t K) {
+  const int s = linear_splits(T, N, K);
+  return s > 1 ? (size_t)s * T * N * 4 : 0;
+}
+
 template <class E, int FMT>
 int run_linear(const Call& c) {
-  const Args g = args_of(c, c.x, c.D, c.H, c.y);
+  Args g = args_of(c, c.x, c.D, c.H, c.y);
   const Shape f = shape_of(c.T, 1, 1, false, true);
   const bool wide = (c.D + 31) / 32 >= 3 * dev_ncu();
   if (f.rows == 8) {
@@ -1045,8 +1077,16 @@ int run_linear(const Call& c) {
     if (wide) return gateup_own<E, FMT, 2, 16, true>(g, 1, c.stream);
     return gateup_own<E, FMT, 1, 16, true>(g, 1, c.stream);
   }
-  if (f.rows == 32) return launch_down<E, FMT, 32, 8, 4, kChunk, false>(g, c.stream);
-  return launch_down<E, FMT, 64, 8, 4, kChunk, false>(g, c.stream);
+  g.splits = linear_splits(c.T, c.D, c.H);
+  g.partial = (float*)c.ws;
+  const int rc = f.rows == 32 ? launch_down<E, FMT, 32, 8, 4, kChunk, false>(g, c.stream)
+                              : launch_down<E, FMT, 64, 8, 4, kChunk, false>(g, c.stream);
+  if (rc || g.splits == 1) return rc;
+  StageScope scope(STAGE_FEW_DOWN, c.stream);
+  const int64_t quads = c.T * c.D / 4;
+  hipLaunchKernelGGL((few_sum<E>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, c.stream, (const float*)c.ws,
+                     (typename E::elem*)c.y, quads, g.splits);
+  return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
 }
 
 template <class E, int FMT>

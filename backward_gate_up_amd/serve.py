@@ -297,8 +297,8 @@ def moe_infer(x, w_router, wg, wu, wd, top_k, renormalize=True, y=None, workspac
     return y
 
 
-def w4_linear(x, w, y=None):
-    """Y[T, N] = x[T, K] W^T with a 4-bit weight [N, K]; one launch."""
+def w4_linear(x, w, y=None, workspace=None):
+    """Y[T, N] = x[T, K] W^T with a 4-bit weight [N, K]."""
     _no_grad(x)
     x = x.contiguous()
     if x.dim() != 2 or len(w.shape) != 2 or x.shape[1] != w.shape[1]:
@@ -306,9 +306,11 @@ def w4_linear(x, w, y=None):
     if w.dtype != x.dtype or w.device != x.device:
         raise ValueError("all tensors must share dtype and device")
     _on_gpu(x)
-    T = x.shape[0]
-    y = _buf(y, (T, w.shape[0]), x.dtype, x.device, "y")
-    _check(_L.lib().swiglu_mlp_w4_linear(_ptr(x), w._ref, _ptr(y), T, _DT16[x.dtype], _stream(x.device)),
+    T, (N, K), dt = x.shape[0], w.shape, _DT16[x.dtype]
+    y = _buf(y, (T, N), x.dtype, x.device, "y")
+    need = _bytes("swiglu_mlp_w4_linear_workspace_bytes", T, N, K, dt)
+    ws, nbytes, keep = _workspace(workspace, need, x.device) if need else (None, 0, None)
+    _check(_L.lib().swiglu_mlp_w4_linear(_ptr(x), w._ref, _ptr(y), ws, nbytes, T, dt, _stream(x.device)),
            "swiglu_mlp_w4_linear")
     return y
 

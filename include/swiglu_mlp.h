@@ -288,9 +288,12 @@ int swiglu_mlp_w4_pack(const void* codes, const void* scales, const void* zeros,
                        int64_t experts, int64_t N, int64_t K, int group, hipStream_t stream);
 int swiglu_mlp_w4_dequantize(const swiglu_w4_t* w, void* W, int dtype, hipStream_t stream);
 
-/* Y [T, N] = X [T, K] W^T. One launch, no workspace. */
-int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, int64_t T, int dtype,
-                         hipStream_t stream);
+/* Y [T, N] = X [T, K] W^T. One launch; with more than 16 tokens and few output
+ * columns two, and a workspace of partial sums between them (0 bytes
+ * otherwise; may be NULL then). */
+size_t swiglu_mlp_w4_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype);
+int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, void* workspace,
+                         size_t workspace_bytes, int64_t T, int dtype, hipStream_t stream);
 
 /* The dense block with 4-bit weights, two launches; workspace: A [T, H], then
  * counters and partial sums as a mixture's. The three weights share group

@@ -144,8 +144,8 @@ def _codes(L):
         return L.swiglu_mlp_moe_infer(a["X"], Wr, a["Wg"], a["Wu"], a["Wd"], a["Y"], a["ws"], a["n"], a["T"], a["D"],
                                       a["H"], a["E"], a["k"], 1, a["dt"], None)
 
-    def linear(w=None, X=at[0], Y=at[1], T=4, dt=0):
-        return L.swiglu_mlp_w4_linear(X, r(w or _w4(2)), Y, T, dt, None)
+    def linear(w=None, X=at[0], Y=at[1], ws=None, n=0, T=4, dt=0):
+        return L.swiglu_mlp_w4_linear(X, r(w or _w4(2)), Y, ws, n, T, dt, None)
 
     def block(wg=None, wu=None, wd=None, X=at[0], Y=at[1], ws=at[2], n=1 << 30, T=4, dt=0):
         return L.swiglu_mlp_w4_infer(X, r(wg or _w4(3)), r(wu or _w4(4)), r(wd or _w4(5, 128, 64)), Y, ws, n, T, dt, None)
@@ -169,6 +169,11 @@ def test_host_validation_codes():
     assert linear(dt=2) == 3 and block(dt=2) == 3
     for bad in (_w4(2, group=48), _w4(2, K=100), _w4(2, N=12), _w4(2, experts=2), _w4(2, K=0)):
         assert linear(bad) == 2
+    need = L.swiglu_mlp_w4_linear_workspace_bytes(32, 64, 4096, 0)
+    assert need % (32 * 64 * 4) == 0 and need > 0 and L.swiglu_mlp_w4_linear_workspace_bytes(4, 64, 4096, 0) == 0
+    long = _w4(2, 64, 4096)
+    assert linear(long, T=32) == 6 and linear(long, T=32, ws=at[3], n=need - 1) == 6
+    assert linear(long, T=32, ws=at[3] + 8, n=need) == 4 and linear(long, T=32, ws=at[1], n=need) == 5
     assert linear(_w4(2, data=0)) == 1 and linear(_w4(2, data=at[2] + 8)) == 4 and linear(Y=at[2] + 256) == 5
     assert block(wu=_w4(4, 128, 64)) == 2 and block(wd=_w4(5)) == 2 and block(wu=_w4(4, group=64)) == 2
     assert block(ws=None, n=0) == 6 and block(n=4 * 64 * 2 - 1) == 6
@@ -261,7 +266,7 @@ def expert_weights(g, E, D, H, dtype):
             randn(g, (E, D, H), H ** -0.5, dtype))
 
 
-SHAPES = [(1, 8, 2, 128, 256), (1, 6, 6, 1000, 712), (2, 4, 1, 8, 8), (16, 16, 4, 264, 40), (17, 5, 3, 96, 72),
+SHAPES = [(40, 2, 1, 1000, 328), (64, 4, 2, 64, 6200), (1, 8, 2, 128, 256), (1, 6, 6, 1000, 712), (2, 4, 1, 8, 8), (16, 16, 4, 264, 40), (17, 5, 3, 96, 72),
           (64, 4, 2, 256, 136), (65, 9, 2, 64, 200), (130, 3, 2, 72, 64), (9, 1, 1, 512, 1024), (3, 200, 8, 64, 64)]
 
 
@@ -396,7 +401,8 @@ def test_w4_quantize(group, zeros, dt):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("T,N,K,group", [(1, 8, 32, 32), (1, 4096, 512, 128), (2, 40, 160, 32), (16, 1000, 192, 64),
                                          (17, 264, 1152, 128), (33, 128, 2816, 64), (64, 72, 416, 32), (65, 16, 128, 128),
-                                         (200, 24, 96, 32), (0, 16, 64, 32)])
+                                         (200, 24, 96, 32), (0, 16, 64, 32), (20, 104, 2112, 32), (48, 320, 4992, 64),
+                                         (70, 136, 1536, 128)])
 def test_w4_linear(T, N, K, group, zeros, dt):
     banner(f"w4_linear {dt} T={T} N={N} K={K} g={group} zeros={zeros}")
     g = gen(N + K)
@@ -426,7 +432,8 @@ def test_w4_offset_sums_keep_their_digits(dt):
 @gpu
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("T,D,H,group,zeros", [(1, 256, 512, 128, False), (5, 160, 96, 32, True), (16, 1024, 704, 64, False),
-                                               (40, 128, 1408, 128, True), (70, 64, 64, 64, False)])
+                                               (40, 128, 1408, 128, True), (70, 64, 64, 64, False),
+                                               (20, 256, 1088, 32, True), (40, 64, 12416, 64, False)])
 def test_infer_w4(T, D, H, group, zeros, dt):
     banner(f"infer_w4 {dt} T={T} D={D} H={H} g={group} zeros={zeros}")
     g = gen(D + H)

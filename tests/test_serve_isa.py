@@ -3,8 +3,10 @@
 Their loads into LDS come from inline assembly, whose hazards the compiler does
 not see: between a vector instruction that writes a scalar register and a memory
 instruction that reads it, five wait states are needed, and one between a write
-of M0 and a load into LDS. Checked for every such load in program order, with a
-self-test that a short distance is caught. And no kernel may use scratch.
+of M0 and a load into LDS. Likewise a matrix instruction reads what a vector
+instruction wrote only two wait states later: the compiler sees to that for its
+own instructions and not for assembly. Checked in program order, with self-tests
+that a short distance is caught. And no kernel may use scratch.
 """
 
 import os
@@ -17,7 +19,7 @@ import pytest
 
 from backward_gate_up_amd import build as B
 
-COMBOS = [(0, 0), (2, 0), (0, 128), (1, 32), (1, 64)]
+COMBOS = [(0, 0), (2, 0), (0, 128), (0, 32), (1, 32), (1, 64)]
 LOAD = re.compile(r"^buffer_load_dword(?:x4)? v\d+, (s\[(\d+):(\d+)\]|v\S+), (\S+) offen.* lds")
 DST = re.compile(r"^(v_\w+) (m0|vcc|s\d+|s\[\d+:\d+\])(?:,|$)")
 
@@ -64,6 +66,34 @@ def hazards(asm):
     return bad, n
 
 
+def vectors(t):
+    m = re.match(r"v\[(\d+):(\d+)\]$", t)
+    if m:
+        return range(int(m.group(1)), int(m.group(2)) + 1)
+    return [int(t[1:])] if re.match(r"v\d+$", t) else []
+
+
+def matrix_hazards(asm):
+    """Matrix instructions with fewer than 2 wait states after a vector
+    instruction's write of one of their operands; and how many there are."""
+    bad, at, written, n = [], 0, {}, 0
+    for t, states in instructions(asm):
+        op, _, rest = t.partition(" ")
+        args = [a.strip() for a in rest.split(",")]
+        if op.startswith("v_mfma"):
+            n += 1
+            for a in args[1:4]:
+                bad += [f"v{r} written {at - written[r] - 1} states before: {t}" for r in vectors(a)
+                        if at - written.get(r, -99) < 3]
+        for r in vectors(args[0]):
+            if op.startswith("v_") and not op.startswith("v_mfma"):
+                written[r] = at
+            elif op.startswith(("v_mfma", "ds_read", "buffer_load", "global_load")):
+                written.pop(r, None)
+        at += states
+    return bad, n
+
+
 @pytest.fixture(scope="module")
 def kernels():
     def one(c):
@@ -93,6 +123,23 @@ def test_lds_loads_keep_their_wait_states(kernels, combo):
         assert not bad, (name, bad[:3])
         assert scratch == 0, name
     assert loads >= 20
+
+
+@pytest.mark.parametrize("combo", COMBOS)
+def test_matrix_operands_keep_their_wait_states(kernels, combo):
+    count = 0
+    for name, (asm, _) in kernels[combo].items():
+        bad, n = matrix_hazards(asm)
+        count += n
+        assert not bad, (name, bad[:3])
+    assert count >= 40
+
+
+def test_matrix_checker_catches_short_distances():
+    mfma = "v_mfma_f32_16x16x32_bf16 v[0:3], v[4:7], v[8:11], v[0:3]\n"
+    assert matrix_hazards("v_and_or_b32 v9, v1, s0, v2\ns_nop 1\n" + mfma) == ([], 1)
+    assert matrix_hazards("v_and_or_b32 v9, v1, s0, v2\ns_nop 0\n" + mfma)[0]
+    assert not matrix_hazards("v_mov_b32 v9, v1\nds_read_b128 v[8:11], v20\n" + mfma)[0]
 
 
 def test_checker_catches_short_distances():
