@@ -50,14 +50,16 @@ template <class E>
 __device__ __forceinline__ float add_squares(u32x4_t v, float s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    // A copy, since a bit cast of a vector's element v[i] reads element 0.
+    const uint32_t b = v[i];
     if constexpr (std::is_same<E, Bf16>::value) {
       typedef __bf16 v2 __attribute__((ext_vector_type(2)));
-      s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2, v[i]), __builtin_bit_cast(v2, v[i]), s, false);
+      s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2, b), __builtin_bit_cast(v2, b), s, false);
     } else if constexpr (std::is_same<E, Fp16>::value) {
       typedef _Float16 v2 __attribute__((ext_vector_type(2)));
-      s = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2, v[i]), __builtin_bit_cast(v2, v[i]), s, false);
+      s = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2, b), __builtin_bit_cast(v2, b), s, false);
     } else {
-      const float f = __builtin_bit_cast(float, v[i]);
+      const float f = __builtin_bit_cast(float, b);
       s = fmaf(f, f, s);
     }
   }

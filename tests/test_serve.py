@@ -243,6 +243,28 @@ def test_route_ties_and_near_ties(dt):
 
 
 @gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("lane", [0, 1, 2, 5, 7])
+@pytest.mark.parametrize("T", [12, 600])
+def test_route_order_below_fp32(T, lane, dt):
+    """Experts that differ in the last digits of a long sum: only exact logits
+    give their order. The data sits in one element of every eight, so that each
+    part of a 16-byte chunk has to count in the bound that asks for them."""
+    banner(f"route order T={T} lane={lane} {dt}")
+    D, E, k = 4096, 12, 5
+    g = gen(lane)
+    at = torch.arange(lane, D, 8)
+    x, base = torch.zeros(T, D), torch.zeros(E, D)
+    x[:, at] = torch.randn((T, at.numel()), generator=g)
+    base[:, at] = torch.randn(at.numel(), generator=g)
+    base[:, at[-1]] *= 1 + torch.arange(E).float()[torch.randperm(E, generator=g)] * 2.0 ** -6
+    x[:, at[-1]] *= 2.0 ** -12
+    x, wr = x.to(DT[dt]), base.to(DT[dt])
+    _, ids = m.moe_route(x.cuda(), wr.cuda(), k)
+    assert np.array_equal(ids.cpu().numpy(), ref_route(f64(x), f64(wr), k, True)[0])
+
+
+@gpu
 def test_route_nonfinite_tokens_stay_in_range():
     banner("route NaN / Inf")
     g = gen(4)
