@@ -113,7 +113,7 @@ struct MoePlan {
 static MoePlan moe_plan(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, bool w4, size_t e) {
   const size_t p = (size_t)T * k;
   MoePlan m;
-  m.wts = few::block_plan(few::shape_of(T, k, E, true, w4), T, D, H, k, e).total;
+  m.wts = few::block_plan(few::shape_of(T, k, E, true, w4, e), T, D, H, k, e).total;
   const size_t r = up256(route::route_bytes(T, D, E, e));
   if (m.wts < r) m.wts = r;
   m.ids = m.wts + up256(p * 4);
@@ -376,7 +376,7 @@ int swiglu_mlp_w4_linear(const void* X, const swiglu_w4_t* w, void* Y, void* wor
 size_t swiglu_mlp_w4_infer_workspace_bytes(int64_t T, int64_t D, int64_t H, int dtype) {
   const size_t e = elt_bytes(dtype);
   if (e != 2 || T <= 0 || T > SWIGLU_FEW_MAX_T || !ld_ok(D) || !ld_ok(H)) return 0;
-  return few::block_plan(few::shape_of(T, 1, 1, false, true), T, D, H, 1, e).total;
+  return few::block_plan(few::shape_of(T, 1, 1, false, true, 2), T, D, H, 1, e).total;
 }
 
 int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t* wu, const swiglu_w4_t* wd, void* Y,
@@ -389,7 +389,8 @@ int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* wg, const swiglu_w4_t*
       wd->experts != 1 || wu->group != wg->group || wd->group != wg->group || !wu->has_zeros != !wg->has_zeros ||
       !wd->has_zeros != !wg->has_zeros || T < 0 || T > SWIGLU_FEW_MAX_T)
     return SWIGLU_ERR_SHAPE;
-  const size_t td = (size_t)T * wg->K * e, need = few::block_plan(few::shape_of(T, 1, 1, false, true), T, wg->K, wg->N, 1, e).total;
+  const size_t td = (size_t)T * wg->K * e;
+  const size_t need = few::block_plan(few::shape_of(T, 1, 1, false, true, 2), T, wg->K, wg->N, 1, e).total;
   const Range in[] = {{X, td}, w4_range(wg), w4_range(wu), w4_range(wd)};
   const Range out[] = {{Y, td}, {workspace, need}};
   if ((rc = check_ptrs(in, 4)) || (rc = check_ptrs(out, 1))) return rc;

@@ -923,21 +923,32 @@ __global__ void __launch_bounds__(256) few_sum(const float* partial, typename E:
 
 // ---- launches ---------------------------------------------------------------------
 // Token rows per stage (8: as few as a load instruction covers, 8 or in 4 bits
-// 4). Dense: what the tokens need. Routed: what an expert's share of the pairs
-// mostly needs, T k / E on average; a more crowded expert takes several passes
-// over its weights. 4-bit experts with 16 pairs each on average (T = 64, E = 16,
-// k = 4, D = 2048): 32 rows 50.6 us, 64 rows 62. Above 16 rows waves have to
-// share them, and 8 waves cannot share the loads of 32 rows of 128 bytes.
+// 4). Dense: what the tokens need. Routed: what an expert's share of a chunk's
+// pairs mostly needs; a more crowded expert takes several passes over its
+// weights. Where it pays to go up was measured with E = 16, D = 2048, H = 1408,
+// k = 8 and E = 6, D = 3056, H = 1264, k = 3 (4 bits: D = 2688, H = 1024), by
+// the average load of an expert:
+//   16 rows against 64, 16 bits   load 10: 63.5/72.9, 53.9/64.6 us
+//                                 load 12: 78.9/74.1, 58.6/68.4
+//                                 load 16: 91.3/76.0, 69.3/71.2
+//   fp32, bound by its products   load 10: 113/210, 82/139
+//                                 load 24: 207/216, 136/149; load 32: 276/220, 164/153
+//   4 bits, 16 rows against 32    load 12: 49.3/51.7, 39.6/46.2
+//                                 load 16: 64.0/53.4, 47.9/48.2
+//   32 against 64                 load 16: 53.4/63.2, 48.2/51.2
+// Above 16 rows waves have to share them, and 8 waves cannot share the loads of
+// 32 rows of 128 bytes.
 struct Shape {
   int rows;  // token rows
   bool own;  // private rings, several workgroups of 4 waves per CU; else one of 8 waves
   int per;   // such workgroups per CU
 };
-static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool w4) {
-  const int64_t few = w4 ? 4 : 8, load = routed ? T * k : 0;  // load <= m E: m pairs per expert on average
+static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool w4, size_t e) {
+  // load <= m E: m pairs per expert on average
+  const int64_t few = w4 ? 4 : 8, load = routed ? (T < kChunk ? T : kChunk) * k : 0;
   int rows = 64;
   if (T <= few || (routed && 4 * load <= few * E)) rows = 8;
-  else if (T <= 16 || (routed && load <= 6 * E)) rows = 16;
+  else if (T <= 16 || (routed && load <= (e == 4 ? 24 : w4 ? 12 : 10) * E)) rows = 16;
   else if (w4 && (T <= 32 || (routed && load <= 20 * E))) rows = 32;
   return {rows, rows <= 16, rows > 16 ? 1 : w4 && rows == 8 ? 3 : 2};
 }
@@ -1072,7 +1083,7 @@ static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
 // 4 waves along K; where those are few, K is split over workgroups as well and a
 // second launch adds the parts (N = 1248, K = 9792, T = 48: 57 us without).
 static inline int linear_splits(int64_t T, int64_t N, int64_t K) {
-  if (shape_of(T, 1, 1, false, true).own) return 1;
+  if (shape_of(T, 1, 1, false, true, 2).own) return 1;
   const int64_t tiles = (N + 63) / 64 * ((T + kChunk - 1) / kChunk), most = (K + 127) / 128 / 6;
   int64_t s = 256 / tiles;
   if (s > most) s = most;
@@ -1086,7 +1097,7 @@ static inline size_t linear_bytes(int64_t T, int64_t N, int64_t K) {
 template <class E, int FMT>
 int run_linear(const Call& c) {
   Args g = args_of(c, c.x, c.D, c.H, c.y);
-  const Shape f = shape_of(c.T, 1, 1, false, true);
+  const Shape f = shape_of(c.T, 1, 1, false, true, 2);
   const bool wide = (c.D + 31) / 32 >= 3 * dev_ncu();
   if (f.rows == 8) {
     if (wide) return gateup_own<E, FMT, 2, 4, true>(g, 1, c.stream);
@@ -1110,7 +1121,7 @@ int run_linear(const Call& c) {
 
 template <class E, int FMT>
 int run_block(const Call& c) {
-  const Shape f = shape_of(c.T, c.k, c.E, c.ids != nullptr, FMT != 0);
+  const Shape f = shape_of(c.T, c.k, c.E, c.ids != nullptr, FMT != 0, E::kBytes);
   const BlockPlan p = block_plan(f, c.T, c.D, c.H, c.k, E::kBytes);
   Args g = args_of(c, c.x, c.H, c.D, c.ws);
   g.w0 = c.wg;
