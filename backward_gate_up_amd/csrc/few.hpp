@@ -583,6 +583,12 @@ struct Walk {
 // items. SH = 1: 16 HB columns, the waves take equal parts of K and their sums
 // meet in LDS; SH = NW: 16 HB columns per wave, all of K. The rings run on
 // from item to item: while one is finished, the loads of the next are in flight.
+// Bound by HBM where there is enough to read: E = 64, T = 16, k = 8, D = 2048,
+// H = 1408, bf16: 93 us for the 55 or so experts that occur, 651 MB, 7.0 TB/s; the
+// 64 rows of E = 8, T = 64, D = 4096, H = 11008 271 us, 5.3 TB/s, LDS reads of the
+// token rows being on the way. One token of E = 8, D = 1024, H = 2816 (23 MB) is
+// 9 us: start, a first load's latency and the reduction. In 4 bits (E = 64, T = 8)
+// 31 us, 4.1 TB/s, where widening the codes is half of the wave's instructions.
 // RING: bytes of LDS for the workgroup's rings. PLAIN: y = x W^T instead, one
 // weight block per 16 columns and no SwiGLU (dense, w0 and out = y).
 template <class E, int FMT, int HB, int XR, int NW, int SH, int RING, bool PLAIN>
@@ -739,7 +745,11 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 // many steps; more than one of them only for a dense product.
 // HALVES: A comes as two values (see few_gateup), in rows 0 .. XR - 1 and
 // XR .. 2 XR - 1 of the token operand, which repeats nothing then: no more
-// matrix instructions than with one.
+// matrix instructions than with one. Measured where few_gateup was: 51 us for
+// 326 MB (6.3 TB/s), 149 us (4.8 TB/s), 8.7 us for 11.5 MB, and 22 us in 4 bits.
+// W4, T = 33, N = 11008, K = 4096, g = 64, fp16: 20.8 us, 25 MB: bound by the waves'
+// instructions (codes to widen, LDS reads of the tokens, a scale per group and
+// output) on the 172 of 256 CUs that have a tile of 64 columns.
 template <class E, int FMT, int NT, int XR, int NW, int SH, int RING, int TC, bool HALVES>
 __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 : 2)) few_down(const Args g) {
   using S = typename StreamOf<E, FMT, NT, (HALVES ? 2 * XR : XR), SH, RING / (NW / SH)>::type;

@@ -259,7 +259,8 @@ __device__ __forceinline__ float gamma_of(int stages, int parts) {
   return 1.01f * (float)((E::kBytes == 4 ? 32 : 16) + stages + parts) * 0x1p-24f;
 }
 
-// Few tokens: 16 experts (grid x), a part of K (y), XR tokens (z).
+// Few tokens: 16 experts (grid x), a part of K (y), XR tokens (z). 3.8 us for
+// T = 1, E = 64, D = 2048, of which an empty kernel takes 1.7: latency.
 constexpr int kPartWaves = 4, kMaxSplits = 4;
 template <class E, int XR>
 __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g) {
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g)
   if (col == 0 && blockIdx.x == 0 && row < tc) px[(int64_t)blockIdx.y * g.T + t] = vx;
 }
 
-// Second launch: one wave per token.
+// Second launch: one wave per token. T = 8192, E = 128, k = 8, D = 4096: 15 us, bound
+// by its instructions (the wave-wide maxima of k rounds); 3.7 us at T = 1.
 template <class E, int NPL>
 __global__ void __launch_bounds__(256, NPL <= 4 ? 8 : 2) route_pick(const Args g) {
   const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -360,7 +362,9 @@ __global__ void __launch_bounds__(256, NPL <= 4 ? 8 : 2) route_pick(const Args g
 }
 
 // Many tokens: 32 (grid x), a part of K (y). Each of the 4 waves takes 32 of
-// every 128 experts and a quarter of the token rows' loads.
+// every 128 experts and a quarter of the token rows' loads. T = 8192, E = 128,
+// D = 4096, fp16: 22.8 us, 2.9 TB/s of tokens and 377 TFLOP/s; every 32 tokens read
+// the whole weight (1 MiB), so the CUs draw 12 TB/s from L2.
 constexpr int kManyTok = 32, kManyRing = 60 * 1024;
 template <class E>
 __global__ void __launch_bounds__(256, 2) route_logits_many(const Args g) {

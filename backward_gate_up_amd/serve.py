@@ -274,7 +274,7 @@ def moe_experts(x, weights, ids, wg, wu, wd, y=None, workspace=None):
 
 def moe_infer(x, w_router, wg, wu, wd, top_k, renormalize=True, y=None, workspace=None):
     """A whole mixture-of-experts layer: ``moe_route`` then ``moe_experts``,
-    three launches in one call. x [T, D], w_router [E, D]; wg, wu [E, H, D] and
+    four launches in one call. x [T, D], w_router [E, D]; wg, wu [E, H, D] and
     wd [E, D, H], tensors of x's dtype or three ``W4Weight``."""
     _no_grad(x, w_router, *(() if isinstance(wg, W4Weight) else (wg, wu, wd)))
     x, w_router = x.contiguous(), w_router.contiguous()
