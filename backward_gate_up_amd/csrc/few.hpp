@@ -825,8 +825,39 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
         f32x4_t acc[NT][MT] = {};
 #pragma unroll 1
         for (int s = 0; s < count; ++s) r.step(st, acc, lane, issue);
-        // one token row at a time: a token listed twice for one expert is
-        // then added twice, in order
+        // lane i: the i-th pair's token; pairs come in order, so a token that is
+        // listed twice for one expert is the next one's too
+        const int tok = (int)((uint32_t)mine * g.kinv >> 16), next = __shfl(tok, (lane + 1) & 63);
+        if (!__any(lane + 1 < rows && tok == next)) {
+          // all rows side by side (T = 64, N = 8944, K = 2176 in 4 bits: 16.5 us, one
+          // row after another 24.1)
+          float old[NT][MT][4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = 16 * m + 4 * (lane >> 4) + j;
+              const int at = __shfl(tok, row & 63) * C + (lane & 15);
+#pragma unroll
+              for (int b = 0; b < NT; ++b) old[b][m][j] = row < rows ? y[at + 16 * b] : 0.f;
+            }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = 16 * m + 4 * (lane >> 4) + j;
+              const int at = __shfl(tok, row & 63) * C + (lane & 15);
+              const float f = __shfl(wt, row & 63);
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                float v = acc[b][m][j];
+                if constexpr (HALVES) v += __shfl_xor(v, 4 * XR);  // row + XR: what A's rounding left
+                if (row < rows) y[at + 16 * b] = fmaf(f, v, old[b][m][j]);
+              }
+            }
+          continue;
+        }
+        // one row at a time: the token's rows are added in order
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll 1
