@@ -585,7 +585,7 @@ struct Walk {
 // from item to item: while one is finished, the loads of the next are in flight.
 // Bound by HBM where there is enough to read: E = 64, T = 16, k = 8, D = 2048,
 // H = 1408, bf16: 93 us for the 55 or so experts that occur, 651 MB, 7.0 TB/s; the
-// 64 rows of E = 8, T = 64, D = 4096, H = 11008 271 us, 5.3 TB/s, LDS reads of the
+// 64 rows of E = 8, T = 64, D = 4096, H = 11008 266 us, 5.4 TB/s, LDS reads of the
 // token rows being on the way. One token of E = 8, D = 1024, H = 2816 (23 MB) is
 // 9 us: start, a first load's latency and the reduction. In 4 bits (E = 64, T = 8)
 // 31 us, 4.1 TB/s, where widening the codes is half of the wave's instructions.
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 // XR .. 2 XR - 1 of the token operand, which repeats nothing then: no more
 // matrix instructions than with one. Measured where few_gateup was: 51 us for
 // 326 MB (6.3 TB/s), 149 us (4.8 TB/s), 8.7 us for 11.5 MB, and 22 us in 4 bits.
-// W4, T = 33, N = 11008, K = 4096, g = 64, fp16: 20.8 us, 25 MB: bound by the waves'
+// W4, T = 33, N = 11008, K = 4096, g = 64, fp16: 19.0 us, 25 MB: bound by the waves'
 // instructions (codes to widen, LDS reads of the tokens, a scale per group and
 // output) on the 172 of 256 CUs that have a tile of 64 columns.
 template <class E, int FMT, int NT, int XR, int NW, int SH, int RING, int TC, bool HALVES>
