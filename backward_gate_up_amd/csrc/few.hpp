@@ -717,8 +717,8 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
         float gate = 0.f, up = 0.f;
 #pragma unroll
         for (int v = 0; v < NW; ++v) {
-          gate += red[(v * NT + 2 * b) * MT * 256 + at];
-          up += red[(v * NT + 2 * b + 1) * MT * 256 + at];
+          gate += red[(v * NT + (PLAIN ? b : 2 * b)) * MT * 256 + at];
+          if constexpr (!PLAIN) up += red[(v * NT + 2 * b + 1) * MT * 256 + at];
         }
         const int pair = use.pair(row), h = row0 + 16 * b + col;
         if (row < n && h < g.N) store(pair, h, gate, up);
