@@ -1020,6 +1020,7 @@ struct BlockPlan {
 };
 static inline BlockPlan block_plan(const Shape& f, int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  if (T == 0) return BlockPlan{};  // no tiles
   BlockPlan p;
   p.down = down_shape(f, T, D);
   p.n_ctr = p.down.splits > 1 ? (int)((D + p.down.cols - 1) / p.down.cols * ((T + kChunk - 1) / kChunk)) : 0;

@@ -4,13 +4,19 @@ tests/test_serve.py: a result of one product carries one rounding of half a step
 one of two products two, and 1e-5 for the fp32 sums.
 """
 
+import os
+import subprocess
+import sys
+
 import pytest
+import torch
 
 import backward_gate_up_amd as m
 from tests._util import assert_local, banner, f64
-from tests.test_serve import DT, bound, cuda, gen, make_w4, randn, ref_w4
+from tests.test_serve import DT, bound, cuda, expert_weights, gen, make_w4, randn, ref_w4
 
 gpu = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def check_linear(T, N, K, group, zeros, dt):
@@ -30,3 +36,50 @@ def test_w4_linear_many_columns(T, N, K, group, dt):
     """Tiles of 32 columns (more than 24544 on 256 CUs), N that ends in either half."""
     banner(f"w4_linear {dt} T={T} N={N} K={K} g={group}")
     check_linear(T, N, K, group, T % 2 == 0, dt)
+
+
+# ---- calls without a token ----------------------------------------------------------
+
+EMPTY_CALLS = {
+    "moe_experts": "L.swiglu_mlp_moe_experts(*at[:8], 1 << 30, 0, 64, 128, 8, 2, 0, None)",
+    "moe_infer": "L.swiglu_mlp_moe_infer(at[0], at[8], *at[3:8], 1 << 30, 0, 64, 128, 8, 2, 1, 0, None)",
+    "moe_experts, NULL": "L.swiglu_mlp_moe_experts(None, None, None, *at[3:6], None, None, 0, 0, 64, 128, 8, 2, 0, None)",
+    "moe_experts_w4": "L.swiglu_mlp_moe_experts_w4(*at[:3], *w(8), at[6], at[7], 1 << 30, 0, 2, 0, None)",
+    "moe_infer_w4": "L.swiglu_mlp_moe_infer_w4(at[0], at[8], *w(8), at[6], at[7], 1 << 30, 0, 2, 1, 0, None)",
+    "w4_infer": "L.swiglu_mlp_w4_infer(at[0], *w(1), at[6], at[7], 1 << 30, 0, 0, None)",
+    "w4_infer, NULL": "L.swiglu_mlp_w4_infer(None, *w(1), None, None, 0, 0, 0, None)",
+    "w4_linear": "L.swiglu_mlp_w4_linear(at[0], w(1)[0], at[6], None, 0, 0, 0, None)",
+    "moe_route": "L.swiglu_mlp_moe_route(at[0], at[8], at[1], at[2], None, 0, 0, 64, 8, 2, 1, 0, None)",
+}
+
+
+@pytest.mark.parametrize("call", EMPTY_CALLS)
+def test_no_tokens_at_the_c_entries(call):
+    """T = 0 passes the argument checks and does nothing (a process of its own:
+    addresses are made up, and nothing may end the process)."""
+    code = ("import ctypes\nfrom backward_gate_up_amd import _lib\nL = _lib.lib()\n"
+            "at = [(1 << 40) + (i << 34) for i in range(9)]\n"
+            "w4 = lambda i, E, N, K: ctypes.byref(_lib.W4(at[i], E, N, K, 32, 0))\n"
+            "w = lambda E: [w4(3, E, 64, 128), w4(4, E, 64, 128), w4(5, E, 128, 64)]\n"
+            f"print('status', {EMPTY_CALLS[call]})\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120, cwd=ROOT)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+    assert int(r.stdout.split("status")[1]) in (0, 7), r.stdout  # 7: no gfx950 here
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_no_tokens(dt):
+    banner(f"no tokens {dt}")
+    g, E, D, H, k = gen(1), 4, 64, 96, 2
+    x, wr = torch.empty((0, D), dtype=DT[dt], device="cuda"), randn(g, (E, D), 1, DT[dt]).cuda()
+    w = cuda(expert_weights(g, E, D, H, DT[dt]))
+    p, ids = m.moe_route(x, wr, k)
+    assert p.shape == ids.shape == (0, k)
+    assert m.moe_experts(x, p, ids, *w).shape == m.moe_infer(x, wr, *w, k).shape == (0, D)
+    if dt == "fp32":
+        return
+    w4 = [m.W4Weight.quantize(t, 32) for t in w]
+    assert m.moe_experts(x, p, ids, *w4).shape == m.moe_infer(x, wr, *w4, k).shape == (0, D)
+    dense = [m.W4Weight.quantize(t[0], 32) for t in w]
+    assert m.infer_w4(x, *dense).shape == (0, D) and m.w4_linear(x, dense[0]).shape == (0, H)
