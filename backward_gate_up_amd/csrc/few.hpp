@@ -578,6 +578,12 @@ struct Walk {
   __device__ __forceinline__ int pair(int i) const { return __shfl(p.pair, ((first & 63) + i) & 63); }
 };
 
+// The largest finite value of a 16-bit type (A's two parts; fp32 has one).
+template <class E>
+__device__ __forceinline__ constexpr float largest() {
+  return std::is_same<E, Bf16>::value ? 0x1.fep127f : 65504.f;
+}
+
 // ---- gate/up ------------------------------------------------------------------
 // An item is a tile of hidden columns of one pass; the workgroup takes a run of
 // items. SH = 1: 16 HB columns, the waves take equal parts of K and their sums
@@ -675,11 +681,20 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
   // those; with more tokens it stays out.
   auto store = [&](int pair, int h, float gate, float up) {
     const float a = PLAIN ? gate : gate * sigmoid_f32<E>(gate) * up;
-    const typename E::elem hi = E::from_f32(a);
     const int64_t p = (int64_t)t0 * g.k + pair;
     typename E::elem* out = (typename E::elem*)g.out + (g.halves ? 2 * p : p) * g.N + h;
+    if (!g.halves) {
+      out[0] = E::from_f32(a);
+      return;
+    }
+    // Past the type's range (fp16: 65504) the first part is its largest value, and
+    // the second holds the rest up to as much again; an infinity leaves nothing
+    // (Inf - Inf would be NaN).
+    const float size = fabsf(a);
+    const bool inf = size == __builtin_inff();
+    const typename E::elem hi = E::from_f32(size > largest<E>() && !inf ? copysignf(largest<E>(), a) : a);
     out[0] = hi;
-    if (g.halves) out[g.N] = E::from_f32(a - E::to_f32(hi));
+    out[g.N] = E::from_f32(inf ? 0.f : a - E::to_f32(hi));
   };
   use.expert(nth, lane);
   while (true) {

@@ -8,12 +8,13 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 import backward_gate_up_amd as m
 from tests._util import assert_local, banner, f64
-from tests.test_serve import DT, bound, cuda, expert_weights, gen, make_w4, randn, ref_w4
+from tests.test_serve import DT, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_w4
 
 gpu = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -83,3 +84,59 @@ def test_no_tokens(dt):
     assert m.moe_experts(x, p, ids, *w4).shape == m.moe_infer(x, wr, *w4, k).shape == (0, D)
     dense = [m.W4Weight.quantize(t[0], 32) for t in w]
     assert m.infer_w4(x, *dense).shape == (0, D) and m.w4_linear(x, dense[0]).shape == (0, H)
+
+
+# ---- values past the storage type's range -------------------------------------------
+
+
+def large_block(D, H, dt, a):
+    """Weights of one expert and a token for which every A = SiLU(g) u is about
+    `a` or -a: g = u's magnitude = sqrt(a), and down weights of both signs."""
+    g = gen(D + H)
+    x = torch.ones(1, D)
+    wg = torch.full((1, H, D), a ** 0.5 / D)
+    wu = wg * torch.where(torch.rand((1, H, 1), generator=g) < 0.5, -1.0, 1.0)
+    wd = torch.randn((1, D, H), generator=g) / 64
+    return tuple(t.to(dt) for t in (x, wg, wu, wd))
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 5, 8])
+@pytest.mark.parametrize("a", [4e4, 6.55e4, 9e4, 1.3e5])
+def test_hidden_values_past_the_range_of_fp16(T, a):
+    """With 8 or fewer token rows A is held in two parts: values to twice the
+    type's largest come out as the finite results they are."""
+    banner(f"large A T={T} a={a}")
+    D, H, dt = 128, 200, torch.float16
+    x, wg, wu, wd = large_block(D, H, dt, a)
+    x = x.repeat(T, 1)
+    p, ids = torch.ones(T, 1), torch.zeros((T, 1), dtype=torch.int32)
+    y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *cuda((wg, wu, wd)))
+    ref, got = ref_block(f64(x), *(f64(t[0]) for t in (wg, wu, wd))), f64(y)
+    past = np.abs(ref) >= 65520  # results that are past the range themselves round to infinities
+    assert np.array_equal(got[past], np.sign(ref[past]) * np.inf)
+    got[past] = ref[past] = 0
+    assert_local(got, ref, bound(dt, 2), ("large", T, a))
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 8, 20, 40])
+def test_infinite_hidden_values(T, dt):
+    """A token with an infinity, whose every A is infinite: y is the infinity of
+    the definition's sign in each column of one sign, NaN where both meet, at
+    every number of tokens."""
+    banner(f"infinite A {dt} T={T}")
+    D, H = 128, 200
+    x, wg, wu, wd = large_block(D, H, DT[dt], 100)
+    x = x.repeat(T, 1)
+    x[0, 3] = float("inf")
+    wu, wd = wu.abs(), wd.abs() + 2.0 ** -6
+    wd[0, 1::3] *= -1
+    wd[0, 2::3, ::2] *= -1
+    p, ids = torch.ones(T, 1), torch.zeros((T, 1), dtype=torch.int32)
+    y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *cuda((wg, wu, wd))).float().cpu()
+    assert (y[0, 0::3] == float("inf")).all() and (y[0, 1::3] == -float("inf")).all() and y[0, 2::3].isnan().all()
+    ref = ref_block(f64(x)[1:], *(f64(t[0]) for t in (wg, wu, wd)))
+    if T > 1:
+        assert_local(f64(y)[1:], ref, bound(DT[dt], 2), ("rest", T))
