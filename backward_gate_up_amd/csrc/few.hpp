@@ -51,13 +51,12 @@ struct Weight {
 struct Args {
   const char* x;     // gate/up: [T, K] tokens; down: [T * k, K] pairs (dense: [T, K])
   Weight w0, w1;     // gate/up: gate and up; down: w0
-  char* out;         // gate/up: A [T * k, N]; down: y [T, N]
+  char* out;         // gate/up: A [T * k, N] (in two parts [T * k][2][N]); down: y [T, N]
   const int* ids;    // [T, k]; nullptr: dense
   const float* wts;  // [T, k]; nullptr: dense
   int T, k, E, N, K;
   uint32_t kinv;     // ceil(65536 / k): p / k = p * kinv >> 16 for a chunk's p < 2048, k <= 32
   int zeros;         // 4 bits: the weights have zero points (else every one is 8)
-  int halves;        // gate/up: A as [T * k][2][N], the rounded value and what it left
   int once;          // rows of whole 128-byte lines, read once
   int splits;        // down: workgroups per output tile
   float* partial;    // down, splits > 1: [splits][T][N]
@@ -291,6 +290,11 @@ struct W4Stream {
     const int len = row0 < N ? stages(kb >> 1) * rec : 0;
     rw[n] = scalar_rsrc(rsrc_words(wt.w + (int64_t)e * wt.expert + (int64_t)(row0 >> 4) * len, len));
   }
+  // the same block for the compiler's loads
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t records(const Weight& wt, int e, int row0, int N) const {
+    const int len = row0 < N ? stages(kb >> 1) * rec : 0;
+    return make_rsrc(wt.w + (int64_t)e * wt.expert + (int64_t)(row0 >> 4) * len, len);
+  }
   static __device__ __forceinline__ uint32_t chunk(int r, int lane) { return ((lane & 15) ^ (r & 15)) << 4; }
   __device__ __forceinline__ void token_row(int j, uint32_t row, int lane) {
     x_off[j] = row == kOOB ? kOOB : row + chunk(x_row(j, lane), lane);
@@ -348,6 +352,80 @@ struct W4Stream {
       v[i] = __builtin_bit_cast(uint32_t, d);
     }
     return v;
+  }
+  // Where the offset cannot be taken off a sum: x (OFF + q) and (OFF + z) x are
+  // infinities of one sign where x is one (their difference NaN), and large finite x
+  // (bf16, from about 1e34 on) overflow in both. Either leaves a sum that is not finite,
+  // and those are formed again from x and s (q - z), in fp64, for one token row at a
+  // time: lane l takes row l % 16 of the weights and the K that its codes have. Other
+  // rows keep their values. Stages [s0, s1); block(n): the record descriptor of weight
+  // block n; row(i): where the tokens' buffer has operand row i, or kOOB. Costs
+  // nothing but the test where every sum is finite, and a pass over the
+  // codes for each row and block where one is not.
+  template <class Block, class Row>
+  __device__ __forceinline__ void settle(f32x4_t (&acc)[NT][MT], int s0, int s1, int lane, Block&& block, Row&& row) const {
+    if constexpr (kExact) return;
+    f32x4_t all{};  // finite only if every sum is
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) all += acc[n][m];
+    const bool bad = !(fabsf((all[0] + all[1]) + (all[2] + all[3])) < __builtin_inff());
+    if (__builtin_expect(!__any(bad), 1)) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const __amdgpu_buffer_rsrc_t w = block(n);
+#pragma unroll 1
+      for (int at = 0; at < 4 * MT; ++at) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * MT; ++i)
+          if (at == i) v = acc[n][i / 4][i % 4];
+        for (uint64_t left = __ballot(!(fabsf(v) < __builtin_inff())); left;) {
+          const int c = (__ffsll((unsigned long long)left) - 1) >> 4;  // operand row i is on lanes 16 c .. 16 c + 15
+          const int i = 16 * (at >> 2) + 4 * c + (at & 3);
+          double sum = again(w, row(i), s0, s1, lane);
+          sum += __shfl_xor(sum, 16);
+          sum += __shfl_xor(sum, 32);
+          if ((lane >> 4) == c && !(fabsf(v) < __builtin_inff())) v = (float)sum;
+          left &= ~(0xffffull << (16 * c));
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * MT; ++i)
+          if (at == i) acc[n][i / 4][i % 4] = v;
+      }
+    }
+  }
+  // The lane's part of one token row's product with weight row l % 16.
+  __device__ __forceinline__ double again(__amdgpu_buffer_rsrc_t w, uint32_t row, int s0, int s1, int lane) const {
+    const int r = lane & 15, c = lane >> 4;
+    // rx's base and size, for the compiler's loads
+    const __amdgpu_buffer_rsrc_t x = make_rsrc32((const void*)((uint64_t)(uint32_t)rx[0] | (uint64_t)(uint32_t)rx[1] << 32), rx[2]);
+    typedef typename E::elem vec8 __attribute__((ext_vector_type(8)));
+    double sum = 0.0;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {
+      const uint32_t at = (uint32_t)s * (uint32_t)rec;
+      const u32x4_t code = load16(w, at + lane * 16);
+      const uint32_t zs =
+          zeros ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w, at + 1024 + 32 * GP + r * 2, 0, 0) : 0x8888u;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int k = s * 128 + 32 * d + 8 * c;  // of the row; K is a multiple of 32
+        if (2 * k >= kb || row == kOOB) continue;
+        const int q = d * GP / 4;
+        const uint16_t sb = __builtin_amdgcn_raw_buffer_load_b16(w, at + 1024 + (r * GP + q) * 2, 0, 0);
+        const float scale = E::to_f32(__builtin_bit_cast(typename E::elem, sb)), z = (float)((zs >> (4 * q)) & 15u);
+        const vec8 xv = __builtin_bit_cast(vec8, load16(x, row + 2 * (uint32_t)k));
+        const uint32_t v = code[d];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          sum = fma((double)E::to_f32(xv[2 * p]), (double)(scale * ((float)((v >> (4 * p)) & 15u) - z)), sum);
+          sum = fma((double)E::to_f32(xv[2 * p + 1]), (double)(scale * ((float)((v >> (16 + 4 * p)) & 15u) - z)), sum);
+        }
+      }
+    }
+    return sum;
   }
   __device__ __forceinline__ void compute(const char* slot, f32x4_t (&acc)[NT][MT], int lane) const {
     const int r = lane & 15, c = lane >> 4, rr = XR < 16 ? r & (XR - 1) : r;
@@ -578,6 +656,9 @@ struct Walk {
   __device__ __forceinline__ int pair(int i) const { return __shfl(p.pair, ((first & 63) + i) & 63); }
 };
 
+// Whether A is held in two parts (few_down): at 8 token rows per stage, in 4 bits 4.
+static __host__ __device__ constexpr bool halves(int rows, size_t e) { return rows <= 8 && e == 2; }
+
 // The largest finite value of a 16-bit type (A's two parts; fp32 has one).
 template <class E>
 __device__ __forceinline__ constexpr float largest() {
@@ -600,6 +681,7 @@ __device__ __forceinline__ constexpr float largest() {
 template <class E, int FMT, int HB, int XR, int NW, int SH, int RING, bool PLAIN>
 __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 : 2)) few_gateup(const Args g) {
   constexpr int NT = PLAIN ? HB : 2 * HB, COLS = 16 * HB * SH;
+  constexpr bool HALVES = !PLAIN && halves(XR, E::kBytes);
   using S = typename StreamOf<E, FMT, NT, XR, SH, (SH > 1 ? RING : RING / NW)>::type;
   constexpr int MT = S::MT;
   __shared__ __attribute__((aligned(1024))) char lds[RING];
@@ -682,8 +764,8 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
   auto store = [&](int pair, int h, float gate, float up) {
     const float a = PLAIN ? gate : gate * sigmoid_f32<E>(gate) * up;
     const int64_t p = (int64_t)t0 * g.k + pair;
-    typename E::elem* out = (typename E::elem*)g.out + (g.halves ? 2 * p : p) * g.N + h;
-    if (!g.halves) {
+    typename E::elem* out = (typename E::elem*)g.out + (HALVES ? 2 * p : p) * g.N + h;
+    if constexpr (!HALVES) {
       out[0] = E::from_f32(a);
       return;
     }
@@ -702,6 +784,13 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 #pragma unroll 1
     for (int s = 0; s < per; ++s) r.step(st, acc, lane, issue);
     const int n = use.rows(XR), row0 = tile * COLS + wcol;
+    if constexpr (FMT != 0)
+      st.settle(
+          acc, s0, s1, lane,
+          [&](int b) {
+            return st.records(PLAIN || b % 2 == 0 ? g.w0 : g.w1, use.e, row0 + 16 * (PLAIN ? b : b / 2), g.N);
+          },
+          [&](int i) { return i < n ? ((use.pair(i) * g.kinv) >> 16) * (uint32_t)(g.K * E::kBytes) : kOOB; });
     if constexpr (SH > 1) {
       // the wave has all of K: lane -> hidden column l % 16, token rows 4 (l / 16) + j
 #pragma unroll
@@ -840,6 +929,15 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
         f32x4_t acc[NT][MT] = {};
 #pragma unroll 1
         for (int s = 0; s < count; ++s) r.step(st, acc, lane, issue);
+        if constexpr (FMT != 0)
+          st.settle(
+              acc, begin_of(n), end_of(n), lane,
+              [&](int b) { return st.records(g.w0, use.e, col0 + 16 * b, g.N); },
+              [&](int i) {
+                return i < PARTS * XR && i % XR < rows
+                           ? (uint32_t)use.pair(i % XR) * row_bytes + (uint32_t)(i / XR * g.K) * E::kBytes
+                           : kOOB;
+              });
         // lane i: the i-th pair's token; pairs come in order, so a token that is
         // listed twice for one expert is the next one's too
         const int tok = (int)((uint32_t)mine * g.kinv >> 16), next = __shfl(tok, (lane + 1) & 63);
@@ -1031,7 +1129,6 @@ struct BlockPlan {
   size_t ctr, partial, total;
   DownShape down;
   int n_ctr;
-  bool halves;
 };
 static inline BlockPlan block_plan(const Shape& f, int64_t T, int64_t D, int64_t H, int64_t k, size_t e) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
@@ -1039,8 +1136,7 @@ static inline BlockPlan block_plan(const Shape& f, int64_t T, int64_t D, int64_t
   BlockPlan p;
   p.down = down_shape(f, T, D);
   p.n_ctr = p.down.splits > 1 ? (int)((D + p.down.cols - 1) / p.down.cols * ((T + kChunk - 1) / kChunk)) : 0;
-  p.halves = f.rows == 8 && e == 2;
-  p.ctr = up((size_t)T * k * H * e * (p.halves ? 2 : 1));
+  p.ctr = up((size_t)T * k * H * e * (halves(f.rows, e) ? 2 : 1));
   p.partial = p.ctr + up((size_t)p.n_ctr * 4);
   p.total = p.partial + (p.down.splits > 1 ? up((size_t)p.down.splits * T * D * 4) : 0);
   return p;
@@ -1091,7 +1187,7 @@ static int launch_down(const Args& g, hipStream_t s) {
 
 static inline Args args_of(const Call& c, const char* x, int64_t N, int64_t K, char* out) {
   return Args{x, c.wd, c.wd, out, c.ids, c.wts, (int)c.T, c.k, c.E, (int)N, (int)K, (65535u + c.k) / c.k,
-              c.zeros, 0, 0, 1, nullptr, nullptr, 0};
+              c.zeros, 0, 1, nullptr, nullptr, 0};
 }
 template <class E, int FMT, int XR, bool HALVES>
 static int down_own(const Args& g, int waves, hipStream_t s) {
@@ -1104,7 +1200,7 @@ static int down_own(const Args& g, int waves, hipStream_t s) {
 }
 template <class E, int FMT>
 static int down_for(const Args& g, const Shape& f, int waves, hipStream_t s) {
-  if (f.rows == 8) return down_own<E, FMT, FMT ? 4 : 8, E::kBytes == 2>(g, waves, s);
+  if (f.rows == 8) return down_own<E, FMT, FMT ? 4 : 8, halves(8, E::kBytes)>(g, waves, s);
   if (f.rows == 16) return down_own<E, FMT, 16, false>(g, waves, s);
   if constexpr (FMT != 0) {
     if (f.rows == 32) return launch_down<E, FMT, 32, 8, 8, kChunk, false>(g, s);
@@ -1183,7 +1279,6 @@ int run_block(const Call& c) {
   Args g = args_of(c, c.x, c.H, c.D, c.ws);
   g.w0 = c.wg;
   g.w1 = c.wu;
-  g.halves = p.halves;
   g.once = c.D * E::kBytes % 128 == 0;
   g.ctr = (unsigned*)(c.ws + p.ctr);
   g.n_ctr = p.n_ctr;

@@ -140,3 +140,94 @@ def test_infinite_hidden_values(T, dt):
     ref = ref_block(f64(x)[1:], *(f64(t[0]) for t in (wg, wu, wd)))
     if T > 1:
         assert_local(f64(y)[1:], ref, bound(DT[dt], 2), ("rest", T))
+
+
+def same_values(got, ref, tol):
+    """NaN and infinities in the same places with the same signs, the rest within tol of the largest."""
+    fin = np.isfinite(ref)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(got[~fin & ~np.isnan(ref)], ref[~fin & ~np.isnan(ref)])
+    if fin.any():
+        assert np.abs(got[fin] - ref[fin]).max() <= tol * np.abs(ref[fin]).max()
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 4, 5, 16, 17, 40, 70])
+@pytest.mark.parametrize("N,K,group,zeros", [(72, 416, 32, True), (264, 1152, 128, False), (136, 6272, 64, True)])
+def test_w4_linear_infinite_and_large_tokens(T, N, K, group, zeros, dt):
+    """An infinity in x gives s (q - z) times it, NaN where q = z, and large values
+    the finite results they have, at every number of tokens; other tokens keep
+    their bits."""
+    banner(f"w4 inf {dt} T={T} N={N} K={K}")
+    g = gen(N + K)
+    raw = make_w4(g, (N, K), group, zeros, DT[dt])
+    w = m.w4_pack(*cuda(raw))
+    x = randn(g, (T, K), 1, DT[dt])
+    clean = m.w4_linear(x.cuda(), w)
+    big = 3e37 if dt == "bf16" else 6e4
+    for t, what in ((0, "inf"), (T // 2, "large"), (T - 1, "-inf")):
+        z = x.clone()
+        if what == "large":
+            z[t, 5], z[t, K - 3] = big, -big
+        else:
+            z[t, K // 2 + 1] = float(what)
+        y = m.w4_linear(z.cuda(), w)
+        with np.errstate(invalid="ignore"):
+            ref = (f64(z)[t] * ref_w4(*raw)).sum(1)
+        same_values(f64(y)[t], ref, bound(DT[dt], 1))
+        rest = [i for i in range(T) if i != t]
+        assert torch.equal(y[rest], clean[rest])
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,D,H,group", [(1, 256, 128, 64), (4, 6272, 64, 64), (16, 160, 96, 32), (20, 64, 128, 32),
+                                         (40, 64, 128, 64)])
+def test_infer_w4_infinite_tokens(T, D, H, group, dt):
+    """Infinite gate and up values, and infinite A, through the 4-bit block: no zero
+    weights, signs such that nothing cancels."""
+    banner(f"infer_w4 inf {dt} T={T} D={D} H={H}")
+    g = gen(D)
+    raw = [make_w4(g, s, group, False, DT[dt]) for s in ((H, D), (H, D), (D, H))]
+    for i, (codes, _, _) in enumerate(raw):  # gate above zero, up too; down rows of one sign
+        high, low = codes | 0x99, codes & 0x77  # q >= 9, q <= 7: weights above and below zero
+        codes[:] = high
+        if i == 2:
+            codes[1::2] = low[1::2]
+    w = [m.w4_pack(*cuda(r)) for r in raw]
+    x = randn(g, (T, D), 1, DT[dt])
+    clean = m.infer_w4(x.cuda(), *w)
+    z = x.clone()
+    z[T // 2, 7] = float("inf")
+    y = m.infer_w4(z.cuda(), *w).float().cpu()
+    assert (y[T // 2, 0::2] == float("inf")).all() and (y[T // 2, 1::2] == -float("inf")).all()
+    rest = [i for i in range(T) if i != T // 2]
+    assert torch.equal(y[rest], clean.float().cpu()[rest])
+    z[T // 2, 7] = -float("inf")  # SiLU(-inf) = -inf / inf
+    assert m.infer_w4(z.cuda(), *w)[T // 2].isnan().all()
+
+
+@gpu
+@pytest.mark.parametrize("T,E,k", [(1, 4, 2), (24, 4, 2), (64, 6, 3), (60, 48, 12)])
+def test_moe_w4_infinite_tokens(T, E, k):
+    banner(f"moe_w4 inf T={T} E={E} k={k}")
+    D, H, group, dt = 128, 256, 64, torch.bfloat16
+    g = gen(T + E)
+    raw = [make_w4(g, s, group, False, dt) for s in ((E, H, D), (E, H, D), (E, D, H))]
+    for i, (codes, _, _) in enumerate(raw):
+        high, low = codes | 0x99, codes & 0x77
+        codes[:] = high
+        if i == 2:
+            codes[:, 1::2] = low[:, 1::2]
+    w = [m.w4_pack(*cuda(r)) for r in raw]
+    x = randn(g, (T, D), 1, dt)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    p = torch.rand((T, k), generator=g) + 0.1
+    clean = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *w)
+    z = x.clone()
+    z[T // 3, 90] = float("inf")
+    y = m.moe_experts(z.cuda(), p.cuda(), ids.cuda(), *w).float().cpu()
+    assert (y[T // 3, 0::2] == float("inf")).all() and (y[T // 3, 1::2] == -float("inf")).all()
+    rest = [i for i in range(T) if i != T // 3]
+    assert torch.equal(y[rest], clean.float().cpu()[rest])
