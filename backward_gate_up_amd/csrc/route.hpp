@@ -316,6 +316,19 @@ __global__ void __launch_bounds__(kPartWaves * 64, 2) route_logits(const Args g)
   if (col == 0 && blockIdx.x == 0 && row < tc) px[(int64_t)blockIdx.y * g.T + t] = vx;
 }
 
+// Whether a row holds nothing but zeros; one wave, the same on every lane.
+template <class E>
+__device__ __forceinline__ bool all_zero(const char* row, int kb, int lane) {
+  const __amdgpu_buffer_rsrc_t r = make_rsrc32(row, kb);
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (int o = lane * 16; o - lane * 16 < kb; o += 1024) {
+    const u32x4_t v = few::load16(r, o);
+    bits |= v[0] | v[1] | v[2] | v[3];
+  }
+  return !__any((bits & (E::kBytes == 2 ? 0x7fff7fffu : 0x7fffffffu)) != 0u);
+}
+
 // Second launch: one wave per token. T = 8192, E = 128, k = 8, D = 4096: 15 us, bound
 // by its instructions (the wave-wide maxima of k rounds); 3.7 us at T = 1.
 template <class E, int NPL>
@@ -357,7 +370,12 @@ __global__ void __launch_bounds__(256, NPL <= 4 ? 8 : 2) route_pick(const Args g
   // not negative, so the bits order as the values do
   wmax = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, wmax)));
   const int parts = g.splits * (g.many ? 1 : kPartWaves), stages = (g.D * E::kBytes + 127) >> 7;
-  const float bound = gamma_of<E>((stages + parts - 1) / parts, parts) * sqrtf(x2) * sqrtf(wmax);
+  // Squares and products below 2^-126 vanish, which counts as up to 2^-126 each; the
+  // logits of a token of zeros (padding) are exact.
+  const float least = (float)g.D * 0x1p-125f;
+  const bool zeros = __builtin_expect(x2 == 0.f, 0) && all_zero<E>(g.x + (int64_t)t * g.D * E::kBytes, g.D * E::kBytes, lane);
+  const float bound =
+      zeros ? 0.f : gamma_of<E>((stages + parts - 1) / parts, parts) * sqrtf(x2 + least) * sqrtf(wmax + least) + least;
   choose<E, NPL>(g, t, l, bound, lane);
 }
 

@@ -14,7 +14,7 @@ import torch
 
 import backward_gate_up_amd as m
 from tests._util import assert_local, banner, f64
-from tests.test_serve import DT, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_w4
+from tests.test_serve import DT, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_route, ref_w4
 
 gpu = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -231,3 +231,42 @@ def test_moe_w4_infinite_tokens(T, E, k):
     assert (y[T // 3, 0::2] == float("inf")).all() and (y[T // 3, 1::2] == -float("inf")).all()
     rest = [i for i in range(T) if i != T // 3]
     assert torch.equal(y[rest], clean.float().cpu()[rest])
+
+
+# ---- the router's order for very small numbers ----------------------------------------
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [3, 12, 600])
+@pytest.mark.parametrize("sx,sw", [(-80, 0), (0, -80), (-60, -60), (-78, -40), (-100, 20)])
+def test_route_order_of_small_numbers(T, sx, sw, dt):
+    """Experts that differ in the last digits of a long sum, with tokens or weights
+    whose squares are below fp32's range: the order is the exact logits'."""
+    banner(f"route small T={T} 2^{sx} 2^{sw} {dt}")
+    D, E, k = 1024, 12, 5
+    g = gen(T)
+    x, base = torch.randn((T, D), generator=g), torch.randn((1, D), generator=g).repeat(E, 1)
+    base[:, 17] *= 1 + torch.arange(E).float()[torch.randperm(E, generator=g)] * 2.0 ** -6
+    x[:, 17] *= 2.0 ** -12
+    # powers of two change no digit (none falls below the smallest normal number)
+    x, wr = x.to(DT[dt]) * 2.0 ** sx, base.to(DT[dt]) * 2.0 ** sw
+    _, ids = m.moe_route(x.cuda(), wr.cuda(), k)
+    assert np.array_equal(ids.cpu().numpy(), ref_route(f64(x), f64(wr), k, True)[0])
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [3, 12, 600])
+def test_route_of_zeros(T, dt):
+    banner(f"route zeros T={T} {dt}")
+    D, E, k = 1000, 100, 6
+    g = gen(T)
+    x, wr = randn(g, (T, D), 1, DT[dt]), randn(g, (E, D), D ** -0.5, DT[dt])
+    x[1] = 0
+    x[2] = -0.0
+    p, ids = m.moe_route(x.cuda(), wr.cuda(), k, False)
+    assert (ids[1:3].cpu() == torch.arange(k)).all() and (p[1:3].cpu() - 0.01).abs().max() < 1e-8
+    assert np.array_equal(ids.cpu().numpy(), ref_route(f64(x), f64(wr), k, False)[0])
+    p, ids = m.moe_route(x.cuda(), torch.zeros_like(wr).cuda(), k, True)
+    assert (ids.cpu() == torch.arange(k)).all() and (p.cpu() - 1 / k).abs().max() < 1e-7
