@@ -111,6 +111,12 @@ class W4Weight:
 
     requires_grad = False
 
+    def __getstate__(self):  # the C structure holds an address: copies and loads make their own
+        return self.data, self.shape, self.group, self.has_zeros, self.dtype
+
+    def __setstate__(self, state):
+        self.__init__(*state)
+
     @classmethod
     def quantize(cls, w, group=128, zeros=False):
         """The nearest 4-bit weight of ``w`` under ``w4_quantize``'s rule."""
@@ -354,6 +360,12 @@ class _W4Module(torch.nn.Module):
         if data.data_ptr() != w._c.data:
             w = self._forms[name] = W4Weight(data, w.shape, w.group, w.has_zeros, w.dtype)
         return w
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        for name in self._forms:  # a move: the old buffers go
+            self._weight(name)
+        return self
 
 
 class SwiGLUMLPW4(_W4Module):

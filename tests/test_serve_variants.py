@@ -4,17 +4,24 @@ tests/test_serve.py: a result of one product carries one rounding of half a step
 one of two products two, and 1e-5 for the fp32 sums.
 """
 
+import copy
+import gc
+import io
 import os
+import pickle
 import subprocess
 import sys
+import weakref
 
 import numpy as np
 import pytest
 import torch
 
 import backward_gate_up_amd as m
+from backward_gate_up_amd import _lib
 from tests._util import assert_local, banner, f64
-from tests.test_serve import DT, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_route, ref_w4
+from tests.test_serve import (DT, _moe_config, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_route,
+                              ref_w4)
 
 gpu = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -270,3 +277,57 @@ def test_route_of_zeros(T, dt):
     assert np.array_equal(ids.cpu().numpy(), ref_route(f64(x), f64(wr), k, False)[0])
     p, ids = m.moe_route(x.cuda(), torch.zeros_like(wr).cuda(), k, True)
     assert (ids.cpu() == torch.arange(k)).all() and (p.cpu() - 1 / k).abs().max() < 1e-7
+
+
+# ---- 4-bit weights and modules as objects (host) ---------------------------------------
+
+
+def host_w4(g, shape, group, zeros, dtype=torch.bfloat16):
+    """A 4-bit weight of random bytes in host memory, which no kernel reads."""
+    *lead, N, K = shape
+    n = _lib.lib().swiglu_mlp_w4_bytes(lead[0] if lead else 1, N, K, group, zeros)
+    return m.W4Weight(torch.randint(0, 256, (n,), generator=g, dtype=torch.uint8), shape, group, zeros, dtype)
+
+
+def host_moe(seed, group=32, zeros=False):
+    """SwiGLUMoE with 4-bit experts in host memory."""
+    mod = m.SwiGLUMoE(_moe_config())
+    for name in ("gate_proj", "up_proj", "down_proj"):
+        w = host_w4(gen(seed), getattr(mod, name).shape, group, zeros)
+        delattr(mod, name)
+        mod._keep(name, w)
+    return mod
+
+
+def same_w4(a, b):
+    form = lambda w: (w.shape, w.group, w.has_zeros, w.dtype, w.experts, w.device)  # noqa: E731
+    return form(a) == form(b) and torch.equal(a.data, b.data) and a._c.data == a.data.data_ptr()
+
+
+def test_w4_weights_can_be_copied_and_saved():
+    w = host_w4(gen(1), (3, 16, 128), 64, True, torch.float16)
+    for c in (copy.copy(w), copy.deepcopy(w), pickle.loads(pickle.dumps(w))):
+        assert same_w4(c, w) and (c._c.N, c._c.K, c._c.group, c._c.has_zeros) == (16, 128, 64, 1)
+    assert copy.deepcopy(w).data.data_ptr() != w.data.data_ptr()
+
+
+def test_modules_with_4_bit_weights_can_be_copied_and_saved():
+    mod = host_moe(2)
+    buf = io.BytesIO()
+    torch.save(mod, buf)
+    buf.seek(0)
+    for c in (copy.deepcopy(mod), torch.load(buf, weights_only=False)):  # our own file
+        assert set(c.state_dict()) == set(mod.state_dict())
+        for name in ("gate_proj", "up_proj", "down_proj"):
+            assert same_w4(c._weight(name), mod._weight(name))
+            assert c._weight(name).data is getattr(c, name)
+
+
+def test_modules_let_go_of_the_weights_they_replace():
+    """After a move the module holds no copy of the old buffers."""
+    mod = host_moe(3)
+    old = [weakref.ref(getattr(mod, n)) for n in ("gate_proj", "up_proj", "down_proj")]
+    mod._apply(lambda t: t.clone())
+    gc.collect()
+    assert all(r() is None for r in old)
+    assert mod._weight("up_proj").data is mod.up_proj
