@@ -349,11 +349,35 @@ def infer_w4(x, wg, wu, wd, y=None, workspace=None):
 
 class _W4Module(torch.nn.Module):
     """Keeps 4-bit weights as byte buffers, so that they follow the module to
-    another device and into its state dict, and hands them out as W4Weight."""
+    another device and into its state dict, and hands them out as W4Weight. Their
+    form (shape, group, zero points, type) stands in the state dict's metadata, and a
+    module that loads it takes that form, whatever it held before; a state dict
+    without metadata has to be of the module's own form."""
 
     def _keep(self, name, w):
+        if name in self._parameters:
+            del self._parameters[name]
         self.register_buffer(name, w.data)
         self._forms[name] = w
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        if self._forms and hasattr(destination, "_metadata"):
+            destination._metadata[prefix[:-1]]["w4"] = {n: (w.shape, w.group, w.has_zeros, w.dtype)
+                                                        for n, w in self._forms.items()}
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
+        forms = {n: f for n, f in (local_metadata.get("w4") or {}).items() if prefix + n in state_dict and hasattr(self, n)}
+        for name, (shape, group, zeros, _) in forms.items():
+            data, mine = state_dict[prefix + name], self._forms.get(name, getattr(self, name))
+            if tuple(mine.shape) != shape or data.numel() != _L.lib().swiglu_mlp_w4_bytes(*_w4_shape(shape, group), group, zeros):
+                error_msgs.append(f"4-bit weight {prefix + name} {list(shape)} of {data.numel()} bytes does not fit the "
+                                  f"module's {list(mine.shape)}")
+                return
+        for name, (shape, group, zeros, dtype) in forms.items():
+            room = torch.empty(state_dict[prefix + name].numel(), dtype=torch.uint8, device=getattr(self, name).device)
+            self._keep(name, W4Weight(room, shape, group, zeros, dtype))
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)
 
     def _weight(self, name):
         data, w = self._buffers[name], self._forms[name]

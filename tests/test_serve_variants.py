@@ -331,3 +331,54 @@ def test_modules_let_go_of_the_weights_they_replace():
     gc.collect()
     assert all(r() is None for r in old)
     assert mod._weight("up_proj").data is mod.up_proj
+
+
+def saved(state):
+    buf = io.BytesIO()
+    torch.save(state, buf)
+    buf.seek(0)
+    return torch.load(buf, weights_only=True)
+
+
+@pytest.mark.parametrize("assign", [False, True])
+def test_state_dicts_carry_the_form_of_4_bit_weights(assign):
+    """Group size, zero points and type travel in the state dict's metadata: a saved
+    module of 4-bit experts loads into a fresh one, inside a larger model too, and
+    over weights of another form of equally many bytes."""
+    src = host_moe(4, 32, True)
+    names = ("gate_proj", "up_proj", "down_proj")
+    assert set(src.state_dict()) == {"gate.weight", *names}
+    fresh = m.SwiGLUMoE(_moe_config())
+    fresh.load_state_dict(saved(src.state_dict()), assign=assign)
+    assert all(same_w4(fresh._weight(n), src._weight(n)) for n in names) and not list(fresh.named_parameters())[1:]
+    assert torch.equal(fresh.gate.weight, src.gate.weight)
+    model = torch.nn.ModuleDict({"layer": m.SwiGLUMoE(_moe_config())})
+    model.load_state_dict(saved(torch.nn.ModuleDict({"layer": src}).state_dict()), assign=assign)
+    assert all(same_w4(model["layer"]._weight(n), src._weight(n)) for n in names)
+    # 64 without and 128 with zero points take the same bytes
+    cfg = dict(hidden_size=128, moe_intermediate_size=256)
+    a, b = m.SwiGLUMoE(_moe_config(**cfg)), m.SwiGLUMoE(_moe_config(**cfg))
+    for mod, group, zeros in ((a, 64, False), (b, 128, True)):
+        for n in names:
+            w = host_w4(gen(group), getattr(mod, n).shape, group, zeros)
+            delattr(mod, n)
+            mod._keep(n, w)
+    assert a.up_proj.numel() == b.up_proj.numel()
+    b.load_state_dict(saved(a.state_dict()), assign=assign)
+    assert all(same_w4(b._weight(n), a._weight(n)) for n in names)
+
+
+def test_state_dicts_that_do_not_fit_are_refused():
+    src = host_moe(5)
+    other = m.SwiGLUMoE(_moe_config(moe_intermediate_size=128))
+    with pytest.raises(RuntimeError, match="4-bit weight"):
+        other.load_state_dict(src.state_dict())
+    assert other.gate_proj.shape == (6, 128, 64)  # as it was
+    with pytest.raises(RuntimeError, match="size mismatch"):
+        src.load_state_dict(m.SwiGLUMoE(_moe_config()).state_dict())
+    # without metadata (another file format) the module's own form is taken
+    again = host_moe(6)
+    again.load_state_dict(dict(src.state_dict()))
+    assert same_w4(again._weight("up_proj"), src._weight("up_proj"))
+    with pytest.raises(RuntimeError, match="size mismatch"):
+        m.SwiGLUMoE(_moe_config()).load_state_dict(dict(src.state_dict()))
