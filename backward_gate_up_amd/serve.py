@@ -394,15 +394,18 @@ class _W4Module(torch.nn.Module):
 
 class SwiGLUMLPW4(_W4Module):
     """The dense SwiGLU block with 4-bit weights, made from a ``SwiGLUMLP`` (or any
-    module with gate_proj, up_proj and down_proj). No gradients. Above
+    module with gate_proj, up_proj and down_proj layers without bias). No gradients. Above
     ``long_tokens`` tokens the weights are written back to rows and the no-grad
     path of 16-bit weights runs, which is bound by arithmetic then."""
 
     def __init__(self, mlp, group=128, zeros=False, long_tokens=512):
         super().__init__()
         self._forms, self.long_tokens = {}, long_tokens
-        for name in ("gate_proj", "up_proj", "down_proj"):
-            self._keep(name, W4Weight.quantize(getattr(mlp, name).weight, group, zeros))
+        layers = {name: getattr(mlp, name) for name in ("gate_proj", "up_proj", "down_proj")}
+        if any(getattr(layer, "bias", None) is not None for layer in layers.values()):
+            raise ValueError("SwiGLUMLPW4 has no bias terms")
+        for name, layer in layers.items():
+            self._keep(name, W4Weight.quantize(layer.weight, group, zeros))
 
     def forward(self, x):
         w = [self._weight(n) for n in ("gate_proj", "up_proj", "down_proj")]

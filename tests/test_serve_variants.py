@@ -382,3 +382,12 @@ def test_state_dicts_that_do_not_fit_are_refused():
     assert same_w4(again._weight("up_proj"), src._weight("up_proj"))
     with pytest.raises(RuntimeError, match="size mismatch"):
         m.SwiGLUMoE(_moe_config()).load_state_dict(dict(src.state_dict()))
+
+
+@pytest.mark.parametrize("biased", ["gate_proj", "up_proj", "down_proj", None])
+def test_biases_are_refused_in_the_4_bit_block(biased):
+    block = torch.nn.Module()
+    for name, (n_in, n_out) in (("gate_proj", (64, 96)), ("up_proj", (64, 96)), ("down_proj", (96, 64))):
+        setattr(block, name, torch.nn.Linear(n_in, n_out, bias=name == biased))
+    with pytest.raises(ValueError, match="bias" if biased else "GPU"):  # without one, as far as the device
+        m.SwiGLUMLPW4(block, 32)
