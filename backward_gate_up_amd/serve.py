@@ -461,9 +461,10 @@ class SwiGLUMoE(_W4Module):
 
     def quantize_(self, group=128, zeros=False):
         """Replaces the experts' weights by 4-bit ones (in place; not undone)."""
-        for name in ("gate_proj", "up_proj", "down_proj"):
-            w = W4Weight.quantize(getattr(self, name), group, zeros)
-            delattr(self, name)
+        if self._forms:
+            raise RuntimeError("the experts' weights are in 4 bits already")
+        names = ("gate_proj", "up_proj", "down_proj")
+        for name, w in zip(names, [W4Weight.quantize(getattr(self, n), group, zeros) for n in names]):
             self._keep(name, w)
         return self
 

@@ -391,3 +391,22 @@ def test_biases_are_refused_in_the_4_bit_block(biased):
         setattr(block, name, torch.nn.Linear(n_in, n_out, bias=name == biased))
     with pytest.raises(ValueError, match="bias" if biased else "GPU"):  # without one, as far as the device
         m.SwiGLUMLPW4(block, 32)
+
+
+def test_quantize_leaves_the_module_whole_when_it_is_refused(monkeypatch):
+    """A group that divides one weight's K and not another's: nothing is replaced."""
+    mod = m.SwiGLUMoE(_moe_config())  # K 64, 64 and 96
+    before = {n: p for n, p in mod.named_parameters()}
+
+    def quantize(w, group=128, zeros=False):
+        m.serve._w4_shape(tuple(w.shape), group)
+        return host_w4(gen(1), tuple(w.shape), group, zeros)
+
+    monkeypatch.setattr(m.W4Weight, "quantize", quantize)
+    with pytest.raises(ValueError, match="group"):
+        mod.quantize_(64)
+    assert not mod._forms and all(p is before[n] for n, p in mod.named_parameters()) and len(before) == 4
+    mod.quantize_(32)
+    assert set(mod._forms) == {"gate_proj", "up_proj", "down_proj"} and [n for n, _ in mod.named_parameters()] == ["gate.weight"]
+    with pytest.raises(RuntimeError, match="4 bits"):
+        mod.quantize_(32)
