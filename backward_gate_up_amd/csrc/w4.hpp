@@ -92,7 +92,8 @@ __global__ void w4_unpack(const char* data, Layout l, int has_zeros, int64_t exp
 // points: scale = rnd(max |w| / 7.5), code = clamp(round(w / scale) + 8); with
 // them: scale = rnd((max(w, 0) - min(w, 0)) / 15), zero = round(-min / scale),
 // code = clamp(round(w / scale) + zero). The rounded scale is the one that is
-// divided by. Eight elements per thread; a group is 4 to 16 neighbouring lanes.
+// divided by. A NaN makes its group's scale NaN, so that no finite weight stands in
+// its place. Eight elements per thread; a group is 4 to 16 neighbouring lanes.
 template <class E>
 __global__ void w4_quantize(const typename E::elem* w, int64_t n8, int group, uint32_t* codes,
                             typename E::elem* scales, uint8_t* zeros) {
@@ -104,16 +105,20 @@ __global__ void w4_quantize(const typename E::elem* w, int64_t n8, int group, ui
     const bool in = i < n8;
     const vec8 v = *(const vec8*)(w + (in ? i : 0) * 8);
     float lo = 0.f, hi = 0.f;
+    int nan = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      nan |= v[j] != v[j];
       lo = fminf(lo, E::to_f32(v[j]));
       hi = fmaxf(hi, E::to_f32(v[j]));
     }
     for (int d = 1; d < lanes; d <<= 1) {
       lo = fminf(lo, __shfl_xor(lo, d));
       hi = fmaxf(hi, __shfl_xor(hi, d));
+      nan |= __shfl_xor(nan, d);
     }
-    const typename E::elem sc = E::from_f32(zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.5f);
+    const typename E::elem sc =
+        E::from_f32(nan ? __builtin_nanf("") : zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.5f);
     const float sf = E::to_f32(sc);
     const float z = zeros ? (sf > 0.f ? fminf(fmaxf(rintf(-lo / sf), 0.f), 15.f) : 0.f) : 8.f;
     uint32_t c = 0;

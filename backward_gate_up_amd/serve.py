@@ -151,7 +151,8 @@ def w4_quantize(w, group=128, zeros=False):
     [.., N, K/group] in w's dtype, zero points [.., N, K/group] uint8. Without
     zero points scale = max|w| / 7.5 and code = round(w / scale) + 8, with
     them scale = (max(w, 0) - min(w, 0)) / 15 and code = round(w / scale) +
-    round(-min / scale), all clamped to 0..15."""
+    round(-min / scale), all clamped to 0..15. A NaN in ``w`` makes its group's
+    scale NaN."""
     w = w.detach().contiguous()
     _on_gpu(w)
     dt = _code(w, _DT16)

@@ -410,3 +410,21 @@ def test_quantize_leaves_the_module_whole_when_it_is_refused(monkeypatch):
     assert set(mod._forms) == {"gate_proj", "up_proj", "down_proj"} and [n for n, _ in mod.named_parameters()] == ["gate.weight"]
     with pytest.raises(RuntimeError, match="4 bits"):
         mod.quantize_(32)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_quantize_keeps_nan(group, zeros, dt):
+    """A group with a NaN or an infinity does not become finite numbers; others are not touched."""
+    banner(f"quantize NaN {dt} g={group} zeros={zeros}")
+    w = randn(gen(9), (16, 384), 0.05, DT[dt])
+    bad = w.clone()
+    bad[3, 5], bad[8, 383], bad[11, 2 * group] = float("nan"), float("nan"), float("inf")
+    clean, got = (m.W4Weight.quantize(t.cuda(), group, zeros).dequantize().cpu().view(16, -1, group) for t in (w, bad))
+    hit = [(3, 0), (8, 384 // group - 1), (11, 2)]
+    assert all(got[r, c].isnan().all() for r, c in hit[:2]) and not got[hit[2]].isfinite().any()
+    for r, c in hit:
+        got[r, c] = clean[r, c]
+    assert torch.equal(got, clean)
