@@ -20,8 +20,8 @@ import torch
 import backward_gate_up_amd as m
 from backward_gate_up_amd import _lib
 from tests._util import assert_local, banner, f64
-from tests.test_serve import (DT, _moe_config, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_route,
-                              ref_w4)
+from tests.test_serve import (DT, _moe_config, bound, cuda, expert_weights, gen, make_w4, randn, ref_block, ref_experts,
+                              ref_route, ref_w4)
 
 gpu = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -428,3 +428,89 @@ def test_w4_quantize_keeps_nan(group, zeros, dt):
     for r, c in hit:
         got[r, c] = clean[r, c]
     assert torch.equal(got, clean)
+
+
+# ---- variants chosen by length and width ------------------------------------------------
+
+
+def check_moe(T, E, k, D, H, dt):
+    g = gen(T * E + D)
+    x, w = randn(g, (T, D), 1, DT[dt]), expert_weights(g, E, D, H, DT[dt])
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    p = torch.rand((T, k), generator=g) + 0.1
+    y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *cuda(w))
+    assert_local(f64(y), ref_experts(f64(x), f64(p), ids.numpy(), *map(f64, w)), bound(DT[dt], 2), (T, D, H))
+
+
+def check_block_w4(T, D, H, group, zeros, dt):
+    g = gen(D + H)
+    raw = [make_w4(g, s, group, zeros, DT[dt]) for s in ((H, D), (H, D), (D, H))]
+    x = randn(g, (T, D), 1, DT[dt])
+    y = m.infer_w4(x.cuda(), *(m.w4_pack(*cuda(r)) for r in raw))
+    assert_local(f64(y), ref_block(f64(x), *(ref_w4(*r) for r in raw)), bound(DT[dt], 2), ("w4", T, D, H))
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [1, 5, 12])
+@pytest.mark.parametrize("D", [3136, 3144, 4360])
+def test_long_rows_few_tiles(T, D, dt):
+    """48 stages of K or more and fewer tiles than CUs: 8 waves split K."""
+    banner(f"8 waves {dt} T={T} D={D}")
+    check_moe(T, 4, 2, D // 16 * 8 if dt == "fp32" else D, 40, dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 4, 16])
+@pytest.mark.parametrize("D,group,zeros", [(6144, 128, False), (6176, 32, True), (8256, 64, False)])
+def test_long_rows_few_tiles_w4(T, D, group, zeros, dt):
+    banner(f"8 waves in 4 bits {dt} T={T} D={D}")
+    check_block_w4(T, D, 2 * group, group, zeros, dt)
+    check_linear(T, 72, D, group, zeros, dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [1, 8, 12, 16])
+@pytest.mark.parametrize("D", [2552, 2560, 6136, 6152, 8192, 16392])
+def test_wide_down_projections(T, D, dt):
+    """160, 384 and 1024 tiles of 16 columns: 16, 8 and 4 waves, no split."""
+    banner(f"down {dt} T={T} D={D}")
+    check_moe(T, 3, 2, D, 72, dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 4, 9, 16])
+@pytest.mark.parametrize("D,group,zeros", [(2560, 64, False), (6176, 32, True), (8192, 128, False), (16416, 32, False)])
+def test_wide_down_projections_w4(T, D, group, zeros, dt):
+    banner(f"down in 4 bits {dt} T={T} D={D}")
+    check_block_w4(T, D, 128, group, zeros, dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [17, 20, 32, 33, 64])
+@pytest.mark.parametrize("D,H,group,zeros", [(64, 12224, 32, True), (128, 12416, 64, False), (320, 12288, 64, True)])
+def test_wide_gate_up_w4_shared_rows(T, D, H, group, zeros, dt):
+    """96 tiles of 128 hidden columns: 32 and 64 token rows shared by 8 waves."""
+    banner(f"shared rows in 4 bits {dt} T={T} D={D} H={H}")
+    check_block_w4(T, D, H, group, zeros, dt)
+
+
+@gpu
+@pytest.mark.parametrize("T,E,k", [(64, 48, 12), (64, 48, 16), (40, 64, 32)])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_moe_w4_shared_rows(T, E, k, dt):
+    """An average of more than 12 pairs per expert in 4 bits, and 96 tiles."""
+    banner(f"experts' shared rows in 4 bits {dt} T={T} E={E} k={k}")
+    D, H, group = 160, 256, 32
+    g = gen(T + E)
+    raw = [make_w4(g, s, group, True, DT[dt]) for s in ((E, H, D), (E, H, D), (E, D, H))]
+    x = randn(g, (T, D), 1, DT[dt])
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    ids[:, 0] = 1  # one expert that takes every token: several passes
+    p = torch.rand((T, k), generator=g) + 0.1
+    y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *(m.w4_pack(*cuda(r)) for r in raw))
+    assert_local(f64(y), ref_experts(f64(x), f64(p), ids.numpy(), *(ref_w4(*r) for r in raw)), bound(DT[dt], 2), (T, E, k))
