@@ -1209,17 +1209,17 @@ static int down_for(const Args& g, const Shape& f, int waves, hipStream_t s) {
 }
 // Private rings: 4 waves, or 8 where each CU would run one workgroup at most and K
 // is long (4-bit N = 4096: K = 11008 10.6 -> 9.5 us, K = 4096 5.4 -> 5.6 us).
-template <class E, int FMT, int HB, int XR, bool PLAIN>
+template <class E, int FMT, int XR, bool PLAIN>
 static int gateup_own(const Args& g, int slots, hipStream_t s) {
-  const int64_t items = (int64_t)slots * ((g.N + 16 * HB - 1) / (16 * HB)) * ((g.T + kChunk - 1) / kChunk);
+  const int64_t items = (int64_t)slots * ((g.N + 15) / 16) * ((g.T + kChunk - 1) / kChunk);
   const int stages = StreamOf<E, FMT, 1, 16, 1, 16384>::type::stages(g.K);
-  if (items <= dev_ncu() && stages >= 48) return launch_gateup<E, FMT, HB, XR, 8, 1, PLAIN>(g, slots, s);
-  return launch_gateup<E, FMT, HB, XR, 4, 1, PLAIN>(g, slots, s);
+  if (items <= dev_ncu() && stages >= 48) return launch_gateup<E, FMT, 1, XR, 8, 1, PLAIN>(g, slots, s);
+  return launch_gateup<E, FMT, 1, XR, 4, 1, PLAIN>(g, slots, s);
 }
 template <class E, int FMT>
 static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
-  if (f.rows == 8) return gateup_own<E, FMT, 1, FMT ? 4 : 8, false>(g, slots, s);
-  if (f.rows == 16) return gateup_own<E, FMT, 1, 16, false>(g, slots, s);
+  if (f.rows == 8) return gateup_own<E, FMT, FMT ? 4 : 8, false>(g, slots, s);
+  if (f.rows == 16) return gateup_own<E, FMT, 16, false>(g, slots, s);
   // With so few tiles of 128 columns that most CUs would idle, tiles of 16 whose
   // waves split K on private rings, each row loaded by one of them (4 bits: 32
   // rows at a time, more leave no room).
@@ -1253,12 +1253,12 @@ int run_linear(const Call& c) {
   const Shape f = shape_of(c.T, 1, 1, false, true, 2);
   const bool wide = (c.D + 31) / 32 >= 3 * dev_ncu();
   if (f.rows == 8) {
-    if (wide) return gateup_own<E, FMT, 2, 4, true>(g, 1, c.stream);
-    return gateup_own<E, FMT, 1, 4, true>(g, 1, c.stream);
+    if (wide) return launch_gateup<E, FMT, 2, 4, 4, 1, true>(g, 1, c.stream);
+    return gateup_own<E, FMT, 4, true>(g, 1, c.stream);
   }
   if (f.rows == 16) {
-    if (wide) return gateup_own<E, FMT, 2, 16, true>(g, 1, c.stream);
-    return gateup_own<E, FMT, 1, 16, true>(g, 1, c.stream);
+    if (wide) return launch_gateup<E, FMT, 2, 16, 4, 1, true>(g, 1, c.stream);
+    return gateup_own<E, FMT, 16, true>(g, 1, c.stream);
   }
   g.splits = linear_splits(c.T, c.D, c.H);
   g.partial = (float*)c.ws;

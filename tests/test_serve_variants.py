@@ -514,3 +514,34 @@ def test_moe_w4_shared_rows(T, E, k, dt):
     p = torch.rand((T, k), generator=g) + 0.1
     y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *(m.w4_pack(*cuda(r)) for r in raw))
     assert_local(f64(y), ref_experts(f64(x), f64(p), ids.numpy(), *(ref_w4(*r) for r in raw)), bound(DT[dt], 2), (T, E, k))
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,D,H", [(1, 256, 128), (1, 2688, 128), (16, 256, 256), (16, 2688, 128), (20, 128, 12288), (20, 256, 128),
+                                   (40, 128, 12288), (40, 256, 128)])
+def test_every_group_size(T, D, H, group, dt):
+    banner(f"group {group} {dt} T={T} D={D} H={H}")
+    check_block_w4(T, D, H, group, T % 16 == 4, dt)
+    check_linear(T, 72, 2 * D, group, T % 16 == 4, dt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [("bf16", 0), ("fp16", 0), ("fp32", 0)] + [(t, n) for t in ("bf16", "fp16") for n in (32, 64, 128)])
+@pytest.mark.parametrize("T,E,k", [(40, 64, 1), (40, 20, 2), (70, 64, 1), (70, 30, 3)])
+def test_lightly_loaded_experts(T, E, k, fmt):
+    """More than 16 tokens with few pairs per expert: 4, 8 or 16 token rows, whole chunks' sums."""
+    dt, group = fmt
+    banner(f"light experts {dt} g={group} T={T} E={E} k={k}")
+    D, H = 256, 128
+    if not group:
+        check_moe(T, E, k, D, H, dt)
+        return
+    g = gen(T + E)
+    raw = [make_w4(g, s, group, False, DT[dt]) for s in ((E, H, D), (E, H, D), (E, D, H))]
+    x = randn(g, (T, D), 1, DT[dt])
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    p = torch.rand((T, k), generator=g) + 0.1
+    y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *(m.w4_pack(*cuda(r)) for r in raw))
+    assert_local(f64(y), ref_experts(f64(x), f64(p), ids.numpy(), *(ref_w4(*r) for r in raw)), bound(DT[dt], 2), (T, E, k))
