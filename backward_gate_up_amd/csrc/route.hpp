@@ -443,13 +443,19 @@ __global__ void __launch_bounds__(256, 2) route_logits_many(const Args g) {
   ring::wait_vmcnt<0>();
 }
 
-static inline bool route_many(int64_t T) { return T >= 512; }
+// Which kernel forms the logits, by the tokens from which the one for many is ahead on
+// most sizes (both, us): bf16 E=64, D=4096 T=512 17.8/13.5 few, T=1024 18.3/14.8, T=1536
+// 18.8/19.8; E=128, D=4096 T=512 18.2/15.5, T=1024 18.2/21.1; E=256, D=7168 T=1024
+// 40.4/36.5, T=1536 41.1/47.5. fp32 E=64, D=4096 T=1024 37.0/25.1, T=2048 43.6/40.1, T=4096
+// 54.9/61.5; E=256, D=7168 T=1024 114/69, T=2048 116/119; E=160, D=5120 T=2048 85/73.
+// (Few experts would stay with the other one for longer: E=8, D=1024 fp32 T=8192 34/17.)
+static inline bool route_many(int64_t T, size_t e) { return T >= (e == 4 ? 2048 : 1024); }
 // Workgroups along K: few tokens, about 128 over all, each wave with at least one
 // stage; many, about two per CU.
 static inline int route_splits(int64_t T, int64_t D, int64_t E, size_t e) {
   const int64_t stages = ((int64_t)D * e + 127) / 128;
   int64_t s, most;
-  if (route_many(T)) {
+  if (route_many(T, e)) {
     s = 512 / ((T + kManyTok - 1) / kManyTok);
     most = stages;
   } else {
@@ -474,9 +480,9 @@ template <class E>
 int run_route(Args g, hipStream_t stream) {
   if (g.T == 0) return SWIGLU_OK;
   g.splits = route_splits(g.T, g.D, g.E, E::kBytes);
-  g.many = route_many(g.T);
+  g.many = route_many(g.T, E::kBytes);
   const unsigned blocks = (g.E + 15) / 16, tiles = (g.T + 15) / 16;
-  if (route_many(g.T)) SWIGLU_ROUTE_LAUNCH((route_logits_many<E>), ((g.T + kManyTok - 1) / kManyTok, g.splits), 256);
+  if (g.many) SWIGLU_ROUTE_LAUNCH((route_logits_many<E>), ((g.T + kManyTok - 1) / kManyTok, g.splits), 256);
   else if (g.T <= 8) SWIGLU_ROUTE_LAUNCH((route_logits<E, 8>), (blocks, g.splits, 1), kPartWaves * 64);
   else SWIGLU_ROUTE_LAUNCH((route_logits<E, 16>), (blocks, g.splits, tiles), kPartWaves * 64);
   const unsigned groups = (g.T + 3) / 4;

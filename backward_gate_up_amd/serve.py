@@ -397,9 +397,11 @@ class SwiGLUMLPW4(_W4Module):
     """The dense SwiGLU block with 4-bit weights, made from a ``SwiGLUMLP`` (or any
     module with gate_proj, up_proj and down_proj layers without bias). No gradients. Above
     ``long_tokens`` tokens the weights are written back to rows and the no-grad
-    path of 16-bit weights runs, which is bound by arithmetic then."""
+    path of 16-bit weights runs, which is bound by arithmetic then (D = 4096, H = 11008,
+    4 bits against rows: 512 tokens 248 and 462 us, 768 400 and 459, 1024 475 and 479;
+    D = 2048, H = 5632: 512 tokens 94 and 136, 1024 148 and 168)."""
 
-    def __init__(self, mlp, group=128, zeros=False, long_tokens=512):
+    def __init__(self, mlp, group=128, zeros=False, long_tokens=1024):
         super().__init__()
         self._forms, self.long_tokens = {}, long_tokens
         layers = {name: getattr(mlp, name) for name in ("gate_proj", "up_proj", "down_proj")}

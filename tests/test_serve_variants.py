@@ -545,3 +545,38 @@ def test_lightly_loaded_experts(T, E, k, fmt):
     p = torch.rand((T, k), generator=g) + 0.1
     y = m.moe_experts(x.cuda(), p.cuda(), ids.cuda(), *(m.w4_pack(*cuda(r)) for r in raw))
     assert_local(f64(y), ref_experts(f64(x), f64(p), ids.numpy(), *(ref_w4(*r) for r in raw)), bound(DT[dt], 2), (T, E, k))
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,E,k,D", [(1023, 60, 4, 520), (1024, 64, 8, 264), (2047, 33, 2, 136), (2048, 129, 3, 72), (2085, 256, 8, 1000)])
+def test_route_around_many_tokens(T, E, k, D, dt):
+    """The logits come from another kernel from 1024 tokens on, in fp32 from 2048."""
+    banner(f"route {dt} T={T} E={E} k={k} D={D}")
+    g = gen(T + E)
+    x, wr = randn(g, (T, D), 1, DT[dt]), randn(g, (E, D), D ** -0.5, DT[dt])
+    for renorm in (True, False):
+        p, ids = m.moe_route(x.cuda(), wr.cuda(), k, renorm)
+        ri, rp = ref_route(f64(x), f64(wr), k, renorm)
+        assert np.array_equal(ids.cpu().numpy(), ri)
+        assert np.all(np.abs(f64(p) - rp) <= 3e-5 * rp)  # as in tests/test_serve.py
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("lane", [0, 3, 7])
+@pytest.mark.parametrize("small", [0, -80])
+def test_route_order_of_many_tokens(lane, small, dt):
+    """Orders below fp32's steps at 2050 tokens, at ordinary and (bf16, fp32) very small sizes."""
+    banner(f"route order 2050 lane={lane} {dt}")
+    T, D, E, k = 2050, 1024, 12, 5
+    g = gen(lane)
+    at = torch.arange(lane, D, 8)
+    x, base = torch.zeros(T, D), torch.zeros(E, D)
+    x[:, at] = torch.randn((T, at.numel()), generator=g)
+    base[:, at] = torch.randn(at.numel(), generator=g)
+    base[:, at[-1]] *= 1 + torch.arange(E).float()[torch.randperm(E, generator=g)] * 2.0 ** -6
+    x[:, at[-1]] *= 2.0 ** -12
+    x, wr = x.to(DT[dt]) * (1.0 if dt == "fp16" else 2.0 ** small), base.to(DT[dt])
+    _, ids = m.moe_route(x.cuda(), wr.cuda(), k)
+    assert np.array_equal(ids.cpu().numpy(), ref_route(f64(x), f64(wr), k, True)[0])
