@@ -165,7 +165,7 @@ __device__ __forceinline__ void choose(const Args& g, int t, const float (&l)[NP
       e = min(e, __builtin_amdgcn_readlane(at, __ffsll((unsigned long long)m) - 1));
     const float v = key_value(top);
     if (n == 0) mx = v;
-    if (n >= g.k && !(v >= kth - 2.f * bound)) break;
+    if (n >= g.k && !(bound > 0.f && v >= kth - 2.f * bound)) break;  // exact logits: the k first
     if (lane == n) {
       my_id = e;
       my_l = v;
