@@ -656,7 +656,12 @@ struct Walk {
   __device__ __forceinline__ int pair(int i) const { return __shfl(p.pair, ((first & 63) + i) & 63); }
 };
 
-// Whether A is held in two parts (few_down): at 8 token rows per stage, in 4 bits 4.
+// Whether A is held in two parts (few_down): at 8 token rows per stage, in 4 bits 4, where
+// the second part takes operand rows that are free. More rows would double the
+// products and the LDS reads of tokens, so there A is rounded once, as the
+// framework's other paths do, and y's error in 64 bits is 1.4 times that of fp32
+// sums alone (fp16 T = 37 2.9e-4 of the norm against 2.1e-4, bf16 T = 64 2.35e-3
+// against 1.66e-3) instead of 1.0.
 static __host__ __device__ constexpr bool halves(int rows, size_t e) { return rows <= 8 && e == 2; }
 
 // The largest finite value of a 16-bit type (A's two parts; fp32 has one).
@@ -758,9 +763,8 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 
   // g and u stay in fp32; A is rounded to the storage type the down
   // projection's matrix instructions take. That one rounding would add as much
-  // error to y as y's own (1.41 times the norm, measured), so where the token
-  // operand has room for a second set of rows (few_down) what it left goes into
-  // those; with more tokens it stays out.
+  // error to y as y's own, so where the token operand has room for a second set
+  // of rows (halves) what it left goes into those.
   auto store = [&](int pair, int h, float gate, float up) {
     const float a = PLAIN ? gate : gate * sigmoid_f32<E>(gate) * up;
     const int64_t p = (int64_t)t0 * g.k + pair;
@@ -850,7 +854,7 @@ __global__ void __launch_bounds__(NW * 64, (SH == 1 && FMT != 0 && XR < 16 ? 3 :
 // HALVES: A comes as two values (see few_gateup), in rows 0 .. XR - 1 and
 // XR .. 2 XR - 1 of the token operand, which repeats nothing then: no more
 // matrix instructions than with one. Measured where few_gateup was: 51 us for
-// 326 MB (6.3 TB/s), 149 us (4.8 TB/s), 8.7 us for 11.5 MB, and 22 us in 4 bits.
+// 326 MB (6.3 TB/s), 149 us (4.8 TB/s), 8.7 us for 11.5 MB, and 23 us in 4 bits.
 // W4, T = 33, N = 11008, K = 4096, g = 64, fp16: 19.0 us, 25 MB: bound by the waves'
 // instructions (codes to widen, LDS reads of the tokens, a scale per group and
 // output) on the 172 of 256 CUs that have a tile of 64 columns.
@@ -1110,9 +1114,19 @@ static inline Shape shape_of(int64_t T, int64_t k, int64_t E, bool routed, bool 
 // The down projection's workgroups: columns of a tile, waves, and workgroups per
 // tile, so that all CUs pull weights. One workgroup of many waves per tile adds
 // its sums in LDS; several leave partial sums and count arrivals, which costs
-// about 3 us (T = 1, D = 4096, H = 11008 in 4 bits: 10.2 us with three of 4
-// waves): only where there are too few tiles, or chunks too long for the waves'
-// [token][column] tiles.
+// about 3 us: only where there are too few tiles, or chunks too long for the waves'
+// [token][column] tiles. Whole blocks in us with K split over workgroups of 4 waves, and
+// unsplit with 16, 8 and 4 waves (rows: bf16, 2 of 8 experts, H = 5632, T = 12; 4 bits: the
+// dense block, H = 5632, T = 1):
+//   D =  1024,   64 tiles   rows 52/76/74/74       4 bits 13.1/12.5/11.5/12.1
+//   D =  2048,  128 tiles   rows 82/95/92/93       4 bits 14.4/13.7/12.9/13.7
+//   D =  2560,  160 tiles   rows 121/126/123/123   4 bits 17.6/14.5/13.5/14.3
+//   D =  4096,  256 tiles   rows 155/155/153/154   4 bits 17.2/15.9/14.9/15.9
+//   D =  6144,  384 tiles   rows 271/276/275/269   4 bits 20.5/23.6/19.5/19.0
+//   D = 16384, 1024 tiles   rows 703/689/677/675   4 bits 42.3/51.4/42.2/41.6
+// and with H = 11008, D = 4096: rows T = 16 201/217/211 unsplit, 4 bits 21.6/21.1/22.4. So 16
+// waves for the fewest tiles, whose K is cut finest, and fewer from 384 and 1024 on.
+// (In 4 bits below 160 tiles the split is 1 to 3 us behind; rows need it.)
 struct DownShape {
   int cols, waves, splits;
 };
@@ -1231,10 +1245,16 @@ static int gateup_for(const Args& g, const Shape& f, int slots, hipStream_t s) {
   return launch_gateup<E, FMT, 1, 64, 8, 8, false>(g, slots, s);
 }
 
-// y = x W^T (dense). At most 16 rows: items of 16 columns, or 32 where those
-// still give every workgroup one. More: tiles of 64 columns with two groups of
-// 4 waves along K; where those are few, K is split over workgroups as well and a
-// second launch adds the parts (N = 1248, K = 9792, T = 48: 57 us without).
+// y = x W^T (dense). At most 16 rows: items of 16 columns, or 32 where those still
+// give every workgroup one (K = 4096, g = 128, 16 columns/32 in us: N = 24576 T = 1
+// 12.6/11.8, T = 16 17.5/16.6; N = 32000 15.9/16.0, 21.3/16.9; N = 65536 31.8/28.7,
+// 51.1/40.5, 4.8 TB/s at T = 1; N = 128256 61.4/56.0, 101/80). More: tiles of 64 columns
+// with two groups of 4 waves along K; where those are few, K is split over
+// workgroups as well and a second launch adds the parts. A part has 6 records at
+// least (us with none, 12, 6, 3 or 1; bf16, g = 64, T = 48: N = 1248, K = 9792 46.5, 16.9,
+// 14.6, 14.9, 15.2; N = 4096, K = 4096 22.2, 16.6, 13.7, 13.8, 14.0; N = 2048, K = 1408 13.2,
+// 13.2, 13.4, 11.2, 11.1; N = 256, K = 4096 22.0, 16.0, 13.6, 12.1, 10.4: the fewest columns
+// would take shorter parts).
 static inline int linear_splits(int64_t T, int64_t N, int64_t K) {
   if (shape_of(T, 1, 1, false, true, 2).own) return 1;
   const int64_t tiles = (N + 63) / 64 * ((T + kChunk - 1) / kChunk), most = (K + 127) / 128 / 6;

@@ -1,5 +1,7 @@
 // w4.hpp -- 4-bit weights: quantisation, the layout of few.hpp's W4Stream, and
-// the way back. Load-time kernels: one pass each, bound by HBM.
+// the way back. One pass each, mostly over HBM: 11008 x 4096 in bf16, g = 128, takes
+// w4_quantize 35 us (3.25 TB/s), w4_pack 16 us (2.9: its reads of 4 bytes are 16 rows
+// apart) and w4_unpack 28 us (4.1 TB/s), which long prompts pay for each weight.
 #pragma once
 #include "few.hpp"
 

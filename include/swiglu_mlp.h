@@ -206,17 +206,22 @@ int swiglu_mlp_infer_noalloc(const void* X, const void* Wg, const void* Wu, cons
  * whose time is that of reading the weights (a decoding step: one token per
  * sequence). No backward. All weights are in the nn.Linear layout; sums are
  * fp32, A is rounded once to the storage type between the two launches, Y
- * once at the end. Any T up to SWIGLU_FEW_MAX_T is computed, in chunks of 64
- * tokens that each read the weights they need again; the kernels are meant
- * for T up to about 64.
+ * once at the end. For few tokens (T <= 8, or up to 2 choices per expert on
+ * average; 4-bit weights 4 and 1) a 16-bit A also keeps what its rounding left,
+ * so that its values may reach twice the type's largest; else those past the
+ * range are infinities. Any T up to SWIGLU_FEW_MAX_T is computed, in chunks of
+ * 64 tokens that each read the weights they need again; the kernels are meant
+ * for T up to about 64. T = 0 passes the checks and does nothing. Infinities
+ * and NaN stay with their token and have the values of the formulas.
  *
  * Router (swiglu_mlp_moe_route): logits l = X Wr^T over E experts, the k
  * largest of each token in descending order (equal logits: the lower index
  * first; NaN before everything), weights softmax(l) over all E, divided by
  * the chosen ones' sum when `renorm` is nonzero. X [T, D], Wr [E, D] in one
- * dtype; weights fp32 and ids int32 [T, k], 4-byte aligned. The order is that of the exact logits: those
- * closer to a neighbour than the fp32 sums can tell apart are summed again in
- * fp64 (among the 64 leading ones of a token).
+ * dtype; weights fp32 (from the fp32 logits: about 3e-7 relative) and ids int32
+ * [T, k], 4-byte aligned. The order is that of the exact logits: those closer to
+ * a neighbour than the fp32 sums can tell apart are summed again in fp64 (among
+ * the 64 leading ones of a token).
  *
  * Experts (swiglu_mlp_moe_experts): Y[t] = sum_j weights[t][j] *
  * ((SiLU(X[t] Wg_e^T) * (X[t] Wu_e^T)) Wd_e^T), e = ids[t][j]; Wg, Wu
@@ -234,10 +239,10 @@ int swiglu_mlp_infer_noalloc(const void* X, const void* Wg, const void* Wu, cons
  * codes [X][N][K/2] (two to a byte, the even k in the low half), scales
  * [X][N][K/group] in the storage type and zeros [X][N][K/group] bytes (or
  * NULL). swiglu_mlp_w4_quantize makes codes, scales and, where zeros is not
- * NULL, zero points from a 16-bit W [X][N][K]; swiglu_mlp_w4_dequantize
- * writes the packed weight back as rows (for a long prompt, whose products
- * are bound by arithmetic). Products are exact per code and scaled in fp32:
- * no weight is rounded. */
+ * NULL, zero points from a 16-bit W [X][N][K] (a NaN makes its group's scale
+ * NaN); swiglu_mlp_w4_dequantize writes the packed weight back as rows (for a
+ * long prompt, whose products are bound by arithmetic). Products are exact per
+ * code and scaled in fp32: no weight is rounded. */
 #define SWIGLU_FEW_MAX_T 65536
 #define SWIGLU_FEW_MAX_D 131072
 
