@@ -11,14 +11,17 @@ STATUS = {
     0: "SWIGLU_OK", 1: "SWIGLU_ERR_NULL", 2: "SWIGLU_ERR_SHAPE", 3: "SWIGLU_ERR_DTYPE",
     4: "SWIGLU_ERR_ALIGN", 5: "SWIGLU_ERR_ALIAS", 6: "SWIGLU_ERR_WORKSPACE",
     7: "SWIGLU_ERR_DEVICE", 8: "SWIGLU_ERR_LAUNCH", 9: "SWIGLU_ERR_FLAGS", 10: "SWIGLU_ERR_SCRATCH",
+    11: "SWIGLU_ERR_ARG",
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20
 FLAG_TWO_ROUND = 1
 FLAG_LINEAR_WEIGHTS = 2
-NUM_STAGES = 13
+NUM_STAGES = 19
 STAGE_NAMES = ("gateup_swiglu", "down_proj", "dgu_inplace", "dwd", "dwgu", "dx",
                "infer_gateup", "infer_down", "dwd+dgu", "dwgu+dx",
-               "moe_route", "few_gateup", "few_down")
+               "moe_route", "few_gateup", "few_down",
+               "norm_fwd", "norm_bwd", "linear", "linear_dz", "linear_dx", "linear_dw")
+ACTS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 FEW_MAX_T = 65536
 
 
@@ -86,7 +89,15 @@ def lib():
             ("w4_linear_workspace_bytes", [i64] * 3 + [i32], sz),
             ("w4_linear", [vp, w4, vp, vp, sz, i64, i32, vp], i32),
             ("w4_infer_workspace_bytes", [i64] * 3 + [i32], sz),
-            ("w4_infer", [vp] + [w4] * 3 + [vp, vp, sz, i64, i32, vp], i32)):
+            ("w4_infer", [vp] + [w4] * 3 + [vp, vp, sz, i64, i32, vp], i32),
+            ("norm_stats_bytes", [i64, i32], sz),
+            ("norm_bwd_workspace_bytes", [i64, i64, i32, i32], sz),
+            ("norm_fwd", [vp] * 5 + [i64, i64, ctypes.c_float, i32, i32, vp], i32),
+            ("norm_bwd", [vp] * 9 + [sz, i64, i64, i32, i32, vp], i32),
+            ("linear_workspace_bytes", [i64] * 3 + [i32], sz),
+            ("linear_fwd", [vp] * 7 + [sz] + [i64] * 3 + [i32, i32, vp], i32),
+            ("linear_bwd_workspace_bytes", [i64] * 3 + [i32, i32], sz),
+            ("linear_bwd", [vp] * 8 + [sz] + [i64] * 3 + [i32, i32, vp], i32)):
         f = getattr(L, "swiglu_mlp_" + name)
         f.argtypes, f.restype = args, res
     L.swiglu_mlp_status_string.argtypes = [i32]

@@ -3,8 +3,9 @@
 The kernels are instantiated in eighteen translation units (csrc/instantiate.hip
 compiled once per dtype, entry point and weight layout), the few-token serving
 kernels in nine more (csrc/few_instantiate.hip, once per dtype and weight
-format), plus the C ABI (csrc/swiglu_mlp.hip, csrc/few.hip); they compile in
-parallel and are linked into one shared library.
+format), the norms and the linear layer in sixteen (csrc/dense_instantiate.hip,
+once per dtype and part), plus the C ABI (csrc/swiglu_mlp.hip, csrc/few.hip,
+csrc/dense.hip); they compile in parallel and are linked into one shared library.
 """
 
 import os
@@ -39,6 +40,9 @@ UNITS = [("abi", "swiglu_mlp.hip", [])] + [
 ] + [("few", "few.hip", [])] + [
     (f"{dt}_few_{fmt}", "few_instantiate.hip", [f"-DSWIGLU_INST_DTYPE={i}", f"-DSWIGLU_INST_FMT={fmt}"])
     for i, dt in enumerate(("bf16", "fp16", "fp32")) for fmt in (0, 32, 64, 128) if fmt == 0 or dt != "fp32"
+] + [("dense", "dense.hip", [])] + [
+    (f"{dt}_dense_{part}", "dense_instantiate.hip", [f"-DSWIGLU_INST_DTYPE={i}", f"-DSWIGLU_INST_PART={part}"])
+    for i, dt in enumerate(("bf16", "fp16", "fp32")) for part in range(7) if part < 2 or dt != "fp32"
 ]
 
 

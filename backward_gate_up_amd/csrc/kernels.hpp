@@ -38,11 +38,12 @@
 #include "gemm_ring.hpp"
 #include "gemm_skinny.hpp"
 #include "gemm_stream.hpp"
+#include "act.hpp"
 #include "swiglu_mlp.h"
 
 namespace swiglu {
 
-enum Kind { GATEUP = 0, PLAIN = 1, DSWIGLU = 2, DX = 3 };
+enum Kind { GATEUP = 0, PLAIN = 1, DSWIGLU = 2, DX = 3, LINEAR = 4 };
 
 struct KArgs {
   Operand a0, a1;  // A operand; a1 = second K half (DX)
@@ -65,6 +66,10 @@ struct KArgs {
   int n_split;     // weight-gradient launch: tiles split over K (items n_full ..)
   unsigned* zero_ctr;  // no-grad gate/up: arrival counters of the down launch to clear (or nullptr)
   int n_zero;          // ... and how many
+  const char* bias;    // LINEAR: [N] or nullptr
+  const char* res;     // LINEAR: added after the activation, laid out as C, or nullptr
+  char* z;             // LINEAR: the values before the activation, laid out as C, or nullptr
+  int act;             // LINEAR: SWIGLU_ACT_*
 };
 
 // Workgroup 0 of a no-grad gate/up launch clears the arrival counters that
@@ -170,6 +175,34 @@ __device__ __forceinline__ void dswiglu4(const float (&da)[4], const float (&gf)
   }
 }
 
+// LINEAR: four consecutive outputs (m, n .. n + 3) from their sums z: the bias, the
+// value before the activation where it is kept, the activation, the residual.
+template <class E>
+__device__ __forceinline__ void linear_store(const KArgs& g, int m, int n, f32x4_t z) {
+  using V4 = typename E::vec4;
+  const int64_t off = ((int64_t)m * g.ldc + n) * E::kBytes;
+  if (g.bias) {
+    const V4 b = *(const V4*)(g.bias + (int64_t)n * E::kBytes);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] += E::to_f32(b[e]);
+  }
+  V4 v;
+  if (g.z) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = E::from_f32(z[e]);
+    *(V4*)(g.z + off) = v;
+  }
+  act4<E::kBytes == 4>(g.act, z);
+  if (g.res) {
+    const V4 r = *(const V4*)(g.res + off);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] += E::to_f32(r[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = E::from_f32(z[e]);
+  *(V4*)(g.c0 + off) = v;
+}
+
 // Epilogue of one tile. acc[i][j][r] holds output
 //   m = m0 + a_rows[i] + (lane & 31),
 //   n = (column base of subtile j) + (r / 4) * 8 + (lane / 32) * 4 + r % 4,
@@ -236,6 +269,24 @@ __device__ __forceinline__ void epilogue(const KArgs& g, char* C, f32x16_t (&acc
           }
           *(V4*)(g.c0 + off) = dg;
           *(V4*)(g.c1 + off) = du;
+        }
+      }
+    }
+  } else if constexpr (KIND == LINEAR) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = m0 + a_rows[i] + ml;
+      if (m >= g.M) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + b_rows[j] + q * 8 + nl;
+          if (n >= g.N) continue;
+          f32x4_t z;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = acc[i][j][q * 4 + e];
+          linear_store<E>(g, m, n, z);
         }
       }
     }
@@ -525,7 +576,7 @@ struct WaveBlock {
   }
 };
 
-template <class E, int KIND>
+template <class E, int KIND, int ACT = -1>
 __device__ __forceinline__ void ring_epilogue(const KArgs& g, char* C, f32x4_t (&acc)[8][8], int m0, int n0,
                                               int wm, int wn, int lane, char* wbuf) {
   using V4 = typename E::vec4;
@@ -649,6 +700,84 @@ __device__ __forceinline__ void ring_epilogue(const KArgs& g, char* C, f32x4_t (
       pg.template write_chunks<4>(vg, 0, g.c0, g.ldc, r0, c0, g.M, g.N, lane);
       pu.template write_chunks<4>(vu, 0, g.c1, g.ldc, r0, c0, g.M, g.N, lane);
     }
+  } else if constexpr (KIND == LINEAR) {
+    static_assert(ACT >= 0, "the ring kernels' activation is fixed at compile time");
+    // wave block: 128 x 128 outputs in eight parts of 16 rows, four LDS slots of
+    // 8 KiB. A slot's first half takes the part's residual, then its y; the second
+    // half the values before the activation. Loads as for DSWIGLU above, 4 per
+    // part; a part stores 4 times, or 8 with the values before the activation,
+    // which only makes the counts below wait for more than they have to.
+    const int c0 = n0 + wn * 128;
+    f32x4_t bias[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      bias[j] = f32x4_t{};
+      const int n = c0 + j * 16 + nl;
+      if (g.bias && n < g.N) {
+        const V4 b = *(const V4*)(g.bias + (int64_t)n * 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[j][e] = E::to_f32(b[e]);
+      }
+    }
+    auto parts = [&](auto RES) {
+      constexpr bool kRes = decltype(RES)::value;
+      auto issue = [&](int q) {
+        WaveBlock<E, 128>{wbuf + (q & 3) * 8192}.load(g.res, g.ldc, (int64_t)g.M * g.ldc * 2, m0 + wm * 128 + q * 16, c0,
+                                                      16, lane);
+      };
+      if constexpr (kRes) {
+        issue(0);
+        issue(1);
+        issue(2);
+        issue(3);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if constexpr (kRes) {
+          if (q == 0) ring::wait_vmcnt<12>();
+          else if (q == 1 || q == 7) ring::wait_vmcnt<16>();
+          else if (q == 2 || q == 6) ring::wait_vmcnt<20>();
+          else if (q == 3 || q == 5) ring::wait_vmcnt<24>();
+          else ring::wait_vmcnt<28>();
+        }
+        WaveBlock<E, 128> py{wbuf + (q & 3) * 8192}, pz{wbuf + (q & 3) * 8192 + 4096};
+        V4 rv[8];
+        if constexpr (kRes) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) rv[j] = py.get4(ml, j * 16 + nl);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          V4 v;
+          f32x4_t z = acc[q][j] + bias[j];
+          if (g.z) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = E::from_f32(z[e]);
+            pz.put4(ml, j * 16 + nl, v);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[e] = act_f32<false, ACT>(z[e]);
+            if constexpr (kRes) z[e] += E::to_f32(rv[j][e]);
+            v[e] = E::from_f32(z[e]);
+          }
+          py.put4(ml, j * 16 + nl, v);
+        }
+        u32x4_t vy[4], vz[4];
+        py.template read_chunks<4>(vy, 0, lane);
+        if (g.z) pz.template read_chunks<4>(vz, 0, lane);
+        if constexpr (kRes) {
+          // the slot's contents are in registers: part q + 4 may load into it
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          if (q + 4 < 8) issue(q + 4);
+        }
+        const int r0 = m0 + wm * 128 + q * 16;
+        py.template write_chunks<4>(vy, 0, g.c0, g.ldc, r0, c0, g.M, g.N, lane);
+        if (g.z) pz.template write_chunks<4>(vz, 0, g.z, g.ldc, r0, c0, g.M, g.N, lane);
+      }
+    };
+    if (g.res) parts(std::true_type{});
+    else parts(std::false_type{});
   } else {
     // PLAIN / DX: 128 x 128 block of C
     WaveBlock<E, 128> pc{wbuf};
@@ -921,7 +1050,7 @@ __device__ __forceinline__ void ring_tile(const KArgs& g, char* st0, char* st1, 
 // Before the last sub-step of stage s this wave's loads up to B of stage s + 1
 // are waited for (vmcnt counts this wave's loads in issue order), then a
 // barrier publishes stage s + 1.
-template <class E, int AL, int BL, int KIND>
+template <class E, int AL, int BL, int KIND, int ACT = -1>
 __device__ __forceinline__ void ring5_tile(const KArgs& g, char* const (&R)[5], int bid, int bz, int ks = 0,
                                            int piece = -1) {
   using namespace ring;
@@ -1117,7 +1246,7 @@ __device__ __forceinline__ void ring5_tile(const KArgs& g, char* const (&R)[5], 
     }
   }
   // (a select, not R[wave]: indexing R at run time would keep it in scratch)
-  ring_epilogue<E, KIND>(g, C, acc, m0, n0, wm, wn, lane, reg(wave));
+  ring_epilogue<E, KIND, ACT>(g, C, acc, m0, n0, wm, wn, lane, reg(wave));
 }
 
 // Pipeline per operand layouts: 4 = four stages of 32 K (ring_tile), 5 =
@@ -1874,6 +2003,9 @@ extern Timer g_timer;  // defined once, in swiglu_mlp.hip
 
 // Stage ids of the few-token serving kernels (include/swiglu_mlp.h).
 enum { STAGE_ROUTE = 10, STAGE_FEW_GATEUP = 11, STAGE_FEW_DOWN = 12 };
+// Stage ids of the norms and of the linear layer.
+enum { STAGE_NORM_FWD = 13, STAGE_NORM_BWD = 14, STAGE_LINEAR = 15, STAGE_LINEAR_DZ = 16, STAGE_LINEAR_DX = 17,
+       STAGE_LINEAR_DW = 18 };
 
 struct StageScope {
   int s;

@@ -262,6 +262,8 @@ const char* swiglu_mlp_status_string(int status) {
     case SWIGLU_ERR_SCRATCH:
       return "the call needs more than the fixed scratch of the allocation-free entry point (see "
              "SWIGLU_NOALLOC_SCRATCH_BYTES)";
+    case SWIGLU_ERR_ARG:
+      return "unknown activation or norm, eps negative or not a number, or a bias where there is none";
     default: return "unknown status";
   }
 }

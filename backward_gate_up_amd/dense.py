@@ -1,0 +1,298 @@
+"""Norms and the linear layer with an epilogue, forward and backward.
+
+What stands before and beside the SwiGLU block in the same models. Op level, as in
+the package's other wrappers (every arithmetic step runs in the HIP kernels
+behind the C ABI of include/swiglu_mlp.h; no fallback):
+
+* ``norm_fwd``, ``norm_bwd``      layer norm and RMS norm over the last axis
+* ``linear_fwd``, ``linear_bwd``  y = act(x W^T + b) + residual
+
+with autograd: ``layer_norm``, ``rms_norm``, ``linear``; and the module
+``FeedForward``, the ungated feed-forward layer x + fc2(act(fc1(norm(x)))) of them.
+All tensors of a call share dtype (bf16, fp16 or fp32) and device.
+
+Second derivatives are refused. The backward may run more than once
+(``retain_graph``): it changes nothing that the forward kept.
+"""
+
+import contextlib
+import math
+
+import torch
+
+from . import _lib as _L
+from .serve import _bytes, _check, _code, _on_gpu, _ptr, _stream, _workspace
+
+ACTIVATIONS = tuple(_L.ACTS)
+
+
+def _on(device):
+    """The library launches on the current device: makes it the tensors'."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _act(activation):
+    try:
+        return _L.ACTS[activation]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {activation!r}; use one of {ACTIVATIONS}") from None
+
+
+def _same(x, *others):
+    for t in others:
+        if t is not None and (t.dtype != x.dtype or t.device != x.device):
+            raise ValueError("all tensors must share dtype and device")
+    _on_gpu(x)
+
+
+def _opt(t):
+    return None if t is None else _ptr(t)
+
+
+# ---- norms ------------------------------------------------------------------
+
+
+def _norm_shapes(x, weight, bias, eps, rms):
+    if x.dim() != 2 or weight.dim() != 1 or weight.shape[0] != x.shape[1] or x.shape[1] == 0:
+        raise ValueError(f"expected X[T,D] and weight[D]: X{tuple(x.shape)} weight{tuple(weight.shape)}")
+    if bias is not None and (rms or bias.shape != weight.shape):
+        raise ValueError("RMS norm has no bias" if rms else f"bias must be [D]: {tuple(bias.shape)}")
+    if not 0 <= eps < math.inf:
+        raise ValueError(f"eps must be a number from 0 up: got {eps}")
+    _same(x, weight, bias)
+
+
+def norm_fwd(x, weight, bias=None, eps=1e-5, rms=False, stats=True):
+    """Y = (x - mean) rstd weight + bias over the last axis of x[T, D], rstd = 1 /
+    sqrt(mean((x - mean)^2) + eps); with ``rms`` the mean is 0 and there is no
+    bias. Returns (Y, stats): fp32 [2, T] (mean, rstd), with ``rms`` [1, T]
+    (rstd), for ``norm_bwd``; None without ``stats``."""
+    x, weight = x.contiguous(), weight.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    _norm_shapes(x, weight, bias, eps, rms)
+    T, D = x.shape
+    dt = _code(x)
+    y = torch.empty_like(x)
+    st = torch.empty((1 if rms else 2, T), dtype=torch.float32, device=x.device) if stats else None
+    with _on(x.device):
+        rc = _L.lib().swiglu_mlp_norm_fwd(_ptr(x), _ptr(weight), _opt(bias), _ptr(y), _opt(st), T, D, eps, bool(rms), dt,
+                                          _stream(x.device))
+    _check(rc, "swiglu_mlp_norm_fwd")
+    return y, st
+
+
+def norm_bwd(dy, x, weight, stats, rms=False, bias=False, dres=None, workspace=None):
+    """(dX, dweight, dbias) of ``norm_fwd``; dbias is None unless ``bias``. ``dres``
+    [T, D] is added to dX (the gradient that reaches x past the norm)."""
+    dy, x, weight, stats = dy.contiguous(), x.contiguous(), weight.contiguous(), stats.contiguous()
+    dres = None if dres is None else dres.contiguous()
+    if dy.shape != x.shape or (dres is not None and dres.shape != x.shape):
+        raise ValueError("dY and dres must match X in shape")
+    _norm_shapes(x, weight, None, 0.0, rms)
+    T, D = x.shape
+    _same(x, dy, dres)
+    if tuple(stats.shape) != (1 if rms else 2, T) or stats.dtype != torch.float32 or stats.device != x.device:
+        raise ValueError("stats must be the fp32 tensor returned by norm_fwd")
+    if bias and rms:
+        raise ValueError("RMS norm has no bias")
+    dt = _code(x)
+    dx, dw = torch.empty_like(x), torch.empty_like(weight)
+    db = torch.empty_like(weight) if bias else None
+    with _on(x.device):
+        need = _L.lib().swiglu_mlp_norm_bwd_workspace_bytes(T, D, bool(rms), dt)
+        ws, nbytes, keep = _workspace(workspace, need, x.device) if need else (None, 0, None)
+        rc = _L.lib().swiglu_mlp_norm_bwd(_ptr(dy), _ptr(x), _ptr(weight), _ptr(stats), _opt(dres), _ptr(dx), _ptr(dw),
+                                          _opt(db), ws, nbytes, T, D, bool(rms), dt, _stream(x.device))
+    _check(rc, "swiglu_mlp_norm_bwd")
+    return dx, dw, db
+
+
+def _no_second(ctx):
+    if torch.is_grad_enabled():
+        raise RuntimeError("create_graph=True (double backward) is not supported")
+
+
+class NormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, rms):
+        y, stats = norm_fwd(x, weight, bias, eps, rms)
+        ctx.save_for_backward(x, weight, stats)
+        ctx.form = rms, bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        _no_second(ctx)
+        x, weight, stats = ctx.saved_tensors
+        rms, bias = ctx.form
+        dx, dw, db = norm_bwd(dy, x, weight, stats, rms, bias)
+        return dx, dw, db, None, None
+
+
+def _norm(x, weight, bias, eps, rms):
+    if x.dim() == 0:
+        raise ValueError("expected X[..., D]")
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
+        y = NormFunction.apply(x2, weight, bias, eps, rms)
+    else:
+        y = norm_fwd(x2, weight, bias, eps, rms, stats=False)[0]
+    return y if x.dim() == 2 else y.reshape(x.shape)
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5):
+    """Layer norm over the last axis of x[..., D]: (x - mean) / sqrt(var + eps) *
+    weight + bias."""
+    return _norm(x, weight, bias, eps, False)
+
+
+def rms_norm(x, weight, eps=1e-6):
+    """RMS norm over the last axis of x[..., D]: x / sqrt(mean(x^2) + eps) *
+    weight."""
+    return _norm(x, weight, None, eps, True)
+
+
+# ---- linear layer -------------------------------------------------------------
+
+
+def _linear_shapes(x, w, bias, residual):
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"shape mismatch (expected X[T,K], W[N,K]): X{tuple(x.shape)} W{tuple(w.shape)}")
+    T, (N, K) = x.shape[0], w.shape
+    if bias is not None and tuple(bias.shape) != (N,):
+        raise ValueError(f"bias must be [N] = [{N}]: {tuple(bias.shape)}")
+    if residual is not None and tuple(residual.shape) != (T, N):
+        raise ValueError(f"residual must be [T, N] = {[T, N]}: {tuple(residual.shape)}")
+    _same(x, w, bias, residual)
+    return T, N, K
+
+
+def linear_fwd(x, w, bias=None, activation=None, residual=None, keep=True, workspace=None):
+    """Y = act(x W^T + bias) + residual: x[T, K], w[N, K], bias[N], residual[T, N];
+    ``activation`` None, "relu", "gelu", "gelu_tanh" or "silu". K and N are
+    multiples of 8. Returns (Y, Z): Z[T, N] is the activation's argument in the
+    inputs' dtype, for ``linear_bwd``; None without an activation or ``keep``."""
+    act = _act(activation)
+    x, w = x.contiguous(), w.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    residual = None if residual is None else residual.contiguous()
+    T, N, K = _linear_shapes(x, w, bias, residual)
+    dt, L = _code(x), _L.lib()
+    y = torch.empty((T, N), dtype=x.dtype, device=x.device)
+    z = torch.empty_like(y) if keep and act else None
+    with _on(x.device):
+        need = L.swiglu_mlp_linear_workspace_bytes(T, N, K, dt)
+        ws, nbytes, held = _workspace(workspace, need, x.device) if need else (None, 0, None)
+        rc = L.swiglu_mlp_linear_fwd(_ptr(x), _ptr(w), _opt(bias), _opt(residual), _ptr(y), _opt(z), ws, nbytes, T, N, K, act,
+                                     dt, _stream(x.device))
+    _check(rc, "swiglu_mlp_linear_fwd")
+    return y, z
+
+
+def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), workspace=None):
+    """(dX, dW, dbias) of ``linear_fwd``; ``needs`` says which are wanted, the
+    others are None. ``z``: what ``linear_fwd`` kept, where there is an
+    activation. The residual's gradient is dY."""
+    act = _act(activation)
+    dy, x, w = dy.contiguous(), x.contiguous(), w.contiguous()
+    if dy.dim() != 2 or tuple(dy.shape) != (x.shape[0], w.shape[0]):
+        raise ValueError(f"dY must be [T, N]: {tuple(dy.shape)}")
+    if act and (z is None or z.shape != dy.shape):
+        raise ValueError("z must be the [T, N] tensor returned by linear_fwd")
+    z = z.contiguous() if act else None
+    T, N, K = _linear_shapes(x, w, None, dy)
+    _same(x, z)
+    dt, L = _code(x), _L.lib()
+    dx = torch.empty_like(x) if needs[0] else None
+    dw = torch.empty_like(w) if needs[1] else None
+    db = torch.empty(N, dtype=x.dtype, device=x.device) if needs[2] else None
+    with _on(x.device):
+        need = L.swiglu_mlp_linear_bwd_workspace_bytes(T, N, K, act, dt)
+        ws, nbytes, held = _workspace(workspace, need, x.device) if need else (None, 0, None)
+        rc = L.swiglu_mlp_linear_bwd(_ptr(dy), _ptr(x), _ptr(w), _opt(z), _opt(dx), _opt(dw), _opt(db), ws, nbytes, T, N, K,
+                                     act, dt, _stream(x.device))
+    _check(rc, "swiglu_mlp_linear_bwd")
+    return dx, dw, db
+
+
+class LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation):
+        y, z = linear_fwd(x, w, bias, activation, residual)
+        ctx.save_for_backward(x, w, z)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        _no_second(ctx)
+        x, w, z = ctx.saved_tensors
+        nx, nw, nb, nr, _ = ctx.needs_input_grad
+        dx = dw = db = None
+        if nx or nw or nb:
+            dx, dw, db = linear_bwd(dy, x, w, z, ctx.activation, (nx, nw, nb))
+        return dx, dw, db, dy if nr else None, None
+
+
+def linear(x, w, bias=None, activation=None, residual=None):
+    """Y = act(x W^T + bias) + residual for x[..., K]: the product with bias,
+    activation and residual in its epilogue. w[N, K] (nn.Linear layout), bias[N],
+    residual[..., N] or None; ``activation`` None, "relu", "gelu", "gelu_tanh"
+    or "silu"."""
+    if x.dim() == 0 or w.dim() != 2:
+        raise ValueError("expected X[..., K] and W[N, K]")
+    shape = (*x.shape[:-1], w.shape[0])
+    if residual is not None and tuple(residual.shape) != shape:
+        raise ValueError(f"residual must be {list(shape)}: {tuple(residual.shape)}")
+    if x.dim() != 2:
+        x = x.reshape(-1, x.shape[-1])
+        residual = None if residual is None else residual.reshape(-1, shape[-1])
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, bias, residual)):
+        y = LinearFunction.apply(x, w, bias, residual, activation)
+    else:
+        y = linear_fwd(x, w, bias, activation, residual, keep=False)[0]
+    return y if len(shape) == 2 else y.reshape(shape)
+
+
+# ---- the layer of them ----------------------------------------------------------
+
+_CONFIG_ACTS = {"relu": "relu", "gelu": "gelu", "gelu_new": "gelu_tanh", "gelu_pytorch_tanh": "gelu_tanh",
+                "gelu_tanh": "gelu_tanh", "silu": "silu", "swish": "silu"}
+
+
+class FeedForward(torch.nn.Module):
+    """The ungated feed-forward layer with its norm in front and the stream added:
+    y = x + fc2(act(fc1(norm(x)))). ``config`` has hidden_size, intermediate_size
+    and optionally hidden_act (default "gelu"), mlp_bias (default true) and the
+    norm's epsilon, as layer_norm_eps (default 1e-5) or, for an RMS norm in front,
+    rms_norm_eps. Submodules ``norm``, ``fc1`` and ``fc2`` are torch's, whose
+    weights the kernels read in place."""
+
+    def __init__(self, config):
+        super().__init__()
+        act = getattr(config, "hidden_act", "gelu")
+        if act not in _CONFIG_ACTS:
+            raise ValueError(f"FeedForward has no activation {act!r}; use one of {tuple(_CONFIG_ACTS)}")
+        self.activation = _CONFIG_ACTS[act]
+        D, H = int(config.hidden_size), int(config.intermediate_size)
+        bias = bool(getattr(config, "mlp_bias", True))
+        rms = getattr(config, "rms_norm_eps", None)
+        if rms is not None:
+            self.norm = torch.nn.RMSNorm(D, eps=float(rms))
+        else:
+            self.norm = torch.nn.LayerNorm(D, eps=float(getattr(config, "layer_norm_eps", 1e-5)))
+        self.fc1 = torch.nn.Linear(D, H, bias=bias)
+        self.fc2 = torch.nn.Linear(H, D, bias=bias)
+
+    def forward(self, x):
+        if isinstance(self.norm, torch.nn.RMSNorm):
+            n = rms_norm(x, self.norm.weight, self.norm.eps)
+        else:
+            n = layer_norm(x, self.norm.weight, self.norm.bias, self.norm.eps)
+        a = linear(n, self.fc1.weight, self.fc1.bias, self.activation)
+        return linear(a, self.fc2.weight, self.fc2.bias, residual=x)
+
+    def extra_repr(self):
+        return f"activation={self.activation!r}"

@@ -75,7 +75,9 @@ typedef enum {
   SWIGLU_ERR_DEVICE = 7,    /* current device is not gfx950, or a HIP query failed */
   SWIGLU_ERR_LAUNCH = 8,    /* a kernel launch failed (work may be partially enqueued) */
   SWIGLU_ERR_FLAGS = 9,     /* unknown bits in the flags of an _ex entry point */
-  SWIGLU_ERR_SCRATCH = 10   /* swiglu_mlp_infer_noalloc: the call needs more than its fixed scratch */
+  SWIGLU_ERR_SCRATCH = 10,  /* swiglu_mlp_infer_noalloc: the call needs more than its fixed scratch */
+  SWIGLU_ERR_ARG = 11       /* norms, linear layer: unknown activation or form, eps negative or not a number,
+                               a bias where there is none */
 } swiglu_status_t;
 
 /* Flags of the _ex entry points (swiglu_mlp_fwd_ex, swiglu_mlp_bwd_ex,
@@ -308,6 +310,62 @@ int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* Wg, const swiglu_w4_t*
                         const swiglu_w4_t* Wd, void* Y, void* workspace, size_t workspace_bytes,
                         int64_t T, int dtype, hipStream_t stream);
 
+/* ---- Norms and the linear layer -------------------------------------------
+ * What stands before and beside the block in the same models, for training
+ * and for inference.
+ *
+ * Norms over the last axis of X [T, D] (rms = 0: layer norm, 1: RMS norm):
+ *   n = (x - mean) rstd, y = n weight + bias, rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * and for RMS norm the same with mean = 0 and no bias. Sums are fp32, the
+ * variance that of the differences from the mean; squares past fp32's range
+ * are infinities. Any D from 1 to SWIGLU_NORM_MAX_D; pointers need the alignment
+ * of an element only (workspace: 16 bytes). stats, [2][T] (mean, rstd; RMS
+ * norm [T], rstd) in fp32, is what the backward needs; NULL without one.
+ * The backward writes dX (plus dres where that is not NULL: the gradient
+ * that reaches x past the norm, as in x + f(norm(x))), dweight and dbias (NULL:
+ * not wanted). The sums over tokens have a fixed order. T = 0 writes zero
+ * weight gradients. workspace: fp32 parts of those sums; contents on entry do
+ * not matter. */
+#define SWIGLU_NORM_MAX_D 1048576
+size_t swiglu_mlp_norm_stats_bytes(int64_t T, int rms);
+size_t swiglu_mlp_norm_bwd_workspace_bytes(int64_t T, int64_t D, int rms, int dtype);
+int swiglu_mlp_norm_fwd(const void* X, const void* weight, const void* bias, void* Y, float* stats,
+                        int64_t T, int64_t D, float eps, int rms, int dtype, hipStream_t stream);
+int swiglu_mlp_norm_bwd(const void* dY, const void* X, const void* weight, const float* stats,
+                        const void* dres, void* dX, void* dweight, void* dbias, void* workspace,
+                        size_t workspace_bytes, int64_t T, int64_t D, int rms, int dtype,
+                        hipStream_t stream);
+
+/* Linear layer with its epilogue: Z = X W^T + bias, Y = act(Z) + residual. X
+ * [T, K], W [N, K] (nn.Linear layout), bias [N], residual, Y, Z [T, N]; bias,
+ * residual and Z may be NULL. T, N and K as T, D and H above. Z is the fp32 sum
+ * rounded to the storage type, kept for the backward; Y comes from the fp32
+ * sum itself and is rounded once. At most 64 tokens stream the weight.
+ * The backward reads dY, X, W and, where there is an activation, Z, and
+ * writes dX = dZ W, dW = dZ^T X and dbias = sum over tokens of dZ, where dZ =
+ * dY act'(Z) (rounded to the storage type for the two products, not for the
+ * sum); NULL: not wanted. The residual's gradient is dY. T = 0 writes zero
+ * weight gradients. gelu is z Phi(z), gelu_tanh its form with tanh; relu's
+ * derivative at 0 and at NaN is 0. In bf16 and fp16 silu and gelu_tanh of values
+ * below about -87 (2u for gelu_tanh) may be a zero. workspace contents on entry do
+ * not matter; calls that share one must be stream-ordered. */
+typedef enum {
+  SWIGLU_ACT_NONE = 0,
+  SWIGLU_ACT_RELU = 1,
+  SWIGLU_ACT_GELU = 2,
+  SWIGLU_ACT_GELU_TANH = 3,
+  SWIGLU_ACT_SILU = 4
+} swiglu_act_t;
+#define SWIGLU_NUM_ACTS 5
+size_t swiglu_mlp_linear_workspace_bytes(int64_t T, int64_t N, int64_t K, int dtype);
+int swiglu_mlp_linear_fwd(const void* X, const void* W, const void* bias, const void* residual, void* Y,
+                          void* Z, void* workspace, size_t workspace_bytes, int64_t T, int64_t N,
+                          int64_t K, int act, int dtype, hipStream_t stream);
+size_t swiglu_mlp_linear_bwd_workspace_bytes(int64_t T, int64_t N, int64_t K, int act, int dtype);
+int swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W, const void* Z, void* dX, void* dW,
+                          void* dbias, void* workspace, size_t workspace_bytes, int64_t T, int64_t N,
+                          int64_t K, int act, int dtype, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* swiglu_mlp_status_string(int status);
 
@@ -320,6 +378,9 @@ const char* swiglu_mlp_status_string(int status);
  *   8 stages 3 + 2 in one launch       9 stages 4 + 5 in one launch
  *  10 router                          11 few-token gate/up (experts, 4-bit)
  *  12 few-token down projection or 4-bit product
+ *  13 norm                            14 norm's backward
+ *  15 linear layer                    16 its dZ and dbias
+ *  17 its dX                          18 its dW
  * (bf16/fp16 run every stage as its own launch; in fp32 with T > 512 the
  * backward runs as launches 8 and 9, where the long-K weight-gradient tiles
  * are dispatched first and the short tiles of the other stage fill in
@@ -330,7 +391,7 @@ const char* swiglu_mlp_status_string(int status);
  * waits for the recorded events and writes, for each of the first `n` stages,
  * the summed milliseconds to ms[s] and the launch count to count[s], then
  * disables recording. Not thread-safe; meant for a benchmark's timed loop. */
-#define SWIGLU_NUM_STAGES 13
+#define SWIGLU_NUM_STAGES 19
 int swiglu_mlp_timer_start(int capacity);
 int swiglu_mlp_timer_stop(double* ms, int* count, int n);
 
