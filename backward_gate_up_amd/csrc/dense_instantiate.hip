@@ -1,7 +1,8 @@
 // dense_instantiate.hip -- defines the drivers of norm.hpp and linear.hpp (and so
 // instantiates their kernels). Compiled with -DSWIGLU_INST_DTYPE=0|1|2 (bf16,
 // fp16, fp32) and -DSWIGLU_INST_PART=0 (norms), 1 (linear layer) or, for 16-bit
-// types, 2 .. 6 (the ring kernel of activation 0 .. 4).
+// types, 2 .. 6 (the ring kernel of activation 0 .. 4, with 0
+// that of a tile's parts).
 #include "linear.hpp"
 
 #if !defined(SWIGLU_INST_DTYPE) || !defined(SWIGLU_INST_PART)
@@ -32,7 +33,10 @@ template int run_bwd<InstE>(const Bwd&);
 }  // namespace lin
 #else
 namespace lin {
-template int launch_lin_ring<InstE, SWIGLU_INST_PART - 2>(KArgs, hipStream_t);
+template int launch_lin_ring<InstE, SWIGLU_INST_PART - 2>(const KArgs&, hipStream_t);
+#if SWIGLU_INST_PART == 2
+template int launch_lin_ring_parts<InstE>(const KArgs&, hipStream_t);
+#endif
 }  // namespace lin
 #endif
 }  // namespace swiglu

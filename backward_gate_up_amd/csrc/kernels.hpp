@@ -59,7 +59,8 @@ struct KArgs {
   int plane_a;     // PLAIN, two planes: plane 1 takes its A operand from a1 (B shared) instead of B from b1
   int group_m;     // M-tiles per group of the tile walk (tile_coords); 0 = 8
   int two_round;   // GATEUP: A = rnd(rnd(SiLU(g)) * u) instead of rnd(SiLU(g) * u)
-  float* P;        // PLAIN, split K: fp32 partial tiles, 256 x 256 each (else nullptr)
+  float* P;        // PLAIN, split K: fp32 partial tiles, 256 x 256 each (else nullptr);
+                   // LINEAR on the tile engine: [ksplit][M][N]
   int kchunk;      // PLAIN, split K: K stages per piece
   int n_full;      // weight-gradient launch: items (plane-major tiles) run whole
   int ksplit;      // weight-gradient launch: pieces per split tile
@@ -286,7 +287,8 @@ __device__ __forceinline__ void epilogue(const KArgs& g, char* C, f32x16_t (&acc
           f32x4_t z;
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[e] = acc[i][j][q * 4 + e];
-          linear_store<E>(g, m, n, z);
+          if (g.ksplit > 1) *(f32x4_t*)((float*)C + (int64_t)m * g.N + n) = z;
+          else linear_store<E>(g, m, n, z);
         }
       }
     }
@@ -333,6 +335,16 @@ __device__ __forceinline__ void gemm_tile(const KArgs& g, char* smem, int bid, i
     if (g.plane_a) A = g.a1;
     else B = g.b1;
     C = g.c1;
+  }
+  if constexpr (KIND == LINEAR) {
+    if (g.ksplit > 1) {
+      // part bz of K: kchunk values from bz * kchunk on (a multiple of BK)
+      const int kb = bz * g.kchunk, left = A.k - kb;
+      A.base += (int64_t)kb * (AL == KC ? 1 : A.ld) * EB;
+      B.base += (int64_t)kb * (BL == KC ? 1 : B.ld) * EB;
+      A.k = B.k = left < g.kchunk ? left : g.kchunk;
+      C = (char*)(g.P + (int64_t)bz * g.M * g.N);
+    }
   }
 
   int a_rows[TM], b_rows[TN];
@@ -708,16 +720,12 @@ __device__ __forceinline__ void ring_epilogue(const KArgs& g, char* C, f32x4_t (
     // part; a part stores 4 times, or 8 with the values before the activation,
     // which only makes the counts below wait for more than they have to.
     const int c0 = n0 + wn * 128;
-    f32x4_t bias[8];
+    V4 bias[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      bias[j] = f32x4_t{};
+      bias[j] = V4{};
       const int n = c0 + j * 16 + nl;
-      if (g.bias && n < g.N) {
-        const V4 b = *(const V4*)(g.bias + (int64_t)n * 2);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bias[j][e] = E::to_f32(b[e]);
-      }
+      if (g.bias && n < g.N) bias[j] = *(const V4*)(g.bias + (int64_t)n * 2);
     }
     auto parts = [&](auto RES) {
       constexpr bool kRes = decltype(RES)::value;
@@ -749,7 +757,9 @@ __device__ __forceinline__ void ring_epilogue(const KArgs& g, char* C, f32x4_t (
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           V4 v;
-          f32x4_t z = acc[q][j] + bias[j];
+          f32x4_t z;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = acc[q][j][e] + E::to_f32(bias[j][e]);
           if (g.z) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = E::from_f32(z[e]);

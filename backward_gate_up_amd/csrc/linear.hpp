@@ -110,18 +110,22 @@ __global__ void __launch_bounds__(NW * 64, (NW == 4 ? 2 : 1)) lin_few(const FewA
   ring::wait_vmcnt<0>();  // no load may land in LDS after the workgroup's end
 }
 
-// The epilogue on the sums of the splits' parts, four columns of a token per thread.
+// The epilogue on the sums of parts, four columns of a row per thread, for one or
+// two products (qa and qb such quads).
 template <class E>
-__global__ void __launch_bounds__(256) lin_join(const KArgs g, const float* partial, int splits, int64_t quads) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) lin_join(const KArgs a, const KArgs b, int64_t qa, int64_t qb) {
+  const int64_t blocks = (qa + 255) / 256;
+  const bool second = blockIdx.x >= blocks;
+  const KArgs& g = second ? b : a;
+  const int64_t quads = second ? qb : qa, i = (blockIdx.x - (second ? blocks : 0)) * 256 + threadIdx.x;
   if (i >= quads) return;
   f32x4_t v{};
-  for (int s0 = 0; s0 < splits; s0 += 4) {
-    f32x4_t b[4];
+  for (int s0 = 0; s0 < g.ksplit; s0 += 4) {
+    f32x4_t p[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) b[s] = s0 + s < splits ? ((const f32x4_t*)partial)[(s0 + s) * quads + i] : f32x4_t{};
+    for (int s = 0; s < 4; ++s) p[s] = s0 + s < g.ksplit ? ((const f32x4_t*)g.P)[(s0 + s) * quads + i] : f32x4_t{};
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v += b[s];
+    for (int s = 0; s < 4; ++s) v += p[s];
   }
   const int q = g.N / 4;
   linear_store<E>(g, (int)(i / q), (int)(i % q) * 4, v);
@@ -139,13 +143,13 @@ struct DzArgs {
   int64_t T;
   int N, act;
 };
-template <class E, int ACT>
+template <class E, int ACT, int STEP>
 __device__ __forceinline__ void dz_rows(const DzArgs& g, int at, int64_t t0, int64_t t1, float (&sum)[16 / E::kBytes]) {
   using P = norm::Piece<E>;
   constexpr int V = P::V;
   const int64_t rowb = (int64_t)g.N * E::kBytes;
 #pragma unroll 4
-  for (int64_t t = t0; t < t1; t += 4) {
+  for (int64_t t = t0; t < t1; t += STEP) {
     P dy, z, dz;
     dy.template load<true>(g.dy + t * rowb, at, g.N);
     if constexpr (ACT != SWIGLU_ACT_NONE) z.template load<true>(g.z + t * rowb, at, g.N);
@@ -161,6 +165,14 @@ __device__ __forceinline__ void dz_rows(const DzArgs& g, int at, int64_t t0, int
     if constexpr (ACT != SWIGLU_ACT_NONE) dz.template store<true>(g.dz + t * rowb, at, g.N);
   }
 }
+template <class E, int STEP>
+__device__ __forceinline__ void dz_rows_of(const DzArgs& g, int at, int64_t t0, int64_t t1, float (&sum)[16 / E::kBytes]) {
+  if (!g.z) dz_rows<E, SWIGLU_ACT_NONE, STEP>(g, at, t0, t1, sum);
+  else if (g.act == SWIGLU_ACT_RELU) dz_rows<E, SWIGLU_ACT_RELU, STEP>(g, at, t0, t1, sum);
+  else if (g.act == SWIGLU_ACT_GELU) dz_rows<E, SWIGLU_ACT_GELU, STEP>(g, at, t0, t1, sum);
+  else if (g.act == SWIGLU_ACT_GELU_TANH) dz_rows<E, SWIGLU_ACT_GELU_TANH, STEP>(g, at, t0, t1, sum);
+  else dz_rows<E, SWIGLU_ACT_SILU, STEP>(g, at, t0, t1, sum);
+}
 template <class E>
 __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
   constexpr int V = 16 / E::kBytes;
@@ -169,13 +181,7 @@ __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
   const int at = (blockIdx.x * 64 + lane) * V;
   const int64_t t0 = g.T * blockIdx.y / gridDim.y + wave, t1 = g.T * (blockIdx.y + 1) / gridDim.y;
   float sum[V] = {};
-  if (at < g.N) {
-    if (!g.z) dz_rows<E, SWIGLU_ACT_NONE>(g, at, t0, t1, sum);
-    else if (g.act == SWIGLU_ACT_RELU) dz_rows<E, SWIGLU_ACT_RELU>(g, at, t0, t1, sum);
-    else if (g.act == SWIGLU_ACT_GELU) dz_rows<E, SWIGLU_ACT_GELU>(g, at, t0, t1, sum);
-    else if (g.act == SWIGLU_ACT_GELU_TANH) dz_rows<E, SWIGLU_ACT_GELU_TANH>(g, at, t0, t1, sum);
-    else dz_rows<E, SWIGLU_ACT_SILU>(g, at, t0, t1, sum);
-  }
+  if (at < g.N) dz_rows_of<E, 4>(g, at, t0, t1, sum);
   if (!g.partial) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) red[wave][i][lane] = sum[i];
@@ -183,6 +189,30 @@ __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
   for (int i = threadIdx.x; i < 64 * V; i += 256) {
     const int n = blockIdx.x * 64 * V + i, l = i / V, e = i % V;
     if (n < g.N) g.partial[(int64_t)blockIdx.y * g.N + n] = ((red[0][e][l] + red[1][e][l]) + red[2][e][l]) + red[3][e][l];
+  }
+}
+// The same with all rows in one workgroup of sixteen waves per 256 bytes of columns,
+// which writes db itself: up to kDzRows rows one launch less is worth more than
+// the strips.
+constexpr int kDzRows = 512;
+template <class E>
+__global__ void __launch_bounds__(1024) lin_dz_few(const DzArgs g, char* db) {
+  constexpr int V = 16 / E::kBytes;
+  __shared__ float red[64][16 * V + 1];
+  const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const int at = (blockIdx.x * 16 + col) * V;
+  float sum[V] = {};
+  if (at < g.N) dz_rows_of<E, 64>(g, at, row, g.T, sum);
+  if (!db) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[row][col * V + i] = sum[i];
+  __syncthreads();
+  const int n = blockIdx.x * 16 * V + threadIdx.x;
+  if (threadIdx.x < 16 * V && n < g.N) {
+    float v = 0.f;
+#pragma unroll 16
+    for (int r = 0; r < 64; ++r) v += red[r][threadIdx.x];
+    ((typename E::elem*)db)[n] = E::from_f32(v);
   }
 }
 static inline int dz_strips(int64_t T, int64_t N, size_t e) {
@@ -221,31 +251,358 @@ static inline int few_splits(int64_t T, int64_t N, int64_t K, size_t e) {
   if (s > most) s = most;
   return s < 2 ? 1 : s > 16 ? 16 : (int)s;
 }
+
+// How a product [M, N] over K runs: on register-staged tiles, several workgroups
+// per CU, or (16 bits) on the ring of 256 x 256 tiles, one per CU, which is the
+// fastest where there are enough of them; with K split where there are too few
+// tiles for the CUs (of the ring's, those of a last round that fills less than
+// all), the parts being joined by a second launch.
+//
+// Chosen by the time of a model in us: a tile takes lat K alone and thr K of its
+// CU's time among others. Measured in ns per unit of K, lat / thr: 64 x 64 7.5 /
+// 3.4 (fp32 19.8 / 15.7), 64 x 128 9.3 / 5.9, 128 x 128 10.7 / 9.3, ring 20.1 /
+// 24.7 (its clock falls as the chip fills). fp32 has only 64 x 64: wider ones were
+// behind at every size but the largest, by 3 % there (M = N = 2000, K = 8000 503
+// against 487 us). What the choice is worth (us, unsplit 64 x 64 / 128 x 128 / best
+// split; bf16): 256 x 1024, K = 8192 62 / 88 / 17.5; 4096 x 2048, K = 5632 154 /
+// 105, on the ring 113; 4096 x 5632, K = 2048 164 / 118, ring 96.
+enum { T64 = 0, T64x128 = 1, T128 = 2, TRING = 3 };
+struct Product {
+  int tile, splits, kchunk;  // kchunk: K values per part (ring: stages)
+  int n_full, n_split;       // ring
+  double us;
+};
+struct TileCost {
+  int bm, bn;
+  double lat, thr;
+};
+static inline TileCost tile_cost(int tile, size_t e) {
+  if (e == 4) return {64, 64, 19.8e-3, 15.7e-3};
+  if (tile == T64) return {64, 64, 7.5e-3, 3.4e-3};
+  if (tile == T64x128) return {64, 128, 9.3e-3, 5.9e-3};
+  if (tile == T128) return {128, 128, 10.7e-3, 9.3e-3};
+  return {256, 256, 20.1e-3, 24.7e-3};
+}
+// Writing and reading fp32 parts, and the launch that joins them.
+static inline double join_us(double values) { return 5.0 + values * 8 / 5.0e6; }
+static Product plan_product(int64_t M, int64_t N, int64_t K, size_t e) {
+  const int ncu = dev_ncu(), bk = e == 4 ? 32 : 64, nk = K > 0 ? cdiv(K, bk) : 1;
+  Product best{};
+  best.us = 1e30;
+  for (int tile = T64; tile <= (e == 4 ? T64 : T128); ++tile) {
+    const TileCost c = tile_cost(tile, e);
+    const int64_t n = (int64_t)cdiv(M, c.bm) * cdiv(N, c.bn);
+    for (int s = 1; s <= 16 && (s == 1 || (nk / s >= 4 && n * s <= 4 * ncu)); ++s) {
+      const int per = cdiv(nk, s), parts = cdiv(nk, per);
+      if (parts != s) continue;
+      const double load = c.thr * (double)((n * s + ncu - 1) / ncu);
+      const double us = (double)per * bk * (load > c.lat ? load : c.lat) + (s > 1 ? join_us((double)s * M * N) : 0);
+      if (us < best.us) best = {tile, s, per * bk, 0, 0, us};
+    }
+  }
+  if (e == 4) return best;
+  // the ring, where it has at least half a round of tiles
+  const TileCost c = tile_cost(TRING, e);
+  const int64_t nt = (int64_t)cdiv(M, 256) * cdiv(N, 256), rem = nt % ncu;
+  if (2 * nt < ncu) return best;
+  const double tile = (double)nk * bk * c.thr, whole = (double)(nt / ncu) * tile;
+  const double alone = 2 * rem > ncu || nt > rem ? tile : (double)nk * bk * c.lat;
+  if (whole + (rem ? alone : 0) < best.us) best = {TRING, 1, nk, (int)nt, 0, whole + (rem ? alone : 0)};
+  for (int s = 2; rem && s <= 8 && nk / s >= 8; ++s) {
+    const int per = cdiv(nk, s), parts = cdiv(nk, per);
+    if (parts != s) continue;
+    const double us = whole + (double)((rem * s + ncu - 1) / ncu) * tile * per / nk + join_us((double)rem * s * 65536);
+    if (us < 0.97 * best.us) best = {TRING, s, per, (int)(nt - rem), (int)rem, us};
+  }
+  return best;
+}
+static inline size_t product_bytes(const Product& p, int64_t M, int64_t N) {
+  if (p.tile == TRING) return (size_t)p.n_split * p.splits * 65536 * 4;
+  return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
+}
+// The backward's two products, dW [N, K] over T and dx [T, K] over N. Both in one
+// launch, so that the short tiles of one fill the CUs that the other's last round
+// leaves: on the ring (the longer tiles first), or on 64 x 64 tiles, where it also
+// saves a launch; or each on its own as above. The ring's two, T = 4096, N = 2048,
+// K = 5632, bf16: 176 tiles over 4096 and 352 over 2048 in one launch.
+struct Grads {
+  bool together, ring;
+  Product w, x;
+};
+static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool dx) {
+  Grads g{};
+  if (dw) g.w = plan_product(N, K, T, e);
+  if (dx) g.x = plan_product(T, K, N, e);
+  if (!dw || !dx || T == 0) return g;
+  double best = g.w.us + g.x.us + 3.0;
+  const int ncu = dev_ncu();
+  {
+    // 64 x 64 tiles together: each product's parts as many as it takes alone
+    const TileCost c = tile_cost(T64, e);
+    const int bk = e == 4 ? 32 : 64;
+    auto split = [&](int64_t M, int64_t n_cols, int64_t len) {
+      const int nk = cdiv(len, bk);
+      const int64_t n = (int64_t)cdiv(M, 64) * cdiv(n_cols, 64);
+      Product p{T64, 1, nk * bk, 0, 0, 0};
+      for (int s = 2; s <= 16 && nk / s >= 4 && n * s <= 2 * ncu; ++s) {
+        const int per = cdiv(nk, s);
+        if (cdiv(nk, per) == s) p = {T64, s, per * bk, 0, 0, 0};
+      }
+      return p;
+    };
+    const Product w = split(N, K, T), x = split(T, K, N);
+    const double nw = (double)cdiv(N, 64) * cdiv(K, 64), nx = (double)cdiv(T, 64) * cdiv(K, 64);
+    const double load = c.thr * (nw * T + nx * N) / ncu;
+    const double lat = c.lat * (w.kchunk > x.kchunk ? w.kchunk : x.kchunk);
+    const double parts = (w.splits > 1 ? (double)w.splits * N * K : 0) + (x.splits > 1 ? (double)x.splits * T * K : 0);
+    // (the last tiles to start end half a tile late)
+    const double us = (load > lat ? load + 0.5 * lat : lat) + (parts > 0 ? join_us(parts) : 0);
+    if (us < best) {
+      best = us;
+      g = {true, false, w, x};
+    }
+  }
+  if (e == 2) {
+    const TileCost c = tile_cost(TRING, e);
+    const int64_t nw = (int64_t)cdiv(N, 256) * cdiv(K, 256), nx = (int64_t)cdiv(T, 256) * cdiv(K, 256);
+    // a tiles of length l first, then b of length s
+    const int64_t a = T >= N ? nw : nx, b = T >= N ? nx : nw;
+    const double l = (T >= N ? T : N) * c.thr, s = (T >= N ? N : T) * c.thr;
+    const int64_t r = a % ncu, meanwhile = r ? (ncu - r) * (int64_t)(l / s) : 0;
+    const int64_t rest = b > meanwhile ? b - meanwhile : 0;
+    const double us = (double)(a / ncu) * l + (r ? l : 0) + (double)((rest + ncu - 1) / ncu) * s;
+    // (the two together run 3 to 5 % slower than each alone at its best: their panels share L2)
+    if (nw + nx >= ncu && 1.05 * us < best) {
+      best = us;
+      g = {true, true, Product{TRING, 1, 0, (int)nw, 0, 0}, Product{TRING, 1, 0, (int)nx, 0, 0}};
+    }
+  }
+  return g;
+}
+
+// Plans by their sizes: a model calls with the same few, and a plan takes about as
+// long as a launch.
+template <class P>
+struct Plans {
+  struct Key {
+    int64_t T = -1, N = 0, K = 0, form = 0;
+    bool operator==(const Key& o) const { return T == o.T && N == o.N && K == o.K && form == o.form; }
+  };
+  static constexpr int kSlots = 64;
+  Key key[kSlots];
+  P plan[kSlots];
+  template <class Make>
+  const P& get(int64_t T, int64_t N, int64_t K, int64_t form, Make&& make) {
+    Key k;
+    k.T = T;
+    k.N = N;
+    k.K = K;
+    k.form = form * 4096 + dev_ncu();
+    const int i = (int)(((uint64_t)(T * 31 + N * 7 + K * 3 + form) * 0x9E3779B97F4A7C15ull) >> 58);
+    if (!(key[i] == k)) {
+      plan[i] = make();
+      key[i] = k;
+    }
+    return plan[i];
+  }
+};
+static inline Product fwd_plan(int64_t T, int64_t N, int64_t K, size_t e) {
+  static thread_local Plans<Product> plans;
+  return plans.get(T, N, K, (int64_t)e, [&] { return plan_product(T, N, K, e); });
+}
 static inline size_t fwd_bytes(int64_t T, int64_t N, int64_t K, size_t e) {
-  if (T <= 0 || T > kFewT) return 0;
+  if (T <= 0) return 0;
+  if (T > kFewT) return product_bytes(fwd_plan(T, N, K, e), T, N);
   const int s = few_splits(T, N, K, e);
   return s > 1 ? (size_t)s * T * N * 4 : 0;
 }
 
 // Backward workspace: dz, then the column sums' parts or (they come one after the
-// other) the weight gradient's parts, each 256-byte aligned.
-static inline bool ring_dw(int64_t T, size_t e) { return e == 2 && T > 512; }
+// other) the products' parts, each 256-byte aligned. grads: by what is wanted, 1
+// dW, 2 dx, 3 both.
 struct BwdPlan {
-  size_t sums, total;
+  size_t parts, total;
   int strips;
+  Grads grads[4];
 };
-static inline BwdPlan bwd_plan(int64_t T, int64_t N, int64_t K, size_t e, bool act) {
+static BwdPlan make_bwd_plan(int64_t T, int64_t N, int64_t K, size_t e, bool act) {
   BwdPlan p{};
-  p.strips = dz_strips(T, N, e);
-  p.sums = act ? align256((size_t)T * N * e) : 0;
-  size_t parts = (size_t)p.strips * N * 4;
-  if (ring_dw(T, e)) {
-    const WgradPlan w = wgrad_plan(cdiv(N, 256) * cdiv(K, 256), T, dev_ncu(), wgrad_bk<STAGE_LINEAR_DW>());
-    const size_t b = (size_t)w.n_split * w.ksplit * 65536 * 4;
-    if (b > parts) parts = b;
+  p.strips = T <= kDzRows ? 0 : dz_strips(T, N, e);
+  p.parts = act ? align256((size_t)T * N * e) : 0;
+  size_t most = (size_t)p.strips * N * 4;
+  for (int wants = 1; wants <= 3; ++wants) {
+    const Grads g = p.grads[wants] = plan_grads(T, N, K, e, wants & 1, wants & 2);
+    const size_t w = wants & 1 ? align256(product_bytes(g.w, N, K)) : 0;
+    const size_t b = w + (wants & 2 ? product_bytes(g.x, T, K) : 0);
+    if (b > most) most = b;
   }
-  p.total = p.sums + align256(parts);
+  p.total = p.parts + align256(most);
   return p;
+}
+static inline BwdPlan bwd_plan(int64_t T, int64_t N, int64_t K, size_t e, bool act) {
+  static thread_local Plans<BwdPlan> plans;
+  return plans.get(T, N, K, (int64_t)e * 2 + act, [&] { return make_bwd_plan(T, N, K, e, act); });
+}
+
+// ---- launches ------------------------------------------------------------------------
+// A product on register-staged tiles: LINEAR's epilogue, or its parts.
+template <class E, int BM, int BN, int AL, int BL, int STAGE>
+__global__ void __launch_bounds__(256, (BM == 64 && BN == 64 ? 3 : 2)) lin_tile(const KArgs g) {
+  __shared__ __attribute__((aligned(16))) char smem[Geometry<E, BM, BN, AL, BL>::LDS];
+  const int nt = g.tiles_m * g.tiles_n, b = blockIdx.x;
+  gemm_tile<E, BM, BN, AL, BL, LINEAR>(g, smem, b % nt, b / nt);
+}
+// dW and dx on 64 x 64 tiles.
+template <class E>
+__global__ void __launch_bounds__(256, 3) lin_tile_grads(const KArgs w, const KArgs x) {
+  constexpr int LW = Geometry<E, 64, 64, MC, MC>::LDS, LX = Geometry<E, 64, 64, KC, MC>::LDS;
+  __shared__ __attribute__((aligned(16))) char smem[LW > LX ? LW : LX];
+  const int nw = w.tiles_m * w.tiles_n, nx = x.tiles_m * x.tiles_n, b = blockIdx.x - nw * w.ksplit;
+  if (b < 0) gemm_tile<E, 64, 64, MC, MC, LINEAR>(w, smem, blockIdx.x % nw, blockIdx.x / nw);
+  else gemm_tile<E, 64, 64, KC, MC, LINEAR>(x, smem, b % nx, b / nx);
+}
+
+// The ring: the first n_full tiles, with the epilogue.
+template <class E, int ACT>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring(const KArgs g) {
+  SWIGLU_RING_LDS(true)
+  ring5_tile<E, KC, KC, LINEAR, ACT>(g, R, blockIdx.x, 0);
+}
+// The parts of the tiles from n_full on (a kernel that ended in either the
+// epilogue or a part's sums spilled accumulators: 1210 us became 1314).
+template <class E>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring_parts(const KArgs g) {
+  SWIGLU_RING_LDS(true)
+  const int piece = blockIdx.x;
+  ring5_tile<E, KC, KC, PLAIN>(g, R, g.n_full + piece / g.ksplit, 0, piece % g.ksplit, piece);
+}
+// dx: whole tiles, then parts. (The host pass of the compiler refuses to
+// instantiate this tile from two kernels.)
+template <class E>
+__device__ __forceinline__ void dx_tile(const KArgs& g, char* const (&R)[5], int item, int ks, int piece) {
+  ring5_tile<E, KC, MC, PLAIN>(g, R, item, 0, ks, piece);
+}
+template <class E>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring_dx(const KArgs g) {
+  SWIGLU_RING_LDS(true)
+  int item = blockIdx.x, ks = 0, piece = -1;
+  if (item >= g.n_full) {
+    piece = item - g.n_full;
+    item = g.n_full + piece / g.ksplit;
+    ks = piece % g.ksplit;
+  }
+  dx_tile<E>(g, R, item, ks, piece);
+}
+// Joins the parts of the ring's split tiles: four columns of a row per thread.
+template <class E>
+__global__ void __launch_bounds__(256) lin_join_tiles(const KArgs g) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int r = (int)(i >> 14), rr = (int)(i >> 6) & 255, cq = (int)i & 63;
+  int tm, tn;
+  tile_coords(g.n_full + r, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+  const int m = tm * 256 + rr, n = tn * 256 + cq * 4;
+  if (m >= g.M || n >= g.N) return;
+  const float* p = g.P + (int64_t)r * g.ksplit * 65536 + rr * 256 + cq * 4;
+  f32x4_t sum{};
+  for (int s = 0; s < g.ksplit; ++s) sum += *(const f32x4_t*)(p + (int64_t)s * 65536);
+  linear_store<E>(g, m, n, sum);
+}
+// dW and dx on the ring, the longer tiles first.
+template <class E>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+lin_ring_grads(const KArgs w, const KArgs x, int first) {
+  SWIGLU_RING_LDS(true)
+  const int nw = w.tiles_m * w.tiles_n, nx = x.tiles_m * x.tiles_n, b = blockIdx.x;
+  if (first ? b >= nx : b < nw) ring5_tile<E, MC, MC, PLAIN>(w, R, first ? b - nx : b, 0);
+  else dx_tile<E>(x, R, first ? b : b - nw, 0, -1);
+}
+
+static inline int status() { return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH; }
+
+template <class E, int ACT>
+int launch_lin_ring(const KArgs& a, hipStream_t s) {
+  if (a.n_full) hipLaunchKernelGGL((lin_ring<E, ACT>), dim3(a.n_full), dim3(256), 0, s, a);
+  return status();
+}
+template <class E>
+int launch_lin_ring_parts(const KArgs& a, hipStream_t s) {
+  if (a.n_split) hipLaunchKernelGGL((lin_ring_parts<E>), dim3(a.n_split * a.ksplit), dim3(256), 0, s, a);
+  return status();
+}
+template <class E>
+static int launch_ring_dx(const KArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((lin_ring_dx<E>), dim3(a.n_full + a.n_split * a.ksplit), dim3(256), 0, s, a);
+  return status();
+}
+template <class E>
+static int launch_ring_dw(const KArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((ring_wgrad<E, MC, MC, STAGE_LINEAR_DW>), dim3(a.n_full + a.n_split * a.ksplit), dim3(256), 0, s, a);
+  return status();
+}
+#define SWIGLU_LIN_RING_DECL(PREFIX, E)                                             \
+  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_NONE>(const KArgs&, hipStream_t);      \
+  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_RELU>(const KArgs&, hipStream_t);      \
+  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_GELU>(const KArgs&, hipStream_t);      \
+  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_GELU_TANH>(const KArgs&, hipStream_t); \
+  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_SILU>(const KArgs&, hipStream_t);      \
+  PREFIX template int launch_lin_ring_parts<E>(const KArgs&, hipStream_t);
+
+template <class E, int XR, int NW, int SH, int RING>
+static int launch_few(const FewArgs& a, int grid, hipStream_t s) {
+  StageScope scope(STAGE_LINEAR, s);
+  hipLaunchKernelGGL((lin_few<E, XR, NW, SH, RING>), dim3(grid, a.splits), dim3(NW * 64), 0, s, a);
+  return status();
+}
+template <class E, int XR>
+static int few_own(const FewArgs& a, hipStream_t s) {
+  const int tiles = cdiv(a.f.N, 16), ncu = dev_ncu();
+  if (tiles <= ncu) return launch_few<E, XR, 16, 1, 131072>(a, tiles, s);
+  const int fit = 2 * ncu;
+  return launch_few<E, XR, 4, 1, 65536>(a, tiles < fit ? tiles : fit, s);
+}
+// The parts of up to two products (quads of columns each) joined in one launch.
+template <class E>
+static int launch_join(const KArgs& a, const KArgs& b, hipStream_t s) {
+  const int64_t qa = a.ksplit > 1 ? (int64_t)a.M * a.N / 4 : 0, qb = b.ksplit > 1 ? (int64_t)b.M * b.N / 4 : 0;
+  if (qa + qb == 0) return SWIGLU_OK;
+  hipLaunchKernelGGL((lin_join<E>), dim3((unsigned)((qa + 255) / 256 + (qb + 255) / 256)), dim3(256), 0, s, a, b, qa, qb);
+  return status();
+}
+
+template <class E, int AL, int BL, int STAGE, int BM, int BN>
+static int launch_tiles(KArgs a, hipStream_t s) {
+  a.tiles_m = cdiv(a.M, BM);
+  a.tiles_n = cdiv(a.N, BN);
+  if (a.tiles_m * a.tiles_n == 0) return SWIGLU_OK;
+  hipLaunchKernelGGL((lin_tile<E, BM, BN, AL, BL, STAGE>), dim3(a.tiles_m * a.tiles_n * a.ksplit), dim3(256), 0, s, a);
+  const int rc = status();
+  return rc ? rc : launch_join<E>(a, KArgs{}, s);
+}
+// A product as planned; `ring` launches it there.
+using RingLaunch = int (*)(const KArgs&, hipStream_t);
+template <class E, int AL, int BL, int STAGE>
+static int run_product(KArgs a, const Product& p, float* parts, hipStream_t s, RingLaunch ring, RingLaunch rest = nullptr) {
+  a.planes = 1;
+  a.ksplit = p.splits;
+  a.kchunk = p.kchunk;
+  a.P = parts;
+  if constexpr (E::kBytes == 2) {
+    if (p.tile == TRING) {
+      a.tiles_m = cdiv(a.M, 256);
+      a.tiles_n = cdiv(a.N, 256);
+      a.n_full = p.n_full;
+      a.n_split = p.n_split;
+      a.group_m = 2;
+      int rc = ring(a, s);
+      if (!rc && rest) rc = rest(a, s);
+      if (rc || p.n_split == 0) return rc;
+      hipLaunchKernelGGL((lin_join_tiles<E>), dim3(p.n_split * 64), dim3(256), 0, s, a);
+      return status();
+    }
+    if (p.tile == T64x128) return launch_tiles<E, AL, BL, STAGE, 64, 128>(a, s);
+    if (p.tile == T128) return launch_tiles<E, AL, BL, STAGE, 128, 128>(a, s);
+  }
+  return launch_tiles<E, AL, BL, STAGE, 64, 64>(a, s);
 }
 
 static inline KArgs fwd_args(const Fwd& c) {
@@ -261,56 +618,6 @@ static inline KArgs fwd_args(const Fwd& c) {
   a.z = (char*)c.z;
   a.act = c.act;
   return a;
-}
-
-// ---- many tokens, 16 bits: the ring, its activation fixed at compile time -----------
-template <class E, int ACT>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring(const KArgs g) {
-  SWIGLU_RING_LDS(true)
-  ring5_tile<E, KC, KC, LINEAR, ACT>(g, R, blockIdx.x, 0);
-}
-template <class E, int ACT>
-int launch_lin_ring(KArgs a, hipStream_t s) {
-  a.group_m = 2;
-  StageScope scope(STAGE_LINEAR, s);
-  hipLaunchKernelGGL((lin_ring<E, ACT>), dim3(a.tiles_m * a.tiles_n), dim3(256), 0, s, a);
-  return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
-}
-#define SWIGLU_LIN_RING_DECL(PREFIX, E)                                       \
-  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_NONE>(KArgs, hipStream_t);      \
-  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_RELU>(KArgs, hipStream_t);      \
-  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_GELU>(KArgs, hipStream_t);      \
-  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_GELU_TANH>(KArgs, hipStream_t); \
-  PREFIX template int launch_lin_ring<E, SWIGLU_ACT_SILU>(KArgs, hipStream_t);
-
-template <class E, int XR, int NW, int SH, int RING>
-static int launch_few(const FewArgs& a, int grid, hipStream_t s) {
-  StageScope scope(STAGE_LINEAR, s);
-  hipLaunchKernelGGL((lin_few<E, XR, NW, SH, RING>), dim3(grid, a.splits), dim3(NW * 64), 0, s, a);
-  return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
-}
-template <class E, int XR>
-static int few_own(const FewArgs& a, hipStream_t s) {
-  const int tiles = cdiv(a.f.N, 16), ncu = dev_ncu();
-  if (tiles <= ncu) return launch_few<E, XR, 16, 1, 131072>(a, tiles, s);
-  const int fit = 2 * ncu;
-  return launch_few<E, XR, 4, 1, 65536>(a, tiles < fit ? tiles : fit, s);
-}
-
-// Tiles of 64 rows: the widest that still gives every CU one.
-template <class E, int AL, int BL, int KIND, int STAGE>
-static int launch_rows64(KArgs a, hipStream_t s) {
-  a.tiles_m = cdiv(a.M, 64);
-  if (a.tiles_m * cdiv(a.N, 256) >= dev_ncu()) {
-    a.tiles_n = cdiv(a.N, 256);
-    return launch<E, 64, 256, AL, BL, KIND, STAGE>(a, 1, s);
-  }
-  if (a.tiles_m * cdiv(a.N, 128) >= dev_ncu()) {
-    a.tiles_n = cdiv(a.N, 128);
-    return launch<E, 64, 128, AL, BL, KIND, STAGE>(a, 1, s);
-  }
-  a.tiles_n = cdiv(a.N, 64);
-  return launch<E, 64, 64, AL, BL, KIND, STAGE>(a, 1, s);
 }
 
 template <class E>
@@ -332,82 +639,103 @@ int run_fwd(const Fwd& c) {
     const int rc = launch_few<E, 64, 8, 4, 122880>(f, cdiv(c.N, 64), c.stream);
     if (rc || f.splits == 1) return rc;
     StageScope scope(STAGE_LINEAR, c.stream);
-    const int64_t quads = c.T * c.N / 4;
-    hipLaunchKernelGGL((lin_join<E>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, c.stream, a,
-                       (const float*)f.partial, f.splits, quads);
-    return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
+    a.P = f.partial;
+    a.ksplit = f.splits;
+    return launch_join<E>(a, KArgs{}, c.stream);
   }
+  RingLaunch ring = nullptr, rest = nullptr;
   if constexpr (E::kBytes == 2) {
-    a.tiles_m = cdiv(c.T, 256);
-    a.tiles_n = cdiv(c.N, 256);
-    // (64-row tiles where those fit one round on the CUs, as in the SwiGLU block)
-    if (c.T > 512 && cdiv(c.T, 64) * a.tiles_n > dev_ncu()) {
-      switch (c.act) {
-        case SWIGLU_ACT_RELU: return launch_lin_ring<E, SWIGLU_ACT_RELU>(a, c.stream);
-        case SWIGLU_ACT_GELU: return launch_lin_ring<E, SWIGLU_ACT_GELU>(a, c.stream);
-        case SWIGLU_ACT_GELU_TANH: return launch_lin_ring<E, SWIGLU_ACT_GELU_TANH>(a, c.stream);
-        case SWIGLU_ACT_SILU: return launch_lin_ring<E, SWIGLU_ACT_SILU>(a, c.stream);
-        default: return launch_lin_ring<E, SWIGLU_ACT_NONE>(a, c.stream);
-      }
-    }
+    rest = &launch_lin_ring_parts<E>;
+    ring = c.act == SWIGLU_ACT_RELU        ? &launch_lin_ring<E, SWIGLU_ACT_RELU>
+           : c.act == SWIGLU_ACT_GELU      ? &launch_lin_ring<E, SWIGLU_ACT_GELU>
+           : c.act == SWIGLU_ACT_GELU_TANH ? &launch_lin_ring<E, SWIGLU_ACT_GELU_TANH>
+           : c.act == SWIGLU_ACT_SILU      ? &launch_lin_ring<E, SWIGLU_ACT_SILU>
+                                           : &launch_lin_ring<E, SWIGLU_ACT_NONE>;
   }
-  return launch_rows64<E, KC, KC, LINEAR, STAGE_LINEAR>(a, c.stream);
+  StageScope scope(STAGE_LINEAR, c.stream);
+  return run_product<E, KC, KC, STAGE_LINEAR>(a, fwd_plan(c.T, c.N, c.K, E::kBytes), (float*)c.ws, c.stream, ring, rest);
 }
 
 template <class E>
 int run_bwd(const Bwd& c) {
-  const BwdPlan p = bwd_plan(c.T, c.N, c.K, E::kBytes, c.act != SWIGLU_ACT_NONE);
-  const char* dz = (const char*)c.dy;
-  float* parts = (float*)(c.ws + p.sums);
   const bool act = c.act != SWIGLU_ACT_NONE;
+  const BwdPlan p = bwd_plan(c.T, c.N, c.K, E::kBytes, act);
+  const char* dz = (const char*)c.dy;
+  float* parts = (float*)(c.ws + p.parts);
+  hipStream_t s = c.stream;
   if (c.db || (act && (c.dx || c.dw))) {
-    StageScope scope(STAGE_LINEAR_DZ, c.stream);
-    DzArgs d{(const char*)c.dy, act ? (const char*)c.z : nullptr, act ? c.ws : nullptr, c.db ? parts : nullptr,
-             c.T, (int)c.N, c.act};
+    StageScope scope(STAGE_LINEAR_DZ, s);
+    const char* z = act ? (const char*)c.z : nullptr;
     if (act) dz = c.ws;
-    hipLaunchKernelGGL((lin_dz<E>), dim3((unsigned)((c.N * E::kBytes + 1023) / 1024), p.strips), dim3(256), 0, c.stream, d);
-    if (hipGetLastError() != hipSuccess) return SWIGLU_ERR_LAUNCH;
-    if (c.db) {
-      const int rc = norm::launch_sum_parts<E>(parts, p.strips, 1, c.N, c.db, nullptr, c.stream);
-      if (rc) return rc;
-    }
-  }
-  if (c.dw) {
-    KArgs a{};  // dW [N, K]: rows dz^T, columns x, summed over tokens
-    a.a0 = opnd(dz, c.N, c.N, c.T);
-    a.b0 = opnd(c.x, c.K, c.K, c.T);
-    a.c0 = (char*)c.dw;
-    a.ldc = c.K;
-    a.M = (int)c.N;
-    a.N = (int)c.K;
-    int rc = SWIGLU_OK;
-    bool done = false;
-    if constexpr (E::kBytes == 2) {
-      if (ring_dw(c.T, E::kBytes)) {
-        a.tiles_m = cdiv(a.M, 256);
-        a.tiles_n = cdiv(a.N, 256);
-        rc = launch_ring_wgrad<E, MC, MC, STAGE_LINEAR_DW>(a, 1, parts, c.stream);
-        done = true;
+    if (p.strips == 0) {
+      const DzArgs d{(const char*)c.dy, z, c.ws, nullptr, c.T, (int)c.N, c.act};
+      hipLaunchKernelGGL((lin_dz_few<E>), dim3((unsigned)((c.N * E::kBytes + 255) / 256)), dim3(1024), 0, s, d, (char*)c.db);
+      if (status()) return SWIGLU_ERR_LAUNCH;
+    } else {
+      const DzArgs d{(const char*)c.dy, z, c.ws, c.db ? parts : nullptr, c.T, (int)c.N, c.act};
+      hipLaunchKernelGGL((lin_dz<E>), dim3((unsigned)((c.N * E::kBytes + 1023) / 1024), p.strips), dim3(256), 0, s, d);
+      if (status()) return SWIGLU_ERR_LAUNCH;
+      if (c.db) {
+        const int rc = norm::launch_sum_parts<E>(parts, p.strips, 1, c.N, c.db, nullptr, s);
+        if (rc) return rc;
       }
     }
-    if (!done) rc = launch_rows64<E, MC, MC, PLAIN, STAGE_LINEAR_DW>(a, c.stream);
+  }
+  if (!c.dw && !c.dx) return SWIGLU_OK;
+  KArgs w{}, x{};
+  w.a0 = opnd(dz, c.N, c.N, c.T);  // dW [N, K]: rows dz^T, columns x, summed over tokens
+  w.b0 = opnd(c.x, c.K, c.K, c.T);
+  w.c0 = (char*)c.dw;
+  w.ldc = c.K;
+  w.M = (int)c.N;
+  w.N = (int)c.K;
+  x.a0 = opnd(dz, c.N, c.T, c.N);  // dx [T, K]: rows dz, columns of W, summed over N
+  x.b0 = opnd(c.w, c.K, c.K, c.N);
+  x.c0 = (char*)c.dx;
+  x.ldc = c.K;
+  x.M = (int)c.T;
+  x.N = (int)c.K;
+  const Grads& g = p.grads[(c.dw ? 1 : 0) + (c.dx ? 2 : 0)];
+  float* x_parts = (float*)((char*)parts + (c.dw ? align256(product_bytes(g.w, c.N, c.K)) : 0));
+  if (g.together) {
+    StageScope scope(STAGE_LINEAR_DW, s);
+    if constexpr (E::kBytes == 2) {
+      if (g.ring) {
+        w.tiles_m = cdiv(w.M, 256);
+        x.tiles_m = cdiv(x.M, 256);
+        w.tiles_n = x.tiles_n = cdiv(w.N, 256);
+        w.group_m = x.group_m = 4;
+        hipLaunchKernelGGL((lin_ring_grads<E>), dim3(g.w.n_full + g.x.n_full), dim3(256), 0, s, w, x, c.T >= c.N ? 0 : 1);
+        return status();
+      }
+    }
+    w.tiles_m = cdiv(w.M, 64);
+    x.tiles_m = cdiv(x.M, 64);
+    w.tiles_n = x.tiles_n = cdiv(w.N, 64);
+    w.ksplit = g.w.splits;
+    w.kchunk = g.w.kchunk;
+    w.P = parts;
+    x.ksplit = g.x.splits;
+    x.kchunk = g.x.kchunk;
+    x.P = x_parts;
+    const int n = w.tiles_n * (w.tiles_m * w.ksplit + x.tiles_m * x.ksplit);
+    hipLaunchKernelGGL((lin_tile_grads<E>), dim3(n), dim3(256), 0, s, w, x);
+    const int rc = status();
+    return rc ? rc : launch_join<E>(w, x, s);
+  }
+  RingLaunch dw_ring = nullptr, dx_ring = nullptr;
+  if constexpr (E::kBytes == 2) {
+    dw_ring = &launch_ring_dw<E>;
+    dx_ring = &launch_ring_dx<E>;
+  }
+  if (c.dw) {
+    StageScope scope(STAGE_LINEAR_DW, s);
+    const int rc = run_product<E, MC, MC, STAGE_LINEAR_DW>(w, g.w, parts, s, dw_ring);
     if (rc) return rc;
   }
   if (c.dx) {
-    KArgs a{};  // dx [T, K]: rows dz, columns of W, summed over N
-    a.a0 = opnd(dz, c.N, c.T, c.N);
-    a.b0 = opnd(c.w, c.K, c.K, c.N);
-    a.c0 = (char*)c.dx;
-    a.ldc = c.K;
-    a.M = (int)c.T;
-    a.N = (int)c.K;
-    if constexpr (E::kBytes == 2) {
-      a.tiles_m = cdiv(c.T, 256);
-      a.tiles_n = cdiv(c.K, 256);
-      if (c.T > 512 && cdiv(c.T, 64) * a.tiles_n > dev_ncu())
-        return launch_ring<E, KC, MC, PLAIN, STAGE_LINEAR_DX>(a, 1, c.stream);
-    }
-    return launch_rows64<E, KC, MC, PLAIN, STAGE_LINEAR_DX>(a, c.stream);
+    StageScope scope(STAGE_LINEAR_DX, s);
+    return run_product<E, KC, MC, STAGE_LINEAR_DX>(x, g.x, x_parts, s, dx_ring);
   }
   return SWIGLU_OK;
 }

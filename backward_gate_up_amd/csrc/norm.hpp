@@ -117,7 +117,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (&red)[2][K][16], i
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
   if constexpr (W > 1) {
-    const int wave = threadIdx.x >> 6;
+    const int wave = (threadIdx.x >> 6) % W;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) red[at][k][wave] = v[k];
@@ -293,53 +293,60 @@ __device__ __forceinline__ void load_stats(const Args& g, int64_t t, float& mean
   rstd = g.stats[RMS ? t : g.T + t];
 }
 
+// Rows that a workgroup works on at a time: as many groups of W waves as its
+// registers allow, so that the sums over rows meet in LDS before they leave the
+// workgroup (one of sixteen waves per CU instead of two of four: 16384 x 4096 bf16
+// BWD_MEASURED).
+template <int W, int NC>
+constexpr int kBwdRows = W == 1 ? (NC == 4 ? 8 : 16) : W == 4 ? (NC == 4 ? 2 : 4) : 1;
+
 // dx of every row and the workgroup's sums of dw (and db) in partial[blockIdx.x].
 template <class E, bool RMS, int W, int NC, bool EVEN>
-__global__ void __launch_bounds__(kThreads<W>, (W == 16 ? 4 : 2)) norm_bwd(const Args g) {
+__global__ void __launch_bounds__((64 * W * kBwdRows<W, NC>)) norm_bwd(const Args g) {
   using P = Piece<E>;
-  constexpr int V = P::V, K = RMS ? 1 : 2;
-  __shared__ float red[2][K][16];
-  // W = 1: the waves' sums of the weight's gradient, one after another
-  __shared__ float join[W == 1 ? K * 64 * NC * V : 1];
-  const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x, wave = threadIdx.x >> 6;
-  const int64_t rowb = (int64_t)g.D * E::kBytes, step = (int64_t)gridDim.x * kRows<W>;
-  int64_t t = (int64_t)blockIdx.x * kRows<W> + (W == 1 ? wave : 0);
+  constexpr int V = P::V, K = RMS ? 1 : 2, R = kBwdRows<W, NC>;
+  __shared__ float red[R][2][K][16];
+  // half of the groups' sums of the weight's gradient, one lane's value apart
+  __shared__ float join[R > 1 ? R / 2 * K * NC * V * 64 * W : 1];
+  const int lane = threadIdx.x % (64 * W);
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * W));
+  const int64_t rowb = (int64_t)g.D * E::kBytes, step = (int64_t)gridDim.x * R;
+  int64_t t = (int64_t)blockIdx.x * R + group;
   int where[NC];
   P w[NC];
-  float dw[NC][V], db[RMS ? 1 : NC][RMS ? 1 : V];
+  float sum[K][NC][V];  // dw, db
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     where[c] = (c * 64 * W + lane) * V;
     w[c].template load<EVEN>(g.w, where[c], g.D);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      dw[c][i] = 0.f;
-      if constexpr (!RMS) db[c][i] = 0.f;
-    }
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k) sum[k][c][i] = 0.f;
   }
   int at = 0;
   P x[NC], dy[NC];
   float mean = 0.f, rstd = 0.f;
-  if (t < g.T) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      x[c].template load<EVEN>(g.x + t * rowb, where[c], g.D);
-      dy[c].template load<EVEN>(g.dy + t * rowb, where[c], g.D);
-    }
-    load_stats<RMS>(g, t, mean, rstd);
-  }
-  while (t < g.T) {
-    const int64_t next = t + step;
-    P nx[NC], ndy[NC];
-    float nmean = 0.f, nrstd = 0.f;
-    if (kAhead<W> && next < g.T) {
+  // rows past the last are zeros and not stored: every group passes every barrier
+  auto load = [&](P (&xs)[NC], P (&ds)[NC], float& m, float& r, int64_t row) {
+    if (row < g.T) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        nx[c].template load<EVEN>(g.x + next * rowb, where[c], g.D);
-        ndy[c].template load<EVEN>(g.dy + next * rowb, where[c], g.D);
+        xs[c].template load<EVEN>(g.x + row * rowb, where[c], g.D);
+        ds[c].template load<EVEN>(g.dy + row * rowb, where[c], g.D);
       }
-      load_stats<RMS>(g, next, nmean, nrstd);
+      load_stats<RMS>(g, row, m, r);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) xs[c].v = ds[c].v = u32x4_t{};
+      m = r = 0.f;
     }
+  };
+  load(x, dy, mean, rstd, t);
+  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < g.T; t0 += step, t += step) {
+    P nx[NC], ndy[NC];
+    float nmean = 0.f, nrstd = 0.f;
+    if constexpr (kAhead<W>) load(nx, ndy, nmean, nrstd, t + step);
     float s[K] = {};  // sum of g n, sum of g (zeros past the row's end: dy is 0 there)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -348,31 +355,32 @@ __global__ void __launch_bounds__(kThreads<W>, (W == 16 ? 4 : 2)) norm_bwd(const
       for (int i = 0; i < V; ++i) {
         const float n = (x[c].get(i) - mean) * rstd, d = dy[c].get(i), gg = d * w[c].get(i);
         s[0] = fmaf(gg, n, s[0]);
-        dw[c][i] = fmaf(d, n, dw[c][i]);
+        sum[0][c][i] = fmaf(d, n, sum[0][c][i]);
         if constexpr (!RMS) {
           s[K - 1] += gg;
-          db[c][i] += d;
+          sum[K - 1][c][i] += d;
         }
       }
     }
-    row_sum<W, K>(s, red, at);
-    const float along = s[0] * g.inv_d, level = RMS ? 0.f : s[K - 1] * g.inv_d;
+    row_sum<W, K>(s, red[group], at);
+    if (t < g.T) {
+      const float along = s[0] * g.inv_d, level = RMS ? 0.f : s[K - 1] * g.inv_d;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if (where[c] >= g.D) continue;
-      P dx, r;
-      dx.v = r.v = u32x4_t{};
-      if (g.dres) r.template load<EVEN>(g.dres + t * rowb, where[c], g.D);
+      for (int c = 0; c < NC; ++c) {
+        if (where[c] >= g.D) continue;
+        P dx, r;
+        dx.v = r.v = u32x4_t{};
+        if (g.dres) r.template load<EVEN>(g.dres + t * rowb, where[c], g.D);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float n = (x[c].get(i) - mean) * rstd, gg = dy[c].get(i) * w[c].get(i);
-        float v = (fmaf(-n, along, gg) - level) * rstd;
-        if (g.dres) v += r.get(i);
-        dx.put(i, E::from_f32(v));
+        for (int i = 0; i < V; ++i) {
+          const float n = (x[c].get(i) - mean) * rstd, gg = dy[c].get(i) * w[c].get(i);
+          float v = (fmaf(-n, along, gg) - level) * rstd;
+          if (g.dres) v += r.get(i);
+          dx.put(i, E::from_f32(v));
+        }
+        dx.template store<EVEN>(g.y + t * rowb, where[c], g.D);
       }
-      dx.template store<EVEN>(g.y + t * rowb, where[c], g.D);
     }
-    t = next;
     if constexpr (kAhead<W>) {
       mean = nmean;
       rstd = nrstd;
@@ -381,93 +389,89 @@ __global__ void __launch_bounds__(kThreads<W>, (W == 16 ? 4 : 2)) norm_bwd(const
         x[c] = nx[c];
         dy[c] = ndy[c];
       }
-    } else if (t < g.T) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        x[c].template load<EVEN>(g.x + t * rowb, where[c], g.D);
-        dy[c].template load<EVEN>(g.dy + t * rowb, where[c], g.D);
-      }
-      load_stats<RMS>(g, t, mean, rstd);
+    } else {
+      load(x, dy, mean, rstd, t + step);
     }
   }
+  // the groups' sums, halved until the first has them all
+#pragma unroll
+  for (int half = R / 2; half; half /= 2) {
+    if (half < R / 2) __syncthreads();  // the last half's have been read
+    float* p = join + (group % half) * (K * NC * V * 64 * W) + lane;
+    if (group >= half && group < 2 * half) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int k = 0; k < K; ++k) p[((k * NC + c) * V + i) * 64 * W] = sum[k][c][i];
+    }
+    __syncthreads();
+    if (group < half) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int k = 0; k < K; ++k) sum[k][c][i] += p[((k * NC + c) * V + i) * 64 * W];
+    }
+  }
+  if (group) return;
   float* out = g.partial + (int64_t)blockIdx.x * K * g.D;
-  if constexpr (W == 1) {
-    // wave 0 puts its sums down, each next one adds its own; the last hands on
-    for (int v = 0; v < 4; ++v) {
-      if (wave == v) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+  for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float* p = join + (c * V + i) * 64 + lane;  // lanes on neighbouring banks
-            *p = v ? *p + dw[c][i] : dw[c][i];
-            if constexpr (!RMS) {
-              p += 64 * NC * V;
-              *p = v ? *p + db[c][i] : db[c][i];
-            }
-          }
+    for (int i = 0; i < V; ++i)
+      if (where[c] + i < g.D) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) out[(int64_t)k * g.D + where[c] + i] = sum[k][c][i];
       }
-      __syncthreads();
-    }
-    for (int i = threadIdx.x; i < K * g.D; i += 256) {
-      const int k = !RMS && i >= g.D, d = i - k * g.D;
-      const int c = d / (64 * V), l = d / V % 64, e = d % V;
-      out[i] = join[k * 64 * NC * V + (c * V + e) * 64 + l];
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (where[c] + i < g.D) {
-          out[where[c] + i] = dw[c][i];
-          if constexpr (!RMS) out[g.D + where[c] + i] = db[c][i];
-        }
-  }
 }
 
 // Rows wider than sixteen waves hold: dx (two walks), the weight's gradient in a
 // launch of its own.
 template <class E, bool RMS>
-__global__ void __launch_bounds__(1024) norm_bwd_wide(const Args g) {
+__device__ __forceinline__ void bwd_row(const Args& g, int64_t t, float (&red)[2][RMS ? 1 : 2][16], int& at) {
   using P = Piece<E>;
   constexpr int V = P::V, K = RMS ? 1 : 2;
-  __shared__ float red[2][K][16];
   const int64_t rowb = (int64_t)g.D * E::kBytes;
-  int at = 0;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    float mean, rstd, s[K] = {};
-    load_stats<RMS>(g, t, mean, rstd);
-    for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
-      P x, dy, w;
-      x.load(g.x + t * rowb, d, g.D);
-      dy.load(g.dy + t * rowb, d, g.D);
-      w.load(g.w, d, g.D);
+  float mean, rstd, s[K] = {};
+  load_stats<RMS>(g, t, mean, rstd);
+  for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
+    P x, dy, w;
+    x.load(g.x + t * rowb, d, g.D);
+    dy.load(g.dy + t * rowb, d, g.D);
+    w.load(g.w, d, g.D);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float gg = dy.get(i) * w.get(i);
-        s[0] = fmaf(gg, (x.get(i) - mean) * rstd, s[0]);
-        if constexpr (!RMS) s[K - 1] += gg;
-      }
-    }
-    row_sum<16, K>(s, red, at);
-    const float along = s[0] * g.inv_d, level = RMS ? 0.f : s[K - 1] * g.inv_d;
-    for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
-      P x, dy, w, r, dx;
-      x.load(g.x + t * rowb, d, g.D);
-      dy.load(g.dy + t * rowb, d, g.D);
-      w.load(g.w, d, g.D);
-      r.v = dx.v = u32x4_t{};
-      if (g.dres) r.load(g.dres + t * rowb, d, g.D);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v = (fmaf(-(x.get(i) - mean) * rstd, along, dy.get(i) * w.get(i)) - level) * rstd;
-        if (g.dres) v += r.get(i);
-        dx.put(i, E::from_f32(v));
-      }
-      dx.store(g.y + t * rowb, d, g.D);
+    for (int i = 0; i < V; ++i) {
+      const float gg = dy.get(i) * w.get(i);
+      s[0] = fmaf(gg, (x.get(i) - mean) * rstd, s[0]);
+      if constexpr (!RMS) s[K - 1] += gg;
     }
   }
+  row_sum<16, K>(s, red, at);
+  const float along = s[0] * g.inv_d, level = RMS ? 0.f : s[K - 1] * g.inv_d;
+  for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
+    P x, dy, w, r, dx;
+    x.load(g.x + t * rowb, d, g.D);
+    dy.load(g.dy + t * rowb, d, g.D);
+    w.load(g.w, d, g.D);
+    r.v = dx.v = u32x4_t{};
+    if (g.dres) r.load(g.dres + t * rowb, d, g.D);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v = (fmaf(-(x.get(i) - mean) * rstd, along, dy.get(i) * w.get(i)) - level) * rstd;
+      if (g.dres) v += r.get(i);
+      dx.put(i, E::from_f32(v));
+    }
+    dx.store(g.y + t * rowb, d, g.D);
+  }
+}
+template <class E, bool RMS>
+__global__ void __launch_bounds__(1024) norm_bwd_wide(const Args g) {
+  __shared__ float red[2][RMS ? 1 : 2][16];
+  int at = 0;
+  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) bwd_row<E, RMS>(g, t, red, at);
 }
 // A lane's piece of columns over the rows of strip blockIdx.y.
 template <class E, bool RMS>
@@ -498,6 +502,59 @@ __global__ void __launch_bounds__(256) norm_wgrad_wide(const Args g) {
       out[i] = dw[i];
       if constexpr (!RMS) out[g.D + i] = db[i];
     }
+}
+
+// At most kFewRows rows in one launch, without partial sums: a workgroup per row
+// for dx, as above, then a workgroup per 64 pieces of columns for dw and db, whose
+// sixteen waves take every sixteenth row (x and dy come from L2 there; mean and
+// rstd are known, so neither half waits for the other).
+constexpr int kFewRows = 256;
+template <class E, bool RMS>
+__global__ void __launch_bounds__(1024) norm_bwd_few(const Args g, char* dw_out, char* db_out) {
+  using P = Piece<E>;
+  constexpr int V = P::V, K = RMS ? 1 : 2;
+  __shared__ union {
+    float sum[2][K][16];
+    float cols[16][64 * V];
+  } lds;
+  if (blockIdx.x < g.T) {
+    int at = 0;
+    bwd_row<E, RMS>(g, blockIdx.x, lds.sum, at);
+    return;
+  }
+  const int64_t rowb = (int64_t)g.D * E::kBytes;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = (int)(blockIdx.x - g.T) * 64 * V, at = first + lane * V;
+  float dw[V] = {}, db[V] = {};
+  if (at < g.D) {
+#pragma unroll 4
+    for (int64_t t = wave; t < g.T; t += 16) {
+      float mean, rstd;
+      load_stats<RMS>(g, t, mean, rstd);
+      P x, dy;
+      x.load(g.x + t * rowb, at, g.D);
+      dy.load(g.dy + t * rowb, at, g.D);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dw[i] = fmaf(dy.get(i), (x.get(i) - mean) * rstd, dw[i]);
+        if constexpr (!RMS) db[i] += dy.get(i);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) lds.cols[wave][lane * V + i] = k ? db[i] : dw[i];
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c < 64 * V && first + c < g.D) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) v += lds.cols[w][c];
+      char* out = k ? db_out : dw_out;
+      if (out) ((typename E::elem*)out)[first + c] = E::from_f32(v);
+    }
+  }
 }
 
 // ---- column sums over parts -------------------------------------------------------
@@ -567,18 +624,20 @@ static inline int64_t groups(int64_t T, int rows, int64_t most) {
   const int64_t n = (T + rows - 1) / rows;
   return n < most ? n : most;
 }
-// Workgroups of the backward, each of which leaves a row of partial sums: two per
-// CU (one of sixteen waves), which keeps those rows few.
+// Workgroups of the backward, each of which leaves a row of partial sums: one per CU.
 static inline int bwd_groups(const Shape& f, int64_t T, int64_t D, size_t e) {
   const int ncu = dev_ncu();
   if (f.w == 0) {  // strips of norm_wgrad_wide: about four workgroups per CU
     const int64_t cols = (D * (int64_t)e + 4095) / 4096, s = 4 * ncu / cols;
     return (int)groups(T, 16, s < 1 ? 1 : s > 64 ? 64 : s);
   }
-  return (int)groups(T, f.w == 1 ? 4 : 1, f.w == 16 ? ncu : 2 * ncu);
+  const int rows = f.w == 1 ? (f.nc == 4 ? kBwdRows<1, 4> : kBwdRows<1, 2>)
+                   : f.w == 4 ? (f.nc == 4 ? kBwdRows<4, 4> : kBwdRows<4, 2>)
+                              : 1;
+  return (int)groups(T, rows, ncu);
 }
 static inline size_t bwd_bytes(int64_t T, int64_t D, bool rms, size_t e) {
-  if (T <= 0) return 0;
+  if (T <= kFewRows) return 0;
   return (size_t)bwd_groups(bwd_shape_of(D, e), T, D, e) * (rms ? 1 : 2) * D * 4;
 }
 
@@ -607,16 +666,21 @@ static int fwd(const Args& g, hipStream_t s) {
 template <class E, bool RMS, int W, int NC>
 static void launch_bwd(const Args& g, int n, hipStream_t s) {
   if (W == 16 || g.D % Piece<E>::V == 0)
-    hipLaunchKernelGGL((norm_bwd<E, RMS, W, NC, true>), dim3(n), dim3(kThreads<W>), 0, s, g);
+    hipLaunchKernelGGL((norm_bwd<E, RMS, W, NC, true>), dim3(n), dim3(64 * W * kBwdRows<W, NC>), 0, s, g);
   else if constexpr (W < 16)
-    hipLaunchKernelGGL((norm_bwd<E, RMS, W, NC, false>), dim3(n), dim3(kThreads<W>), 0, s, g);
+    hipLaunchKernelGGL((norm_bwd<E, RMS, W, NC, false>), dim3(n), dim3(64 * W * kBwdRows<W, NC>), 0, s, g);
 }
 template <class E, bool RMS>
 static int bwd(const Args& g, void* dw, void* db, hipStream_t s) {
   StageScope scope(STAGE_NORM_BWD, s);
+  if (g.T <= kFewRows) {  // (without a row dw and db are zeros)
+    const int per = 64 * Piece<E>::V;
+    hipLaunchKernelGGL((norm_bwd_few<E, RMS>), dim3((unsigned)(g.T + (g.D + per - 1) / per)), dim3(1024), 0, s, g, (char*)dw,
+                       (char*)db);
+    return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH;
+  }
   const Shape f = bwd_shape_of(g.D, E::kBytes);
-  const int n = g.T ? bwd_groups(f, g.T, g.D, E::kBytes) : 0;
-  if (n == 0) return launch_sum_parts<E>(nullptr, 0, RMS ? 1 : 2, g.D, dw, db, s);  // no rows: zeros
+  const int n = bwd_groups(f, g.T, g.D, E::kBytes);
   if (f.w == 1 && f.nc == 1) launch_bwd<E, RMS, 1, 1>(g, n, s);
   else if (f.w == 1 && f.nc == 2) launch_bwd<E, RMS, 1, 2>(g, n, s);
   else if (f.w == 1) launch_bwd<E, RMS, 1, 4>(g, n, s);

