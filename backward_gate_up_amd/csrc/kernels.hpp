@@ -176,32 +176,40 @@ __device__ __forceinline__ void dswiglu4(const float (&da)[4], const float (&gf)
   }
 }
 
-// LINEAR: four consecutive outputs (m, n .. n + 3) from their sums z: the bias, the
-// value before the activation where it is kept, the activation, the residual.
+// LINEAR: one 16-byte piece of consecutive outputs (m, n ..) from their sums z: the
+// bias, the value before the activation where it is kept, the activation, the
+// residual.
 template <class E>
-__device__ __forceinline__ void linear_store(const KArgs& g, int m, int n, f32x4_t z) {
-  using V4 = typename E::vec4;
+__device__ __forceinline__ void linear_store(const KArgs& g, int m, int n, float (&z)[16 / E::kBytes]) {
+  constexpr int V = 16 / E::kBytes;
+  typedef typename E::elem piece_t __attribute__((ext_vector_type(V)));
   const int64_t off = ((int64_t)m * g.ldc + n) * E::kBytes;
+  piece_t r{}, v;
+  if (g.res) r = *(const piece_t*)(g.res + off);
   if (g.bias) {
-    const V4 b = *(const V4*)(g.bias + (int64_t)n * E::kBytes);
+    const piece_t b = *(const piece_t*)(g.bias + (int64_t)n * E::kBytes);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] += E::to_f32(b[e]);
+    for (int e = 0; e < V; ++e) z[e] += E::to_f32(b[e]);
   }
-  V4 v;
   if (g.z) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = E::from_f32(z[e]);
-    *(V4*)(g.z + off) = v;
+    for (int e = 0; e < V; ++e) v[e] = E::from_f32(z[e]);
+    *(piece_t*)(g.z + off) = v;
   }
-  act4<E::kBytes == 4>(g.act, z);
+#pragma unroll
+  for (int q = 0; q < V; q += 4) {
+    f32x4_t t{z[q], z[q + 1], z[q + 2], z[q + 3]};
+    act4<E::kBytes == 4>(g.act, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[q + e] = t[e];
+  }
   if (g.res) {
-    const V4 r = *(const V4*)(g.res + off);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] += E::to_f32(r[e]);
+    for (int e = 0; e < V; ++e) z[e] += E::to_f32(r[e]);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = E::from_f32(z[e]);
-  *(V4*)(g.c0 + off) = v;
+  for (int e = 0; e < V; ++e) v[e] = E::from_f32(z[e]);
+  *(piece_t*)(g.c0 + off) = v;
 }
 
 // Epilogue of one tile. acc[i][j][r] holds output
@@ -209,7 +217,7 @@ __device__ __forceinline__ void linear_store(const KArgs& g, int m, int n, f32x4
 //   n = (column base of subtile j) + (r / 4) * 8 + (lane / 32) * 4 + r % 4,
 // so each lane stores runs of 4 consecutive n (8 bytes in bf16).
 template <class E, int BM, int BN, int KIND, int TM, int TN>
-__device__ __forceinline__ void epilogue(const KArgs& g, char* C, f32x16_t (&acc)[TM][TN], int m0, int n0,
+__device__ __forceinline__ void epilogue(const KArgs& g, char* C, char* smem, f32x16_t (&acc)[TM][TN], int m0, int n0,
                                          const int (&a_rows)[TM], const int (&b_rows)[TN], int wn, int lane) {
   constexpr int EB = E::kBytes;
   using V4 = typename E::vec4;
@@ -274,24 +282,52 @@ __device__ __forceinline__ void epilogue(const KArgs& g, char* C, f32x16_t (&acc
       }
     }
   } else if constexpr (KIND == LINEAR) {
+    // A wave's 32 x 32 blocks go through LDS one after another (rows of 36 floats,
+    // so that the 16 lanes of one access fall on distinct banks), so that a lane
+    // has 16 bytes of consecutive outputs and neighbouring lanes a row's 64 or 128
+    // (T = 8192, N = K = 1024, bf16, z kept: LDS_MEASURED).
+    constexpr int V = 16 / EB;
+    float* blk = (float*)smem + (threadIdx.x >> 6) * (32 * 36);
+    __syncthreads();  // every wave is done with the K loop's stages
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int m = m0 + a_rows[i] + ml;
-      if (m >= g.M) continue;
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = n0 + b_rows[j] + q * 8 + nl;
-          if (n >= g.N) continue;
-          f32x4_t z;
+          f32x4_t v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = acc[i][j][q * 4 + e];
-          if (g.ksplit > 1) *(f32x4_t*)((float*)C + (int64_t)m * g.N + n) = z;
-          else linear_store<E>(g, m, n, z);
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][q * 4 + e];
+          *(f32x4_t*)(blk + ml * 36 + q * 8 + nl) = v;
         }
+        __builtin_amdgcn_wave_barrier();
+        const int mb = m0 + a_rows[i], nb = n0 + b_rows[j];
+        if (g.ksplit > 1) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int r = p * 8 + (lane >> 3), c = (lane & 7) * 4;
+            if (mb + r < g.M && nb + c < g.N)
+              *(f32x4_t*)((float*)C + (int64_t)(mb + r) * g.N + nb + c) = *(const f32x4_t*)(blk + r * 36 + c);
+          }
+        } else {
+          constexpr int LPR = 32 / V;  // lanes per row
+#pragma unroll
+          for (int p = 0; p < 32 * LPR / 64; ++p) {
+            const int r = p * (64 / LPR) + lane / LPR, c = lane % LPR * V;
+            if (mb + r < g.M && nb + c < g.N) {
+              float z[V];
+#pragma unroll
+              for (int q = 0; q < V; q += 4) {
+                const f32x4_t t = *(const f32x4_t*)(blk + r * 36 + c + q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[q + e] = t[e];
+              }
+              linear_store<E>(g, mb + r, nb + c, z);
+            }
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
       }
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -459,7 +495,7 @@ __device__ __forceinline__ void gemm_tile(const KArgs& g, char* smem, int bid, i
     body(kt, F_{}, F_{}, F_{});
   }
 
-  epilogue<E, BM, BN, KIND, TM, TN>(g, C, acc, m0, n0, a_rows, b_rows, wn, lane);
+  epilogue<E, BM, BN, KIND, TM, TN>(g, C, smem, acc, m0, n0, a_rows, b_rows, wn, lane);
 }
 
 // One launch = one stage. STAGE only names the kernel (one symbol per

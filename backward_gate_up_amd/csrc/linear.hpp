@@ -110,25 +110,31 @@ __global__ void __launch_bounds__(NW * 64, (NW == 4 ? 2 : 1)) lin_few(const FewA
   ring::wait_vmcnt<0>();  // no load may land in LDS after the workgroup's end
 }
 
-// The epilogue on the sums of parts, four columns of a row per thread, for one or
-// two products (qa and qb such quads).
+// The epilogue on the sums of parts, 16 bytes of a row's outputs per thread, for one
+// or two products (na and nb such pieces).
 template <class E>
-__global__ void __launch_bounds__(256) lin_join(const KArgs a, const KArgs b, int64_t qa, int64_t qb) {
-  const int64_t blocks = (qa + 255) / 256;
+__global__ void __launch_bounds__(256) lin_join(const KArgs a, const KArgs b, int64_t na, int64_t nb) {
+  constexpr int V = 16 / E::kBytes;
+  const int64_t blocks = (na + 255) / 256;
   const bool second = blockIdx.x >= blocks;
   const KArgs& g = second ? b : a;
-  const int64_t quads = second ? qb : qa, i = (blockIdx.x - (second ? blocks : 0)) * 256 + threadIdx.x;
-  if (i >= quads) return;
-  f32x4_t v{};
+  const int64_t pieces = second ? nb : na, i = (blockIdx.x - (second ? blocks : 0)) * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  float z[V] = {};
+  const f32x4_t* at = (const f32x4_t*)(g.P + i * V);
   for (int s0 = 0; s0 < g.ksplit; s0 += 4) {
-    f32x4_t p[4];
+    f32x4_t p[4][V / 4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) p[s] = s0 + s < g.ksplit ? ((const f32x4_t*)g.P)[(s0 + s) * quads + i] : f32x4_t{};
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v += p[s];
+      for (int q = 0; q < V / 4; ++q) p[s][q] = s0 + s < g.ksplit ? at[(s0 + s) * (pieces * V / 4) + q] : f32x4_t{};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int e = 0; e < V; ++e) z[e] += p[s][e / 4][e % 4];
   }
-  const int q = g.N / 4;
-  linear_store<E>(g, (int)(i / q), (int)(i % q) * 4, v);
+  const int q = g.N / V;
+  linear_store<E>(g, (int)(i / q), (int)(i % q) * V, z);
 }
 
 // ---- dz --------------------------------------------------------------------------
@@ -143,13 +149,13 @@ struct DzArgs {
   int64_t T;
   int N, act;
 };
-template <class E, int ACT, int STEP>
+template <class E, int ACT>
 __device__ __forceinline__ void dz_rows(const DzArgs& g, int at, int64_t t0, int64_t t1, float (&sum)[16 / E::kBytes]) {
   using P = norm::Piece<E>;
   constexpr int V = P::V;
   const int64_t rowb = (int64_t)g.N * E::kBytes;
 #pragma unroll 4
-  for (int64_t t = t0; t < t1; t += STEP) {
+  for (int64_t t = t0; t < t1; t += 4) {
     P dy, z, dz;
     dy.template load<true>(g.dy + t * rowb, at, g.N);
     if constexpr (ACT != SWIGLU_ACT_NONE) z.template load<true>(g.z + t * rowb, at, g.N);
@@ -165,14 +171,6 @@ __device__ __forceinline__ void dz_rows(const DzArgs& g, int at, int64_t t0, int
     if constexpr (ACT != SWIGLU_ACT_NONE) dz.template store<true>(g.dz + t * rowb, at, g.N);
   }
 }
-template <class E, int STEP>
-__device__ __forceinline__ void dz_rows_of(const DzArgs& g, int at, int64_t t0, int64_t t1, float (&sum)[16 / E::kBytes]) {
-  if (!g.z) dz_rows<E, SWIGLU_ACT_NONE, STEP>(g, at, t0, t1, sum);
-  else if (g.act == SWIGLU_ACT_RELU) dz_rows<E, SWIGLU_ACT_RELU, STEP>(g, at, t0, t1, sum);
-  else if (g.act == SWIGLU_ACT_GELU) dz_rows<E, SWIGLU_ACT_GELU, STEP>(g, at, t0, t1, sum);
-  else if (g.act == SWIGLU_ACT_GELU_TANH) dz_rows<E, SWIGLU_ACT_GELU_TANH, STEP>(g, at, t0, t1, sum);
-  else dz_rows<E, SWIGLU_ACT_SILU, STEP>(g, at, t0, t1, sum);
-}
 template <class E>
 __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
   constexpr int V = 16 / E::kBytes;
@@ -181,7 +179,13 @@ __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
   const int at = (blockIdx.x * 64 + lane) * V;
   const int64_t t0 = g.T * blockIdx.y / gridDim.y + wave, t1 = g.T * (blockIdx.y + 1) / gridDim.y;
   float sum[V] = {};
-  if (at < g.N) dz_rows_of<E, 4>(g, at, t0, t1, sum);
+  if (at < g.N) {
+    if (!g.z) dz_rows<E, SWIGLU_ACT_NONE>(g, at, t0, t1, sum);
+    else if (g.act == SWIGLU_ACT_RELU) dz_rows<E, SWIGLU_ACT_RELU>(g, at, t0, t1, sum);
+    else if (g.act == SWIGLU_ACT_GELU) dz_rows<E, SWIGLU_ACT_GELU>(g, at, t0, t1, sum);
+    else if (g.act == SWIGLU_ACT_GELU_TANH) dz_rows<E, SWIGLU_ACT_GELU_TANH>(g, at, t0, t1, sum);
+    else dz_rows<E, SWIGLU_ACT_SILU>(g, at, t0, t1, sum);
+  }
   if (!g.partial) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) red[wave][i][lane] = sum[i];
@@ -191,27 +195,73 @@ __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
     if (n < g.N) g.partial[(int64_t)blockIdx.y * g.N + n] = ((red[0][e][l] + red[1][e][l]) + red[2][e][l]) + red[3][e][l];
   }
 }
-// The same with all rows in one workgroup of sixteen waves per 256 bytes of columns,
+// The same with all rows in one workgroup of sixteen waves per 128 bytes of columns,
 // which writes db itself: up to kDzRows rows one launch less is worth more than
-// the strips.
+// the strips. A thread has at most four rows, one after another and the next one's
+// loads ahead: with the rows unrolled the code is four times as long, and a
+// launch this short waits for its instructions (T = 300, N = 712, fp16 DZ_MEASURED).
 constexpr int kDzRows = 512;
+template <class E, int ACT>
+__device__ __forceinline__ void dz_few_rows(const DzArgs& g, int at, int first, float (&sum)[16 / E::kBytes]) {
+  using P = norm::Piece<E>;
+  constexpr int V = P::V;
+  const int64_t rowb = (int64_t)g.N * E::kBytes;
+  P dy, z;
+  auto load = [&](int64_t row) {
+    if (row >= g.T) return;
+    dy.template load<true>(g.dy + row * rowb, at, g.N);
+    if constexpr (ACT != SWIGLU_ACT_NONE) z.template load<true>(g.z + row * rowb, at, g.N);
+  };
+  load(first);
+#pragma unroll 1
+  for (int64_t row = first; row < g.T; row += 128) {
+    const P d = dy, y = z;
+    load(row + 128);
+    P dz;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v = d.get(i);
+      if constexpr (ACT != SWIGLU_ACT_NONE) {
+        v *= act_slope<E::kBytes == 4, ACT>(y.get(i));
+        dz.put(i, E::from_f32(v));
+      }
+      sum[i] += v;
+    }
+    if constexpr (ACT != SWIGLU_ACT_NONE) dz.template store<true>(g.dz + row * rowb, at, g.N);
+  }
+}
 template <class E>
 __global__ void __launch_bounds__(1024) lin_dz_few(const DzArgs g, char* db) {
-  constexpr int V = 16 / E::kBytes;
-  __shared__ float red[64][16 * V + 1];
-  const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-  const int at = (blockIdx.x * 16 + col) * V;
+  constexpr int V = 16 / E::kBytes, C = 8 * V;  // columns
+  __shared__ float red[128][C + 1];
+  const int lane = threadIdx.x & 7, row = threadIdx.x >> 3;
+  const int at = (blockIdx.x * 8 + lane) * V;
   float sum[V] = {};
-  if (at < g.N) dz_rows_of<E, 64>(g, at, row, g.T, sum);
+  if (at < g.N) {
+    if (!g.z) dz_few_rows<E, SWIGLU_ACT_NONE>(g, at, row, sum);
+    else if (g.act == SWIGLU_ACT_RELU) dz_few_rows<E, SWIGLU_ACT_RELU>(g, at, row, sum);
+    else if (g.act == SWIGLU_ACT_GELU) dz_few_rows<E, SWIGLU_ACT_GELU>(g, at, row, sum);
+    else if (g.act == SWIGLU_ACT_GELU_TANH) dz_few_rows<E, SWIGLU_ACT_GELU_TANH>(g, at, row, sum);
+    else dz_few_rows<E, SWIGLU_ACT_SILU>(g, at, row, sum);
+  }
   if (!db) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) red[row][col * V + i] = sum[i];
+  for (int i = 0; i < V; ++i) red[row][lane * V + i] = sum[i];
   __syncthreads();
-  const int n = blockIdx.x * 16 * V + threadIdx.x;
-  if (threadIdx.x < 16 * V && n < g.N) {
-    float v = 0.f;
-#pragma unroll 16
-    for (int r = 0; r < 64; ++r) v += red[r][threadIdx.x];
+  // eight rows' sums per thread, then the sixteen of a column
+  const int c = threadIdx.x % C, p = threadIdx.x / C, n = blockIdx.x * C + c;
+  float v = 0.f;
+  if (p < 16) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v += red[p * 8 + r][c];
+  }
+  __syncthreads();
+  if (p < 16) red[p][c] = v;
+  __syncthreads();
+  if (p == 0 && n < g.N) {
+    v = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v += red[r][c];
     ((typename E::elem*)db)[n] = E::from_f32(v);
   }
 }
@@ -337,29 +387,31 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
   double best = g.w.us + g.x.us + 3.0;
   const int ncu = dev_ncu();
   {
-    // 64 x 64 tiles together: each product's parts as many as it takes alone
+    // 64 x 64 tiles together, whole or in as many parts as give two per CU
     const TileCost c = tile_cost(T64, e);
     const int bk = e == 4 ? 32 : 64;
-    auto split = [&](int64_t M, int64_t n_cols, int64_t len) {
+    auto split = [&](int64_t M, int64_t n_cols, int64_t len, bool parts) {
       const int nk = cdiv(len, bk);
       const int64_t n = (int64_t)cdiv(M, 64) * cdiv(n_cols, 64);
       Product p{T64, 1, nk * bk, 0, 0, 0};
-      for (int s = 2; s <= 16 && nk / s >= 4 && n * s <= 2 * ncu; ++s) {
+      for (int s = 2; parts && s <= 16 && nk / s >= 4 && n * s <= 2 * ncu; ++s) {
         const int per = cdiv(nk, s);
         if (cdiv(nk, per) == s) p = {T64, s, per * bk, 0, 0, 0};
       }
       return p;
     };
-    const Product w = split(N, K, T), x = split(T, K, N);
     const double nw = (double)cdiv(N, 64) * cdiv(K, 64), nx = (double)cdiv(T, 64) * cdiv(K, 64);
     const double load = c.thr * (nw * T + nx * N) / ncu;
-    const double lat = c.lat * (w.kchunk > x.kchunk ? w.kchunk : x.kchunk);
-    const double parts = (w.splits > 1 ? (double)w.splits * N * K : 0) + (x.splits > 1 ? (double)x.splits * T * K : 0);
-    // (the last tiles to start end half a tile late)
-    const double us = (load > lat ? load + 0.5 * lat : lat) + (parts > 0 ? join_us(parts) : 0);
-    if (us < best) {
-      best = us;
-      g = {true, false, w, x};
+    for (int parts = 0; parts < 2; ++parts) {
+      const Product w = split(N, K, T, parts), x = split(T, K, N, parts);
+      const double lat = c.lat * (w.kchunk > x.kchunk ? w.kchunk : x.kchunk);
+      const double v = (w.splits > 1 ? (double)w.splits * N * K : 0) + (x.splits > 1 ? (double)x.splits * T * K : 0);
+      // (the last tiles to start end half a tile late)
+      const double us = (load > lat ? load + 0.5 * lat : lat) + (v > 0 ? join_us(v) : 0);
+      if (us < best) {
+        best = us;
+        g = {true, false, w, x};
+      }
     }
   }
   if (e == 2) {
@@ -493,19 +545,22 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))
   }
   dx_tile<E>(g, R, item, ks, piece);
 }
-// Joins the parts of the ring's split tiles: four columns of a row per thread.
+// Joins the parts of the ring's split tiles (16 bits): eight columns of a row per
+// thread.
 template <class E>
 __global__ void __launch_bounds__(256) lin_join_tiles(const KArgs g) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int r = (int)(i >> 14), rr = (int)(i >> 6) & 255, cq = (int)i & 63;
+  const int r = (int)(i >> 13), rr = (int)(i >> 5) & 255, c = ((int)i & 31) * 8;
   int tm, tn;
   tile_coords(g.n_full + r, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
-  const int m = tm * 256 + rr, n = tn * 256 + cq * 4;
+  const int m = tm * 256 + rr, n = tn * 256 + c;
   if (m >= g.M || n >= g.N) return;
-  const float* p = g.P + (int64_t)r * g.ksplit * 65536 + rr * 256 + cq * 4;
-  f32x4_t sum{};
-  for (int s = 0; s < g.ksplit; ++s) sum += *(const f32x4_t*)(p + (int64_t)s * 65536);
-  linear_store<E>(g, m, n, sum);
+  const float* p = g.P + (int64_t)r * g.ksplit * 65536 + rr * 256 + c;
+  float z[8] = {};
+  for (int s = 0; s < g.ksplit; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] += p[(int64_t)s * 65536 + e];
+  linear_store<E>(g, m, n, z);
 }
 // dW and dx on the ring, the longer tiles first.
 template <class E>
@@ -560,10 +615,11 @@ static int few_own(const FewArgs& a, hipStream_t s) {
   const int fit = 2 * ncu;
   return launch_few<E, XR, 4, 1, 65536>(a, tiles < fit ? tiles : fit, s);
 }
-// The parts of up to two products (quads of columns each) joined in one launch.
+// The parts of up to two products joined in one launch.
 template <class E>
 static int launch_join(const KArgs& a, const KArgs& b, hipStream_t s) {
-  const int64_t qa = a.ksplit > 1 ? (int64_t)a.M * a.N / 4 : 0, qb = b.ksplit > 1 ? (int64_t)b.M * b.N / 4 : 0;
+  constexpr int V = 16 / E::kBytes;
+  const int64_t qa = a.ksplit > 1 ? (int64_t)a.M * a.N / V : 0, qb = b.ksplit > 1 ? (int64_t)b.M * b.N / V : 0;
   if (qa + qb == 0) return SWIGLU_OK;
   hipLaunchKernelGGL((lin_join<E>), dim3((unsigned)((qa + 255) / 256 + (qb + 255) / 256)), dim3(256), 0, s, a, b, qa, qb);
   return status();
@@ -592,11 +648,11 @@ static int run_product(KArgs a, const Product& p, float* parts, hipStream_t s, R
       a.tiles_n = cdiv(a.N, 256);
       a.n_full = p.n_full;
       a.n_split = p.n_split;
-      a.group_m = 2;
+      a.group_m = AL == MC ? 4 : BL == MC ? 1 : 2;
       int rc = ring(a, s);
       if (!rc && rest) rc = rest(a, s);
       if (rc || p.n_split == 0) return rc;
-      hipLaunchKernelGGL((lin_join_tiles<E>), dim3(p.n_split * 64), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((lin_join_tiles<E>), dim3(p.n_split * 32), dim3(256), 0, s, a);
       return status();
     }
     if (p.tile == T64x128) return launch_tiles<E, AL, BL, STAGE, 64, 128>(a, s);
@@ -669,7 +725,7 @@ int run_bwd(const Bwd& c) {
     if (act) dz = c.ws;
     if (p.strips == 0) {
       const DzArgs d{(const char*)c.dy, z, c.ws, nullptr, c.T, (int)c.N, c.act};
-      hipLaunchKernelGGL((lin_dz_few<E>), dim3((unsigned)((c.N * E::kBytes + 255) / 256)), dim3(1024), 0, s, d, (char*)c.db);
+      hipLaunchKernelGGL((lin_dz_few<E>), dim3((unsigned)((c.N * E::kBytes + 127) / 128)), dim3(1024), 0, s, d, (char*)c.db);
       if (status()) return SWIGLU_ERR_LAUNCH;
     } else {
       const DzArgs d{(const char*)c.dy, z, c.ws, c.db ? parts : nullptr, c.T, (int)c.N, c.act};
@@ -704,7 +760,8 @@ int run_bwd(const Bwd& c) {
         w.tiles_m = cdiv(w.M, 256);
         x.tiles_m = cdiv(x.M, 256);
         w.tiles_n = x.tiles_n = cdiv(w.N, 256);
-        w.group_m = x.group_m = 4;
+        w.group_m = 4;
+        x.group_m = 1;
         hipLaunchKernelGGL((lin_ring_grads<E>), dim3(g.w.n_full + g.x.n_full), dim3(256), 0, s, w, x, c.T >= c.N ? 0 : 1);
         return status();
       }
