@@ -21,7 +21,7 @@ group scales (``W4Weight``, ``w4_linear``, ``infer_w4``, module ``SwiGLUMLPW4``)
 
 Before and beside the block (dense.py), with gradients: ``layer_norm``,
 ``rms_norm`` and ``linear``, the product with bias, activation and residual in
-its epilogue; module ``FeedForward`` of them.
+its epilogue; ``feed_forward`` and the module ``FeedForward`` of them.
 
 Weight layouts (``linear``): False (kernel layout): Wg, Wu [D, H], Wd [H, D];
 True (nn.Linear layout): Wg, Wu [H, D], Wd [D, H]. Weight gradients come back
@@ -37,14 +37,15 @@ from ._lib import SwiGLUError, STAGE_NAMES, NUM_STAGES  # noqa: F401
 from .serve import (moe_route, moe_experts, moe_infer, w4_quantize, w4_pack, w4_linear, infer_w4,  # noqa: F401
                     W4Weight, SwiGLUMLPW4, SwiGLUMoE)
 from .dense import (layer_norm, rms_norm, linear, norm_fwd, norm_bwd, linear_fwd, linear_bwd, NormFunction,  # noqa: F401
-                    LinearFunction, FeedForward)
+                    LinearFunction, FeedForwardFunction, feed_forward, FeedForward)
 
 __all__ = ["fwd", "bwd", "infer", "infer_noalloc", "SwiGLUMLPFunction", "swiglu_mlp", "SwiGLUMLP",
            "SwiGLUMLPPacked", "saved_bytes",
            "infer_workspace_bytes", "bwd_workspace_bytes", "SwiGLUError", "StageTimer",
            "moe_route", "moe_experts", "moe_infer", "w4_quantize", "w4_pack", "w4_linear", "infer_w4", "W4Weight",
            "SwiGLUMLPW4", "SwiGLUMoE", "layer_norm", "rms_norm", "linear", "norm_fwd", "norm_bwd", "linear_fwd",
-           "linear_bwd", "NormFunction", "LinearFunction", "FeedForward"]
+           "linear_bwd", "NormFunction", "LinearFunction", "FeedForwardFunction",
+           "feed_forward", "FeedForward"]
 
 _DT = {torch.bfloat16: _L.BF16, torch.float16: _L.FP16, torch.float32: _L.FP32}
 

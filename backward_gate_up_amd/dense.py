@@ -7,8 +7,9 @@ behind the C ABI of include/swiglu_mlp.h; no fallback):
 * ``norm_fwd``, ``norm_bwd``      layer norm and RMS norm over the last axis
 * ``linear_fwd``, ``linear_bwd``  y = act(x W^T + b) + residual
 
-with autograd: ``layer_norm``, ``rms_norm``, ``linear``; and the module
-``FeedForward``, the ungated feed-forward layer x + fc2(act(fc1(norm(x)))) of them.
+with autograd: ``layer_norm``, ``rms_norm``, ``linear`` and, of all three, the
+ungated feed-forward layer x + fc2(act(fc1(norm(x)))): ``feed_forward`` and the
+module ``FeedForward``.
 All tensors of a call share dtype (bf16, fp16 or fp32) and device.
 
 Second derivatives are refused. The backward may run more than once
@@ -74,6 +75,16 @@ def _opt(t):
 
 def _flat(t):
     return t if t is None or t.is_contiguous() else t.contiguous()
+
+
+def _flat16(t):
+    """Contiguous and at an address that the matrix kernels take (a gradient may
+    be a view that starts anywhere)."""
+    if t is None:
+        return t
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 # ---- norms ------------------------------------------------------------------
@@ -202,7 +213,7 @@ def linear_fwd(x, w, bias=None, activation=None, residual=None, keep=True, works
     inputs' dtype, for ``linear_bwd``; None without an activation or ``keep``."""
     act = _act(activation)
     T, N, K = _linear_shapes(x, w, bias, residual)
-    x, w, bias, residual = _flat(x), _flat(w), _flat(bias), _flat(residual)
+    x, w, bias, residual = _flat16(x), _flat16(w), _flat16(bias), _flat16(residual)
     dt, device = _code(x), x.device
     y = torch.empty((T, N), dtype=x.dtype, device=device)
     z = torch.empty_like(y) if keep and act else None
@@ -243,13 +254,13 @@ def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), work
     _linear_shapes(x, w, None, dy)
     _same(x, z)
     _code(x)
-    return _linear_bwd(_flat(dy), _flat(x), _flat(w), _flat(z), act, needs, workspace)
+    return _linear_bwd(_flat16(dy), _flat16(x), _flat16(w), _flat16(z), act, needs, workspace)
 
 
 class LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, activation):
-        x, w = _flat(x), _flat(w)
+        x, w = _flat16(x), _flat16(w)
         y, z = linear_fwd(x, w, bias, activation, residual)
         ctx.save_for_backward(x, w, z)
         ctx.act = _L.ACTS[activation]
@@ -262,7 +273,7 @@ class LinearFunction(torch.autograd.Function):
         needs = ctx.needs_input_grad
         dx = dw = db = None
         if needs[0] or needs[1] or needs[2]:
-            dx, dw, db = _linear_bwd(_flat(dy), x, w, z, ctx.act, needs)
+            dx, dw, db = _linear_bwd(_flat16(dy), x, w, z, ctx.act, needs)
         return dx, dw, db, dy if needs[3] else None, None
 
 
@@ -288,6 +299,60 @@ def linear(x, w, bias=None, activation=None, residual=None):
 
 
 # ---- the layer of them ----------------------------------------------------------
+
+
+class FeedForwardFunction(torch.autograd.Function):
+    """The layer as one node: its backward hands the stream's gradient to the norm's
+    backward, which adds it to its own, instead of leaving a sum of two tensors."""
+
+    @staticmethod
+    def forward(ctx, x, nw, nb, w1, b1, w2, b2, activation, eps, rms):
+        x, nw, w1, w2 = _flat16(x), _flat(nw), _flat16(w1), _flat16(w2)
+        n, stats = norm_fwd(x, nw, nb, eps, rms)
+        a, z = linear_fwd(n, w1, b1, activation)
+        y = linear_fwd(a, w2, b2, None, x)[0]
+        ctx.save_for_backward(x, nw, w1, w2, n, stats, a, z)
+        ctx.form = _L.ACTS[activation], rms, nb is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        _no_second()
+        x, nw, w1, w2, n, stats, a, z = ctx.saved_tensors
+        act, rms, norm_bias = ctx.form
+        need = ctx.needs_input_grad
+        dy = _flat16(dy)
+        norm = need[0] or need[1] or need[2]
+        inner = norm or need[3] or need[4]
+        da, dw2, db2 = _linear_bwd(dy, a, w2, None, 0, (inner, need[5], need[6]))
+        dx = dnw = dnb = dw1 = db1 = None
+        if inner:
+            dn, dw1, db1 = _linear_bwd(da, n, w1, z, act, (norm, need[3], need[4]))
+            del da
+            if norm:
+                dx, dnw, dnb = _norm_bwd(dn, x, nw, stats, rms, norm_bias, dy)
+        return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
+
+
+def feed_forward(x, norm_weight, norm_bias, w1, b1, w2, b2, activation="gelu", eps=1e-5, rms=False):
+    """Y = x + act(norm(x) w1^T + b1) w2^T + b2 for x[..., D]: the ungated feed-forward
+    layer with its norm in front and the stream added. norm_weight[D], w1[H, D],
+    w2[D, H]; norm_bias, b1 and b2 or None; ``activation`` as in ``linear``; with
+    ``rms`` an RMS norm (no norm_bias)."""
+    if x.dim() == 0:
+        raise ValueError("expected X[..., D]")
+    if not activation:
+        raise ValueError(f"a feed-forward layer needs an activation: one of {ACTIVATIONS[1:]}")
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                       for t in (x, norm_weight, norm_bias, w1, b1, w2, b2)):
+        y = FeedForwardFunction.apply(x2, norm_weight, norm_bias, w1, b1, w2, b2, activation, eps, rms)
+    else:
+        n = norm_fwd(x2, norm_weight, norm_bias, eps, rms, False)[0]
+        a = linear_fwd(n, w1, b1, activation, None, False)[0]
+        y = linear_fwd(a, w2, b2, None, x2, False)[0]
+    return y if x.dim() == 2 else y.reshape(x.shape)
+
 
 _CONFIG_ACTS = {"relu": "relu", "gelu": "gelu", "gelu_new": "gelu_tanh", "gelu_pytorch_tanh": "gelu_tanh",
                 "gelu_tanh": "gelu_tanh", "silu": "silu", "swish": "silu"}
@@ -318,12 +383,9 @@ class FeedForward(torch.nn.Module):
         self.fc2 = torch.nn.Linear(H, D, bias=bias)
 
     def forward(self, x):
-        if isinstance(self.norm, torch.nn.RMSNorm):
-            n = rms_norm(x, self.norm.weight, self.norm.eps)
-        else:
-            n = layer_norm(x, self.norm.weight, self.norm.bias, self.norm.eps)
-        a = linear(n, self.fc1.weight, self.fc1.bias, self.activation)
-        return linear(a, self.fc2.weight, self.fc2.bias, residual=x)
+        rms = isinstance(self.norm, torch.nn.RMSNorm)
+        return feed_forward(x, self.norm.weight, None if rms else self.norm.bias, self.fc1.weight, self.fc1.bias,
+                            self.fc2.weight, self.fc2.bias, self.activation, self.norm.eps, rms)
 
     def extra_repr(self):
         return f"activation={self.activation!r}"

@@ -586,6 +586,84 @@ def test_feed_forward(kw):
     assert {"norm.weight", "fc1.weight", "fc2.weight"} <= names and ("fc1.bias" in names) == kw.get("mlp_bias", True)
 
 
+@pytest.mark.gpu
+def test_feed_forward_is_its_operators():
+    """The layer's one node gives what its operators give one after another, with
+    any of its weights frozen."""
+    banner("feed_forward")
+    dt = torch.bfloat16
+    sh = {"x": (90, 136), "nw": (136,), "nb": (136,), "w1": (264, 136), "b1": (264,), "w2": (136, 264), "b2": (136,)}
+    t = {k: normal(gen(i), s, dt, 0.1 if k[0] == "w" else 1.0) for i, (k, s) in enumerate(sh.items())}
+    dy = normal(gen(50), (90, 136), dt)
+    n, st = mlp.norm_fwd(t["x"], t["nw"], t["nb"])
+    a, z = mlp.linear_fwd(n, t["w1"], t["b1"], "silu")
+    y = mlp.linear_fwd(a, t["w2"], t["b2"], None, t["x"])[0]
+    da, dw2, db2 = mlp.linear_bwd(dy, a, t["w2"])
+    dn, dw1, db1 = mlp.linear_bwd(da, n, t["w1"], z, "silu")
+    dx, dnw, dnb = mlp.norm_bwd(dn, t["x"], t["nw"], st, bias=True, dres=dy)
+    want = dict(x=dx, nw=dnw, nb=dnb, w1=dw1, b1=db1, w2=dw2, b2=db2)
+    assert torch.equal(mlp.feed_forward(*t.values(), activation="silu"), y)
+    for wanted in (list(sh), ["x"], ["w1"], ["b1", "w2"], ["b2"], ["nb"], ["w1", "w2"]):
+        leaves = {k: v.detach().clone().requires_grad_(k in wanted) for k, v in t.items()}
+        out = mlp.feed_forward(*leaves.values(), activation="silu")
+        assert torch.equal(out, y)
+        got = torch.autograd.grad(out, [leaves[k] for k in wanted], dy)
+        for k, g in zip(wanted, got):
+            assert torch.equal(g, want[k]), (wanted, k)
+
+
+@pytest.mark.gpu
+def test_gradients_that_start_anywhere():
+    """Views at odd addresses: of inputs, and as the gradient that a flattened
+    concatenation hands back."""
+    banner("odd addresses")
+    dt = torch.bfloat16
+    x, w = normal(gen(1), (20, 64), dt).requires_grad_(), normal(gen(2), (72, 64), dt).requires_grad_()
+    room = normal(gen(3), (20 * 64 + 72 + 3,), dt)
+    xo, bo = room[1:1 + 20 * 64].view(20, 64), room[1 + 20 * 64:1 + 20 * 64 + 72]
+    assert torch.equal(mlp.linear(xo, w, bo, "relu"), mlp.linear(xo.clone(), w, bo.clone(), "relu"))
+    y = mlp.linear(x, w, None, "gelu")
+    weights = normal(gen(4), (1 + 20 * 72,), dt)
+    out = (torch.cat([torch.ones(1, dtype=dt, device=DEV), y.flatten()]) * weights).sum()
+    gx, gw = torch.autograd.grad(out, (x, w))
+    _, z = mlp.linear_fwd(x.detach(), w.detach(), None, "gelu")
+    want = mlp.linear_bwd(weights[1:].view(20, 72).clone(), x.detach(), w.detach(), z, "gelu")
+    assert torch.equal(gx, want[0]) and torch.equal(gw, want[1])
+
+
+@pytest.mark.gpu
+def test_training_step_in_a_graph():
+    """Forward and backward of the layer through autograd, captured; replayed
+    between eager steps of other leaves on other values."""
+    banner("training step in a graph")
+    torch.manual_seed(1)
+    block = mlp.FeedForward(Config(hidden_size=136, intermediate_size=264)).to(DEV, torch.bfloat16)
+    eager = copy.deepcopy(block)
+    for T in (5, 600):
+        x, dy = normal(gen(T), (T, 136), torch.bfloat16), normal(gen(T + 1), (T, 136), torch.bfloat16)
+
+        def step(m, x, dy):
+            x = x.detach().requires_grad_()
+            y = m(x)
+            return (y.detach(), *torch.autograd.grad(y, [x, *m.parameters()], dy))
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(block, x, dy)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(block, x, dy)
+        for i in range(4):
+            x.copy_(normal(gen(100 + i), (T, 136), torch.bfloat16))
+            dy.copy_(normal(gen(200 + i), (T, 136), torch.bfloat16))
+            want = step(eager, x, dy)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, c) for a, c in zip(out, want)), (T, i)
+
+
 # ---- refusals (CPU) ------------------------------------------------------------------
 
 
@@ -631,6 +709,8 @@ def test_python_refusals():
         mlp.linear_bwd(cpu(4, 32), x, w, None, "gelu")
     with pytest.raises(ValueError, match="must match X"):
         mlp.norm_bwd(cpu(4, 32), x, cpu(64), torch.zeros(2, 4))
+    with pytest.raises(ValueError, match="needs an activation"):
+        mlp.feed_forward(x, cpu(64), None, w, None, cpu(64, 32), None, activation=None)
     with pytest.raises(ValueError, match="no activation"):
         mlp.FeedForward(Config(hidden_size=8, intermediate_size=8, hidden_act="tanh"))
 
