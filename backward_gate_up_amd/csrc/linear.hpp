@@ -308,14 +308,16 @@ static inline int few_splits(int64_t T, int64_t N, int64_t K, size_t e) {
 // tiles for the CUs (of the ring's, those of a last round that fills less than
 // all), the parts being joined by a second launch.
 //
-// Chosen by the time of a model in us: a tile takes lat K alone and thr K of its
-// CU's time among others. Measured in ns per unit of K, lat / thr: 64 x 64 7.5 /
-// 3.4 (fp32 19.8 / 15.7), 64 x 128 9.3 / 5.9, 128 x 128 10.7 / 9.3, ring 20.1 /
-// 24.7 (its clock falls as the chip fills). fp32 has only 64 x 64: wider ones were
-// behind at every size but the largest, by 3 % there (M = N = 2000, K = 8000 503
-// against 487 us). What the choice is worth (us, unsplit 64 x 64 / 128 x 128 / best
-// split; bf16): 256 x 1024, K = 8192 62 / 88 / 17.5; 4096 x 2048, K = 5632 154 /
-// 105, on the ring 113; 4096 x 5632, K = 2048 164 / 118, ring 96.
+// Chosen by the time of a model in us: r tiles that a CU runs at once (at most
+// `most`) take fix r + K max(lat, thr r), parts of K a launch and a pass over them
+// more. The figures were fitted to the times of 7 thousand products of random
+// sizes (65 to 16384 by 256 to 11008, all three layouts), each on several tiles in 1
+// to 16 parts, and are 9 % off in the mean; what is chosen takes 1.3 % longer than
+// the best of what was timed. fp32 has only 64 x 64: wider ones were behind at every
+// size but the largest, by 3 % there (M = N = 2000, K = 8000 503 against 487 us).
+// What the choice is worth (us, unsplit 64 x 64 / 128 x 128 / best split; bf16): 256
+// x 1024, K = 8192 62 / 88 / 17.5; 4096 x 2048, K = 5632 154 / 105 / 97 (ring); 4096
+// x 5632, K = 2048 164 / 118, ring 96.
 enum { T64 = 0, T64x128 = 1, T128 = 2, TRING = 3 };
 struct Product {
   int tile, splits, kchunk;  // kchunk: K values per part (ring: stages)
@@ -323,18 +325,24 @@ struct Product {
   double us;
 };
 struct TileCost {
-  int bm, bn;
-  double lat, thr;
+  int bm, bn, most;
+  double lat, thr, fix;
+  // a CU's share of r tiles over a K
+  double us(double r, double k) const {
+    const double rounds = (double)(int64_t)(r / most), rest = r - rounds * most;
+    auto one = [&](double n) { return n > 0 ? (lat > thr * n ? lat : thr * n) : 0.0; };
+    return fix * r + k * (rounds * one(most) + one(rest));
+  }
 };
 static inline TileCost tile_cost(int tile, size_t e) {
-  if (e == 4) return {64, 64, 19.8e-3, 15.7e-3};
-  if (tile == T64) return {64, 64, 7.5e-3, 3.4e-3};
-  if (tile == T64x128) return {64, 128, 9.3e-3, 5.9e-3};
-  if (tile == T128) return {128, 128, 10.7e-3, 9.3e-3};
-  return {256, 256, 20.1e-3, 24.7e-3};
+  if (e == 4) return {64, 64, 4, 19.1e-3, 16.0e-3, 0.72};
+  if (tile == T64) return {64, 64, 4, 6.4e-3, 4.0e-3, 0.38};
+  if (tile == T64x128) return {64, 128, 2, 8.7e-3, 5.8e-3, 1.2};
+  if (tile == T128) return {128, 128, 2, 10.9e-3, 8.1e-3, 2.2};
+  return {256, 256, 1, 17.0e-3, 20.8e-3, 13.4};
 }
 // Writing and reading fp32 parts, and the launch that joins them.
-static inline double join_us(double values) { return 5.0 + values * 8 / 5.0e6; }
+static inline double join_us(double values) { return 5.0 + values * 1.0e-6; }
 static Product plan_product(int64_t M, int64_t N, int64_t K, size_t e) {
   const int ncu = dev_ncu(), bk = e == 4 ? 32 : 64, nk = K > 0 ? cdiv(K, bk) : 1;
   Product best{};
@@ -342,27 +350,27 @@ static Product plan_product(int64_t M, int64_t N, int64_t K, size_t e) {
   for (int tile = T64; tile <= (e == 4 ? T64 : T128); ++tile) {
     const TileCost c = tile_cost(tile, e);
     const int64_t n = (int64_t)cdiv(M, c.bm) * cdiv(N, c.bn);
-    for (int s = 1; s <= 16 && (s == 1 || (nk / s >= 4 && n * s <= 4 * ncu)); ++s) {
+    for (int s = 1; s <= 16 && (s == 1 || (nk / s >= 4 && n * s <= 8 * ncu)); ++s) {
       const int per = cdiv(nk, s), parts = cdiv(nk, per);
       if (parts != s) continue;
-      const double load = c.thr * (double)((n * s + ncu - 1) / ncu);
-      const double us = (double)per * bk * (load > c.lat ? load : c.lat) + (s > 1 ? join_us((double)s * M * N) : 0);
+      const double us = c.us((double)((n * s + ncu - 1) / ncu), (double)per * bk) + (s > 1 ? join_us((double)s * M * N) : 0);
       if (us < best.us) best = {tile, s, per * bk, 0, 0, us};
     }
   }
   if (e == 4) return best;
-  // the ring, where it has at least half a round of tiles
+  // the ring, where it has at least a quarter of a round of tiles
   const TileCost c = tile_cost(TRING, e);
   const int64_t nt = (int64_t)cdiv(M, 256) * cdiv(N, 256), rem = nt % ncu;
-  if (2 * nt < ncu) return best;
-  const double tile = (double)nk * bk * c.thr, whole = (double)(nt / ncu) * tile;
-  const double alone = 2 * rem > ncu || nt > rem ? tile : (double)nk * bk * c.lat;
+  if (4 * nt < ncu) return best;
+  const double tile = (double)nk * bk * c.thr, whole = (double)(nt / ncu) * (tile + c.fix);
+  const double alone = c.fix + (2 * rem > ncu || nt > rem ? tile : (double)nk * bk * c.lat);
   if (whole + (rem ? alone : 0) < best.us) best = {TRING, 1, nk, (int)nt, 0, whole + (rem ? alone : 0)};
   for (int s = 2; rem && s <= 8 && nk / s >= 8; ++s) {
     const int per = cdiv(nk, s), parts = cdiv(nk, per);
     if (parts != s) continue;
-    const double us = whole + (double)((rem * s + ncu - 1) / ncu) * tile * per / nk + join_us((double)rem * s * 65536);
-    if (us < 0.97 * best.us) best = {TRING, s, per, (int)(nt - rem), (int)rem, us};
+    const double rounds = (double)((rem * s + ncu - 1) / ncu);
+    const double us = whole + rounds * (tile * per / nk + c.fix) + join_us((double)rem * s * 65536);
+    if (us < best.us) best = {TRING, s, per, (int)(nt - rem), (int)rem, us};
   }
   return best;
 }
@@ -384,7 +392,7 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
   if (dw) g.w = plan_product(N, K, T, e);
   if (dx) g.x = plan_product(T, K, N, e);
   if (!dw || !dx || T == 0) return g;
-  double best = g.w.us + g.x.us + 3.0;
+  double best = g.w.us + g.x.us + 4.7;  // (a launch)
   const int ncu = dev_ncu();
   {
     // 64 x 64 tiles together, whole or in as many parts as give two per CU
@@ -401,7 +409,7 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
       return p;
     };
     const double nw = (double)cdiv(N, 64) * cdiv(K, 64), nx = (double)cdiv(T, 64) * cdiv(K, 64);
-    const double load = c.thr * (nw * T + nx * N) / ncu;
+    const double load = c.thr * (nw * T + nx * N) / ncu + c.fix * (nw + nx) / ncu;
     for (int parts = 0; parts < 2; ++parts) {
       const Product w = split(N, K, T, parts), x = split(T, K, N, parts);
       const double lat = c.lat * (w.kchunk > x.kchunk ? w.kchunk : x.kchunk);
@@ -419,10 +427,10 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
     const int64_t nw = (int64_t)cdiv(N, 256) * cdiv(K, 256), nx = (int64_t)cdiv(T, 256) * cdiv(K, 256);
     // a tiles of length l first, then b of length s
     const int64_t a = T >= N ? nw : nx, b = T >= N ? nx : nw;
-    const double l = (T >= N ? T : N) * c.thr, s = (T >= N ? N : T) * c.thr;
-    const int64_t r = a % ncu, meanwhile = r ? (ncu - r) * (int64_t)(l / s) : 0;
-    const int64_t rest = b > meanwhile ? b - meanwhile : 0;
-    const double us = (double)(a / ncu) * l + (r ? l : 0) + (double)((rest + ncu - 1) / ncu) * s;
+    const double l = (T >= N ? T : N) * c.thr + c.fix, s = (T >= N ? N : T) * c.thr + c.fix;
+    // (all CUs busy until the last tiles, which start half a short one late)
+    const double work = (a * l + b * s) / ncu + 0.5 * s, longest = (double)((a + ncu - 1) / ncu) * l;
+    const double us = work > longest ? work : longest;
     // (the two together run 3 to 5 % slower than each alone at its best: their panels share L2)
     if (nw + nx >= ncu && 1.05 * us < best) {
       best = us;

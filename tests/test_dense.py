@@ -29,7 +29,7 @@ import torch
 
 import backward_gate_up_amd as mlp
 from backward_gate_up_amd import _lib, dense
-from tests._util import FMT, TOL, assert_local, banner, f64
+from tests._util import FMT, TOL, banner
 
 U = 2.0 ** -24
 DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
@@ -61,11 +61,20 @@ def inside(got, ref, tol, what):
 
 
 def near(got, ref, what):
-    """Normalized L2 of the whole, and of every row and block."""
+    """Normalized L2 of the whole, of every row, 32 x 32 block and 256 x 256 tile, as
+    tests/_util.py's assert_local has them, on the GPU."""
     if ref.numel() == 0:
         return
     tol = TOL[FMT[got.dtype]]
-    assert_local(f64(got), ref.cpu().numpy(), tol, what)
+    diff, ref = (got.double() - ref) ** 2, ref ** 2
+    floor = ref.mean()
+    assert (diff.sum() / ref.sum()).sqrt() <= tol, (what, "whole")
+    for m, n in ((1, ref.shape[1]), (32, 32), (256, 256)):
+        pad = lambda t: torch.nn.functional.pad(t, (0, -t.shape[1] % n, 0, -t.shape[0] % m))  # noqa: E731
+        total = lambda t: pad(t).unflatten(1, (-1, n)).unflatten(0, (-1, m)).sum((1, 3))  # noqa: E731
+        count = total(torch.ones_like(ref))
+        err = (total(diff) / count).sqrt() / torch.maximum(total(ref) / count, floor).sqrt()
+        assert (err <= tol).all(), (what, (m, n), float(err.max()), (err == err.max()).nonzero()[0].tolist())
 
 
 # ---- norms ----------------------------------------------------------------------
@@ -153,6 +162,27 @@ def test_norm_of_many_rows(T, D, rms):
     for name, a, (r, tol) in zip(("y", "dx", "dw", "db"), got, norm_reference(x, w, b, 1e-5, rms, dy)):
         if a is not None:
             inside(a, r, tol, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_norm_every_width(dtype, rms):
+    """More rows than one launch's gradient takes, at widths for each number of waves
+    and pieces, whole and odd."""
+    dt = DTYPES[dtype]
+    for i, D in enumerate((512, 1000, 2048, 4096, 8192, 16384, 16392, 511, 1001, 2047, 4095, 8191, 12345, 40001)):
+        D = D if dt != torch.float32 else D // 2
+        T = 257 + 13 * i % 50
+        banner(f"norm width {dtype} rms={rms} T={T} D={D}")
+        g = gen(300 + i)
+        x, w, dy = normal(g, (T, D), dt, 1.0, 0.5), normal(g, (D,), dt, 0.2, 1.0), normal(g, (T, D), dt)
+        b, dres = None if rms else normal(g, (D,), dt), normal(g, (T, D), dt) if i % 2 else None
+        y, stats = mlp.norm_fwd(x, w, b, 1e-5, rms)
+        got = (y, *mlp.norm_bwd(dy, x, w, stats, rms, not rms, dres))
+        for name, a, (r, tol) in zip(("y", "dx", "dw", "db"), got, norm_reference(x, w, b, 1e-5, rms, dy, dres)):
+            if a is not None:
+                inside(a, r, tol, (name, T, D))
 
 
 @pytest.mark.gpu
@@ -279,7 +309,10 @@ def product_error(a, b, dt):
     return C * U * (a.abs() @ b.abs())
 
 
-def check_linear(T, N, K, dt, act, bias, res, seed, needs=(True, True, True)):
+ALL = (True, True, True)
+
+
+def check_linear(T, N, K, dt, act, bias, res, seed, needs=(ALL,)):
     g = gen(seed)
     x, w = normal(g, (T, K), dt), normal(g, (N, K), dt, 1.5 / math.sqrt(K))
     b = normal(g, (N,), dt, 0.5) if bias else None
@@ -300,24 +333,24 @@ def check_linear(T, N, K, dt, act, bias, res, seed, needs=(True, True, True)):
     if z is not None:
         inside(z, zr, h * zr.abs() + ez, ("z", T, N, K))
     # the backward differentiates at the values kept
-    dx, dw, db = mlp.linear_bwd(dy, x, w, z, act, needs)
     slope = act64(z.double(), act)[1] if act else torch.ones_like(zr)
     dz = dy.double() * slope
     ed = 0 if act is None else es * dy.double().abs()
-    r_dz = (h if act else 0) * dz.abs() + ed + tiny(dt) * (1 if act else 0)
-    for name, got, ref, tol in (
-            ("dx", dx, dz @ w.double(), lambda: product_error(dz, w.double(), dt) + (r_dz + 0 * dz) @ w.double().abs()),
-            ("dw", dw, dz.t() @ x.double(),
-             lambda: product_error(dz.t(), x.double(), dt) + (r_dz + 0 * dz).t() @ x.double().abs()),
-            ("db", db, dz.sum(0), lambda: ((T / 4 + 64) * U * dz.abs() + ed).sum(0))):
-        if got is None:
-            continue
-        inside(got, ref, h * ref.abs() + 1.01 * tol(), (name, T, N, K))
-        if name != "db":
-            near(got, ref, (name, T, N, K))
-    again = mlp.linear_bwd(dy, x, w, z, act, needs)
-    assert all(a is None or torch.equal(a, c) for a, c in zip(again, (dx, dw, db)))
-    return dx, dw, db
+    r_dz = (h if act else 0) * dz.abs() + ed + tiny(dt) * (1 if act else 0) + 0 * dz
+    refs = {"dx": (dz @ w.double(), product_error(dz, w.double(), dt) + r_dz @ w.double().abs()),
+            "dw": (dz.t() @ x.double(), product_error(dz.t(), x.double(), dt) + r_dz.t() @ x.double().abs()),
+            "db": (dz.sum(0), ((T / 4 + 64) * U * dz.abs() + ed).sum(0))}
+    for wanted in needs:
+        grads = mlp.linear_bwd(dy, x, w, z, act, wanted)
+        for name, got, want in zip(("dx", "dw", "db"), grads, wanted):
+            assert (got is not None) == want
+            if want:
+                ref, tol = refs[name]
+                inside(got, ref, h * ref.abs() + 1.01 * tol, (name, T, N, K, wanted))
+                if name != "db":
+                    near(got, ref, (name, T, N, K, wanted))
+        again = mlp.linear_bwd(dy, x, w, z, act, wanted)
+        assert all(a is None or torch.equal(a, c) for a, c in zip(again, grads))
 
 
 # (T, N, K): each launch variant, with partial tiles and stages
@@ -358,14 +391,45 @@ def test_linear_every_epilogue(T, N, K, act):
         check_linear(T, N, K, torch.bfloat16 if k % 2 else torch.float16, act, bias, res, 3000 + k)
 
 
+# (T, N, K) that the plan gives other launches, 16 bits: what each is there for
+VARIANTS = {
+    (1183, 3296, 240): "64 x 128 tiles", (313, 1672, 3856): "64 x 128 in parts", (471, 4664, 880): "dW on 64 x 128",
+    (1677, 208, 4672): "dx on 64 x 128", (136, 2848, 1288): "dW on 128 x 128", (892, 176, 3944): "dx on 128 x 128",
+    (1048, 3648, 464): "dx on 128 x 128 in parts", (2987, 80, 4232): "dW on 128 x 128 in parts", (548, 208, 176): "dx on 64 x 64",
+    (1106, 288, 200): "dW on 64 x 64 in parts", (2100, 4104, 72): "both gradients together in parts",
+    (2100, 2056, 4104): "ring, all tiles in parts; both gradients on the ring", (4200, 4104, 2056): "ring with a split rest",
+    (2100, 4104, 2056): "dW on the ring, dx there in parts", (2056, 4200, 4104): "both on the ring, dx's tiles longer; dW with a split rest",
+    (4096, 2048, 5632): "dx on the ring with a split rest",
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", list(VARIANTS))
+def test_linear_launch_variants(T, N, K, dtype):
+    banner(f"linear variants {dtype} T={T} N={N} K={K}")
+    i = list(VARIANTS).index((T, N, K)) + (dtype == "fp16")
+    check_linear(T, N, K, DTYPES[dtype], ACTS[i % 5], True, i % 2 == 0, 4000 + i,
+                 (ALL, (False, True, False), (True, False, False)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_linear_epilogues_on_the_ring(dtype, act):
+    """Whole ring tiles with partial edges in every direction."""
+    banner(f"ring epilogue {dtype} {act}")
+    for k, (bias, res) in enumerate(((True, True), (False, False))):
+        check_linear(4100, 2056, 1032, DTYPES[dtype], act, bias, res, 5000 + k, ())
+
+
 @pytest.mark.gpu
 def test_linear_gradients_that_are_not_wanted():
     banner("linear needs")
-    for k in range(8):
-        needs = (bool(k & 1), bool(k & 2), bool(k & 4))
-        for T in (6, 700):
-            got = check_linear(T, 264, 136, torch.bfloat16, "gelu" if T == 6 else None, True, False, 77, needs)
-            assert tuple(g is not None for g in got) == needs
+    every = [(bool(k & 1), bool(k & 2), bool(k & 4)) for k in range(8)]
+    for T, act in ((6, "gelu"), (300, None), (700, None), (700, "relu")):
+        check_linear(T, 264, 136, torch.bfloat16, act, True, False, 77, every)
+        check_linear(T, 264, 136, torch.float32, act, True, False, 78, every)
 
 
 @pytest.mark.gpu
