@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(256) lin_dz(const DzArgs g) {
 // which writes db itself: up to kDzRows rows one launch less is worth more than
 // the strips. A thread has at most four rows, one after another and the next one's
 // loads ahead: with the rows unrolled the code is four times as long, and a
-// launch this short waits for its instructions (T = 300, N = 712, fp16 DZ_MEASURED).
+// launch this short waits for its instructions (T = 300, N = 712, fp16 9.8 -> 6.1
+// us).
 constexpr int kDzRows = 512;
 template <class E, int ACT>
 __device__ __forceinline__ void dz_few_rows(const DzArgs& g, int at, int first, float (&sum)[16 / E::kBytes]) {
@@ -305,15 +306,18 @@ static inline int few_splits(int64_t T, int64_t N, int64_t K, size_t e) {
 // How a product [M, N] over K runs: on register-staged tiles, several workgroups
 // per CU, or (16 bits) on the ring of 256 x 256 tiles, one per CU, which is the
 // fastest where there are enough of them; with K split where there are too few
-// tiles for the CUs (of the ring's, those of a last round that fills less than
-// all), the parts being joined by a second launch.
+// tiles for the CUs, the parts being joined by a second launch. The ring's tiles
+// are split where at least two parts of each find a CU (128 tiles of K = 5632 110 ->
+// 90 us); to split the tiles of a last, partly filled round is slower, whose CUs
+// clock higher instead (688 tiles of K = 16384 1098 us, the last 176 in four parts
+// 1169).
 //
 // Chosen by the time of a model in us: r tiles that a CU runs at once (at most
 // `most`) take fix r + K max(lat, thr r), parts of K a launch and a pass over them
 // more. The figures were fitted to the times of 7 thousand products of random
 // sizes (65 to 16384 by 256 to 11008, all three layouts), each on several tiles in 1
-// to 16 parts, and are 9 % off in the mean; what is chosen takes 1.3 % longer than
-// the best of what was timed. fp32 has only 64 x 64: wider ones were behind at every
+// to 16 parts, and are 9 % off in the mean; what is chosen takes 1.2 % longer than
+// the best of what was timed, over two thousand others. fp32 has only 64 x 64: wider ones were behind at every
 // size but the largest, by 3 % there (M = N = 2000, K = 8000 503 against 487 us).
 // What the choice is worth (us, unsplit 64 x 64 / 128 x 128 / best split; bf16): 256
 // x 1024, K = 8192 62 / 88 / 17.5; 4096 x 2048, K = 5632 154 / 105 / 97 (ring); 4096
@@ -321,7 +325,6 @@ static inline int few_splits(int64_t T, int64_t N, int64_t K, size_t e) {
 enum { T64 = 0, T64x128 = 1, T128 = 2, TRING = 3 };
 struct Product {
   int tile, splits, kchunk;  // kchunk: K values per part (ring: stages)
-  int n_full, n_split;       // ring
   double us;
 };
 struct TileCost {
@@ -338,8 +341,15 @@ static inline TileCost tile_cost(int tile, size_t e) {
   if (e == 4) return {64, 64, 4, 19.1e-3, 16.0e-3, 0.72};
   if (tile == T64) return {64, 64, 4, 6.4e-3, 4.0e-3, 0.38};
   if (tile == T64x128) return {64, 128, 2, 8.7e-3, 5.8e-3, 1.2};
-  if (tile == T128) return {128, 128, 2, 10.9e-3, 8.1e-3, 2.2};
-  return {256, 256, 1, 17.0e-3, 20.8e-3, 13.4};
+  return {128, 128, 2, 10.9e-3, 8.1e-3, 2.2};
+}
+// n ring tiles over k, one per CU at a time. The clock falls under the power limit as
+// the CUs fill and with the length of the tiles (a full round of K = 2048 47.5 us,
+// 4096 93, 11008 249, 16384 366; a quarter of one of K = 8425 134).
+static inline double ring_us(int64_t n, double k, int ncu) {
+  const double fix = 13.4, least = 12.5e-3, full = 17.0e-3 + 4.5e-7 * (k < 1e4 ? k : 1e4);
+  const double rest = (double)(n % ncu) / ncu;
+  return (double)(n / ncu) * (fix + k * full) + (rest > 0 ? fix + k * (least + rest * (full - least)) : 0);
 }
 // Writing and reading fp32 parts, and the launch that joins them.
 static inline double join_us(double values) { return 5.0 + values * 1.0e-6; }
@@ -354,35 +364,30 @@ static Product plan_product(int64_t M, int64_t N, int64_t K, size_t e) {
       const int per = cdiv(nk, s), parts = cdiv(nk, per);
       if (parts != s) continue;
       const double us = c.us((double)((n * s + ncu - 1) / ncu), (double)per * bk) + (s > 1 ? join_us((double)s * M * N) : 0);
-      if (us < best.us) best = {tile, s, per * bk, 0, 0, us};
+      if (us < best.us) best = {tile, s, per * bk, us};
     }
   }
   if (e == 4) return best;
-  // the ring, where it has at least a quarter of a round of tiles
-  const TileCost c = tile_cost(TRING, e);
-  const int64_t nt = (int64_t)cdiv(M, 256) * cdiv(N, 256), rem = nt % ncu;
+  const int64_t nt = (int64_t)cdiv(M, 256) * cdiv(N, 256);
   if (4 * nt < ncu) return best;
-  const double tile = (double)nk * bk * c.thr, whole = (double)(nt / ncu) * (tile + c.fix);
-  const double alone = c.fix + (2 * rem > ncu || nt > rem ? tile : (double)nk * bk * c.lat);
-  if (whole + (rem ? alone : 0) < best.us) best = {TRING, 1, nk, (int)nt, 0, whole + (rem ? alone : 0)};
-  for (int s = 2; rem && s <= 8 && nk / s >= 8; ++s) {
+  for (int s = 1; s <= 4 && (s == 1 || (nt * s <= ncu && nk / s >= 8)); ++s) {
     const int per = cdiv(nk, s), parts = cdiv(nk, per);
     if (parts != s) continue;
-    const double rounds = (double)((rem * s + ncu - 1) / ncu);
-    const double us = whole + rounds * (tile * per / nk + c.fix) + join_us((double)rem * s * 65536);
-    if (us < best.us) best = {TRING, s, per, (int)(nt - rem), (int)rem, us};
+    const double us = ring_us(nt * s, (double)per * bk, ncu) + (s > 1 ? join_us((double)nt * s * 65536) : 0);
+    if (us < best.us) best = {TRING, s, per, us};
   }
   return best;
 }
 static inline size_t product_bytes(const Product& p, int64_t M, int64_t N) {
-  if (p.tile == TRING) return (size_t)p.n_split * p.splits * 65536 * 4;
-  return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
+  if (p.splits == 1) return 0;
+  return (size_t)p.splits * 4 * (p.tile == TRING ? (size_t)cdiv(M, 256) * cdiv(N, 256) * 65536 : (size_t)M * N);
 }
 // The backward's two products, dW [N, K] over T and dx [T, K] over N. Both in one
 // launch, so that the short tiles of one fill the CUs that the other's last round
-// leaves: on the ring (the longer tiles first), or on 64 x 64 tiles, where it also
-// saves a launch; or each on its own as above. The ring's two, T = 4096, N = 2048,
-// K = 5632, bf16: 176 tiles over 4096 and 352 over 2048 in one launch.
+// leaves: on the ring, or on 64 x 64 tiles, where it also saves a launch, the longer
+// tiles first either way; or each on its own as above. T = 4096, N = 2048, K = 5632,
+// bf16, 176 ring tiles over 4096 and 352 over 2048: 157 us, apart 91 and 95; over
+// four thousand random sizes 0.80 of the time of the two apart.
 struct Grads {
   bool together, ring;
   Product w, x;
@@ -401,10 +406,10 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
     auto split = [&](int64_t M, int64_t n_cols, int64_t len, bool parts) {
       const int nk = cdiv(len, bk);
       const int64_t n = (int64_t)cdiv(M, 64) * cdiv(n_cols, 64);
-      Product p{T64, 1, nk * bk, 0, 0, 0};
+      Product p{T64, 1, nk * bk, 0};
       for (int s = 2; parts && s <= 16 && nk / s >= 4 && n * s <= 2 * ncu; ++s) {
         const int per = cdiv(nk, s);
-        if (cdiv(nk, per) == s) p = {T64, s, per * bk, 0, 0, 0};
+        if (cdiv(nk, per) == s) p = {T64, s, per * bk, 0};
       }
       return p;
     };
@@ -414,8 +419,8 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
       const Product w = split(N, K, T, parts), x = split(T, K, N, parts);
       const double lat = c.lat * (w.kchunk > x.kchunk ? w.kchunk : x.kchunk);
       const double v = (w.splits > 1 ? (double)w.splits * N * K : 0) + (x.splits > 1 ? (double)x.splits * T * K : 0);
-      // (the last tiles to start end half a tile late)
-      const double us = (load > lat ? load + 0.5 * lat : lat) + (v > 0 ? join_us(v) : 0);
+      // (neither the work nor the longest tile alone: the short tiles wait for the long ones' CUs)
+      const double us = 1.1 * (load > lat ? load + 0.5 * lat : lat + 0.5 * load) + (v > 0 ? join_us(v) : 0);
       if (us < best) {
         best = us;
         g = {true, false, w, x};
@@ -423,18 +428,17 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
     }
   }
   if (e == 2) {
-    const TileCost c = tile_cost(TRING, e);
     const int64_t nw = (int64_t)cdiv(N, 256) * cdiv(K, 256), nx = (int64_t)cdiv(T, 256) * cdiv(K, 256);
     // a tiles of length l first, then b of length s
     const int64_t a = T >= N ? nw : nx, b = T >= N ? nx : nw;
-    const double l = (T >= N ? T : N) * c.thr + c.fix, s = (T >= N ? N : T) * c.thr + c.fix;
+    const double l = ring_us(ncu, T >= N ? T : N, ncu), s = ring_us(ncu, T >= N ? N : T, ncu);
     // (all CUs busy until the last tiles, which start half a short one late)
     const double work = (a * l + b * s) / ncu + 0.5 * s, longest = (double)((a + ncu - 1) / ncu) * l;
     const double us = work > longest ? work : longest;
     // (the two together run 3 to 5 % slower than each alone at its best: their panels share L2)
     if (nw + nx >= ncu && 1.05 * us < best) {
       best = us;
-      g = {true, true, Product{TRING, 1, 0, (int)nw, 0, 0}, Product{TRING, 1, 0, (int)nx, 0, 0}};
+      g = {true, true, Product{TRING, 1, 0, 0}, Product{TRING, 1, 0, 0}};
     }
   }
   return g;
@@ -512,32 +516,34 @@ __global__ void __launch_bounds__(256, (BM == 64 && BN == 64 ? 3 : 2)) lin_tile(
   const int nt = g.tiles_m * g.tiles_n, b = blockIdx.x;
   gemm_tile<E, BM, BN, AL, BL, LINEAR>(g, smem, b % nt, b / nt);
 }
-// dW and dx on 64 x 64 tiles.
+// dW and dx on 64 x 64 tiles, the longer ones first.
 template <class E>
-__global__ void __launch_bounds__(256, 3) lin_tile_grads(const KArgs w, const KArgs x) {
+__global__ void __launch_bounds__(256, 3) lin_tile_grads(const KArgs w, const KArgs x, int x_first) {
   constexpr int LW = Geometry<E, 64, 64, MC, MC>::LDS, LX = Geometry<E, 64, 64, KC, MC>::LDS;
   __shared__ __attribute__((aligned(16))) char smem[LW > LX ? LW : LX];
-  const int nw = w.tiles_m * w.tiles_n, nx = x.tiles_m * x.tiles_n, b = blockIdx.x - nw * w.ksplit;
-  if (b < 0) gemm_tile<E, 64, 64, MC, MC, LINEAR>(w, smem, blockIdx.x % nw, blockIdx.x / nw);
-  else gemm_tile<E, 64, 64, KC, MC, LINEAR>(x, smem, b % nx, b / nx);
+  const int nw = w.tiles_m * w.tiles_n, nx = x.tiles_m * x.tiles_n, b = blockIdx.x;
+  const int bw = b - (x_first ? nx * x.ksplit : 0), bx = b - (x_first ? 0 : nw * w.ksplit);
+  if (x_first ? bw >= 0 : bx < 0) gemm_tile<E, 64, 64, MC, MC, LINEAR>(w, smem, bw % nw, bw / nw);
+  else gemm_tile<E, 64, 64, KC, MC, LINEAR>(x, smem, bx % nx, bx / nx);
 }
 
-// The ring: the first n_full tiles, with the epilogue.
+// The ring, whole tiles with the epilogue.
 template <class E, int ACT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring(const KArgs g) {
   SWIGLU_RING_LDS(true)
   ring5_tile<E, KC, KC, LINEAR, ACT>(g, R, blockIdx.x, 0);
 }
-// The parts of the tiles from n_full on (a kernel that ended in either the
-// epilogue or a part's sums spilled accumulators: 1210 us became 1314).
+// Parts of its tiles, workgroup i being part i % ksplit of tile i / ksplit. (A kernel
+// that ended in either the epilogue or a part's sums spilled accumulators: 1210 us
+// became 1314.)
 template <class E>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring_parts(const KArgs g) {
   SWIGLU_RING_LDS(true)
-  const int piece = blockIdx.x;
-  ring5_tile<E, KC, KC, PLAIN>(g, R, g.n_full + piece / g.ksplit, 0, piece % g.ksplit, piece);
+  const int i = blockIdx.x;
+  ring5_tile<E, KC, KC, PLAIN>(g, R, i / g.ksplit, 0, i % g.ksplit, i);
 }
-// dx: whole tiles, then parts. (The host pass of the compiler refuses to
-// instantiate this tile from two kernels.)
+// dx, whole tiles or parts. (The host pass of the compiler refuses to instantiate
+// this tile from two kernels.)
 template <class E>
 __device__ __forceinline__ void dx_tile(const KArgs& g, char* const (&R)[5], int item, int ks, int piece) {
   ring5_tile<E, KC, MC, PLAIN>(g, R, item, 0, ks, piece);
@@ -545,25 +551,25 @@ __device__ __forceinline__ void dx_tile(const KArgs& g, char* const (&R)[5], int
 template <class E>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring_dx(const KArgs g) {
   SWIGLU_RING_LDS(true)
-  int item = blockIdx.x, ks = 0, piece = -1;
-  if (item >= g.n_full) {
-    piece = item - g.n_full;
-    item = g.n_full + piece / g.ksplit;
-    ks = piece % g.ksplit;
-  }
-  dx_tile<E>(g, R, item, ks, piece);
+  const int i = blockIdx.x;
+  dx_tile<E>(g, R, i / g.ksplit, i % g.ksplit, g.ksplit > 1 ? i : -1);
 }
-// Joins the parts of the ring's split tiles (16 bits): eight columns of a row per
-// thread.
+template <class E>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring_dw(const KArgs g) {
+  SWIGLU_RING_LDS(true)
+  const int i = blockIdx.x;
+  ring5_tile<E, MC, MC, PLAIN>(g, R, i / g.ksplit, 0, i % g.ksplit, g.ksplit > 1 ? i : -1);
+}
+// Joins the parts of the ring's tiles (16 bits): eight columns of a row per thread.
 template <class E>
 __global__ void __launch_bounds__(256) lin_join_tiles(const KArgs g) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int r = (int)(i >> 13), rr = (int)(i >> 5) & 255, c = ((int)i & 31) * 8;
+  const int t = (int)(i >> 13), r = (int)(i >> 5) & 255, c = ((int)i & 31) * 8;
   int tm, tn;
-  tile_coords(g.n_full + r, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
-  const int m = tm * 256 + rr, n = tn * 256 + c;
+  tile_coords(t, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+  const int m = tm * 256 + r, n = tn * 256 + c;
   if (m >= g.M || n >= g.N) return;
-  const float* p = g.P + (int64_t)r * g.ksplit * 65536 + rr * 256 + c;
+  const float* p = g.P + (int64_t)t * g.ksplit * 65536 + r * 256 + c;
   float z[8] = {};
   for (int s = 0; s < g.ksplit; ++s)
 #pragma unroll
@@ -582,24 +588,25 @@ lin_ring_grads(const KArgs w, const KArgs x, int first) {
 
 static inline int status() { return hipGetLastError() == hipSuccess ? SWIGLU_OK : SWIGLU_ERR_LAUNCH; }
 
+static inline dim3 ring_grid(const KArgs& a) { return dim3(a.tiles_m * a.tiles_n * a.ksplit); }
 template <class E, int ACT>
 int launch_lin_ring(const KArgs& a, hipStream_t s) {
-  if (a.n_full) hipLaunchKernelGGL((lin_ring<E, ACT>), dim3(a.n_full), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((lin_ring<E, ACT>), ring_grid(a), dim3(256), 0, s, a);
   return status();
 }
 template <class E>
 int launch_lin_ring_parts(const KArgs& a, hipStream_t s) {
-  if (a.n_split) hipLaunchKernelGGL((lin_ring_parts<E>), dim3(a.n_split * a.ksplit), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((lin_ring_parts<E>), ring_grid(a), dim3(256), 0, s, a);
   return status();
 }
 template <class E>
 static int launch_ring_dx(const KArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((lin_ring_dx<E>), dim3(a.n_full + a.n_split * a.ksplit), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((lin_ring_dx<E>), ring_grid(a), dim3(256), 0, s, a);
   return status();
 }
 template <class E>
 static int launch_ring_dw(const KArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((ring_wgrad<E, MC, MC, STAGE_LINEAR_DW>), dim3(a.n_full + a.n_split * a.ksplit), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((lin_ring_dw<E>), ring_grid(a), dim3(256), 0, s, a);
   return status();
 }
 #define SWIGLU_LIN_RING_DECL(PREFIX, E)                                             \
@@ -642,25 +649,23 @@ static int launch_tiles(KArgs a, hipStream_t s) {
   const int rc = status();
   return rc ? rc : launch_join<E>(a, KArgs{}, s);
 }
-// A product as planned; `ring` launches it there.
+// A product as planned; on the ring `whole` launches it, or `parts` its parts.
 using RingLaunch = int (*)(const KArgs&, hipStream_t);
 template <class E, int AL, int BL, int STAGE>
-static int run_product(KArgs a, const Product& p, float* parts, hipStream_t s, RingLaunch ring, RingLaunch rest = nullptr) {
+static int run_product(KArgs a, const Product& p, float* sums, hipStream_t s, RingLaunch whole, RingLaunch parts) {
   a.planes = 1;
   a.ksplit = p.splits;
   a.kchunk = p.kchunk;
-  a.P = parts;
+  a.P = sums;
   if constexpr (E::kBytes == 2) {
     if (p.tile == TRING) {
       a.tiles_m = cdiv(a.M, 256);
       a.tiles_n = cdiv(a.N, 256);
-      a.n_full = p.n_full;
-      a.n_split = p.n_split;
       a.group_m = AL == MC ? 4 : BL == MC ? 1 : 2;
-      int rc = ring(a, s);
-      if (!rc && rest) rc = rest(a, s);
-      if (rc || p.n_split == 0) return rc;
-      hipLaunchKernelGGL((lin_join_tiles<E>), dim3(p.n_split * 32), dim3(256), 0, s, a);
+      if (p.splits == 1) return whole(a, s);
+      const int rc = parts(a, s);
+      if (rc) return rc;
+      hipLaunchKernelGGL((lin_join_tiles<E>), dim3(a.tiles_m * a.tiles_n * 32), dim3(256), 0, s, a);
       return status();
     }
     if (p.tile == T64x128) return launch_tiles<E, AL, BL, STAGE, 64, 128>(a, s);
@@ -707,17 +712,17 @@ int run_fwd(const Fwd& c) {
     a.ksplit = f.splits;
     return launch_join<E>(a, KArgs{}, c.stream);
   }
-  RingLaunch ring = nullptr, rest = nullptr;
+  RingLaunch whole = nullptr, parts = nullptr;
   if constexpr (E::kBytes == 2) {
-    rest = &launch_lin_ring_parts<E>;
-    ring = c.act == SWIGLU_ACT_RELU        ? &launch_lin_ring<E, SWIGLU_ACT_RELU>
-           : c.act == SWIGLU_ACT_GELU      ? &launch_lin_ring<E, SWIGLU_ACT_GELU>
-           : c.act == SWIGLU_ACT_GELU_TANH ? &launch_lin_ring<E, SWIGLU_ACT_GELU_TANH>
-           : c.act == SWIGLU_ACT_SILU      ? &launch_lin_ring<E, SWIGLU_ACT_SILU>
-                                           : &launch_lin_ring<E, SWIGLU_ACT_NONE>;
+    parts = &launch_lin_ring_parts<E>;
+    whole = c.act == SWIGLU_ACT_RELU        ? &launch_lin_ring<E, SWIGLU_ACT_RELU>
+            : c.act == SWIGLU_ACT_GELU      ? &launch_lin_ring<E, SWIGLU_ACT_GELU>
+            : c.act == SWIGLU_ACT_GELU_TANH ? &launch_lin_ring<E, SWIGLU_ACT_GELU_TANH>
+            : c.act == SWIGLU_ACT_SILU      ? &launch_lin_ring<E, SWIGLU_ACT_SILU>
+                                            : &launch_lin_ring<E, SWIGLU_ACT_NONE>;
   }
   StageScope scope(STAGE_LINEAR, c.stream);
-  return run_product<E, KC, KC, STAGE_LINEAR>(a, fwd_plan(c.T, c.N, c.K, E::kBytes), (float*)c.ws, c.stream, ring, rest);
+  return run_product<E, KC, KC, STAGE_LINEAR>(a, fwd_plan(c.T, c.N, c.K, E::kBytes), (float*)c.ws, c.stream, whole, parts);
 }
 
 template <class E>
@@ -770,7 +775,8 @@ int run_bwd(const Bwd& c) {
         w.tiles_n = x.tiles_n = cdiv(w.N, 256);
         w.group_m = 4;
         x.group_m = 1;
-        hipLaunchKernelGGL((lin_ring_grads<E>), dim3(g.w.n_full + g.x.n_full), dim3(256), 0, s, w, x, c.T >= c.N ? 0 : 1);
+        hipLaunchKernelGGL((lin_ring_grads<E>), dim3((w.tiles_m + x.tiles_m) * w.tiles_n), dim3(256), 0, s, w, x,
+                           c.T >= c.N ? 0 : 1);
         return status();
       }
     }
@@ -784,7 +790,7 @@ int run_bwd(const Bwd& c) {
     x.kchunk = g.x.kchunk;
     x.P = x_parts;
     const int n = w.tiles_n * (w.tiles_m * w.ksplit + x.tiles_m * x.ksplit);
-    hipLaunchKernelGGL((lin_tile_grads<E>), dim3(n), dim3(256), 0, s, w, x);
+    hipLaunchKernelGGL((lin_tile_grads<E>), dim3(n), dim3(256), 0, s, w, x, x.kchunk > w.kchunk);
     const int rc = status();
     return rc ? rc : launch_join<E>(w, x, s);
   }
@@ -795,12 +801,12 @@ int run_bwd(const Bwd& c) {
   }
   if (c.dw) {
     StageScope scope(STAGE_LINEAR_DW, s);
-    const int rc = run_product<E, MC, MC, STAGE_LINEAR_DW>(w, g.w, parts, s, dw_ring);
+    const int rc = run_product<E, MC, MC, STAGE_LINEAR_DW>(w, g.w, parts, s, dw_ring, dw_ring);
     if (rc) return rc;
   }
   if (c.dx) {
     StageScope scope(STAGE_LINEAR_DX, s);
-    return run_product<E, KC, MC, STAGE_LINEAR_DX>(x, g.x, x_parts, s, dx_ring);
+    return run_product<E, KC, MC, STAGE_LINEAR_DX>(x, g.x, x_parts, s, dx_ring, dx_ring);
   }
   return SWIGLU_OK;
 }

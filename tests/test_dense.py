@@ -171,7 +171,7 @@ def test_norm_every_width(dtype, rms):
     """More rows than one launch's gradient takes, at widths for each number of waves
     and pieces, whole and odd."""
     dt = DTYPES[dtype]
-    for i, D in enumerate((512, 1000, 2048, 4096, 8192, 16384, 16392, 511, 1001, 2047, 4095, 8191, 12345, 40001)):
+    for i, D in enumerate((512, 1000, 2048, 4096, 8192, 16384, 16392, 511, 701, 1001, 2047, 4095, 8191, 12345, 40001)):
         D = D if dt != torch.float32 else D // 2
         T = 257 + 13 * i % 50
         banner(f"norm width {dtype} rms={rms} T={T} D={D}")
@@ -397,9 +397,9 @@ VARIANTS = {
     (1677, 208, 4672): "dx on 64 x 128", (136, 2848, 1288): "dW on 128 x 128", (892, 176, 3944): "dx on 128 x 128",
     (1048, 3648, 464): "dx on 128 x 128 in parts", (2987, 80, 4232): "dW on 128 x 128 in parts", (548, 208, 176): "dx on 64 x 64",
     (1106, 288, 200): "dW on 64 x 64 in parts", (2100, 4104, 72): "both gradients together in parts",
-    (2100, 2056, 4104): "ring, all tiles in parts; both gradients on the ring", (4200, 4104, 2056): "ring with a split rest",
-    (2100, 4104, 2056): "dW on the ring, dx there in parts", (2056, 4200, 4104): "both on the ring, dx's tiles longer; dW with a split rest",
-    (4096, 2048, 5632): "dx on the ring with a split rest",
+    (2100, 2056, 4104): "ring, all tiles in parts; both gradients on the ring", (4200, 4104, 2056): "more than a round of ring tiles",
+    (2100, 4104, 2056): "dW on the ring, dx there in parts", (2056, 4200, 4104): "both on the ring, dx's tiles the longer",
+    (4096, 2048, 5632): "ring tiles in two parts",
 }
 
 
