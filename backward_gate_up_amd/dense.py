@@ -40,19 +40,12 @@ def _c(name):
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _on(fn):
-    """The library launches on the current device: makes it that of the first
-    tensor."""
-
-    @functools.wraps(fn)
-    def call(x, *args, **kw):
-        device = x.device
-        if device.type != "cuda" or device.index == _device():  # (other tensors are refused further in)
-            return fn(x, *args, **kw)
-        with torch.cuda.device(device):
-            return fn(x, *args, **kw)
-
-    return call
+def _on(device, call, *args):
+    """call(*args) with ``device`` current: the library launches on the current one."""
+    if device.index == _device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def _act(activation):
@@ -63,10 +56,15 @@ def _act(activation):
 
 
 def _same(x, *others):
+    """(dtype's code, device) of tensors that share them."""
+    dtype, device = x.dtype, x.device
     for t in others:
-        if t is not None and (t.dtype != x.dtype or t.device != x.device):
+        if t is not None and (t.dtype != dtype or t.device != device):
             raise ValueError("all tensors must share dtype and device")
-    _on_gpu(x)
+    if not x.is_cuda:
+        _on_gpu(x)
+    dt = _DT.get(dtype)
+    return (_code(x) if dt is None else dt), device
 
 
 def _opt(t):
@@ -90,59 +88,65 @@ def _flat16(t):
 # ---- norms ------------------------------------------------------------------
 
 
-def _norm_shapes(x, weight, bias, eps, rms):
-    if x.dim() != 2 or weight.dim() != 1 or weight.shape[0] != x.shape[1] or x.shape[1] == 0:
-        raise ValueError(f"expected X[T,D] and weight[D]: X{tuple(x.shape)} weight{tuple(weight.shape)}")
+def _norm_args(x, weight, bias, eps, rms):
+    """(dtype's code, device), after checking the arguments."""
+    shape = x.shape
+    if len(shape) != 2 or weight.shape != shape[1:] or shape[1] == 0:
+        raise ValueError(f"expected X[T,D] and weight[D]: X{tuple(shape)} weight{tuple(weight.shape)}")
     if bias is not None and (rms or bias.shape != weight.shape):
         raise ValueError("RMS norm has no bias" if rms else f"bias must be [D]: {tuple(bias.shape)}")
     if not 0 <= eps < math.inf:
         raise ValueError(f"eps must be a number from 0 up: got {eps}")
-    _same(x, weight, bias)
+    return _same(x, weight, bias)
 
 
-@_on
+def _norm_fwd(x, weight, bias, eps, rms, stats, dt, device):
+    T, D = x.shape
+    y = torch.empty_like(x)
+    st = torch.empty((1 if rms else 2, T), dtype=torch.float32, device=device) if stats else None
+    rc = _c("norm_fwd")(x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
+                        st.data_ptr() if stats else None, T, D, eps, rms, dt, _stream(device))
+    if rc:
+        _check(rc, "swiglu_mlp_norm_fwd")
+    return y, st
+
+
 def norm_fwd(x, weight, bias=None, eps=1e-5, rms=False, stats=True):
     """Y = (x - mean) rstd weight + bias over the last axis of x[T, D], rstd = 1 /
     sqrt(mean((x - mean)^2) + eps); with ``rms`` the mean is 0 and there is no
     bias. Returns (Y, stats): fp32 [2, T] (mean, rstd), with ``rms`` [1, T]
     (rstd), for ``norm_bwd``; None without ``stats``."""
-    _norm_shapes(x, weight, bias, eps, rms)
-    x, weight, bias = _flat(x), _flat(weight), _flat(bias)
-    T, D = x.shape
-    y = torch.empty_like(x)
-    st = torch.empty((1 if rms else 2, T), dtype=torch.float32, device=x.device) if stats else None
-    rc = _c("norm_fwd")(_ptr(x), weight.data_ptr(), _opt(bias), _ptr(y), _opt(st), T, D, eps, rms, _code(x), _stream(x.device))
-    _check(rc, "swiglu_mlp_norm_fwd")
-    return y, st
+    dt, device = _norm_args(x, weight, bias, eps, rms)
+    return _on(device, _norm_fwd, _flat(x), _flat(weight), _flat(bias), eps, bool(rms), stats, dt, device)
 
 
-def _norm_bwd(dy, x, weight, st, rms, bias, dres=None, workspace=None):
+def _norm_bwd(dy, x, weight, st, rms, bias, dt, device, dres=None, workspace=None):
     T, D = x.shape
-    dt, device = _DT[x.dtype], x.device
     dx, dw = torch.empty_like(x), torch.empty_like(weight)
     db = torch.empty_like(weight) if bias else None
     need = _bytes("swiglu_mlp_norm_bwd_workspace_bytes", T, D, rms, dt)
     ws, nbytes, keep = _workspace(workspace, need, device) if need else (None, 0, None)
-    rc = _c("norm_bwd")(_ptr(dy), _ptr(x), weight.data_ptr(), _ptr(st), _opt(dres), _ptr(dx), dw.data_ptr(),
-                        db.data_ptr() if bias else None, ws, nbytes, T, D, rms, dt, _stream(device))
-    _check(rc, "swiglu_mlp_norm_bwd")
+    rc = _c("norm_bwd")(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), st.data_ptr(), None if dres is None else dres.data_ptr(),
+                        dx.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else None, ws, nbytes, T, D, rms, dt,
+                        _stream(device))
+    if rc:
+        _check(rc, "swiglu_mlp_norm_bwd")
     return dx, dw, db
 
 
-@_on
 def norm_bwd(dy, x, weight, stats, rms=False, bias=False, dres=None, workspace=None):
     """(dX, dweight, dbias) of ``norm_fwd``; dbias is None unless ``bias``. ``dres``
     [T, D] is added to dX (the gradient that reaches x past the norm)."""
     if dy.shape != x.shape or (dres is not None and dres.shape != x.shape):
         raise ValueError("dY and dres must match X in shape")
-    _norm_shapes(x, weight, None, 0.0, rms)
-    _same(x, dy, dres)
-    _code(x)
-    if tuple(stats.shape) != (1 if rms else 2, x.shape[0]) or stats.dtype != torch.float32 or stats.device != x.device:
+    _norm_args(x, weight, None, 0.0, rms)
+    dt, device = _same(x, dy, dres)
+    if tuple(stats.shape) != (1 if rms else 2, x.shape[0]) or stats.dtype != torch.float32 or stats.device != device:
         raise ValueError("stats must be the fp32 tensor returned by norm_fwd")
     if bias and rms:
         raise ValueError("RMS norm has no bias")
-    return _norm_bwd(_flat(dy), _flat(x), _flat(weight), _flat(stats), bool(rms), bool(bias), _flat(dres), workspace)
+    return _on(device, _norm_bwd, _flat(dy), _flat(x), _flat(weight), _flat(stats), bool(rms), bool(bias), dt, device,
+               _flat(dres), workspace)
 
 
 def _no_second():
@@ -153,10 +157,11 @@ def _no_second():
 class NormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, rms):
+        dt, device = _norm_args(x, weight, bias, eps, rms)
         x, weight = _flat(x), _flat(weight)
-        y, stats = norm_fwd(x, weight, bias, eps, rms)
+        y, stats = _on(device, _norm_fwd, x, weight, _flat(bias), eps, rms, True, dt, device)
         ctx.save_for_backward(x, weight, stats)
-        ctx.form = rms, bias is not None
+        ctx.form = rms, bias is not None, dt, device
         return y
 
     @staticmethod
@@ -168,14 +173,16 @@ class NormFunction(torch.autograd.Function):
 
 
 def _norm(x, weight, bias, eps, rms):
-    if x.dim() == 0:
+    n = x.dim()
+    if n == 0:
         raise ValueError("expected X[..., D]")
-    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    x2 = x if n == 2 else x.reshape(-1, x.shape[-1])
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
         y = NormFunction.apply(x2, weight, bias, eps, rms)
     else:
-        y = norm_fwd(x2, weight, bias, eps, rms, False)[0]
-    return y if x.dim() == 2 else y.reshape(x.shape)
+        dt, device = _norm_args(x2, weight, bias, eps, rms)
+        y = _on(device, _norm_fwd, _flat(x2), _flat(weight), _flat(bias), eps, rms, False, dt, device)[0]
+    return y if n == 2 else y.reshape(x.shape)
 
 
 def layer_norm(x, weight, bias=None, eps=1e-5):
@@ -193,54 +200,57 @@ def rms_norm(x, weight, eps=1e-6):
 # ---- linear layer -------------------------------------------------------------
 
 
-def _linear_shapes(x, w, bias, residual):
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError(f"shape mismatch (expected X[T,K], W[N,K]): X{tuple(x.shape)} W{tuple(w.shape)}")
-    T, (N, K) = x.shape[0], w.shape
+def _linear_args(x, w, bias, residual):
+    """(dtype's code, device), after checking the arguments."""
+    shape, (N, K) = x.shape, w.shape if w.dim() == 2 else (None, None)
+    if len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"shape mismatch (expected X[T,K], W[N,K]): X{tuple(shape)} W{tuple(w.shape)}")
     if bias is not None and bias.shape != (N,):
         raise ValueError(f"bias must be [N] = [{N}]: {tuple(bias.shape)}")
-    if residual is not None and residual.shape != (T, N):
-        raise ValueError(f"residual must be [T, N] = {[T, N]}: {tuple(residual.shape)}")
-    _same(x, w, bias, residual)
-    return T, N, K
+    if residual is not None and residual.shape != (shape[0], N):
+        raise ValueError(f"residual must be [T, N] = {[shape[0], N]}: {tuple(residual.shape)}")
+    return _same(x, w, bias, residual)
 
 
-@_on
+def _linear_fwd(x, w, bias, act, residual, keep, dt, device, workspace=None):
+    T, K = x.shape
+    N = w.shape[0]
+    y = torch.empty((T, N), dtype=x.dtype, device=device)
+    z = torch.empty_like(y) if keep and act else None
+    need = _bytes("swiglu_mlp_linear_workspace_bytes", T, N, K, dt)
+    ws, nbytes, held = _workspace(workspace, need, device) if need else (None, 0, None)
+    rc = _c("linear_fwd")(x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(), _opt(residual), y.data_ptr(),
+                          _opt(z), ws, nbytes, T, N, K, act, dt, _stream(device))
+    if rc:
+        _check(rc, "swiglu_mlp_linear_fwd")
+    return y, z
+
+
 def linear_fwd(x, w, bias=None, activation=None, residual=None, keep=True, workspace=None):
     """Y = act(x W^T + bias) + residual: x[T, K], w[N, K], bias[N], residual[T, N];
     ``activation`` None, "relu", "gelu", "gelu_tanh" or "silu". K and N are
     multiples of 8. Returns (Y, Z): Z[T, N] is the activation's argument in the
     inputs' dtype, for ``linear_bwd``; None without an activation or ``keep``."""
     act = _act(activation)
-    T, N, K = _linear_shapes(x, w, bias, residual)
-    x, w, bias, residual = _flat16(x), _flat16(w), _flat16(bias), _flat16(residual)
-    dt, device = _code(x), x.device
-    y = torch.empty((T, N), dtype=x.dtype, device=device)
-    z = torch.empty_like(y) if keep and act else None
-    need = _bytes("swiglu_mlp_linear_workspace_bytes", T, N, K, dt)
-    ws, nbytes, held = _workspace(workspace, need, device) if need else (None, 0, None)
-    rc = _c("linear_fwd")(_ptr(x), _ptr(w), _opt(bias), _opt(residual), _ptr(y), _opt(z), ws, nbytes, T, N, K, act, dt,
-                          _stream(device))
-    _check(rc, "swiglu_mlp_linear_fwd")
-    return y, z
+    dt, device = _linear_args(x, w, bias, residual)
+    return _on(device, _linear_fwd, _flat16(x), _flat16(w), _flat16(bias), act, _flat16(residual), keep, dt, device, workspace)
 
 
-def _linear_bwd(dy, x, w, z, act, needs, workspace=None):
+def _linear_bwd(dy, x, w, z, act, needs, dt, device, workspace=None):
     T, K = x.shape
     N = w.shape[0]
-    dt, device = _DT[x.dtype], x.device
     dx = torch.empty_like(x) if needs[0] else None
     dw = torch.empty_like(w) if needs[1] else None
     db = torch.empty(N, dtype=x.dtype, device=device) if needs[2] else None
     need = _bytes("swiglu_mlp_linear_bwd_workspace_bytes", T, N, K, act, dt)
     ws, nbytes, held = _workspace(workspace, need, device) if need else (None, 0, None)
-    rc = _c("linear_bwd")(_ptr(dy), _ptr(x), w.data_ptr(), _opt(z), _opt(dx), _opt(dw), _opt(db), ws, nbytes, T, N, K, act, dt,
-                          _stream(device))
-    _check(rc, "swiglu_mlp_linear_bwd")
+    rc = _c("linear_bwd")(dy.data_ptr(), x.data_ptr(), w.data_ptr(), z.data_ptr() if act else None, _opt(dx), _opt(dw), _opt(db),
+                          ws, nbytes, T, N, K, act, dt, _stream(device))
+    if rc:
+        _check(rc, "swiglu_mlp_linear_bwd")
     return dx, dw, db
 
 
-@_on
 def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), workspace=None):
     """(dX, dW, dbias) of ``linear_fwd``; ``needs`` says which are wanted, the
     others are None. ``z``: what ``linear_fwd`` kept, where there is an
@@ -251,29 +261,31 @@ def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), work
     if act and (z is None or z.shape != dy.shape):
         raise ValueError("z must be the [T, N] tensor returned by linear_fwd")
     z = z if act else None
-    _linear_shapes(x, w, None, dy)
+    dt, device = _linear_args(x, w, None, dy)
     _same(x, z)
-    _code(x)
-    return _linear_bwd(_flat16(dy), _flat16(x), _flat16(w), _flat16(z), act, needs, workspace)
+    return _on(device, _linear_bwd, _flat16(dy), _flat16(x), _flat16(w), _flat16(z), act, needs, dt, device, workspace)
 
 
 class LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, activation):
+        act = _act(activation)
+        dt, device = _linear_args(x, w, bias, residual)
         x, w = _flat16(x), _flat16(w)
-        y, z = linear_fwd(x, w, bias, activation, residual)
+        y, z = _on(device, _linear_fwd, x, w, _flat16(bias), act, _flat16(residual), True, dt, device)
         ctx.save_for_backward(x, w, z)
-        ctx.act = _L.ACTS[activation]
+        ctx.form = act, dt, device
         return y
 
     @staticmethod
     def backward(ctx, dy):
         _no_second()
         x, w, z = ctx.saved_tensors
+        act, dt, device = ctx.form
         needs = ctx.needs_input_grad
         dx = dw = db = None
         if needs[0] or needs[1] or needs[2]:
-            dx, dw, db = _linear_bwd(_flat16(dy), x, w, z, ctx.act, needs)
+            dx, dw, db = _linear_bwd(_flat16(dy), x, w, z, act, needs, dt, device)
         return dx, dw, db, dy if needs[3] else None, None
 
 
@@ -294,7 +306,9 @@ def linear(x, w, bias=None, activation=None, residual=None):
                                     or (residual is not None and residual.requires_grad)):
         y = LinearFunction.apply(x, w, bias, residual, activation)
     else:
-        y = linear_fwd(x, w, bias, activation, residual, False)[0]
+        act = _act(activation)
+        dt, device = _linear_args(x, w, bias, residual)
+        y = _on(device, _linear_fwd, _flat16(x), _flat16(w), _flat16(bias), act, _flat16(residual), False, dt, device)[0]
     return y if len(shape) == 2 else y.reshape(shape)
 
 
@@ -312,25 +326,25 @@ class FeedForwardFunction(torch.autograd.Function):
         a, z = linear_fwd(n, w1, b1, activation)
         y = linear_fwd(a, w2, b2, None, x)[0]
         ctx.save_for_backward(x, nw, w1, w2, n, stats, a, z)
-        ctx.form = _L.ACTS[activation], rms, nb is not None
+        ctx.form = _L.ACTS[activation], rms, nb is not None, _DT[x.dtype], x.device
         return y
 
     @staticmethod
     def backward(ctx, dy):
         _no_second()
         x, nw, w1, w2, n, stats, a, z = ctx.saved_tensors
-        act, rms, norm_bias = ctx.form
+        act, rms, norm_bias, dt, device = ctx.form
         need = ctx.needs_input_grad
         dy = _flat16(dy)
         norm = need[0] or need[1] or need[2]
         inner = norm or need[3] or need[4]
-        da, dw2, db2 = _linear_bwd(dy, a, w2, None, 0, (inner, need[5], need[6]))
+        da, dw2, db2 = _linear_bwd(dy, a, w2, None, 0, (inner, need[5], need[6]), dt, device)
         dx = dnw = dnb = dw1 = db1 = None
         if inner:
-            dn, dw1, db1 = _linear_bwd(da, n, w1, z, act, (norm, need[3], need[4]))
+            dn, dw1, db1 = _linear_bwd(da, n, w1, z, act, (norm, need[3], need[4]), dt, device)
             del da
             if norm:
-                dx, dnw, dnb = _norm_bwd(dn, x, nw, stats, rms, norm_bias, dy)
+                dx, dnw, dnb = _norm_bwd(dn, x, nw, stats, rms, norm_bias, dt, device, dy)
         return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
 
 

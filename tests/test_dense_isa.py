@@ -68,8 +68,7 @@ def test_streams_keep_their_wait_states(asm):
 def test_no_scratch(asm):
     for unit, text in asm.items():
         for m in re.finditer(r"^(_ZN6swiglu\w+):\s.*?ScratchSize: (\d+)", text, re.M | re.S):
-            # the ring's last stages read their array pointers from scratch, and kernels that end in
-            # either an epilogue or a part's sums put some of them there on the way: none of it in a loop
-            # of matrix instructions (above)
-            limit = 512 if "ring" in m.group(1) else 0
+            # a ring's last stages read their array pointers from scratch: none of it in a loop of matrix
+            # instructions (above)
+            limit = 64 if "ring" in m.group(1) else 0
             assert int(m.group(2)) <= limit, (unit, m.group(1), m.group(2))
