@@ -80,21 +80,24 @@ __device__ __forceinline__ float act_f32(float z) {
   else return z;
 }
 
-// the derivative
+// The derivative. At an infinity it is the limit, 0 or 1 and not 0 times an infinity:
+// z may be one because a finite sum left the storage type's range, whose y is finite.
+// The factors beside z are 0 from |z| = 104 on, so z is cut off at 1000 there; a NaN
+// stays one by those factors.
 template <bool IEEE, int ACT>
 __device__ __forceinline__ float act_slope(float z) {
+  const float cut = __builtin_amdgcn_fmed3f(z, -1000.0f, 1000.0f);
   if constexpr (ACT == SWIGLU_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   else if constexpr (ACT == SWIGLU_ACT_GELU) {
     float e;
     const float c = normal_cdf<IEEE>(z, e);
-    return fmaf(z * e, 0.39894228040143268f, c);
+    return fmaf(cut * e, 0.39894228040143268f, c);
   } else if constexpr (ACT == SWIGLU_ACT_GELU_TANH) {
     const float s = sigma<IEEE>(tanh_arg(z));
-    // (past |z| = 1000 s (1 - s) is zero, and z^2 must not be an infinity beside it)
-    return fmaf(z * s * (1.0f - s), kTwoRoot2OverPi * fmaf(fminf(z * z, 1e6f), 3.0f * 0.044715f, 1.0f), s);
+    return fmaf(cut * s * (1.0f - s), kTwoRoot2OverPi * fmaf(cut * cut, 3.0f * 0.044715f, 1.0f), s);
   } else if constexpr (ACT == SWIGLU_ACT_SILU) {
     const float s = sigma<IEEE>(z);
-    return fmaf(z * s, 1.0f - s, s);
+    return fmaf(cut * s, 1.0f - s, s);
   } else return 1.0f;
 }
 

@@ -346,7 +346,8 @@ int swiglu_mlp_norm_bwd(const void* dY, const void* X, const void* weight, const
  * dY act'(Z) (rounded to the storage type for the two products, not for the
  * sum); NULL: not wanted. The residual's gradient is dY. T = 0 writes zero
  * weight gradients. gelu is z Phi(z), gelu_tanh its form with tanh; relu's
- * derivative at 0 and at NaN is 0. In bf16 and fp16 silu and gelu_tanh of values
+ * derivative at 0 and at NaN is 0, every derivative at an infinity its limit (a
+ * Z past the storage type's range). In bf16 and fp16 silu and gelu_tanh of values
  * below about -87 (2u for gelu_tanh) may be a zero. workspace contents on entry do
  * not matter; calls that share one must be stream-ordered. */
 typedef enum {

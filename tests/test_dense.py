@@ -477,6 +477,35 @@ def test_linear_nan_and_infinity_keep_their_place():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_slopes_at_infinity_are_their_limits(act, dtype):
+    """A sum past the storage type's range is kept as an infinity, y of a negative one
+    is 0: its gradient is 0, that of a positive one dY; NaN stays NaN."""
+    banner(f"slopes at infinity {act} {dtype}")
+    dt, N, K = DTYPES[dtype], 64, 72
+    for T in (5, 700):
+        g = gen(T)
+        x, w, dy = normal(g, (T, K), dt), normal(g, (N, K), dt), normal(g, (T, N), dt)
+        z = torch.full((T, N), math.inf, dtype=dt, device=DEV)
+        z[:, 1::2] = -math.inf
+        z[2, 4] = math.nan
+        dx, dw, db = mlp.linear_bwd(dy, x, w, z, act)
+        dz = dy.double()
+        dz[:, 1::2] = 0
+        dz[2, 4] = 0 if act == "relu" else math.nan
+        ref = (dz @ w.double(), dz.mT.contiguous() @ x.double(), dz.sum(0))
+        bad = [torch.isnan(t) for t in ref]
+        size = (dz.nan_to_num().abs() @ w.double().abs(), dz.nan_to_num().abs().mT.contiguous() @ x.double().abs(),
+                dz.nan_to_num().abs().sum(0))
+        for got, want, nan, s, n in zip((dx, dw, db), ref, bad, size, (N, T, T)):
+            assert torch.equal(got.isnan(), nan), (act, T)
+            # dz is exact; n fp32 additions and the rounding of the output
+            bound = n * 2.0 ** -24 * s + half(dt) * want.abs() + tiny(dt)
+            assert ((got.double() - want).abs() <= bound)[~nan].all(), (act, T)
+
+
+@pytest.mark.gpu
 def test_rows_behind_the_last_token_are_left():
     banner("linear rows behind")
     L = _lib.lib()
