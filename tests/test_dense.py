@@ -545,6 +545,93 @@ def test_no_tokens():
     assert s[0].shape == (0, 64) and (dw == 0).all() and (db == 0).all()
 
 
+def long(T, N, seed):
+    """[T, N] in bf16 with rows that differ, made on the GPU."""
+    g = torch.Generator(DEV).manual_seed(seed)
+    t = torch.empty((T, N), dtype=torch.bfloat16, device=DEV)
+    for i in range(0, T, 65536):
+        t[i : i + 65536].normal_(generator=g)
+    return t
+
+
+@pytest.mark.gpu
+def test_widest_rows():
+    """Rows of SWIGLU_NORM_MAX_D elements, few of them and as many as leave partial sums."""
+    D = 1 << 20
+    for T, rms in ((2, False), (300, True)):
+        banner(f"widest rows {T}")
+        g = gen(T)
+        x, w, dy = long(T, D, T), normal(g, (D,), torch.bfloat16), long(T, D, T + 1)
+        b = None if rms else normal(g, (D,), torch.bfloat16)
+        y, st = mlp.norm_fwd(x, w, b, 1e-6, rms)
+        dx, dw, db = mlp.norm_bwd(dy, x, w, st, rms, not rms)
+        rows = [0, T // 2, T - 1]
+        ref = norm_reference(x[rows], w, b, 1e-6, rms, dy[rows])
+        inside(y[rows], *ref[0], ("y", T))
+        inside(dx[rows], *ref[1], ("dx", T))
+        # the weight's gradient at a piece of the columns, from the statistics of all rows
+        cols = torch.cat([torch.arange(0, 64), torch.arange(D - 64, D)]).to(DEV)
+        mean = torch.zeros(T, 1, device=DEV, dtype=torch.float64) if rms else torch.stack([r.double().mean() for r in x])[:, None]
+        rstd = torch.stack([1 / (((r.double() - m) ** 2).mean() + 1e-6).sqrt() for r, m in zip(x, mean)])[:, None]
+        n, d = (x[:, cols].double() - mean) * rstd, dy[:, cols].double()
+        # n's own error (G U, G = 72 + D / 1024, of rows whose mean is small beside their size) and T additions
+        e = (72 + D / 1024) * U * (n.abs() + 1) * d.abs() + T * U * (n * d).abs()
+        inside(dw[cols], (n * d).sum(0), half(torch.bfloat16) * (n * d).sum(0).abs() + e.sum(0), ("dw", T))
+        if not rms:
+            inside(db[cols], d.sum(0), half(torch.bfloat16) * d.sum(0).abs() + T * U * d.abs().sum(0), ("db", T))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements per tensor: rows behind that are as the others."""
+    U_bf16 = half(torch.bfloat16)
+    banner("norm past 32 bits")
+    T, D = 1060000, 2048
+    x, dy = long(T, D, 1), long(T, D, 2)
+    w, b = normal(gen(3), (D,), torch.bfloat16), normal(gen(4), (D,), torch.bfloat16)
+    rows = [0, 1, T // 2 + 1, (1 << 31) // D - 1, (1 << 31) // D, T - 2, T - 1]
+    y, st = mlp.norm_fwd(x, w, b)
+    ref = norm_reference(x[rows], w, b, 1e-5, False, dy[rows])
+    inside(y[rows], *ref[0], "y")
+    del y
+    dx, dw, db = mlp.norm_bwd(dy, x, w, st, bias=True)
+    inside(dx[rows], *ref[1], "dx")
+    cols = torch.tensor([0, 1, 1000, D - 1], device=DEV)
+    d, n = dy[:, cols].double(), (x[:, cols].double() - st[0][:, None]) * st[1][:, None]
+    # 2 rows' sums at a time per workgroup, T / 512 of them, then 256 parts
+    C = T / 512 + 256 + 64
+    for got, v in ((dw, n * d), (db, d)):
+        want = v.sum(0)
+        inside(got[cols], want, U_bf16 * want.abs() + (C + 8) * U * v.abs().sum(0), "dw, db")
+    del x, dy, dx, st, d, n
+    banner("linear past 32 bits")
+    T, N, K = 264000, 8200, 72
+    x, w = long(T, K, 5), normal(gen(6), (N, K), torch.bfloat16, 0.2)
+    dy = long(T, N, 7)
+    bias = normal(gen(8), (N,), torch.bfloat16)
+    y, z = mlp.linear_fwd(x, w, bias, "silu", dy)
+    rows = [0, 255, 256, T // 2, (1 << 31) // N - 1, (1 << 31) // N, T - 300, T - 2, T - 1]
+    xr, wr = x[rows].double(), w.double()
+    zr = xr @ wr.mT.contiguous() + bias.double()
+    ez = (K / 4 + 64) * U * (xr.abs() @ wr.abs().mT.contiguous()) + 2 * U * zr.abs()
+    inside(z[rows], zr, U_bf16 * zr.abs() + ez, "z")
+    yr = act64(zr, "silu")[0]
+    inside(y[rows], yr + dy[rows].double(), U_bf16 * (yr + dy[rows].double()).abs() + 1.2 * ez + 2e-5 * yr.abs()
+           + 2 * U * (yr.abs() + dy[rows].double().abs()), "y")
+    del y
+    dx, dw, db = mlp.linear_bwd(dy, x, w, z, "silu")
+    dz = dy[rows].double() * act64(z[rows].double(), "silu")[1]
+    e = U_bf16 * dz.abs() + 3e-5 * dy[rows].double().abs()
+    inside(dx[rows], dz @ wr, U_bf16 * (dz @ wr).abs() + 1.01 * (e @ wr.abs() + (N / 4 + 64) * U * (dz.abs() @ wr.abs())), "dx")
+    cols = torch.tensor([0, 1, 4097, N - 1], device=DEV)
+    dz = dy[:, cols].double() * act64(z[:, cols].double(), "silu")[1]
+    e = U_bf16 * dz.abs() + 3e-5 * dy[:, cols].double().abs()
+    want, size = (dz.mT.contiguous() @ x.double()), (dz.abs().mT.contiguous() @ x.double().abs())
+    inside(dw[cols], want, U_bf16 * want.abs() + 1.01 * (e.mT.contiguous() @ x.double().abs() + (T / 4 + 64) * U * size), "dw")
+    want = dz.sum(0)
+    inside(db[cols], want, U_bf16 * want.abs() + ((T / 256 + 320) * U * dz.abs() + 3e-5 * dy[:, cols].double().abs()).sum(0), "db")
+
+
 @pytest.mark.gpu
 def test_strides_streams_and_leading_dimensions():
     banner("strides and streams")
