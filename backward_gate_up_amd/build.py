@@ -1,4 +1,5 @@
-"""Build the HIP library in-tree: backward_gate_up_amd/libswiglu_mlp.so (gfx950).
+"""Build the HIP library in-tree: backward_gate_up_amd/libswiglu_mlp.so (gfx950),
+and the autograd nodes in C++ that call it: backward_gate_up_amd/_nodes.so.
 
 The kernels are instantiated in eighteen translation units (csrc/instantiate.hip
 compiled once per dtype, entry point and weight layout), the few-token serving
@@ -6,6 +7,7 @@ kernels in nine more (csrc/few_instantiate.hip, once per dtype and weight
 format), the norms and the linear layer in sixteen (csrc/dense_instantiate.hip,
 once per dtype and part), plus the C ABI (csrc/swiglu_mlp.hip, csrc/few.hip,
 csrc/dense.hip); they compile in parallel and are linked into one shared library.
+The nodes (csrc/nodes.cpp, host code) are compiled against torch's headers.
 """
 
 import os
@@ -18,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libswiglu_mlp.so")
+NODES = os.path.join(HERE, "_nodes.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -46,39 +49,52 @@ UNITS = [("abi", "swiglu_mlp.hip", [])] + [
 ]
 
 
+def _node_commands(obj, tmp):
+    """Compiling and linking csrc/nodes.cpp."""
+    import sysconfig
+
+    from torch.utils import cpp_extension as ext
+
+    includes = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *ext.include_paths(),
+                os.path.join(os.path.dirname(HIPCC), os.pardir, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-DTORCH_EXTENSION_NAME=_nodes"]
+    compile_ += [f"-I{d}" for d in includes[:2]] + [a for d in includes[2:] for a in ("-isystem", d)]
+    compile_ += ["-c", "-o", obj, os.path.join(CSRC, "nodes.cpp")]
+    link = ["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-lswiglu_mlp", "-Wl,-rpath,$ORIGIN"]
+    link += [f"-L{d}" for d in ext.library_paths()] + ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    return compile_, link
+
+
 def _filter(text):
     return [ln for ln in text.splitlines() if "packed-fp32-ops' is not a recognized feature" not in ln]
 
 
 def build(verbose=False, jobs=None):
-    """Compile every unit and link the library (always). Raises on failure."""
+    """Compile every unit and link the libraries (always). Raises on failure."""
     jobs = jobs or max(1, min(len(UNITS), len(os.sched_getaffinity(0))))
     with tempfile.TemporaryDirectory(prefix="swiglu_build_") as tmpdir:
-        def compile_unit(u):
-            name, src, defs = u
-            obj = os.path.join(tmpdir, name + ".o")
-            cmd = [HIPCC] + FLAGS + defs + ["-c", "-o", obj, os.path.join(CSRC, src)]
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            return name, cmd, r, obj
-
+        nodes = os.path.join(tmpdir, "nodes.o")
+        compile_nodes, link_nodes = _node_commands(nodes, NODES + ".tmp")
+        objs = [os.path.join(tmpdir, name + ".o") for name, _, _ in UNITS]
+        work = [("nodes", compile_nodes)] + [
+            (name, [HIPCC] + FLAGS + defs + ["-c", "-o", obj, os.path.join(CSRC, src)])
+            for (name, src, defs), obj in zip(UNITS, objs)]
         with ThreadPoolExecutor(jobs) as ex:
-            results = list(ex.map(compile_unit, UNITS))
-        objs = []
-        for name, cmd, r, obj in results:
+            results = list(ex.map(lambda w: subprocess.run(w[1], capture_output=True, text=True), work))
+        for (name, cmd), r in zip(work, results):
             msgs = _filter(r.stdout + r.stderr)
             if verbose:
                 print(" ".join(cmd), flush=True)
                 if msgs:
                     print("\n".join(msgs))
             if r.returncode != 0:
-                raise RuntimeError(f"hipcc failed on {name}:\n" + "\n".join(msgs))
-            objs.append(obj)
-        tmp = OUT + ".tmp"
-        cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n" + "\n".join(_filter(r.stdout + r.stderr)))
-        os.replace(tmp, OUT)
+                raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {name}:\n" + "\n".join(msgs))
+        link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", OUT + ".tmp"] + objs
+        for cmd, tmp, out in ((link, OUT + ".tmp", OUT), (link_nodes, NODES + ".tmp", NODES)):
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError("link failed:\n" + "\n".join(_filter(r.stdout + r.stderr)))
+            os.replace(tmp, out)
     return OUT
 
 

@@ -9,11 +9,16 @@ behind the C ABI of include/swiglu_mlp.h; no fallback):
 
 with autograd: ``layer_norm``, ``rms_norm``, ``linear`` and, of all three, the
 ungated feed-forward layer x + fc2(act(fc1(norm(x)))): ``feed_forward`` and the
-module ``FeedForward``.
+module ``FeedForward``. Their nodes are in C++ (csrc/nodes.cpp), since small training
+steps are bound by host code; they call the same library.
 All tensors of a call share dtype (bf16, fp16 or fp32) and device.
 
 Second derivatives are refused. The backward may run more than once
 (``retain_graph``): it changes nothing that the forward kept.
+
+Calls can be captured in a graph, with their backward. As with torch's own
+operators, no autograd graph of the same leaves that was built outside the capture
+may be alive then: its accumulation nodes belong to the stream they were made on.
 """
 
 import functools
@@ -26,10 +31,17 @@ from .serve import _DT, _bytes, _check, _code, _on_gpu, _ptr, _stream, _workspac
 
 ACTIVATIONS = tuple(_L.ACTS)
 
-# A small training step is bound by the host: an autograd engine's thread runs the
-# backward on a core whose caches are cold, where every Python call counts double.
-# So arguments are checked once, in the forward; what the backward gets from
-# autograd (shape, dtype, device) the engine has checked.
+
+@functools.lru_cache(maxsize=None)
+def _nodes():
+    """The autograd nodes (csrc/nodes.cpp), which call the library."""
+    _L.lib()
+    try:
+        from . import _nodes as nodes
+    except ImportError as e:
+        raise ImportError("backward_gate_up_amd/_nodes.so is missing or does not load: build it with "
+                          "`python -m backward_gate_up_amd.build` (there is no fallback)") from e
+    return nodes
 
 
 @functools.lru_cache(maxsize=None)
@@ -72,17 +84,17 @@ def _opt(t):
 
 
 def _flat(t):
-    return t if t is None or t.is_contiguous() else t.contiguous()
+    """Contiguous, and without a negation that torch has put off."""
+    if t is None or (t.is_contiguous() and not t.is_neg()):
+        return t
+    return t.resolve_neg().contiguous()
 
 
 def _flat16(t):
-    """Contiguous and at an address that the matrix kernels take (a gradient may
+    """As ``_flat``, and at an address that the matrix kernels take (a gradient may
     be a view that starts anywhere)."""
-    if t is None:
-        return t
-    if not t.is_contiguous():
-        t = t.contiguous()
-    return t.clone() if t.data_ptr() & 15 else t
+    t = _flat(t)
+    return t.clone() if t is not None and t.data_ptr() & 15 else t
 
 
 # ---- norms ------------------------------------------------------------------
@@ -149,52 +161,16 @@ def norm_bwd(dy, x, weight, stats, rms=False, bias=False, dres=None, workspace=N
                _flat(dres), workspace)
 
 
-def _no_second():
-    if torch.is_grad_enabled():
-        raise RuntimeError("create_graph=True (double backward) is not supported")
-
-
-class NormFunction(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, bias, eps, rms):
-        dt, device = _norm_args(x, weight, bias, eps, rms)
-        x, weight = _flat(x), _flat(weight)
-        y, stats = _on(device, _norm_fwd, x, weight, _flat(bias), eps, rms, True, dt, device)
-        ctx.save_for_backward(x, weight, stats)
-        ctx.form = rms, bias is not None, dt, device
-        return y
-
-    @staticmethod
-    def backward(ctx, dy):
-        _no_second()
-        x, weight, stats = ctx.saved_tensors
-        dx, dw, db = _norm_bwd(_flat(dy), x, weight, stats, *ctx.form)
-        return dx, dw, db, None, None
-
-
-def _norm(x, weight, bias, eps, rms):
-    n = x.dim()
-    if n == 0:
-        raise ValueError("expected X[..., D]")
-    x2 = x if n == 2 else x.reshape(-1, x.shape[-1])
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
-        y = NormFunction.apply(x2, weight, bias, eps, rms)
-    else:
-        dt, device = _norm_args(x2, weight, bias, eps, rms)
-        y = _on(device, _norm_fwd, _flat(x2), _flat(weight), _flat(bias), eps, rms, False, dt, device)[0]
-    return y if n == 2 else y.reshape(x.shape)
-
-
 def layer_norm(x, weight, bias=None, eps=1e-5):
     """Layer norm over the last axis of x[..., D]: (x - mean) / sqrt(var + eps) *
     weight + bias."""
-    return _norm(x, weight, bias, eps, False)
+    return _nodes().norm(x, weight, bias, eps, False)
 
 
 def rms_norm(x, weight, eps=1e-6):
     """RMS norm over the last axis of x[..., D]: x / sqrt(mean(x^2) + eps) *
     weight."""
-    return _norm(x, weight, None, eps, True)
+    return _nodes().norm(x, weight, None, eps, True)
 
 
 # ---- linear layer -------------------------------------------------------------
@@ -266,86 +242,15 @@ def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), work
     return _on(device, _linear_bwd, _flat16(dy), _flat16(x), _flat16(w), _flat16(z), act, needs, dt, device, workspace)
 
 
-class LinearFunction(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w, bias, residual, activation):
-        act = _act(activation)
-        dt, device = _linear_args(x, w, bias, residual)
-        x, w = _flat16(x), _flat16(w)
-        y, z = _on(device, _linear_fwd, x, w, _flat16(bias), act, _flat16(residual), True, dt, device)
-        ctx.save_for_backward(x, w, z)
-        ctx.form = act, dt, device
-        return y
-
-    @staticmethod
-    def backward(ctx, dy):
-        _no_second()
-        x, w, z = ctx.saved_tensors
-        act, dt, device = ctx.form
-        needs = ctx.needs_input_grad
-        dx = dw = db = None
-        if needs[0] or needs[1] or needs[2]:
-            dx, dw, db = _linear_bwd(_flat16(dy), x, w, z, act, needs, dt, device)
-        return dx, dw, db, dy if needs[3] else None, None
-
-
 def linear(x, w, bias=None, activation=None, residual=None):
     """Y = act(x W^T + bias) + residual for x[..., K]: the product with bias,
     activation and residual in its epilogue. w[N, K] (nn.Linear layout), bias[N],
     residual[..., N] or None; ``activation`` None, "relu", "gelu", "gelu_tanh"
     or "silu"."""
-    if x.dim() == 0 or w.dim() != 2:
-        raise ValueError("expected X[..., K] and W[N, K]")
-    shape = (*x.shape[:-1], w.shape[0])
-    if residual is not None and residual.shape != shape:
-        raise ValueError(f"residual must be {list(shape)}: {tuple(residual.shape)}")
-    if len(shape) != 2:
-        x = x.reshape(-1, x.shape[-1])
-        residual = None if residual is None else residual.reshape(-1, shape[-1])
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)
-                                    or (residual is not None and residual.requires_grad)):
-        y = LinearFunction.apply(x, w, bias, residual, activation)
-    else:
-        act = _act(activation)
-        dt, device = _linear_args(x, w, bias, residual)
-        y = _on(device, _linear_fwd, _flat16(x), _flat16(w), _flat16(bias), act, _flat16(residual), False, dt, device)[0]
-    return y if len(shape) == 2 else y.reshape(shape)
+    return _nodes().linear(x, w, bias, residual, _act(activation))
 
 
 # ---- the layer of them ----------------------------------------------------------
-
-
-class FeedForwardFunction(torch.autograd.Function):
-    """The layer as one node: its backward hands the stream's gradient to the norm's
-    backward, which adds it to its own, instead of leaving a sum of two tensors."""
-
-    @staticmethod
-    def forward(ctx, x, nw, nb, w1, b1, w2, b2, activation, eps, rms):
-        x, nw, w1, w2 = _flat16(x), _flat(nw), _flat16(w1), _flat16(w2)
-        n, stats = norm_fwd(x, nw, nb, eps, rms)
-        a, z = linear_fwd(n, w1, b1, activation)
-        y = linear_fwd(a, w2, b2, None, x)[0]
-        ctx.save_for_backward(x, nw, w1, w2, n, stats, a, z)
-        ctx.form = _L.ACTS[activation], rms, nb is not None, _DT[x.dtype], x.device
-        return y
-
-    @staticmethod
-    def backward(ctx, dy):
-        _no_second()
-        x, nw, w1, w2, n, stats, a, z = ctx.saved_tensors
-        act, rms, norm_bias, dt, device = ctx.form
-        need = ctx.needs_input_grad
-        dy = _flat16(dy)
-        norm = need[0] or need[1] or need[2]
-        inner = norm or need[3] or need[4]
-        da, dw2, db2 = _linear_bwd(dy, a, w2, None, 0, (inner, need[5], need[6]), dt, device)
-        dx = dnw = dnb = dw1 = db1 = None
-        if inner:
-            dn, dw1, db1 = _linear_bwd(da, n, w1, z, act, (norm, need[3], need[4]), dt, device)
-            del da
-            if norm:
-                dx, dnw, dnb = _norm_bwd(dn, x, nw, stats, rms, norm_bias, dt, device, dy)
-        return dx, dnw, dnb, dw1, db1, dw2, db2, None, None, None
 
 
 def feed_forward(x, norm_weight, norm_bias, w1, b1, w2, b2, activation="gelu", eps=1e-5, rms=False):
@@ -353,19 +258,10 @@ def feed_forward(x, norm_weight, norm_bias, w1, b1, w2, b2, activation="gelu", e
     layer with its norm in front and the stream added. norm_weight[D], w1[H, D],
     w2[D, H]; norm_bias, b1 and b2 or None; ``activation`` as in ``linear``; with
     ``rms`` an RMS norm (no norm_bias)."""
-    if x.dim() == 0:
-        raise ValueError("expected X[..., D]")
-    if not activation:
+    act = _act(activation)
+    if not act:
         raise ValueError(f"a feed-forward layer needs an activation: one of {ACTIVATIONS[1:]}")
-    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (x, norm_weight, norm_bias, w1, b1, w2, b2)):
-        y = FeedForwardFunction.apply(x2, norm_weight, norm_bias, w1, b1, w2, b2, activation, eps, rms)
-    else:
-        n = norm_fwd(x2, norm_weight, norm_bias, eps, rms, False)[0]
-        a = linear_fwd(n, w1, b1, activation, None, False)[0]
-        y = linear_fwd(a, w2, b2, None, x2, False)[0]
-    return y if x.dim() == 2 else y.reshape(x.shape)
+    return _nodes().feed_forward(x, norm_weight, norm_bias, w1, b1, w2, b2, act, eps, rms)
 
 
 _CONFIG_ACTS = {"relu": "relu", "gelu": "gelu", "gelu_new": "gelu_tanh", "gelu_pytorch_tanh": "gelu_tanh",

@@ -793,6 +793,86 @@ def test_feed_forward_is_its_operators():
 
 
 @pytest.mark.gpu
+def test_gradients_without_some_inputs():
+    """Inputs that are absent shift no other input's gradient, wanted or not."""
+    banner("absent inputs")
+    dt = torch.bfloat16
+    sh = {"x": (90, 136), "nw": (136,), "nb": (136,), "w1": (264, 136), "b1": (264,), "w2": (136, 264), "b2": (136,)}
+    t = {k: normal(gen(i), s, dt, 0.1 if k[0] == "w" else 1.0) for i, (k, s) in enumerate(sh.items())}
+    dy = normal(gen(50), (90, 136), dt)
+    zero = lambda k: torch.zeros_like(t[k])  # noqa: E731
+    for absent in (("nb",), ("b1",), ("nb", "b2"), ("nb", "b1", "b2")):
+        full = {k: (zero(k) if k in absent else v).clone().requires_grad_() for k, v in t.items()}
+        want = dict(zip(sh, torch.autograd.grad(mlp.feed_forward(*full.values(), activation="gelu"), list(full.values()), dy)))
+        for wanted in ([k for k in sh if k not in absent], ["w2"], ["w1", "x"], ["nw"]):
+            leaves = {k: None if k in absent else v.clone().requires_grad_(k in wanted) for k, v in t.items()}
+            out = mlp.feed_forward(*leaves.values(), activation="gelu")
+            for k, g in zip(wanted, torch.autograd.grad(out, [leaves[k] for k in wanted], dy)):
+                assert torch.equal(g, want[k]), (absent, wanted, k)
+    x, w, b, r = t["x"], t["w1"], t["b1"], normal(gen(51), (90, 264), dt)
+    dz = normal(gen(52), (90, 264), dt)
+    for act in (None, "silu"):
+        z = mlp.linear_fwd(x, w, None, act, r)[1]
+        want = dict(zip("xwb", mlp.linear_bwd(dz, x, w, z, act)), r=dz)
+        for wanted in ("xwr", "r", "wr", "x"):
+            leaves = {k: v.clone().requires_grad_(k in wanted) for k, v in zip("xwr", (x, w, r))}
+            out = mlp.linear(leaves["x"], leaves["w"], None, act, leaves["r"])
+            for k, g in zip(wanted, torch.autograd.grad(out, [leaves[k] for k in wanted], dz)):
+                assert torch.equal(g, want[k]), (act, wanted, k)
+        z = mlp.linear_fwd(x, w, b, act)[1]
+        gb, = torch.autograd.grad(mlp.linear(x, w, b.requires_grad_(), act), b, dz)
+        assert torch.equal(gb, mlp.linear_bwd(dz, x, w, z, act)[2])
+        b = b.detach()
+
+
+@pytest.mark.gpu
+def test_views_with_a_negation_put_off():
+    banner("negations")
+    c = torch.randn(20, 64, dtype=torch.complex64, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    x, w = c.conj().imag, normal(gen(2), (72, 64), torch.float32)
+    assert x.is_neg()
+    plain = (-c.imag).contiguous()
+    assert torch.equal(mlp.linear(x, w, None, "gelu"), mlp.linear(plain, w, None, "gelu"))
+    assert torch.equal(mlp.linear_fwd(x, w)[0], mlp.linear_fwd(plain, w)[0])
+    assert torch.equal(mlp.layer_norm(x, w[0], x[1]), mlp.layer_norm(plain, w[0], plain[1]))
+    assert torch.equal(mlp.norm_fwd(x, w[0], x[1])[0], mlp.norm_fwd(plain, w[0], plain[1])[0])
+
+
+@pytest.mark.gpu
+def test_backward_from_two_threads():
+    """Nodes built on one stream and run backward from two threads at once give
+    what one call gives."""
+    banner("threads")
+    import threading
+
+    dt = torch.bfloat16
+    x, w, b = (normal(gen(i), s, dt) for i, s in enumerate(((90, 136), (264, 136), (264,))))
+    dy = normal(gen(9), (90, 264), dt)
+
+    def one():
+        xs, ws, bs = (t.clone().requires_grad_() for t in (x, w, b))
+        n = mlp.rms_norm(xs, torch.ones_like(x[0]))
+        return torch.autograd.grad(mlp.linear(n, ws, bs, "gelu"), (xs, ws, bs), dy)
+
+    want, got = one(), {}
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = one()
+            torch.cuda.current_stream().synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert all(torch.equal(a, c) for a, c in zip(got[i], want))
+
+
+@pytest.mark.gpu
 def test_gradients_that_start_anywhere():
     """Views at odd addresses: of inputs, and as the gradient that a flattened
     concatenation hands back."""
