@@ -247,6 +247,24 @@ bool wants_grad(std::initializer_list<const Tensor*> ts) {
     if (t && t->requires_grad()) return true;
   return false;
 }
+// A leaf's accumulation node belongs to the stream it was made on and lives as long as a
+// graph that uses it. Where that is the default stream, a captured backward would
+// make the default stream wait for the capture, which is an error that ends the
+// capture in the engine's threads: refused here instead.
+void check_capture(std::initializer_list<const Tensor*> ts) {
+  const Tensor& x = **ts.begin();
+  hipStream_t s = stream(x);
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  if (!s || hipStreamIsCapturing(s, &status) != hipSuccess || status == hipStreamCaptureStatusNone) return;
+  for (const Tensor* t : ts) {
+    if (!t || !t->requires_grad() || !t->is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+    const auto made_on = node ? node->stream() : std::nullopt;
+    TORCH_CHECK(!made_on || made_on->id() != 0,
+                "an autograd graph of the same leaves, built on the default stream, is alive: its accumulation would leave "
+                "this capture; delete it (its loss and outputs) or build it on a side stream");
+  }
+}
 // x [..., D] as rows
 Tensor rows(const Tensor& x) {
   if (x.dim() == 2) return x;
@@ -259,6 +277,7 @@ Tensor norm(const Tensor& x_, const Tensor& w, const Maybe& b, double eps, bool 
   norm_args(x, w, b, eps, rms);
   Tensor y;
   if (wants_grad({&x, &w, opt(b)})) {
+    check_capture({&x_, &w, opt(b)});
     y = Norm::apply(x, w, b, eps, rms);
   } else {
     const at::DeviceGuard guard(x.device());
@@ -277,6 +296,7 @@ Tensor linear(const Tensor& x_, const Tensor& w, const Maybe& b, const Maybe& r_
   linear_args(x, w, b, r);
   Tensor y;
   if (wants_grad({&x, &w, opt(b), opt(r)})) {
+    check_capture({&x_, &w, opt(b), opt(r_)});
     y = Linear::apply(x, w, b, r, act);
   } else {
     const at::DeviceGuard guard(x.device());
@@ -296,6 +316,7 @@ Tensor feed_forward(const Tensor& x_, const Tensor& nw, const Maybe& nb, const T
   same(x, {&w2, opt(b2)});
   Tensor y;
   if (wants_grad({&x, &nw, opt(nb), &w1, opt(b1), &w2, opt(b2)})) {
+    check_capture({&x_, &nw, opt(nb), &w1, opt(b1), &w2, opt(b2)});
     y = FeedForward::apply(x, nw, nb, w1, b1, w2, b2, act, eps, rms);
   } else {
     const at::DeviceGuard guard(x.device());

@@ -16,9 +16,9 @@ All tensors of a call share dtype (bf16, fp16 or fp32) and device.
 Second derivatives are refused. The backward may run more than once
 (``retain_graph``): it changes nothing that the forward kept.
 
-Calls can be captured in a graph, with their backward. As with torch's own
-operators, no autograd graph of the same leaves that was built outside the capture
-may be alive then: its accumulation nodes belong to the stream they were made on.
+Calls can be captured in a graph, with their backward. While an autograd graph of
+the same leaves that was built on the default stream is alive, a captured call that
+needs gradients is refused: the leaves' accumulation would leave the capture.
 """
 
 import functools

@@ -924,6 +924,47 @@ def test_training_step_in_a_graph():
             assert all(torch.equal(a, c) for a, c in zip(out, want)), (T, i)
 
 
+@pytest.mark.gpu
+def test_capture_beside_a_live_eager_graph_is_refused():
+    """A graph of the same leaves on the default stream keeps their accumulation
+    nodes there; the captured forward says so. Without it the capture goes through."""
+    banner("capture beside an eager graph")
+    x, w = normal(gen(1), (5, 64), torch.bfloat16), normal(gen(2), (72, 64), torch.bfloat16).requires_grad_()
+    n = normal(gen(3), (64,), torch.bfloat16).requires_grad_()
+    dy = normal(gen(4), (5, 72), torch.bfloat16)
+    step = lambda: mlp.linear(mlp.rms_norm(x, n), w, None, "gelu")  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(step(), (n, w), dy)
+    torch.cuda.current_stream().wait_stream(side)
+    for alive in (lambda: mlp.linear(x, w), lambda: x * n):
+        eager = alive()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="is alive"):
+            with torch.cuda.graph(graph):
+                dy + 0  # a graph of nothing would warn
+                step()
+        del eager, graph
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step()
+        grads = torch.autograd.grad(y, (n, w), dy)
+    y = y.detach()
+    for i in range(3):
+        x.copy_(normal(gen(10 + i), (5, 64), torch.bfloat16))
+        with torch.no_grad():
+            want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    m, v = n.detach().requires_grad_(), w.detach().requires_grad_()
+    again = torch.autograd.grad(mlp.linear(mlp.rms_norm(x, m), v, None, "gelu"), (m, v), dy)
+    assert all(torch.equal(a, c) for a, c in zip(grads, again))
+
+
 # ---- refusals (CPU) ------------------------------------------------------------------
 
 
