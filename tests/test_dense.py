@@ -826,6 +826,44 @@ def test_gradients_without_some_inputs():
 
 
 @pytest.mark.gpu
+def test_nodes_under_checkpoints_hooks_and_without_tokens():
+    """The nodes keep what they need through autograd's own means: recomputed,
+    moved to the host and back, for no tokens at all, after an in-place change."""
+    banner("checkpoints")
+    from torch.utils.checkpoint import checkpoint
+
+    dt = torch.bfloat16
+    block = mlp.FeedForward(Config(hidden_size=136, intermediate_size=264)).to(DEV, dt)
+    x, dy = normal(gen(1), (3, 30, 136), dt).requires_grad_(), normal(gen(2), (3, 30, 136), dt)
+    leaves = [x, *block.parameters()]
+
+    def both(t):
+        return mlp.linear(mlp.layer_norm(block(t), block.norm.weight, block.norm.bias), block.fc1.weight, None, "silu")
+
+    dz = normal(gen(3), (3, 30, 264), dt)
+    want = torch.autograd.grad(both(x), leaves, dz, allow_unused=True)
+    for reentrant in (False, True):
+        for p in leaves:
+            p.grad = None
+        checkpoint(both, x, use_reentrant=reentrant).backward(dz)
+        assert all(torch.equal(p.grad, g) for p, g in zip(leaves, want) if g is not None)
+    with torch.autograd.graph.save_on_cpu():
+        y = both(x)
+    got = torch.autograd.grad(y, leaves, dz, allow_unused=True)
+    assert all(torch.equal(a, c) for a, c in zip(got, want) if c is not None)
+    none = torch.zeros(0, 7, 136, dtype=dt, device=DEV, requires_grad=True)
+    y = both(none)
+    assert y.shape == (0, 7, 264)
+    grads = torch.autograd.grad(y, [none, *leaves[1:]], torch.zeros_like(y), allow_unused=True)
+    assert grads[0].shape == none.shape and all((g == 0).all() for g in grads if g is not None)
+    y = block(x)
+    with torch.no_grad():
+        block.fc2.weight.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(y, x, dy)
+
+
+@pytest.mark.gpu
 def test_views_with_a_negation_put_off():
     banner("negations")
     c = torch.randn(20, 64, dtype=torch.complex64, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
