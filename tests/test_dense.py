@@ -690,6 +690,33 @@ def test_autograd_matches_the_operators():
 
 
 @pytest.mark.gpu
+def test_refusals_on_a_gpu():
+    """What the library refuses comes back as the package's exception, also where
+    gradients are wanted; nothing is launched for mixed types or devices."""
+    x, w = torch.zeros(4, 60, device=DEV), torch.zeros(32, 60, device=DEV)
+    for grad in (False, True):
+        w.requires_grad_(grad)
+        with pytest.raises(mlp.SwiGLUError) as e:
+            mlp.linear(x, w)
+        assert _lib.STATUS[e.value.status] == "SWIGLU_ERR_SHAPE"
+        with pytest.raises(mlp.SwiGLUError) as e:
+            mlp.feed_forward(x, x[0], None, w, None, w.mT)
+        assert _lib.STATUS[e.value.status] == "SWIGLU_ERR_SHAPE"
+        with pytest.raises(ValueError, match="share dtype and device"):
+            mlp.linear(x, w.bfloat16())
+        with pytest.raises(ValueError, match="share dtype and device"):
+            mlp.layer_norm(x, w[0].cpu())
+        with pytest.raises(TypeError, match="unsupported dtype"):
+            mlp.linear(x.double(), w.double())
+        with pytest.raises(ValueError, match="bias must be"):
+            mlp.linear(x, w, x[0])
+        with pytest.raises(ValueError, match="residual must be"):
+            mlp.linear(x, w, None, None, x)
+        with pytest.raises(ValueError, match="a number from 0 up"):
+            mlp.rms_norm(x, x[0], eps=math.nan)
+
+
+@pytest.mark.gpu
 def test_graph_replays():
     """Operators captured and replayed between eager work on other values."""
     banner("graph")
