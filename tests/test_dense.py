@@ -700,7 +700,7 @@ def test_refusals_on_a_gpu():
             mlp.linear(x, w)
         assert _lib.STATUS[e.value.status] == "SWIGLU_ERR_SHAPE"
         with pytest.raises(mlp.SwiGLUError) as e:
-            mlp.feed_forward(x, x[0], None, w, None, w.mT)
+            mlp.feed_forward(x, x[0], None, w, None, w.mT, None)
         assert _lib.STATUS[e.value.status] == "SWIGLU_ERR_SHAPE"
         with pytest.raises(ValueError, match="share dtype and device"):
             mlp.linear(x, w.bfloat16())
