@@ -318,8 +318,10 @@ static inline int few_splits(int64_t T, int64_t N, int64_t K, size_t e) {
 // `most`) take fix r + K max(lat, thr r), parts of K a launch and a pass over them
 // more. The figures were fitted to the times of 7 thousand products of random
 // sizes (65 to 16384 by 256 to 11008, all three layouts), each on several tiles in 1
-// to 16 parts, and are 9 % off in the mean; what is chosen takes 1.2 % longer than
-// the best of what was timed, over two thousand others. fp32 has only 64 x 64: wider ones were behind at every
+// to 16 parts. With the tiles' loads two stages ahead they are 5 to 15 % long for
+// them, which changes no choice by much: what is chosen takes 1.5 % longer than the
+// best of what was timed, over nine thousand others, and with figures fitted again 0.3 % less.
+// fp32 has only 64 x 64: wider ones were behind at every
 // size but the largest, by 3 % there (M = N = 2000, K = 8000 503 against 487 us).
 // What the choice is worth (us, unsplit 64 x 64 / 128 x 128 / best split; bf16): 256
 // x 1024, K = 8192 62 / 88 / 17.5; 4096 x 2048, K = 5632 154 / 105 / 97 (ring); 4096
@@ -399,7 +401,9 @@ static Grads plan_grads(int64_t T, int64_t N, int64_t K, size_t e, bool dw, bool
   if (dw) g.w = plan_product(N, K, T, e);
   if (dx) g.x = plan_product(T, K, N, e);
   if (!dw || !dx || T == 0) return g;
-  double best = g.w.us + g.x.us + 4.7;  // (a launch)
+  // (a launch; fp32 always both in one, 1.5 % shorter over 160 sizes, 15 % at best and 3 %
+  // longer at worst, where the model's choice left half of that)
+  double best = e == 4 ? 1e30 : g.w.us + g.x.us + 4.7;
   const int ncu = dev_ncu();
   {
     // 64 x 64 tiles together, whole or in as many parts as give two per CU
@@ -512,8 +516,8 @@ static inline BwdPlan bwd_plan(int64_t T, int64_t N, int64_t K, size_t e, bool a
 
 // ---- launches ------------------------------------------------------------------------
 // A product on register-staged tiles: LINEAR's epilogue, or its parts. fp32, T = 1000, N
-// = 2816, K = 1024, gelu: 65 us, 89 TFLOP/s on 2.75 tiles per CU; 1024 x 4096 x 4096
-// 259 us, 132 (the library's 8192^3 152). fp16, T = 300, N = 712, K = 1000 12 us: latency.
+// = 2816, K = 1024, gelu: 62 us, 92 TFLOP/s on 2.75 tiles per CU; 1024 x 4096 x 4096
+// 249 us, 138 (the library's 8192^3 152). fp16, T = 300, N = 712, K = 1000 11 us: latency.
 template <class E, int BM, int BN, int AL, int BL, int STAGE>
 __global__ void __launch_bounds__(256, (BM == 64 && BN == 64 ? 3 : 2)) lin_tile(const KArgs g) {
   __shared__ __attribute__((aligned(16))) char smem[Geometry<E, BM, BN, AL, BL>::LDS];
