@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(256, 3) lin_tile_grads(const KArgs w, const KA
 }
 
 // The ring, whole tiles with the epilogue. T = 16384, N = 11008, K = 4096, bf16, gelu
-// with z kept: 1151 us, 1283 TFLOP/s (dW 1084 and dx 953 us, 1363 and 1551; a plain
+// with z kept: 1164 us, 1270 TFLOP/s (dW 1090 and dx 955 us, 1356 and 1547; a plain
 // 8192^3 product of the library 1365).
 template <class E, int ACT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) lin_ring(const KArgs g) {
