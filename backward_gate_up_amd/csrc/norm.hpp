@@ -12,6 +12,14 @@
 // variance is that of the differences from the mean and not a difference of two
 // large sums. All sums are fp32.
 //
+// The mean is formed twice: the row's sum times 1 / D is off by the sum's roundings
+// and by that of 1 / D, an error of |mean| and not of the spread, which rstd
+// multiplies by up to 1 / sqrt(eps) (a constant row of 1000 with D = 1000 gave n =
+// -0.019). The pass that sums the squares of x - mean also sums x - mean itself;
+// its mean is what the first was off by, and its square comes off the variance. So a
+// constant row's mean is exact, and any row's off by its own rounding and by roundings
+// of the spread.
+//
 // Split: W waves hold a row, NC pieces of 16 bytes per lane: one wave up to 4
 // KiB, four up to 16 KiB, sixteen up to 32 KiB; wider rows are walked three times
 // (they come from L2 after the first). A group of waves walks rows with the
@@ -114,25 +122,57 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// v plus that of the lane N further on in the same row of sixteen (DPP row_ror)
+template <int N>
+__device__ __forceinline__ float turn_add(float v) {
+  const int u = __builtin_bit_cast(int, v);
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, 0x120 + N, 0xf, 0xf, false));
+}
+// Of two values in as many exchanges: the first's sum in lanes 0..31, the second's in
+// lanes 32..63, each added in wave_sum's order. (Forward of 4096 x 11008
+// bf16: 53 us without the mean's correction, 60 with it as two sums, 56 so.)
+__device__ __forceinline__ float wave_sum_halves(float a, float b) {
+  const bool low = (threadIdx.x & 32) == 0;
+  float v = (low ? a : b) + __shfl_xor(low ? b : a, 32);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
 // Sums of K values over the W waves that hold a row; `at` alternates between
 // two places in LDS, so that one barrier per sum is enough (a wave that writes a
 // place again has passed the barrier after every wave's reads of it).
 template <int W, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float (&red)[2][K][16], int& at) {
+  static_assert(K == 1 || K == 2, "one or two sums");
+  float part;
+  if constexpr (K == 1) part = wave_sum(v[0]);
+  else part = wave_sum_halves(v[0], v[1]);
+  if constexpr (W == 1) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
-  if constexpr (W > 1) {
+    for (int k = 0; k < K; ++k) v[k] = lane_of(part, 32 * k);
+  } else {
     const int wave = (threadIdx.x >> 6) % W;
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) red[at][k][wave] = v[k];
-    }
+    if ((threadIdx.x & (K == 1 ? 63 : 31)) == 0) red[at][K == 1 ? 0 : threadIdx.x >> 5 & 1][wave] = part;
     __syncthreads();
+    if constexpr (K == 2 && W == 16) {
+      // a wave's value per lane, added by turning rows of sixteen lanes
+      float r = red[at][threadIdx.x >> 4 & 1][threadIdx.x & 15];
+      r = turn_add<8>(r);
+      r = turn_add<4>(r);
+      r = turn_add<2>(r);
+      r = turn_add<1>(r);
+      v[0] = lane_of(r, 0);
+      v[1] = lane_of(r, 16);
+    } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      v[k] = 0.f;
+      for (int k = 0; k < K; ++k) {
+        v[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) v[k] += red[at][k][w];
+        for (int w = 0; w < W; ++w) v[k] += red[at][k][w];
+      }
     }
     at ^= 1;
   }
@@ -140,6 +180,28 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (&red)[2][K][16], i
 
 // 1 / sqrt in IEEE steps: the row's only one.
 __device__ __forceinline__ float inv_sqrt(float v) { return 1.0f / sqrtf(v); }
+
+// The variance plus eps from q[0], the sum of the squares of x - mean, and (layer
+// norm) the corrected mean from q[1], the sum of x - mean. The multiply and add of
+// the correction's square is one rounding, so an infinite sum of squares stays one;
+// a NaN passes the comparison.
+template <bool RMS>
+__device__ __forceinline__ float spread(const float (&q)[RMS ? 1 : 2], float inv_d, float eps, float& mean) {
+  if constexpr (RMS) {
+    return fmaf(q[0], inv_d, eps);
+  } else {
+    const float shift = q[1] * inv_d, var = fmaf(-shift, shift, q[0] * inv_d);
+    mean += shift;
+    return (var < 0.f ? 0.f : var) + eps;
+  }
+}
+
+// s / D: the product with 1 / D and what it leaves of s, so that a gradient that is the
+// same everywhere has its own mean (a division's steps cost the backward 1 %).
+__device__ __forceinline__ float mean_of(float s, const Args& g) {
+  const float m = s * g.inv_d;
+  return fmaf(fmaf(-m, (float)g.D, s), g.inv_d, m);
+}
 
 // Rows of a workgroup: one wave each for W = 1, else one for all.
 template <int W>
@@ -156,8 +218,8 @@ constexpr bool kAhead = W < 16;
 template <class E, bool RMS, int W, int NC, bool EVEN>
 __global__ void __launch_bounds__(kThreads<W>) norm_fwd(const Args g) {
   using P = Piece<E>;
-  constexpr int V = P::V;
-  __shared__ float red[2][1][16];
+  constexpr int V = P::V, K = RMS ? 1 : 2;
+  __shared__ float red[2][1][16], red_q[2][K][16];
   const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x, wave = threadIdx.x >> 6;
   const int64_t rowb = (int64_t)g.D * E::kBytes, step = (int64_t)gridDim.x * kRows<W>;
   int64_t t = (int64_t)blockIdx.x * kRows<W> + (W == 1 ? wave : 0);
@@ -193,18 +255,21 @@ __global__ void __launch_bounds__(kThreads<W>) norm_fwd(const Args g) {
       row_sum<W, 1>(s, red, at);
       mean = s[0] * g.inv_d;
     }
-    float q[1] = {};
+    float q[K] = {};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (where[c] >= g.D) continue;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float d = x[c].get(i) - mean;
-        if (EVEN || where[c] + i < g.D) q[0] = fmaf(d, d, q[0]);
+        if (EVEN || where[c] + i < g.D) {
+          q[0] = fmaf(d, d, q[0]);
+          if constexpr (!RMS) q[K - 1] += d;
+        }
       }
     }
-    row_sum<W, 1>(q, red, at);
-    const float rstd = inv_sqrt(fmaf(q[0], g.inv_d, g.eps));
+    row_sum<W, K>(q, red_q, at);
+    const float rstd = inv_sqrt(spread<RMS>(q, g.inv_d, g.eps, mean));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (where[c] >= g.D) continue;
@@ -240,8 +305,8 @@ __global__ void __launch_bounds__(kThreads<W>) norm_fwd(const Args g) {
 template <class E, bool RMS>
 __global__ void __launch_bounds__(1024) norm_fwd_wide(const Args g) {
   using P = Piece<E>;
-  constexpr int V = P::V;
-  __shared__ float red[2][1][16];
+  constexpr int V = P::V, K = RMS ? 1 : 2;
+  __shared__ float red[2][1][16], red_q[2][K][16];
   const int64_t rowb = (int64_t)g.D * E::kBytes;
   int at = 0;
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
@@ -258,18 +323,21 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide(const Args g) {
       row_sum<16, 1>(s, red, at);
       mean = s[0] * g.inv_d;
     }
-    float q[1] = {};
+    float q[K] = {};
     for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
       P x;
       x.load(row, d, g.D);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float v = x.get(i) - mean;
-        if (d + i < g.D) q[0] = fmaf(v, v, q[0]);
+        if (d + i < g.D) {
+          q[0] = fmaf(v, v, q[0]);
+          if constexpr (!RMS) q[K - 1] += v;
+        }
       }
     }
-    row_sum<16, 1>(q, red, at);
-    const float rstd = inv_sqrt(fmaf(q[0], g.inv_d, g.eps));
+    row_sum<16, K>(q, red_q, at);
+    const float rstd = inv_sqrt(spread<RMS>(q, g.inv_d, g.eps, mean));
     for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
       P x, w, b, y;
       x.load(row, d, g.D);
@@ -369,7 +437,7 @@ __global__ void __launch_bounds__((64 * W * kBwdRows<W, NC>)) norm_bwd(const Arg
     }
     row_sum<W, K>(s, red[group], at);
     if (t < g.T) {
-      const float along = s[0] * g.inv_d, level = RMS ? 0.f : s[K - 1] * g.inv_d;
+      const float along = s[0] * g.inv_d, level = RMS ? 0.f : mean_of(s[K - 1], g);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         if (where[c] >= g.D) continue;
@@ -455,7 +523,7 @@ __device__ __forceinline__ void bwd_row(const Args& g, int64_t t, float (&red)[2
     }
   }
   row_sum<16, K>(s, red, at);
-  const float along = s[0] * g.inv_d, level = RMS ? 0.f : s[K - 1] * g.inv_d;
+  const float along = s[0] * g.inv_d, level = RMS ? 0.f : mean_of(s[K - 1], g);
   for (int d = threadIdx.x * V; d < g.D; d += 1024 * V) {
     P x, dy, w, r, dx;
     x.load(g.x + t * rowb, d, g.D);

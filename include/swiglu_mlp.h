@@ -317,7 +317,8 @@ int swiglu_mlp_w4_infer(const void* X, const swiglu_w4_t* Wg, const swiglu_w4_t*
  * Norms over the last axis of X [T, D] (rms = 0: layer norm, 1: RMS norm):
  *   n = (x - mean) rstd, y = n weight + bias, rstd = 1 / sqrt(mean((x - mean)^2) + eps)
  * and for RMS norm the same with mean = 0 and no bias. Sums are fp32, the
- * variance that of the differences from the mean; squares past fp32's range
+ * variance that of the differences from the mean, the mean corrected by theirs
+ * (a row of one number has it as its mean); squares past fp32's range
  * are infinities. Any D from 1 to SWIGLU_NORM_MAX_D; pointers need the alignment
  * of an element only (workspace: 16 bytes). stats, [2][T] (mean, rstd; RMS
  * norm [T], rstd) in fp32, is what the backward needs; NULL without one.
