@@ -31,6 +31,16 @@ class W4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("experts", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("group", ctypes.c_int32), ("has_zeros", ctypes.c_int32)]
 
+
+class LinearPlan(ctypes.Structure):
+    """swiglu_linear_plan_t."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("fwd_engine", "fwd_parts", "dw_engine", "dw_parts", "dx_engine", "dx_parts",
+                                              "together")]
+
+
+ENGINES = ("stream", "64x64", "64x128", "128x128", "ring")
+
 _lib = None
 
 
@@ -97,7 +107,8 @@ def lib():
             ("linear_workspace_bytes", [i64] * 3 + [i32], sz),
             ("linear_fwd", [vp] * 7 + [sz] + [i64] * 3 + [i32, i32, vp], i32),
             ("linear_bwd_workspace_bytes", [i64] * 3 + [i32, i32], sz),
-            ("linear_bwd", [vp] * 8 + [sz] + [i64] * 3 + [i32, i32, vp], i32)):
+            ("linear_bwd", [vp] * 8 + [sz] + [i64] * 3 + [i32, i32, vp], i32),
+            ("linear_plan", [i64] * 3 + [i32] * 3 + [ctypes.POINTER(LinearPlan)], i32)):
         f = getattr(L, "swiglu_mlp_" + name)
         f.argtypes, f.restype = args, res
     L.swiglu_mlp_status_string.argtypes = [i32]

@@ -183,4 +183,25 @@ int swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W, const vo
   }
 }
 
+int swiglu_mlp_linear_plan(int64_t T, int64_t N, int64_t K, int dtype, int dw, int dx, swiglu_linear_plan_t* plan) {
+  const size_t e = elt_bytes(dtype);
+  if (!e) return SWIGLU_ERR_DTYPE;
+  if (!plan) return SWIGLU_ERR_NULL;
+  const int rc = check_shape(T, N, K, e);
+  if (rc) return rc;
+  *plan = swiglu_linear_plan_t{};
+  if (!dw && !dx) {
+    const bool few = T <= lin::kFewT;
+    const lin::Product p = few ? lin::Product{} : lin::fwd_plan(T, N, K, e);
+    plan->fwd_engine = few ? 0 : 1 + p.tile;
+    plan->fwd_parts = few ? lin::few_splits(T, N, K, e) : p.splits;
+    return SWIGLU_OK;
+  }
+  const lin::Grads g = lin::bwd_plan(T, N, K, e, true).grads[(dw ? 1 : 0) + (dx ? 2 : 0)];
+  if (dw) plan->dw_engine = 1 + g.w.tile, plan->dw_parts = g.w.splits;
+  if (dx) plan->dx_engine = 1 + g.x.tile, plan->dx_parts = g.x.splits;
+  plan->together = g.together;
+  return SWIGLU_OK;
+}
+
 }  // extern "C"

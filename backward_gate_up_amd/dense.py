@@ -21,6 +21,7 @@ the same leaves that was built on the default stream is alive, a captured call t
 needs gradients is refused: the leaves' accumulation would leave the capture.
 """
 
+import ctypes
 import functools
 import math
 
@@ -240,6 +241,26 @@ def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), work
     dt, device = _linear_args(x, w, None, dy)
     _same(x, z)
     return _on(device, _linear_bwd, _flat16(dy), _flat16(x), _flat16(w), _flat16(z), act, needs, dt, device, workspace)
+
+
+def linear_plan(T, N, K, dtype, dw=False, dx=False):
+    """How a linear layer of these sizes runs on the current device, for profiles and
+    tests: {"fwd": (engine, parts of K)}, or with ``dw`` or ``dx`` what the backward
+    does for them, {"dw": ..., "dx": ..., "together": both in one launch}. Engines are
+    "stream" (of the weight), tiles "64x64", "64x128", "128x128", and "ring" (of 256 x
+    256 tiles)."""
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16, float16, float32")
+    p = _L.LinearPlan()
+    _check(_c("linear_plan")(T, N, K, _DT[dtype], dw, dx, ctypes.byref(p)), "swiglu_mlp_linear_plan")
+    if not (dw or dx):
+        return {"fwd": (_L.ENGINES[p.fwd_engine], p.fwd_parts)}
+    plan = {"together": bool(p.together)}
+    if dw:
+        plan["dw"] = (_L.ENGINES[p.dw_engine], p.dw_parts)
+    if dx:
+        plan["dx"] = (_L.ENGINES[p.dx_engine], p.dx_parts)
+    return plan
 
 
 def linear(x, w, bias=None, activation=None, residual=None):

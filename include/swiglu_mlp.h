@@ -368,6 +368,17 @@ int swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W, const vo
                           void* dbias, void* workspace, size_t workspace_bytes, int64_t T, int64_t N,
                           int64_t K, int act, int dtype, hipStream_t stream);
 
+/* How a linear layer of these sizes runs on the current device (launches nothing;
+ * for profiles and tests). engine: 0 stream of the weight, 1 tiles of 64 x 64, 2 of
+ * 64 x 128, 3 of 128 x 128, 4 ring of 256 x 256 tiles; parts: of the summed axis.
+ * dw, dx: whether the backward is asked for them; neither: the forward. The
+ * entries of what is not asked for are 0; `together`: both gradients in one launch. */
+typedef struct {
+  int32_t fwd_engine, fwd_parts, dw_engine, dw_parts, dx_engine, dx_parts, together;
+} swiglu_linear_plan_t;
+int swiglu_mlp_linear_plan(int64_t T, int64_t N, int64_t K, int dtype, int dw, int dx,
+                           swiglu_linear_plan_t* plan);
+
 /* Static description of a status code (never NULL). */
 const char* swiglu_mlp_status_string(int status);
 
