@@ -28,7 +28,7 @@ import math
 import torch
 
 from . import _lib as _L
-from .serve import _DT, _bytes, _check, _code, _on_gpu, _ptr, _stream, _workspace
+from .serve import _DT, _bytes, _check, _code, _device, _on_gpu, _ptr, _stream, _workspace
 
 ACTIVATIONS = tuple(_L.ACTS)
 
@@ -48,9 +48,6 @@ def _nodes():
 @functools.lru_cache(maxsize=None)
 def _c(name):
     return getattr(_L.lib(), "swiglu_mlp_" + name)
-
-
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _on(device, call, *args):

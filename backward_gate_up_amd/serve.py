@@ -47,9 +47,17 @@ def _ptr(t):
     return t.data_ptr() if t.numel() else None
 
 
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 @functools.lru_cache(maxsize=4096)
-def _bytes(query, *sizes):
+def _bytes_on(device, query, *sizes):
     return getattr(_L.lib(), query)(*sizes)
+
+
+def _bytes(query, *sizes):
+    # plans, and so sizes, go by the current device's number of compute units
+    return _bytes_on(_device(), query, *sizes)
 
 
 def _code(t, table=_DT):
