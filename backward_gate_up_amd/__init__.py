@@ -34,6 +34,7 @@ import torch
 
 from . import _lib as _L
 from ._lib import SwiGLUError, STAGE_NAMES, NUM_STAGES  # noqa: F401
+from .serve import _no_transforms
 from .serve import (moe_route, moe_experts, moe_infer, w4_quantize, w4_pack, w4_linear, infer_w4,  # noqa: F401
                     W4Weight, SwiGLUMLPW4, SwiGLUMoE)
 from .dense import (layer_norm, rms_norm, linear, norm_fwd, norm_bwd, linear_fwd, linear_bwd, feed_forward,  # noqa: F401
@@ -118,6 +119,11 @@ def fwd(x, wg, wu, wd, y=None, saved=None, two_round=False, linear=False):
     [3, T, H] A|G|U buffer that ``bwd`` consumes. ``two_round`` selects the
     historical two-round SwiGLU program A = rnd(rnd(SiLU(g)) u) instead of
     the one-round A = rnd(SiLU(g) u); ``linear``: nn.Linear weight layout."""
+    _no_transforms(x, wg, wu, wd)
+    return _fwd(x, wg, wu, wd, y, saved, two_round, linear)
+
+
+def _fwd(x, wg, wu, wd, y=None, saved=None, two_round=False, linear=False):
     x, wg, wu, wd = (t.contiguous() for t in (x, wg, wu, wd))
     T, D, H = _shapes(x, wg, wu, wd, linear)
     y = _buf(y, (T, D), x, "y")
@@ -137,6 +143,7 @@ def bwd(dy, x, wg, wu, wd, saved, dx=None, dwg=None, dwu=None, dwd=None, workspa
     Returns (dX, dWg, dWu, dWd), the weight gradients in their weights'
     layout. ``workspace``: at least ``bwd_workspace_bytes`` bytes (allocated
     here when None and needed)."""
+    _no_transforms(dy, x, wg, wu, wd)
     dy, x, wg, wu, wd = (t.contiguous() for t in (dy, x, wg, wu, wd))
     T, D, H = _shapes(x, wg, wu, wd, linear)
     if tuple(dy.shape) != (T, D) or dy.dtype != x.dtype or dy.device != x.device:
@@ -163,6 +170,7 @@ def infer(x, wg, wu, wd, y=None, workspace=None, two_round=False, linear=False):
     """No-grad forward: only the workspace (A[T,H], plus arrival counters and
     fp32 partial sums for T <= 128; ``infer_workspace_bytes`` bytes) and
     Y[T,D] are written."""
+    _no_transforms(x, wg, wu, wd)
     x, wg, wu, wd = (t.contiguous() for t in (x, wg, wu, wd))
     T, D, H = _shapes(x, wg, wu, wd, linear)
     y = _buf(y, (T, D), x, "y")
@@ -182,6 +190,7 @@ def infer_noalloc(x, wg, wu, wd, y=None, two_round=False, linear=False):
     fixed per-device scratch holds the workspace (calls on one device must
     not overlap). Raises SwiGLUError (SWIGLU_ERR_SCRATCH) when the shape
     needs more than that scratch."""
+    _no_transforms(x, wg, wu, wd)
     x, wg, wu, wd = (t.contiguous() for t in (x, wg, wu, wd))
     T, D, H = _shapes(x, wg, wu, wd, linear)
     y = _buf(y, (T, D), x, "y")
@@ -199,7 +208,7 @@ class SwiGLUMLPFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, wg, wu, wd, two_round=False, linear=False):
-        y, saved = fwd(x, wg, wu, wd, two_round=two_round, linear=linear)
+        y, saved = _fwd(x, wg, wu, wd, two_round=two_round, linear=linear)
         ctx.save_for_backward(x, wg, wu, wd)
         ctx.saved_buf = saved
         ctx.linear = linear
@@ -221,10 +230,14 @@ class SwiGLUMLPFunction(torch.autograd.Function):
 def swiglu_mlp(x, wg, wu, wd, two_round=False, linear=False):
     """Y = (SiLU(x Wg) * (x Wu)) Wd for x[..., D] (with ``linear``, the
     nn.Linear weights: Y = down(SiLU(gate(x)) * up(x))). Uses the no-grad
-    path when autograd does not need gradients."""
+    path when autograd does not need gradients. Forward-mode derivatives and make_fx are
+    refused; torch.jit.trace records the call where gradients are needed (as a Python
+    function) and is refused where they are not."""
+    needs = torch.is_grad_enabled() and any(t.requires_grad for t in (x, wg, wu, wd))
+    if needs:  # (infer has its own check)
+        _no_transforms(x, wg, wu, wd, traced=True)
     lead = x.shape[:-1]
     x2 = x.reshape(-1, x.shape[-1])
-    needs = torch.is_grad_enabled() and any(t.requires_grad for t in (x, wg, wu, wd))
     if needs:
         y = SwiGLUMLPFunction.apply(x2, wg, wu, wd, two_round, linear)
     else:

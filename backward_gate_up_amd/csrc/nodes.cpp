@@ -7,7 +7,10 @@
 // caches (RMS norm of 33 x 11008 with gradients 86 us as a Python node, 58 as this
 // one; layer norm of 777 x 1001 101 and 72).
 #include <ATen/DeviceGuard.h>
+#include <c10/core/AutogradState.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
 #include <cmath>
@@ -241,6 +244,18 @@ struct FeedForward : torch::autograd::Function<FeedForward> {
 };
 
 // ---- entries ----------------------------------------------------------------------
+// The kernels' work is seen by no tracer and by no forward-mode derivative: refused,
+// where a traced call would be left out of the graph and its output be whatever the
+// memory holds, and a derivative be zero.
+void check_transforms(std::initializer_list<const Tensor*> ts) {
+  using Modes = c10::impl::TorchDispatchModeTLS;
+  TORCH_CHECK(!torch::jit::tracer::isTracing() &&
+                  !(Modes::any_modes_set() && Modes::get_mode(c10::impl::TorchDispatchModeKey::PROXY).has_value()),
+              "this operator cannot be traced (torch.jit.trace, make_fx): its kernels would be left out of the graph");
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+  for (const Tensor* t : ts)
+    TORCH_CHECK(!t || !t->_fw_grad(0).defined(), "this operator has no forward-mode derivative, and an input has a tangent");
+}
 bool wants_grad(std::initializer_list<const Tensor*> ts) {
   if (!at::GradMode::is_enabled()) return false;
   for (const Tensor* t : ts)
@@ -273,6 +288,7 @@ Tensor rows(const Tensor& x) {
 }
 
 Tensor norm(const Tensor& x_, const Tensor& w, const Maybe& b, double eps, bool rms) {
+  check_transforms({&x_, &w, opt(b)});
   const Tensor x = rows(x_);
   norm_args(x, w, b, eps, rms);
   Tensor y;
@@ -287,6 +303,7 @@ Tensor norm(const Tensor& x_, const Tensor& w, const Maybe& b, double eps, bool 
 }
 
 Tensor linear(const Tensor& x_, const Tensor& w, const Maybe& b, const Maybe& r_, int64_t act) {
+  check_transforms({&x_, &w, opt(b), opt(r_)});
   TORCH_CHECK_VALUE(x_.dim() > 0 && w.dim() == 2, "expected X[..., K] and W[N, K]");
   auto shape = x_.sizes().vec();
   shape.back() = w.size(0);
@@ -307,6 +324,7 @@ Tensor linear(const Tensor& x_, const Tensor& w, const Maybe& b, const Maybe& r_
 
 Tensor feed_forward(const Tensor& x_, const Tensor& nw, const Maybe& nb, const Tensor& w1, const Maybe& b1, const Tensor& w2,
                     const Maybe& b2, int64_t act, double eps, bool rms) {
+  check_transforms({&x_, &nw, opt(nb), &w1, opt(b1), &w2, opt(b2)});
   const Tensor x = rows(x_);
   norm_args(x, nw, nb, eps, rms);
   linear_args(x, w1, b1, Maybe());

@@ -13,7 +13,8 @@ module ``FeedForward``. Their nodes are in C++ (csrc/nodes.cpp), since small tra
 steps are bound by host code; they call the same library.
 All tensors of a call share dtype (bf16, fp16 or fp32) and device.
 
-Second derivatives are refused. The backward may run more than once
+Second derivatives, forward-mode derivatives and tracers (torch.jit.trace, make_fx) are
+refused. The backward may run more than once
 (``retain_graph``): it changes nothing that the forward kept.
 
 Calls can be captured in a graph, with their backward. While an autograd graph of
@@ -28,7 +29,7 @@ import math
 import torch
 
 from . import _lib as _L
-from .serve import _DT, _bytes, _check, _code, _device, _on_gpu, _ptr, _stream, _workspace
+from .serve import _DT, _bytes, _check, _code, _device, _no_transforms, _on_gpu, _ptr, _stream, _workspace
 
 ACTIVATIONS = tuple(_L.ACTS)
 
@@ -126,6 +127,7 @@ def norm_fwd(x, weight, bias=None, eps=1e-5, rms=False, stats=True):
     sqrt(mean((x - mean)^2) + eps); with ``rms`` the mean is 0 and there is no
     bias. Returns (Y, stats): fp32 [2, T] (mean, rstd), with ``rms`` [1, T]
     (rstd), for ``norm_bwd``; None without ``stats``."""
+    _no_transforms(x, weight, bias)
     dt, device = _norm_args(x, weight, bias, eps, rms)
     return _on(device, _norm_fwd, _flat(x), _flat(weight), _flat(bias), eps, bool(rms), stats, dt, device)
 
@@ -147,6 +149,7 @@ def _norm_bwd(dy, x, weight, st, rms, bias, dt, device, dres=None, workspace=Non
 def norm_bwd(dy, x, weight, stats, rms=False, bias=False, dres=None, workspace=None):
     """(dX, dweight, dbias) of ``norm_fwd``; dbias is None unless ``bias``. ``dres``
     [T, D] is added to dX (the gradient that reaches x past the norm)."""
+    _no_transforms(dy, x, weight, dres)
     if dy.shape != x.shape or (dres is not None and dres.shape != x.shape):
         raise ValueError("dY and dres must match X in shape")
     _norm_args(x, weight, None, 0.0, rms)
@@ -205,6 +208,7 @@ def linear_fwd(x, w, bias=None, activation=None, residual=None, keep=True, works
     ``activation`` None, "relu", "gelu", "gelu_tanh" or "silu". K and N are
     multiples of 8. Returns (Y, Z): Z[T, N] is the activation's argument in the
     inputs' dtype, for ``linear_bwd``; None without an activation or ``keep``."""
+    _no_transforms(x, w, bias, residual)
     act = _act(activation)
     dt, device = _linear_args(x, w, bias, residual)
     return _on(device, _linear_fwd, _flat16(x), _flat16(w), _flat16(bias), act, _flat16(residual), keep, dt, device, workspace)
@@ -229,6 +233,7 @@ def linear_bwd(dy, x, w, z=None, activation=None, needs=(True, True, True), work
     """(dX, dW, dbias) of ``linear_fwd``; ``needs`` says which are wanted, the
     others are None. ``z``: what ``linear_fwd`` kept, where there is an
     activation. The residual's gradient is dY."""
+    _no_transforms(dy, x, w)
     act = _act(activation)
     if dy.dim() != 2 or tuple(dy.shape) != (x.shape[0], w.shape[0]):
         raise ValueError(f"dY must be [T, N]: {tuple(dy.shape)}")

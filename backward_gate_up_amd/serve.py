@@ -19,6 +19,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd import forward_ad as _fw
 
 from . import _lib as _L
 from ._lib import SwiGLUError
@@ -68,7 +69,25 @@ def _code(t, table=_DT):
         raise TypeError(f"unsupported dtype {t.dtype}; use {names}") from None
 
 
+_tracing, _modes, _mode = torch._C._is_tracing, torch._C._len_torch_dispatch_stack, torch._C._get_dispatch_mode
+_PROXY = torch._C._TorchDispatchModeKey.PROXY
+
+
+def _no_transforms(*tensors, traced=False):
+    """The kernels' work is seen by no tracer and by no forward-mode derivative: refused,
+    where a traced call would be left out of the graph and its output be whatever the
+    memory holds, and a derivative be zero. ``traced``: torch.jit.trace records the call
+    by other means (as an autograd Function in Python)."""
+    if (_tracing() and not traced) or (_modes() and _mode(_PROXY) is not None):
+        raise RuntimeError("this operator cannot be traced (torch.jit.trace, make_fx): its kernels would be left out of the graph")
+    if _fw._current_level >= 0 and torch._C._is_fwd_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and _fw.unpack_dual(t).tangent is not None:
+                raise RuntimeError("this operator has no forward-mode derivative, and an input has a tangent")
+
+
 def _no_grad(*tensors):
+    _no_transforms(*tensors)
     if not torch.is_grad_enabled():
         return
     if any(t.requires_grad for t in tensors):
@@ -133,6 +152,7 @@ class W4Weight:
     def dequantize(self):
         """The weight as rows in ``dtype``, each value rounded once (for
         prompts long enough that ``infer(..., linear=True)`` is the faster)."""
+        _no_transforms()
         w = torch.empty(self.shape, dtype=self.dtype, device=self.device)
         _check(_L.lib().swiglu_mlp_w4_dequantize(self._ref, w.data_ptr(), _DT16[self.dtype], _stream(w.device)),
                "swiglu_mlp_w4_dequantize")
@@ -161,6 +181,7 @@ def w4_quantize(w, group=128, zeros=False):
     them scale = (max(w, 0) - min(w, 0)) / 15 and code = round(w / scale) +
     round(-min / scale), all clamped to 0..15. A NaN in ``w`` makes its group's
     scale NaN."""
+    _no_transforms(w)
     w = w.detach().contiguous()
     _on_gpu(w)
     dt = _code(w, _DT16)
@@ -179,6 +200,7 @@ def w4_pack(codes, scales, zeros=None):
     """The ``W4Weight`` of codes, scales and zero points laid out as
     ``w4_quantize`` returns them (any quantiser's, with codes and zero points
     0..15). W = scale * (code - zero), zero = 8 where ``zeros`` is None."""
+    _no_transforms(scales)
     codes, scales = codes.contiguous(), scales.contiguous()
     _on_gpu(codes)
     _code(scales, _DT16)

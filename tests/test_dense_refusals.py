@@ -27,3 +27,105 @@ def test_workspace_sizes_are_kept_by_device(monkeypatch):
         got.append(dense._bytes("some_workspace_bytes", 3, 4))
     assert got == [1007, 2007, 1007, 2007]
     assert asked == [(0, (3, 4)), (1, (3, 4))]  # each asked once
+
+
+# ---- forward mode and tracers -----------------------------------------------------
+
+
+def entries(device, dtype=torch.bfloat16):
+    """name -> (call of its first input, that input) of every operator, the rest at hand."""
+    z = lambda *s: torch.randn(s, device=device, generator=torch.Generator(device).manual_seed(len(s))).to(dtype)  # noqa: E731
+    x, w, v, b, r = z(4, 64), z(72, 64), z(64), z(72), z(4, 72)
+    wl, wd, e = z(72, 64), z(64, 72), z(2, 72, 64)
+    ids, weights = torch.zeros(4, 1, dtype=torch.int32, device=device), torch.ones(4, 1, device=device)
+    stats = torch.ones(2, 4, device=device)
+    return {
+        "layer_norm": (lambda t: mlp.layer_norm(t, v, v), x), "layer_norm weight": (lambda t: mlp.layer_norm(x, t), v),
+        "rms_norm": (lambda t: mlp.rms_norm(t, v), x),
+        "linear": (lambda t: mlp.linear(t, w, b, "gelu", r), x), "linear w": (lambda t: mlp.linear(x, t), w),
+        "linear bias": (lambda t: mlp.linear(x, w, t), b), "linear residual": (lambda t: mlp.linear(x, w, None, None, t), r),
+        "feed_forward": (lambda t: mlp.feed_forward(t, v, None, wl, None, wd, None), x),
+        "feed_forward w2": (lambda t: mlp.feed_forward(x, v, None, wl, None, t, None), wd),
+        "norm_fwd": (lambda t: mlp.norm_fwd(t, v)[0], x), "norm_bwd": (lambda t: mlp.norm_bwd(t, x, v, stats)[0], x),
+        "linear_fwd": (lambda t: mlp.linear_fwd(t, w)[0], x), "linear_bwd": (lambda t: mlp.linear_bwd(t, x, w)[0], r),
+        "swiglu_mlp": (lambda t: mlp.swiglu_mlp(t, wl, wl, wd, linear=True), x),
+        "fwd": (lambda t: mlp.fwd(t, wl, wl, wd, linear=True)[0], x), "infer": (lambda t: mlp.infer(t, wl, wl, wd, linear=True), x),
+        "infer_noalloc": (lambda t: mlp.infer_noalloc(t, wl, wl, wd, linear=True), x),
+        "moe_route": (lambda t: mlp.moe_route(t, w, 2)[0], x),
+        "moe_experts": (lambda t: mlp.moe_experts(t, weights, ids, e, e, e.mT.contiguous()), x),
+        "moe_infer": (lambda t: mlp.moe_infer(t, w[:2], e, e, e.mT.contiguous(), 1), x),
+        "w4_quantize": (lambda t: mlp.w4_quantize(t, 32)[1], w),
+    }
+
+
+ENTRIES = list(entries("cpu"))
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_tangents_are_refused(name):
+    """An input with a tangent, with and without reverse-mode gradients: no operator
+    has a forward-mode derivative, and none returns an output without one."""
+    f, t = entries("cpu")[name]
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))
+        for grad in (torch.no_grad(), torch.enable_grad()):
+            with grad, pytest.raises(RuntimeError, match="no forward-mode derivative"):
+                f(dual)
+        # where forward mode is off, and for inputs without a tangent, the call goes on
+        with torch.autograd.forward_ad._set_fwd_grad_enabled(False), pytest.raises(ValueError, match="on a GPU"):
+            f(dual)
+        with pytest.raises(ValueError, match="on a GPU"):
+            f(t)
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_tracers_are_refused(name):
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    f, t = entries("cpu")[name]
+    with torch.no_grad():
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            torch.jit.trace(f, (t,), check_trace=False)
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            make_fx(f)(t)
+    if name in ("layer_norm", "rms_norm", "linear", "feed_forward", "swiglu_mlp"):
+        t = t.clone().requires_grad_()
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            make_fx(f)(t)
+        if name != "swiglu_mlp":
+            with pytest.raises(RuntimeError, match="cannot be traced"):
+                torch.jit.trace(f, (t,), check_trace=False)
+    with pytest.raises(ValueError, match="on a GPU"):
+        f(t)
+
+
+@pytest.mark.gpu
+def test_what_is_recorded_still_is():
+    """swiglu_mlp with gradients under torch.jit.trace, as before; the dense operators under
+    torch.compile, which leaves them to be run as they are; a dispatch mode that only looks."""
+    x = torch.randn(5, 64, device="cuda").bfloat16()
+    wl, wd = (torch.randn(s, device="cuda").bfloat16().requires_grad_() for s in ((72, 64), (64, 72)))
+    block = lambda t: mlp.swiglu_mlp(t, wl, wl, wd, linear=True)  # noqa: E731
+    # (weights as inputs: torch takes none that need gradients as constants of a trace)
+    traced = torch.jit.trace(lambda t, w, d: mlp.swiglu_mlp(t, w, w, d, linear=True), (x, wl, wd), check_trace=False)
+    assert torch.equal(traced(x + 1, wl, wd), block(x + 1))
+    dense_chain = lambda t: mlp.linear(mlp.rms_norm(t, wd[:, 0]), wl, None, "gelu") * 2  # noqa: E731
+    layer = lambda t: mlp.feed_forward(t * 2, wd[:, 0], None, wl, None, wd, None)  # noqa: E731
+    for f in (dense_chain, layer):
+        compiled = torch.compile(f, backend="eager")
+        for grad in (False, True):
+            with torch.set_grad_enabled(grad):
+                y, want = compiled(x), f(x)
+                assert torch.equal(y, want)
+            if grad:
+                dy = torch.randn_like(y)
+                got, ref = (torch.autograd.grad(t, (wl, wd), dy) for t in (y, want))
+                assert all(torch.equal(a, c) for a, c in zip(got, ref))
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Sees(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            return func(*args, **(kwargs or {}))
+
+    with Sees():
+        assert torch.equal(layer(x), layer(x))
