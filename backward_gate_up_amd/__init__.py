@@ -253,7 +253,8 @@ class SwiGLUMLP(torch.nn.Module):
     hidden_size) as bias-free nn.Linear layers, so a state dict of such a
     module loads unchanged, and y = down_proj(SiLU(gate_proj(x)) *
     up_proj(x)) computed by the fused kernels, which read the nn.Linear
-    weights in place. Standard SwiGLU only: ``config.mlp_bias`` must be false
+    weights in place: the submodules are never called, so hooks on them and the
+    forward of a layer put in their place do not run. Standard SwiGLU only: ``config.mlp_bias`` must be false
     and ``config.hidden_act`` "silu" (or "swish"). Parameters must be bf16,
     fp16 or fp32 on a gfx950 GPU. ``two_round`` (keyword) selects the
     historical two-round SwiGLU epilogue."""

@@ -291,13 +291,31 @@ _CONFIG_ACTS = {"relu": "relu", "gelu": "gelu", "gelu_new": "gelu_tanh", "gelu_p
                 "gelu_tanh": "gelu_tanh", "silu": "silu", "swish": "silu"}
 
 
+_HOOKS = ("_forward_pre_hooks", "_forward_hooks", "_backward_pre_hooks", "_backward_hooks")
+
+
+def _own(name, layer, *kinds):
+    """``layer``, of which only the weights are read: one of torch's ``kinds`` (or a
+    parametrized one), as it is. A layer of another kind in its place and hooks on it
+    would not run, so they are refused."""
+    if not any(type(layer).forward is k.forward for k in kinds) or "forward" in layer.__dict__:
+        raise TypeError(f"FeedForward reads the weights of {name} and does not call it: it has to be a "
+                        f"{' or '.join('torch.nn.' + k.__name__ for k in kinds)}, got {type(layer).__name__}")
+    if any(layer.__dict__[h] for h in _HOOKS):
+        raise RuntimeError(f"FeedForward reads the weights of {name} and does not call it: hooks on it would not run "
+                           f"(hook the FeedForward itself)")
+    return layer
+
+
 class FeedForward(torch.nn.Module):
     """The ungated feed-forward layer with its norm in front and the stream added:
     y = x + fc2(act(fc1(norm(x)))). ``config`` has hidden_size, intermediate_size
     and optionally hidden_act (default "gelu"), mlp_bias (default true) and the
     norm's epsilon, as layer_norm_eps (default 1e-5) or, for an RMS norm in front,
     rms_norm_eps. Submodules ``norm``, ``fc1`` and ``fc2`` are torch's, whose
-    weights the kernels read in place."""
+    weights the kernels read in place: they are never called, so layers of another kind
+    in their place (adapters, quantised ones) and hooks on them are refused;
+    parametrizations of their weights work."""
 
     def __init__(self, config):
         super().__init__()
@@ -316,9 +334,11 @@ class FeedForward(torch.nn.Module):
         self.fc2 = torch.nn.Linear(H, D, bias=bias)
 
     def forward(self, x):
-        rms = isinstance(self.norm, torch.nn.RMSNorm)
-        return feed_forward(x, self.norm.weight, None if rms else self.norm.bias, self.fc1.weight, self.fc1.bias,
-                            self.fc2.weight, self.fc2.bias, self.activation, self.norm.eps, rms)
+        norm = _own("norm", self.norm, torch.nn.LayerNorm, torch.nn.RMSNorm)
+        fc1, fc2 = _own("fc1", self.fc1, torch.nn.Linear), _own("fc2", self.fc2, torch.nn.Linear)
+        rms = isinstance(norm, torch.nn.RMSNorm)
+        return feed_forward(x, norm.weight, None if rms else norm.bias, fc1.weight, fc1.bias, fc2.weight, fc2.bias,
+                            self.activation, norm.eps, rms)
 
     def extra_repr(self):
         return f"activation={self.activation!r}"

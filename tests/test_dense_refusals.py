@@ -129,3 +129,67 @@ def test_what_is_recorded_still_is():
 
     with Sees():
         assert torch.equal(layer(x), layer(x))
+
+
+# ---- the layer's submodules -------------------------------------------------------
+
+
+class Config:
+    hidden_size, intermediate_size, hidden_act = 64, 72, "silu"
+
+
+class Adapted(torch.nn.Linear):
+    """A linear layer with something of its own beside its weight."""
+
+    def forward(self, x):
+        return super().forward(x) + 1
+
+
+@pytest.mark.parametrize("name", ["norm", "fc1", "fc2"])
+def test_layers_that_would_not_run_are_refused(name):
+    x = torch.zeros(3, 64)
+    block = mlp.FeedForward(Config())
+    layer = getattr(block, name)
+    with pytest.raises(ValueError, match="on a GPU"):  # nothing to refuse but the host's tensors
+        block(x)
+    for add in ("register_forward_pre_hook", "register_forward_hook", "register_full_backward_hook",
+                "register_full_backward_pre_hook"):
+        handle = getattr(layer, add)(lambda *a: None)
+        with pytest.raises(RuntimeError, match=f"of {name} and does not call it: hooks"):
+            block(x)
+        handle.remove()
+    with pytest.raises(ValueError, match="on a GPU"):
+        block(x)
+    layer.forward = layer.forward
+    with pytest.raises(TypeError, match=f"of {name} and does not call it: it has to be a torch.nn"):
+        block(x)
+    del layer.forward
+    for other in (Adapted(64, 72), torch.nn.Identity(), torch.nn.Sequential(layer)):
+        setattr(block, name, other)
+        with pytest.raises(TypeError, match=f"of {name} and does not call it: it has to be a torch.nn"):
+            block(x)
+    setattr(block, name, layer)
+    with pytest.raises(ValueError, match="on a GPU"):
+        block(x)
+
+
+@pytest.mark.gpu
+def test_parametrized_layers_and_hooks_on_the_layer_run():
+    """A parametrization's weight is the layer's weight, its gradient reaches what it
+    is made of; hooks on the FeedForward itself run; so do copies."""
+    import copy
+
+    torch.manual_seed(1)
+    block = mlp.FeedForward(Config()).to("cuda")
+    torch.nn.utils.parametrizations.weight_norm(block.fc1)
+    block.fc1.parametrizations.weight.original0.data.mul_(1.5)
+    x = torch.randn(5, 64, device="cuda")
+    want = mlp.feed_forward(x, block.norm.weight, block.norm.bias, block.fc1.weight, block.fc1.bias, block.fc2.weight,
+                            block.fc2.bias, "silu")
+    seen = []
+    block.register_forward_hook(lambda m, args, out: seen.append(out))
+    for m in (block, copy.deepcopy(block)):
+        y = m(x)
+        assert torch.equal(y, want) and seen.pop() is y
+        y.sum().backward()
+        assert m.fc1.parametrizations.weight.original0.grad.abs().sum() > 0
