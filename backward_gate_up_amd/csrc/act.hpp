@@ -13,9 +13,11 @@
 // Phi: with a = |z|, Phi(-a) = Q(a) exp(-a^2 / 2), Q falling from 1/2 like 1 / (a
 // sqrt(2 pi)). Q(a) = t p(t), t = 1 / (1 + c a), p fitted to the scaled
 // complementary error function for the smallest relative error on 0 <= a <= 14
-// (past that the exponential is zero): degree 8 for IEEE (2.8e-8, 2.1e-7 as
-// evaluated in fp32; the math library's erfc took 12 of the 67 us of T = 1000, K =
-// 1024, N = 2816), degree 5 for fast (4.8e-6, a hundredth of fp16's half step).
+// (past that the exponential is zero): degree 8 for IEEE, 2.8e-8 in exact
+// arithmetic, 7.8e-8 with the coefficients in fp32, and 4.2e-7 evaluated in fp32
+// step by step, t and its roundings with it and the exponential without (the math
+// library's erfc took 12 of the 67 us of T = 1000, K = 1024, N = 2816); degree 5 for
+// fast, 4.8e-6, evaluated 5.0e-6, a hundredth of fp16's half step.
 // The exponential also serves the derivative's density.
 #pragma once
 #include "gemm_tile.hpp"
