@@ -169,7 +169,7 @@ int swiglu_mlp_linear_bwd(const void* dY, const void* X, const void* W, const vo
   if (rc) return rc;
   const size_t tn = (size_t)T * N * e, tk = (size_t)T * K * e, nk = (size_t)N * K * e;
   const size_t need = swiglu_mlp_linear_bwd_workspace_bytes(T, N, K, act, dtype);
-  const Range in[] = {{dY, tn}, {X, tk}, {W, nk}, {Z, act == SWIGLU_ACT_NONE ? 0 : tn}};
+  const Range in[] = {{dY, tn}, {X, X || dW ? tk : 0}, {W, W || dX ? nk : 0}, {Z, act == SWIGLU_ACT_NONE ? 0 : tn}};
   const Range out[] = {optional(dX, tk), optional(dW, nk), optional(dbias, (size_t)N * e), {workspace, need}};
   if ((rc = check_ptrs(in, 4)) || (rc = check_ptrs(out, 3))) return rc;
   if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_WORKSPACE;

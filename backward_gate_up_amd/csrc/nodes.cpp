@@ -137,18 +137,19 @@ Projected linear_forward(const Tensor& x, const Tensor& w, const Tensor& b, cons
 struct LinearGrads {
   Tensor x, w, b;
 };
-LinearGrads linear_backward(const Tensor& dy, const Tensor& x, const Tensor& w, const Tensor& z, int64_t act, bool dx, bool dw,
-                            bool db) {
-  const int64_t T = x.size(0), N = w.size(0), K = x.size(1);
+// x is read for dw, w for dx: what is not wanted may be undefined. K: x's columns.
+LinearGrads linear_backward(const Tensor& dy, const Tensor& x, const Tensor& w, const Tensor& z, int64_t K, int64_t act, bool dx,
+                            bool dw, bool db) {
+  const int64_t T = dy.size(0), N = dy.size(1);
   LinearGrads g;
   if (!dx && !dw && !db) return g;
-  if (dx) g.x = at::empty_like(x);
-  if (dw) g.w = at::empty_like(w);
-  if (db) g.b = at::empty({N}, x.options());
-  const size_t need = swiglu_mlp_linear_bwd_workspace_bytes(T, N, K, (int)act, code(x));
-  const Tensor ws = workspace(need, x);
+  if (dx) g.x = at::empty({T, K}, dy.options());
+  if (dw) g.w = at::empty({N, K}, dy.options());
+  if (db) g.b = at::empty({N}, dy.options());
+  const size_t need = swiglu_mlp_linear_bwd_workspace_bytes(T, N, K, (int)act, code(dy));
+  const Tensor ws = workspace(need, dy);
   check(swiglu_mlp_linear_bwd(ptr(dy), ptr(x), ptr(w), ptr(z), ptr(g.x), ptr(g.w), ptr(g.b), ptr(ws), need, T, N, K, (int)act,
-                              code(x), stream(x)),
+                              code(dy), stream(dy)),
         "swiglu_mlp_linear_bwd");
   return g;
 }
@@ -163,6 +164,12 @@ struct Needs {
 };
 void no_second() { TORCH_CHECK(!at::GradMode::is_enabled(), "create_graph=True (double backward) is not supported"); }
 int64_t kept(AutogradContext* ctx, const char* key) { return ctx->saved_data[key].toInt(); }
+
+// Only what a wanted gradient reads is kept: a frozen weight's input is free to go, or to
+// be changed in place.
+Tensor kept_if(bool wanted, const Tensor& t) { return wanted ? t : Tensor(); }
+bool wants(const Tensor& t) { return t.requires_grad(); }
+bool wants(const Maybe& t) { return there(t) && t->requires_grad(); }
 
 struct Norm : torch::autograd::Function<Norm> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x_, const Tensor& w_, const Maybe& b_, double eps, bool rms) {
@@ -188,9 +195,11 @@ struct Linear : torch::autograd::Function<Linear> {
                         int64_t act) {
     const at::DeviceGuard guard(x_.device());
     const Tensor x = flat16(x_), w = flat16(w_);
-    const Projected o = linear_forward(x, w, flat16(b_), flat16(r_), act, true);
-    ctx->save_for_backward({x, w, o.z});
+    const bool dz = wants(x_) || wants(w_) || wants(b_);
+    const Projected o = linear_forward(x, w, flat16(b_), flat16(r_), act, dz);
+    ctx->save_for_backward({kept_if(wants(w_), x), kept_if(wants(x_), w), o.z});
     ctx->saved_data["act"] = act;
+    ctx->saved_data["K"] = x.size(1);
     ctx->saved_data["form"] = (int64_t)(there(b_) + 2 * there(r_));
     return o.y;
   }
@@ -200,8 +209,8 @@ struct Linear : torch::autograd::Function<Linear> {
     const int64_t form = kept(ctx, "form");
     Needs needs{ctx};
     const bool dx = needs.next(true), dw = needs.next(true), db = needs.next(form & 1), dr = needs.next(form & 2);
-    const at::DeviceGuard guard(s[0].device());
-    const LinearGrads g = linear_backward(flat16(dy[0]), s[0], s[1], s[2], kept(ctx, "act"), dx, dw, db);
+    const at::DeviceGuard guard(dy[0].device());
+    const LinearGrads g = linear_backward(flat16(dy[0]), s[0], s[1], s[2], kept(ctx, "K"), kept(ctx, "act"), dx, dw, db);
     return {g.x, g.w, g.b, dr ? dy[0] : Tensor(), Tensor()};
   }
 };
@@ -213,11 +222,14 @@ struct FeedForward : torch::autograd::Function<FeedForward> {
                         const Maybe& b1_, const Tensor& w2_, const Maybe& b2_, int64_t act, double eps, bool rms) {
     const at::DeviceGuard guard(x_.device());
     const Tensor x = flat16(x_), nw = flat(nw_), w1 = flat16(w1_), w2 = flat16(w2_);
-    const Normed n = norm_forward(x, nw, flat(nb_), eps, rms, true);
-    const Projected a = linear_forward(n.y, w1, flat16(b1_), Tensor(), act, true);
+    const bool norm = wants(x_) || wants(nw_) || wants(nb_), inner = norm || wants(w1_) || wants(b1_);
+    const Normed n = norm_forward(x, nw, flat(nb_), eps, rms, norm);
+    const Projected a = linear_forward(n.y, w1, flat16(b1_), Tensor(), act, inner);
     const Projected y = linear_forward(a.y, w2, flat16(b2_), x, SWIGLU_ACT_NONE, false);
-    ctx->save_for_backward({x, nw, w1, w2, n.y, n.stats, a.y, a.z});
+    ctx->save_for_backward({kept_if(norm, x), kept_if(norm, nw), kept_if(norm, w1), kept_if(inner, w2), kept_if(wants(w1_), n.y), n.stats,
+                            kept_if(wants(w2_), a.y), a.z});
     ctx->saved_data["act"] = act;
+    ctx->saved_data["H"] = w1.size(0);
     ctx->saved_data["form"] = (int64_t)(rms + 2 * there(nb_) + 4 * there(b1_) + 8 * there(b2_));
     return y.y;
   }
@@ -230,12 +242,12 @@ struct FeedForward : torch::autograd::Function<FeedForward> {
     const bool dx = needs.next(true), dnw = needs.next(true), dnb = needs.next(form & 2), dw1 = needs.next(true),
                db1 = needs.next(form & 4), dw2 = needs.next(true), db2 = needs.next(form & 8);
     const bool norm = dx || dnw || dnb, inner = norm || dw1 || db1;
-    const at::DeviceGuard guard(x.device());
+    const at::DeviceGuard guard(dy_[0].device());
     const Tensor dy = flat16(dy_[0]);
-    LinearGrads g2 = linear_backward(dy, a, w2, Tensor(), SWIGLU_ACT_NONE, inner, dw2, db2), g1;
+    LinearGrads g2 = linear_backward(dy, a, w2, Tensor(), kept(ctx, "H"), SWIGLU_ACT_NONE, inner, dw2, db2), g1;
     NormGrads g0;
     if (inner) {
-      g1 = linear_backward(g2.x, n, w1, z, kept(ctx, "act"), norm, dw1, db1);
+      g1 = linear_backward(g2.x, n, w1, z, dy.size(1), kept(ctx, "act"), norm, dw1, db1);
       g2.x = Tensor();  // (its memory serves what follows)
       if (norm) g0 = norm_backward(g1.x, x, nw, stats, dy, form & 1, form & 2);
     }

@@ -345,7 +345,8 @@ int swiglu_mlp_norm_bwd(const void* dY, const void* X, const void* weight, const
  * The backward reads dY, X, W and, where there is an activation, Z, and
  * writes dX = dZ W, dW = dZ^T X and dbias = sum over tokens of dZ, where dZ =
  * dY act'(Z) (rounded to the storage type for the two products, not for the
- * sum); NULL: not wanted. The residual's gradient is dY. T = 0 writes zero
+ * sum); NULL: not wanted, and X may be NULL where dW is, W where dX is. The
+ * residual's gradient is dY. T = 0 writes zero
  * weight gradients. gelu is z Phi(z), gelu_tanh its form with tanh; relu's
  * derivative at 0 and at NaN is 0, every derivative at an infinity its limit (a
  * Z past the storage type's range). In bf16 and fp16 silu and gelu_tanh of values
