@@ -277,7 +277,10 @@ bool wants_grad(std::initializer_list<const Tensor*> ts) {
 // A leaf's accumulation node belongs to the stream it was made on and lives as long as a
 // graph that uses it. Where that is the default stream, a captured backward would
 // make the default stream wait for the capture, which is an error that ends the
-// capture in the engine's threads: refused here instead.
+// capture in the engine's threads: refused here instead. In the forward, although only a
+// backward would leave the capture, since other operators' nodes of the same step may
+// reach such a leaf before these nodes are asked; a forward without a backward belongs under
+// torch.no_grad, which nothing refuses.
 void check_capture(std::initializer_list<const Tensor*> ts) {
   const Tensor& x = **ts.begin();
   hipStream_t s = stream(x);
@@ -289,7 +292,8 @@ void check_capture(std::initializer_list<const Tensor*> ts) {
     const auto made_on = node ? node->stream() : std::nullopt;
     TORCH_CHECK(!made_on || made_on->id() != 0,
                 "an autograd graph of the same leaves, built on the default stream, is alive: its accumulation would leave "
-                "this capture; delete it (its loss and outputs) or build it on a side stream");
+                "this capture; delete it (its loss and outputs) or build it on a side stream; capture a forward without a backward under "
+                "torch.no_grad()");
   }
 }
 // x [..., D] as rows

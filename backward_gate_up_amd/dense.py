@@ -19,7 +19,8 @@ refused. The backward may run more than once
 
 Calls can be captured in a graph, with their backward. While an autograd graph of
 the same leaves that was built on the default stream is alive, a captured call that
-needs gradients is refused: the leaves' accumulation would leave the capture.
+needs gradients is refused: the leaves' accumulation would leave the capture. A forward
+without a backward is captured under torch.no_grad.
 """
 
 import ctypes

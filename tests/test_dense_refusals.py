@@ -100,6 +100,37 @@ def test_tracers_are_refused(name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name", [n for n in ENTRIES if n != "w4_quantize"])
+def test_function_transforms_are_refused(name):
+    """torch.func's transforms and vmap wrap the inputs, which have no memory of their own."""
+    f, t = entries("cuda")[name]
+    with torch.no_grad():
+        f(t)
+        for transform in (lambda: torch.func.jvp(f, (t,), (torch.ones_like(t),)), lambda: torch.vmap(f)(torch.stack([t, t])),
+                          lambda: torch.func.vjp(f, t)):
+            with pytest.raises(RuntimeError):
+                transform()
+
+
+@pytest.mark.gpu
+def test_a_forward_is_captured_beside_a_live_graph_without_gradients():
+    x, w = (torch.randn(s, device="cuda").bfloat16() for s in ((5, 64), (72, 64)))
+    w.requires_grad_()
+    eager = mlp.linear(x, w, None, "gelu")  # alive, on the default stream
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(graph):
+        y = mlp.linear(x, w, None, "gelu")
+    for i in range(3):
+        x.copy_(torch.randn_like(x))
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.no_grad():
+            assert torch.equal(y, mlp.linear(x, w, None, "gelu"))
+    assert eager.requires_grad
+
+
+@pytest.mark.gpu
 def test_what_is_recorded_still_is():
     """swiglu_mlp with gradients under torch.jit.trace, as before; the dense operators under
     torch.compile, which leaves them to be run as they are; a dispatch mode that only looks."""
