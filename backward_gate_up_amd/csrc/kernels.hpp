@@ -487,8 +487,9 @@ __device__ __forceinline__ void gemm_tile(const KArgs& g, char* smem, int bid, i
   if constexpr (KIND == LINEAR) {
     // The same pipeline with two sets of registers, tile j in set j % 2, so that a
     // load has seven quarters of a stage to arrive instead of three: most LINEAR
-    // launches have one or two tiles per CU, which wait for their loads (T = 1000, N = 2816, K
-    // = 1024 in fp32 60.0 -> 56.3 us, its gradients 118 -> 102; bf16, 1000 x 1024 x 2816
+    // launches have one or two tiles per CU, which wait for their loads (calls back to back
+    // in a graph: T = 1000, N = 2816, K = 1024 in fp32 60.0 -> 56.3 us, its gradients 118 -> 102,
+    // which a trace of eager calls has as 62 to 65 and 110 to 114; bf16, 1000 x 1024 x 2816
     // 23.1 -> 20.5; 2048^3 27.6 -> 26.3). Four sets cost the large tiles their registers and
     // short K its start. Loads past the last tile read that one again instead.
     TileLoader<E, BM, AL> pa[2];

@@ -320,7 +320,13 @@ static inline int few_splits(int64_t T, int64_t N, int64_t K, size_t e) {
 // sizes (65 to 16384 by 256 to 11008, all three layouts), each on several tiles in 1
 // to 16 parts. With the tiles' loads two stages ahead they are 5 to 15 % long for
 // them, which changes no choice by much: what is chosen takes 1.5 % longer than the
-// best of what was timed, over nine thousand others, and with figures fitted again 0.3 % less.
+// best of what was timed in the geometric mean over nine thousand others, and with
+// figures fitted again 0.3 % less. 235 of those are more than 15 % behind, 41 more
+// than 25: 49 with a short K and a large output, where the ring is taken for tiles up
+// to 46 % faster (ring_us has no term for its outputs, which no other tile of a CU
+// covers; 15773 x 10712 over 368 317 us, 128 x 128 tiles 218); 52 with a long K and a
+// narrow output, where it is not (below 64 of its tiles it is left out; 4403 x 712 over
+// 8536 103 us, the ring in four parts 73); else products of tiles of 10 to 30 us.
 // fp32 has only 64 x 64: wider ones were behind at every
 // size but the largest, by 3 % there (M = N = 2000, K = 8000 503 against 487 us).
 // What the choice is worth (us, unsplit 64 x 64 / 128 x 128 / best split; bf16): 256
@@ -516,7 +522,7 @@ static inline BwdPlan bwd_plan(int64_t T, int64_t N, int64_t K, size_t e, bool a
 
 // ---- launches ------------------------------------------------------------------------
 // A product on register-staged tiles: LINEAR's epilogue, or its parts. fp32, T = 1000, N
-// = 2816, K = 1024, gelu: 62 us, 92 TFLOP/s on 2.75 tiles per CU; 1024 x 4096 x 4096
+// = 2816, K = 1024, gelu: 62 to 65 us, 92 TFLOP/s on 2.75 tiles per CU; 1024 x 4096 x 4096
 // 249 us, 138 (the library's 8192^3 152). fp16, T = 300, N = 712, K = 1000 11 us: latency.
 template <class E, int BM, int BN, int AL, int BL, int STAGE>
 __global__ void __launch_bounds__(256, (BM == 64 && BN == 64 ? 3 : 2)) lin_tile(const KArgs g) {

@@ -26,10 +26,12 @@
 // stride of the grid, keeps w and b, and asks for the next row before it works
 // on the one it has.
 //
-// Measured (bf16): forward of 16384 x 4096 45 us and of 65536 x 1024 45 us, 6.0
-// TB/s; their backward 89 us (4.5 TB/s, two sums per row between loads and
-// stores) and, RMS, 80 us (5.0 TB/s), the join of the weight's gradient 5 us.
-// A 2 GiB copy reaches 4.9 TB/s. 16 rows of 2048 3.3 us, a launch and two latencies.
+// Measured (bf16): forward of 16384 x 4096 53 us and of 65536 x 1024 54 us, 5.1 and
+// 5.0 TB/s, the rate of a copy; RMS 50 and 52. Where a call writes the last one's y
+// again, of which the 256 MB cache holds a part, 46, 48, 45 and 48. Their backward 90 us
+// (4.5 TB/s, two sums per row between loads and stores) and, RMS of 65536 x 1024, 81 us
+// (5.0 TB/s), the join of the weight's gradient 5 us. fp32, 16384 x 4096, 104 and 160
+// us (5.2 and 5.0 TB/s). 16 rows of 2048 3.3 us, a launch and two latencies.
 //
 // The weight's gradient is summed in the same pass over x and dy: each lane owns
 // its columns for all rows of its group, so its sums are registers. They are
